@@ -74,7 +74,7 @@ def draw(rng):
         topk_group = n_group if n_group == 1 else rng.randint(max(1, -(-k * n_group // E)), n_group)
         return _route(None, T, E, k, rng.choice(["softmax", "sigmoid"]), rng.choice(list(TYPES)),
                       normalize=rng.random() < 0.75, scale=rng.choice([1.0, 2.5]), n_group=n_group,
-                      topk_group=topk_group, group_topn=rng.randint(1, 3), bias=rng.random() < 0.5,
+                      topk_group=topk_group, group_topn=rng.randint(1, min(3, E // n_group)), bias=rng.random() < 0.5,
                       S=min(T, _log(rng, 1, 64)), pad=rng.choice([0, 0, 1, 8]), masked=rng.random() < 0.4,
                       off=rng.random() < 0.3, train=rng.random() < 0.75)
     if op == "bias":
