@@ -264,6 +264,148 @@ moe_status_t moe_forward(const void *x, const int32_t *topk_idx, const float *to
                          const void *w1, const void *w2, const moe_shape_t *shape, void *y,
                          void *ws, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------ the trainable router
+ *
+ * moe_router gives its aux score as a number: no gradient reaches it, every row
+ * of x is a token, and sel_bias is only read. The three calls below are the
+ * router's part of a training step from logits that the caller computes (and
+ * differentiates), in fp32, bf16 or fp16.
+ */
+
+#define MOE_DTYPE_F32 0
+#define MOE_DTYPE_BF16 1
+#define MOE_DTYPE_F16 2
+
+typedef struct moe_route_shape {
+    int64_t T;      /* tokens */
+    int64_t E;      /* experts */
+    int64_t S;      /* sequences the tokens are packed from (1 where seq_offsets is NULL) */
+    int64_t ld;     /* elements from a token's logits to the next one's, >= E */
+    int32_t k;      /* experts per token */
+    int32_t dtype;  /* of the logits: MOE_DTYPE_* */
+} moe_route_shape_t;
+
+/* Bytes of workspace that moe_route needs for its statistics. Host-only. */
+moe_status_t moe_route_workspace_size(const moe_route_shape_t *shape, size_t *bytes);
+
+/*
+ * Selection from logits, with the balance statistics of a training step.
+ *
+ *   expert e is off for token t when l[t,e] = -inf: score 0, never chosen
+ *   token t is live when token_mask[t] != 0 and not all its experts are off
+ *   s      = softmax(l[t,:]) or sigmoid(l[t,:])
+ *   key    = l without sel_bias, else s + sel_bias
+ *   groups = (n_group > 1) keep the topk_group groups with the largest sum of
+ *            their group_topn best s + sel_bias
+ *   topk_idx = the k experts of the kept groups with the largest key, best
+ *            first, ties to the lower index; -1 in slots left over (a token
+ *            that is not live, or has fewer than k experts on)
+ *   topk_w = s of those / (their sum + 1e-20) if normalize, * scale; 0 in slots
+ *            left over
+ *   counts[b,e] = slots of sequence b on expert e
+ *   seq_tokens  = live tokens of each sequence [0, S), of all [S], and the
+ *            number of sequences that have any [S + 1]
+ *   losses[0] = 1/S' sum_b sum_e E counts[b,e] / (k n_b) P[b,e],
+ *            P[b,e] = 1/n_b sum_{t in b, live} s[t,e] / (sum_f s[t,f] + 1e-20)
+ *   losses[1] = 1/N sum_{t live} log(sum_e exp l[t,e])^2
+ *
+ * (with sigmoid scores the shares are normalised, so that lowering every score
+ * does not lower the balance term). The order of experts, and of groups, whose
+ * keys are nearer than fp32 resolves is decided in fp64. A NaN logit of a live
+ * token is never chosen; with softmax it makes that token's weights NaN.
+ * Values in rows whose mask is 0 reach no output.
+ *
+ * logits [T,E] with rows ld apart, dtype-aligned; sel_bias fp32 [E] or NULL;
+ * token_mask uint8 [T] or NULL (all set); seq_offsets int32 [S+1] on the
+ * device, 0 first, T last, not decreasing (sequences may be empty), or NULL
+ * with S = 1. counts int32 [S,E], seq_tokens int32 [S+2] and losses fp32 [2]
+ * are all given, with ws, or all NULL: then only the selection runs, in one
+ * launch. Every output has the same bits on every call. Limits: 1 <= k <= 32,
+ * k <= E <= 1024, T <= 2^30, S <= 2^24, n_group as for moe_router. In moe_forward
+ * a slot of -1 is dropped, and recorded as MOE_DEVERR_BAD_EXPERT_INDEX.
+ */
+moe_status_t moe_route(const void *logits, const float *sel_bias, const uint8_t *token_mask,
+                       const int32_t *seq_offsets, const moe_route_shape_t *shape,
+                       const moe_router_cfg_t *cfg, int32_t *topk_idx, float *topk_w, int32_t *counts,
+                       int32_t *seq_tokens, float *losses, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Gradient of moe_route's topk_w and losses with respect to the logits:
+ * dlogits [T,E], dense, of the logits' type, fully written (0 for experts that
+ * are off and tokens that are not live). The selection and the counts carry no
+ * gradient. dtopk_w fp32 [T,k]; dlosses fp32 [2] on the device, or NULL where
+ * the losses are not used (counts, seq_tokens and seq_offsets are then not
+ * read). topk_idx, counts and seq_tokens are moe_route's.
+ */
+moe_status_t moe_route_backward(const void *logits, const uint8_t *token_mask, const int32_t *seq_offsets,
+                                const moe_route_shape_t *shape, const moe_router_cfg_t *cfg,
+                                const int32_t *topk_idx, const float *dtopk_w, const int32_t *counts,
+                                const int32_t *seq_tokens, const float *dlosses, void *dlogits, void *stream);
+
+/*
+ * Balance without a loss: after a step, the selection bias of every expert that
+ * received less than the average goes up by `rate`, of every other one down:
+ *   bias[l,e] += rate * sign(sum_f c[l,f] - E c[l,e]),  c[l,e] = sum_b counts[l,b,e]
+ * bias fp32 [L,E] in place, counts int32 [L,S,E] (moe_route's, one block per
+ * layer). E <= 1024. The sums and the comparison are exact.
+ */
+moe_status_t moe_bias_update(float *bias, const int32_t *counts, int64_t L, int64_t S, int64_t E, float rate,
+                             void *stream);
+
+/* ------------------------------------------------------------------ the optimizer's end of a step
+ *
+ * Over lists of n tensors: host arrays of device pointers, element counts and
+ * MOE_DTYPE_* types, read before the call returns. A tensor is its `numel`
+ * consecutive elements, aligned to its element; it may be empty, and tensors
+ * do not overlap. The total is at most 2^42 elements. ws: moe_tensors_workspace_size
+ * bytes, 16-byte aligned, not initialised. Nothing is read back by the host.
+ */
+#define MOE_NORM_INF 0
+#define MOE_NORM_1 1
+#define MOE_NORM_2 2
+
+moe_status_t moe_tensors_workspace_size(int32_t n, size_t *bytes);
+
+/* norm[0] (fp32, device) = the norm of all elements of all tensors together.
+ * Sums are held in fp64, so no value of the types over- or underflows in them;
+ * NaN and infinity propagate. The same bits on every call. */
+moe_status_t moe_grad_norm(const void *const *grads, const int64_t *numel, const int32_t *dtype, int32_t n,
+                           int32_t norm_type, float *norm, void *ws, size_t ws_bytes, void *stream);
+
+/* The same norm, and every element of every tensor times
+ * min(1, max_norm / (norm + 1e-6)), in place (rounded once to its type;
+ * untouched where the factor is 1). max_norm > 0. A NaN norm makes every
+ * element NaN and an infinite one every finite element 0. */
+moe_status_t moe_clip_grads(void *const *grads, const int64_t *numel, const int32_t *dtype, int32_t n,
+                            int32_t norm_type, float max_norm, float *norm, void *ws, size_t ws_bytes,
+                            void *stream);
+
+typedef struct moe_adamw_cfg {
+    float beta1, beta2;      /* in [0, 1) */
+    float eps;               /* >= 0 */
+    float weight_decay;
+    float max_norm;          /* clip by the gradients' global 2-norm; 0: no clipping */
+    int32_t skip_nonfinite;  /* 1: where that norm is not finite, change nothing and do not count the step */
+} moe_adamw_cfg_t;
+
+/*
+ * One AdamW step, t = step[0] + 1 (step[0] becomes t):
+ *   g = f grad, f = min(1, max_norm / (norm + 1e-6)) or 1
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p -= lr (weight_decay p + (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps))
+ * in fp32. params[i] of type param_dtype[i]; grads[i] of grad_dtype[i], not
+ * changed; exp_avg[i], exp_avg_sq[i] fp32. masters[i]: fp32 copy of the
+ * parameter that the step reads and writes, the parameter being its rounding;
+ * where masters or masters[i] is NULL, the parameter itself (rounded to nearest
+ * at every step).
+ * lr fp32 [1] and step int32 [1] are on the device, so that a captured step
+ * can be replayed. norm fp32 [1] on the device, or NULL.
+ */
+moe_status_t moe_adamw(void *const *params, const int32_t *param_dtype, const void *const *grads,
+                       const int32_t *grad_dtype, float *const *exp_avg, float *const *exp_avg_sq,
+                       float *const *masters, const int64_t *numel, int32_t n, const moe_adamw_cfg_t *cfg,
+                       const float *lr, int32_t *step, float *norm, void *ws, size_t ws_bytes, void *stream);
+
 /* ------------------------------------------------------------------ expert parallelism
  *
  * Across devices the guide fuses the dispatch all-to-all into

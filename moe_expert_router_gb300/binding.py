@@ -14,7 +14,7 @@ import os
 
 import torch
 
-from .build import LIB_PATH
+from .build import LIB_PATH, LISTS_PATH
 
 MOE_OK = 0
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
@@ -27,6 +27,8 @@ SCORE_SIGMOID = 1
 SHAPE_TRAINING = 0x1
 SHAPE_MXFP8 = 0x2
 SHAPE_PACKED_WEIGHTS = 0x4
+DTYPE_CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+NORM_CODES = {float("inf"): 0, 1.0: 1, 2.0: 2}
 
 
 class MoEError(RuntimeError):
@@ -44,6 +46,16 @@ class RouterCfg(ctypes.Structure):
     _fields_ = [("score_fn", ctypes.c_int32), ("normalize", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("n_group", ctypes.c_int32),
                 ("topk_group", ctypes.c_int32), ("group_topn", ctypes.c_int32)]
+
+
+class RouteShape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("S", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("k", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class AdamWCfg(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_float), ("beta2", ctypes.c_float), ("eps", ctypes.c_float),
+                ("weight_decay", ctypes.c_float), ("max_norm", ctypes.c_float), ("skip_nonfinite", ctypes.c_int32)]
 
 
 class WsLayout(ctypes.Structure):
@@ -100,6 +112,17 @@ _SIG = {
     "moe_packed_weights_size": [ctypes.POINTER(Shape), ctypes.POINTER(ctypes.c_size_t),
                                 ctypes.POINTER(ctypes.c_size_t)],
     "moe_pack_weights": [_P, _P, ctypes.POINTER(Shape), _P, _P, _P],
+    "moe_route_workspace_size": [ctypes.POINTER(RouteShape), ctypes.POINTER(ctypes.c_size_t)],
+    "moe_route": [_P, _P, _P, _P, ctypes.POINTER(RouteShape), ctypes.POINTER(RouterCfg), _P, _P, _P, _P, _P, _P,
+                  ctypes.c_size_t, _P],
+    "moe_route_backward": [_P, _P, _P, ctypes.POINTER(RouteShape), ctypes.POINTER(RouterCfg), _P, _P, _P, _P, _P, _P,
+                           _P],
+    "moe_bias_update": [_P, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_float, _P],
+    "moe_tensors_workspace_size": [ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_grad_norm": [_P, _P, _P, ctypes.c_int32, ctypes.c_int32, _P, _P, ctypes.c_size_t, _P],
+    "moe_clip_grads": [_P, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_float, _P, _P, ctypes.c_size_t, _P],
+    "moe_adamw": [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int32, ctypes.POINTER(AdamWCfg), _P, _P, _P, _P,
+                  ctypes.c_size_t, _P],
     "moe_get_device_error": [_P, ctypes.POINTER(ctypes.c_int32), _P],
     "moe_status_string": [ctypes.c_int],
     "moe_kernel_launch_count": [],
@@ -107,6 +130,7 @@ _SIG = {
 _RESTYPES = {"moe_status_string": ctypes.c_char_p, "moe_kernel_launch_count": ctypes.c_uint64}
 
 _lib = None
+_lists = None
 
 
 def load(path: str = LIB_PATH):
@@ -446,3 +470,160 @@ def new_workspace(shp: Shape, device=None) -> torch.Tensor:
     ws = ws[off:off + n]
     moe_workspace_init(ws)
     return ws
+
+
+# ------------------------------------------------------------------ the trainable router
+
+def _typed(t, name, dtype, shape):
+    """Checks an optional dense tensor and gives its address."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _mask_ptr(mask, T):
+    if mask is not None and mask.dtype == torch.uint8:
+        return _typed(mask, "token_mask", torch.uint8, (T,))
+    return _typed(mask, "token_mask", torch.bool, (T,))
+
+
+def _route_shape(logits, topk_idx, seq_offsets):
+    if logits.dim() != 2 or topk_idx.dim() != 2:
+        raise ValueError("logits must be [T, E] and topk_idx [T, k]")
+    if logits.dtype not in DTYPE_CODES:
+        raise TypeError(f"logits must be float32, bfloat16 or float16, not {logits.dtype}")
+    if not logits.is_cuda:
+        raise ValueError("libmoe takes CUDA tensors only")
+    T, E = logits.shape
+    if E > 1 and logits.stride(1) != 1:
+        raise ValueError("the experts of a row of logits must be consecutive")
+    ld = logits.stride(0) if T > 1 else E
+    if ld < E:
+        raise ValueError("the rows of logits overlap")
+    if seq_offsets is not None and (seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2):
+        raise ValueError("seq_offsets must be [S + 1] with S >= 1")
+    S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+    return RouteShape(T, E, S, ld, topk_idx.shape[1], DTYPE_CODES[logits.dtype])
+
+
+def moe_route_workspace_size(T, E, S=1, k=1) -> int:
+    n = ctypes.c_size_t()
+    shp = RouteShape(T, E, S, E, k, 0)
+    _check("moe_route_workspace_size", load().moe_route_workspace_size(ctypes.byref(shp), ctypes.byref(n)))
+    return int(n.value)
+
+
+def moe_route(logits, cfg, topk_idx, topk_w, sel_bias=None, token_mask=None, seq_offsets=None, counts=None,
+              seq_tokens=None, losses=None, ws=None, stream=None):
+    """Selection from logits [T, E] (fp32, bf16 or fp16; rows may be apart), with the balance
+    statistics of a training step where counts [S, E], seq_tokens [S + 2], losses [2] and a
+    workspace of moe_route_workspace_size bytes are given. token_mask: bool or uint8 [T]."""
+    shp = _route_shape(logits, topk_idx, seq_offsets)
+    T, E, S, k = shp.T, shp.E, shp.S, shp.k
+    _check("moe_route", load().moe_route(
+        ctypes.c_void_p(logits.data_ptr()), _typed(sel_bias, "sel_bias", torch.float32, (E,)), _mask_ptr(token_mask, T),
+        _typed(seq_offsets, "seq_offsets", torch.int32, (S + 1,)), ctypes.byref(shp), ctypes.byref(cfg),
+        _typed(topk_idx, "topk_idx", torch.int32, (T, k)), _typed(topk_w, "topk_w", torch.float32, (T, k)),
+        _typed(counts, "counts", torch.int32, (S, E)), _typed(seq_tokens, "seq_tokens", torch.int32, (S + 2,)),
+        _typed(losses, "losses", torch.float32, (2,)), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+        _stream(stream, logits)))
+
+
+def moe_route_backward(logits, cfg, topk_idx, dtopk_w, dlogits, token_mask=None, seq_offsets=None, counts=None,
+                       seq_tokens=None, dlosses=None, stream=None):
+    """Gradient of moe_route's topk_w and losses with respect to the logits, into dlogits [T, E]
+    (dense, the logits' type)."""
+    shp = _route_shape(logits, topk_idx, seq_offsets)
+    T, E, S, k = shp.T, shp.E, shp.S, shp.k
+    _check("moe_route_backward", load().moe_route_backward(
+        ctypes.c_void_p(logits.data_ptr()), _mask_ptr(token_mask, T),
+        _typed(seq_offsets, "seq_offsets", torch.int32, (S + 1,)), ctypes.byref(shp), ctypes.byref(cfg),
+        _typed(topk_idx, "topk_idx", torch.int32, (T, k)), _typed(dtopk_w, "dtopk_w", torch.float32, (T, k)),
+        _typed(counts, "counts", torch.int32, (S, E)), _typed(seq_tokens, "seq_tokens", torch.int32, (S + 2,)),
+        _typed(dlosses, "dlosses", torch.float32, (2,)), _typed(dlogits, "dlogits", logits.dtype, (T, E)),
+        _stream(stream, logits)))
+
+
+def moe_bias_update(bias, counts, rate, stream=None):
+    """bias [E] or [L, E] += rate * sign(mean count - count), in place; counts int32 [S, E] or
+    [L, S, E], added over the sequences."""
+    if bias.dim() not in (1, 2) or counts.dim() != bias.dim() + 1:
+        raise ValueError("bias must be [E] and counts [S, E], or [L, E] and [L, S, E]")
+    L, E, S = (1 if bias.dim() == 1 else bias.shape[0]), bias.shape[-1], counts.shape[-2]
+    if counts.shape[-1] != E or (bias.dim() == 2 and counts.shape[0] != L):
+        raise ValueError(f"bias is {tuple(bias.shape)}, counts {tuple(counts.shape)}")
+    _check("moe_bias_update", load().moe_bias_update(
+        _typed(bias, "bias", torch.float32, bias.shape), _typed(counts, "counts", torch.int32, counts.shape), L, S, E,
+        float(rate), _stream(stream, bias)))
+
+
+# ------------------------------------------------------------------ lists of tensors
+
+def _gather(tensors, name, device, dtype=None, like=None, optional=False):
+    """A list's addresses, element counts and types as C arrays (bytes), checked to be dense
+    tensors on one device, of one type and like the parameters where asked."""
+    global _lists
+    if _lists is None:
+        try:
+            from . import _lists as native
+        except ImportError as e:
+            raise RuntimeError(f"{LISTS_PATH} is missing: build it first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
+        _lists = native
+    return _lists.gather(tensors, name, device, -1 if dtype is None else DTYPE_CODES[dtype], like, optional)
+
+
+def _device_of(t):
+    if not t.is_cuda:
+        raise ValueError("libmoe takes CUDA tensors only")
+    return t.get_device()
+
+
+def moe_tensors_workspace_size(n) -> int:
+    size = ctypes.c_size_t()
+    _check("moe_tensors_workspace_size", load().moe_tensors_workspace_size(n, ctypes.byref(size)))
+    return int(size.value)
+
+
+def _norm_code(norm_type):
+    try:
+        return NORM_CODES[float(norm_type)]
+    except KeyError:
+        raise ValueError(f"norm_type must be 1, 2 or inf, not {norm_type}") from None
+
+
+def moe_grad_norm(grads, norm, ws, norm_type=2.0, stream=None):
+    """norm [1] = the norm of all the tensors' elements together."""
+    ptr, numel, dtype = _gather(grads, "grads", _device_of(norm))
+    _check("moe_grad_norm", load().moe_grad_norm(
+        ptr, numel, dtype, len(grads), _norm_code(norm_type), _typed(norm, "norm", torch.float32, (1,)), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream, norm)))
+
+
+def moe_clip_grads(grads, max_norm, norm, ws, norm_type=2.0, stream=None):
+    """The same norm, and every tensor times min(1, max_norm / (norm + 1e-6)), in place."""
+    ptr, numel, dtype = _gather(grads, "grads", _device_of(norm))
+    _check("moe_clip_grads", load().moe_clip_grads(
+        ptr, numel, dtype, len(grads), _norm_code(norm_type), float(max_norm),
+        _typed(norm, "norm", torch.float32, (1,)), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream, norm)))
+
+
+def moe_adamw(params, grads, exp_avg, exp_avg_sq, lr, step, ws, cfg, masters=None, norm=None, stream=None):
+    """One AdamW step over lists of tensors, in place; masters: a list with an fp32 tensor or None
+    for each parameter, or None."""
+    device = _device_of(lr)
+    p, numel, p_dtype = _gather(params, "params", device)
+    g, _, g_dtype = _gather(grads, "grads", device, None, params)
+    m = _gather(exp_avg, "exp_avg", device, torch.float32, params)[0]
+    v = _gather(exp_avg_sq, "exp_avg_sq", device, torch.float32, params)[0]
+    x = None if masters is None else _gather(masters, "masters", device, torch.float32, params, True)[0]
+    _check("moe_adamw", load().moe_adamw(
+        p, p_dtype, g, g_dtype, m, v, x, numel, len(params), ctypes.byref(cfg), _typed(lr, "lr", torch.float32, (1,)),
+        _typed(step, "step", torch.int32, (1,)), _typed(norm, "norm", torch.float32, (1,)), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream, lr)))

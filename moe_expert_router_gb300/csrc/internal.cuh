@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
 #include <utility>
 
 #include "moe.h"
@@ -369,6 +370,82 @@ bool encode_bf16_3d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t
 // wider row-major tensor.
 bool encode_bf16_2d_strided(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows,
                             uint64_t row_stride, uint32_t box_inner, uint32_t box_rows);
+
+// The trainable router (route.cu). Tokens are dealt to blocks of per_block
+// consecutive ones; a (block, sequence) pair has slot block + sequence, of
+// blocks + S - 1.
+constexpr int64_t kRouteMaxBlocks = 152 * 6;
+struct RouteTiles {
+    int64_t blocks, per_block;
+};
+RouteTiles route_tiles(int64_t T, int64_t E);
+struct RouteLaunch {
+    const void *logits;         // [T, E], rows ld elements apart
+    int dtype;                  // MOE_DTYPE_*
+    int vec;                    // rows are 16-byte aligned
+    int64_t ld;
+    const float *sel_bias;      // [E] or null
+    const uint8_t *mask;        // [T] or null
+    const int32_t *seq_offsets; // [S + 1], read where S > 1
+    int T, E, k, S;
+    int score_fn, normalize;
+    float scale;
+    int n_group, topk_group, group_topn;
+    int32_t *topk_idx;
+    float *topk_w;
+    int32_t *counts;            // [S, E]
+    int32_t *seq_tokens;        // [S + 2]
+    float *losses;              // [2]; null: selection alone, none of the statistics
+    int per_block;
+    float *part_score, *part_z; // [slots, E], [slots]
+    int32_t *part_count, *part_n;
+    float *part_balance, *seq_z; // [S, ceil(E / 32)], [S]
+    int32_t *ticket;
+};
+struct RouteBackwardLaunch {
+    const void *logits;
+    int dtype, vec, vec_out;
+    int64_t ld;
+    const uint8_t *mask;
+    const int32_t *seq_offsets;
+    int T, E, k, S;
+    int score_fn, normalize;
+    float scale;
+    const int32_t *topk_idx;
+    const float *dtopk_w;
+    const int32_t *counts, *seq_tokens;
+    const float *dlosses;       // [2] or null
+    void *dlogits;              // [T, E] dense, the logits' type
+    int per_block;
+};
+cudaError_t launch_route(const RouteLaunch &p, cudaStream_t st);
+cudaError_t launch_route_backward(const RouteBackwardLaunch &p, cudaStream_t st);
+cudaError_t launch_bias_update(float *bias, const int32_t *counts, int L, int S, int E, float rate, cudaStream_t st);
+
+// Operators over lists of tensors (multi_tensor.cu); host arrays of device pointers.
+struct TensorList {
+    const void *const *ptr;
+    const int64_t *numel;
+    const int32_t *dtype;
+    int n;
+};
+struct AdamwLaunch {
+    TensorList params, grads;   // the same lengths; types differ
+    void *const *exp_avg;       // fp32
+    void *const *exp_avg_sq;    // fp32
+    void *const *masters;       // fp32, or null
+    float beta1, beta2, eps, weight_decay, max_norm;
+    int skip_nonfinite;
+    const float *lr;            // [1] device
+    int32_t *step;              // [1] device
+    float *norm;                // [1] device or null
+    void *ws;
+};
+size_t multi_tensor_ws_bytes(int64_t n);
+cudaError_t launch_grad_norm(const TensorList &grads, int norm_type, float *norm, void *ws, cudaStream_t st);
+cudaError_t launch_clip_grads(const TensorList &grads, int norm_type, float max_norm, float *norm, void *ws,
+                              cudaStream_t st);
+cudaError_t launch_adamw(const AdamwLaunch &p, cudaStream_t st);
 
 // Statistics: kernels launched by this library.
 void note_launches(int n);

@@ -1423,3 +1423,288 @@ const char *moe_status_string(moe_status_t status) {
 uint64_t moe_kernel_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }
 
 }  // extern "C"
+
+namespace {
+
+struct RouteWs {
+    size_t score, count, z, n, balance, seq_z, ticket, total;
+};
+
+RouteWs route_layout(const moe_route_shape_t &s) {
+    const RouteTiles tiles = route_tiles(s.T, s.E);
+    const size_t slots = static_cast<size_t>(tiles.blocks + s.S - 1);
+    RouteWs w;
+    w.score = 0;
+    w.count = w.score + align256(4 * slots * s.E);
+    w.z = w.count + align256(4 * slots * s.E);
+    w.n = w.z + align256(4 * slots);
+    w.balance = w.n + align256(4 * slots);
+    w.seq_z = w.balance + align256(4 * static_cast<size_t>(s.S) * ((s.E + 31) / 32));
+    w.ticket = w.seq_z + align256(4 * static_cast<size_t>(s.S));
+    w.total = w.ticket + 256;
+    return w;
+}
+
+moe_status_t check_route_shape(const moe_route_shape_t *s) {
+    if (s == nullptr || s->T < 0 || s->E < 1 || s->S < 1 || s->k < 1 || s->ld < s->E) return MOE_ERR_INVALID_ARG;
+    if (s->dtype < MOE_DTYPE_F32 || s->dtype > MOE_DTYPE_F16) return MOE_ERR_INVALID_ARG;
+    if (s->k > 32 || s->k > s->E || s->E > 1024 || s->T > (1 << 30) || s->S > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+    if (s->ld > (static_cast<int64_t>(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+moe_status_t check_route_cfg(const moe_route_shape_t *s, const moe_router_cfg_t *cfg) {
+    if (cfg == nullptr) return MOE_ERR_INVALID_ARG;
+    moe_shape_t m = {};
+    m.E = s->E;
+    m.k = s->k;
+    return check_router_cfg(&m, cfg);
+}
+
+bool aligned_to(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+size_t dtype_size(int32_t dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+
+// Whole 16-byte vectors of experts can be read from (written to) every row.
+int rows_vectorized(const void *p, int64_t ld, int32_t dtype) {
+    return aligned16(p) && (ld * static_cast<int64_t>(dtype_size(dtype))) % 16 == 0;
+}
+
+moe_status_t check_list(const void *const *ptr, const int64_t *numel, const int32_t *dtype, int32_t n,
+                        bool optional = false) {
+    if (n < 0 || (n > 0 && (ptr == nullptr || numel == nullptr))) return MOE_ERR_INVALID_ARG;
+    int64_t total = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        if (numel[i] < 0) return MOE_ERR_INVALID_ARG;
+        const int32_t t = dtype != nullptr ? dtype[i] : MOE_DTYPE_F32;
+        if (t < MOE_DTYPE_F32 || t > MOE_DTYPE_F16) return MOE_ERR_INVALID_ARG;
+        if (numel[i] == 0 || (optional && ptr[i] == nullptr)) continue;
+        if (ptr[i] == nullptr || !aligned_to(ptr[i], dtype_size(t))) return MOE_ERR_INVALID_ARG;
+        if (numel[i] > (static_cast<int64_t>(1) << 42) - total) return MOE_ERR_UNSUPPORTED;
+        total += numel[i];
+    }
+    return MOE_OK;
+}
+
+moe_status_t check_list_ws(const void *ws, size_t ws_bytes, int32_t n) {
+    if (ws == nullptr || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
+    return ws_bytes < multi_tensor_ws_bytes(n) ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_route_workspace_size(const moe_route_shape_t *shape, size_t *bytes) {
+    const moe_status_t r = check_route_shape(shape);
+    if (r != MOE_OK) return r;
+    if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+    *bytes = shape->T == 0 ? 256 : route_layout(*shape).total;
+    return MOE_OK;
+}
+
+moe_status_t moe_route(const void *logits, const float *sel_bias, const uint8_t *token_mask,
+                       const int32_t *seq_offsets, const moe_route_shape_t *shape,
+                       const moe_router_cfg_t *cfg, int32_t *topk_idx, float *topk_w, int32_t *counts,
+                       int32_t *seq_tokens, float *losses, void *ws, size_t ws_bytes, void *stream) {
+    moe_status_t r = check_route_shape(shape);
+    if (r != MOE_OK) return r;
+    if ((r = check_route_cfg(shape, cfg)) != MOE_OK) return r;
+    const bool stats = counts != nullptr || seq_tokens != nullptr || losses != nullptr;
+    if (stats) {
+        if (counts == nullptr || seq_tokens == nullptr || losses == nullptr) return MOE_ERR_INVALID_ARG;
+        if (!aligned_to(counts, 4) || !aligned_to(seq_tokens, 4) || !aligned_to(losses, 4)) return MOE_ERR_INVALID_ARG;
+        if (shape->S > 1 && (seq_offsets == nullptr || !aligned_to(seq_offsets, 4))) return MOE_ERR_INVALID_ARG;
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (shape->T == 0) {
+        if (!stats) return MOE_OK;
+        const size_t S = static_cast<size_t>(shape->S);
+        if (cudaMemsetAsync(counts, 0, 4 * S * shape->E, st) != cudaSuccess ||
+            cudaMemsetAsync(seq_tokens, 0, 4 * (S + 2), st) != cudaSuccess ||
+            cudaMemsetAsync(losses, 0, 8, st) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    if (logits == nullptr || topk_idx == nullptr || topk_w == nullptr) return MOE_ERR_INVALID_ARG;
+    if (!aligned_to(logits, dtype_size(shape->dtype)) || !aligned_to(topk_idx, 4) || !aligned_to(topk_w, 4) ||
+        !aligned_to(sel_bias, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (stats) {
+        if (ws == nullptr || !aligned_to(ws, 256)) return MOE_ERR_INVALID_ARG;
+        if (ws_bytes < route_layout(*shape).total) return MOE_ERR_WORKSPACE;
+    }
+    DeviceState *d = nullptr;
+    if ((r = device_state(&d)) != MOE_OK) return r;
+    RouteLaunch p{};
+    p.logits = logits;
+    p.dtype = shape->dtype;
+    p.vec = rows_vectorized(logits, shape->ld, shape->dtype);
+    p.ld = shape->ld;
+    p.sel_bias = sel_bias;
+    p.mask = token_mask;
+    p.seq_offsets = seq_offsets;
+    p.T = static_cast<int>(shape->T);
+    p.E = static_cast<int>(shape->E);
+    p.k = shape->k;
+    p.S = stats ? static_cast<int>(shape->S) : 1;
+    p.score_fn = cfg->score_fn;
+    p.normalize = cfg->normalize;
+    p.scale = cfg->scale;
+    p.n_group = cfg->n_group;
+    p.topk_group = cfg->topk_group;
+    p.group_topn = cfg->group_topn;
+    p.topk_idx = topk_idx;
+    p.topk_w = topk_w;
+    p.counts = counts;
+    p.seq_tokens = seq_tokens;
+    p.losses = losses;
+    p.per_block = static_cast<int>(route_tiles(shape->T, shape->E).per_block);
+    if (stats) {
+        const RouteWs w = route_layout(*shape);
+        char *b = static_cast<char *>(ws);
+        p.part_score = reinterpret_cast<float *>(b + w.score);
+        p.part_count = reinterpret_cast<int32_t *>(b + w.count);
+        p.part_z = reinterpret_cast<float *>(b + w.z);
+        p.part_n = reinterpret_cast<int32_t *>(b + w.n);
+        p.part_balance = reinterpret_cast<float *>(b + w.balance);
+        p.seq_z = reinterpret_cast<float *>(b + w.seq_z);
+        p.ticket = reinterpret_cast<int32_t *>(b + w.ticket);
+    }
+    return cuda_status(launch_route(p, st));
+}
+
+moe_status_t moe_route_backward(const void *logits, const uint8_t *token_mask, const int32_t *seq_offsets,
+                                const moe_route_shape_t *shape, const moe_router_cfg_t *cfg,
+                                const int32_t *topk_idx, const float *dtopk_w, const int32_t *counts,
+                                const int32_t *seq_tokens, const float *dlosses, void *dlogits, void *stream) {
+    moe_status_t r = check_route_shape(shape);
+    if (r != MOE_OK) return r;
+    if ((r = check_route_cfg(shape, cfg)) != MOE_OK) return r;
+    if (shape->T == 0) return MOE_OK;
+    if (logits == nullptr || topk_idx == nullptr || dtopk_w == nullptr || dlogits == nullptr) return MOE_ERR_INVALID_ARG;
+    if (!aligned_to(logits, dtype_size(shape->dtype)) || !aligned_to(dlogits, dtype_size(shape->dtype)) ||
+        !aligned_to(topk_idx, 4) || !aligned_to(dtopk_w, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (dlosses != nullptr) {
+        if (counts == nullptr || seq_tokens == nullptr || (shape->S > 1 && seq_offsets == nullptr))
+            return MOE_ERR_INVALID_ARG;
+        if (!aligned_to(counts, 4) || !aligned_to(seq_tokens, 4) || !aligned_to(seq_offsets, 4) ||
+            !aligned_to(dlosses, 4))
+            return MOE_ERR_INVALID_ARG;
+    }
+    DeviceState *d = nullptr;
+    if ((r = device_state(&d)) != MOE_OK) return r;
+    RouteBackwardLaunch p{};
+    p.logits = logits;
+    p.dtype = shape->dtype;
+    p.vec = rows_vectorized(logits, shape->ld, shape->dtype);
+    p.vec_out = rows_vectorized(dlogits, shape->E, shape->dtype);
+    p.ld = shape->ld;
+    p.mask = token_mask;
+    p.seq_offsets = seq_offsets;
+    p.T = static_cast<int>(shape->T);
+    p.E = static_cast<int>(shape->E);
+    p.k = shape->k;
+    p.S = static_cast<int>(shape->S);
+    p.score_fn = cfg->score_fn;
+    p.normalize = cfg->normalize;
+    p.scale = cfg->scale;
+    p.topk_idx = topk_idx;
+    p.dtopk_w = dtopk_w;
+    p.counts = counts;
+    p.seq_tokens = seq_tokens;
+    p.dlosses = dlosses;
+    p.dlogits = dlogits;
+    p.per_block = static_cast<int>(route_tiles(shape->T, shape->E).per_block);
+    return cuda_status(launch_route_backward(p, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_bias_update(float *bias, const int32_t *counts, int64_t L, int64_t S, int64_t E, float rate,
+                             void *stream) {
+    if (L < 0 || S < 0 || E < 1) return MOE_ERR_INVALID_ARG;
+    if (E > 1024 || L > 0x7fffffff || S > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+    if (L == 0) return MOE_OK;
+    if (bias == nullptr || (counts == nullptr && S > 0) || !aligned_to(bias, 4) || !aligned_to(counts, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (S == 0) return MOE_OK;
+    DeviceState *d = nullptr;
+    const moe_status_t r = device_state(&d);
+    if (r != MOE_OK) return r;
+    return cuda_status(launch_bias_update(bias, counts, static_cast<int>(L), static_cast<int>(S), static_cast<int>(E),
+                                          rate, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_tensors_workspace_size(int32_t n, size_t *bytes) {
+    if (n < 0 || bytes == nullptr) return MOE_ERR_INVALID_ARG;
+    *bytes = multi_tensor_ws_bytes(n);
+    return MOE_OK;
+}
+
+moe_status_t moe_grad_norm(const void *const *grads, const int64_t *numel, const int32_t *dtype, int32_t n,
+                           int32_t norm_type, float *norm, void *ws, size_t ws_bytes, void *stream) {
+    moe_status_t r = check_list(grads, numel, dtype, n);
+    if (r != MOE_OK) return r;
+    if ((n > 0 && dtype == nullptr) || norm_type < MOE_NORM_INF || norm_type > MOE_NORM_2) return MOE_ERR_INVALID_ARG;
+    if (norm == nullptr || !aligned_to(norm, 4)) return MOE_ERR_INVALID_ARG;
+    if ((r = check_list_ws(ws, ws_bytes, n)) != MOE_OK) return r;
+    DeviceState *d = nullptr;
+    if ((r = device_state(&d)) != MOE_OK) return r;
+    return cuda_status(launch_grad_norm({grads, numel, dtype, n}, norm_type, norm, ws, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_clip_grads(void *const *grads, const int64_t *numel, const int32_t *dtype, int32_t n,
+                            int32_t norm_type, float max_norm, float *norm, void *ws, size_t ws_bytes,
+                            void *stream) {
+    moe_status_t r = check_list(grads, numel, dtype, n);
+    if (r != MOE_OK) return r;
+    if ((n > 0 && dtype == nullptr) || norm_type < MOE_NORM_INF || norm_type > MOE_NORM_2 || !(max_norm > 0.0f))
+        return MOE_ERR_INVALID_ARG;
+    if (norm == nullptr || !aligned_to(norm, 4)) return MOE_ERR_INVALID_ARG;
+    if ((r = check_list_ws(ws, ws_bytes, n)) != MOE_OK) return r;
+    DeviceState *d = nullptr;
+    if ((r = device_state(&d)) != MOE_OK) return r;
+    return cuda_status(launch_clip_grads({grads, numel, dtype, n}, norm_type, max_norm, norm, ws,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_adamw(void *const *params, const int32_t *param_dtype, const void *const *grads,
+                       const int32_t *grad_dtype, float *const *exp_avg, float *const *exp_avg_sq,
+                       float *const *masters, const int64_t *numel, int32_t n, const moe_adamw_cfg_t *cfg,
+                       const float *lr, int32_t *step, float *norm, void *ws, size_t ws_bytes, void *stream) {
+    if (cfg == nullptr || lr == nullptr || step == nullptr) return MOE_ERR_INVALID_ARG;
+    if (!(cfg->beta1 >= 0.0f && cfg->beta1 < 1.0f && cfg->beta2 >= 0.0f && cfg->beta2 < 1.0f && cfg->eps >= 0.0f &&
+          cfg->max_norm >= 0.0f))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned_to(lr, 4) || !aligned_to(step, 4) || !aligned_to(norm, 4)) return MOE_ERR_INVALID_ARG;
+    if (n > 0 && (param_dtype == nullptr || grad_dtype == nullptr)) return MOE_ERR_INVALID_ARG;
+    const void *const *lists[] = {params, grads, reinterpret_cast<const void *const *>(exp_avg),
+                                  reinterpret_cast<const void *const *>(exp_avg_sq),
+                                  reinterpret_cast<const void *const *>(masters)};
+    const int32_t *types[] = {param_dtype, grad_dtype, nullptr, nullptr, nullptr};
+    moe_status_t r = MOE_OK;
+    for (int i = 0; i < (masters != nullptr ? 5 : 4); ++i)
+        if ((r = check_list(lists[i], numel, types[i], n, i == 4)) != MOE_OK) return r;
+    if ((r = check_list_ws(ws, ws_bytes, n)) != MOE_OK) return r;
+    DeviceState *d = nullptr;
+    if ((r = device_state(&d)) != MOE_OK) return r;
+    AdamwLaunch p{};
+    p.params = {params, numel, param_dtype, n};
+    p.grads = {grads, numel, grad_dtype, n};
+    p.exp_avg = reinterpret_cast<void *const *>(exp_avg);
+    p.exp_avg_sq = reinterpret_cast<void *const *>(exp_avg_sq);
+    p.masters = reinterpret_cast<void *const *>(masters);
+    p.beta1 = cfg->beta1;
+    p.beta2 = cfg->beta2;
+    p.eps = cfg->eps;
+    p.weight_decay = cfg->weight_decay;
+    p.max_norm = cfg->max_norm;
+    p.skip_nonfinite = cfg->skip_nonfinite;
+    p.lr = lr;
+    p.step = step;
+    p.norm = norm;
+    p.ws = ws;
+    return cuda_status(launch_adamw(p, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,507 @@
+// multi_tensor.cu -- the end of a training step, over lists of tensors of any sizes
+// and types: the global gradient norm, clipping by it, and the AdamW update.
+//
+//   norm = sqrt(sum x^2), sum |x| or max |x| over every element of every tensor
+//   f    = min(1, max_norm / (norm + 1e-6)),  x <- f x
+//   AdamW, step t:  g = f grad,  m <- b1 m + (1 - b1) g,  v <- b2 v + (1 - b2) g^2
+//                   p <- p - lr (wd p + (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps))
+//
+// Lists reach the device in the kernels' arguments (pointers, sizes and types), so a
+// call copies nothing, keeps nothing and can be captured into a graph. Tensors are cut
+// into chunks; block b takes chunks b, b + grid, ...: the same sums on every call.
+//
+// All three are bound by HBM. The norm reads each element once. Clipping reads and
+// writes each once more, from the last chunk backwards, so that it starts on what the
+// norm has left in L2, and does nothing where f is 1. AdamW takes f as it reads the
+// gradients, which saves that pass.
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "internal.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxGrid = 152 * 6;
+constexpr int64_t kChunk = 16384;           // elements of a chunk
+constexpr int64_t kAdamChunk = 4096;
+
+template <int N>
+struct Table {                              // one pointer a tensor
+    void *ptr[N];
+    int64_t numel[N];
+    int32_t first[N + 1];                   // first chunk
+    uint8_t dtype[N];
+    int n;
+};
+template <int N>
+struct AdamTable {
+    void *p[N], *g[N], *m[N], *v[N], *x[N];
+    int64_t numel[N];
+    int32_t first[N + 1];
+    uint8_t p_dtype[N], g_dtype[N];
+    int n;
+};
+// a short list is launched with a short argument block: 64 tensors are 1.4 KB, 1000 are 21 KB
+constexpr int kShort = 64, kLong = 1000, kAdamShort = 64, kAdamLong = 560;
+static_assert(sizeof(Table<kLong>) < 32000 && sizeof(AdamTable<kAdamLong>) < 32000, "kernel arguments");
+
+// Header of the scratch: what the update reads.
+struct Hyper {
+    float norm, factor, lr, inv_c1, inv_c2;
+    int skip;
+};
+constexpr size_t kHeader = 256;
+
+__device__ __forceinline__ int find_tensor(const int32_t *first, int n, int c) {
+    int lo = 0, hi = n - 1;                 // the last tensor with first <= c
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= c) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ float widen(uint32_t bits16, int dtype) {
+    return dtype == MOE_DTYPE_BF16 ? __uint_as_float(bits16 << 16)
+                                   : __half2float(__ushort_as_half(static_cast<unsigned short>(bits16)));
+}
+__device__ __forceinline__ uint32_t narrow(float v, int dtype) {
+    return dtype == MOE_DTYPE_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+__device__ __forceinline__ float load_elem(const void *p, int dtype, int64_t i) {
+    return dtype == MOE_DTYPE_F32 ? static_cast<const float *>(p)[i]
+                                  : widen(static_cast<const unsigned short *>(p)[i], dtype);
+}
+__device__ __forceinline__ void store_elem(void *p, int dtype, int64_t i, float v) {
+    if (dtype == MOE_DTYPE_F32) static_cast<float *>(p)[i] = v;
+    else static_cast<unsigned short *>(p)[i] = static_cast<unsigned short>(narrow(v, dtype));
+}
+
+// The elements of chunk c of a tensor: a body of whole 16-byte vectors
+// [v0, v1) (in vectors from `body`), and for the first chunk the elements before
+// and after the body.
+struct Span {
+    int64_t head, v0, v1, tail0, tail1;
+};
+__device__ __forceinline__ Span span_of(const void *ptr, int64_t numel, int size, int64_t c) {
+    const int per = 16 / size;
+    Span s;
+    const int64_t mis = (16 - (reinterpret_cast<uintptr_t>(ptr) & 15)) & 15;
+    s.head = min(numel, mis / size);
+    const int64_t vecs = (numel - s.head) / per;
+    s.v0 = min(vecs, c * (kChunk / per));
+    s.v1 = min(vecs, (c + 1) * (kChunk / per));
+    s.tail0 = s.head + vecs * per;
+    s.tail1 = numel;
+    return s;
+}
+
+// Running value of the norm. Squares are added in fp32 over 64 elements and folded
+// into 64 bits; where those 64 left fp32's comfortable range (all below 1e-12, or
+// some above 1e15) they are added again, scaled by a power of two.
+template <int kType>
+struct Sum {
+    double acc = 0.0;
+    uint32_t top = 0;                       // max |x| as bits: NaN is above everything
+    __device__ __forceinline__ void fold(const float *x, int n) {
+        if constexpr (kType == MOE_NORM_INF) {
+#pragma unroll
+            for (int i = 0; i < n; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+        } else {
+            float q[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                if constexpr (kType == MOE_NORM_2) q[i & 3] = fmaf(x[i], x[i], q[i & 3]);
+                else q[i & 3] += fabsf(x[i]);
+            }
+            const float s = (q[0] + q[1]) + (q[2] + q[3]);
+            if (s > 1e-24f && s < 1e30f) acc += static_cast<double>(s);
+            else if (s != 0.0f || kType == MOE_NORM_2) acc += scaled(x, n, s);
+        }
+    }
+    __device__ __forceinline__ double scaled(const float *x, int n, float s) const {
+        const float f = s < 1.0f ? 0x1p96f : 0x1p-96f;
+        float q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float y = x[i] * f;
+            q += kType == MOE_NORM_2 ? y * y : fabsf(y);
+        }
+        const double back = s < 1.0f ? 0x1p-96 : 0x1p96;
+        return static_cast<double>(q) * (kType == MOE_NORM_2 ? back * back : back);
+    }
+    __device__ __forceinline__ void join(double a, uint32_t t) {
+        acc += a;
+        top = max(top, t);
+    }
+};
+
+template <int kType>
+__device__ __forceinline__ double block_value(Sum<kType> s) {
+    __shared__ double part[kThreads / 32];
+    __shared__ uint32_t part_top[kThreads / 32];
+    if constexpr (kType == MOE_NORM_INF) {
+        s.top = __reduce_max_sync(0xffffffffu, s.top);
+    } else {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) s.acc += __shfl_xor_sync(0xffffffffu, s.acc, off);
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) {
+        part[threadIdx.x >> 5] = s.acc;
+        part_top[threadIdx.x >> 5] = s.top;
+    }
+    __syncthreads();
+    Sum<kType> t;
+    for (int i = 0; i < kThreads / 32; ++i) t.join(part[i], part_top[i]);
+    if constexpr (kType == MOE_NORM_INF) return static_cast<double>(__uint_as_float(t.top));
+    return t.acc;
+}
+
+constexpr int kBatch = 8;                   // 16-byte loads of a thread in flight
+
+template <int kType, int N>
+__global__ void __launch_bounds__(kThreads)
+norm_kernel(const __grid_constant__ Table<N> tab, double *__restrict__ part) {
+    griddep_wait();
+    Sum<kType> sum;
+    const int chunks = tab.first[tab.n];
+    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const int i = find_tensor(tab.first, tab.n, c);
+        const int dtype = tab.dtype[i];
+        const int size = dtype == MOE_DTYPE_F32 ? 4 : 2;
+        const int64_t cc = c - tab.first[i];
+        const Span s = span_of(tab.ptr[i], tab.numel[i], size, cc);
+        const uint4 *body = reinterpret_cast<const uint4 *>(static_cast<const char *>(tab.ptr[i]) + s.head * size);
+        for (int64_t v = s.v0 + threadIdx.x; v < s.v1; v += kThreads * kBatch) {
+            uint4 r[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                r[j] = v + j * kThreads < s.v1 ? __ldg(body + v + j * kThreads) : make_uint4(0u, 0u, 0u, 0u);
+            if (dtype == MOE_DTYPE_F32) {
+                float x[4 * kBatch];
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    x[4 * j] = __uint_as_float(r[j].x);
+                    x[4 * j + 1] = __uint_as_float(r[j].y);
+                    x[4 * j + 2] = __uint_as_float(r[j].z);
+                    x[4 * j + 3] = __uint_as_float(r[j].w);
+                }
+                sum.fold(x, 4 * kBatch);
+            } else {
+                float x[8 * kBatch];
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        x[8 * j + 2 * q] = widen(w[q] & 0xffffu, dtype);
+                        x[8 * j + 2 * q + 1] = widen(w[q] >> 16, dtype);
+                    }
+                }
+                sum.fold(x, 8 * kBatch);
+            }
+        }
+        if (cc == 0) {
+            for (int64_t e = threadIdx.x; e < s.head + (s.tail1 - s.tail0); e += kThreads) {
+                const float x[1] = {load_elem(tab.ptr[i], dtype, e < s.head ? e : s.tail0 + (e - s.head))};
+                sum.fold(x, 1);
+            }
+        }
+    }
+    const double v = block_value<kType>(sum);
+    if (threadIdx.x == 0) part[blockIdx.x] = v;
+}
+
+// The norm from the blocks' values, in order; the same in every block that asks.
+template <int kType>
+__device__ __forceinline__ float total_norm(const double *__restrict__ part, int n) {
+    Sum<kType> s;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const double v = __ldcg(part + i);
+        if constexpr (kType == MOE_NORM_INF) s.join(0.0, __float_as_uint(static_cast<float>(v)));
+        else s.join(v, 0u);
+    }
+    const double v = block_value<kType>(s);
+    return static_cast<float>(kType == MOE_NORM_2 ? sqrt(v) : v);
+}
+
+// max_norm / (norm + 1e-6), at most 1; NaN stays NaN
+__device__ __forceinline__ float clip_factor(float norm, float max_norm) {
+    const float f = max_norm / (norm + 1e-6f);
+    return f > 1.0f ? 1.0f : f;
+}
+
+template <int kType>
+__global__ void __launch_bounds__(kThreads)
+norm_total_kernel(const double *__restrict__ part, int n, float *__restrict__ norm) {
+    griddep_wait();
+    const float v = total_norm<kType>(part, n);
+    if (threadIdx.x == 0) *norm = v;
+}
+
+template <int kType, int N>
+__global__ void __launch_bounds__(kThreads)
+clip_kernel(const __grid_constant__ Table<N> tab, const double *__restrict__ part, int n_part, float max_norm,
+            float *__restrict__ norm) {
+    griddep_wait();
+    const float total = total_norm<kType>(part, n_part);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
+    const float f = clip_factor(total, max_norm);
+    if (f == 1.0f) return;                  // x * 1 = x
+    const int chunks = tab.first[tab.n];
+    for (int c = chunks - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
+        const int i = find_tensor(tab.first, tab.n, c);
+        const int dtype = tab.dtype[i];
+        const int size = dtype == MOE_DTYPE_F32 ? 4 : 2;
+        const int64_t cc = c - tab.first[i];
+        const Span s = span_of(tab.ptr[i], tab.numel[i], size, cc);
+        uint4 *body = reinterpret_cast<uint4 *>(static_cast<char *>(tab.ptr[i]) + s.head * size);
+        for (int64_t v = s.v0 + threadIdx.x; v < s.v1; v += kThreads * kBatch) {
+            uint4 r[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (v + j * kThreads < s.v1) r[j] = body[v + j * kThreads];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (v + j * kThreads >= s.v1) continue;
+                uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (dtype == MOE_DTYPE_F32)
+                        w[q] = __float_as_uint(__uint_as_float(w[q]) * f);
+                    else
+                        w[q] = narrow(widen(w[q] & 0xffffu, dtype) * f, dtype) |
+                               narrow(widen(w[q] >> 16, dtype) * f, dtype) << 16;
+                }
+                body[v + j * kThreads] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        if (cc == 0) {
+            for (int64_t k = threadIdx.x; k < s.head + (s.tail1 - s.tail0); k += kThreads) {
+                const int64_t e = k < s.head ? k : s.tail0 + (k - s.head);
+                store_elem(tab.ptr[i], dtype, e, load_elem(tab.ptr[i], dtype, e) * f);
+            }
+        }
+    }
+}
+
+// Once a step, before the update: the norm and factor, the step count and its
+// bias corrections (64 bits: 1 - b^t loses half of fp32's digits at small t).
+__global__ void __launch_bounds__(kThreads)
+adamw_begin_kernel(const double *__restrict__ part, int n_part, float max_norm, float beta1, float beta2,
+                   int skip_nonfinite, const float *__restrict__ lr, int32_t *__restrict__ step,
+                   float *__restrict__ norm, Hyper *__restrict__ hyper) {
+    griddep_wait();
+    const float total = n_part > 0 ? total_norm<MOE_NORM_2>(part, n_part) : 0.0f;
+    if (threadIdx.x != 0) return;
+    Hyper h;
+    h.norm = total;
+    h.factor = n_part > 0 && max_norm > 0.0f ? clip_factor(total, max_norm) : 1.0f;
+    h.skip = skip_nonfinite && !isfinite(total);
+    h.lr = *lr;
+    const int t = *step + 1;
+    h.inv_c1 = static_cast<float>(1.0 / (1.0 - pow(static_cast<double>(beta1), static_cast<double>(t))));
+    h.inv_c2 = static_cast<float>(1.0 / (1.0 - pow(static_cast<double>(beta2), static_cast<double>(t))));
+    if (!h.skip) *step = t;
+    if (norm != nullptr && n_part > 0) *norm = total;
+    *hyper = h;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads)
+adamw_kernel(const __grid_constant__ AdamTable<N> tab, const Hyper *__restrict__ hyper, float beta1, float beta2,
+             float eps, float weight_decay) {
+    griddep_wait();
+    const Hyper h = *hyper;
+    if (h.skip) return;
+    const int chunks = tab.first[tab.n];
+    for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const int i = find_tensor(tab.first, tab.n, c);
+        const int64_t e0 = (c - tab.first[i]) * kAdamChunk;
+        const int64_t e1 = min(tab.numel[i], e0 + kAdamChunk);
+        const int pt = tab.p_dtype[i], gt = tab.g_dtype[i];
+        float *m = static_cast<float *>(tab.m[i]), *v = static_cast<float *>(tab.v[i]);
+        float *x = static_cast<float *>(tab.x[i]);
+        constexpr int kU = 4;
+        for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads * kU) {
+            float gr[kU], mr[kU], vr[kU], pr[kU];
+#pragma unroll
+            for (int j = 0; j < kU; ++j) {
+                const int64_t a = e + j * kThreads;
+                if (a >= e1) continue;
+                gr[j] = load_elem(tab.g[i], gt, a);
+                mr[j] = m[a];
+                vr[j] = v[a];
+                pr[j] = x != nullptr ? x[a] : load_elem(tab.p[i], pt, a);
+            }
+#pragma unroll
+            for (int j = 0; j < kU; ++j) {
+                const int64_t a = e + j * kThreads;
+                if (a >= e1) continue;
+                const float g = gr[j] * h.factor;
+                const float mn = beta1 * mr[j] + (1.0f - beta1) * g;
+                const float vn = beta2 * vr[j] + (1.0f - beta2) * g * g;
+                const float u = mn * h.inv_c1 / (sqrtf(vn * h.inv_c2) + eps);
+                const float pn = pr[j] - h.lr * (weight_decay * pr[j] + u);
+                m[a] = mn;
+                v[a] = vn;
+                if (x != nullptr) x[a] = pn;
+                store_elem(tab.p[i], pt, a, pn);
+            }
+        }
+    }
+}
+
+int64_t chunks_of(int64_t numel, int64_t chunk) { return (numel + chunk - 1) / chunk; }
+int grid_of(int64_t chunks) { return static_cast<int>(chunks < 1 ? 1 : chunks < kMaxGrid ? chunks : kMaxGrid); }
+
+// The list as tables of at most N tensors: f(table, index of the table) for each.
+template <int N, typename F>
+cudaError_t for_tables(const TensorList &l, F f) {
+    static_assert(std::is_trivially_copyable<Table<N>>::value, "passed as an argument");
+    int at = 0, index = 0;
+    do {
+        Table<N> t;
+        t.n = 0;
+        int64_t first = 0;
+        while (at < l.n && t.n < N) {
+            if (l.numel[at] > 0) {
+                t.ptr[t.n] = const_cast<void *>(l.ptr[at]);
+                t.numel[t.n] = l.numel[at];
+                t.dtype[t.n] = static_cast<uint8_t>(l.dtype[at]);
+                t.first[t.n] = static_cast<int32_t>(first);
+                first += chunks_of(l.numel[at], kChunk);
+                ++t.n;
+            }
+            ++at;
+        }
+        t.first[t.n] = static_cast<int32_t>(first);
+        const cudaError_t e = f(t, index++);
+        if (e != cudaSuccess) return e;
+    } while (at < l.n);
+    return cudaSuccess;
+}
+
+double *partials(void *ws) { return reinterpret_cast<double *>(static_cast<char *>(ws) + kHeader); }
+
+template <int kType, int N>
+cudaError_t norm_parts(const TensorList &l, void *ws, int *n_part, cudaStream_t st) {
+    *n_part = 0;
+    return for_tables<N>(l, [&](const Table<N> &t, int) {
+        const int grid = grid_of(t.first[t.n]);
+        const cudaError_t e = launch_dep(norm_kernel<kType, N>, dim3(grid), dim3(kThreads), 0, st, t, partials(ws) + *n_part);
+        note_launches(1);
+        *n_part += grid;
+        return e;
+    });
+}
+
+template <int kType, int N>
+cudaError_t clip_parts(const TensorList &l, float max_norm, float *norm, void *ws, int n_part, cudaStream_t st) {
+    return for_tables<N>(l, [&](const Table<N> &t, int) {
+        const cudaError_t e = launch_dep(clip_kernel<kType, N>, dim3(grid_of(t.first[t.n])), dim3(kThreads), 0, st, t,
+                                         static_cast<const double *>(partials(ws)), n_part, max_norm, norm);
+        note_launches(1);
+        return e;
+    });
+}
+
+template <int kType>
+cudaError_t norm_typed(const TensorList &l, void *ws, int *n_part, cudaStream_t st) {
+    return l.n <= kShort ? norm_parts<kType, kShort>(l, ws, n_part, st) : norm_parts<kType, kLong>(l, ws, n_part, st);
+}
+
+template <typename F>
+cudaError_t with_norm_type(int type, F f) {
+    if (type == MOE_NORM_1) return f(std::integral_constant<int, MOE_NORM_1>{});
+    if (type == MOE_NORM_2) return f(std::integral_constant<int, MOE_NORM_2>{});
+    return f(std::integral_constant<int, MOE_NORM_INF>{});
+}
+
+template <int N>
+cudaError_t adamw_tables(const AdamwLaunch &p, cudaStream_t st) {
+    int at = 0;
+    do {
+        AdamTable<N> t;
+        t.n = 0;
+        int64_t first = 0;
+        while (at < p.params.n && t.n < N) {
+            if (p.params.numel[at] > 0) {
+                t.p[t.n] = const_cast<void *>(p.params.ptr[at]);
+                t.g[t.n] = const_cast<void *>(p.grads.ptr[at]);
+                t.m[t.n] = p.exp_avg[at];
+                t.v[t.n] = p.exp_avg_sq[at];
+                t.x[t.n] = p.masters != nullptr ? p.masters[at] : nullptr;
+                t.numel[t.n] = p.params.numel[at];
+                t.p_dtype[t.n] = static_cast<uint8_t>(p.params.dtype[at]);
+                t.g_dtype[t.n] = static_cast<uint8_t>(p.grads.dtype[at]);
+                t.first[t.n] = static_cast<int32_t>(first);
+                first += chunks_of(p.params.numel[at], kAdamChunk);
+                ++t.n;
+            }
+            ++at;
+        }
+        t.first[t.n] = static_cast<int32_t>(first);
+        if (t.n == 0) continue;
+        const cudaError_t e =
+            launch_dep(adamw_kernel<N>, dim3(grid_of(first)), dim3(kThreads), 0, st, t,
+                       static_cast<const Hyper *>(p.ws), p.beta1, p.beta2, p.eps, p.weight_decay);
+        note_launches(1);
+        if (e != cudaSuccess) return e;
+    } while (at < p.params.n);
+    return cudaSuccess;
+}
+
+}  // namespace
+
+size_t multi_tensor_ws_bytes(int64_t n) {
+    const int64_t tables = n <= kShort ? 1 : (n + kLong - 1) / kLong;
+    return kHeader + static_cast<size_t>(tables) * kMaxGrid * sizeof(double);
+}
+
+cudaError_t launch_grad_norm(const TensorList &grads, int norm_type, float *norm, void *ws, cudaStream_t st) {
+    return with_norm_type(norm_type, [&](auto type) {
+        constexpr int kType = decltype(type)::value;
+        int n_part = 0;
+        cudaError_t e = norm_typed<kType>(grads, ws, &n_part, st);
+        if (e != cudaSuccess) return e;
+        e = launch_dep(norm_total_kernel<kType>, dim3(1), dim3(kThreads), 0, st,
+                       static_cast<const double *>(partials(ws)), n_part, norm);
+        note_launches(1);
+        return e;
+    });
+}
+
+cudaError_t launch_clip_grads(const TensorList &grads, int norm_type, float max_norm, float *norm, void *ws,
+                              cudaStream_t st) {
+    return with_norm_type(norm_type, [&](auto type) {
+        constexpr int kType = decltype(type)::value;
+        int n_part = 0;
+        const cudaError_t e = norm_typed<kType>(grads, ws, &n_part, st);
+        if (e != cudaSuccess) return e;
+        return grads.n <= kShort ? clip_parts<kType, kShort>(grads, max_norm, norm, ws, n_part, st)
+                                 : clip_parts<kType, kLong>(grads, max_norm, norm, ws, n_part, st);
+    });
+}
+
+cudaError_t launch_adamw(const AdamwLaunch &p, cudaStream_t st) {
+    int n_part = 0;
+    cudaError_t e = cudaSuccess;
+    if (p.norm != nullptr || p.max_norm > 0.0f || p.skip_nonfinite) {
+        e = norm_typed<MOE_NORM_2>(p.grads, p.ws, &n_part, st);
+        if (e != cudaSuccess) return e;
+    }
+    e = launch_dep(adamw_begin_kernel, dim3(1), dim3(kThreads), 0, st, static_cast<const double *>(partials(p.ws)), n_part,
+                   p.max_norm, p.beta1, p.beta2, p.skip_nonfinite, p.lr, p.step, p.norm, static_cast<Hyper *>(p.ws));
+    note_launches(1);
+    if (e != cudaSuccess) return e;
+    return p.params.n <= kAdamShort ? adamw_tables<kAdamShort>(p, st) : adamw_tables<kAdamLong>(p, st);
+}
+
+}  // namespace moe

@@ -1,0 +1,924 @@
+// route.cu -- the trainable router: selection from given logits with its balance
+// terms, the backward of both, and the update of the selection bias.
+//
+// Forward, for token t with logits l (fp32, bf16 or fp16, converted to fp32):
+//   expert e is off when l[e] = -inf; a token is live when its mask is set and not
+//   all experts are off
+//   s   = softmax(l) or sigmoid(l)
+//   key = l without a selection bias (s increases with l), else s + bias
+//   K   = the k best keys of the kept groups, ties to the lower index
+//   w   = s_K / (sum_K s + 1e-20) * scale, or s_K * scale
+// and for sequence b (n_b live tokens, c_be slots on expert e)
+//   balance = 1/S' sum_b sum_e E c_be / (k n_b) P_be,  P_be = 1/n_b sum_t s[t,e] / (sum s[t,:] + 1e-20)
+//   z       = 1/N sum_t log(sum_e exp(l[t,e]))^2
+//
+// A token is held by G lanes of a warp, lane i keeping experts i V .. i V + V - 1 in
+// registers, so that index order is lane order and ties need no compare of indices.
+// The k best are taken in k rounds: every lane keeps the best of its own keys, a
+// round is one maximum over the lanes (redux on whole warps), one ballot, and the
+// winner alone looks its key up, clears it and finds its next best.
+//
+// Keys that pass through exp carry an error of some 1e-7, and two experts nearer
+// than that would be chosen by rounding. Neighbouring chosen keys (and the last
+// kept and first dropped group) are compared with the bound of that error, and the
+// rare token that falls below it (about one in a thousand) is selected again in 64 bits.
+//
+// Statistics are sums without float atomics: a block keeps its tokens' score sums
+// in registers and its counts in shared memory, and writes them to a slot of its
+// own at the end of each sequence it meets (slot = block + sequence: consecutive
+// (block, sequence) pairs never share one); route_reduce_kernel adds the slots of a
+// sequence in a fixed order, so every output has the same bits on every call.
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "internal.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxK = 32;
+constexpr int kMaxGroups = 32;
+constexpr float kEps = 1e-20f;
+// bounds of the relative error of a 32-bit score: sigmoid is one exp (2 ulp), an
+// addition and a division; softmax adds the rounding of l - max and a sum of up to 1024 terms
+constexpr float kSigmoidErr = 5e-7f;
+constexpr float kSoftmaxErr = 4e-6f;
+
+__device__ __forceinline__ float from_bits16(uint32_t v, int dtype) {
+    if (dtype == MOE_DTYPE_BF16) return __uint_as_float(v << 16);
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(v)));
+}
+
+__device__ __forceinline__ float load_one(const void *p, int dtype, int64_t i) {
+    if (dtype == MOE_DTYPE_F32) return __ldg(static_cast<const float *>(p) + i);
+    return from_bits16(__ldg(static_cast<const unsigned short *>(p) + i), dtype);
+}
+
+// Experts e0 .. e0 + V - 1 of the row at element `row`; -inf past E. `vec`: the rows
+// are 16-byte aligned.
+template <int V>
+__device__ __forceinline__ void load_experts(const void *p, int dtype, int vec, int64_t row, int e0, int E,
+                                             float (&l)[V]) {
+    if (vec && e0 + V <= E) {
+        if (dtype == MOE_DTYPE_F32) {
+            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + row + e0);
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) {
+                const float4 x = __ldg(q + i);
+                l[4 * i] = x.x;
+                l[4 * i + 1] = x.y;
+                l[4 * i + 2] = x.z;
+                l[4 * i + 3] = x.w;
+            }
+        } else {
+            const uint2 *q = reinterpret_cast<const uint2 *>(static_cast<const unsigned short *>(p) + row + e0);
+            uint2 x[V / 4];
+            if constexpr (V >= 8) {
+#pragma unroll
+                for (int i = 0; i < V / 8; ++i) {
+                    const uint4 y = __ldg(reinterpret_cast<const uint4 *>(q) + i);
+                    x[2 * i] = make_uint2(y.x, y.y);
+                    x[2 * i + 1] = make_uint2(y.z, y.w);
+                }
+            } else {
+                x[0] = __ldg(q);
+            }
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) {
+                l[4 * i] = from_bits16(x[i].x & 0xffffu, dtype);
+                l[4 * i + 1] = from_bits16(x[i].x >> 16, dtype);
+                l[4 * i + 2] = from_bits16(x[i].y & 0xffffu, dtype);
+                l[4 * i + 3] = from_bits16(x[i].y >> 16, dtype);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = e0 + i < E ? load_one(p, dtype, row + e0 + i) : -INFINITY;
+}
+
+// A float's bits in an order that unsigned compares keep; 0 is below every number.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t u = __float_as_uint(v + 0.0f);       // -0 and 0 tie
+    return v != v ? 0u : ((u >> 31) ? ~u : (u | 0x80000000u));
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float((k >> 31) ? (k & 0x7fffffffu) : ~k);
+}
+
+template <int G, typename F, typename X>
+__device__ __forceinline__ X lanes_reduce(unsigned mask, X v, F f) {
+#pragma unroll
+    for (int off = G / 2; off > 0; off >>= 1) v = f(v, __shfl_xor_sync(mask, v, off));
+    return v;
+}
+template <int G>
+__device__ __forceinline__ float lanes_sum(unsigned mask, float v) {
+    return lanes_reduce<G>(mask, v, [](float a, float b) { return a + b; });
+}
+template <int G>
+__device__ __forceinline__ float lanes_max(unsigned mask, float v) {
+    return lanes_reduce<G>(mask, v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int G>
+__device__ __forceinline__ uint32_t lanes_max_u32(unsigned mask, uint32_t v) {
+    if constexpr (G == 32) return __reduce_max_sync(0xffffffffu, v);
+    return lanes_reduce<G>(mask, v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+
+// The selection's scratch of one token.
+template <int G, int V>
+struct Slots {
+    int idx[kThreads / G][kMaxK + 1];
+    float s[kThreads / G][kMaxK + 1];
+    float sel[kThreads / G][kMaxK + 1];
+    double group[kThreads / G][kMaxGroups];
+};
+
+// One token's selection in 64 bits, from its logits in memory.
+template <int G, int V>
+__device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int sub, unsigned gmask, int *out_idx,
+                                         float *out_s, double *group) {
+    const int e0 = sub * V;
+    double s[V], sel[V];
+    double top = -INFINITY;
+    for (int i = 0; i < V; ++i) {
+        s[i] = e0 + i < p.E ? static_cast<double>(load_one(p.logits, p.dtype, row + e0 + i)) : -INFINITY;
+        if (s[i] > top) top = s[i];
+    }
+    auto dmax = [](double a, double b) { return a > b ? a : b; };
+    top = lanes_reduce<G>(gmask, top, dmax);
+    double z = 0.0;
+    unsigned open = 0;                              // experts that may still be chosen
+    for (int i = 0; i < V; ++i) {
+        if (s[i] > -INFINITY) open |= 1u << i;
+        sel[i] = s[i];
+        if (p.score_fn == MOE_SCORE_SOFTMAX) {
+            s[i] = s[i] == -INFINITY ? 0.0 : exp(s[i] - top);
+            z += s[i];
+        } else {
+            s[i] = s[i] == -INFINITY ? 0.0 : 1.0 / (1.0 + exp(-s[i]));
+        }
+    }
+    if (p.score_fn == MOE_SCORE_SOFTMAX) {
+        z = lanes_reduce<G>(gmask, z, [](double a, double b) { return a + b; });
+        for (int i = 0; i < V; ++i) s[i] /= z;
+    }
+    auto with_bias = [&](int i) {
+        return s[i] + (p.sel_bias != nullptr ? static_cast<double>(__ldg(p.sel_bias + e0 + i)) : 0.0);
+    };
+    if (p.n_group > 1) {
+        const int gs = p.E / p.n_group;
+        for (int g = 0; g < p.n_group; ++g) {
+            double pv = INFINITY, total = -INFINITY;
+            int pi = -1;
+            for (int n = 0; n < p.group_topn; ++n) {
+                double bv = -INFINITY;
+                int bi = 0x7fffffff;
+                for (int i = 0; i < V; ++i) {
+                    const int e = e0 + i;
+                    if (!((open >> i) & 1u) || e / gs != g) continue;
+                    const double v = with_bias(i);
+                    if (!(v < pv || (v == pv && e > pi))) continue;
+                    if (v > bv || (v == bv && e < bi)) {
+                        bv = v;
+                        bi = e;
+                    }
+                }
+                for (int off = G / 2; off > 0; off >>= 1) {
+                    const double ov = __shfl_xor_sync(gmask, bv, off);
+                    const int oi = __shfl_xor_sync(gmask, bi, off);
+                    if (ov > bv || (ov == bv && oi < bi)) {
+                        bv = ov;
+                        bi = oi;
+                    }
+                }
+                if (bi == 0x7fffffff) break;
+                total = n == 0 ? bv : total + bv;
+                pv = bv;
+                pi = bi;
+            }
+            if (sub == 0) group[g] = total;
+        }
+        __syncwarp(gmask);
+        for (int i = 0; i < V; ++i) {
+            if (!((open >> i) & 1u)) continue;
+            const int g = (e0 + i) / gs;
+            const double mine = group[g];
+            int before = 0;
+            for (int o = 0; o < p.n_group; ++o) before += group[o] > mine || (group[o] == mine && o < g);
+            if (before >= p.topk_group) open &= ~(1u << i);
+        }
+        __syncwarp(gmask);
+    }
+    if (p.sel_bias != nullptr)
+        for (int i = 0; i < V; ++i)
+            if ((open >> i) & 1u) sel[i] = with_bias(i);
+    for (int j = 0; j < p.k; ++j) {
+        double bv = -INFINITY;
+        int bi = 0x7fffffff;
+        for (int i = 0; i < V; ++i)
+            if (((open >> i) & 1u) && (bi == 0x7fffffff || sel[i] > bv)) {
+                bv = sel[i];
+                bi = e0 + i;
+            }
+        for (int off = G / 2; off > 0; off >>= 1) {
+            const double ov = __shfl_xor_sync(gmask, bv, off);
+            const int oi = __shfl_xor_sync(gmask, bi, off);
+            if (ov > bv || (ov == bv && oi < bi)) {
+                bv = ov;
+                bi = oi;
+            }
+        }
+        if (bi == 0x7fffffff) {
+            if (sub == 0) {
+                out_idx[j] = -1;
+                out_s[j] = 0.0f;
+            }
+        } else if (bi >= e0 && bi < e0 + V) {
+            out_idx[j] = bi;
+            out_s[j] = static_cast<float>(s[bi - e0]);
+            open &= ~(1u << (bi - e0));
+        }
+    }
+    __syncwarp(gmask);
+}
+
+// Tokens [per_block b, per_block (b + 1)) in block b, kThreads / G at a time.
+template <int G, int V, bool kStats>
+__global__ void __launch_bounds__(kThreads)
+route_kernel(const RouteLaunch p) {
+    constexpr int kRows = kThreads / G;
+    __shared__ Slots<G, V> slots;
+    __shared__ float buf[kRows * G * V];
+    __shared__ int hist[kStats ? G * V : 1];
+    __shared__ float red_z[kRows];
+    __shared__ int red_n[kRows];
+    griddep_wait();
+    const int row = threadIdx.x / G, sub = threadIdx.x % G;
+    const int lane = threadIdx.x & 31;
+    const unsigned gmask = G == 32 ? 0xffffffffu : ((1u << G) - 1u) << (lane / G * G);
+    const int e0 = sub * V;
+    const int t_begin = blockIdx.x * p.per_block;
+    const int t_end = min(p.T, t_begin + p.per_block);
+    int seq = 0;
+    float acc[V];
+    float z_acc = 0.0f;
+    int n_acc = 0;
+    if constexpr (kStats) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+        for (int e = threadIdx.x; e < G * V; e += kThreads) hist[e] = 0;
+        for (int b = 1; b < p.S; b += kThreads) {
+            const int i = b + static_cast<int>(threadIdx.x);
+            seq += __syncthreads_count(i < p.S && __ldg(p.seq_offsets + i) <= t_begin);
+        }
+        __syncthreads();
+    }
+    int t = t_begin;
+    while (t < t_end) {
+        int seg_end = t_end;
+        if constexpr (kStats) {
+            while (seq < p.S - 1 && __ldg(p.seq_offsets + seq + 1) <= t) ++seq;
+            if (seq < p.S - 1) seg_end = min(t_end, __ldg(p.seq_offsets + seq + 1));
+        }
+        for (int base = t; base < seg_end; base += kRows) {
+            const int tok = base + row;
+            const bool inside = tok < seg_end;
+            const bool given = inside && (p.mask == nullptr || __ldg(p.mask + tok) != 0);
+            const int64_t lrow = static_cast<int64_t>(tok) * p.ld;
+            float l[V], s[V];
+            if (given) {
+                load_experts<V>(p.logits, p.dtype, p.vec, lrow, e0, p.E, l);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) l[i] = -INFINITY;
+            }
+            float top = -INFINITY;
+            unsigned on = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                top = fmaxf(top, l[i]);
+                on |= l[i] != -INFINITY ? 1u << i : 0u;
+            }
+            top = lanes_max<G>(gmask, top);
+            const bool live = (__ballot_sync(0xffffffffu, on != 0) & gmask) != 0;
+            // scores
+            float ssum = 0.0f, s_max = 1.0f;         // s_max: no score is above it
+            if (p.score_fn == MOE_SCORE_SOFTMAX) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    s[i] = (on >> i) & 1u ? expf(l[i] - top) : 0.0f;
+                    ssum += s[i];
+                }
+                ssum = lanes_sum<G>(gmask, ssum);
+                const float inv = 1.0f / (live ? ssum : 1.0f);
+                s_max = inv;
+#pragma unroll
+                for (int i = 0; i < V; ++i) s[i] *= inv;
+                if (kStats && live && sub == 0) {
+                    const float lse = top + logf(ssum);
+                    z_acc += lse * lse;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) s[i] = (on >> i) & 1u ? 1.0f / (1.0f + expf(-l[i])) : 0.0f;
+                if constexpr (kStats) {
+                    float ex = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        ssum += s[i];
+                        ex += (on >> i) & 1u ? expf(l[i] - top) : 0.0f;
+                    }
+                    ssum = lanes_sum<G>(gmask, ssum);
+                    ex = lanes_sum<G>(gmask, ex);
+                    if (live && sub == 0) {
+                        const float lse = top + logf(ex);
+                        z_acc += lse * lse;
+                    }
+                }
+            }
+            if constexpr (kStats) {
+                if (live) {
+                    const float share = p.score_fn == MOE_SCORE_SOFTMAX ? 1.0f : 1.0f / (ssum + kEps);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[i] += s[i] * share;
+                    n_acc += sub == 0;
+                }
+            }
+            // keys
+            const float rel = p.score_fn == MOE_SCORE_SOFTMAX ? kSoftmaxErr : kSigmoidErr;
+            const bool by_score = p.sel_bias != nullptr;
+            uint32_t key[V];
+            bool near = false;                       // nearer than the error of a 32-bit key
+            float bias[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                bias[i] = by_score && e0 + i < p.E ? __ldg(p.sel_bias + e0 + i) : 0.0f;
+                key[i] = (on >> i) & 1u ? order_key(by_score ? s[i] + bias[i] : l[i]) : 0u;
+            }
+            if (p.n_group > 1 && p.topk_group < p.n_group) {
+                // each group's sum of its group_topn best, one group a lane
+                const int gs = p.E / p.n_group;
+                float *sel_row = buf + row * G * V;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    sel_row[e0 + i] = (on >> i) & 1u ? s[i] + bias[i] : -INFINITY;
+                __syncwarp();
+                float *sums = reinterpret_cast<float *>(slots.group[row]);
+                float mag = 0.0f;                    // largest sum of magnitudes
+                for (int g = sub; g < p.n_group; g += G) {
+                    float pv = INFINITY, total = -INFINITY, size = 0.0f;
+                    int pi = -1;
+                    for (int n = 0; n < p.group_topn; ++n) {
+                        float bv = -INFINITY;
+                        int bi = -1;
+                        for (int i = 0; i < gs; ++i) {
+                            const float v = sel_row[g * gs + i];
+                            if ((v < pv || (v == pv && i > pi)) && v > bv) {
+                                bv = v;
+                                bi = i;
+                            }
+                        }
+                        if (bi < 0) break;
+                        total = n == 0 ? bv : total + bv;
+                        size += fabsf(bv);
+                        pv = bv;
+                        pi = bi;
+                    }
+                    sums[g] = total;
+                    mag = fmaxf(mag, size);
+                }
+                __syncwarp();
+                unsigned kept = 0;
+                float worst_kept = INFINITY, best_lost = -INFINITY;
+                for (int g = sub; g < p.n_group; g += G) {
+                    const float mine = sums[g];
+                    int before = 0;
+                    for (int o = 0; o < p.n_group; ++o) before += sums[o] > mine || (sums[o] == mine && o < g);
+                    if (before < p.topk_group) {
+                        kept |= 1u << g;
+                        worst_kept = fminf(worst_kept, mine);
+                    } else {
+                        best_lost = fmaxf(best_lost, mine);
+                    }
+                }
+                kept = lanes_reduce<G>(gmask, kept, [](unsigned a, unsigned b) { return a | b; });
+                worst_kept = -lanes_max<G>(gmask, -worst_kept);
+                best_lost = lanes_max<G>(gmask, best_lost);
+                mag = lanes_max<G>(gmask, mag);
+                near = worst_kept > -INFINITY && best_lost > -INFINITY &&
+                       worst_kept - best_lost <= static_cast<float>(p.group_topn) * (2.0f * rel * s_max + 1.2e-7f * mag);
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (e0 + i < p.E && !((kept >> ((e0 + i) / gs)) & 1u)) key[i] = 0u;
+            }
+            // k rounds (one more where the last chosen key is compared with the next)
+            uint32_t best = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) best = max(best, key[i]);
+            const int rounds = p.k + (by_score ? 1 : 0);
+            for (int j = 0; j < rounds; ++j) {
+                const uint32_t m = lanes_max_u32<G>(gmask, best);
+                const unsigned who = __ballot_sync(0xffffffffu, best == m) & gmask;
+                if (lane == __ffs(who) - 1) {
+                    int at = -1;
+                    float sv = 0.0f;
+                    if (m != 0) {
+#pragma unroll
+                        for (int i = V - 1; i >= 0; --i)
+                            if (key[i] == m) {
+                                at = i;
+                                sv = s[i];
+                            }
+                        best = 0;
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            if (i == at) key[i] = 0u;
+                            best = max(best, key[i]);
+                        }
+                    }
+                    slots.idx[row][j] = at < 0 ? -1 : e0 + at;
+                    slots.s[row][j] = sv;
+                    slots.sel[row][j] = key_value(m);
+                }
+            }
+            __syncwarp();
+            if (by_score) {
+                for (int j = sub; j < p.k; j += G) {
+                    const int a = slots.idx[row][j], b = slots.idx[row][j + 1];
+                    if (a < 0 || b < 0) continue;
+                    const float x = slots.sel[row][j], y = slots.sel[row][j + 1];
+                    const float bound = rel * (slots.s[row][j] + slots.s[row][j + 1]) + 1.2e-7f * (fabsf(x) + fabsf(y));
+                    if (x - y <= bound &&
+                        !(load_one(p.logits, p.dtype, lrow + a) == load_one(p.logits, p.dtype, lrow + b) &&
+                          __ldg(p.sel_bias + a) == __ldg(p.sel_bias + b)))
+                        near = true;
+                }
+            }
+            if (__ballot_sync(0xffffffffu, near) & gmask)
+                select_wide<G, V>(p, lrow, sub, gmask, slots.idx[row], slots.s[row], slots.group[row]);
+            __syncwarp();
+            // weights
+            float chosen = 0.0f;
+            for (int j = sub; j < p.k; j += G) chosen += slots.s[row][j];
+            chosen = lanes_sum<G>(gmask, chosen);
+            if (inside) {
+                for (int j = sub; j < p.k; j += G) {
+                    const int e = slots.idx[row][j];
+                    float w = slots.s[row][j];
+                    if (p.normalize) w = w / (chosen + kEps);
+                    p.topk_idx[static_cast<int64_t>(tok) * p.k + j] = e;
+                    p.topk_w[static_cast<int64_t>(tok) * p.k + j] = w * p.scale;
+                    if (kStats && e >= 0) atomicAdd(&hist[e], 1);
+                }
+            }
+            __syncwarp();
+        }
+        if constexpr (kStats) {
+            // this block's sums of the sequence, rows in order
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                buf[row * G * V + e0 + i] = acc[i];
+                acc[i] = 0.0f;
+            }
+            if (sub == 0) {
+                red_z[row] = z_acc;
+                red_n[row] = n_acc;
+            }
+            z_acc = 0.0f;
+            n_acc = 0;
+            __syncthreads();
+            const int64_t slot = static_cast<int64_t>(blockIdx.x) + seq;
+            for (int e = threadIdx.x; e < p.E; e += kThreads) {
+                float v = 0.0f;
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) v += buf[r * G * V + e];
+                p.part_score[slot * p.E + e] = v;
+                p.part_count[slot * p.E + e] = hist[e];
+                hist[e] = 0;
+            }
+            if (threadIdx.x == 0) {
+                float zz = 0.0f;
+                int n = 0;
+                for (int r = 0; r < kRows; ++r) {
+                    zz += red_z[r];
+                    n += red_n[r];
+                }
+                p.part_z[slot] = zz;
+                p.part_n[slot] = n;
+            }
+            __syncthreads();
+        }
+        t = seg_end;
+    }
+}
+
+// Counts, live tokens and the two terms from the slots. Block (32-expert chunk,
+// sequences blockIdx.y, + gridDim.y, ...): 16 rows of threads walk the sequence's
+// slots; the last block to finish adds the sequences' terms in order.
+constexpr int kReduceRows = 16;
+
+__global__ void __launch_bounds__(32 * kReduceRows)
+route_reduce_kernel(const RouteLaunch p) {
+    griddep_wait();
+    __shared__ float sh_s[kReduceRows][32];
+    __shared__ int sh_c[kReduceRows][32];
+    __shared__ float sh_z[kReduceRows];
+    __shared__ int sh_n[kReduceRows];
+    __shared__ int last;
+    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+    const int e = blockIdx.x * 32 + lane;
+    for (int q = blockIdx.y; q < p.S; q += gridDim.y) {
+        const int a = q > 0 ? max(0, min(p.T, __ldg(p.seq_offsets + q))) : 0;
+        const int z = q < p.S - 1 ? max(0, min(p.T, __ldg(p.seq_offsets + q + 1))) : p.T;
+        const int b0 = a / p.per_block, b1 = z > a ? (z - 1) / p.per_block : b0 - 1;
+        float s = 0.0f, zs = 0.0f;
+        int c = 0, n = 0;
+#pragma unroll 4
+        for (int b = b0 + row; b <= b1; b += kReduceRows) {
+            const int64_t slot = static_cast<int64_t>(b) + q;
+            if (e < p.E) {
+                s += __ldcg(p.part_score + slot * p.E + e);
+                c += __ldcg(p.part_count + slot * p.E + e);
+            }
+        }
+        for (int b = b0 + threadIdx.x; b <= b1; b += 32 * kReduceRows) {
+            n += __ldcg(p.part_n + b + q);
+            zs += __ldcg(p.part_z + b + q);
+        }
+        for (int off = 16; off > 0; off >>= 1) {
+            n += __shfl_xor_sync(0xffffffffu, n, off);
+            zs += __shfl_xor_sync(0xffffffffu, zs, off);
+        }
+        __syncthreads();
+        sh_s[row][lane] = s;
+        sh_c[row][lane] = c;
+        if (lane == 0) {
+            sh_z[row] = zs;
+            sh_n[row] = n;
+        }
+        __syncthreads();
+        if (row == 0) {
+            s = 0.0f;
+            c = 0;
+            zs = 0.0f;
+            n = 0;
+#pragma unroll
+            for (int r = 0; r < kReduceRows; ++r) {
+                s += sh_s[r][lane];
+                c += sh_c[r][lane];
+                zs += sh_z[r];
+                n += sh_n[r];
+            }
+            if (e < p.E) p.counts[static_cast<int64_t>(q) * p.E + e] = c;
+            const float nf = static_cast<float>(max(n, 1));
+            float term = (s / nf) * (static_cast<float>(c) / (nf * static_cast<float>(p.k)));
+            for (int off = 16; off > 0; off >>= 1) term += __shfl_xor_sync(0xffffffffu, term, off);
+            if (lane == 0) {
+                p.part_balance[static_cast<int64_t>(q) * gridDim.x + blockIdx.x] = term;
+                if (blockIdx.x == 0) {
+                    p.seq_tokens[q] = n;
+                    p.seq_z[q] = zs;
+                }
+            }
+        }
+    }
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last = atomicAdd(p.ticket, 1) == static_cast<int>(gridDim.x * gridDim.y) - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    float bal = 0.0f, zs = 0.0f;
+    int n = 0, used = 0;
+    const int64_t terms = static_cast<int64_t>(p.S) * gridDim.x;
+    for (int64_t i = threadIdx.x; i < terms; i += 32 * kReduceRows) bal += __ldcg(p.part_balance + i);
+    for (int q = threadIdx.x; q < p.S; q += 32 * kReduceRows) {
+        const int m = __ldcg(p.seq_tokens + q);
+        n += m;
+        used += m > 0;
+        zs += __ldcg(p.seq_z + q);
+    }
+    for (int off = 16; off > 0; off >>= 1) {
+        bal += __shfl_xor_sync(0xffffffffu, bal, off);
+        zs += __shfl_xor_sync(0xffffffffu, zs, off);
+        n += __shfl_xor_sync(0xffffffffu, n, off);
+        used += __shfl_xor_sync(0xffffffffu, used, off);
+    }
+    if (lane == 0) {
+        sh_s[0][row] = bal;
+        sh_z[row] = zs;
+        sh_n[row] = n;
+        sh_c[0][row] = used;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        bal = 0.0f;
+        zs = 0.0f;
+        n = 0;
+        used = 0;
+        for (int r = 0; r < kReduceRows; ++r) {
+            bal += sh_s[0][r];
+            zs += sh_z[r];
+            n += sh_n[r];
+            used += sh_c[0][r];
+        }
+        p.seq_tokens[p.S] = n;
+        p.seq_tokens[p.S + 1] = used;
+        p.losses[0] = static_cast<float>(p.E) * bal / static_cast<float>(max(used, 1));
+        p.losses[1] = zs / static_cast<float>(max(n, 1));
+    }
+}
+
+// Gradient of the logits. With gw the weights' gradient at the chosen scores (taken
+// through their normalisation), a_e = dbalance E c_be / (S' k n_b^2) that of the
+// shares and Z = sum s + 1e-20:
+//   softmax: dl = s (g - sum s g),  g = gw (chosen) + a
+//   sigmoid: dl = s (1 - s) (gw (chosen) + (a - sum s a / Z) / Z)
+// and dl += dz 2/N lse softmax(l). One pass: a token's logits are read, its scores
+// recomputed, its gradient written.
+template <int G, int V>
+__global__ void __launch_bounds__(kThreads)
+route_backward_kernel(const RouteBackwardLaunch p) {
+    constexpr int kRows = kThreads / G;
+    __shared__ float buf[kRows * G * V];
+    griddep_wait();
+    const int row = threadIdx.x / G, sub = threadIdx.x % G;
+    const int lane = threadIdx.x & 31;
+    const unsigned gmask = G == 32 ? 0xffffffffu : ((1u << G) - 1u) << (lane / G * G);
+    const int e0 = sub * V;
+    const int t_begin = blockIdx.x * p.per_block;
+    const int t_end = min(p.T, t_begin + p.per_block);
+    const bool terms = p.dlosses != nullptr;
+    float dbal = 0.0f, dz = 0.0f;
+    int seq = 0;
+    if (terms) {
+        dbal = __ldg(p.dlosses);
+        dz = 2.0f * __ldg(p.dlosses + 1) / static_cast<float>(max(1, __ldg(p.seq_tokens + p.S)));
+        for (int b = 1; b < p.S; b += kThreads) {
+            const int i = b + static_cast<int>(threadIdx.x);
+            seq += __syncthreads_count(i < p.S && __ldg(p.seq_offsets + i) <= t_begin);
+        }
+    }
+    float *g_row = buf + row * G * V;
+    int t = t_begin;
+    while (t < t_end) {
+        int seg_end = t_end;
+        float a[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) a[i] = 0.0f;
+        if (terms) {
+            while (seq < p.S - 1 && __ldg(p.seq_offsets + seq + 1) <= t) ++seq;
+            if (seq < p.S - 1) seg_end = min(t_end, __ldg(p.seq_offsets + seq + 1));
+            const float n = static_cast<float>(max(1, __ldg(p.seq_tokens + seq)));
+            const float used = static_cast<float>(max(1, __ldg(p.seq_tokens + p.S + 1)));
+            const float f = dbal / used * (static_cast<float>(p.E) / n) / (n * static_cast<float>(p.k));
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (e0 + i < p.E)
+                    a[i] = f * static_cast<float>(__ldg(p.counts + static_cast<int64_t>(seq) * p.E + e0 + i));
+        }
+        for (int base = t; base < seg_end; base += kRows) {
+            const int tok = base + row;
+            const bool inside = tok < seg_end;
+            const bool given = inside && (p.mask == nullptr || __ldg(p.mask + tok) != 0);
+            const int64_t lrow = static_cast<int64_t>(tok) * p.ld;
+            float l[V], s[V], g[V];
+            if (given) {
+                load_experts<V>(p.logits, p.dtype, p.vec, lrow, e0, p.E, l);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) l[i] = -INFINITY;
+            }
+            float top = -INFINITY;
+            unsigned on = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                top = fmaxf(top, l[i]);
+                on |= l[i] != -INFINITY ? 1u << i : 0u;
+                g_row[e0 + i] = 0.0f;
+            }
+            top = lanes_max<G>(gmask, top);
+            const bool live = (__ballot_sync(0xffffffffu, on != 0) & gmask) != 0;
+            const bool softmax = p.score_fn == MOE_SCORE_SOFTMAX;
+            float exsum = 1.0f, lse = 0.0f;
+            float ex[V];
+            if (softmax || dz != 0.0f) {
+                exsum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    ex[i] = (on >> i) & 1u ? expf(l[i] - top) : 0.0f;
+                    exsum += ex[i];
+                }
+                exsum = lanes_sum<G>(gmask, exsum);
+                lse = live ? top + logf(exsum) : 0.0f;
+                exsum = live ? 1.0f / exsum : 0.0f;
+            }
+            float Z = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (softmax) {
+                    s[i] = ex[i] * exsum;
+                } else {
+                    s[i] = (on >> i) & 1u ? 1.0f / (1.0f + expf(-l[i])) : 0.0f;
+                    Z += s[i];
+                }
+            }
+            // the weights' gradient, taken to the chosen scores: lane j has slots j, j + G, ...
+            constexpr int kOwn = kMaxK / G;
+            int ce[kOwn];
+            float cs[kOwn], cw[kOwn];
+            float chosen = 0.0f, dot = 0.0f;
+#pragma unroll
+            for (int q = 0; q < kOwn; ++q) {
+                const int j = sub + q * G;
+                const int64_t at = static_cast<int64_t>(tok) * p.k + j;
+                int e = live && j < p.k ? __ldg(p.topk_idx + at) : -1;
+                if (e >= p.E) e = -1;
+                ce[q] = e;
+                cs[q] = cw[q] = 0.0f;
+                if (e >= 0) {
+                    cw[q] = __ldg(p.dtopk_w + at);
+                    const float lj = load_one(p.logits, p.dtype, lrow + e);
+                    if (lj != -INFINITY) cs[q] = softmax ? expf(lj - top) * exsum : 1.0f / (1.0f + expf(-lj));
+                }
+                chosen += cs[q];
+            }
+            __syncwarp();
+            if (p.normalize) {
+                chosen = lanes_sum<G>(gmask, chosen) + kEps;
+#pragma unroll
+                for (int q = 0; q < kOwn; ++q) dot += cs[q] / chosen * cw[q];
+                dot = lanes_sum<G>(gmask, dot);
+            }
+#pragma unroll
+            for (int q = 0; q < kOwn; ++q)
+                if (ce[q] >= 0) g_row[ce[q]] = p.normalize ? p.scale / chosen * (cw[q] - dot) : p.scale * cw[q];
+            __syncwarp();
+            float sg = 0.0f, sa = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                g[i] = g_row[e0 + i];
+                // the chosen scores' part of sum s g vanishes where the weights are normalised
+                if (softmax) sg += s[i] * (p.normalize ? a[i] : g[i] + a[i]);
+                else sa += s[i] * a[i];
+            }
+            __syncwarp();
+            if (softmax) {
+                sg = lanes_sum<G>(gmask, sg);
+            } else if (terms) {
+                Z = lanes_sum<G>(gmask, Z);
+                sa = lanes_sum<G>(gmask, sa);
+            }
+            const float invZ = !softmax && terms && live ? 1.0f / (Z + kEps) : 0.0f;
+            const float zc = dz * lse * exsum;
+            float dl[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float v;
+                if (softmax) v = s[i] * (g[i] + a[i] - sg);
+                else v = s[i] * (1.0f - s[i]) * (g[i] + (a[i] - sa * invZ) * invZ);
+                if (dz != 0.0f) v += zc * ex[i];
+                dl[i] = (on >> i) & 1u ? v : 0.0f;
+            }
+            if (inside) {
+                const int64_t out = static_cast<int64_t>(tok) * p.E + e0;
+                if (p.dtype == MOE_DTYPE_F32) {
+                    float *q = static_cast<float *>(p.dlogits) + out;
+                    if (p.vec_out && e0 + V <= p.E) {
+#pragma unroll
+                        for (int i = 0; i < V / 4; ++i)
+                            reinterpret_cast<float4 *>(q)[i] = make_float4(dl[4 * i], dl[4 * i + 1], dl[4 * i + 2],
+                                                                           dl[4 * i + 3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < V; ++i)
+                            if (e0 + i < p.E) q[i] = dl[i];
+                    }
+                } else {
+                    uint32_t pk[V / 2];
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) {
+                        if (p.dtype == MOE_DTYPE_BF16) {
+                            pk[i] = pack_bf16x2(dl[2 * i], dl[2 * i + 1]);
+                        } else {
+                            const __half2 h = __floats2half2_rn(dl[2 * i], dl[2 * i + 1]);
+                            pk[i] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                    }
+                    unsigned short *q = static_cast<unsigned short *>(p.dlogits) + out;
+                    if (p.vec_out && e0 + V <= p.E) {
+#pragma unroll
+                        for (int i = 0; i < V / 4; ++i)
+                            reinterpret_cast<uint2 *>(q)[i] = make_uint2(pk[2 * i], pk[2 * i + 1]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < V; ++i)
+                            if (e0 + i < p.E) q[i] = static_cast<unsigned short>(pk[i / 2] >> (16 * (i & 1)));
+                    }
+                }
+            }
+        }
+        t = seg_end;
+    }
+}
+
+// Selection bias, one layer a block: b_e += rate sign(sum_e' c_e' - E c_e), the
+// counts added over the sequences as integers.
+constexpr int kBiasThreads = 1024;
+
+__global__ void __launch_bounds__(kBiasThreads)
+bias_update_kernel(float *__restrict__ bias, const int32_t *__restrict__ counts, int S, int E, float rate) {
+    griddep_wait();
+    __shared__ long long part[kBiasThreads];
+    __shared__ long long warp_part[32];
+    const int width = (E + 31) / 32 * 32;
+    const int rows = kBiasThreads / width;
+    const int r = threadIdx.x / width, e = threadIdx.x - r * width;
+    const int32_t *c = counts + static_cast<int64_t>(blockIdx.x) * S * E;
+    long long n = 0;
+    if (r < rows && e < E) {
+#pragma unroll 8
+        for (int q = r; q < S; q += rows) n += __ldg(c + static_cast<int64_t>(q) * E + e);
+    }
+    part[threadIdx.x] = n;
+    long long all = n;
+    for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
+    if ((threadIdx.x & 31) == 0) warp_part[threadIdx.x >> 5] = all;
+    __syncthreads();
+    if (threadIdx.x < E) {
+        long long mine = 0, total = 0;
+        for (int i = 0; i < rows; ++i) mine += part[i * width + threadIdx.x];
+        for (int i = 0; i < 32; ++i) total += warp_part[i];
+        const long long d = total - static_cast<long long>(E) * mine;
+        float *b = bias + static_cast<int64_t>(blockIdx.x) * E + threadIdx.x;
+        *b += d > 0 ? rate : d < 0 ? -rate : 0.0f;
+    }
+}
+
+// (lanes of a token, experts of a lane) for E experts.
+template <typename F>
+cudaError_t with_layout(int E, F f) {
+    if (E <= 32) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
+    if (E <= 64) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{});
+    if (E <= 128) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 8>{});
+    if (E <= 256) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 8>{});
+    if (E <= 512) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 16>{});
+    return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 32>{});
+}
+
+int rows_of(int E) { return E <= 64 ? 32 : E <= 128 ? 16 : 8; }
+
+}  // namespace
+
+RouteTiles route_tiles(int64_t T, int64_t E) {
+    const int64_t rows = rows_of(static_cast<int>(E));
+    const int64_t passes = (T + rows - 1) / rows;
+    const int64_t each = (passes + kRouteMaxBlocks - 1) / kRouteMaxBlocks;
+    RouteTiles r;
+    r.per_block = each * rows;
+    r.blocks = (passes + each - 1) / each;
+    return r;
+}
+
+cudaError_t launch_route(const RouteLaunch &p, cudaStream_t st) {
+    const RouteTiles tiles = route_tiles(p.T, p.E);
+    cudaError_t err = with_layout(p.E, [&](auto g, auto v) {
+        constexpr int G = decltype(g)::value, V = decltype(v)::value;
+        if (p.losses != nullptr)
+            return launch_dep(route_kernel<G, V, true>, dim3(static_cast<unsigned>(tiles.blocks)), dim3(kThreads), 0, st, p);
+        return launch_dep(route_kernel<G, V, false>, dim3(static_cast<unsigned>(tiles.blocks)), dim3(kThreads), 0, st, p);
+    });
+    note_launches(1);
+    if (err != cudaSuccess || p.losses == nullptr) return err;
+    const int chunks = (p.E + 31) / 32;
+    const int seqs = p.S < 1024 ? p.S : 1024;
+    err = launch_dep(route_reduce_kernel, dim3(chunks, seqs), dim3(32 * kReduceRows), 0, st, p);
+    note_launches(1);
+    return err;
+}
+
+cudaError_t launch_route_backward(const RouteBackwardLaunch &p, cudaStream_t st) {
+    const RouteTiles tiles = route_tiles(p.T, p.E);
+    const cudaError_t err = with_layout(p.E, [&](auto g, auto v) {
+        constexpr int G = decltype(g)::value, V = decltype(v)::value;
+        return launch_dep(route_backward_kernel<G, V>, dim3(static_cast<unsigned>(tiles.blocks)), dim3(kThreads), 0, st, p);
+    });
+    note_launches(1);
+    return err;
+}
+
+cudaError_t launch_bias_update(float *bias, const int32_t *counts, int L, int S, int E, float rate, cudaStream_t st) {
+    const cudaError_t err = launch_dep(bias_update_kernel, dim3(L), dim3(kBiasThreads), 0, st, bias, counts, S, E, rate);
+    note_launches(1);
+    return err;
+}
+
+}  // namespace moe

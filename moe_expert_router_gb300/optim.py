@@ -1,0 +1,99 @@
+"""The optimizer's end of a training step: gradient norm, clipping and AdamW over all
+parameters at once, on libmoe's kernels.
+
+Every call takes whole lists of tensors (fp32, bf16, fp16, mixed; any sizes), enqueues
+two or three kernels on the current stream and reads nothing back: the norm, the clip
+factor, the learning rate and the step count stay on the device, so a step can be
+captured into a CUDA graph and replayed.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding as B
+
+
+def _lists(tensors, name):
+    tensors = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
+    if not tensors:
+        raise ValueError(f"{name} is empty")
+    return tensors
+
+
+def _distinct(tensors, name):
+    if len({t.data_ptr() for t in tensors if t.numel()}) != sum(1 for t in tensors if t.numel()):
+        raise ValueError(f"{name} hold the same memory twice")
+
+
+def _workspace(n, device):
+    return torch.empty(B.moe_tensors_workspace_size(n), dtype=torch.uint8, device=device)
+
+
+def grad_norm(grads, norm_type=2.0):
+    """The norm (norm_type 1, 2 or inf) of all elements of `grads` together, an fp32 scalar
+    tensor on their device."""
+    grads = _lists(grads, "grads")
+    norm = torch.empty((1,), dtype=torch.float32, device=grads[0].device)
+    B.moe_grad_norm(grads, norm, _workspace(len(grads), norm.device), norm_type)
+    return norm[0]
+
+
+def clip_grad_norm_(grads, max_norm, norm_type=2.0):
+    """Multiplies every tensor of `grads` in place by min(1, max_norm / (norm + 1e-6)) and
+    returns the norm before that, as a tensor on the device."""
+    grads = _lists(grads, "grads")
+    _distinct(grads, "grads")
+    norm = torch.empty((1,), dtype=torch.float32, device=grads[0].device)
+    B.moe_clip_grads(grads, max_norm, norm, _workspace(len(grads), norm.device), norm_type)
+    return norm[0]
+
+
+def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr, masters=None, betas=(0.9, 0.999), eps=1e-8,
+               weight_decay=0.01, max_norm=0.0, skip_nonfinite=False):
+    """One AdamW step on tensors that the caller holds, in place. step int32 [1] and lr fp32 [1]
+    are on the device; exp_avg, exp_avg_sq and masters fp32. With max_norm > 0 the gradients are
+    taken times min(1, max_norm / (their global 2-norm + 1e-6)), without being changed. Returns
+    the norm as a tensor (None where max_norm is 0 and skip_nonfinite is False)."""
+    params, grads = _lists(params, "params"), _lists(grads, "grads")
+    _distinct(params, "params")
+    norm = None
+    if max_norm > 0.0 or skip_nonfinite:
+        norm = torch.empty((1,), dtype=torch.float32, device=params[0].device)
+    cfg = B.AdamWCfg(betas[0], betas[1], eps, weight_decay, max_norm, int(bool(skip_nonfinite)))
+    B.moe_adamw(params, grads, exp_avg, exp_avg_sq, lr, step, _workspace(len(params), params[0].device), cfg, masters,
+                norm)
+    return None if norm is None else norm[0]
+
+
+class AdamW:
+    """AdamW over `params` with fp32 state, and fp32 masters for 16-bit parameters (masters=False:
+    those are updated themselves, rounded to nearest at every step).
+
+    `step(grads=None, max_norm=0.0)` uses the parameters' .grad where no list is given; parameters
+    without a gradient are left alone. `lr` and `step_count` are device tensors: write into `lr`
+    for a schedule. After an update in place, drop the weights' MXFP8 copies
+    (`MxWeightCache.invalidate`)."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, masters=True,
+                 skip_nonfinite=False):
+        self.params = _lists(params, "params")
+        device = self.params[0].device
+        self.betas, self.eps, self.weight_decay, self.skip_nonfinite = betas, eps, weight_decay, skip_nonfinite
+        self.lr = torch.full((1,), lr, dtype=torch.float32, device=device)
+        self.step_count = torch.zeros((1,), dtype=torch.int32, device=device)
+        self.exp_avg = [torch.zeros_like(p, dtype=torch.float32) for p in self.params]
+        self.exp_avg_sq = [torch.zeros_like(p, dtype=torch.float32) for p in self.params]
+        self.masters = [p.detach().float() if masters and p.dtype != torch.float32 else None for p in self.params]
+
+    def step(self, grads=None, max_norm=0.0):
+        """One update; returns the gradients' norm as in adamw_step."""
+        grads = [p.grad for p in self.params] if grads is None else list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError("one gradient for each parameter")
+        at = [i for i, g in enumerate(grads) if g is not None]
+        if not at:
+            return None
+        return adamw_step([self.params[i].detach() for i in at], [grads[i] for i in at],
+                          [self.exp_avg[i] for i in at], [self.exp_avg_sq[i] for i in at], self.step_count, self.lr,
+                          [self.masters[i] for i in at], self.betas, self.eps, self.weight_decay, max_norm,
+                          self.skip_nonfinite)

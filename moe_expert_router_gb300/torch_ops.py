@@ -31,8 +31,14 @@ are returned without a gradient (the library does not differentiate aux).
 in MXFP8 (`layer_train_mx` / `layer_backward_mx`; the data gradients stay bf16, as in
 the guide's section "Expert precision") on E4M3 copies of w1 and w2 from an
 `MxWeightCache`.
+
+For training with balance terms the layer comes in two differentiable parts: `route`
+(selection from logits of any float type, with the balance and z losses, a token mask and
+packed sequences) and `moe_experts` (dispatch, both expert stages and the combine, with a
+gradient for the routing weights too); `moe_bias_update` in the binding moves the selection
+bias from route's counts.
 """
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -398,6 +404,211 @@ def _layer_mx_backward_rule(ctx, dy, *unused):
 
 
 layer_train_mx.register_autograd(_layer_mx_backward_rule, setup_context=_layer_mx_setup_context)
+
+# ------------------------------------------------------------------ routing with balance terms
+
+
+def _check_route_args(logits, k, score, sel_bias, token_mask, seq_offsets):
+    if score not in ("softmax", "sigmoid"):
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', not {score!r}")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    if logits.dtype not in B.DTYPE_CODES:
+        raise TypeError(f"logits must be float32, bfloat16 or float16, not {logits.dtype}")
+    T, E = logits.shape
+    if not 1 <= k <= E:
+        raise ValueError(f"k must be in [1, E = {E}], not {k}")
+    if sel_bias is not None:
+        _expect(sel_bias, "sel_bias", torch.float32, (E,))
+    if token_mask is not None:
+        _expect(token_mask, "token_mask", torch.bool, (T,))
+    if seq_offsets is not None:
+        if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
+            raise ValueError("seq_offsets must be [S + 1] with S >= 1")
+        _expect(seq_offsets, "seq_offsets", torch.int32, seq_offsets.shape)
+
+
+def _rows(logits):
+    """Logits whose experts are consecutive and whose rows do not overlap, copied where they are not."""
+    T, E = logits.shape
+    if (E > 1 and logits.stride(1) != 1) or (T > 1 and logits.stride(0) < E):
+        return logits.contiguous()
+    return logits
+
+
+@torch.library.custom_op(f"{_LIB}::route_train", mutates_args=())
+def route_train(logits: torch.Tensor, k: int, score: str = "softmax", normalize: bool = True, scale: float = 1.0,
+                n_group: int = 1, topk_group: int = 1, group_topn: int = 2, sel_bias: Optional[torch.Tensor] = None,
+                token_mask: Optional[torch.Tensor] = None, seq_offsets: Optional[torch.Tensor] = None
+                ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """moe_route with its statistics: (topk_idx, topk_w, losses, counts, seq_tokens)."""
+    _check_route_args(logits, k, score, sel_bias, token_mask, seq_offsets)
+    logits = _rows(logits)
+    T, E = logits.shape
+    S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+    dev = logits.device
+    idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+    w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    losses = torch.empty((2,), dtype=torch.float32, device=dev)
+    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+    seq_tokens = torch.empty((S + 2,), dtype=torch.int32, device=dev)
+    ws = torch.empty((B.moe_route_workspace_size(T, E, S, k),), dtype=torch.uint8, device=dev)
+    B.moe_route(logits, B.router_cfg(score, normalize, scale, n_group, topk_group, group_topn), idx, w,
+                sel_bias=sel_bias, token_mask=token_mask, seq_offsets=seq_offsets, counts=counts,
+                seq_tokens=seq_tokens, losses=losses, ws=ws)
+    return idx, w, losses, counts, seq_tokens
+
+
+@route_train.register_fake
+def _route_train_fake(logits, k, score="softmax", normalize=True, scale=1.0, n_group=1, topk_group=1, group_topn=2,
+                      sel_bias=None, token_mask=None, seq_offsets=None):
+    _check_route_args(logits, k, score, sel_bias, token_mask, seq_offsets)
+    T, E = logits.shape
+    S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+    return (logits.new_empty((T, k), dtype=torch.int32), logits.new_empty((T, k), dtype=torch.float32),
+            logits.new_empty((2,), dtype=torch.float32), logits.new_empty((S, E), dtype=torch.int32),
+            logits.new_empty((S + 2,), dtype=torch.int32))
+
+
+@torch.library.custom_op(f"{_LIB}::route_backward", mutates_args=())
+def route_backward(logits: torch.Tensor, topk_idx: torch.Tensor, dtopk_w: torch.Tensor, dlosses: torch.Tensor,
+                   counts: torch.Tensor, seq_tokens: torch.Tensor, score: str = "softmax", normalize: bool = True,
+                   scale: float = 1.0, n_group: int = 1, topk_group: int = 1, group_topn: int = 2,
+                   token_mask: Optional[torch.Tensor] = None, seq_offsets: Optional[torch.Tensor] = None
+                   ) -> torch.Tensor:
+    """Gradient of topk_w and losses with respect to the logits."""
+    logits = _rows(logits)
+    dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    B.moe_route_backward(logits, B.router_cfg(score, normalize, scale, n_group, topk_group, group_topn), topk_idx,
+                         dtopk_w.contiguous(), dlogits, token_mask=token_mask, seq_offsets=seq_offsets, counts=counts,
+                         seq_tokens=seq_tokens, dlosses=dlosses.contiguous())
+    return dlogits
+
+
+@route_backward.register_fake
+def _route_backward_fake(logits, topk_idx, dtopk_w, dlosses, counts, seq_tokens, score="softmax", normalize=True,
+                         scale=1.0, n_group=1, topk_group=1, group_topn=2, token_mask=None, seq_offsets=None):
+    return logits.new_empty(logits.shape)
+
+
+def _route_setup_context(ctx, inputs, output):
+    logits, _, score, normalize, scale, n_group, topk_group, group_topn, _, token_mask, seq_offsets = inputs
+    idx, _, _, counts, seq_tokens = output
+    ctx.save_for_backward(logits, idx, counts, seq_tokens, token_mask, seq_offsets)
+    ctx.cfg = (score, normalize, scale, n_group, topk_group, group_topn)
+    ctx.mark_non_differentiable(idx, counts, seq_tokens)
+
+
+def _route_backward_rule(ctx, _idx, dw, dlosses, _counts, _tokens):
+    logits, idx, counts, seq_tokens, token_mask, seq_offsets = ctx.saved_tensors
+    return (route_backward(logits, idx, dw, dlosses, counts, seq_tokens, *ctx.cfg, token_mask, seq_offsets),) + (None,) * 10
+
+
+route_train.register_autograd(_route_backward_rule, setup_context=_route_setup_context)
+
+
+class Routing(NamedTuple):
+    """What `route` returns. topk_w, balance and z carry gradients to the logits; counts
+    int32 [S, E] and seq_tokens int32 [S + 2] are moe_route's."""
+    topk_idx: torch.Tensor
+    topk_w: torch.Tensor
+    balance: torch.Tensor
+    z: torch.Tensor
+    counts: torch.Tensor
+    seq_tokens: torch.Tensor
+
+
+def route(logits, k, score="softmax", normalize=True, scale=1.0, n_group=1, topk_group=1, group_topn=2, sel_bias=None,
+          token_mask=None, seq_offsets=None) -> Routing:
+    """Differentiable routing from logits [T, E] (fp32, bf16 or fp16): a Routing with the k
+    experts and weights of each token and the step's balance and z losses (fp32 scalars).
+
+    A logit of -inf switches an expert off for a token; token_mask (bool [T]) takes padding
+    out of the selection (index -1, weight 0), the losses and the counts; seq_offsets (int32
+    [S + 1], on the device) gives the packed sequences over which balance is taken. Add
+    multiples of balance and z to the training loss, or leave them and move sel_bias with
+    `binding.moe_bias_update(sel_bias, counts, rate)` after the step."""
+    idx, w, losses, counts, seq_tokens = route_train(logits, k, score, normalize, scale, n_group, topk_group, group_topn,
+                                                     sel_bias, token_mask, seq_offsets)
+    return Routing(idx, w, losses[0], losses[1], counts, seq_tokens)
+
+
+@torch.library.custom_op(f"{_LIB}::experts_train", mutates_args=())
+def experts_train(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor, w1: torch.Tensor, w2: torch.Tensor
+                  ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The expert path's training forward on a given routing: (y, h, ws), the last two for
+    experts_backward."""
+    _check_forward_args(x, topk_idx, topk_w, w1, w2)
+    T, H = x.shape
+    E, two_i, _ = w1.shape
+    k = topk_idx.shape[1]
+    shp = B.shape(T, H, two_i // 2, E, k, training=True)
+    ws = _train_workspace(shp, x.device)
+    a = torch.empty((T * k, two_i // 2), dtype=torch.bfloat16, device=x.device)
+    h = torch.empty((T * k, two_i), dtype=torch.bfloat16, device=x.device)
+    y = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    x, topk_idx, topk_w = x.contiguous(), topk_idx.contiguous(), topk_w.contiguous()
+    B.moe_routing_metadata(topk_idx, shp, ws)
+    B.moe_dispatch_gemm1_train(x, w1, shp, a, h, ws)
+    B.moe_swiglu_gemm2_combine(a, topk_w, w2, shp, y, ws)
+    return y, h, ws
+
+
+@experts_train.register_fake
+def _experts_train_fake(x, topk_idx, topk_w, w1, w2):
+    _check_forward_args(x, topk_idx, topk_w, w1, w2)
+    T, H = x.shape
+    E, two_i, _ = w1.shape
+    k = topk_idx.shape[1]
+    n = B.moe_workspace_size(B.shape(int(T), int(H), int(two_i) // 2, int(E), int(k), training=True))
+    return (x.new_empty((T, H), dtype=torch.bfloat16), x.new_empty((T * k, two_i), dtype=torch.bfloat16),
+            x.new_empty((n,), dtype=torch.uint8))
+
+
+@torch.library.custom_op(f"{_LIB}::experts_backward", mutates_args=("ws",))
+def experts_backward(dy: torch.Tensor, x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                     w1: torch.Tensor, w2: torch.Tensor, h: torch.Tensor, ws: torch.Tensor
+                     ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(dX, dtopk_w, dW1, dW2) of experts_train from dY."""
+    _expect(dy, "dy", torch.bfloat16, tuple(x.shape))
+    T, H = x.shape
+    E, two_i, _ = w1.shape
+    shp = B.shape(T, H, two_i // 2, E, topk_idx.shape[1], training=True)
+    dx = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    dtw = torch.empty(topk_w.shape, dtype=torch.float32, device=x.device)
+    dw1, dw2 = torch.empty_like(w1), torch.empty_like(w2)
+    B.moe_backward(x.contiguous(), topk_idx.contiguous(), topk_w.contiguous(), w1, w2, h, dy.contiguous(), shp, dx, dw1,
+                   dw2, ws, dtopk_w=dtw)
+    return dx, dtw, dw1, dw2
+
+
+@experts_backward.register_fake
+def _experts_backward_fake(dy, x, topk_idx, topk_w, w1, w2, h, ws):
+    return (x.new_empty(x.shape, dtype=torch.bfloat16), topk_w.new_empty(topk_w.shape, dtype=torch.float32),
+            w1.new_empty(w1.shape), w2.new_empty(w2.shape))
+
+
+def _experts_setup_context(ctx, inputs, output):
+    x, idx, w, w1, w2 = inputs
+    _, h, ws = output
+    ctx.save_for_backward(x, idx, w, w1, w2, h, ws)
+    ctx.mark_non_differentiable(h, ws)
+
+
+def _experts_backward_rule(ctx, dy, *unused):
+    dx, dtw, dw1, dw2 = experts_backward(dy, *ctx.saved_tensors)
+    return dx, None, dtw, dw1, dw2
+
+
+experts_train.register_autograd(_experts_backward_rule, setup_context=_experts_setup_context)
+
+
+def moe_experts(x, topk_idx, topk_w, w1, w2):
+    """The expert path (dispatch, both stages, combine; bf16) on a routing such as `route`'s, as
+    one differentiable call: y bf16 [T, H]; gradients for x, topk_w, w1 and w2. Slots of -1 are
+    left out: their tokens' rows get nothing from them."""
+    return experts_train(x, topk_idx, topk_w, w1, w2)[0]
+
 
 # the E4M3 copies of the expert weights that moe_layer(..., precision="mxfp8") uses when
 # no cache is passed; call .invalidate() once per optimizer step
