@@ -27,7 +27,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxGrid = 152 * 6;
 constexpr int64_t kChunk = 16384;           // elements of a chunk
-constexpr int64_t kAdamChunk = 4096;
+constexpr int64_t kAdamChunk = 4096;         // a multiple of 4
 
 template <int N>
 struct Table {                              // one pointer a tensor
@@ -43,10 +43,12 @@ struct AdamTable {
     int64_t numel[N];
     int32_t first[N + 1];
     uint8_t p_dtype[N], g_dtype[N];
+    uint8_t head[N];                        // elements before the first vector of four, kScalar: none
     int n;
 };
+constexpr uint8_t kScalar = 255;
 // a short list is launched with a short argument block: 64 tensors are 1.4 KB, 1000 are 21 KB
-constexpr int kShort = 64, kLong = 1000, kAdamShort = 64, kAdamLong = 560;
+constexpr int kShort = 64, kLong = 1000, kAdamShort = 64, kAdamLong = 550;
 static_assert(sizeof(Table<kLong>) < 32000 && sizeof(AdamTable<kAdamLong>) < 32000, "kernel arguments");
 
 // Header of the scratch: what the update reads.
@@ -228,7 +230,9 @@ __device__ __forceinline__ float total_norm(const double *__restrict__ part, int
         else s.join(v, 0u);
     }
     const double v = block_value<kType>(s);
-    return static_cast<float>(kType == MOE_NORM_2 ? sqrt(v) : v);
+    if (kType != MOE_NORM_2) return static_cast<float>(v);
+    // the root in 32 bits (1.5 roundings) wherever the sum is in its range
+    return v > 1e-30 && v < 1e38 ? sqrtf(static_cast<float>(v)) : static_cast<float>(sqrt(v));
 }
 
 // max_norm / (norm + 1e-6), at most 1; NaN stays NaN
@@ -292,9 +296,10 @@ clip_kernel(const __grid_constant__ Table<N> tab, const double *__restrict__ par
 }
 
 // Once a step, before the update: the norm and factor, the step count and its
-// bias corrections (64 bits: 1 - b^t loses half of fp32's digits at small t).
+// bias corrections. 1 - b^t = -expm1(t ln b): ln b comes from the host in 64 bits, and
+// expm1 keeps fp32's digits where b^t is near 1.
 __global__ void __launch_bounds__(kThreads)
-adamw_begin_kernel(const double *__restrict__ part, int n_part, float max_norm, float beta1, float beta2,
+adamw_begin_kernel(const double *__restrict__ part, int n_part, float max_norm, double ln_beta1, double ln_beta2,
                    int skip_nonfinite, const float *__restrict__ lr, int32_t *__restrict__ step,
                    float *__restrict__ norm, Hyper *__restrict__ hyper) {
     griddep_wait();
@@ -306,55 +311,111 @@ adamw_begin_kernel(const double *__restrict__ part, int n_part, float max_norm, 
     h.skip = skip_nonfinite && !isfinite(total);
     h.lr = *lr;
     const int t = *step + 1;
-    h.inv_c1 = static_cast<float>(1.0 / (1.0 - pow(static_cast<double>(beta1), static_cast<double>(t))));
-    h.inv_c2 = static_cast<float>(1.0 / (1.0 - pow(static_cast<double>(beta2), static_cast<double>(t))));
+    h.inv_c1 = -1.0f / expm1f(static_cast<float>(t * ln_beta1));
+    h.inv_c2 = -1.0f / expm1f(static_cast<float>(t * ln_beta2));
     if (!h.skip) *step = t;
     if (norm != nullptr && n_part > 0) *norm = total;
     *hyper = h;
 }
 
+struct AdamConst {
+    float beta1, beta2, eps, weight_decay;
+};
+
+__device__ __forceinline__ void adam_element(const Hyper &h, const AdamConst &c, float grad, float &m, float &v, float &p) {
+    const float g = grad * h.factor;
+    m = c.beta1 * m + (1.0f - c.beta1) * g;
+    v = c.beta2 * v + (1.0f - c.beta2) * g * g;
+    const float u = m * h.inv_c1 / (sqrtf(v * h.inv_c2) + c.eps);
+    p = p - h.lr * (c.weight_decay * p + u);
+}
+
+// Four elements as they lie in memory: 16 bytes of fp32, 8 of a 16-bit type (in x, y).
+__device__ __forceinline__ uint4 load_four(const void *p, int dtype, int64_t i) {
+    if (dtype == MOE_DTYPE_F32) return __ldcs(reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i));
+    const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(static_cast<const unsigned short *>(p) + i));
+    return make_uint4(v.x, v.y, 0u, 0u);
+}
+__device__ __forceinline__ float4 four_floats(const uint4 &r, int dtype) {
+    if (dtype == MOE_DTYPE_F32)
+        return make_float4(__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z), __uint_as_float(r.w));
+    return make_float4(widen(r.x & 0xffffu, dtype), widen(r.x >> 16, dtype), widen(r.y & 0xffffu, dtype),
+                       widen(r.y >> 16, dtype));
+}
+
+// 28 bytes an element with bf16 parameters and gradients and fp32 masters, and some 20
+// operations: bound by HBM, so by the loads in flight. A thread has two groups of four
+// elements of every operand under way before it computes (112 bytes); 16-bit and fp32
+// operands are converted after all loads are issued.
 template <int N>
 __global__ void __launch_bounds__(kThreads)
-adamw_kernel(const __grid_constant__ AdamTable<N> tab, const Hyper *__restrict__ hyper, float beta1, float beta2,
-             float eps, float weight_decay) {
+adamw_kernel(const __grid_constant__ AdamTable<N> tab, const Hyper *__restrict__ hyper, const AdamConst k) {
     griddep_wait();
     const Hyper h = *hyper;
     if (h.skip) return;
     const int chunks = tab.first[tab.n];
     for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
         const int i = find_tensor(tab.first, tab.n, c);
-        const int64_t e0 = (c - tab.first[i]) * kAdamChunk;
-        const int64_t e1 = min(tab.numel[i], e0 + kAdamChunk);
+        const int64_t cc = c - tab.first[i];
         const int pt = tab.p_dtype[i], gt = tab.g_dtype[i];
         float *m = static_cast<float *>(tab.m[i]), *v = static_cast<float *>(tab.v[i]);
         float *x = static_cast<float *>(tab.x[i]);
-        constexpr int kU = 4;
-        for (int64_t e = e0 + threadIdx.x; e < e1; e += kThreads * kU) {
-            float gr[kU], mr[kU], vr[kU], pr[kU];
+        const void *pin = x != nullptr ? x : tab.p[i];
+        const int xt = x != nullptr ? MOE_DTYPE_F32 : pt;
+        const int64_t numel = tab.numel[i];
+        auto single = [&](int64_t e) {
+            float mv = m[e], vv = v[e], pv = load_elem(pin, xt, e);
+            adam_element(h, k, load_elem(tab.g[i], gt, e), mv, vv, pv);
+            m[e] = mv;
+            v[e] = vv;
+            if (x != nullptr) x[e] = pv;
+            store_elem(tab.p[i], pt, e, pv);
+        };
+        if (tab.head[i] == kScalar) {
+            const int64_t e1 = min(numel, (cc + 1) * kAdamChunk);
+#pragma unroll 4
+            for (int64_t e = cc * kAdamChunk + threadIdx.x; e < e1; e += kThreads) single(e);
+            continue;
+        }
+        const int64_t head = min(numel, static_cast<int64_t>(tab.head[i]));
+        const int64_t body = (numel - head) / 4 * 4;
+        const int64_t end = head + min(body, (cc + 1) * kAdamChunk);
+        constexpr int kU = 2;
+        for (int64_t e = head + cc * kAdamChunk + threadIdx.x * 4; e < end; e += kThreads * 4 * kU) {
+            uint4 rg[kU], rp[kU];
+            float4 rm[kU], rv[kU];
 #pragma unroll
             for (int j = 0; j < kU; ++j) {
-                const int64_t a = e + j * kThreads;
-                if (a >= e1) continue;
-                gr[j] = load_elem(tab.g[i], gt, a);
-                mr[j] = m[a];
-                vr[j] = v[a];
-                pr[j] = x != nullptr ? x[a] : load_elem(tab.p[i], pt, a);
+                const int64_t a = e + j * kThreads * 4;
+                if (a >= end) break;
+                rg[j] = load_four(tab.g[i], gt, a);
+                rm[j] = __ldcs(reinterpret_cast<const float4 *>(m + a));
+                rv[j] = __ldcs(reinterpret_cast<const float4 *>(v + a));
+                rp[j] = load_four(pin, xt, a);
             }
 #pragma unroll
             for (int j = 0; j < kU; ++j) {
-                const int64_t a = e + j * kThreads;
-                if (a >= e1) continue;
-                const float g = gr[j] * h.factor;
-                const float mn = beta1 * mr[j] + (1.0f - beta1) * g;
-                const float vn = beta2 * vr[j] + (1.0f - beta2) * g * g;
-                const float u = mn * h.inv_c1 / (sqrtf(vn * h.inv_c2) + eps);
-                const float pn = pr[j] - h.lr * (weight_decay * pr[j] + u);
-                m[a] = mn;
-                v[a] = vn;
-                if (x != nullptr) x[a] = pn;
-                store_elem(tab.p[i], pt, a, pn);
+                const int64_t a = e + j * kThreads * 4;
+                if (a >= end) break;
+                const float4 g = four_floats(rg[j], gt);
+                float4 p = four_floats(rp[j], xt);
+                adam_element(h, k, g.x, rm[j].x, rv[j].x, p.x);
+                adam_element(h, k, g.y, rm[j].y, rv[j].y, p.y);
+                adam_element(h, k, g.z, rm[j].z, rv[j].z, p.z);
+                adam_element(h, k, g.w, rm[j].w, rv[j].w, p.w);
+                __stcs(reinterpret_cast<float4 *>(m + a), rm[j]);
+                __stcs(reinterpret_cast<float4 *>(v + a), rv[j]);
+                if (x != nullptr) __stcs(reinterpret_cast<float4 *>(x + a), p);
+                if (pt == MOE_DTYPE_F32) {
+                    __stcs(reinterpret_cast<float4 *>(static_cast<float *>(tab.p[i]) + a), p);
+                } else {
+                    const uint2 o = make_uint2(narrow(p.x, pt) | narrow(p.y, pt) << 16, narrow(p.z, pt) | narrow(p.w, pt) << 16);
+                    __stcs(reinterpret_cast<uint2 *>(static_cast<unsigned short *>(tab.p[i]) + a), o);
+                }
             }
         }
+        if (cc == 0)
+            for (int64_t e = threadIdx.x; e < numel - body; e += kThreads) single(e < head ? e : e + body);
     }
 }
 
@@ -424,6 +485,22 @@ cudaError_t with_norm_type(int type, F f) {
     return f(std::integral_constant<int, MOE_NORM_INF>{});
 }
 
+// Elements until every operand of a parameter is aligned for groups of four, kScalar where
+// they never are together.
+uint8_t vector_head(const AdamwLaunch &p, int i) {
+    auto aligned = [](const void *q, int32_t dtype, int h) {
+        const uintptr_t size = dtype == MOE_DTYPE_F32 ? 4 : 2;
+        return (reinterpret_cast<uintptr_t>(q) + h * size) % (4 * size) == 0;
+    };
+    for (int h = 0; h < 4; ++h) {
+        if (aligned(p.params.ptr[i], p.params.dtype[i], h) && aligned(p.grads.ptr[i], p.grads.dtype[i], h) &&
+            aligned(p.exp_avg[i], MOE_DTYPE_F32, h) && aligned(p.exp_avg_sq[i], MOE_DTYPE_F32, h) &&
+            (p.masters == nullptr || p.masters[i] == nullptr || aligned(p.masters[i], MOE_DTYPE_F32, h)))
+            return static_cast<uint8_t>(h);
+    }
+    return kScalar;
+}
+
 template <int N>
 cudaError_t adamw_tables(const AdamwLaunch &p, cudaStream_t st) {
     int at = 0;
@@ -442,6 +519,7 @@ cudaError_t adamw_tables(const AdamwLaunch &p, cudaStream_t st) {
                 t.p_dtype[t.n] = static_cast<uint8_t>(p.params.dtype[at]);
                 t.g_dtype[t.n] = static_cast<uint8_t>(p.grads.dtype[at]);
                 t.first[t.n] = static_cast<int32_t>(first);
+                t.head[t.n] = vector_head(p, at);
                 first += chunks_of(p.params.numel[at], kAdamChunk);
                 ++t.n;
             }
@@ -451,7 +529,7 @@ cudaError_t adamw_tables(const AdamwLaunch &p, cudaStream_t st) {
         if (t.n == 0) continue;
         const cudaError_t e =
             launch_dep(adamw_kernel<N>, dim3(grid_of(first)), dim3(kThreads), 0, st, t,
-                       static_cast<const Hyper *>(p.ws), p.beta1, p.beta2, p.eps, p.weight_decay);
+                       static_cast<const Hyper *>(p.ws), AdamConst{p.beta1, p.beta2, p.eps, p.weight_decay});
         note_launches(1);
         if (e != cudaSuccess) return e;
     } while (at < p.params.n);
@@ -498,7 +576,8 @@ cudaError_t launch_adamw(const AdamwLaunch &p, cudaStream_t st) {
         if (e != cudaSuccess) return e;
     }
     e = launch_dep(adamw_begin_kernel, dim3(1), dim3(kThreads), 0, st, static_cast<const double *>(partials(p.ws)), n_part,
-                   p.max_norm, p.beta1, p.beta2, p.skip_nonfinite, p.lr, p.step, p.norm, static_cast<Hyper *>(p.ws));
+                   p.max_norm, log(static_cast<double>(p.beta1)), log(static_cast<double>(p.beta2)), p.skip_nonfinite, p.lr,
+                   p.step, p.norm, static_cast<Hyper *>(p.ws));
     note_launches(1);
     if (e != cudaSuccess) return e;
     return p.params.n <= kAdamShort ? adamw_tables<kAdamShort>(p, st) : adamw_tables<kAdamLong>(p, st);

@@ -42,10 +42,14 @@ constexpr int kThreads = 256;
 constexpr int kMaxK = 32;
 constexpr int kMaxGroups = 32;
 constexpr float kEps = 1e-20f;
-// bounds of the relative error of a 32-bit score: sigmoid is one exp (2 ulp), an
-// addition and a division; softmax adds the rounding of l - max and a sum of up to 1024 terms
-constexpr float kSigmoidErr = 5e-7f;
-constexpr float kSoftmaxErr = 4e-6f;
+// Bounds of the relative error of a 32-bit score, in units of 2^-24. Sigmoid: exp (2 ulp),
+// an addition, a reciprocal (1 ulp). Softmax with V experts a lane: the sum's V + 5 additions,
+// two exps' worth, a division and a product (the rounding of l - max is at most 2^-24 of the
+// row's largest score, and is added apart).
+constexpr float kUlp = 6e-8f;
+constexpr float kSigmoidErr = 8.0f * kUlp;
+template <int V>
+__device__ constexpr float softmax_err() { return (V + 12) * kUlp; }
 
 __device__ __forceinline__ float from_bits16(uint32_t v, int dtype) {
     if (dtype == MOE_DTYPE_BF16) return __uint_as_float(v << 16);
@@ -129,129 +133,271 @@ __device__ __forceinline__ uint32_t lanes_max_u32(unsigned mask, uint32_t v) {
     return lanes_reduce<G>(mask, v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 
-// The selection's scratch of one token.
+// The scratch of a block's tokens.
 template <int G, int V>
 struct Slots {
     int idx[kThreads / G][kMaxK + 1];
     float s[kThreads / G][kMaxK + 1];
-    float sel[kThreads / G][kMaxK + 1];
+    uint32_t key[kThreads / G][kMaxK + 1];
     double group[kThreads / G][kMaxGroups];
 };
 
-// One token's selection in 64 bits, from its logits in memory.
-template <int G, int V>
-__device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int sub, unsigned gmask, int *out_idx,
-                                         float *out_s, double *group) {
-    const int e0 = sub * V;
-    double s[V], sel[V];
-    double top = -INFINITY;
-    for (int i = 0; i < V; ++i) {
-        s[i] = e0 + i < p.E ? static_cast<double>(load_one(p.logits, p.dtype, row + e0 + i)) : -INFINITY;
-        if (s[i] > top) top = s[i];
+// A double's bits in an order that unsigned compares keep (64-bit floating-point
+// instructions, compares among them, take some 16 cycles a warp here).
+__device__ __forceinline__ uint64_t order_key64(double v) {
+    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+    return v != v ? 0u : ((u >> 63) ? ~u : (u | 0x8000000000000000ull));
+}
+
+template <int G>
+__device__ __forceinline__ uint64_t lanes_max_u64(unsigned mask, uint64_t v) {
+    const uint32_t hi = lanes_max_u32<G>(mask, static_cast<uint32_t>(v >> 32));
+    const uint32_t lo = lanes_max_u32<G>(mask, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+    return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
+// A token's scores in 64 bits: what softmax needs of the whole row, then one expert's.
+struct WideScore {
+    double top, inv;                                 // softmax only
+    __device__ __forceinline__ double operator()(bool softmax, double l) const {
+        return softmax ? exp(l - top) * inv : 1.0 / (1.0 + exp(-l));
     }
-    auto dmax = [](double a, double b) { return a > b ? a : b; };
-    top = lanes_reduce<G>(gmask, top, dmax);
+};
+template <int G, int V>
+__device__ __forceinline__ WideScore wide_score(const RouteLaunch &p, int64_t row, int e0, unsigned gmask) {
+    WideScore w = {0.0, 1.0};
+    if (p.score_fn != MOE_SCORE_SOFTMAX) return w;
+    float top = -INFINITY;
+    for (int i = 0; i < V; ++i)
+        if (e0 + i < p.E) top = fmaxf(top, load_one(p.logits, p.dtype, row + e0 + i));
+    w.top = lanes_max<G>(gmask, top);
     double z = 0.0;
-    unsigned open = 0;                              // experts that may still be chosen
+    for (int i = 0; i < V; ++i)
+        if (e0 + i < p.E) z += exp(static_cast<double>(load_one(p.logits, p.dtype, row + e0 + i)) - w.top);
+    for (int off = G / 2; off > 0; off >>= 1) z += __shfl_xor_sync(gmask, z, off);
+    w.inv = 1.0 / z;
+    return w;
+}
+
+// Selection in 64 bits among the experts marked in `cand` (at most G of the token's, all
+// that can be among its k best): one expert a lane, and its rank is the number of better ones.
+template <int G, int V>
+__device__ __noinline__ void select_near(const RouteLaunch &p, int64_t row, int sub, unsigned gmask, unsigned cand,
+                                         int *out_idx, float *out_s) {
+    const int e0 = sub * V, lane = threadIdx.x & 31;
+    const WideScore score = wide_score<G, V>(p, row, e0, gmask);
+    int n = 0;
     for (int i = 0; i < V; ++i) {
-        if (s[i] > -INFINITY) open |= 1u << i;
-        sel[i] = s[i];
-        if (p.score_fn == MOE_SCORE_SOFTMAX) {
-            s[i] = s[i] == -INFINITY ? 0.0 : exp(s[i] - top);
-            z += s[i];
-        } else {
-            s[i] = s[i] == -INFINITY ? 0.0 : 1.0 / (1.0 + exp(-s[i]));
+        const unsigned b = __ballot_sync(gmask, (cand >> i) & 1u) & gmask;
+        if ((cand >> i) & 1u) out_idx[n + __popc(b & ((1u << lane) - 1u))] = e0 + i;
+        n += __popc(b);
+    }
+    __syncwarp(gmask);
+    const int e = sub < n ? out_idx[sub] : 0x7fffffff;
+    __syncwarp(gmask);
+    uint64_t key = 0;
+    float s32 = 0.0f;
+    if (sub < n) {
+        const double s = score(p.score_fn == MOE_SCORE_SOFTMAX, load_one(p.logits, p.dtype, row + e));
+        s32 = static_cast<float>(s);
+        key = order_key64(s + static_cast<double>(__ldg(p.sel_bias + e)));
+    }
+    int rank = 0;
+    for (int c = 0; c < n; ++c) {
+        const uint64_t ok = __shfl_sync(gmask, key, c, G);
+        const int oe = __shfl_sync(gmask, e, c, G);
+        rank += ok > key || (ok == key && oe < e);
+    }
+    if (sub < n && rank < p.k) {
+        out_idx[rank] = e;
+        out_s[rank] = s32;
+    }
+    __syncwarp(gmask);
+}
+
+// One token's whole selection in 64 bits: the groups in `sure` stay, of those in `near`
+// the best stay as far as topk_group allows, then k rounds.
+template <int G, int V>
+__device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int sub, unsigned gmask, unsigned sure,
+                                         unsigned near, int *out_idx, float *out_s, double *group) {
+    const int e0 = sub * V;
+    const WideScore score = wide_score<G, V>(p, row, e0, gmask);
+    const bool softmax = p.score_fn == MOE_SCORE_SOFTMAX;
+    const int gs = p.E / p.n_group;
+    double sel[V];
+    uint64_t key[V];
+    unsigned open = 0;                               // experts that may still be chosen
+    for (int i = 0; i < V; ++i) {
+        key[i] = 0;
+        if (e0 + i >= p.E || !(((sure | near) >> ((e0 + i) / gs)) & 1u)) continue;
+        const float l = load_one(p.logits, p.dtype, row + e0 + i);
+        if (l == -INFINITY) continue;
+        open |= 1u << i;
+        sel[i] = score(softmax, l) + (p.sel_bias != nullptr ? static_cast<double>(__ldg(p.sel_bias + e0 + i)) : 0.0);
+        key[i] = order_key64(sel[i]);
+    }
+    if (near != 0) {
+        for (unsigned left = near; left != 0; left &= left - 1u) {
+            const int g = __ffs(left) - 1;
+            unsigned taken = 0;
+            double total = -INFINITY;
+            for (int n = 0; n < p.group_topn; ++n) {
+                uint64_t b = 0;
+                for (int i = 0; i < V; ++i)
+                    if (((open & ~taken) >> i) & 1u && (e0 + i) / gs == g && key[i] > b) b = key[i];
+                const uint64_t m = lanes_max_u64<G>(gmask, b);
+                if (m == 0) break;
+                const unsigned who = __ballot_sync(gmask, b == m) & gmask;
+                const int from = __ffs(who) - 1;
+                double v = 0.0;
+                if ((threadIdx.x & 31) == from) {
+                    int at = 0;
+                    for (int i = V - 1; i >= 0; --i)
+                        if (((open & ~taken) >> i) & 1u && (e0 + i) / gs == g && key[i] == m) at = i;
+                    taken |= 1u << at;
+                    v = sel[at];
+                }
+                v = __shfl_sync(gmask, v, from);
+                total = n == 0 ? v : total + v;
+            }
+            if (sub == 0) group[g] = total;
+        }
+        __syncwarp(gmask);
+        const int room = p.topk_group - __popc(sure);
+        for (int i = 0; i < V; ++i) {
+            if (!((open >> i) & 1u)) continue;
+            const int g = (e0 + i) / gs;
+            if (!((near >> g) & 1u)) continue;
+            int before = 0;
+            for (unsigned left = near; left != 0; left &= left - 1u) {
+                const int o = __ffs(left) - 1;
+                before += group[o] > group[g] || (group[o] == group[g] && o < g);
+            }
+            if (before >= room) {
+                open &= ~(1u << i);
+                key[i] = 0;
+            }
+        }
+        __syncwarp(gmask);
+    }
+    if (p.sel_bias == nullptr)                       // the score's order is the logit's
+        for (int i = 0; i < V; ++i)
+            if ((open >> i) & 1u) key[i] = order_key64(load_one(p.logits, p.dtype, row + e0 + i));
+    for (int j = 0; j < p.k; ++j) {
+        uint64_t b = 0;
+        for (int i = 0; i < V; ++i) b = max(b, key[i]);
+        const uint64_t m = lanes_max_u64<G>(gmask, b);
+        const unsigned who = __ballot_sync(gmask, b == m) & gmask;
+        if ((threadIdx.x & 31) == __ffs(who) - 1) {
+            int at = -1;
+            if (m != 0)
+                for (int i = V - 1; i >= 0; --i)
+                    if (key[i] == m) at = i;
+            if (at >= 0) key[at] = 0;
+            out_idx[j] = at < 0 ? -1 : e0 + at;
         }
     }
-    if (p.score_fn == MOE_SCORE_SOFTMAX) {
-        z = lanes_reduce<G>(gmask, z, [](double a, double b) { return a + b; });
-        for (int i = 0; i < V; ++i) s[i] /= z;
+    __syncwarp(gmask);
+    for (int j = sub; j < p.k; j += G) {
+        const int e = out_idx[j];
+        out_s[j] = e >= 0 ? static_cast<float>(score(softmax, load_one(p.logits, p.dtype, row + e))) : 0.0f;
     }
-    auto with_bias = [&](int i) {
-        return s[i] + (p.sel_bias != nullptr ? static_cast<double>(__ldg(p.sel_bias + e0 + i)) : 0.0);
-    };
-    if (p.n_group > 1) {
-        const int gs = p.E / p.n_group;
-        for (int g = 0; g < p.n_group; ++g) {
-            double pv = INFINITY, total = -INFINITY;
+    __syncwarp(gmask);
+}
+
+// The groups of one token that stay, as bits; sel_row: its selection scores. A group is
+// searched by a power of two of lanes (four for eight groups of a 256-expert token), each
+// taking every fourth expert, and the lanes' best are merged. `near`: the groups that could
+// be on either side, where the last kept and the first dropped sum differ by no more than
+// `err`, the error of two sums; 0 where none could.
+template <int G>
+__device__ __forceinline__ unsigned kept_groups(const RouteLaunch &p, const float *sel_row, float *sums, int sub,
+                                                unsigned gmask, float err, unsigned &near) {
+    const int gs = p.E / p.n_group;
+    int per = G;                                     // lanes of a group
+    while (per > 1 && per * p.n_group > G) per >>= 1;
+    const int part = sub & (per - 1);
+    for (int g0 = 0; g0 < p.n_group; g0 += G / per) {
+        const int g = g0 + sub / per;
+        const float *row = sel_row + g * gs;
+        // a lane's experts part, part + per, ... from a start that spreads the banks
+        const int n = g < p.n_group && part < gs ? (gs - part + per - 1) / per : 0;
+        int i = n > 0 ? g % n : 0;
+        float total = -INFINITY;
+        if (p.group_topn <= 2) {
+            float a = -INFINITY, b = -INFINITY;      // the two best, a >= b
+            for (int c = 0; c < n; ++c) {
+                const float v = row[part + per * i];
+                b = fmaxf(b, fminf(a, v));
+                a = fmaxf(a, v);
+                i = i + 1 == n ? 0 : i + 1;
+            }
+            for (int off = per >> 1; off > 0; off >>= 1) {
+                const float oa = __shfl_xor_sync(gmask, a, off), ob = __shfl_xor_sync(gmask, b, off);
+                b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+                a = fmaxf(a, oa);
+            }
+            total = p.group_topn == 2 && b > -INFINITY ? a + b : a;
+        } else {
+            float pv = INFINITY;
             int pi = -1;
-            for (int n = 0; n < p.group_topn; ++n) {
-                double bv = -INFINITY;
+            for (int r = 0; r < p.group_topn; ++r) {
+                float bv = -INFINITY;
                 int bi = 0x7fffffff;
-                for (int i = 0; i < V; ++i) {
-                    const int e = e0 + i;
-                    if (!((open >> i) & 1u) || e / gs != g) continue;
-                    const double v = with_bias(i);
-                    if (!(v < pv || (v == pv && e > pi))) continue;
-                    if (v > bv || (v == bv && e < bi)) {
+                for (int c = 0; c < n; ++c) {
+                    const int e = part + per * c;
+                    const float v = row[e];
+                    if ((v < pv || (v == pv && e > pi)) && v > bv) {
                         bv = v;
                         bi = e;
                     }
                 }
-                for (int off = G / 2; off > 0; off >>= 1) {
-                    const double ov = __shfl_xor_sync(gmask, bv, off);
+                for (int off = per >> 1; off > 0; off >>= 1) {
+                    const float ov = __shfl_xor_sync(gmask, bv, off);
                     const int oi = __shfl_xor_sync(gmask, bi, off);
                     if (ov > bv || (ov == bv && oi < bi)) {
                         bv = ov;
                         bi = oi;
                     }
                 }
-                if (bi == 0x7fffffff) break;
-                total = n == 0 ? bv : total + bv;
-                pv = bv;
+                if (bi != 0x7fffffff) total = total == -INFINITY ? bv : total + bv;
+                pv = bi == 0x7fffffff ? -INFINITY : bv;
                 pi = bi;
             }
-            if (sub == 0) group[g] = total;
         }
-        __syncwarp(gmask);
-        for (int i = 0; i < V; ++i) {
-            if (!((open >> i) & 1u)) continue;
-            const int g = (e0 + i) / gs;
-            const double mine = group[g];
-            int before = 0;
-            for (int o = 0; o < p.n_group; ++o) before += group[o] > mine || (group[o] == mine && o < g);
-            if (before >= p.topk_group) open &= ~(1u << i);
-        }
+        if (part == 0 && g < p.n_group) sums[g] = total;
+    }
+    __syncwarp();
+    unsigned kept = 0;
+    for (int g = sub; g < p.n_group; g += G) {
+        const float mine = sums[g];
+        int before = 0;
+        for (int o = 0; o < p.n_group; ++o) before += sums[o] > mine || (sums[o] == mine && o < g);
+        if (before < p.topk_group) kept |= 1u << g;
+        // the sums at the border
+        if (before == p.topk_group - 1) sums[kMaxGroups] = mine;
+        if (before == p.topk_group) sums[kMaxGroups + 1] = mine;
+    }
+    kept = lanes_reduce<G>(gmask, kept, [](unsigned a, unsigned b) { return a | b; });
+    __syncwarp();
+    const float in = sums[kMaxGroups], out = sums[kMaxGroups + 1];
+    near = 0;
+    if (out > -INFINITY && in - out <= err) {
+        // a sum above out + err outranks every dropped group, one below in - err no kept one
+        for (int g = sub; g < p.n_group; g += G)
+            if (sums[g] <= out + err && sums[g] >= in - err) near |= 1u << g;
+        near = lanes_reduce<G>(gmask, near, [](unsigned a, unsigned b) { return a | b; });
         __syncwarp(gmask);
     }
-    if (p.sel_bias != nullptr)
-        for (int i = 0; i < V; ++i)
-            if ((open >> i) & 1u) sel[i] = with_bias(i);
-    for (int j = 0; j < p.k; ++j) {
-        double bv = -INFINITY;
-        int bi = 0x7fffffff;
-        for (int i = 0; i < V; ++i)
-            if (((open >> i) & 1u) && (bi == 0x7fffffff || sel[i] > bv)) {
-                bv = sel[i];
-                bi = e0 + i;
-            }
-        for (int off = G / 2; off > 0; off >>= 1) {
-            const double ov = __shfl_xor_sync(gmask, bv, off);
-            const int oi = __shfl_xor_sync(gmask, bi, off);
-            if (ov > bv || (ov == bv && oi < bi)) {
-                bv = ov;
-                bi = oi;
-            }
-        }
-        if (bi == 0x7fffffff) {
-            if (sub == 0) {
-                out_idx[j] = -1;
-                out_s[j] = 0.0f;
-            }
-        } else if (bi >= e0 && bi < e0 + V) {
-            out_idx[j] = bi;
-            out_s[j] = static_cast<float>(s[bi - e0]);
-            open &= ~(1u << (bi - e0));
-        }
-    }
-    __syncwarp(gmask);
+    return kept;
 }
 
 // Tokens [per_block b, per_block (b + 1)) in block b, kThreads / G at a time.
 template <int G, int V, bool kStats>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, V <= 8 ? 3 : V == 16 ? 2 : 1)
 route_kernel(const RouteLaunch p) {
     constexpr int kRows = kThreads / G;
+    constexpr int kOwn = kMaxK / G;                  // slots of a lane
     __shared__ Slots<G, V> slots;
     __shared__ float buf[kRows * G * V];
     __shared__ int hist[kStats ? G * V : 1];
@@ -264,6 +410,25 @@ route_kernel(const RouteLaunch p) {
     const int e0 = sub * V;
     const int t_begin = blockIdx.x * p.per_block;
     const int t_end = min(p.T, t_begin + p.per_block);
+    const bool by_score = p.sel_bias != nullptr;
+    const bool grouped = p.n_group > 1 && p.topk_group < p.n_group;
+    const bool softmax = p.score_fn == MOE_SCORE_SOFTMAX;
+    const int gs = p.E / p.n_group, g_first = e0 / gs;
+    float *own_row = buf + row * G * V;
+    // a lane's biases stay in registers where there are few
+    constexpr int kHeld = V <= 8 ? V : 1;
+    float held[kHeld], bias_max = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float b = by_score && e0 + i < p.E ? __ldg(p.sel_bias + e0 + i) : 0.0f;
+        if (V <= 8) held[i % kHeld] = b;
+        bias_max = fmaxf(bias_max, fabsf(b));
+    }
+    auto bias = [&](int i) {
+        if (V <= 8) return held[i % kHeld];
+        return by_score && e0 + i < p.E ? __ldg(p.sel_bias + e0 + i) : 0.0f;
+    };
+    if (by_score) bias_max = lanes_max<G>(gmask, bias_max);
     int seq = 0;
     float acc[V];
     float z_acc = 0.0f;
@@ -305,118 +470,89 @@ route_kernel(const RouteLaunch p) {
                 top = fmaxf(top, l[i]);
                 on |= l[i] != -INFINITY ? 1u << i : 0u;
             }
-            top = lanes_max<G>(gmask, top);
             const bool live = (__ballot_sync(0xffffffffu, on != 0) & gmask) != 0;
-            // scores
-            float ssum = 0.0f, s_max = 1.0f;         // s_max: no score is above it
-            if (p.score_fn == MOE_SCORE_SOFTMAX) {
+            if (softmax || kStats) top = lanes_max<G>(gmask, top);
+            // scores (exp(-inf) = 0 puts out the experts that are off)
+            float s_max = 1.0f;                      // no score is above it
+            if (softmax) {
+                float ssum = 0.0f;
+                const float shift = live ? top : 0.0f;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    s[i] = (on >> i) & 1u ? expf(l[i] - top) : 0.0f;
+                    s[i] = expf(l[i] - shift);
                     ssum += s[i];
                 }
                 ssum = lanes_sum<G>(gmask, ssum);
-                const float inv = 1.0f / (live ? ssum : 1.0f);
-                s_max = inv;
+                s_max = 1.0f / (live ? ssum : 1.0f);
 #pragma unroll
-                for (int i = 0; i < V; ++i) s[i] *= inv;
+                for (int i = 0; i < V; ++i) s[i] *= s_max;
                 if (kStats && live && sub == 0) {
                     const float lse = top + logf(ssum);
                     z_acc += lse * lse;
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) s[i] = (on >> i) & 1u ? 1.0f / (1.0f + expf(-l[i])) : 0.0f;
                 if constexpr (kStats) {
-                    float ex = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
+                    for (int i = 0; i < V; ++i) acc[i] += s[i];
+                }
+            } else {
+                float ex = 0.0f, ssum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float e = expf(-l[i]);
+                    s[i] = __fdividef(1.0f, 1.0f + e);
+                    if constexpr (kStats) {
                         ssum += s[i];
-                        ex += (on >> i) & 1u ? expf(l[i] - top) : 0.0f;
+                        ex += __fdividef(1.0f, e);   // exp(l)
+                    }
+                }
+                if constexpr (kStats) {
+                    float shift = 0.0f;
+                    if (!(top < 80.0f && top > -60.0f)) {
+                        // exp(l) leaves fp32: about the maximum, as softmax does
+                        shift = live ? top : 0.0f;
+                        ex = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < V; ++i) ex += expf(l[i] - shift);
                     }
                     ssum = lanes_sum<G>(gmask, ssum);
                     ex = lanes_sum<G>(gmask, ex);
                     if (live && sub == 0) {
-                        const float lse = top + logf(ex);
+                        const float lse = shift + logf(ex);
                         z_acc += lse * lse;
                     }
-                }
-            }
-            if constexpr (kStats) {
-                if (live) {
-                    const float share = p.score_fn == MOE_SCORE_SOFTMAX ? 1.0f : 1.0f / (ssum + kEps);
+                    const float share = live ? 1.0f / (ssum + kEps) : 0.0f;
 #pragma unroll
                     for (int i = 0; i < V; ++i) acc[i] += s[i] * share;
-                    n_acc += sub == 0;
                 }
             }
+            if (kStats) n_acc += live && sub == 0;
             // keys
-            const float rel = p.score_fn == MOE_SCORE_SOFTMAX ? kSoftmaxErr : kSigmoidErr;
-            const bool by_score = p.sel_bias != nullptr;
+            const float rel = softmax ? softmax_err<V>() : kSigmoidErr;
             uint32_t key[V];
+            unsigned kept = 0xffffffffu, near_groups = 0;
             bool near = false;                       // nearer than the error of a 32-bit key
-            float bias[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                bias[i] = by_score && e0 + i < p.E ? __ldg(p.sel_bias + e0 + i) : 0.0f;
-                key[i] = (on >> i) & 1u ? order_key(by_score ? s[i] + bias[i] : l[i]) : 0u;
-            }
-            if (p.n_group > 1 && p.topk_group < p.n_group) {
-                // each group's sum of its group_topn best, one group a lane
-                const int gs = p.E / p.n_group;
-                float *sel_row = buf + row * G * V;
+            for (int i = 0; i < V; ++i) key[i] = (on >> i) & 1u ? order_key(by_score ? s[i] + bias(i) : l[i]) : 0u;
+            if (grouped) {
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    sel_row[e0 + i] = (on >> i) & 1u ? s[i] + bias[i] : -INFINITY;
+                for (int i = 0; i < V; ++i) own_row[e0 + i] = (on >> i) & 1u ? s[i] + bias(i) : -INFINITY;
                 __syncwarp();
-                float *sums = reinterpret_cast<float *>(slots.group[row]);
-                float mag = 0.0f;                    // largest sum of magnitudes
-                for (int g = sub; g < p.n_group; g += G) {
-                    float pv = INFINITY, total = -INFINITY, size = 0.0f;
-                    int pi = -1;
-                    for (int n = 0; n < p.group_topn; ++n) {
-                        float bv = -INFINITY;
-                        int bi = -1;
-                        for (int i = 0; i < gs; ++i) {
-                            const float v = sel_row[g * gs + i];
-                            if ((v < pv || (v == pv && i > pi)) && v > bv) {
-                                bv = v;
-                                bi = i;
-                            }
-                        }
-                        if (bi < 0) break;
-                        total = n == 0 ? bv : total + bv;
-                        size += fabsf(bv);
-                        pv = bv;
-                        pi = bi;
+                const float n = static_cast<float>(p.group_topn);
+                kept = kept_groups<G>(p, own_row, reinterpret_cast<float *>(slots.group[row]), sub, gmask,
+                                      2.0f * n * (rel * s_max + kUlp * (2.0f + n) * (s_max + bias_max)), near_groups);
+                int g = g_first, next = (g + 1) * gs;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if (e0 + i == next) {
+                        ++g;
+                        next += gs;
                     }
-                    sums[g] = total;
-                    mag = fmaxf(mag, size);
+                    if (!((kept >> (g & 31)) & 1u)) key[i] = 0u;
                 }
                 __syncwarp();
-                unsigned kept = 0;
-                float worst_kept = INFINITY, best_lost = -INFINITY;
-                for (int g = sub; g < p.n_group; g += G) {
-                    const float mine = sums[g];
-                    int before = 0;
-                    for (int o = 0; o < p.n_group; ++o) before += sums[o] > mine || (sums[o] == mine && o < g);
-                    if (before < p.topk_group) {
-                        kept |= 1u << g;
-                        worst_kept = fminf(worst_kept, mine);
-                    } else {
-                        best_lost = fmaxf(best_lost, mine);
-                    }
-                }
-                kept = lanes_reduce<G>(gmask, kept, [](unsigned a, unsigned b) { return a | b; });
-                worst_kept = -lanes_max<G>(gmask, -worst_kept);
-                best_lost = lanes_max<G>(gmask, best_lost);
-                mag = lanes_max<G>(gmask, mag);
-                near = worst_kept > -INFINITY && best_lost > -INFINITY &&
-                       worst_kept - best_lost <= static_cast<float>(p.group_topn) * (2.0f * rel * s_max + 1.2e-7f * mag);
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (e0 + i < p.E && !((kept >> ((e0 + i) / gs)) & 1u)) key[i] = 0u;
             }
+#pragma unroll
+            for (int i = 0; i < V; ++i) own_row[e0 + i] = s[i];
             // k rounds (one more where the last chosen key is compared with the next)
             uint32_t best = 0;
 #pragma unroll
@@ -427,14 +563,10 @@ route_kernel(const RouteLaunch p) {
                 const unsigned who = __ballot_sync(0xffffffffu, best == m) & gmask;
                 if (lane == __ffs(who) - 1) {
                     int at = -1;
-                    float sv = 0.0f;
                     if (m != 0) {
 #pragma unroll
                         for (int i = V - 1; i >= 0; --i)
-                            if (key[i] == m) {
-                                at = i;
-                                sv = s[i];
-                            }
+                            if (key[i] == m) at = i;
                         best = 0;
 #pragma unroll
                         for (int i = 0; i < V; ++i) {
@@ -443,38 +575,77 @@ route_kernel(const RouteLaunch p) {
                         }
                     }
                     slots.idx[row][j] = at < 0 ? -1 : e0 + at;
-                    slots.s[row][j] = sv;
-                    slots.sel[row][j] = key_value(m);
+                    slots.key[row][j] = m;
                 }
             }
             __syncwarp();
+            float sv[kOwn];
+            int ev[kOwn];
+#pragma unroll
+            for (int q = 0; q < kOwn; ++q) {
+                const int j = sub + q * G;
+                ev[q] = j < p.k ? slots.idx[row][j] : -1;
+                sv[q] = ev[q] >= 0 ? own_row[ev[q]] : 0.0f;
+            }
             if (by_score) {
-                for (int j = sub; j < p.k; j += G) {
-                    const int a = slots.idx[row][j], b = slots.idx[row][j + 1];
-                    if (a < 0 || b < 0) continue;
-                    const float x = slots.sel[row][j], y = slots.sel[row][j + 1];
-                    const float bound = rel * (slots.s[row][j] + slots.s[row][j + 1]) + 1.2e-7f * (fabsf(x) + fabsf(y));
-                    if (x - y <= bound &&
-                        !(load_one(p.logits, p.dtype, lrow + a) == load_one(p.logits, p.dtype, lrow + b) &&
-                          __ldg(p.sel_bias + a) == __ldg(p.sel_bias + b)))
+#pragma unroll
+                for (int q = 0; q < kOwn; ++q) {
+                    // this slot's key against the next one's (the last one's: the first not chosen)
+                    const int b = ev[q] >= 0 ? slots.idx[row][sub + q * G + 1] : -1;
+                    if (b < 0) continue;
+                    const float x = key_value(slots.key[row][sub + q * G]), y = key_value(slots.key[row][sub + q * G + 1]);
+                    if (x - y <= rel * (sv[q] + own_row[b]) + kUlp * (2.0f * (fabsf(x) + fabsf(y)) + s_max) &&
+                        // not near: a tie of the same logit and bias
+                        !(load_one(p.logits, p.dtype, lrow + ev[q]) == load_one(p.logits, p.dtype, lrow + b) &&
+                          __ldg(p.sel_bias + ev[q]) == __ldg(p.sel_bias + b)))
                         near = true;
                 }
             }
-            if (__ballot_sync(0xffffffffu, near) & gmask)
-                select_wide<G, V>(p, lrow, sub, gmask, slots.idx[row], slots.s[row], slots.group[row]);
-            __syncwarp();
+            // the vote is the whole warp's: it stands before any branch that a token takes alone
+            const bool any_near = (__ballot_sync(0xffffffffu, near || near_groups != 0) & gmask) != 0;
+            if (any_near) {
+                // candidates: no more than the error below the first key that was not chosen
+                unsigned cand = 0;
+                int n = G + 1;
+                if (near_groups == 0) {
+                    const int b = slots.idx[row][p.k];
+                    const float last = b >= 0 ? key_value(slots.key[row][p.k]) : -INFINITY;
+                    const float floor = last - 2.0f * (rel * s_max + 2.0f * kUlp * (s_max + bias_max));
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float v = s[i] + bias(i);
+                        if ((on >> i) & 1u && v >= floor && (!grouped || (kept >> ((e0 + i) / gs)) & 1u)) cand |= 1u << i;
+                    }
+                    n = lanes_reduce<G>(gmask, __popc(cand), [](int a, int b) { return a + b; });
+                }
+                if (n <= G)
+                    select_near<G, V>(p, lrow, sub, gmask, cand, slots.idx[row], slots.s[row]);
+                else
+                    select_wide<G, V>(p, lrow, sub, gmask, kept & ~near_groups, near_groups, slots.idx[row], slots.s[row],
+                                      slots.group[row]);
+#pragma unroll
+                for (int q = 0; q < kOwn; ++q) {
+                    const int j = sub + q * G;
+                    ev[q] = j < p.k ? slots.idx[row][j] : -1;
+                    sv[q] = ev[q] >= 0 ? slots.s[row][j] : 0.0f;
+                }
+            }
             // weights
-            float chosen = 0.0f;
-            for (int j = sub; j < p.k; j += G) chosen += slots.s[row][j];
-            chosen = lanes_sum<G>(gmask, chosen);
+            float chosen = 1.0f;
+            if (p.normalize) {
+                chosen = 0.0f;
+#pragma unroll
+                for (int q = 0; q < kOwn; ++q) chosen += sv[q];
+                chosen = lanes_sum<G>(gmask, chosen) + kEps;
+            }
             if (inside) {
-                for (int j = sub; j < p.k; j += G) {
-                    const int e = slots.idx[row][j];
-                    float w = slots.s[row][j];
-                    if (p.normalize) w = w / (chosen + kEps);
-                    p.topk_idx[static_cast<int64_t>(tok) * p.k + j] = e;
-                    p.topk_w[static_cast<int64_t>(tok) * p.k + j] = w * p.scale;
-                    if (kStats && e >= 0) atomicAdd(&hist[e], 1);
+#pragma unroll
+                for (int q = 0; q < kOwn; ++q) {
+                    const int j = sub + q * G;
+                    if (j >= p.k) break;
+                    p.topk_idx[static_cast<int64_t>(tok) * p.k + j] = ev[q];
+                    p.topk_w[static_cast<int64_t>(tok) * p.k + j] = sv[q] / chosen * p.scale;
+                    if (kStats && ev[q] >= 0) atomicAdd(&hist[ev[q]], 1);
                 }
             }
             __syncwarp();
@@ -484,7 +655,7 @@ route_kernel(const RouteLaunch p) {
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                buf[row * G * V + e0 + i] = acc[i];
+                own_row[e0 + i] = acc[i];
                 acc[i] = 0.0f;
             }
             if (sub == 0) {
