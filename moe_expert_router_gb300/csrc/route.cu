@@ -38,7 +38,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 256;
+// Threads of a block; with 32 experts a lane fewer, for their shared memory.
+template <int V>
+constexpr int kBlock = V > 16 ? 128 : 256;
 constexpr int kMaxK = 32;
 constexpr int kMaxGroups = 32;
 constexpr float kEps = 1e-20f;
@@ -79,7 +81,7 @@ __device__ __forceinline__ void load_experts(const void *p, int dtype, int vec, 
             }
         } else {
             const uint2 *q = reinterpret_cast<const uint2 *>(static_cast<const unsigned short *>(p) + row + e0);
-            uint2 x[V / 4];
+            uint2 x[V / 4];                          // four 16-bit values each
             if constexpr (V >= 8) {
 #pragma unroll
                 for (int i = 0; i < V / 8; ++i) {
@@ -90,12 +92,24 @@ __device__ __forceinline__ void load_experts(const void *p, int dtype, int vec, 
             } else {
                 x[0] = __ldg(q);
             }
+            if (dtype == MOE_DTYPE_BF16) {
 #pragma unroll
-            for (int i = 0; i < V / 4; ++i) {
-                l[4 * i] = from_bits16(x[i].x & 0xffffu, dtype);
-                l[4 * i + 1] = from_bits16(x[i].x >> 16, dtype);
-                l[4 * i + 2] = from_bits16(x[i].y & 0xffffu, dtype);
-                l[4 * i + 3] = from_bits16(x[i].y >> 16, dtype);
+                for (int i = 0; i < V / 4; ++i) {
+                    l[4 * i] = __uint_as_float(x[i].x << 16);
+                    l[4 * i + 1] = __uint_as_float(x[i].x & 0xffff0000u);
+                    l[4 * i + 2] = __uint_as_float(x[i].y << 16);
+                    l[4 * i + 3] = __uint_as_float(x[i].y & 0xffff0000u);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V / 4; ++i) {
+                    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&x[i].x));
+                    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&x[i].y));
+                    l[4 * i] = a.x;
+                    l[4 * i + 1] = a.y;
+                    l[4 * i + 2] = b.x;
+                    l[4 * i + 3] = b.y;
+                }
             }
         }
         return;
@@ -103,6 +117,15 @@ __device__ __forceinline__ void load_experts(const void *p, int dtype, int vec, 
 #pragma unroll
     for (int i = 0; i < V; ++i) l[i] = e0 + i < E ? load_one(p, dtype, row + e0 + i) : -INFINITY;
 }
+
+// 2^x (2 ulp). softmax's exp(l - top) is taken as 2^((l - top) log2 e), whose exponent has
+// two roundings: 2^-23 |x| 2^x of the row's largest score, less than 2^-24 of it.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 
 // A float's bits in an order that unsigned compares keep; 0 is below every number.
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -133,13 +156,17 @@ __device__ __forceinline__ uint32_t lanes_max_u32(unsigned mask, uint32_t v) {
     return lanes_reduce<G>(mask, v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 
+constexpr uint32_t kIndexBits = 0x1fffu;
+constexpr int kIndexMax = 1023;
+
 // The scratch of a block's tokens.
 template <int G, int V>
 struct Slots {
-    int idx[kThreads / G][kMaxK + 1];
-    float s[kThreads / G][kMaxK + 1];
-    uint32_t key[kThreads / G][kMaxK + 1];
-    double group[kThreads / G][kMaxGroups];
+    static constexpr int kRows = kBlock<V> / G;
+    int idx[kRows][kMaxK + 1];
+    float s[kRows][kMaxK + 1];
+    uint32_t key[kRows][kMaxK + 1];
+    double group[kRows][kMaxGroups];
 };
 
 // A double's bits in an order that unsigned compares keep (64-bit floating-point
@@ -156,6 +183,8 @@ __device__ __forceinline__ uint64_t lanes_max_u64(unsigned mask, uint64_t v) {
     return static_cast<uint64_t>(hi) << 32 | lo;
 }
 
+// In what follows a lane's experts are unrolled where they are few; the rest is in local memory.
+
 // A token's scores in 64 bits: what softmax needs of the whole row, then one expert's.
 struct WideScore {
     double top, inv;                                 // softmax only
@@ -168,10 +197,12 @@ __device__ __forceinline__ WideScore wide_score(const RouteLaunch &p, int64_t ro
     WideScore w = {0.0, 1.0};
     if (p.score_fn != MOE_SCORE_SOFTMAX) return w;
     float top = -INFINITY;
+#pragma unroll (V <= 8 ? V : 1)
     for (int i = 0; i < V; ++i)
         if (e0 + i < p.E) top = fmaxf(top, load_one(p.logits, p.dtype, row + e0 + i));
     w.top = lanes_max<G>(gmask, top);
     double z = 0.0;
+#pragma unroll (V <= 8 ? V : 1)
     for (int i = 0; i < V; ++i)
         if (e0 + i < p.E) z += exp(static_cast<double>(load_one(p.logits, p.dtype, row + e0 + i)) - w.top);
     for (int off = G / 2; off > 0; off >>= 1) z += __shfl_xor_sync(gmask, z, off);
@@ -187,6 +218,7 @@ __device__ __noinline__ void select_near(const RouteLaunch &p, int64_t row, int 
     const int e0 = sub * V, lane = threadIdx.x & 31;
     const WideScore score = wide_score<G, V>(p, row, e0, gmask);
     int n = 0;
+#pragma unroll (V <= 8 ? V : 1)
     for (int i = 0; i < V; ++i) {
         const unsigned b = __ballot_sync(gmask, (cand >> i) & 1u) & gmask;
         if ((cand >> i) & 1u) out_idx[n + __popc(b & ((1u << lane) - 1u))] = e0 + i;
@@ -227,6 +259,7 @@ __device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int 
     double sel[V];
     uint64_t key[V];
     unsigned open = 0;                               // experts that may still be chosen
+#pragma unroll (V <= 8 ? V : 1)
     for (int i = 0; i < V; ++i) {
         key[i] = 0;
         if (e0 + i >= p.E || !(((sure | near) >> ((e0 + i) / gs)) & 1u)) continue;
@@ -243,6 +276,7 @@ __device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int 
             double total = -INFINITY;
             for (int n = 0; n < p.group_topn; ++n) {
                 uint64_t b = 0;
+#pragma unroll (V <= 8 ? V : 1)
                 for (int i = 0; i < V; ++i)
                     if (((open & ~taken) >> i) & 1u && (e0 + i) / gs == g && key[i] > b) b = key[i];
                 const uint64_t m = lanes_max_u64<G>(gmask, b);
@@ -252,6 +286,7 @@ __device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int 
                 double v = 0.0;
                 if ((threadIdx.x & 31) == from) {
                     int at = 0;
+#pragma unroll (V <= 8 ? V : 1)
                     for (int i = V - 1; i >= 0; --i)
                         if (((open & ~taken) >> i) & 1u && (e0 + i) / gs == g && key[i] == m) at = i;
                     taken |= 1u << at;
@@ -264,6 +299,7 @@ __device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int 
         }
         __syncwarp(gmask);
         const int room = p.topk_group - __popc(sure);
+#pragma unroll (V <= 8 ? V : 1)
         for (int i = 0; i < V; ++i) {
             if (!((open >> i) & 1u)) continue;
             const int g = (e0 + i) / gs;
@@ -281,16 +317,19 @@ __device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int 
         __syncwarp(gmask);
     }
     if (p.sel_bias == nullptr)                       // the score's order is the logit's
+#pragma unroll (V <= 8 ? V : 1)
         for (int i = 0; i < V; ++i)
             if ((open >> i) & 1u) key[i] = order_key64(load_one(p.logits, p.dtype, row + e0 + i));
     for (int j = 0; j < p.k; ++j) {
         uint64_t b = 0;
+#pragma unroll (V <= 8 ? V : 1)
         for (int i = 0; i < V; ++i) b = max(b, key[i]);
         const uint64_t m = lanes_max_u64<G>(gmask, b);
         const unsigned who = __ballot_sync(gmask, b == m) & gmask;
         if ((threadIdx.x & 31) == __ffs(who) - 1) {
             int at = -1;
             if (m != 0)
+#pragma unroll (V <= 8 ? V : 1)
                 for (int i = V - 1; i >= 0; --i)
                     if (key[i] == m) at = i;
             if (at >= 0) key[at] = 0;
@@ -393,13 +432,19 @@ __device__ __forceinline__ unsigned kept_groups(const RouteLaunch &p, const floa
 }
 
 // Tokens [per_block b, per_block (b + 1)) in block b, kThreads / G at a time.
-template <int G, int V, bool kStats>
-__global__ void __launch_bounds__(kThreads, V <= 8 ? 3 : V == 16 ? 2 : 1)
+// kShort: 16-bit logits without a selection bias. An fp32 of such a value has its low 13
+// bits clear, which hold the expert's index instead: one 32-bit key tells both, no two are
+// equal, and a round is a maximum and a clearing without a branch.
+template <int G, int V, bool kStats, bool kShort>
+__global__ void __launch_bounds__(kBlock<V>, V <= 8 ? 3 : V == 16 ? 2 : 1)
 route_kernel(const RouteLaunch p) {
-    constexpr int kRows = kThreads / G;
+    constexpr int kThreads = kBlock<V>, kRows = kThreads / G;
+    // score sums of a lane's experts: in registers, or where those run out in shared memory
+    constexpr bool kShared = V > 16;
     constexpr int kOwn = kMaxK / G;                  // slots of a lane
     __shared__ Slots<G, V> slots;
-    __shared__ float buf[kRows * G * V];
+    __shared__ __align__(16) float buf[kRows * G * V];
+    __shared__ __align__(16) float sums_buf[kStats && kShared ? kRows * G * V : 1];
     __shared__ int hist[kStats ? G * V : 1];
     __shared__ float red_z[kRows];
     __shared__ int red_n[kRows];
@@ -410,7 +455,7 @@ route_kernel(const RouteLaunch p) {
     const int e0 = sub * V;
     const int t_begin = blockIdx.x * p.per_block;
     const int t_end = min(p.T, t_begin + p.per_block);
-    const bool by_score = p.sel_bias != nullptr;
+    const bool by_score = !kShort && p.sel_bias != nullptr;
     const bool grouped = p.n_group > 1 && p.topk_group < p.n_group;
     const bool softmax = p.score_fn == MOE_SCORE_SOFTMAX;
     const int gs = p.E / p.n_group, g_first = e0 / gs;
@@ -430,13 +475,21 @@ route_kernel(const RouteLaunch p) {
     };
     if (by_score) bias_max = lanes_max<G>(gmask, bias_max);
     int seq = 0;
-    float acc[V];
+    float acc[kShared ? 1 : V];
+    float *own_sums = sums_buf + (kStats && kShared ? row * G * V + e0 : 0);
+    auto add = [&](int i, float v) {
+        if (kShared) own_sums[i] += v;
+        else acc[kShared ? 0 : i] += v;
+    };
     float z_acc = 0.0f;
     int n_acc = 0;
     if constexpr (kStats) {
         if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+        for (int i = 0; i < V; ++i) {
+            if (kShared) own_sums[i] = 0.0f;
+            else acc[kShared ? 0 : i] = 0.0f;
+        }
         for (int e = threadIdx.x; e < G * V; e += kThreads) hist[e] = 0;
         for (int b = 1; b < p.S; b += kThreads) {
             const int i = b + static_cast<int>(threadIdx.x);
@@ -479,7 +532,7 @@ route_kernel(const RouteLaunch p) {
                 const float shift = live ? top : 0.0f;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    s[i] = expf(l[i] - shift);
+                    s[i] = exp2_fast((l[i] - shift) * kLog2e);
                     ssum += s[i];
                 }
                 ssum = lanes_sum<G>(gmask, ssum);
@@ -492,7 +545,7 @@ route_kernel(const RouteLaunch p) {
                 }
                 if constexpr (kStats) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) acc[i] += s[i];
+                    for (int i = 0; i < V; ++i) add(i, s[i]);
                 }
             } else {
                 float ex = 0.0f, ssum = 0.0f;
@@ -522,7 +575,7 @@ route_kernel(const RouteLaunch p) {
                     }
                     const float share = live ? 1.0f / (ssum + kEps) : 0.0f;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) acc[i] += s[i] * share;
+                    for (int i = 0; i < V; ++i) add(i, s[i] * share);
                 }
             }
             if (kStats) n_acc += live && sub == 0;
@@ -532,7 +585,11 @@ route_kernel(const RouteLaunch p) {
             unsigned kept = 0xffffffffu, near_groups = 0;
             bool near = false;                       // nearer than the error of a 32-bit key
 #pragma unroll
-            for (int i = 0; i < V; ++i) key[i] = (on >> i) & 1u ? order_key(by_score ? s[i] + bias(i) : l[i]) : 0u;
+            for (int i = 0; i < V; ++i) {
+                const uint32_t u = order_key(by_score ? s[i] + bias(i) : l[i]);
+                const uint32_t v = kShort && u != 0 ? (u & ~kIndexBits) | (kIndexMax - (e0 + i)) : u;
+                key[i] = (on >> i) & 1u ? v : 0u;
+            }
             if (grouped) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) own_row[e0 + i] = (on >> i) & 1u ? s[i] + bias(i) : -INFINITY;
@@ -557,36 +614,57 @@ route_kernel(const RouteLaunch p) {
             uint32_t best = 0;
 #pragma unroll
             for (int i = 0; i < V; ++i) best = max(best, key[i]);
-            const int rounds = p.k + (by_score ? 1 : 0);
-            for (int j = 0; j < rounds; ++j) {
-                const uint32_t m = lanes_max_u32<G>(gmask, best);
-                const unsigned who = __ballot_sync(0xffffffffu, best == m) & gmask;
-                if (lane == __ffs(who) - 1) {
-                    int at = -1;
-                    if (m != 0) {
-#pragma unroll
-                        for (int i = V - 1; i >= 0; --i)
-                            if (key[i] == m) at = i;
-                        best = 0;
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            if (i == at) key[i] = 0u;
-                            best = max(best, key[i]);
-                        }
-                    }
-                    slots.idx[row][j] = at < 0 ? -1 : e0 + at;
-                    slots.key[row][j] = m;
-                }
-            }
-            __syncwarp();
             float sv[kOwn];
             int ev[kOwn];
+            if constexpr (kShort) {
 #pragma unroll
-            for (int q = 0; q < kOwn; ++q) {
-                const int j = sub + q * G;
-                ev[q] = j < p.k ? slots.idx[row][j] : -1;
-                sv[q] = ev[q] >= 0 ? own_row[ev[q]] : 0.0f;
+                for (int q = 0; q < kOwn; ++q) ev[q] = -1;
+                for (int j = 0; j < p.k; ++j) {
+                    const uint32_t m = lanes_max_u32<G>(gmask, best);
+#pragma unroll
+                    for (int q = 0; q < kOwn; ++q)
+                        if (j == sub + q * G && m != 0) ev[q] = kIndexMax - static_cast<int>(m & kIndexBits);
+                    best = 0;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        key[i] = key[i] == m ? 0u : key[i];
+                        best = max(best, key[i]);
+                    }
+                }
+                if (grouped) {                       // where the selection in 64 bits starts from
+#pragma unroll
+                    for (int q = 0; q < kOwn; ++q)
+                        if (sub + q * G < p.k) slots.idx[row][sub + q * G] = ev[q];
+                }
+                __syncwarp();
+            } else {
+                const int rounds = p.k + (by_score ? 1 : 0);
+                for (int j = 0; j < rounds; ++j) {
+                    const uint32_t m = lanes_max_u32<G>(gmask, best);
+                    const unsigned who = __ballot_sync(0xffffffffu, best == m) & gmask;
+                    if (lane == __ffs(who) - 1) {
+                        int at = -1;
+                        if (m != 0) {
+#pragma unroll
+                            for (int i = V - 1; i >= 0; --i)
+                                if (key[i] == m) at = i;
+                            best = 0;
+#pragma unroll
+                            for (int i = 0; i < V; ++i) {
+                                if (i == at) key[i] = 0u;
+                                best = max(best, key[i]);
+                            }
+                        }
+                        slots.idx[row][j] = at < 0 ? -1 : e0 + at;
+                        slots.key[row][j] = m;
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < kOwn; ++q) ev[q] = sub + q * G < p.k ? slots.idx[row][sub + q * G] : -1;
             }
+#pragma unroll
+            for (int q = 0; q < kOwn; ++q) sv[q] = ev[q] >= 0 ? own_row[ev[q]] : 0.0f;
             if (by_score) {
 #pragma unroll
                 for (int q = 0; q < kOwn; ++q) {
@@ -613,7 +691,7 @@ route_kernel(const RouteLaunch p) {
                     const float floor = last - 2.0f * (rel * s_max + 2.0f * kUlp * (s_max + bias_max));
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        const float v = s[i] + bias(i);
+                        const float v = own_row[e0 + i] + bias(i);
                         if ((on >> i) & 1u && v >= floor && (!grouped || (kept >> ((e0 + i) / gs)) & 1u)) cand |= 1u << i;
                     }
                     n = lanes_reduce<G>(gmask, __popc(cand), [](int a, int b) { return a + b; });
@@ -655,8 +733,9 @@ route_kernel(const RouteLaunch p) {
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                own_row[e0 + i] = acc[i];
-                acc[i] = 0.0f;
+                own_row[e0 + i] = kShared ? own_sums[i] : acc[kShared ? 0 : i];
+                if (kShared) own_sums[i] = 0.0f;
+                else acc[kShared ? 0 : i] = 0.0f;
             }
             if (sub == 0) {
                 red_z[row] = z_acc;
@@ -816,10 +895,11 @@ route_reduce_kernel(const RouteLaunch p) {
 // and dl += dz 2/N lse softmax(l). One pass: a token's logits are read, its scores
 // recomputed, its gradient written.
 template <int G, int V>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kBlock<V>, V <= 8 ? 4 : V == 16 ? 2 : 1)
 route_backward_kernel(const RouteBackwardLaunch p) {
-    constexpr int kRows = kThreads / G;
-    __shared__ float buf[kRows * G * V];
+    constexpr int kThreads = kBlock<V>, kRows = kThreads / G;
+    constexpr int kOwn = kMaxK / G;                  // slots of a lane
+    __shared__ __align__(16) float s_buf[kRows * G * V], g_buf[kRows * G * V];
     griddep_wait();
     const int row = threadIdx.x / G, sub = threadIdx.x % G;
     const int lane = threadIdx.x & 31;
@@ -828,6 +908,7 @@ route_backward_kernel(const RouteBackwardLaunch p) {
     const int t_begin = blockIdx.x * p.per_block;
     const int t_end = min(p.T, t_begin + p.per_block);
     const bool terms = p.dlosses != nullptr;
+    const bool softmax = p.score_fn == MOE_SCORE_SOFTMAX;
     float dbal = 0.0f, dz = 0.0f;
     int seq = 0;
     if (terms) {
@@ -838,7 +919,10 @@ route_backward_kernel(const RouteBackwardLaunch p) {
             seq += __syncthreads_count(i < p.S && __ldg(p.seq_offsets + i) <= t_begin);
         }
     }
-    float *g_row = buf + row * G * V;
+    float *s_row = s_buf + row * G * V, *g_row = g_buf + row * G * V;
+    float4 *s_own = reinterpret_cast<float4 *>(s_row + e0), *g_own = reinterpret_cast<float4 *>(g_row + e0);
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) g_own[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     int t = t_begin;
     while (t < t_end) {
         int seg_end = t_end;
@@ -860,105 +944,123 @@ route_backward_kernel(const RouteBackwardLaunch p) {
             const int tok = base + row;
             const bool inside = tok < seg_end;
             const bool given = inside && (p.mask == nullptr || __ldg(p.mask + tok) != 0);
-            const int64_t lrow = static_cast<int64_t>(tok) * p.ld;
-            float l[V], s[V], g[V];
+            float l[V], s[V];
+            int ce[kOwn];                            // lane j has slots j, j + G, ...
+            float cw[kOwn];
+#pragma unroll
+            for (int q = 0; q < kOwn; ++q) {
+                const int j = sub + q * G;
+                ce[q] = -1;
+                cw[q] = 0.0f;
+                if (given && j < p.k) {
+                    const int64_t at = static_cast<int64_t>(tok) * p.k + j;
+                    ce[q] = __ldg(p.topk_idx + at);
+                    cw[q] = __ldg(p.dtopk_w + at);
+                }
+            }
             if (given) {
-                load_experts<V>(p.logits, p.dtype, p.vec, lrow, e0, p.E, l);
+                load_experts<V>(p.logits, p.dtype, p.vec, static_cast<int64_t>(tok) * p.ld, e0, p.E, l);
             } else {
 #pragma unroll
                 for (int i = 0; i < V; ++i) l[i] = -INFINITY;
             }
-            float top = -INFINITY;
-            unsigned on = 0;
+            float top = l[0];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                top = fmaxf(top, l[i]);
-                on |= l[i] != -INFINITY ? 1u << i : 0u;
-                g_row[e0 + i] = 0.0f;
-            }
-            top = lanes_max<G>(gmask, top);
-            const bool live = (__ballot_sync(0xffffffffu, on != 0) & gmask) != 0;
-            const bool softmax = p.score_fn == MOE_SCORE_SOFTMAX;
-            float exsum = 1.0f, lse = 0.0f;
-            float ex[V];
+            for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < V; ++i) any |= l[i] != -INFINITY;
+            const bool live = (__ballot_sync(0xffffffffu, any) & gmask) != 0;
+            float inv = 0.0f, zc = 0.0f;             // softmax: s = ex inv; z's coefficient at ex
+            float Z = 0.0f;
             if (softmax || dz != 0.0f) {
-                exsum = 0.0f;
+                top = lanes_max<G>(gmask, top);
+                const float shift = live ? top : 0.0f;
+                float sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    ex[i] = (on >> i) & 1u ? expf(l[i] - top) : 0.0f;
-                    exsum += ex[i];
+                    s[i] = exp2_fast((l[i] - shift) * kLog2e);
+                    sum += s[i];
                 }
-                exsum = lanes_sum<G>(gmask, exsum);
-                lse = live ? top + logf(exsum) : 0.0f;
-                exsum = live ? 1.0f / exsum : 0.0f;
+                sum = lanes_sum<G>(gmask, sum);
+                if (live) {
+                    inv = 1.0f / sum;
+                    zc = dz * (top + logf(sum)) * inv;
+                }
             }
-            float Z = 0.0f;
+            float z[V];                              // the z term, and for sigmoid the scores anew
+            if (softmax) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if (softmax) {
-                    s[i] = ex[i] * exsum;
-                } else {
-                    s[i] = (on >> i) & 1u ? 1.0f / (1.0f + expf(-l[i])) : 0.0f;
+                for (int i = 0; i < V; ++i) s[i] *= inv;
+                zc = live ? zc / inv : 0.0f;         // at s
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    z[i] = dz != 0.0f ? zc * s[i] : 0.0f;
+                    s[i] = __fdividef(1.0f, 1.0f + expf(-l[i]));
                     Z += s[i];
                 }
             }
-            // the weights' gradient, taken to the chosen scores: lane j has slots j, j + G, ...
-            constexpr int kOwn = kMaxK / G;
-            int ce[kOwn];
-            float cs[kOwn], cw[kOwn];
-            float chosen = 0.0f, dot = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) s_own[i] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+            __syncwarp();
+            // the weights' gradient, taken to the chosen scores
+            float cs[kOwn], chosen = 0.0f, dot = 0.0f;
 #pragma unroll
             for (int q = 0; q < kOwn; ++q) {
-                const int j = sub + q * G;
-                const int64_t at = static_cast<int64_t>(tok) * p.k + j;
-                int e = live && j < p.k ? __ldg(p.topk_idx + at) : -1;
-                if (e >= p.E) e = -1;
-                ce[q] = e;
-                cs[q] = cw[q] = 0.0f;
-                if (e >= 0) {
-                    cw[q] = __ldg(p.dtopk_w + at);
-                    const float lj = load_one(p.logits, p.dtype, lrow + e);
-                    if (lj != -INFINITY) cs[q] = softmax ? expf(lj - top) * exsum : 1.0f / (1.0f + expf(-lj));
-                }
+                if (ce[q] >= p.E) ce[q] = -1;
+                cs[q] = ce[q] >= 0 ? s_row[ce[q]] : 0.0f;
                 chosen += cs[q];
             }
-            __syncwarp();
             if (p.normalize) {
                 chosen = lanes_sum<G>(gmask, chosen) + kEps;
 #pragma unroll
                 for (int q = 0; q < kOwn; ++q) dot += cs[q] / chosen * cw[q];
                 dot = lanes_sum<G>(gmask, dot);
             }
+            const float to_score = p.normalize ? p.scale / chosen : p.scale;
 #pragma unroll
             for (int q = 0; q < kOwn; ++q)
-                if (ce[q] >= 0) g_row[ce[q]] = p.normalize ? p.scale / chosen * (cw[q] - dot) : p.scale * cw[q];
+                if (ce[q] >= 0) g_row[ce[q]] = to_score * (cw[q] - dot);
             __syncwarp();
-            float sg = 0.0f, sa = 0.0f;
+            float g[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                g[i] = g_row[e0 + i];
-                // the chosen scores' part of sum s g vanishes where the weights are normalised
-                if (softmax) sg += s[i] * (p.normalize ? a[i] : g[i] + a[i]);
-                else sa += s[i] * a[i];
+            for (int i = 0; i < V / 4; ++i) {
+                const float4 x = g_own[i];
+                g[4 * i] = x.x;
+                g[4 * i + 1] = x.y;
+                g[4 * i + 2] = x.z;
+                g[4 * i + 3] = x.w;
+                g_own[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
-            __syncwarp();
+            // through the score function
+            float sum = 0.0f;
             if (softmax) {
-                sg = lanes_sum<G>(gmask, sg);
-            } else if (terms) {
-                Z = lanes_sum<G>(gmask, Z);
-                sa = lanes_sum<G>(gmask, sa);
-            }
-            const float invZ = !softmax && terms && live ? 1.0f / (Z + kEps) : 0.0f;
-            const float zc = dz * lse * exsum;
-            float dl[V];
+                // the chosen scores' part of sum s g vanishes where the weights are normalised
+                if (terms || !p.normalize) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float v;
-                if (softmax) v = s[i] * (g[i] + a[i] - sg);
-                else v = s[i] * (1.0f - s[i]) * (g[i] + (a[i] - sa * invZ) * invZ);
-                if (dz != 0.0f) v += zc * ex[i];
-                dl[i] = (on >> i) & 1u ? v : 0.0f;
+                    for (int i = 0; i < V; ++i) sum += s[i] * (p.normalize ? a[i] : g[i] + a[i]);
+                    sum = lanes_sum<G>(gmask, sum);
+                }
+                const float minus = zc - sum;
+#pragma unroll
+                for (int i = 0; i < V; ++i) g[i] = s[i] * (g[i] + (a[i] + minus));
+            } else {
+                float invZ = 0.0f;
+                if (terms) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum += s[i] * a[i];
+                    sum = lanes_sum<G>(gmask, sum);
+                    Z = lanes_sum<G>(gmask, Z);
+                    invZ = live ? 1.0f / (Z + kEps) : 0.0f;
+                    sum *= invZ;
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) g[i] = s[i] * (1.0f - s[i]) * (g[i] + (a[i] - sum) * invZ) + z[i];
             }
+            // off experts have s = 0, and their products are 0; infinite ones are put out
+#pragma unroll
+            for (int i = 0; i < V; ++i) g[i] = l[i] == -INFINITY ? 0.0f : g[i];
             if (inside) {
                 const int64_t out = static_cast<int64_t>(tok) * p.E + e0;
                 if (p.dtype == MOE_DTYPE_F32) {
@@ -966,29 +1068,33 @@ route_backward_kernel(const RouteBackwardLaunch p) {
                     if (p.vec_out && e0 + V <= p.E) {
 #pragma unroll
                         for (int i = 0; i < V / 4; ++i)
-                            reinterpret_cast<float4 *>(q)[i] = make_float4(dl[4 * i], dl[4 * i + 1], dl[4 * i + 2],
-                                                                           dl[4 * i + 3]);
+                            reinterpret_cast<float4 *>(q)[i] = make_float4(g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]);
                     } else {
 #pragma unroll
                         for (int i = 0; i < V; ++i)
-                            if (e0 + i < p.E) q[i] = dl[i];
+                            if (e0 + i < p.E) q[i] = g[i];
                     }
                 } else {
                     uint32_t pk[V / 2];
+                    if (p.dtype == MOE_DTYPE_BF16) {
 #pragma unroll
-                    for (int i = 0; i < V / 2; ++i) {
-                        if (p.dtype == MOE_DTYPE_BF16) {
-                            pk[i] = pack_bf16x2(dl[2 * i], dl[2 * i + 1]);
-                        } else {
-                            const __half2 h = __floats2half2_rn(dl[2 * i], dl[2 * i + 1]);
+                        for (int i = 0; i < V / 2; ++i) pk[i] = pack_bf16x2(g[2 * i], g[2 * i + 1]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < V / 2; ++i) {
+                            const __half2 h = __floats2half2_rn(g[2 * i], g[2 * i + 1]);
                             pk[i] = *reinterpret_cast<const uint32_t *>(&h);
                         }
                     }
                     unsigned short *q = static_cast<unsigned short *>(p.dlogits) + out;
                     if (p.vec_out && e0 + V <= p.E) {
+                        if constexpr (V >= 8) {
 #pragma unroll
-                        for (int i = 0; i < V / 4; ++i)
-                            reinterpret_cast<uint2 *>(q)[i] = make_uint2(pk[2 * i], pk[2 * i + 1]);
+                            for (int i = 0; i < V / 8; ++i)
+                                reinterpret_cast<uint4 *>(q)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                        } else {
+                            *reinterpret_cast<uint2 *>(q) = make_uint2(pk[0], pk[1]);
+                        }
                     } else {
 #pragma unroll
                         for (int i = 0; i < V; ++i)
@@ -1045,7 +1151,7 @@ cudaError_t with_layout(int E, F f) {
     return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 32>{});
 }
 
-int rows_of(int E) { return E <= 64 ? 32 : E <= 128 ? 16 : 8; }
+int rows_of(int E) { return E <= 64 ? 32 : E <= 128 ? 16 : E <= 512 ? 8 : 4; }
 
 }  // namespace
 
@@ -1063,9 +1169,13 @@ cudaError_t launch_route(const RouteLaunch &p, cudaStream_t st) {
     const RouteTiles tiles = route_tiles(p.T, p.E);
     cudaError_t err = with_layout(p.E, [&](auto g, auto v) {
         constexpr int G = decltype(g)::value, V = decltype(v)::value;
+        const dim3 grid(static_cast<unsigned>(tiles.blocks));
+        const bool brief = p.dtype != MOE_DTYPE_F32 && p.sel_bias == nullptr;
         if (p.losses != nullptr)
-            return launch_dep(route_kernel<G, V, true>, dim3(static_cast<unsigned>(tiles.blocks)), dim3(kThreads), 0, st, p);
-        return launch_dep(route_kernel<G, V, false>, dim3(static_cast<unsigned>(tiles.blocks)), dim3(kThreads), 0, st, p);
+            return brief ? launch_dep(route_kernel<G, V, true, true>, grid, dim3(kBlock<V>), 0, st, p)
+                         : launch_dep(route_kernel<G, V, true, false>, grid, dim3(kBlock<V>), 0, st, p);
+        return brief ? launch_dep(route_kernel<G, V, false, true>, grid, dim3(kBlock<V>), 0, st, p)
+                     : launch_dep(route_kernel<G, V, false, false>, grid, dim3(kBlock<V>), 0, st, p);
     });
     note_launches(1);
     if (err != cudaSuccess || p.losses == nullptr) return err;
@@ -1080,7 +1190,7 @@ cudaError_t launch_route_backward(const RouteBackwardLaunch &p, cudaStream_t st)
     const RouteTiles tiles = route_tiles(p.T, p.E);
     const cudaError_t err = with_layout(p.E, [&](auto g, auto v) {
         constexpr int G = decltype(g)::value, V = decltype(v)::value;
-        return launch_dep(route_backward_kernel<G, V>, dim3(static_cast<unsigned>(tiles.blocks)), dim3(kThreads), 0, st, p);
+        return launch_dep(route_backward_kernel<G, V>, dim3(static_cast<unsigned>(tiles.blocks)), dim3(kBlock<V>), 0, st, p);
     });
     note_launches(1);
     return err;
