@@ -374,7 +374,7 @@ moe_status_t moe_grad_norm(const void *const *grads, const int64_t *numel, const
 
 /* The same norm, and every element of every tensor times
  * min(1, max_norm / (norm + 1e-6)), in place (rounded once to its type;
- * untouched where the factor is 1). max_norm > 0. A NaN norm makes every
+ * untouched where the factor is 1). max_norm >= 0 (0: all become 0). A NaN norm makes every
  * element NaN and an infinite one every finite element 0. */
 moe_status_t moe_clip_grads(void *const *grads, const int64_t *numel, const int32_t *dtype, int32_t n,
                             int32_t norm_type, float max_norm, float *norm, void *ws, size_t ws_bytes,

@@ -10,11 +10,12 @@ on the tensors' device.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
 
-from .build import LIB_PATH, LISTS_PATH
+from .build import LIB_PATH, NATIVE_PATH
 
 MOE_OK = 0
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
@@ -130,7 +131,7 @@ _SIG = {
 _RESTYPES = {"moe_status_string": ctypes.c_char_p, "moe_kernel_launch_count": ctypes.c_uint64}
 
 _lib = None
-_lists = None
+_native = None
 
 
 def load(path: str = LIB_PATH):
@@ -169,7 +170,7 @@ def _ptr(t):
 
 def _stream(stream, like):
     if stream is None:
-        stream = torch.cuda.current_stream(like.device)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(like.get_device()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -474,12 +475,34 @@ def new_workspace(shp: Shape, device=None) -> torch.Tensor:
 
 # ------------------------------------------------------------------ the trainable router
 
+def _module():
+    """csrc/native.cpp, bound to the library: the calls whose cost on the host shows."""
+    global _native
+    if _native is None:
+        lib = load()
+        try:
+            from . import _native as native
+        except ImportError as e:
+            raise RuntimeError(f"{NATIVE_PATH} is missing: build it first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
+        native.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in
+                      (lib.moe_route, lib.moe_route_backward, lib.moe_bias_update)])
+        _native = native
+    return _native
+
+
+def _raw_stream(stream, like):
+    """A stream's handle as a number; the current one's of the tensor's device for None."""
+    if stream is not None:
+        return stream.cuda_stream
+    device = like.get_device()
+    return torch._C._cuda_getCurrentRawStream(device) if device >= 0 else 0
+
+
 def _typed(t, name, dtype, shape):
     """Checks an optional dense tensor and gives its address."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
@@ -487,31 +510,7 @@ def _typed(t, name, dtype, shape):
     return _ptr(t)
 
 
-def _mask_ptr(mask, T):
-    if mask is not None and mask.dtype == torch.uint8:
-        return _typed(mask, "token_mask", torch.uint8, (T,))
-    return _typed(mask, "token_mask", torch.bool, (T,))
-
-
-def _route_shape(logits, topk_idx, seq_offsets):
-    if logits.dim() != 2 or topk_idx.dim() != 2:
-        raise ValueError("logits must be [T, E] and topk_idx [T, k]")
-    if logits.dtype not in DTYPE_CODES:
-        raise TypeError(f"logits must be float32, bfloat16 or float16, not {logits.dtype}")
-    if not logits.is_cuda:
-        raise ValueError("libmoe takes CUDA tensors only")
-    T, E = logits.shape
-    if E > 1 and logits.stride(1) != 1:
-        raise ValueError("the experts of a row of logits must be consecutive")
-    ld = logits.stride(0) if T > 1 else E
-    if ld < E:
-        raise ValueError("the rows of logits overlap")
-    if seq_offsets is not None and (seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2):
-        raise ValueError("seq_offsets must be [S + 1] with S >= 1")
-    S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
-    return RouteShape(T, E, S, ld, topk_idx.shape[1], DTYPE_CODES[logits.dtype])
-
-
+@functools.lru_cache(maxsize=256)
 def moe_route_workspace_size(T, E, S=1, k=1) -> int:
     n = ctypes.c_size_t()
     shp = RouteShape(T, E, S, E, k, 0)
@@ -524,59 +523,31 @@ def moe_route(logits, cfg, topk_idx, topk_w, sel_bias=None, token_mask=None, seq
     """Selection from logits [T, E] (fp32, bf16 or fp16; rows may be apart), with the balance
     statistics of a training step where counts [S, E], seq_tokens [S + 2], losses [2] and a
     workspace of moe_route_workspace_size bytes are given. token_mask: bool or uint8 [T]."""
-    shp = _route_shape(logits, topk_idx, seq_offsets)
-    T, E, S, k = shp.T, shp.E, shp.S, shp.k
-    _check("moe_route", load().moe_route(
-        ctypes.c_void_p(logits.data_ptr()), _typed(sel_bias, "sel_bias", torch.float32, (E,)), _mask_ptr(token_mask, T),
-        _typed(seq_offsets, "seq_offsets", torch.int32, (S + 1,)), ctypes.byref(shp), ctypes.byref(cfg),
-        _typed(topk_idx, "topk_idx", torch.int32, (T, k)), _typed(topk_w, "topk_w", torch.float32, (T, k)),
-        _typed(counts, "counts", torch.int32, (S, E)), _typed(seq_tokens, "seq_tokens", torch.int32, (S + 2,)),
-        _typed(losses, "losses", torch.float32, (2,)), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-        _stream(stream, logits)))
+    _check("moe_route", _module().route(logits, ctypes.addressof(cfg), topk_idx, topk_w, sel_bias, token_mask, seq_offsets,
+                                        counts, seq_tokens, losses, ws, _raw_stream(stream, logits)))
 
 
 def moe_route_backward(logits, cfg, topk_idx, dtopk_w, dlogits, token_mask=None, seq_offsets=None, counts=None,
                        seq_tokens=None, dlosses=None, stream=None):
     """Gradient of moe_route's topk_w and losses with respect to the logits, into dlogits [T, E]
     (dense, the logits' type)."""
-    shp = _route_shape(logits, topk_idx, seq_offsets)
-    T, E, S, k = shp.T, shp.E, shp.S, shp.k
-    _check("moe_route_backward", load().moe_route_backward(
-        ctypes.c_void_p(logits.data_ptr()), _mask_ptr(token_mask, T),
-        _typed(seq_offsets, "seq_offsets", torch.int32, (S + 1,)), ctypes.byref(shp), ctypes.byref(cfg),
-        _typed(topk_idx, "topk_idx", torch.int32, (T, k)), _typed(dtopk_w, "dtopk_w", torch.float32, (T, k)),
-        _typed(counts, "counts", torch.int32, (S, E)), _typed(seq_tokens, "seq_tokens", torch.int32, (S + 2,)),
-        _typed(dlosses, "dlosses", torch.float32, (2,)), _typed(dlogits, "dlogits", logits.dtype, (T, E)),
-        _stream(stream, logits)))
+    _check("moe_route_backward", _module().route_backward(
+        logits, ctypes.addressof(cfg), topk_idx, dtopk_w, dlogits, token_mask, seq_offsets, counts, seq_tokens, dlosses,
+        _raw_stream(stream, logits)))
 
 
 def moe_bias_update(bias, counts, rate, stream=None):
     """bias [E] or [L, E] += rate * sign(mean count - count), in place; counts int32 [S, E] or
     [L, S, E], added over the sequences."""
-    if bias.dim() not in (1, 2) or counts.dim() != bias.dim() + 1:
-        raise ValueError("bias must be [E] and counts [S, E], or [L, E] and [L, S, E]")
-    L, E, S = (1 if bias.dim() == 1 else bias.shape[0]), bias.shape[-1], counts.shape[-2]
-    if counts.shape[-1] != E or (bias.dim() == 2 and counts.shape[0] != L):
-        raise ValueError(f"bias is {tuple(bias.shape)}, counts {tuple(counts.shape)}")
-    _check("moe_bias_update", load().moe_bias_update(
-        _typed(bias, "bias", torch.float32, bias.shape), _typed(counts, "counts", torch.int32, counts.shape), L, S, E,
-        float(rate), _stream(stream, bias)))
+    _check("moe_bias_update", _module().bias_update(bias, counts, float(rate), _raw_stream(stream, bias)))
 
 
 # ------------------------------------------------------------------ lists of tensors
 
-def _gather(tensors, name, device, dtype=None, like=None, optional=False):
+def _gather(tensors, name, device, dtype=None, like=None, optional=False, apart=False):
     """A list's addresses, element counts and types as C arrays (bytes), checked to be dense
-    tensors on one device, of one type and like the parameters where asked."""
-    global _lists
-    if _lists is None:
-        try:
-            from . import _lists as native
-        except ImportError as e:
-            raise RuntimeError(f"{LISTS_PATH} is missing: build it first "
-                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
-        _lists = native
-    return _lists.gather(tensors, name, device, -1 if dtype is None else DTYPE_CODES[dtype], like, optional)
+    tensors on one device, and of one type, like the parameters, or apart where asked."""
+    return _module().gather(tensors, name, device, -1 if dtype is None else DTYPE_CODES[dtype], like, optional, apart)
 
 
 def _device_of(t):
@@ -585,6 +556,7 @@ def _device_of(t):
     return t.get_device()
 
 
+@functools.lru_cache(maxsize=256)
 def moe_tensors_workspace_size(n) -> int:
     size = ctypes.c_size_t()
     _check("moe_tensors_workspace_size", load().moe_tensors_workspace_size(n, ctypes.byref(size)))
@@ -608,7 +580,7 @@ def moe_grad_norm(grads, norm, ws, norm_type=2.0, stream=None):
 
 def moe_clip_grads(grads, max_norm, norm, ws, norm_type=2.0, stream=None):
     """The same norm, and every tensor times min(1, max_norm / (norm + 1e-6)), in place."""
-    ptr, numel, dtype = _gather(grads, "grads", _device_of(norm))
+    ptr, numel, dtype = _gather(grads, "grads", _device_of(norm), apart=True)
     _check("moe_clip_grads", load().moe_clip_grads(
         ptr, numel, dtype, len(grads), _norm_code(norm_type), float(max_norm),
         _typed(norm, "norm", torch.float32, (1,)), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream, norm)))
@@ -618,11 +590,11 @@ def moe_adamw(params, grads, exp_avg, exp_avg_sq, lr, step, ws, cfg, masters=Non
     """One AdamW step over lists of tensors, in place; masters: a list with an fp32 tensor or None
     for each parameter, or None."""
     device = _device_of(lr)
-    p, numel, p_dtype = _gather(params, "params", device)
+    p, numel, p_dtype = _gather(params, "params", device, apart=True)
     g, _, g_dtype = _gather(grads, "grads", device, None, params)
-    m = _gather(exp_avg, "exp_avg", device, torch.float32, params)[0]
-    v = _gather(exp_avg_sq, "exp_avg_sq", device, torch.float32, params)[0]
-    x = None if masters is None else _gather(masters, "masters", device, torch.float32, params, True)[0]
+    m = _gather(exp_avg, "exp_avg", device, torch.float32, params, apart=True)[0]
+    v = _gather(exp_avg_sq, "exp_avg_sq", device, torch.float32, params, apart=True)[0]
+    x = None if masters is None else _gather(masters, "masters", device, torch.float32, params, True, True)[0]
     _check("moe_adamw", load().moe_adamw(
         p, p_dtype, g, g_dtype, m, v, x, numel, len(params), ctypes.byref(cfg), _typed(lr, "lr", torch.float32, (1,)),
         _typed(step, "step", torch.int32, (1,)), _typed(norm, "norm", torch.float32, (1,)), _ptr(ws),

@@ -3,8 +3,8 @@
 Each .cu under csrc/ is compiled to an object in parallel, then linked into
 ``moe_expert_router_gb300/libmoe.so`` with the CUDA runtime linked statically,
 so the library depends on nothing but the driver at run time. Beside it,
-``_lists.so`` is a small CPython module over torch's C++ headers (csrc/lists.cpp)
-that the binding reads lists of tensors with.
+``_native.so`` is a small CPython module over torch's C++ headers (csrc/native.cpp)
+for the binding's calls whose cost on the host shows.
 """
 from __future__ import annotations
 
@@ -21,8 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libmoe.so")
-LISTS_SRC = os.path.join(CSRC, "lists.cpp")
-LISTS_PATH = os.path.join(PKG, "_lists.so")
+NATIVE_SRC = os.path.join(CSRC, "native.cpp")
+NATIVE_PATH = os.path.join(PKG, "_native.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -47,27 +47,27 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(LISTS_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(NATIVE_PATH):
         return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(LISTS_PATH))
-    return all(os.path.getmtime(p) <= t for p in _deps() + [LISTS_SRC])
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(NATIVE_PATH))
+    return all(os.path.getmtime(p) <= t for p in _deps() + [NATIVE_SRC])
 
 
-def _build_lists():
-    """Compile _lists.so against the installed torch."""
+def _build_native():
+    """Compile _native.so against the installed torch."""
     import torch
     root = os.path.dirname(os.path.abspath(torch.__file__))
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], INCLUDE, os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
     lib = os.path.join(root, "lib")
-    tmp = LISTS_PATH + f".tmp{os.getpid()}"
+    tmp = NATIVE_PATH + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *[a for p in inc for a in ("-isystem", p)],
-           LISTS_SRC, "-o", tmp, "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+           NATIVE_SRC, "-o", tmp, "-L", lib, f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"g++ failed on lists.cpp:\n{res.stderr}")
-    os.replace(tmp, LISTS_PATH)
+        raise RuntimeError(f"g++ failed on native.cpp:\n{res.stderr}")
+    os.replace(tmp, NATIVE_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -87,9 +87,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return obj, res.stderr
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        lists = ex.submit(_build_lists)
+        native = ex.submit(_build_native)
         results = list(ex.map(compile_one, _sources()))
-        lists.result()
+        native.result()
     if verbose or ptxas_info:
         for _, log in results:
             if log.strip():

@@ -1658,7 +1658,7 @@ moe_status_t moe_clip_grads(void *const *grads, const int64_t *numel, const int3
                             void *stream) {
     moe_status_t r = check_list(grads, numel, dtype, n);
     if (r != MOE_OK) return r;
-    if ((n > 0 && dtype == nullptr) || norm_type < MOE_NORM_INF || norm_type > MOE_NORM_2 || !(max_norm > 0.0f))
+    if ((n > 0 && dtype == nullptr) || norm_type < MOE_NORM_INF || norm_type > MOE_NORM_2 || !(max_norm >= 0.0f))
         return MOE_ERR_INVALID_ARG;
     if (norm == nullptr || !aligned_to(norm, 4)) return MOE_ERR_INVALID_ARG;
     if ((r = check_list_ws(ws, ws_bytes, n)) != MOE_OK) return r;

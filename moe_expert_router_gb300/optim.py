@@ -20,21 +20,19 @@ def _lists(tensors, name):
     return tensors
 
 
-def _distinct(tensors, name):
-    if len({t.data_ptr() for t in tensors if t.numel()}) != sum(1 for t in tensors if t.numel()):
-        raise ValueError(f"{name} hold the same memory twice")
-
-
-def _workspace(n, device):
-    return torch.empty(B.moe_tensors_workspace_size(n), dtype=torch.uint8, device=device)
+def _scratch(n, device):
+    """Workspace for n tensors, and the norm [1] at its end: one allocation."""
+    ws = torch.empty((B.moe_tensors_workspace_size(n) // 4 + 4,), dtype=torch.float32, device=device)
+    norm = ws[-4:-3]
+    return ws, norm
 
 
 def grad_norm(grads, norm_type=2.0):
     """The norm (norm_type 1, 2 or inf) of all elements of `grads` together, an fp32 scalar
     tensor on their device."""
     grads = _lists(grads, "grads")
-    norm = torch.empty((1,), dtype=torch.float32, device=grads[0].device)
-    B.moe_grad_norm(grads, norm, _workspace(len(grads), norm.device), norm_type)
+    ws, norm = _scratch(len(grads), grads[0].device)
+    B.moe_grad_norm(grads, norm, ws, norm_type)
     return norm[0]
 
 
@@ -42,9 +40,8 @@ def clip_grad_norm_(grads, max_norm, norm_type=2.0):
     """Multiplies every tensor of `grads` in place by min(1, max_norm / (norm + 1e-6)) and
     returns the norm before that, as a tensor on the device."""
     grads = _lists(grads, "grads")
-    _distinct(grads, "grads")
-    norm = torch.empty((1,), dtype=torch.float32, device=grads[0].device)
-    B.moe_clip_grads(grads, max_norm, norm, _workspace(len(grads), norm.device), norm_type)
+    ws, norm = _scratch(len(grads), grads[0].device)
+    B.moe_clip_grads(grads, max_norm, norm, ws, norm_type)
     return norm[0]
 
 
@@ -55,12 +52,11 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr, masters=None, betas
     taken times min(1, max_norm / (their global 2-norm + 1e-6)), without being changed. Returns
     the norm as a tensor (None where max_norm is 0 and skip_nonfinite is False)."""
     params, grads = _lists(params, "params"), _lists(grads, "grads")
-    _distinct(params, "params")
-    norm = None
-    if max_norm > 0.0 or skip_nonfinite:
-        norm = torch.empty((1,), dtype=torch.float32, device=params[0].device)
+    ws, norm = _scratch(len(params), params[0].device)
+    if not (max_norm > 0.0 or skip_nonfinite):
+        norm = None
     cfg = B.AdamWCfg(betas[0], betas[1], eps, weight_decay, max_norm, int(bool(skip_nonfinite)))
-    B.moe_adamw(params, grads, exp_avg, exp_avg_sq, lr, step, _workspace(len(params), params[0].device), cfg, masters,
+    B.moe_adamw(params, grads, exp_avg, exp_avg_sq, lr, step, ws, cfg, masters,
                 norm)
     return None if norm is None else norm[0]
 

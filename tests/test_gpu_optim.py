@@ -128,7 +128,13 @@ def test_dense_layouts_and_refusals():
     with pytest.raises(ValueError):
         optim.grad_norm([x, x.cpu()])
     with pytest.raises(B.MoEError):
-        optim.clip_grad_norm_([x], 0.0)
+        optim.clip_grad_norm_([x], -1.0)
+    y = x.clone()
+    optim.clip_grad_norm_([y], 0.0)
+    assert (y == 0).all()
+    for shared in ([x, x], [x, x[5:]], [x[1:], x[:2]]):    # the same memory twice
+        with pytest.raises(ValueError):
+            optim.clip_grad_norm_(shared, 1.0)
     o = optim.AdamW([x])
     for g in (x.cpu(), x[:5], x.double(), x.permute(2, 0, 1).contiguous()):
         with pytest.raises((ValueError, TypeError)):
