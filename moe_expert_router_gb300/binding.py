@@ -486,7 +486,8 @@ def _module():
             raise RuntimeError(f"{NATIVE_PATH} is missing: build it first "
                                "(python -c 'import __graft_entry__ as g; g.build()')") from e
         native.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in
-                      (lib.moe_route, lib.moe_route_backward, lib.moe_bias_update)])
+                      (lib.moe_route, lib.moe_route_backward, lib.moe_bias_update, lib.moe_grad_norm,
+                       lib.moe_clip_grads, lib.moe_adamw)])
         _native = native
     return _native
 
@@ -497,17 +498,6 @@ def _raw_stream(stream, like):
         return stream.cuda_stream
     device = like.get_device()
     return torch._C._cuda_getCurrentRawStream(device) if device >= 0 else 0
-
-
-def _typed(t, name, dtype, shape):
-    """Checks an optional dense tensor and gives its address."""
-    if t is None:
-        return None
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    return _ptr(t)
 
 
 @functools.lru_cache(maxsize=256)
@@ -544,18 +534,6 @@ def moe_bias_update(bias, counts, rate, stream=None):
 
 # ------------------------------------------------------------------ lists of tensors
 
-def _gather(tensors, name, device, dtype=None, like=None, optional=False, apart=False):
-    """A list's addresses, element counts and types as C arrays (bytes), checked to be dense
-    tensors on one device, and of one type, like the parameters, or apart where asked."""
-    return _module().gather(tensors, name, device, -1 if dtype is None else DTYPE_CODES[dtype], like, optional, apart)
-
-
-def _device_of(t):
-    if not t.is_cuda:
-        raise ValueError("libmoe takes CUDA tensors only")
-    return t.get_device()
-
-
 @functools.lru_cache(maxsize=256)
 def moe_tensors_workspace_size(n) -> int:
     size = ctypes.c_size_t()
@@ -572,30 +550,17 @@ def _norm_code(norm_type):
 
 def moe_grad_norm(grads, norm, ws, norm_type=2.0, stream=None):
     """norm [1] = the norm of all the tensors' elements together."""
-    ptr, numel, dtype = _gather(grads, "grads", _device_of(norm))
-    _check("moe_grad_norm", load().moe_grad_norm(
-        ptr, numel, dtype, len(grads), _norm_code(norm_type), _typed(norm, "norm", torch.float32, (1,)), _ptr(ws),
-        ws.numel() * ws.element_size(), _stream(stream, norm)))
+    _check("moe_grad_norm", _module().grad_norm(grads, _norm_code(norm_type), norm, ws, _raw_stream(stream, norm)))
 
 
 def moe_clip_grads(grads, max_norm, norm, ws, norm_type=2.0, stream=None):
     """The same norm, and every tensor times min(1, max_norm / (norm + 1e-6)), in place."""
-    ptr, numel, dtype = _gather(grads, "grads", _device_of(norm), apart=True)
-    _check("moe_clip_grads", load().moe_clip_grads(
-        ptr, numel, dtype, len(grads), _norm_code(norm_type), float(max_norm),
-        _typed(norm, "norm", torch.float32, (1,)), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream, norm)))
+    _check("moe_clip_grads", _module().clip_grads(grads, _norm_code(norm_type), float(max_norm), norm, ws,
+                                                  _raw_stream(stream, norm)))
 
 
 def moe_adamw(params, grads, exp_avg, exp_avg_sq, lr, step, ws, cfg, masters=None, norm=None, stream=None):
     """One AdamW step over lists of tensors, in place; masters: a list with an fp32 tensor or None
     for each parameter, or None."""
-    device = _device_of(lr)
-    p, numel, p_dtype = _gather(params, "params", device, apart=True)
-    g, _, g_dtype = _gather(grads, "grads", device, None, params)
-    m = _gather(exp_avg, "exp_avg", device, torch.float32, params, apart=True)[0]
-    v = _gather(exp_avg_sq, "exp_avg_sq", device, torch.float32, params, apart=True)[0]
-    x = None if masters is None else _gather(masters, "masters", device, torch.float32, params, True, True)[0]
-    _check("moe_adamw", load().moe_adamw(
-        p, p_dtype, g, g_dtype, m, v, x, numel, len(params), ctypes.byref(cfg), _typed(lr, "lr", torch.float32, (1,)),
-        _typed(step, "step", torch.int32, (1,)), _typed(norm, "norm", torch.float32, (1,)), _ptr(ws),
-        ws.numel() * ws.element_size(), _stream(stream, lr)))
+    _check("moe_adamw", _module().adamw(params, grads, exp_avg, exp_avg_sq, masters, ctypes.addressof(cfg), lr, step, norm,
+                                        ws, _raw_stream(stream, lr)))

@@ -3,17 +3,10 @@
 // Python and ctypes), and lists of tensors, 0.4 us a tensor through Python's attributes.
 // It reads and checks the tensors and calls libmoe's C entry points; nothing else.
 //
-// CPython module `_native`:
-//   bind(moe_route, moe_route_backward, moe_bias_update): the entry points' addresses
-//   route / route_backward / bias_update: the calls, from tensors (None where the C call
-//       takes NULL), with the address of a moe_router_cfg_t and a stream; their status
-//   gather(tensors, name, device, dtype, like, optional, apart)
-//       -> (addresses u64, counts i64, types i32) as bytes in the machine's order
-//     tensors: list or tuple of torch tensors (with `optional`, or None: address 0)
-//     dtype: a MOE_DTYPE_* code that all must have, or -1 for any of them
-//     like: a list of tensors whose shapes and order in memory they must have, or None
-//     apart: they must not overlap (they are written)
-// Raises TypeError / ValueError as the rest of the binding does.
+// CPython module `_native`: bind(addresses of the entry points), then the calls of the same
+// names, from tensors and lists of tensors (None where the C call takes NULL), the address of
+// a configuration, and a stream; they return the call's status. Raises TypeError / ValueError
+// as the rest of the binding does.
 #define PY_SSIZE_T_CLEAN
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -30,6 +23,9 @@ struct Refused {};                          // a Python error is set
 decltype(&moe_route) g_route = nullptr;
 decltype(&moe_route_backward) g_route_backward = nullptr;
 decltype(&moe_bias_update) g_bias_update = nullptr;
+decltype(&moe_grad_norm) g_grad_norm = nullptr;
+decltype(&moe_clip_grads) g_clip_grads = nullptr;
+decltype(&moe_adamw) g_adamw = nullptr;
 
 int code_of(at::ScalarType t) {
     switch (t) {
@@ -163,63 +159,128 @@ PyObject *bias_update(PyObject *const *a) {
                                          static_cast<float>(rate), handle(a[3])));
 }
 
-PyObject *bind(PyObject *const *a) {
-    g_route = reinterpret_cast<decltype(g_route)>(handle(a[0]));
-    g_route_backward = reinterpret_cast<decltype(g_route_backward)>(handle(a[1]));
-    g_bias_update = reinterpret_cast<decltype(g_bias_update)>(handle(a[2]));
-    Py_RETURN_NONE;
-}
+// A list's addresses, element counts and types, checked: dense CUDA tensors on one device,
+// of the type `dtype` (-1: any of the three); like those of `like` in shape and order in
+// memory, where that is not null; with `optional` or None (address 0); not overlapping,
+// where they are written.
+struct List {
+    std::vector<void *> ptr;
+    std::vector<int64_t> numel;
+    std::vector<int32_t> type;
+};
 
-// tensors, name, device, dtype, like, optional, apart
-PyObject *gather(PyObject *const *a) {
-    PyObject *list = a[0], *like = a[4];
-    const char *name = PyUnicode_AsUTF8(a[1]);
-    if (name == nullptr) throw Refused();
-    const long device = PyLong_AsLong(a[2]), dtype = PyLong_AsLong(a[3]);
-    const bool optional = PyObject_IsTrue(a[5]), apart = PyObject_IsTrue(a[6]);
-    if (PyErr_Occurred()) throw Refused();
-    if (!(PyList_Check(list) || PyTuple_Check(list)) || !(like == Py_None || PyList_Check(like) || PyTuple_Check(like)))
-        refuse(PyExc_TypeError, "%s must be a list of tensors", name);
-    const Py_ssize_t n = PySequence_Fast_GET_SIZE(list);
-    if (like != Py_None && PySequence_Fast_GET_SIZE(like) != n)
+bool is_list(PyObject *o) { return PyList_Check(o) || PyTuple_Check(o); }
+
+List list_of(PyObject *o, const char *name, int device, int dtype, PyObject *like, bool optional, bool written) {
+    if (!is_list(o)) refuse(PyExc_TypeError, "%s must be a list of tensors", name);
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(o);
+    if (like != nullptr && PySequence_Fast_GET_SIZE(like) != n)
         refuse(PyExc_ValueError, "%s must be as many as the parameters", name);
-    std::vector<uint64_t> ptr(n);
-    std::vector<int64_t> numel(n);
-    std::vector<int32_t> type(n);
+    List l;
+    l.ptr.resize(n);
+    l.numel.resize(n);
+    l.type.resize(n);
     std::vector<std::pair<uint64_t, uint64_t>> range;
     bool sorted = true;
     for (Py_ssize_t i = 0; i < n; ++i) {
-        PyObject *o = PySequence_Fast_GET_ITEM(list, i);
-        if (optional && o == Py_None) continue;
-        const at::Tensor &t = tensor(o, name);
+        PyObject *item = PySequence_Fast_GET_ITEM(o, i);
+        if (optional && item == Py_None) continue;
+        const at::Tensor &t = tensor(item, name);
         if (!t.is_cuda() || t.get_device() != device) refuse(PyExc_ValueError, "%s must be CUDA tensors on one device", name);
         const int code = code_of(t.scalar_type());
         if (code < 0) refuse(PyExc_TypeError, "%s must be float32, bfloat16 or float16", name);
         if (dtype >= 0 && code != dtype) refuse(PyExc_TypeError, "%s must be %s", name, kNames[dtype]);
         if (t.layout() != at::kStrided || !(t.is_contiguous() || t.is_non_overlapping_and_dense()))
             refuse(PyExc_ValueError, "%s must be dense", name);
-        if (like != Py_None) {
+        if (like != nullptr) {
             const at::Tensor &p = tensor(PySequence_Fast_GET_ITEM(like, i), "params");
             if (t.sizes() != p.sizes()) refuse(PyExc_ValueError, "%s must have the parameters' shapes", name);
             if (!(t.is_contiguous() && p.is_contiguous()) && t.strides() != p.strides())
                 refuse(PyExc_ValueError, "%s must have the parameters' order in memory", name);
         }
-        ptr[i] = reinterpret_cast<uint64_t>(t.data_ptr());
-        numel[i] = t.numel();
-        type[i] = code;
-        if (apart && numel[i] > 0) {
-            const uint64_t end = ptr[i] + static_cast<uint64_t>(numel[i]) * (code == MOE_DTYPE_F32 ? 4 : 2);
-            sorted = sorted && (range.empty() || range.back().first <= ptr[i]);
-            range.emplace_back(ptr[i], end);
+        l.ptr[i] = t.data_ptr();
+        l.numel[i] = t.numel();
+        l.type[i] = code;
+        if (written && l.numel[i] > 0) {
+            const uint64_t at = reinterpret_cast<uint64_t>(l.ptr[i]);
+            sorted = sorted && (range.empty() || range.back().first <= at);
+            range.emplace_back(at, at + static_cast<uint64_t>(l.numel[i]) * (code == MOE_DTYPE_F32 ? 4 : 2));
         }
     }
     if (!sorted) std::sort(range.begin(), range.end());
     for (size_t i = 1; i < range.size(); ++i)
         if (range[i].first < range[i - 1].second) refuse(PyExc_ValueError, "%s hold the same memory twice", name);
-    // N takes the references over; a null among them (no memory) makes the tuple's error
-    return Py_BuildValue("(NNN)", PyBytes_FromStringAndSize(reinterpret_cast<const char *>(ptr.data()), n * 8),
-                         PyBytes_FromStringAndSize(reinterpret_cast<const char *>(numel.data()), n * 8),
-                         PyBytes_FromStringAndSize(reinterpret_cast<const char *>(type.data()), n * 4));
+    return l;
+}
+
+struct Scratch {
+    void *ptr;
+    size_t bytes;
+};
+Scratch scratch(PyObject *o) {
+    const at::Tensor &t = tensor(o, "ws");
+    if (!t.is_cuda() || !t.is_contiguous()) refuse(PyExc_ValueError, "ws must be a contiguous CUDA tensor");
+    return {t.data_ptr(), t.nbytes()};
+}
+
+int device_of(PyObject *o, const char *name) {
+    const at::Tensor &t = tensor(o, name);
+    if (!t.is_cuda()) refuse(PyExc_ValueError, "libmoe takes CUDA tensors only");
+    return t.get_device();
+}
+
+long whole(PyObject *o) {
+    const long v = PyLong_AsLong(o);
+    if (v == -1 && PyErr_Occurred()) throw Refused();
+    return v;
+}
+
+// grads, norm_type, norm, ws, stream
+PyObject *grad_norm(PyObject *const *a) {
+    const List g = list_of(a[0], "grads", device_of(a[2], "norm"), -1, nullptr, false, false);
+    const Scratch ws = scratch(a[3]);
+    return PyLong_FromLong(g_grad_norm(g.ptr.data(), g.numel.data(), g.type.data(), static_cast<int32_t>(g.ptr.size()),
+                                       static_cast<int32_t>(whole(a[1])), as<float>(address(a[2], "norm", at::kFloat, {1})),
+                                       ws.ptr, ws.bytes, handle(a[4])));
+}
+
+// grads, norm_type, max_norm, norm, ws, stream
+PyObject *clip_grads(PyObject *const *a) {
+    const List g = list_of(a[0], "grads", device_of(a[3], "norm"), -1, nullptr, false, true);
+    const Scratch ws = scratch(a[4]);
+    const double most = PyFloat_AsDouble(a[2]);
+    if (most == -1.0 && PyErr_Occurred()) throw Refused();
+    return PyLong_FromLong(g_clip_grads(g.ptr.data(), g.numel.data(), g.type.data(), static_cast<int32_t>(g.ptr.size()),
+                                        static_cast<int32_t>(whole(a[1])), static_cast<float>(most),
+                                        as<float>(address(a[3], "norm", at::kFloat, {1})), ws.ptr, ws.bytes, handle(a[5])));
+}
+
+// params, grads, exp_avg, exp_avg_sq, masters, cfg, lr, step, norm, ws, stream
+PyObject *adamw(PyObject *const *a) {
+    const int device = device_of(a[6], "lr");
+    const List p = list_of(a[0], "params", device, -1, nullptr, false, true);
+    const List g = list_of(a[1], "grads", device, -1, a[0], false, false);
+    const List m = list_of(a[2], "exp_avg", device, MOE_DTYPE_F32, a[0], false, true);
+    const List v = list_of(a[3], "exp_avg_sq", device, MOE_DTYPE_F32, a[0], false, true);
+    List x;
+    if (a[4] != Py_None) x = list_of(a[4], "masters", device, MOE_DTYPE_F32, a[0], true, true);
+    const Scratch ws = scratch(a[9]);
+    auto floats = [](const List &l) { return reinterpret_cast<float *const *>(l.ptr.data()); };
+    return PyLong_FromLong(g_adamw(p.ptr.data(), p.type.data(), g.ptr.data(), g.type.data(), floats(m), floats(v),
+                                   a[4] != Py_None ? floats(x) : nullptr, p.numel.data(), static_cast<int32_t>(p.ptr.size()),
+                                   as<const moe_adamw_cfg_t>(handle(a[5])), as<float>(address(a[6], "lr", at::kFloat, {1})),
+                                   as<int32_t>(address(a[7], "step", at::kInt, {1})),
+                                   as<float>(address(a[8], "norm", at::kFloat, {1})), ws.ptr, ws.bytes, handle(a[10])));
+}
+
+PyObject *bind(PyObject *const *a) {
+    g_route = reinterpret_cast<decltype(g_route)>(handle(a[0]));
+    g_route_backward = reinterpret_cast<decltype(g_route_backward)>(handle(a[1]));
+    g_bias_update = reinterpret_cast<decltype(g_bias_update)>(handle(a[2]));
+    g_grad_norm = reinterpret_cast<decltype(g_grad_norm)>(handle(a[3]));
+    g_clip_grads = reinterpret_cast<decltype(g_clip_grads)>(handle(a[4]));
+    g_adamw = reinterpret_cast<decltype(g_adamw)>(handle(a[5]));
+    Py_RETURN_NONE;
 }
 
 // No C++ exception leaves the module: libtorch's (a tensor without storage, for one) end as Python's.
@@ -241,11 +302,13 @@ PyMethodDef method(const char *name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(&call<F, N>)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef kMethods[] = {method<bind, 3>("bind"),
+PyMethodDef kMethods[] = {method<bind, 6>("bind"),
                           method<route, 12>("route"),
                           method<route_backward, 11>("route_backward"),
                           method<bias_update, 4>("bias_update"),
-                          method<gather, 7>("gather"),
+                          method<grad_norm, 5>("grad_norm"),
+                          method<clip_grads, 6>("clip_grads"),
+                          method<adamw, 11>("adamw"),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

@@ -14,24 +14,25 @@ from . import binding as B
 
 
 def _lists(tensors, name):
-    tensors = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
+    if isinstance(tensors, torch.Tensor):
+        return [tensors]
+    tensors = tensors if isinstance(tensors, (list, tuple)) else list(tensors)
     if not tensors:
         raise ValueError(f"{name} is empty")
     return tensors
 
 
-def _scratch(n, device):
-    """Workspace for n tensors, and the norm [1] at its end: one allocation."""
-    ws = torch.empty((B.moe_tensors_workspace_size(n) // 4 + 4,), dtype=torch.float32, device=device)
-    norm = ws[-4:-3]
-    return ws, norm
+def _scratch(n, like):
+    """Workspace for n tensors whose last element is for the norm, and that as [1]."""
+    ws = torch.empty((B.moe_tensors_workspace_size(n) // 4 + 4,), dtype=torch.float32, device=like.device)
+    return ws, ws[-1:]
 
 
 def grad_norm(grads, norm_type=2.0):
     """The norm (norm_type 1, 2 or inf) of all elements of `grads` together, an fp32 scalar
     tensor on their device."""
     grads = _lists(grads, "grads")
-    ws, norm = _scratch(len(grads), grads[0].device)
+    ws, norm = _scratch(len(grads), grads[0])
     B.moe_grad_norm(grads, norm, ws, norm_type)
     return norm[0]
 
@@ -40,7 +41,7 @@ def clip_grad_norm_(grads, max_norm, norm_type=2.0):
     """Multiplies every tensor of `grads` in place by min(1, max_norm / (norm + 1e-6)) and
     returns the norm before that, as a tensor on the device."""
     grads = _lists(grads, "grads")
-    ws, norm = _scratch(len(grads), grads[0].device)
+    ws, norm = _scratch(len(grads), grads[0])
     B.moe_clip_grads(grads, max_norm, norm, ws, norm_type)
     return norm[0]
 
@@ -52,12 +53,11 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr, masters=None, betas
     taken times min(1, max_norm / (their global 2-norm + 1e-6)), without being changed. Returns
     the norm as a tensor (None where max_norm is 0 and skip_nonfinite is False)."""
     params, grads = _lists(params, "params"), _lists(grads, "grads")
-    ws, norm = _scratch(len(params), params[0].device)
+    ws, norm = _scratch(len(params), params[0])
     if not (max_norm > 0.0 or skip_nonfinite):
         norm = None
     cfg = B.AdamWCfg(betas[0], betas[1], eps, weight_decay, max_norm, int(bool(skip_nonfinite)))
-    B.moe_adamw(params, grads, exp_avg, exp_avg_sq, lr, step, ws, cfg, masters,
-                norm)
+    B.moe_adamw(params, grads, exp_avg, exp_avg_sq, lr, step, ws, cfg, masters, norm)
     return None if norm is None else norm[0]
 
 
@@ -72,7 +72,7 @@ class AdamW:
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, masters=True,
                  skip_nonfinite=False):
-        self.params = _lists(params, "params")
+        self.params = list(_lists(params, "params"))
         device = self.params[0].device
         self.betas, self.eps, self.weight_decay, self.skip_nonfinite = betas, eps, weight_decay, skip_nonfinite
         self.lr = torch.full((1,), lr, dtype=torch.float32, device=device)
@@ -89,7 +89,7 @@ class AdamW:
         at = [i for i, g in enumerate(grads) if g is not None]
         if not at:
             return None
-        return adamw_step([self.params[i].detach() for i in at], [grads[i] for i in at],
+        return adamw_step([self.params[i] for i in at], [grads[i] for i in at],
                           [self.exp_avg[i] for i in at], [self.exp_avg_sq[i] for i in at], self.step_count, self.lr,
                           [self.masters[i] for i in at], self.betas, self.eps, self.weight_decay, max_norm,
                           self.skip_nonfinite)
