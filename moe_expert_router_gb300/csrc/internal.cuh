@@ -379,6 +379,8 @@ struct RouteTiles {
     int64_t blocks, per_block;
 };
 RouteTiles route_tiles(int64_t T, int64_t E);
+// Experts of a slot's row: rows start 16-byte aligned.
+__host__ __device__ __forceinline__ int route_stride(int E) { return (E + 3) & ~3; }
 struct RouteLaunch {
     const void *logits;         // [T, E], rows ld elements apart
     int dtype;                  // MOE_DTYPE_*
@@ -397,7 +399,7 @@ struct RouteLaunch {
     int32_t *seq_tokens;        // [S + 2]
     float *losses;              // [2]; null: selection alone, none of the statistics
     int per_block;
-    float *part_score, *part_z; // [slots, E], [slots]
+    float *part_score, *part_z; // [slots, route_stride(E)], [slots]
     int32_t *part_count, *part_n;
     float *part_balance, *seq_z; // [S, ceil(E / 32)], [S]
     int32_t *ticket;

@@ -1435,8 +1435,9 @@ RouteWs route_layout(const moe_route_shape_t &s) {
     const size_t slots = static_cast<size_t>(tiles.blocks + s.S - 1);
     RouteWs w;
     w.score = 0;
-    w.count = w.score + align256(4 * slots * s.E);
-    w.z = w.count + align256(4 * slots * s.E);
+    const size_t row = 4 * static_cast<size_t>(route_stride(static_cast<int>(s.E)));
+    w.count = w.score + align256(slots * row);
+    w.z = w.count + align256(slots * row);
     w.n = w.z + align256(4 * slots);
     w.balance = w.n + align256(4 * slots);
     w.seq_z = w.balance + align256(4 * static_cast<size_t>(s.S) * ((s.E + 31) / 32));

@@ -455,9 +455,9 @@ route_kernel(const RouteLaunch p) {
     const int e0 = sub * V;
     const int t_begin = blockIdx.x * p.per_block;
     const int t_end = min(p.T, t_begin + p.per_block);
-    const bool by_score = !kShort && p.sel_bias != nullptr;
     const bool grouped = p.n_group > 1 && p.topk_group < p.n_group;
     const bool softmax = p.score_fn == MOE_SCORE_SOFTMAX;
+    const bool biased = !kShort && p.sel_bias != nullptr;
     const int gs = p.E / p.n_group, g_first = e0 / gs;
     float *own_row = buf + row * G * V;
     // a lane's biases stay in registers where there are few
@@ -465,15 +465,19 @@ route_kernel(const RouteLaunch p) {
     float held[kHeld], bias_max = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const float b = by_score && e0 + i < p.E ? __ldg(p.sel_bias + e0 + i) : 0.0f;
+        const float b = biased && e0 + i < p.E ? __ldg(p.sel_bias + e0 + i) : 0.0f;
         if (V <= 8) held[i % kHeld] = b;
         bias_max = fmaxf(bias_max, fabsf(b));
     }
     auto bias = [&](int i) {
         if (V <= 8) return held[i % kHeld];
-        return by_score && e0 + i < p.E ? __ldg(p.sel_bias + e0 + i) : 0.0f;
+        return biased && e0 + i < p.E ? __ldg(p.sel_bias + e0 + i) : 0.0f;
     };
-    if (by_score) bias_max = lanes_max<G>(gmask, bias_max);
+    if (biased) bias_max = lanes_max<G>(gmask, bias_max);
+    // with no bias, or none but zeros, the order is the logits' own, without a rounding; so is
+    // that of groups known by their best expert
+    const bool by_score = biased && !(bias_max == 0.0f);
+    const bool best_only = !by_score && p.group_topn == 1;
     int seq = 0;
     float acc[kShared ? 1 : V];
     float *own_sums = sums_buf + (kStats && kShared ? row * G * V + e0 : 0);
@@ -592,11 +596,13 @@ route_kernel(const RouteLaunch p) {
             }
             if (grouped) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) own_row[e0 + i] = (on >> i) & 1u ? s[i] + bias(i) : -INFINITY;
+                for (int i = 0; i < V; ++i)
+                    own_row[e0 + i] = (on >> i) & 1u ? (best_only ? l[i] : s[i] + bias(i)) : -INFINITY;
                 __syncwarp();
                 const float n = static_cast<float>(p.group_topn);
                 kept = kept_groups<G>(p, own_row, reinterpret_cast<float *>(slots.group[row]), sub, gmask,
-                                      2.0f * n * (rel * s_max + kUlp * (2.0f + n) * (s_max + bias_max)), near_groups);
+                                      best_only ? -1.0f : 2.0f * n * (rel * s_max + kUlp * (2.0f + n) * (s_max + bias_max)),
+                                      near_groups);
                 int g = g_first, next = (g + 1) * gs;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
@@ -745,12 +751,13 @@ route_kernel(const RouteLaunch p) {
             n_acc = 0;
             __syncthreads();
             const int64_t slot = static_cast<int64_t>(blockIdx.x) + seq;
-            for (int e = threadIdx.x; e < p.E; e += kThreads) {
+            const int ld = route_stride(p.E);        // no more than G V; past E the sums are 0
+            for (int e = threadIdx.x; e < ld; e += kThreads) {
                 float v = 0.0f;
 #pragma unroll
                 for (int r = 0; r < kRows; ++r) v += buf[r * G * V + e];
-                p.part_score[slot * p.E + e] = v;
-                p.part_count[slot * p.E + e] = hist[e];
+                p.part_score[slot * ld + e] = v;
+                p.part_count[slot * ld + e] = hist[e];
                 hist[e] = 0;
             }
             if (threadIdx.x == 0) {
@@ -770,66 +777,111 @@ route_kernel(const RouteLaunch p) {
 }
 
 // Counts, live tokens and the two terms from the slots. Block (32-expert chunk,
-// sequences blockIdx.y, + gridDim.y, ...): 16 rows of threads walk the sequence's
-// slots; the last block to finish adds the sequences' terms in order.
-constexpr int kReduceRows = 16;
+// sequences blockIdx.y, + gridDim.y, ...): 64 rows of 8 threads, four experts a thread, walk
+// the sequence's slots, eight loads of each array in flight; the last block to finish adds
+// the sequences' terms in order.
+constexpr int kReduceThreads = 512, kReduceWarps = kReduceThreads / 32;
 
-__global__ void __launch_bounds__(32 * kReduceRows)
+__device__ __forceinline__ float warp_total(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+__device__ __forceinline__ int warp_total(int v) { return __reduce_add_sync(0xffffffffu, v); }
+
+__global__ void __launch_bounds__(kReduceThreads)
 route_reduce_kernel(const RouteLaunch p) {
     griddep_wait();
-    __shared__ float sh_s[kReduceRows][32];
-    __shared__ int sh_c[kReduceRows][32];
-    __shared__ float sh_z[kReduceRows];
-    __shared__ int sh_n[kReduceRows];
+    __shared__ __align__(16) float sh_s[kReduceWarps][32];
+    __shared__ __align__(16) int sh_c[kReduceWarps][32];
+    __shared__ float sh_z[kReduceWarps];
+    __shared__ int sh_n[kReduceWarps], sh_used[kReduceWarps];
     __shared__ int last;
-    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-    const int e = blockIdx.x * 32 + lane;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = threadIdx.x >> 3;                // 0 .. 63
+    const int e4 = blockIdx.x * 32 + (threadIdx.x & 7) * 4;
+    constexpr int kRows = kReduceThreads / 8, kBatch = 8;
+    const int ld = route_stride(p.E);
     for (int q = blockIdx.y; q < p.S; q += gridDim.y) {
         const int a = q > 0 ? max(0, min(p.T, __ldg(p.seq_offsets + q))) : 0;
         const int z = q < p.S - 1 ? max(0, min(p.T, __ldg(p.seq_offsets + q + 1))) : p.T;
         const int b0 = a / p.per_block, b1 = z > a ? (z - 1) / p.per_block : b0 - 1;
-        float s = 0.0f, zs = 0.0f;
-        int c = 0, n = 0;
-#pragma unroll 4
-        for (int b = b0 + row; b <= b1; b += kReduceRows) {
-            const int64_t slot = static_cast<int64_t>(b) + q;
-            if (e < p.E) {
-                s += __ldcg(p.part_score + slot * p.E + e);
-                c += __ldcg(p.part_count + slot * p.E + e);
-            }
-        }
-        for (int b = b0 + threadIdx.x; b <= b1; b += 32 * kReduceRows) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        int4 c = make_int4(0, 0, 0, 0);
+        float zs = 0.0f;
+        int n = 0;
+        for (int b = b0 + threadIdx.x; b <= b1; b += kReduceThreads) {
             n += __ldcg(p.part_n + b + q);
             zs += __ldcg(p.part_z + b + q);
         }
-        for (int off = 16; off > 0; off >>= 1) {
-            n += __shfl_xor_sync(0xffffffffu, n, off);
-            zs += __shfl_xor_sync(0xffffffffu, zs, off);
+        if (e4 < ld) {
+            for (int b = b0 + row; b <= b1; b += kRows * kBatch) {
+                float4 sv[kBatch];
+                int4 cv[kBatch];
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    sv[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    cv[j] = make_int4(0, 0, 0, 0);
+                    if (b + j * kRows <= b1) {
+                        const int64_t at = (static_cast<int64_t>(b) + j * kRows + q) * ld + e4;
+                        sv[j] = __ldcg(reinterpret_cast<const float4 *>(p.part_score + at));
+                        cv[j] = __ldcg(reinterpret_cast<const int4 *>(p.part_count + at));
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    s.x += sv[j].x;
+                    s.y += sv[j].y;
+                    s.z += sv[j].z;
+                    s.w += sv[j].w;
+                    c.x += cv[j].x;
+                    c.y += cv[j].y;
+                    c.z += cv[j].z;
+                    c.w += cv[j].w;
+                }
+            }
         }
-        __syncthreads();
-        sh_s[row][lane] = s;
-        sh_c[row][lane] = c;
+        // the warp's four rows, then the warps in order
+#pragma unroll
+        for (int off = 8; off <= 16; off <<= 1) {
+            s.x += __shfl_xor_sync(0xffffffffu, s.x, off);
+            s.y += __shfl_xor_sync(0xffffffffu, s.y, off);
+            s.z += __shfl_xor_sync(0xffffffffu, s.z, off);
+            s.w += __shfl_xor_sync(0xffffffffu, s.w, off);
+            c.x += __shfl_xor_sync(0xffffffffu, c.x, off);
+            c.y += __shfl_xor_sync(0xffffffffu, c.y, off);
+            c.z += __shfl_xor_sync(0xffffffffu, c.z, off);
+            c.w += __shfl_xor_sync(0xffffffffu, c.w, off);
+        }
+        n = warp_total(n);
+        zs = warp_total(zs);
+        __syncthreads();                             // the last sequence's values are used
+        if (lane < 8) {
+            *reinterpret_cast<float4 *>(&sh_s[warp][lane * 4]) = s;
+            *reinterpret_cast<int4 *>(&sh_c[warp][lane * 4]) = c;
+        }
         if (lane == 0) {
-            sh_z[row] = zs;
-            sh_n[row] = n;
+            sh_z[warp] = zs;
+            sh_n[warp] = n;
         }
         __syncthreads();
-        if (row == 0) {
-            s = 0.0f;
-            c = 0;
+        if (warp == 0) {
+            const int e = blockIdx.x * 32 + lane;
+            float sum = 0.0f;
+            int count = 0;
             zs = 0.0f;
             n = 0;
 #pragma unroll
-            for (int r = 0; r < kReduceRows; ++r) {
-                s += sh_s[r][lane];
-                c += sh_c[r][lane];
+            for (int r = 0; r < kReduceWarps; ++r) {
+                sum += sh_s[r][lane];
+                count += sh_c[r][lane];
                 zs += sh_z[r];
                 n += sh_n[r];
             }
-            if (e < p.E) p.counts[static_cast<int64_t>(q) * p.E + e] = c;
+            if (e < p.E) p.counts[static_cast<int64_t>(q) * p.E + e] = count;
+            else sum = 0.0f;
             const float nf = static_cast<float>(max(n, 1));
-            float term = (s / nf) * (static_cast<float>(c) / (nf * static_cast<float>(p.k)));
-            for (int off = 16; off > 0; off >>= 1) term += __shfl_xor_sync(0xffffffffu, term, off);
+            const float term = warp_total((sum / nf) * (static_cast<float>(count) / (nf * static_cast<float>(p.k))));
             if (lane == 0) {
                 p.part_balance[static_cast<int64_t>(q) * gridDim.x + blockIdx.x] = term;
                 if (blockIdx.x == 0) {
@@ -849,24 +901,22 @@ route_reduce_kernel(const RouteLaunch p) {
     float bal = 0.0f, zs = 0.0f;
     int n = 0, used = 0;
     const int64_t terms = static_cast<int64_t>(p.S) * gridDim.x;
-    for (int64_t i = threadIdx.x; i < terms; i += 32 * kReduceRows) bal += __ldcg(p.part_balance + i);
-    for (int q = threadIdx.x; q < p.S; q += 32 * kReduceRows) {
+    for (int64_t i = threadIdx.x; i < terms; i += kReduceThreads) bal += __ldcg(p.part_balance + i);
+    for (int q = threadIdx.x; q < p.S; q += kReduceThreads) {
         const int m = __ldcg(p.seq_tokens + q);
         n += m;
         used += m > 0;
         zs += __ldcg(p.seq_z + q);
     }
-    for (int off = 16; off > 0; off >>= 1) {
-        bal += __shfl_xor_sync(0xffffffffu, bal, off);
-        zs += __shfl_xor_sync(0xffffffffu, zs, off);
-        n += __shfl_xor_sync(0xffffffffu, n, off);
-        used += __shfl_xor_sync(0xffffffffu, used, off);
-    }
+    bal = warp_total(bal);
+    zs = warp_total(zs);
+    n = warp_total(n);
+    used = warp_total(used);
     if (lane == 0) {
-        sh_s[0][row] = bal;
-        sh_z[row] = zs;
-        sh_n[row] = n;
-        sh_c[0][row] = used;
+        sh_s[warp][0] = bal;
+        sh_z[warp] = zs;
+        sh_n[warp] = n;
+        sh_used[warp] = used;
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -874,11 +924,11 @@ route_reduce_kernel(const RouteLaunch p) {
         zs = 0.0f;
         n = 0;
         used = 0;
-        for (int r = 0; r < kReduceRows; ++r) {
-            bal += sh_s[0][r];
+        for (int r = 0; r < kReduceWarps; ++r) {
+            bal += sh_s[r][0];
             zs += sh_z[r];
             n += sh_n[r];
-            used += sh_c[0][r];
+            used += sh_used[r];
         }
         p.seq_tokens[p.S] = n;
         p.seq_tokens[p.S + 1] = used;
@@ -1181,7 +1231,7 @@ cudaError_t launch_route(const RouteLaunch &p, cudaStream_t st) {
     if (err != cudaSuccess || p.losses == nullptr) return err;
     const int chunks = (p.E + 31) / 32;
     const int seqs = p.S < 1024 ? p.S : 1024;
-    err = launch_dep(route_reduce_kernel, dim3(chunks, seqs), dim3(32 * kReduceRows), 0, st, p);
+    err = launch_dep(route_reduce_kernel, dim3(chunks, seqs), dim3(kReduceThreads), 0, st, p);
     note_launches(1);
     return err;
 }
