@@ -393,6 +393,7 @@ struct RouteLaunch {
     int score_fn, normalize;
     float scale;
     int n_group, topk_group, group_topn;
+    int group_lanes;            // lanes of a group where it is whole lanes, else 0 (launch_route sets it)
     int32_t *topk_idx;
     float *topk_w;
     int32_t *counts;            // [S, E]

@@ -127,14 +127,26 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// A float's bits in an order that unsigned compares keep; 0 is below every number.
-__device__ __forceinline__ uint32_t order_key(float v) {
-    const uint32_t u = __float_as_uint(v + 0.0f);       // -0 and 0 tie
-    return v != v ? 0u : ((u >> 31) ? ~u : (u | 0x80000000u));
+__device__ __forceinline__ float rcp_fast(float x) {       // 1 ulp
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
-__device__ __forceinline__ float key_value(uint32_t k) {
-    return __uint_as_float((k >> 31) ? (k & 0x7fffffffu) : ~k);
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN where either is
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
 }
+
+// A float's bits in the order of signed compares. -0 and 0 tie; NaN takes -inf's key, the
+// lowest, which an expert that is off has. Keys below kFirst are not chosen.
+__device__ __forceinline__ int order_key(float v) {
+    const int u = __float_as_int(fmaxf(v + 0.0f, -INFINITY));
+    return u ^ ((u >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float key_value(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
+constexpr int kFirst = static_cast<int>(0x80800000u);      // of the lowest finite value
+constexpr int kGone = static_cast<int>(0x80000000u);
 
 template <int G, typename F, typename X>
 __device__ __forceinline__ X lanes_reduce(unsigned mask, X v, F f) {
@@ -143,12 +155,22 @@ __device__ __forceinline__ X lanes_reduce(unsigned mask, X v, F f) {
     return v;
 }
 template <int G>
+__device__ __forceinline__ unsigned lanes_or(unsigned mask, unsigned v) {
+    if constexpr (G == 32) return __reduce_or_sync(0xffffffffu, v);
+    return lanes_reduce<G>(mask, v, [](unsigned a, unsigned b) { return a | b; });
+}
+template <int G>
 __device__ __forceinline__ float lanes_sum(unsigned mask, float v) {
     return lanes_reduce<G>(mask, v, [](float a, float b) { return a + b; });
 }
 template <int G>
 __device__ __forceinline__ float lanes_max(unsigned mask, float v) {
     return lanes_reduce<G>(mask, v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int G>
+__device__ __forceinline__ int lanes_max_key(unsigned mask, int v) {
+    if constexpr (G == 32) return __reduce_max_sync(0xffffffffu, v);
+    return lanes_reduce<G>(mask, v, [](int a, int b) { return max(a, b); });
 }
 template <int G>
 __device__ __forceinline__ uint32_t lanes_max_u32(unsigned mask, uint32_t v) {
@@ -165,7 +187,7 @@ struct Slots {
     static constexpr int kRows = kBlock<V> / G;
     int idx[kRows][kMaxK + 1];
     float s[kRows][kMaxK + 1];
-    uint32_t key[kRows][kMaxK + 1];
+    int key[kRows][kMaxK + 1];
     double group[kRows][kMaxGroups];
 };
 
@@ -344,14 +366,10 @@ __device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int 
     __syncwarp(gmask);
 }
 
-// The groups of one token that stay, as bits; sel_row: its selection scores. A group is
-// searched by a power of two of lanes (four for eight groups of a 256-expert token), each
-// taking every fourth expert, and the lanes' best are merged. `near`: the groups that could
-// be on either side, where the last kept and the first dropped sum differ by no more than
-// `err`, the error of two sums; 0 where none could.
+// Sums of the groups' group_topn best of sel_row, a power of two of lanes to each group.
 template <int G>
-__device__ __forceinline__ unsigned kept_groups(const RouteLaunch &p, const float *sel_row, float *sums, int sub,
-                                                unsigned gmask, float err, unsigned &near) {
+__device__ __forceinline__ void search_groups(const RouteLaunch &p, const float *sel_row, float *sums, int sub,
+                                              unsigned gmask) {
     const int gs = p.E / p.n_group;
     int per = G;                                     // lanes of a group
     while (per > 1 && per * p.n_group > G) per >>= 1;
@@ -406,18 +424,50 @@ __device__ __forceinline__ unsigned kept_groups(const RouteLaunch &p, const floa
         }
         if (part == 0 && g < p.n_group) sums[g] = total;
     }
+}
+
+// The groups of one token that stay, as bits; v: the lane's selection scores (-inf: off).
+// Where a group is a power of two of whole lanes (`group_lanes`, from the host) and is known
+// by its best one or two, those are found in registers. Else a group is searched in `sel_row`
+// by a power of two of lanes, each taking every so many of its experts. `near`: the groups
+// that could be on either side, where the last kept and the first dropped sum differ by no
+// more than `err`, the error of two sums; 0 where none could.
+template <int G, int V>
+__device__ __forceinline__ unsigned kept_groups(const RouteLaunch &p, const float (&vals)[V], float *sel_row, float *sums,
+                                                int sub, unsigned gmask, float err, unsigned &near) {
+    if (p.group_lanes != 0) {
+        float a = -INFINITY, b = -INFINITY;          // the two best, a >= b
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            b = fmaxf(b, fminf(a, vals[i]));
+            a = fmaxf(a, vals[i]);
+        }
+        for (int off = 1; off < p.group_lanes; off <<= 1) {
+            const float oa = __shfl_xor_sync(gmask, a, off), ob = __shfl_xor_sync(gmask, b, off);
+            b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+            a = fmaxf(a, oa);
+        }
+        const int g = sub / p.group_lanes;
+        if (g * p.group_lanes == sub && g < p.n_group) sums[g] = p.group_topn == 2 && b > -INFINITY ? a + b : a;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) sel_row[sub * V + i] = vals[i];
+        __syncwarp();
+        search_groups<G>(p, sel_row, sums, sub, gmask);
+    }
     __syncwarp();
     unsigned kept = 0;
     for (int g = sub; g < p.n_group; g += G) {
         const float mine = sums[g];
         int before = 0;
+#pragma unroll 4
         for (int o = 0; o < p.n_group; ++o) before += sums[o] > mine || (sums[o] == mine && o < g);
         if (before < p.topk_group) kept |= 1u << g;
         // the sums at the border
         if (before == p.topk_group - 1) sums[kMaxGroups] = mine;
         if (before == p.topk_group) sums[kMaxGroups + 1] = mine;
     }
-    kept = lanes_reduce<G>(gmask, kept, [](unsigned a, unsigned b) { return a | b; });
+    kept = lanes_or<G>(gmask, kept);
     __syncwarp();
     const float in = sums[kMaxGroups], out = sums[kMaxGroups + 1];
     near = 0;
@@ -425,13 +475,13 @@ __device__ __forceinline__ unsigned kept_groups(const RouteLaunch &p, const floa
         // a sum above out + err outranks every dropped group, one below in - err no kept one
         for (int g = sub; g < p.n_group; g += G)
             if (sums[g] <= out + err && sums[g] >= in - err) near |= 1u << g;
-        near = lanes_reduce<G>(gmask, near, [](unsigned a, unsigned b) { return a | b; });
+        near = lanes_or<G>(gmask, near);
         __syncwarp(gmask);
     }
     return kept;
 }
 
-// Tokens [per_block b, per_block (b + 1)) in block b, kThreads / G at a time.
+// Tokens [per_block b, per_block (b + 1)) in block b, as many at a time as it has rows of lanes.
 // kShort: 16-bit logits without a selection bias. An fp32 of such a value has its low 13
 // bits clear, which hold the expert's index instead: one 32-bit key tells both, no two are
 // equal, and a round is a maximum and a clearing without a branch.
@@ -520,15 +570,13 @@ route_kernel(const RouteLaunch p) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) l[i] = -INFINITY;
             }
-            float top = -INFINITY;
-            unsigned on = 0;
+            // the row's largest logit, NaN where one is; -inf: the token is not live
+            float top = l[0];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                top = fmaxf(top, l[i]);
-                on |= l[i] != -INFINITY ? 1u << i : 0u;
-            }
-            const bool live = (__ballot_sync(0xffffffffu, on != 0) & gmask) != 0;
-            if (softmax || kStats) top = lanes_max<G>(gmask, top);
+            for (int i = 1; i < V; ++i) top = max_nan(top, l[i]);
+            if (softmax || kStats)
+                top = lanes_reduce<G>(gmask, top, [](float a, float b) { return max_nan(a, b); });
+            const bool live = !(top == -INFINITY);
             // scores (exp(-inf) = 0 puts out the experts that are off)
             float s_max = 1.0f;                      // no score is above it
             if (softmax) {
@@ -542,24 +590,23 @@ route_kernel(const RouteLaunch p) {
                 ssum = lanes_sum<G>(gmask, ssum);
                 s_max = 1.0f / (live ? ssum : 1.0f);
 #pragma unroll
-                for (int i = 0; i < V; ++i) s[i] *= s_max;
+                for (int i = 0; i < V; ++i) {
+                    s[i] *= s_max;
+                    if constexpr (kStats) add(i, s[i]);
+                }
                 if (kStats && live && sub == 0) {
                     const float lse = top + logf(ssum);
                     z_acc += lse * lse;
-                }
-                if constexpr (kStats) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) add(i, s[i]);
                 }
             } else {
                 float ex = 0.0f, ssum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const float e = expf(-l[i]);
-                    s[i] = __fdividef(1.0f, 1.0f + e);
+                    s[i] = rcp_fast(1.0f + e);
                     if constexpr (kStats) {
                         ssum += s[i];
-                        ex += __fdividef(1.0f, e);   // exp(l)
+                        ex += rcp_fast(e);           // exp(l)
                     }
                 }
                 if constexpr (kStats) {
@@ -585,24 +632,23 @@ route_kernel(const RouteLaunch p) {
             if (kStats) n_acc += live && sub == 0;
             // keys
             const float rel = softmax ? softmax_err<V>() : kSigmoidErr;
-            uint32_t key[V];
+            int key[V];
             unsigned kept = 0xffffffffu, near_groups = 0;
             bool near = false;                       // nearer than the error of a 32-bit key
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const uint32_t u = order_key(by_score ? s[i] + bias(i) : l[i]);
-                const uint32_t v = kShort && u != 0 ? (u & ~kIndexBits) | (kIndexMax - (e0 + i)) : u;
-                key[i] = (on >> i) & 1u ? v : 0u;
+                const float by = l[i] == -INFINITY ? -INFINITY : s[i] + bias(i);
+                key[i] = order_key(by_score ? by : l[i]);
+                if (kShort) key[i] = (key[i] & ~static_cast<int>(kIndexBits)) | (kIndexMax - (e0 + i));
             }
             if (grouped) {
+                float v[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    own_row[e0 + i] = (on >> i) & 1u ? (best_only ? l[i] : s[i] + bias(i)) : -INFINITY;
-                __syncwarp();
+                for (int i = 0; i < V; ++i) v[i] = best_only || l[i] == -INFINITY ? l[i] : s[i] + bias(i);
                 const float n = static_cast<float>(p.group_topn);
-                kept = kept_groups<G>(p, own_row, reinterpret_cast<float *>(slots.group[row]), sub, gmask,
-                                      best_only ? -1.0f : 2.0f * n * (rel * s_max + kUlp * (2.0f + n) * (s_max + bias_max)),
-                                      near_groups);
+                kept = kept_groups<G, V>(p, v, own_row, reinterpret_cast<float *>(slots.group[row]), sub, gmask,
+                                         best_only ? -1.0f : 2.0f * n * (rel * s_max + kUlp * (2.0f + n) * (s_max + bias_max)),
+                                         near_groups);
                 int g = g_first, next = (g + 1) * gs;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
@@ -610,30 +656,30 @@ route_kernel(const RouteLaunch p) {
                         ++g;
                         next += gs;
                     }
-                    if (!((kept >> (g & 31)) & 1u)) key[i] = 0u;
+                    if (!((kept >> (g & 31)) & 1u)) key[i] = kGone;
                 }
                 __syncwarp();
             }
 #pragma unroll
             for (int i = 0; i < V; ++i) own_row[e0 + i] = s[i];
-            // k rounds (one more where the last chosen key is compared with the next)
-            uint32_t best = 0;
+            int best = key[0];
 #pragma unroll
-            for (int i = 0; i < V; ++i) best = max(best, key[i]);
+            for (int i = 1; i < V; ++i) best = max(best, key[i]);
             float sv[kOwn];
             int ev[kOwn];
             if constexpr (kShort) {
 #pragma unroll
                 for (int q = 0; q < kOwn; ++q) ev[q] = -1;
                 for (int j = 0; j < p.k; ++j) {
-                    const uint32_t m = lanes_max_u32<G>(gmask, best);
+                    const int m = lanes_max_key<G>(gmask, best);
 #pragma unroll
                     for (int q = 0; q < kOwn; ++q)
-                        if (j == sub + q * G && m != 0) ev[q] = kIndexMax - static_cast<int>(m & kIndexBits);
-                    best = 0;
+                        if (j == sub + q * G && m >= kFirst) ev[q] = kIndexMax - (m & static_cast<int>(kIndexBits));
+                    key[0] = key[0] == m ? kGone : key[0];
+                    best = key[0];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        key[i] = key[i] == m ? 0u : key[i];
+                    for (int i = 1; i < V; ++i) {
+                        key[i] = key[i] == m ? kGone : key[i];
                         best = max(best, key[i]);
                     }
                 }
@@ -644,25 +690,69 @@ route_kernel(const RouteLaunch p) {
                 }
                 __syncwarp();
             } else {
+                // one more than k where the last chosen key is compared with the next
                 const int rounds = p.k + (by_score ? 1 : 0);
-                for (int j = 0; j < rounds; ++j) {
-                    const uint32_t m = lanes_max_u32<G>(gmask, best);
-                    const unsigned who = __ballot_sync(0xffffffffu, best == m) & gmask;
-                    if (lane == __ffs(who) - 1) {
-                        int at = -1;
-                        if (m != 0) {
+                // No more than the experts at or above the rounds-th largest of the lanes' best can
+                // be chosen: some ten for eight of 256. Where there are no more than lanes, each is
+                // ranked by a lane of its own against the others, at a third of the rounds' work.
+                int n = G + 1;
+                if (G >= 16 && rounds <= G) {
+                    int lane_best = best, floor = kGone;
+                    for (int j = 0; j < rounds; ++j) {
+                        floor = lanes_max_key<G>(gmask, lane_best);
+                        if (lane_best == floor) lane_best = kGone;
+                    }
+                    floor = max(floor, kFirst);
+                    n = 0;
 #pragma unroll
-                            for (int i = V - 1; i >= 0; --i)
-                                if (key[i] == m) at = i;
-                            best = 0;
-#pragma unroll
-                            for (int i = 0; i < V; ++i) {
-                                if (i == at) key[i] = 0u;
-                                best = max(best, key[i]);
-                            }
+                    for (int i = 0; i < V; ++i) {
+                        const bool in = key[i] >= floor;
+                        const unsigned who = __ballot_sync(0xffffffffu, in) & gmask;
+                        const int at = n + __popc(who & ((1u << lane) - 1u));
+                        if (in && at < G) {
+                            slots.idx[row][at] = e0 + i;
+                            slots.key[row][at] = key[i];
                         }
-                        slots.idx[row][j] = at < 0 ? -1 : e0 + at;
-                        slots.key[row][j] = m;
+                        n += __popc(who);
+                    }
+                }
+                if (__all_sync(0xffffffffu, n <= G)) {
+                    __syncwarp();
+                    int e = -1, k = kGone, rank = sub;
+                    if (sub < n) {
+                        e = slots.idx[row][sub];
+                        k = slots.key[row][sub];
+                        rank = 0;
+                        for (int o = 0; o < n; ++o) {
+                            const int ok = slots.key[row][o];
+                            rank += ok > k || (ok == k && slots.idx[row][o] < e);
+                        }
+                    }
+                    __syncwarp();
+                    if (rank < rounds) {             // lanes past the candidates: slots left over
+                        slots.idx[row][rank] = e;
+                        slots.key[row][rank] = k;
+                    }
+                } else {
+                    for (int j = 0; j < rounds; ++j) {
+                        const int m = lanes_max_key<G>(gmask, best);
+                        const unsigned who = __ballot_sync(0xffffffffu, best == m) & gmask;
+                        if (lane == __ffs(who) - 1) {
+                            int at = -1;
+                            if (m >= kFirst) {
+#pragma unroll
+                                for (int i = V - 1; i >= 0; --i)
+                                    if (key[i] == m) at = i;
+                                best = kGone;
+#pragma unroll
+                                for (int i = 0; i < V; ++i) {
+                                    if (i == at) key[i] = kGone;
+                                    best = max(best, key[i]);
+                                }
+                            }
+                            slots.idx[row][j] = at < 0 ? -1 : e0 + at;
+                            slots.key[row][j] = m;
+                        }
                     }
                 }
                 __syncwarp();
@@ -698,7 +788,7 @@ route_kernel(const RouteLaunch p) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         const float v = own_row[e0 + i] + bias(i);
-                        if ((on >> i) & 1u && v >= floor && (!grouped || (kept >> ((e0 + i) / gs)) & 1u)) cand |= 1u << i;
+                        if (l[i] != -INFINITY && v >= floor && (!grouped || (kept >> ((e0 + i) / gs)) & 1u)) cand |= 1u << i;
                     }
                     n = lanes_reduce<G>(gmask, __popc(cand), [](int a, int b) { return a + b; });
                 }
@@ -1215,10 +1305,13 @@ RouteTiles route_tiles(int64_t T, int64_t E) {
     return r;
 }
 
-cudaError_t launch_route(const RouteLaunch &p, cudaStream_t st) {
+cudaError_t launch_route(const RouteLaunch &launch, cudaStream_t st) {
+    RouteLaunch p = launch;
     const RouteTiles tiles = route_tiles(p.T, p.E);
     cudaError_t err = with_layout(p.E, [&](auto g, auto v) {
         constexpr int G = decltype(g)::value, V = decltype(v)::value;
+        const int gs = p.E / p.n_group, lanes = gs / V;
+        p.group_lanes = p.group_topn <= 2 && gs % V == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
         const dim3 grid(static_cast<unsigned>(tiles.blocks));
         const bool brief = p.dtype != MOE_DTYPE_F32 && p.sel_bias == nullptr;
         if (p.losses != nullptr)
