@@ -347,7 +347,7 @@ moe_status_t moe_route_backward(const void *logits, const uint8_t *token_mask, c
  * received less than the average goes up by `rate`, of every other one down:
  *   bias[l,e] += rate * sign(sum_f c[l,f] - E c[l,e]),  c[l,e] = sum_b counts[l,b,e]
  * bias fp32 [L,E] in place, counts int32 [L,S,E] (moe_route's, one block per
- * layer). E <= 1024. The sums and the comparison are exact.
+ * layer). E <= 1024, L and S <= 2^24. The sums and the comparison are exact.
  */
 moe_status_t moe_bias_update(float *bias, const int32_t *counts, int64_t L, int64_t S, int64_t E, float rate,
                              void *stream);

@@ -541,6 +541,11 @@ def moe_tensors_workspace_size(n) -> int:
     return int(size.value)
 
 
+def tensors_scratch(n, like):
+    """A workspace for lists of n tensors on the device of `like`, and a scalar for their norm."""
+    return _module().scratch(moe_tensors_workspace_size(n), like)
+
+
 def _norm_code(norm_type):
     try:
         return NORM_CODES[float(norm_type)]
@@ -549,7 +554,7 @@ def _norm_code(norm_type):
 
 
 def moe_grad_norm(grads, norm, ws, norm_type=2.0, stream=None):
-    """norm [1] = the norm of all the tensors' elements together."""
+    """norm (one fp32 element) = the norm of all the tensors' elements together."""
     _check("moe_grad_norm", _module().grad_norm(grads, _norm_code(norm_type), norm, ws, _raw_stream(stream, norm)))
 
 

@@ -1624,7 +1624,7 @@ moe_status_t moe_route_backward(const void *logits, const uint8_t *token_mask, c
 moe_status_t moe_bias_update(float *bias, const int32_t *counts, int64_t L, int64_t S, int64_t E, float rate,
                              void *stream) {
     if (L < 0 || S < 0 || E < 1) return MOE_ERR_INVALID_ARG;
-    if (E > 1024 || L > 0x7fffffff || S > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+    if (E > 1024 || L > (1 << 24) || S > (1 << 24)) return MOE_ERR_UNSUPPORTED;
     if (L == 0) return MOE_OK;
     if (bias == nullptr || (counts == nullptr && S > 0) || !aligned_to(bias, 4) || !aligned_to(counts, 4))
         return MOE_ERR_INVALID_ARG;

@@ -8,6 +8,7 @@
 // a configuration, and a stream; they return the call's status. Raises TypeError / ValueError
 // as the rest of the binding does.
 #define PY_SSIZE_T_CLEAN
+#include <ATen/ops/empty.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -223,6 +224,16 @@ Scratch scratch(PyObject *o) {
     return {t.data_ptr(), t.nbytes()};
 }
 
+// The address of the fp32 number that a norm goes to (any shape of one element); NULL for None.
+float *number(PyObject *o, const char *name) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor &t = tensor(o, name);
+    if (t.scalar_type() != at::kFloat) refuse(PyExc_TypeError, "%s must be Float, not %s", name, c10::toString(t.scalar_type()));
+    if (t.numel() != 1) refuse(PyExc_ValueError, "%s must have one element", name);
+    if (!t.is_cuda()) refuse(PyExc_ValueError, "libmoe takes CUDA tensors only");
+    return t.data_ptr<float>();
+}
+
 int device_of(PyObject *o, const char *name) {
     const at::Tensor &t = tensor(o, name);
     if (!t.is_cuda()) refuse(PyExc_ValueError, "libmoe takes CUDA tensors only");
@@ -240,7 +251,7 @@ PyObject *grad_norm(PyObject *const *a) {
     const List g = list_of(a[0], "grads", device_of(a[2], "norm"), -1, nullptr, false, false);
     const Scratch ws = scratch(a[3]);
     return PyLong_FromLong(g_grad_norm(g.ptr.data(), g.numel.data(), g.type.data(), static_cast<int32_t>(g.ptr.size()),
-                                       static_cast<int32_t>(whole(a[1])), as<float>(address(a[2], "norm", at::kFloat, {1})),
+                                       static_cast<int32_t>(whole(a[1])), number(a[2], "norm"),
                                        ws.ptr, ws.bytes, handle(a[4])));
 }
 
@@ -252,7 +263,7 @@ PyObject *clip_grads(PyObject *const *a) {
     if (most == -1.0 && PyErr_Occurred()) throw Refused();
     return PyLong_FromLong(g_clip_grads(g.ptr.data(), g.numel.data(), g.type.data(), static_cast<int32_t>(g.ptr.size()),
                                         static_cast<int32_t>(whole(a[1])), static_cast<float>(most),
-                                        as<float>(address(a[3], "norm", at::kFloat, {1})), ws.ptr, ws.bytes, handle(a[5])));
+                                        number(a[3], "norm"), ws.ptr, ws.bytes, handle(a[5])));
 }
 
 // params, grads, exp_avg, exp_avg_sq, masters, cfg, lr, step, norm, ws, stream
@@ -270,7 +281,15 @@ PyObject *adamw(PyObject *const *a) {
                                    a[4] != Py_None ? floats(x) : nullptr, p.numel.data(), static_cast<int32_t>(p.ptr.size()),
                                    as<const moe_adamw_cfg_t>(handle(a[5])), as<float>(address(a[6], "lr", at::kFloat, {1})),
                                    as<int32_t>(address(a[7], "step", at::kInt, {1})),
-                                   as<float>(address(a[8], "norm", at::kFloat, {1})), ws.ptr, ws.bytes, handle(a[10])));
+                                   number(a[8], "norm"), ws.ptr, ws.bytes, handle(a[10])));
+}
+
+// bytes, like: a workspace on that tensor's device, and an fp32 number at its end
+PyObject *scratch_with_norm(PyObject *const *a) {
+    const at::Tensor &like = tensor(a[1], "tensors");
+    at::Tensor ws = at::empty({whole(a[0]) / 4 + 4}, at::TensorOptions().device(like.device()).dtype(at::kFloat));
+    at::Tensor norm = ws.select(0, -1);
+    return Py_BuildValue("(NN)", THPVariable_Wrap(std::move(ws)), THPVariable_Wrap(std::move(norm)));
 }
 
 PyObject *bind(PyObject *const *a) {
@@ -309,6 +328,7 @@ PyMethodDef kMethods[] = {method<bind, 6>("bind"),
                           method<grad_norm, 5>("grad_norm"),
                           method<clip_grads, 6>("clip_grads"),
                           method<adamw, 11>("adamw"),
+                          method<scratch_with_norm, 2>("scratch"),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

@@ -28,6 +28,7 @@
 // own at the end of each sequence it meets (slot = block + sequence: consecutive
 // (block, sequence) pairs never share one); route_reduce_kernel adds the slots of a
 // sequence in a fixed order, so every output has the same bits on every call.
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -1247,37 +1248,84 @@ route_backward_kernel(const RouteBackwardLaunch p) {
     }
 }
 
-// Selection bias, one layer a block: b_e += rate sign(sum_e' c_e' - E c_e), the
-// counts added over the sequences as integers.
-constexpr int kBiasThreads = 1024;
+// Selection bias, a cluster of four blocks to a layer: b_e += rate sign(sum_e' c_e' - E c_e),
+// the counts added over the sequences as integers. Block r of the cluster has a quarter of the
+// experts; a thread adds W experts' counts (four, where rows are whole 16-byte vectors) over
+// its rows, eight loads in flight. Only the blocks' totals are exchanged, through their shared
+// memory. One block for a layer is bound by its SM's reads (7.2 us for 58 layers of 128
+// sequences and 256 experts).
+constexpr int kBiasThreads = 256, kBiasBlocks = 4;
 
+template <int W>
 __global__ void __launch_bounds__(kBiasThreads)
-bias_update_kernel(float *__restrict__ bias, const int32_t *__restrict__ counts, int S, int E, float rate) {
+bias_update_kernel(float *__restrict__ bias, const int32_t *__restrict__ counts, int S, int E, int quarter, float rate) {
     griddep_wait();
-    __shared__ long long part[kBiasThreads];
-    __shared__ long long warp_part[32];
-    const int width = (E + 31) / 32 * 32;
-    const int rows = kBiasThreads / width;
-    const int r = threadIdx.x / width, e = threadIdx.x - r * width;
-    const int32_t *c = counts + static_cast<int64_t>(blockIdx.x) * S * E;
-    long long n = 0;
-    if (r < rows && e < E) {
-#pragma unroll 8
-        for (int q = r; q < S; q += rows) n += __ldg(c + static_cast<int64_t>(q) * E + e);
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    __shared__ long long part[W][kBiasThreads];
+    __shared__ long long warp_part[kBiasThreads / 32];
+    __shared__ long long block_total;
+    const int layer = blockIdx.x / kBiasBlocks;
+    const int e_first = static_cast<int>(cluster.block_rank()) * quarter;
+    const int mine = max(0, min(quarter, E - e_first));      // experts of this block
+    const int width = quarter / W;                           // threads of a row
+    const int rows = min(min(kBiasThreads / width, 32), S);
+    const int r = threadIdx.x / width, c = threadIdx.x - r * width;
+    const int32_t *from = counts + static_cast<int64_t>(layer) * S * E + e_first + c * W;
+    long long n[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) n[w] = 0;
+    if (r < rows && c * W < mine) {
+        constexpr int kBatch = 8;
+        for (int q = r; q < S; q += rows * kBatch) {
+            int v[kBatch][W];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const bool in = q + j * rows < S;
+                const int32_t *at = from + static_cast<int64_t>(in ? q + j * rows : q) * E;
+                if constexpr (W == 4) {
+                    const int4 x = in ? __ldg(reinterpret_cast<const int4 *>(at)) : make_int4(0, 0, 0, 0);
+                    v[j][0] = x.x;
+                    v[j][1] = x.y;
+                    v[j][2] = x.z;
+                    v[j][3] = x.w;
+                } else {
+                    v[j][0] = in ? __ldg(at) : 0;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+                for (int w = 0; w < W; ++w) n[w] += v[j][w];
+        }
     }
-    part[threadIdx.x] = n;
-    long long all = n;
+    long long all = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        part[w][threadIdx.x] = n[w];
+        all += n[w];
+    }
     for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
     if ((threadIdx.x & 31) == 0) warp_part[threadIdx.x >> 5] = all;
     __syncthreads();
-    if (threadIdx.x < E) {
-        long long mine = 0, total = 0;
-        for (int i = 0; i < rows; ++i) mine += part[i * width + threadIdx.x];
-        for (int i = 0; i < 32; ++i) total += warp_part[i];
-        const long long d = total - static_cast<long long>(E) * mine;
-        float *b = bias + static_cast<int64_t>(blockIdx.x) * E + threadIdx.x;
+    if (threadIdx.x == 0) {
+        long long t = 0;
+#pragma unroll
+        for (int i = 0; i < kBiasThreads / 32; ++i) t += warp_part[i];
+        block_total = t;
+    }
+    cluster.sync();
+    long long total = 0;
+#pragma unroll
+    for (int i = 0; i < kBiasBlocks; ++i) total += *cluster.map_shared_rank(&block_total, i);
+    if (threadIdx.x < mine) {
+        long long own = 0;
+        for (int i = 0; i < rows; ++i) own += part[threadIdx.x % W][i * width + threadIdx.x / W];
+        const long long d = total - static_cast<long long>(E) * own;
+        float *b = bias + static_cast<int64_t>(layer) * E + e_first + threadIdx.x;
         *b += d > 0 ? rate : d < 0 ? -rate : 0.0f;
     }
+    cluster.sync();                                          // the totals are read while their blocks last
 }
 
 // (lanes of a token, experts of a lane) for E experts.
@@ -1340,7 +1388,22 @@ cudaError_t launch_route_backward(const RouteBackwardLaunch &p, cudaStream_t st)
 }
 
 cudaError_t launch_bias_update(float *bias, const int32_t *counts, int L, int S, int E, float rate, cudaStream_t st) {
-    const cudaError_t err = launch_dep(bias_update_kernel, dim3(L), dim3(kBiasThreads), 0, st, bias, counts, S, E, rate);
+    const bool whole = E % 4 == 0 && reinterpret_cast<uintptr_t>(counts) % 16 == 0;
+    const int quarter = (E + 4 * kBiasBlocks - 1) / (4 * kBiasBlocks) * 4;    // experts of a block, at most 256
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(L * kBiasBlocks);
+    cfg.blockDim = dim3(kBiasThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kBiasBlocks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t err = whole ? cudaLaunchKernelEx(&cfg, bias_update_kernel<4>, bias, counts, S, E, quarter, rate)
+                                  : cudaLaunchKernelEx(&cfg, bias_update_kernel<1>, bias, counts, S, E, quarter, rate);
     note_launches(1);
     return err;
 }

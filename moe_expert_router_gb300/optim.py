@@ -22,28 +22,22 @@ def _lists(tensors, name):
     return tensors
 
 
-def _scratch(n, like):
-    """Workspace for n tensors whose last element is for the norm, and that as [1]."""
-    ws = torch.empty((B.moe_tensors_workspace_size(n) // 4 + 4,), dtype=torch.float32, device=like.device)
-    return ws, ws[-1:]
-
-
 def grad_norm(grads, norm_type=2.0):
     """The norm (norm_type 1, 2 or inf) of all elements of `grads` together, an fp32 scalar
     tensor on their device."""
     grads = _lists(grads, "grads")
-    ws, norm = _scratch(len(grads), grads[0])
+    ws, norm = B.tensors_scratch(len(grads), grads[0])
     B.moe_grad_norm(grads, norm, ws, norm_type)
-    return norm[0]
+    return norm
 
 
 def clip_grad_norm_(grads, max_norm, norm_type=2.0):
     """Multiplies every tensor of `grads` in place by min(1, max_norm / (norm + 1e-6)) and
     returns the norm before that, as a tensor on the device."""
     grads = _lists(grads, "grads")
-    ws, norm = _scratch(len(grads), grads[0])
+    ws, norm = B.tensors_scratch(len(grads), grads[0])
     B.moe_clip_grads(grads, max_norm, norm, ws, norm_type)
-    return norm[0]
+    return norm
 
 
 def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr, masters=None, betas=(0.9, 0.999), eps=1e-8,
@@ -53,12 +47,12 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr, masters=None, betas
     taken times min(1, max_norm / (their global 2-norm + 1e-6)), without being changed. Returns
     the norm as a tensor (None where max_norm is 0 and skip_nonfinite is False)."""
     params, grads = _lists(params, "params"), _lists(grads, "grads")
-    ws, norm = _scratch(len(params), params[0])
+    ws, norm = B.tensors_scratch(len(params), params[0])
     if not (max_norm > 0.0 or skip_nonfinite):
         norm = None
     cfg = B.AdamWCfg(betas[0], betas[1], eps, weight_decay, max_norm, int(bool(skip_nonfinite)))
     B.moe_adamw(params, grads, exp_avg, exp_avg_sq, lr, step, ws, cfg, masters, norm)
-    return None if norm is None else norm[0]
+    return norm
 
 
 class AdamW:
