@@ -58,16 +58,11 @@ struct AdamTable {
     Runs runs;
 };
 constexpr uint8_t kScalar = 255;
-// a short list is launched with a short argument block
-constexpr int kShort = 64, kLong = 1000, kAdamShort = 64, kAdamLong = 520;
+// a list is launched with the shortest argument block that holds it (1.7, 6.5 or 25 KB: the host
+// writes it at every launch, some 3 us for the longest)
+constexpr int kShort = 64, kMiddle = 256, kLong = 1000;
+constexpr int kAdamShort = 64, kAdamMiddle = 192, kAdamLong = 520;
 static_assert(sizeof(Table<kLong>) < 32000 && sizeof(AdamTable<kAdamLong>) < 32000, "kernel arguments");
-
-// Header of the scratch: what the update reads.
-struct Hyper {
-    float norm, factor, lr, inv_c1, inv_c2;
-    int skip;
-};
-constexpr size_t kHeader = 256;
 
 // A tensor as elements before the first 16-byte vector, vectors, and elements after.
 struct Span {
@@ -174,8 +169,9 @@ constexpr int kBatch = 8;                   // 16-byte loads of a thread in flig
 
 template <int kType, int N>
 __global__ void __launch_bounds__(kThreads, kNormPerSm)
-norm_kernel(const __grid_constant__ Table<N> tab, double *__restrict__ part) {
+norm_kernel(const __grid_constant__ Table<N> tab, double *__restrict__ part, int32_t *__restrict__ step) {
     griddep_wait();
+    if (step != nullptr && blockIdx.x == 0 && threadIdx.x == 0) ++*step;   // AdamW's, which comes next
     Sum<kType> sum;
     for (int64_t u0 = blockIdx.x * tab.runs.size; u0 < tab.runs.total; u0 += gridDim.x * tab.runs.size) {
         const int64_t u1 = min(tab.runs.total, u0 + tab.runs.size);
@@ -306,32 +302,46 @@ clip_kernel(const __grid_constant__ Table<N> tab, const double *__restrict__ par
     }
 }
 
-// Once a step, before the update: the norm and factor, the step count and its
-// bias corrections. 1 - b^t = -expm1(t ln b): ln b comes from the host in 64 bits, and
-// expm1 keeps fp32's digits where b^t is near 1.
-__global__ void __launch_bounds__(kThreads)
-adamw_begin_kernel(const double *__restrict__ part, int n_part, float max_norm, double ln_beta1, double ln_beta2,
-                   int skip_nonfinite, const float *__restrict__ lr, int32_t *__restrict__ step,
-                   float *__restrict__ norm, Hyper *__restrict__ hyper) {
+// Where AdamW needs no norm, the count of its step alone.
+__global__ void adamw_count_kernel(int32_t *__restrict__ step) {
     griddep_wait();
-    const float total = n_part > 0 ? total_norm<MOE_NORM_2>(part, n_part) : 0.0f;
-    if (threadIdx.x != 0) return;
-    Hyper h;
-    h.norm = total;
-    h.factor = n_part > 0 && max_norm > 0.0f ? clip_factor(total, max_norm) : 1.0f;
-    h.skip = skip_nonfinite && !isfinite(total);
-    h.lr = *lr;
-    const int t = *step + 1;
-    h.inv_c1 = -1.0f / expm1f(static_cast<float>(t * ln_beta1));
-    h.inv_c2 = -1.0f / expm1f(static_cast<float>(t * ln_beta2));
-    if (!h.skip) *step = t;
-    if (norm != nullptr && n_part > 0) *norm = total;
-    *hyper = h;
+    ++*step;
 }
 
+// What a step is made of; step[0] has been counted up. `undo`: the last launch of a step, which
+// takes the count back where the step is skipped.
 struct AdamConst {
-    float beta1, beta2, eps, weight_decay;
+    float beta1, beta2, eps, weight_decay, max_norm;
+    double ln_beta1, ln_beta2;
+    const double *part;
+    int n_part, skip_nonfinite, undo;
+    const float *lr;
+    int32_t *step;
+    float *norm;
 };
+struct Hyper {
+    float factor, lr, inv_c1, inv_c2;
+    int skip;
+};
+
+// The step's numbers, in every block, through its shared memory. 1 - b^t = -expm1(t ln b):
+// ln b comes from the host in 64 bits, and expm1 keeps fp32's digits where b^t is near 1.
+__device__ __forceinline__ void begin_step(const AdamConst &k, Hyper &h) {
+    const float total = k.n_part > 0 ? total_norm<MOE_NORM_2>(k.part, k.n_part) : 0.0f;
+    if (threadIdx.x == 0) {
+        h.skip = k.skip_nonfinite && !isfinite(total);
+        h.factor = k.n_part > 0 && k.max_norm > 0.0f ? clip_factor(total, k.max_norm) : 1.0f;
+        const int t = *k.step;
+        h.lr = *k.lr;
+        h.inv_c1 = -1.0f / expm1f(static_cast<float>(t * k.ln_beta1));
+        h.inv_c2 = -1.0f / expm1f(static_cast<float>(t * k.ln_beta2));
+        if (blockIdx.x == 0) {
+            if (k.n_part > 0 && k.norm != nullptr) *k.norm = total;
+            if (h.skip && k.undo) *k.step = t - 1;
+        }
+    }
+    __syncthreads();
+}
 
 __device__ __forceinline__ void adam_element(const Hyper &h, const AdamConst &c, float grad, float &m, float &v, float &p) {
     const float g = grad * h.factor;
@@ -368,9 +378,11 @@ __device__ __forceinline__ float4 four_floats(const uint4 &r, int dtype) {
 // together, it is eight single elements of each.
 template <int N>
 __global__ void __launch_bounds__(kThreads, kAdamPerSm)
-adamw_kernel(const __grid_constant__ AdamTable<N> tab, const Hyper *__restrict__ hyper, const AdamConst k) {
+adamw_kernel(const __grid_constant__ AdamTable<N> tab, const __grid_constant__ AdamConst k) {
     griddep_wait();
-    const Hyper h = *hyper;
+    __shared__ Hyper shared;
+    begin_step(k, shared);
+    const Hyper h = shared;
     if (h.skip) return;
     for (int64_t u0 = blockIdx.x * tab.runs.size; u0 < tab.runs.total; u0 += gridDim.x * tab.runs.size) {
         const int64_t u1 = min(tab.runs.total, u0 + tab.runs.size);
@@ -501,13 +513,14 @@ cudaError_t for_tables(const TensorList &l, int most, F f) {
     return cudaSuccess;
 }
 
-double *partials(void *ws) { return reinterpret_cast<double *>(static_cast<char *>(ws) + kHeader); }
+double *partials(void *ws) { return static_cast<double *>(ws); }
 
 template <int kType, int N>
-cudaError_t norm_parts(const TensorList &l, void *ws, int *n_part, cudaStream_t st) {
+cudaError_t norm_parts(const TensorList &l, void *ws, int32_t *step, int *n_part, cudaStream_t st) {
     *n_part = 0;
     return for_tables<N>(l, kSms * kNormPerSm, [&](const Table<N> &t, int grid) {
-        const cudaError_t e = launch_dep(norm_kernel<kType, N>, dim3(grid), dim3(kThreads), 0, st, t, partials(ws) + *n_part);
+        const cudaError_t e = launch_dep(norm_kernel<kType, N>, dim3(grid), dim3(kThreads), 0, st, t, partials(ws) + *n_part,
+                                         *n_part == 0 ? step : static_cast<int32_t *>(nullptr));
         note_launches(1);
         *n_part += grid;
         return e;
@@ -525,8 +538,10 @@ cudaError_t clip_parts(const TensorList &l, float max_norm, float *norm, void *w
 }
 
 template <int kType>
-cudaError_t norm_typed(const TensorList &l, void *ws, int *n_part, cudaStream_t st) {
-    return l.n <= kShort ? norm_parts<kType, kShort>(l, ws, n_part, st) : norm_parts<kType, kLong>(l, ws, n_part, st);
+cudaError_t norm_typed(const TensorList &l, void *ws, int32_t *step, int *n_part, cudaStream_t st) {
+    if (l.n <= kShort) return norm_parts<kType, kShort>(l, ws, step, n_part, st);
+    if (l.n <= kMiddle) return norm_parts<kType, kMiddle>(l, ws, step, n_part, st);
+    return norm_parts<kType, kLong>(l, ws, step, n_part, st);
 }
 
 template <typename F>
@@ -553,7 +568,7 @@ uint8_t vector_head(const AdamwLaunch &p, int i) {
 }
 
 template <int N>
-cudaError_t adamw_tables(const AdamwLaunch &p, cudaStream_t st) {
+cudaError_t adamw_tables(const AdamwLaunch &p, AdamConst k, cudaStream_t st) {
     int at = 0;
     do {
         AdamTable<N> t;
@@ -575,11 +590,10 @@ cudaError_t adamw_tables(const AdamwLaunch &p, cudaStream_t st) {
             total += grains(numel / 4 + 1 + kTurn);
             ++n;
         }
-        if (n == 0) break;
+        while (at < p.params.n && p.params.numel[at] == 0) ++at;
+        k.undo = at == p.params.n;
         const int blocks = make_runs(t.runs, n, total, kSms * kAdamPerSm);
-        const cudaError_t e = launch_dep(adamw_kernel<N>, dim3(blocks), dim3(kThreads), 0, st, t,
-                                         static_cast<const Hyper *>(p.ws),
-                                         AdamConst{p.beta1, p.beta2, p.eps, p.weight_decay});
+        const cudaError_t e = launch_dep(adamw_kernel<N>, dim3(blocks), dim3(kThreads), 0, st, t, k);
         note_launches(1);
         if (e != cudaSuccess) return e;
     } while (at < p.params.n);
@@ -589,15 +603,15 @@ cudaError_t adamw_tables(const AdamwLaunch &p, cudaStream_t st) {
 }  // namespace
 
 size_t multi_tensor_ws_bytes(int64_t n) {
-    const int64_t tables = n <= kShort ? 1 : (n + kLong - 1) / kLong;
-    return kHeader + static_cast<size_t>(tables) * kMaxGrid * sizeof(double);
+    const int64_t tables = n <= kLong ? 1 : (n + kLong - 1) / kLong;
+    return static_cast<size_t>(tables) * kMaxGrid * sizeof(double);
 }
 
 cudaError_t launch_grad_norm(const TensorList &grads, int norm_type, float *norm, void *ws, cudaStream_t st) {
     return with_norm_type(norm_type, [&](auto type) {
         constexpr int kType = decltype(type)::value;
         int n_part = 0;
-        cudaError_t e = norm_typed<kType>(grads, ws, &n_part, st);
+        cudaError_t e = norm_typed<kType>(grads, ws, nullptr, &n_part, st);
         if (e != cudaSuccess) return e;
         e = launch_dep(norm_total_kernel<kType>, dim3(1), dim3(kThreads), 0, st,
                        static_cast<const double *>(partials(ws)), n_part, norm);
@@ -611,26 +625,39 @@ cudaError_t launch_clip_grads(const TensorList &grads, int norm_type, float max_
     return with_norm_type(norm_type, [&](auto type) {
         constexpr int kType = decltype(type)::value;
         int n_part = 0;
-        const cudaError_t e = norm_typed<kType>(grads, ws, &n_part, st);
+        const cudaError_t e = norm_typed<kType>(grads, ws, nullptr, &n_part, st);
         if (e != cudaSuccess) return e;
-        return grads.n <= kShort ? clip_parts<kType, kShort>(grads, max_norm, norm, ws, n_part, st)
-                                 : clip_parts<kType, kLong>(grads, max_norm, norm, ws, n_part, st);
+        if (grads.n <= kShort) return clip_parts<kType, kShort>(grads, max_norm, norm, ws, n_part, st);
+        if (grads.n <= kMiddle) return clip_parts<kType, kMiddle>(grads, max_norm, norm, ws, n_part, st);
+        return clip_parts<kType, kLong>(grads, max_norm, norm, ws, n_part, st);
     });
 }
 
 cudaError_t launch_adamw(const AdamwLaunch &p, cudaStream_t st) {
-    int n_part = 0;
-    cudaError_t e = cudaSuccess;
+    AdamConst k = {};
+    k.beta1 = p.beta1;
+    k.beta2 = p.beta2;
+    k.eps = p.eps;
+    k.weight_decay = p.weight_decay;
+    k.max_norm = p.max_norm;
+    k.ln_beta1 = log(static_cast<double>(p.beta1));
+    k.ln_beta2 = log(static_cast<double>(p.beta2));
+    k.part = partials(p.ws);
+    k.skip_nonfinite = p.skip_nonfinite;
+    k.lr = p.lr;
+    k.step = p.step;
+    k.norm = p.norm;
+    cudaError_t e;
     if (p.norm != nullptr || p.max_norm > 0.0f || p.skip_nonfinite) {
-        e = norm_typed<MOE_NORM_2>(p.grads, p.ws, &n_part, st);
-        if (e != cudaSuccess) return e;
+        e = norm_typed<MOE_NORM_2>(p.grads, p.ws, p.step, &k.n_part, st);
+    } else {
+        e = launch_dep(adamw_count_kernel, dim3(1), dim3(1), 0, st, p.step);
+        note_launches(1);
     }
-    e = launch_dep(adamw_begin_kernel, dim3(1), dim3(kThreads), 0, st, static_cast<const double *>(partials(p.ws)), n_part,
-                   p.max_norm, log(static_cast<double>(p.beta1)), log(static_cast<double>(p.beta2)), p.skip_nonfinite, p.lr,
-                   p.step, p.norm, static_cast<Hyper *>(p.ws));
-    note_launches(1);
     if (e != cudaSuccess) return e;
-    return p.params.n <= kAdamShort ? adamw_tables<kAdamShort>(p, st) : adamw_tables<kAdamLong>(p, st);
+    if (p.params.n <= kAdamShort) return adamw_tables<kAdamShort>(p, k, st);
+    if (p.params.n <= kAdamMiddle) return adamw_tables<kAdamMiddle>(p, k, st);
+    return adamw_tables<kAdamLong>(p, k, st);
 }
 
 }  // namespace moe

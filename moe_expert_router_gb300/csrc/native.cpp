@@ -169,19 +169,22 @@ struct List {
     std::vector<int64_t> numel;
     std::vector<int32_t> type;
 };
+// A thread's lists keep their memory from call to call, nothing of what is in them.
+thread_local List t_lists[5];
+thread_local std::vector<std::pair<uint64_t, uint64_t>> t_range;
 
 bool is_list(PyObject *o) { return PyList_Check(o) || PyTuple_Check(o); }
 
-List list_of(PyObject *o, const char *name, int device, int dtype, PyObject *like, bool optional, bool written) {
+const List &list_of(List &l, PyObject *o, const char *name, int device, int dtype, PyObject *like, bool optional, bool written) {
     if (!is_list(o)) refuse(PyExc_TypeError, "%s must be a list of tensors", name);
     const Py_ssize_t n = PySequence_Fast_GET_SIZE(o);
     if (like != nullptr && PySequence_Fast_GET_SIZE(like) != n)
         refuse(PyExc_ValueError, "%s must be as many as the parameters", name);
-    List l;
-    l.ptr.resize(n);
-    l.numel.resize(n);
-    l.type.resize(n);
-    std::vector<std::pair<uint64_t, uint64_t>> range;
+    l.ptr.assign(n, nullptr);
+    l.numel.assign(n, 0);
+    l.type.assign(n, MOE_DTYPE_F32);
+    std::vector<std::pair<uint64_t, uint64_t>> &range = t_range;
+    range.clear();
     bool sorted = true;
     for (Py_ssize_t i = 0; i < n; ++i) {
         PyObject *item = PySequence_Fast_GET_ITEM(o, i);
@@ -248,7 +251,7 @@ long whole(PyObject *o) {
 
 // grads, norm_type, norm, ws, stream
 PyObject *grad_norm(PyObject *const *a) {
-    const List g = list_of(a[0], "grads", device_of(a[2], "norm"), -1, nullptr, false, false);
+    const List &g = list_of(t_lists[0], a[0], "grads", device_of(a[2], "norm"), -1, nullptr, false, false);
     const Scratch ws = scratch(a[3]);
     return PyLong_FromLong(g_grad_norm(g.ptr.data(), g.numel.data(), g.type.data(), static_cast<int32_t>(g.ptr.size()),
                                        static_cast<int32_t>(whole(a[1])), number(a[2], "norm"),
@@ -257,7 +260,7 @@ PyObject *grad_norm(PyObject *const *a) {
 
 // grads, norm_type, max_norm, norm, ws, stream
 PyObject *clip_grads(PyObject *const *a) {
-    const List g = list_of(a[0], "grads", device_of(a[3], "norm"), -1, nullptr, false, true);
+    const List &g = list_of(t_lists[0], a[0], "grads", device_of(a[3], "norm"), -1, nullptr, false, true);
     const Scratch ws = scratch(a[4]);
     const double most = PyFloat_AsDouble(a[2]);
     if (most == -1.0 && PyErr_Occurred()) throw Refused();
@@ -269,12 +272,12 @@ PyObject *clip_grads(PyObject *const *a) {
 // params, grads, exp_avg, exp_avg_sq, masters, cfg, lr, step, norm, ws, stream
 PyObject *adamw(PyObject *const *a) {
     const int device = device_of(a[6], "lr");
-    const List p = list_of(a[0], "params", device, -1, nullptr, false, true);
-    const List g = list_of(a[1], "grads", device, -1, a[0], false, false);
-    const List m = list_of(a[2], "exp_avg", device, MOE_DTYPE_F32, a[0], false, true);
-    const List v = list_of(a[3], "exp_avg_sq", device, MOE_DTYPE_F32, a[0], false, true);
-    List x;
-    if (a[4] != Py_None) x = list_of(a[4], "masters", device, MOE_DTYPE_F32, a[0], true, true);
+    const List &p = list_of(t_lists[0], a[0], "params", device, -1, nullptr, false, true);
+    const List &g = list_of(t_lists[1], a[1], "grads", device, -1, a[0], false, false);
+    const List &m = list_of(t_lists[2], a[2], "exp_avg", device, MOE_DTYPE_F32, a[0], false, true);
+    const List &v = list_of(t_lists[3], a[3], "exp_avg_sq", device, MOE_DTYPE_F32, a[0], false, true);
+    const List &x = t_lists[4];
+    if (a[4] != Py_None) list_of(t_lists[4], a[4], "masters", device, MOE_DTYPE_F32, a[0], true, true);
     const Scratch ws = scratch(a[9]);
     auto floats = [](const List &l) { return reinterpret_cast<float *const *>(l.ptr.data()); };
     return PyLong_FromLong(g_adamw(p.ptr.data(), p.type.data(), g.ptr.data(), g.type.data(), floats(m), floats(v),
