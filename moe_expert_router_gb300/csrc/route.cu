@@ -270,6 +270,93 @@ __device__ __noinline__ void select_near(const RouteLaunch &p, int64_t row, int 
     __syncwarp(gmask);
 }
 
+// The groups that stay of those in `near`, whose sums differ by less than the error of 32-bit
+// ones: the experts that can be among a near group's best (no more than the error `err1` below
+// its last) are scored in 64 bits, one a lane. sel_row: the token's selection scores, -inf where
+// off. Returns the near groups that stay, `room` of them; ~0 where there are more such experts
+// than lanes. Without a bias softmax's sums need no normaliser.
+template <int G, int V>
+__device__ __noinline__ unsigned resolve_groups(const RouteLaunch &p, int64_t row, const float *sel_row, int sub,
+                                                unsigned gmask, unsigned near, int room, float err1, bool biased, int *list,
+                                                double *group) {
+    const int lane = threadIdx.x & 31, e0 = sub * V;
+    const int gs = p.E / p.n_group;
+    const bool softmax = p.score_fn == MOE_SCORE_SOFTMAX;
+    int n = 0;
+    for (unsigned left = near; left != 0; left &= left - 1u) {
+        const int g = __ffs(left) - 1;
+        const int first = max(e0, g * gs), last = min(e0 + V, (g + 1) * gs);
+        // the group's group_topn-th best, ties counted
+        int floor = 0x7fffffff;
+        for (int taken = 0; taken < p.group_topn;) {
+            int best = kGone;
+            for (int e = first; e < last; ++e) {
+                const int k = order_key(sel_row[e]);
+                if (k < floor && k > best) best = k;
+            }
+            const int m = lanes_max_key<G>(gmask, best);
+            if (m < kFirst) break;
+            int same = 0;
+            for (int e = first; e < last; ++e) same += order_key(sel_row[e]) == m;
+            taken += lanes_reduce<G>(gmask, same, [](int a, int b) { return a + b; });
+            floor = m;
+        }
+        const float least = key_value(floor) - 2.0f * err1;
+        for (int i = 0; i < V; ++i) {
+            const int e = e0 + i;
+            const bool in = e >= first && e < last && sel_row[e] > -INFINITY && sel_row[e] >= least;
+            const unsigned who = __ballot_sync(gmask, in) & gmask;
+            const int at = n + __popc(who & ((1u << lane) - 1u));
+            if (in && at < G) list[at] = e;
+            n += __popc(who);
+        }
+    }
+    if (n > G) return ~0u;
+    __syncwarp(gmask);
+    const int e = sub < n ? list[sub] : -1;
+    WideScore score = {0.0, 1.0};
+    if (softmax && biased) {
+        score = wide_score<G, V>(p, row, e0, gmask);
+    } else if (softmax) {                            // about any common factor: the row's first listed expert
+        score.top = load_one(p.logits, p.dtype, row + list[0]);
+    }
+    double v = 0.0;
+    uint64_t key = 0;
+    int own = -1;                                    // group
+    if (e >= 0) {
+        v = score(softmax, load_one(p.logits, p.dtype, row + e));
+        if (biased) v += static_cast<double>(__ldg(p.sel_bias + e));
+        key = order_key64(v);
+        own = e / gs;
+    }
+    int rank = 0;
+    for (int c = 0; c < n; ++c) {
+        const uint64_t ok = __shfl_sync(gmask, key, c, G);
+        const int og = __shfl_sync(gmask, own, c, G);
+        rank += og == own && (ok > key || (ok == key && c < sub));
+    }
+    const double part = rank < p.group_topn ? v : 0.0;
+    double total = 0.0;
+    for (int c = 0; c < n; ++c) {
+        const double x = __shfl_sync(gmask, part, c, G);
+        if (__shfl_sync(gmask, own, c, G) == own) total += x;
+    }
+    if (e >= 0) group[own] = total;                  // the same number from each of its lanes
+    __syncwarp(gmask);
+    unsigned stay = 0;
+    for (unsigned left = near; left != 0; left &= left - 1u) {
+        const int g = __ffs(left) - 1;
+        int before = 0;
+        for (unsigned other = near; other != 0; other &= other - 1u) {
+            const int o = __ffs(other) - 1;
+            before += group[o] > group[g] || (group[o] == group[g] && o < g);
+        }
+        if (before < room) stay |= 1u << g;
+    }
+    __syncwarp(gmask);
+    return stay;
+}
+
 // One token's whole selection in 64 bits: the groups in `sure` stay, of those in `near`
 // the best stay as far as topk_group allows, then k rounds.
 template <int G, int V>
@@ -278,14 +365,15 @@ __device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int 
     const int e0 = sub * V;
     const WideScore score = wide_score<G, V>(p, row, e0, gmask);
     const bool softmax = p.score_fn == MOE_SCORE_SOFTMAX;
-    const int gs = p.E / p.n_group;
+    const int gs = p.E / p.n_group, g_first = e0 / gs, bound = (g_first + 1) * gs;
+    auto group_of = [&](int e) { return gs >= V ? g_first + (e >= bound) : e / gs; };
     double sel[V];
     uint64_t key[V];
     unsigned open = 0;                               // experts that may still be chosen
 #pragma unroll (V <= 8 ? V : 1)
     for (int i = 0; i < V; ++i) {
         key[i] = 0;
-        if (e0 + i >= p.E || !(((sure | near) >> ((e0 + i) / gs)) & 1u)) continue;
+        if (e0 + i >= p.E || !(((sure | near) >> group_of(e0 + i)) & 1u)) continue;
         const float l = load_one(p.logits, p.dtype, row + e0 + i);
         if (l == -INFINITY) continue;
         open |= 1u << i;
@@ -301,7 +389,7 @@ __device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int 
                 uint64_t b = 0;
 #pragma unroll (V <= 8 ? V : 1)
                 for (int i = 0; i < V; ++i)
-                    if (((open & ~taken) >> i) & 1u && (e0 + i) / gs == g && key[i] > b) b = key[i];
+                    if (((open & ~taken) >> i) & 1u && group_of(e0 + i) == g && key[i] > b) b = key[i];
                 const uint64_t m = lanes_max_u64<G>(gmask, b);
                 if (m == 0) break;
                 const unsigned who = __ballot_sync(gmask, b == m) & gmask;
@@ -311,7 +399,7 @@ __device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int 
                     int at = 0;
 #pragma unroll (V <= 8 ? V : 1)
                     for (int i = V - 1; i >= 0; --i)
-                        if (((open & ~taken) >> i) & 1u && (e0 + i) / gs == g && key[i] == m) at = i;
+                        if (((open & ~taken) >> i) & 1u && group_of(e0 + i) == g && key[i] == m) at = i;
                     taken |= 1u << at;
                     v = sel[at];
                 }
@@ -325,7 +413,7 @@ __device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int 
 #pragma unroll (V <= 8 ? V : 1)
         for (int i = 0; i < V; ++i) {
             if (!((open >> i) & 1u)) continue;
-            const int g = (e0 + i) / gs;
+            const int g = group_of(e0 + i);
             if (!((near >> g) & 1u)) continue;
             int before = 0;
             for (unsigned left = near; left != 0; left &= left - 1u) {
@@ -650,6 +738,20 @@ route_kernel(const RouteLaunch p) {
                 kept = kept_groups<G, V>(p, v, own_row, reinterpret_cast<float *>(slots.group[row]), sub, gmask,
                                          best_only ? -1.0f : 2.0f * n * (rel * s_max + kUlp * (2.0f + n) * (s_max + bias_max)),
                                          near_groups);
+                if (near_groups != 0) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) own_row[e0 + i] = v[i];
+                    __syncwarp(gmask);
+                    const unsigned sure = kept & ~near_groups;
+                    const unsigned stay = resolve_groups<G, V>(p, lrow, own_row, sub, gmask, near_groups,
+                                                               p.topk_group - __popc(sure),
+                                                               rel * s_max + 2.0f * kUlp * (s_max + bias_max), by_score,
+                                                               slots.idx[row], slots.group[row]);
+                    if (stay != ~0u) {
+                        kept = sure | stay;
+                        near_groups = 0;
+                    }
+                }
                 int g = g_first, next = (g + 1) * gs;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
