@@ -179,6 +179,27 @@ __device__ __forceinline__ uint32_t lanes_max_u32(unsigned mask, uint32_t v) {
     return lanes_reduce<G>(mask, v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 
+// Eight keys in descending order: a bitonic sequence's last half, and a whole network.
+__device__ __forceinline__ void order_pair(int (&k)[8], int a, int b) {
+    const int hi = max(k[a], k[b]), lo = min(k[a], k[b]);
+    k[a] = hi;
+    k[b] = lo;
+}
+__device__ __forceinline__ void bitonic_merge8(int (&k)[8]) {
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if ((i & d) == 0) order_pair(k, i, i + d);
+}
+__device__ __forceinline__ void sort8(int (&k)[8]) {
+    // Batcher's odd-even merge sort, 19 comparisons
+    constexpr int kPairs[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6}, {5, 7}, {1, 2}, {5, 6},
+                                   {0, 4}, {1, 5}, {2, 6}, {3, 7}, {2, 4}, {3, 5}, {1, 2}, {3, 4}, {5, 6}};
+#pragma unroll
+    for (int i = 0; i < 19; ++i) order_pair(k, kPairs[i][0], kPairs[i][1]);
+}
+
 constexpr uint32_t kIndexBits = 0x1fffu;
 constexpr int kIndexMax = 1023;
 
@@ -684,7 +705,7 @@ route_kernel(const RouteLaunch p) {
                     if constexpr (kStats) add(i, s[i]);
                 }
                 if (kStats && live && sub == 0) {
-                    const float lse = top + logf(ssum);
+                    const float lse = top + __logf(ssum);
                     z_acc += lse * lse;
                 }
             } else {
@@ -710,7 +731,7 @@ route_kernel(const RouteLaunch p) {
                     ssum = lanes_sum<G>(gmask, ssum);
                     ex = lanes_sum<G>(gmask, ex);
                     if (live && sub == 0) {
-                        const float lse = shift + logf(ex);
+                        const float lse = shift + __logf(ex);
                         z_acc += lse * lse;
                     }
                     const float share = live ? 1.0f / (ssum + kEps) : 0.0f;
@@ -773,7 +794,29 @@ route_kernel(const RouteLaunch p) {
             if constexpr (kShort) {
 #pragma unroll
                 for (int q = 0; q < kOwn; ++q) ev[q] = -1;
-                for (int j = 0; j < p.k; ++j) {
+                bool done = false;
+                if constexpr (V == 8) {
+                    if (p.k <= 8) {
+                        done = true;
+                        // every lane's keys in order, then the eight best of two lanes at a time: 200
+                        // instructions for 16 lanes against 310 of eight rounds
+                        sort8(key);
+#pragma unroll
+                        for (int off = 1; off < G; off <<= 1) {
+                            int other[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(gmask, key[i], off);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) key[i] = max(key[i], other[7 - i]);
+                            bitonic_merge8(key);
+                        }
+                        int m = kGone;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) m = sub == i ? key[i] : m;
+                        if (sub < p.k && m >= kFirst) ev[0] = kIndexMax - (m & static_cast<int>(kIndexBits));
+                    }
+                }
+                for (int j = 0; j < p.k && !done; ++j) {
                     const int m = lanes_max_key<G>(gmask, best);
 #pragma unroll
                     for (int q = 0; q < kOwn; ++q)
@@ -1192,9 +1235,10 @@ route_backward_kernel(const RouteBackwardLaunch p) {
             float cw[kOwn];
 #pragma unroll
             for (int q = 0; q < kOwn; ++q) {
-                const int j = sub + q * G;
                 ce[q] = -1;
                 cw[q] = 0.0f;
+                if (q * G >= p.k) continue;
+                const int j = sub + q * G;
                 if (given && j < p.k) {
                     const int64_t at = static_cast<int64_t>(tok) * p.k + j;
                     ce[q] = __ldg(p.topk_idx + at);
@@ -1207,17 +1251,14 @@ route_backward_kernel(const RouteBackwardLaunch p) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) l[i] = -INFINITY;
             }
-            float top = l[0];
-#pragma unroll
-            for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
-            bool any = false;
-#pragma unroll
-            for (int i = 0; i < V; ++i) any |= l[i] != -INFINITY;
-            const bool live = (__ballot_sync(0xffffffffu, any) & gmask) != 0;
-            float inv = 0.0f, zc = 0.0f;             // softmax: s = ex inv; z's coefficient at ex
-            float Z = 0.0f;
+            float zc = 0.0f, Z = 0.0f;               // z's coefficient at s; sigmoid: the sum of scores
+            float z[V];                              // sigmoid: the z term
             if (softmax || dz != 0.0f) {
-                top = lanes_max<G>(gmask, top);
+                float top = l[0];
+#pragma unroll
+                for (int i = 1; i < V; ++i) top = max_nan(top, l[i]);
+                top = lanes_reduce<G>(gmask, top, [](float a, float b) { return max_nan(a, b); });
+                const bool live = !(top == -INFINITY);
                 const float shift = live ? top : 0.0f;
                 float sum = 0.0f;
 #pragma unroll
@@ -1226,21 +1267,16 @@ route_backward_kernel(const RouteBackwardLaunch p) {
                     sum += s[i];
                 }
                 sum = lanes_sum<G>(gmask, sum);
-                if (live) {
-                    inv = 1.0f / sum;
-                    zc = dz * (top + logf(sum)) * inv;
-                }
-            }
-            float z[V];                              // the z term, and for sigmoid the scores anew
-            if (softmax) {
+                const float inv = live ? __fdividef(1.0f, sum) : 0.0f;
+                zc = live ? dz * (top + __logf(sum)) : 0.0f;
 #pragma unroll
                 for (int i = 0; i < V; ++i) s[i] *= inv;
-                zc = live ? zc / inv : 0.0f;         // at s
-            } else {
+            }
+            if (!softmax) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     z[i] = dz != 0.0f ? zc * s[i] : 0.0f;
-                    s[i] = __fdividef(1.0f, 1.0f + expf(-l[i]));
+                    s[i] = rcp_fast(1.0f + expf(-l[i]));
                     Z += s[i];
                 }
             }
@@ -1248,23 +1284,25 @@ route_backward_kernel(const RouteBackwardLaunch p) {
             for (int i = 0; i < V / 4; ++i) s_own[i] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
             __syncwarp();
             // the weights' gradient, taken to the chosen scores
-            float cs[kOwn], chosen = 0.0f, dot = 0.0f;
+            float cs[kOwn], chosen = 0.0f, dot = 0.0f, to_score = p.scale;
 #pragma unroll
             for (int q = 0; q < kOwn; ++q) {
+                cs[q] = 0.0f;
+                if (q * G >= p.k) continue;
                 if (ce[q] >= p.E) ce[q] = -1;
-                cs[q] = ce[q] >= 0 ? s_row[ce[q]] : 0.0f;
+                if (ce[q] >= 0) cs[q] = s_row[ce[q]];
                 chosen += cs[q];
             }
             if (p.normalize) {
-                chosen = lanes_sum<G>(gmask, chosen) + kEps;
+                const float inv = 1.0f / (lanes_sum<G>(gmask, chosen) + kEps);
 #pragma unroll
-                for (int q = 0; q < kOwn; ++q) dot += cs[q] / chosen * cw[q];
+                for (int q = 0; q < kOwn; ++q) dot += cs[q] * inv * cw[q];
                 dot = lanes_sum<G>(gmask, dot);
+                to_score = p.k > 1 ? p.scale * inv : 0.0f;   // one weight alone is the constant scale
             }
-            const float to_score = p.normalize ? p.scale / chosen : p.scale;
 #pragma unroll
             for (int q = 0; q < kOwn; ++q)
-                if (ce[q] >= 0) g_row[ce[q]] = to_score * (cw[q] - dot);
+                if (q * G < p.k && ce[q] >= 0) g_row[ce[q]] = to_score * (cw[q] - dot);
             __syncwarp();
             float g[V];
 #pragma unroll
@@ -1295,13 +1333,13 @@ route_backward_kernel(const RouteBackwardLaunch p) {
                     for (int i = 0; i < V; ++i) sum += s[i] * a[i];
                     sum = lanes_sum<G>(gmask, sum);
                     Z = lanes_sum<G>(gmask, Z);
-                    invZ = live ? 1.0f / (Z + kEps) : 0.0f;
+                    invZ = 1.0f / (Z + kEps);        // a token that is not live has s = 0 and a finite factor
                     sum *= invZ;
                 }
 #pragma unroll
                 for (int i = 0; i < V; ++i) g[i] = s[i] * (1.0f - s[i]) * (g[i] + (a[i] - sum) * invZ) + z[i];
             }
-            // off experts have s = 0, and their products are 0; infinite ones are put out
+            // an expert that is off has s = 0, but NaN beside a NaN
 #pragma unroll
             for (int i = 0; i < V; ++i) g[i] = l[i] == -INFINITY ? 0.0f : g[i];
             if (inside) {
