@@ -12,16 +12,26 @@
 //   balance = 1/S' sum_b sum_e E c_be / (k n_b) P_be,  P_be = 1/n_b sum_t s[t,e] / (sum s[t,:] + 1e-20)
 //   z       = 1/N sum_t log(sum_e exp(l[t,e]))^2
 //
-// A token is held by G lanes of a warp, lane i keeping experts i V .. i V + V - 1 in
-// registers, so that index order is lane order and ties need no compare of indices.
-// The k best are taken in k rounds: every lane keeps the best of its own keys, a
-// round is one maximum over the lanes (redux on whole warps), one ballot, and the
-// winner alone looks its key up, clears it and finds its next best.
+// A token is held by G lanes of a warp, each keeping V experts in registers: up to eight
+// consecutive ones, so that index order is lane order.
+// The k best are found in one of three ways:
+//   16-bit logits, no bias: key and index share one word. k <= 8: every lane sorts its
+//     keys, and the eight best of two lanes are merged log2 G times; larger k: k rounds
+//     of a maximum over the lanes and a clearing, without a branch.
+//   other keys, G >= 16: the few that can be chosen are gathered, one a lane, and ranked.
+//   else: k rounds of a maximum, a ballot, and the winning lane looking up its next best.
 //
-// Keys that pass through exp carry an error of some 1e-7, and two experts nearer
-// than that would be chosen by rounding. Neighbouring chosen keys (and the last
-// kept and first dropped group) are compared with the bound of that error, and the
-// rare token that falls below it (about one in a thousand) is selected again in 64 bits.
+// Keys that pass through exp carry an error of some 1e-7, and two experts nearer than
+// that would be chosen by rounding. Neighbouring chosen keys, and the group sums at the
+// border, are compared with the bound of that error. The rare token below it (one in
+// some thousand) is decided in 64 bits, on the experts that matter, one a lane: the
+// 64-bit pipe takes some 60 cycles for an instruction, so that scoring every expert there
+// cost such a token 20 us.
+//
+// Bound by instructions, not by memory: 131072 tokens of 128 bf16 experts (34 MB, 5 us of
+// HBM) take 58 us at 340 warp instructions a token and 0.62 issued a cycle, with 24 warps
+// an SM; their backward (67 MB) 40 us at 220. At 8192 tokens of 256 experts in groups (24
+// us, 10 us for the backward) the latency of a block's two passes is what is left.
 //
 // Statistics are sums without float atomics: a block keeps its tokens' score sums
 // in registers and its counts in shared memory, and writes them to a slot of its
@@ -64,59 +74,85 @@ __device__ __forceinline__ float load_one(const void *p, int dtype, int64_t i) {
     return from_bits16(__ldg(static_cast<const unsigned short *>(p) + i), dtype);
 }
 
-// Experts e0 .. e0 + V - 1 of the row at element `row`; -inf past E. `vec`: the rows
+// A lane's experts: e0 + at<V>(i). Up to eight are consecutive; more (of a whole warp then) come
+// in fours, each four next to the neighbouring lane's, so that the warp's 16-byte accesses to
+// global and shared memory are consecutive (in one run a lane they met in the same banks, and
+// E = 832 took 2.2 times as long). There index order is not lane order, and ties compare indices.
+template <int V>
+__host__ __device__ constexpr int at(int i) { return V <= 8 ? i : (i >> 2) * 128 + (i & 3); }
+template <int V>
+__device__ __forceinline__ int first_expert(int sub) { return sub * (V <= 8 ? V : 4); }
+
+// The lane's experts of the row at element `row`; -inf past E. `vec`: the rows
 // are 16-byte aligned.
 template <int V>
 __device__ __forceinline__ void load_experts(const void *p, int dtype, int vec, int64_t row, int e0, int E,
                                              float (&l)[V]) {
-    if (vec && e0 + V <= E) {
-        if (dtype == MOE_DTYPE_F32) {
-            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + row + e0);
+    if constexpr (V <= 8) {
+        if (!vec || e0 + V > E) {
 #pragma unroll
-            for (int i = 0; i < V / 4; ++i) {
-                const float4 x = __ldg(q + i);
-                l[4 * i] = x.x;
-                l[4 * i + 1] = x.y;
-                l[4 * i + 2] = x.z;
-                l[4 * i + 3] = x.w;
+            for (int i = 0; i < V; ++i) l[i] = e0 + i < E ? load_one(p, dtype, row + e0 + i) : -INFINITY;
+            return;
+        }
+    }
+    // fours, and for 16-bit types the eight of V = 8 at once
+    if (dtype == MOE_DTYPE_F32) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const int e = e0 + at<V>(i);
+            if (V > 8 && !(vec && e + 4 <= E)) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) l[i + j] = e + j < E ? load_one(p, dtype, row + e + j) : -INFINITY;
+                continue;
             }
-        } else {
-            const uint2 *q = reinterpret_cast<const uint2 *>(static_cast<const unsigned short *>(p) + row + e0);
-            uint2 x[V / 4];                          // four 16-bit values each
-            if constexpr (V >= 8) {
-#pragma unroll
-                for (int i = 0; i < V / 8; ++i) {
-                    const uint4 y = __ldg(reinterpret_cast<const uint4 *>(q) + i);
-                    x[2 * i] = make_uint2(y.x, y.y);
-                    x[2 * i + 1] = make_uint2(y.z, y.w);
-                }
-            } else {
-                x[0] = __ldg(q);
-            }
-            if (dtype == MOE_DTYPE_BF16) {
-#pragma unroll
-                for (int i = 0; i < V / 4; ++i) {
-                    l[4 * i] = __uint_as_float(x[i].x << 16);
-                    l[4 * i + 1] = __uint_as_float(x[i].x & 0xffff0000u);
-                    l[4 * i + 2] = __uint_as_float(x[i].y << 16);
-                    l[4 * i + 3] = __uint_as_float(x[i].y & 0xffff0000u);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < V / 4; ++i) {
-                    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&x[i].x));
-                    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&x[i].y));
-                    l[4 * i] = a.x;
-                    l[4 * i + 1] = a.y;
-                    l[4 * i + 2] = b.x;
-                    l[4 * i + 3] = b.y;
-                }
-            }
+            const float4 x = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + row + e));
+            l[i] = x.x;
+            l[i + 1] = x.y;
+            l[i + 2] = x.z;
+            l[i + 3] = x.w;
         }
         return;
     }
+    const unsigned short *h = static_cast<const unsigned short *>(p) + row + e0;
+    uint2 x[V / 4];
+    if constexpr (V == 8) {
+        const uint4 y = __ldg(reinterpret_cast<const uint4 *>(h));
+        x[0] = make_uint2(y.x, y.y);
+        x[1] = make_uint2(y.z, y.w);
+    } else {
+        const unsigned off = dtype == MOE_DTYPE_BF16 ? 0xff80u : 0xfc00u;      // -inf
 #pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = e0 + i < E ? load_one(p, dtype, row + e0 + i) : -INFINITY;
+        for (int i = 0; i < V / 4; ++i) {
+            const int e = at<V>(4 * i);
+            if (V <= 8 || (vec && e0 + e + 4 <= E)) {
+                x[i] = __ldg(reinterpret_cast<const uint2 *>(h + e));
+            } else {
+                unsigned w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = e0 + e + j < E ? __ldg(h + e + j) : off;
+                x[i] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+            }
+        }
+    }
+    if (dtype == MOE_DTYPE_BF16) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            l[4 * i] = __uint_as_float(x[i].x << 16);
+            l[4 * i + 1] = __uint_as_float(x[i].x & 0xffff0000u);
+            l[4 * i + 2] = __uint_as_float(x[i].y << 16);
+            l[4 * i + 3] = __uint_as_float(x[i].y & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&x[i].x));
+            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&x[i].y));
+            l[4 * i] = a.x;
+            l[4 * i + 1] = a.y;
+            l[4 * i + 2] = b.x;
+            l[4 * i + 3] = b.y;
+        }
+    }
 }
 
 // 2^x (2 ulp). softmax's exp(l - top) is taken as 2^((l - top) log2 e), whose exponent has
@@ -243,12 +279,12 @@ __device__ __forceinline__ WideScore wide_score(const RouteLaunch &p, int64_t ro
     float top = -INFINITY;
 #pragma unroll (V <= 8 ? V : 1)
     for (int i = 0; i < V; ++i)
-        if (e0 + i < p.E) top = fmaxf(top, load_one(p.logits, p.dtype, row + e0 + i));
+        if (e0 + at<V>(i) < p.E) top = fmaxf(top, load_one(p.logits, p.dtype, row + e0 + at<V>(i)));
     w.top = lanes_max<G>(gmask, top);
     double z = 0.0;
 #pragma unroll (V <= 8 ? V : 1)
     for (int i = 0; i < V; ++i)
-        if (e0 + i < p.E) z += exp(static_cast<double>(load_one(p.logits, p.dtype, row + e0 + i)) - w.top);
+        if (e0 + at<V>(i) < p.E) z += exp(static_cast<double>(load_one(p.logits, p.dtype, row + e0 + at<V>(i))) - w.top);
     for (int off = G / 2; off > 0; off >>= 1) z += __shfl_xor_sync(gmask, z, off);
     w.inv = 1.0 / z;
     return w;
@@ -259,13 +295,13 @@ __device__ __forceinline__ WideScore wide_score(const RouteLaunch &p, int64_t ro
 template <int G, int V>
 __device__ __noinline__ void select_near(const RouteLaunch &p, int64_t row, int sub, unsigned gmask, unsigned cand,
                                          int *out_idx, float *out_s) {
-    const int e0 = sub * V, lane = threadIdx.x & 31;
+    const int e0 = first_expert<V>(sub), lane = threadIdx.x & 31;
     const WideScore score = wide_score<G, V>(p, row, e0, gmask);
     int n = 0;
 #pragma unroll (V <= 8 ? V : 1)
     for (int i = 0; i < V; ++i) {
         const unsigned b = __ballot_sync(gmask, (cand >> i) & 1u) & gmask;
-        if ((cand >> i) & 1u) out_idx[n + __popc(b & ((1u << lane) - 1u))] = e0 + i;
+        if ((cand >> i) & 1u) out_idx[n + __popc(b & ((1u << lane) - 1u))] = e0 + at<V>(i);
         n += __popc(b);
     }
     __syncwarp(gmask);
@@ -300,35 +336,38 @@ template <int G, int V>
 __device__ __noinline__ unsigned resolve_groups(const RouteLaunch &p, int64_t row, const float *sel_row, int sub,
                                                 unsigned gmask, unsigned near, int room, float err1, bool biased, int *list,
                                                 double *group) {
-    const int lane = threadIdx.x & 31, e0 = sub * V;
+    const int lane = threadIdx.x & 31, e0 = first_expert<V>(sub);
     const int gs = p.E / p.n_group;
     const bool softmax = p.score_fn == MOE_SCORE_SOFTMAX;
     int n = 0;
     for (unsigned left = near; left != 0; left &= left - 1u) {
         const int g = __ffs(left) - 1;
-        const int first = max(e0, g * gs), last = min(e0 + V, (g + 1) * gs);
+        auto inside = [&](int i) {                   // the lane's i-th expert is one of the group's
+            const int e = e0 + at<V>(i);
+            return e >= g * gs && e < (g + 1) * gs;
+        };
         // the group's group_topn-th best, ties counted
         int floor = 0x7fffffff;
         for (int taken = 0; taken < p.group_topn;) {
             int best = kGone;
-            for (int e = first; e < last; ++e) {
-                const int k = order_key(sel_row[e]);
+            for (int i = 0; i < V; ++i) {
+                const int k = inside(i) ? order_key(sel_row[e0 + at<V>(i)]) : kGone;
                 if (k < floor && k > best) best = k;
             }
             const int m = lanes_max_key<G>(gmask, best);
             if (m < kFirst) break;
             int same = 0;
-            for (int e = first; e < last; ++e) same += order_key(sel_row[e]) == m;
+            for (int i = 0; i < V; ++i) same += inside(i) && order_key(sel_row[e0 + at<V>(i)]) == m;
             taken += lanes_reduce<G>(gmask, same, [](int a, int b) { return a + b; });
             floor = m;
         }
         const float least = key_value(floor) - 2.0f * err1;
         for (int i = 0; i < V; ++i) {
-            const int e = e0 + i;
-            const bool in = e >= first && e < last && sel_row[e] > -INFINITY && sel_row[e] >= least;
+            const int e = e0 + at<V>(i);
+            const bool in = inside(i) && sel_row[e] > -INFINITY && sel_row[e] >= least;
             const unsigned who = __ballot_sync(gmask, in) & gmask;
-            const int at = n + __popc(who & ((1u << lane) - 1u));
-            if (in && at < G) list[at] = e;
+            const int place = n + __popc(who & ((1u << lane) - 1u));
+            if (in && place < G) list[place] = e;
             n += __popc(who);
         }
     }
@@ -383,22 +422,22 @@ __device__ __noinline__ unsigned resolve_groups(const RouteLaunch &p, int64_t ro
 template <int G, int V>
 __device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int sub, unsigned gmask, unsigned sure,
                                          unsigned near, int *out_idx, float *out_s, double *group) {
-    const int e0 = sub * V;
+    const int e0 = first_expert<V>(sub);
     const WideScore score = wide_score<G, V>(p, row, e0, gmask);
     const bool softmax = p.score_fn == MOE_SCORE_SOFTMAX;
     const int gs = p.E / p.n_group, g_first = e0 / gs, bound = (g_first + 1) * gs;
-    auto group_of = [&](int e) { return gs >= V ? g_first + (e >= bound) : e / gs; };
+    auto group_of = [&](int e) { return V <= 8 && gs >= V ? g_first + (e >= bound) : e / gs; };
     double sel[V];
     uint64_t key[V];
     unsigned open = 0;                               // experts that may still be chosen
 #pragma unroll (V <= 8 ? V : 1)
     for (int i = 0; i < V; ++i) {
         key[i] = 0;
-        if (e0 + i >= p.E || !(((sure | near) >> group_of(e0 + i)) & 1u)) continue;
-        const float l = load_one(p.logits, p.dtype, row + e0 + i);
+        if (e0 + at<V>(i) >= p.E || !(((sure | near) >> group_of(e0 + at<V>(i))) & 1u)) continue;
+        const float l = load_one(p.logits, p.dtype, row + e0 + at<V>(i));
         if (l == -INFINITY) continue;
         open |= 1u << i;
-        sel[i] = score(softmax, l) + (p.sel_bias != nullptr ? static_cast<double>(__ldg(p.sel_bias + e0 + i)) : 0.0);
+        sel[i] = score(softmax, l) + (p.sel_bias != nullptr ? static_cast<double>(__ldg(p.sel_bias + e0 + at<V>(i))) : 0.0);
         key[i] = order_key64(sel[i]);
     }
     if (near != 0) {
@@ -410,19 +449,19 @@ __device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int 
                 uint64_t b = 0;
 #pragma unroll (V <= 8 ? V : 1)
                 for (int i = 0; i < V; ++i)
-                    if (((open & ~taken) >> i) & 1u && group_of(e0 + i) == g && key[i] > b) b = key[i];
+                    if (((open & ~taken) >> i) & 1u && group_of(e0 + at<V>(i)) == g && key[i] > b) b = key[i];
                 const uint64_t m = lanes_max_u64<G>(gmask, b);
                 if (m == 0) break;
                 const unsigned who = __ballot_sync(gmask, b == m) & gmask;
                 const int from = __ffs(who) - 1;
                 double v = 0.0;
                 if ((threadIdx.x & 31) == from) {
-                    int at = 0;
+                    int pick = 0;
 #pragma unroll (V <= 8 ? V : 1)
                     for (int i = V - 1; i >= 0; --i)
-                        if (((open & ~taken) >> i) & 1u && group_of(e0 + i) == g && key[i] == m) at = i;
-                    taken |= 1u << at;
-                    v = sel[at];
+                        if (((open & ~taken) >> i) & 1u && group_of(e0 + at<V>(i)) == g && key[i] == m) pick = i;
+                    taken |= 1u << pick;
+                    v = sel[pick];
                 }
                 v = __shfl_sync(gmask, v, from);
                 total = n == 0 ? v : total + v;
@@ -434,7 +473,7 @@ __device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int 
 #pragma unroll (V <= 8 ? V : 1)
         for (int i = 0; i < V; ++i) {
             if (!((open >> i) & 1u)) continue;
-            const int g = group_of(e0 + i);
+            const int g = group_of(e0 + at<V>(i));
             if (!((near >> g) & 1u)) continue;
             int before = 0;
             for (unsigned left = near; left != 0; left &= left - 1u) {
@@ -451,21 +490,24 @@ __device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int 
     if (p.sel_bias == nullptr)                       // the score's order is the logit's
 #pragma unroll (V <= 8 ? V : 1)
         for (int i = 0; i < V; ++i)
-            if ((open >> i) & 1u) key[i] = order_key64(load_one(p.logits, p.dtype, row + e0 + i));
+            if ((open >> i) & 1u) key[i] = order_key64(load_one(p.logits, p.dtype, row + e0 + at<V>(i)));
     for (int j = 0; j < p.k; ++j) {
         uint64_t b = 0;
 #pragma unroll (V <= 8 ? V : 1)
         for (int i = 0; i < V; ++i) b = max(b, key[i]);
         const uint64_t m = lanes_max_u64<G>(gmask, b);
-        const unsigned who = __ballot_sync(gmask, b == m) & gmask;
-        if ((threadIdx.x & 31) == __ffs(who) - 1) {
-            int at = -1;
-            if (m != 0)
+        // the lowest index among equal keys
+        int mine = -1;
 #pragma unroll (V <= 8 ? V : 1)
-                for (int i = V - 1; i >= 0; --i)
-                    if (key[i] == m) at = i;
-            if (at >= 0) key[at] = 0;
-            out_idx[j] = at < 0 ? -1 : e0 + at;
+        for (int i = V - 1; i >= 0; --i)
+            if (m != 0 && key[i] == m) mine = i;
+        const int e = mine < 0 ? -0x7fffffff : -(e0 + at<V>(mine));
+        const int best = lanes_max_key<G>(gmask, e);
+        if (mine >= 0 && e == best) {
+            key[mine] = 0;
+            out_idx[j] = -best;
+        } else if (best == -0x7fffffff && sub == 0) {
+            out_idx[j] = -1;
         }
     }
     __syncwarp(gmask);
@@ -561,7 +603,7 @@ __device__ __forceinline__ unsigned kept_groups(const RouteLaunch &p, const floa
         if (g * p.group_lanes == sub && g < p.n_group) sums[g] = p.group_topn == 2 && b > -INFINITY ? a + b : a;
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) sel_row[sub * V + i] = vals[i];
+        for (int i = 0; i < V; ++i) sel_row[first_expert<V>(sub) + at<V>(i)] = vals[i];
         __syncwarp();
         search_groups<G>(p, sel_row, sums, sub, gmask);
     }
@@ -612,26 +654,30 @@ route_kernel(const RouteLaunch p) {
     const int row = threadIdx.x / G, sub = threadIdx.x % G;
     const int lane = threadIdx.x & 31;
     const unsigned gmask = G == 32 ? 0xffffffffu : ((1u << G) - 1u) << (lane / G * G);
-    const int e0 = sub * V;
+    const int e0 = first_expert<V>(sub);
     const int t_begin = blockIdx.x * p.per_block;
     const int t_end = min(p.T, t_begin + p.per_block);
     const bool grouped = p.n_group > 1 && p.topk_group < p.n_group;
     const bool softmax = p.score_fn == MOE_SCORE_SOFTMAX;
     const bool biased = !kShort && p.sel_bias != nullptr;
-    const int gs = p.E / p.n_group, g_first = e0 / gs;
+    const int gs = p.E / p.n_group;
+    constexpr int kRuns = V <= 8 ? 1 : V / 4, kRun = V / kRuns;   // runs of consecutive experts
+    int run_group[kRuns];
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r) run_group[r] = grouped ? (e0 + at<V>(r * kRun)) / gs : 0;
     float *own_row = buf + row * G * V;
     // a lane's biases stay in registers where there are few
     constexpr int kHeld = V <= 8 ? V : 1;
     float held[kHeld], bias_max = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const float b = biased && e0 + i < p.E ? __ldg(p.sel_bias + e0 + i) : 0.0f;
+        const float b = biased && e0 + at<V>(i) < p.E ? __ldg(p.sel_bias + e0 + at<V>(i)) : 0.0f;
         if (V <= 8) held[i % kHeld] = b;
         bias_max = fmaxf(bias_max, fabsf(b));
     }
     auto bias = [&](int i) {
         if (V <= 8) return held[i % kHeld];
-        return biased && e0 + i < p.E ? __ldg(p.sel_bias + e0 + i) : 0.0f;
+        return biased && e0 + at<V>(i) < p.E ? __ldg(p.sel_bias + e0 + at<V>(i)) : 0.0f;
     };
     if (biased) bias_max = lanes_max<G>(gmask, bias_max);
     // with no bias, or none but zeros, the order is the logits' own, without a rounding; so is
@@ -640,9 +686,9 @@ route_kernel(const RouteLaunch p) {
     const bool best_only = !by_score && p.group_topn == 1;
     int seq = 0;
     float acc[kShared ? 1 : V];
-    float *own_sums = sums_buf + (kStats && kShared ? row * G * V + e0 : 0);
+    float *own_sums = sums_buf + (kStats && kShared ? row * G * V + e0 : 0);      // at<V>(i)
     auto add = [&](int i, float v) {
-        if (kShared) own_sums[i] += v;
+        if (kShared) own_sums[at<V>(i)] += v;
         else acc[kShared ? 0 : i] += v;
     };
     float z_acc = 0.0f;
@@ -651,7 +697,7 @@ route_kernel(const RouteLaunch p) {
         if (blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (kShared) own_sums[i] = 0.0f;
+            if (kShared) own_sums[at<V>(i)] = 0.0f;
             else acc[kShared ? 0 : i] = 0.0f;
         }
         for (int e = threadIdx.x; e < G * V; e += kThreads) hist[e] = 0;
@@ -749,7 +795,7 @@ route_kernel(const RouteLaunch p) {
             for (int i = 0; i < V; ++i) {
                 const float by = l[i] == -INFINITY ? -INFINITY : s[i] + bias(i);
                 key[i] = order_key(by_score ? by : l[i]);
-                if (kShort) key[i] = (key[i] & ~static_cast<int>(kIndexBits)) | (kIndexMax - (e0 + i));
+                if (kShort) key[i] = (key[i] & ~static_cast<int>(kIndexBits)) | (kIndexMax - (e0 + at<V>(i)));
             }
             if (grouped) {
                 float v[V];
@@ -761,7 +807,7 @@ route_kernel(const RouteLaunch p) {
                                          near_groups);
                 if (near_groups != 0) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) own_row[e0 + i] = v[i];
+                    for (int i = 0; i < V; ++i) own_row[e0 + at<V>(i)] = v[i];
                     __syncwarp(gmask);
                     const unsigned sure = kept & ~near_groups;
                     const unsigned stay = resolve_groups<G, V>(p, lrow, own_row, sub, gmask, near_groups,
@@ -773,19 +819,22 @@ route_kernel(const RouteLaunch p) {
                         near_groups = 0;
                     }
                 }
-                int g = g_first, next = (g + 1) * gs;
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    if (e0 + i == next) {
-                        ++g;
-                        next += gs;
+                for (int r = 0; r < kRuns; ++r) {
+                    int g = run_group[r], next = (g + 1) * gs;
+#pragma unroll
+                    for (int i = r * kRun; i < (r + 1) * kRun; ++i) {
+                        if (e0 + at<V>(i) == next) {
+                            ++g;
+                            next += gs;
+                        }
+                        if (!((kept >> (g & 31)) & 1u)) key[i] = kGone;
                     }
-                    if (!((kept >> (g & 31)) & 1u)) key[i] = kGone;
                 }
                 __syncwarp();
             }
 #pragma unroll
-            for (int i = 0; i < V; ++i) own_row[e0 + i] = s[i];
+            for (int i = 0; i < V; ++i) own_row[e0 + at<V>(i)] = s[i];
             int best = key[0];
 #pragma unroll
             for (int i = 1; i < V; ++i) best = max(best, key[i]);
@@ -854,10 +903,10 @@ route_kernel(const RouteLaunch p) {
                     for (int i = 0; i < V; ++i) {
                         const bool in = key[i] >= floor;
                         const unsigned who = __ballot_sync(0xffffffffu, in) & gmask;
-                        const int at = n + __popc(who & ((1u << lane) - 1u));
-                        if (in && at < G) {
-                            slots.idx[row][at] = e0 + i;
-                            slots.key[row][at] = key[i];
+                        const int place = n + __popc(who & ((1u << lane) - 1u));
+                        if (in && place < G) {
+                            slots.idx[row][place] = e0 + at<V>(i);
+                            slots.key[row][place] = key[i];
                         }
                         n += __popc(who);
                     }
@@ -882,21 +931,28 @@ route_kernel(const RouteLaunch p) {
                 } else {
                     for (int j = 0; j < rounds; ++j) {
                         const int m = lanes_max_key<G>(gmask, best);
-                        const unsigned who = __ballot_sync(0xffffffffu, best == m) & gmask;
-                        if (lane == __ffs(who) - 1) {
-                            int at = -1;
-                            if (m >= kFirst) {
+                        int mine = -1;               // the lane's first with that key
 #pragma unroll
-                                for (int i = V - 1; i >= 0; --i)
-                                    if (key[i] == m) at = i;
+                        for (int i = V - 1; i >= 0; --i)
+                            if (key[i] == m) mine = i;
+                        bool wins;
+                        if constexpr (V <= 8) {
+                            const unsigned who = __ballot_sync(0xffffffffu, best == m) & gmask;
+                            wins = lane == __ffs(who) - 1;
+                        } else {
+                            const int e = mine < 0 ? -0x7fffffff : -(e0 + at<V>(mine));
+                            wins = lanes_max_key<G>(gmask, e) == e && mine >= 0;
+                        }
+                        if (wins) {
+                            if (m >= kFirst) {
                                 best = kGone;
 #pragma unroll
                                 for (int i = 0; i < V; ++i) {
-                                    if (i == at) key[i] = kGone;
+                                    if (i == mine) key[i] = kGone;
                                     best = max(best, key[i]);
                                 }
                             }
-                            slots.idx[row][j] = at < 0 ? -1 : e0 + at;
+                            slots.idx[row][j] = m >= kFirst ? e0 + at<V>(mine) : -1;
                             slots.key[row][j] = m;
                         }
                     }
@@ -933,8 +989,8 @@ route_kernel(const RouteLaunch p) {
                     const float floor = last - 2.0f * (rel * s_max + 2.0f * kUlp * (s_max + bias_max));
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        const float v = own_row[e0 + i] + bias(i);
-                        if (l[i] != -INFINITY && v >= floor && (!grouped || (kept >> ((e0 + i) / gs)) & 1u)) cand |= 1u << i;
+                        const float v = own_row[e0 + at<V>(i)] + bias(i);
+                        if (l[i] != -INFINITY && v >= floor && (!grouped || (kept >> ((e0 + at<V>(i)) / gs)) & 1u)) cand |= 1u << i;
                     }
                     n = lanes_reduce<G>(gmask, __popc(cand), [](int a, int b) { return a + b; });
                 }
@@ -975,8 +1031,8 @@ route_kernel(const RouteLaunch p) {
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                own_row[e0 + i] = kShared ? own_sums[i] : acc[kShared ? 0 : i];
-                if (kShared) own_sums[i] = 0.0f;
+                own_row[e0 + at<V>(i)] = kShared ? own_sums[at<V>(i)] : acc[kShared ? 0 : i];
+                if (kShared) own_sums[at<V>(i)] = 0.0f;
                 else acc[kShared ? 0 : i] = 0.0f;
             }
             if (sub == 0) {
@@ -1186,11 +1242,14 @@ route_backward_kernel(const RouteBackwardLaunch p) {
     constexpr int kThreads = kBlock<V>, kRows = kThreads / G;
     constexpr int kOwn = kMaxK / G;                  // slots of a lane
     __shared__ __align__(16) float s_buf[kRows * G * V], g_buf[kRows * G * V];
+    // a's row of the sequence: in registers where a lane has few experts
+    constexpr bool kShared = V > 8;
+    __shared__ float a_buf[kShared ? G * V : 1];
     griddep_wait();
     const int row = threadIdx.x / G, sub = threadIdx.x % G;
     const int lane = threadIdx.x & 31;
     const unsigned gmask = G == 32 ? 0xffffffffu : ((1u << G) - 1u) << (lane / G * G);
-    const int e0 = sub * V;
+    const int e0 = first_expert<V>(sub);
     const int t_begin = blockIdx.x * p.per_block;
     const int t_end = min(p.T, t_begin + p.per_block);
     const bool terms = p.dlosses != nullptr;
@@ -1206,25 +1265,32 @@ route_backward_kernel(const RouteBackwardLaunch p) {
         }
     }
     float *s_row = s_buf + row * G * V, *g_row = g_buf + row * G * V;
-    float4 *s_own = reinterpret_cast<float4 *>(s_row + e0), *g_own = reinterpret_cast<float4 *>(g_row + e0);
+    auto fours = [&](float *of, int i) { return reinterpret_cast<float4 *>(of + e0 + at<V>(4 * i)); };
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) g_own[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = 0; i < V / 4; ++i) *fours(g_row, i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     int t = t_begin;
     while (t < t_end) {
         int seg_end = t_end;
-        float a[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) a[i] = 0.0f;
+        float f = 0.0f;
+        float held[kShared ? 1 : V];
+        auto a = [&](int i) { return kShared ? a_buf[e0 + at<V>(i)] : held[kShared ? 0 : i]; };
         if (terms) {
             while (seq < p.S - 1 && __ldg(p.seq_offsets + seq + 1) <= t) ++seq;
             if (seq < p.S - 1) seg_end = min(t_end, __ldg(p.seq_offsets + seq + 1));
             const float n = static_cast<float>(max(1, __ldg(p.seq_tokens + seq)));
             const float used = static_cast<float>(max(1, __ldg(p.seq_tokens + p.S + 1)));
-            const float f = dbal / used * (static_cast<float>(p.E) / n) / (n * static_cast<float>(p.k));
+            f = dbal / used * (static_cast<float>(p.E) / n) / (n * static_cast<float>(p.k));
+        }
+        auto of = [&](int e) {
+            return terms && e < p.E ? f * static_cast<float>(__ldg(p.counts + static_cast<int64_t>(seq) * p.E + e)) : 0.0f;
+        };
+        if constexpr (kShared) {
+            __syncthreads();                         // the last sequence's are used
+            for (int e = threadIdx.x; e < G * V; e += kThreads) a_buf[e] = of(e);
+            __syncthreads();
+        } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (e0 + i < p.E)
-                    a[i] = f * static_cast<float>(__ldg(p.counts + static_cast<int64_t>(seq) * p.E + e0 + i));
+            for (int i = 0; i < V; ++i) held[i] = of(e0 + at<V>(i));
         }
         for (int base = t; base < seg_end; base += kRows) {
             const int tok = base + row;
@@ -1251,6 +1317,9 @@ route_backward_kernel(const RouteBackwardLaunch p) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) l[i] = -INFINITY;
             }
+            unsigned off = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) off |= l[i] == -INFINITY ? 1u << i : 0u;
             float zc = 0.0f, Z = 0.0f;               // z's coefficient at s; sigmoid: the sum of scores
             float z[V];                              // sigmoid: the z term
             if (softmax || dz != 0.0f) {
@@ -1281,7 +1350,7 @@ route_backward_kernel(const RouteBackwardLaunch p) {
                 }
             }
 #pragma unroll
-            for (int i = 0; i < V / 4; ++i) s_own[i] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+            for (int i = 0; i < V / 4; ++i) *fours(s_row, i) = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
             __syncwarp();
             // the weights' gradient, taken to the chosen scores
             float cs[kOwn], chosen = 0.0f, dot = 0.0f, to_score = p.scale;
@@ -1307,12 +1376,12 @@ route_backward_kernel(const RouteBackwardLaunch p) {
             float g[V];
 #pragma unroll
             for (int i = 0; i < V / 4; ++i) {
-                const float4 x = g_own[i];
+                const float4 x = *fours(g_row, i);
                 g[4 * i] = x.x;
                 g[4 * i + 1] = x.y;
                 g[4 * i + 2] = x.z;
                 g[4 * i + 3] = x.w;
-                g_own[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                *fours(g_row, i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
             // through the score function
             float sum = 0.0f;
@@ -1320,40 +1389,41 @@ route_backward_kernel(const RouteBackwardLaunch p) {
                 // the chosen scores' part of sum s g vanishes where the weights are normalised
                 if (terms || !p.normalize) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) sum += s[i] * (p.normalize ? a[i] : g[i] + a[i]);
+                    for (int i = 0; i < V; ++i) sum += s[i] * (p.normalize ? a(i) : g[i] + a(i));
                     sum = lanes_sum<G>(gmask, sum);
                 }
                 const float minus = zc - sum;
 #pragma unroll
-                for (int i = 0; i < V; ++i) g[i] = s[i] * (g[i] + (a[i] + minus));
+                for (int i = 0; i < V; ++i) g[i] = s[i] * (g[i] + (a(i) + minus));
             } else {
                 float invZ = 0.0f;
                 if (terms) {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) sum += s[i] * a[i];
+                    for (int i = 0; i < V; ++i) sum += s[i] * a(i);
                     sum = lanes_sum<G>(gmask, sum);
                     Z = lanes_sum<G>(gmask, Z);
                     invZ = 1.0f / (Z + kEps);        // a token that is not live has s = 0 and a finite factor
                     sum *= invZ;
                 }
 #pragma unroll
-                for (int i = 0; i < V; ++i) g[i] = s[i] * (1.0f - s[i]) * (g[i] + (a[i] - sum) * invZ) + z[i];
+                for (int i = 0; i < V; ++i) g[i] = s[i] * (1.0f - s[i]) * (g[i] + (a(i) - sum) * invZ) + z[i];
             }
             // an expert that is off has s = 0, but NaN beside a NaN
 #pragma unroll
-            for (int i = 0; i < V; ++i) g[i] = l[i] == -INFINITY ? 0.0f : g[i];
+            for (int i = 0; i < V; ++i) g[i] = (off >> i) & 1u ? 0.0f : g[i];
             if (inside) {
                 const int64_t out = static_cast<int64_t>(tok) * p.E + e0;
                 if (p.dtype == MOE_DTYPE_F32) {
                     float *q = static_cast<float *>(p.dlogits) + out;
-                    if (p.vec_out && e0 + V <= p.E) {
 #pragma unroll
-                        for (int i = 0; i < V / 4; ++i)
-                            reinterpret_cast<float4 *>(q)[i] = make_float4(g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]);
-                    } else {
+                    for (int i = 0; i < V; i += 4) {
+                        if (p.vec_out && e0 + at<V>(i) + 4 <= p.E) {
+                            *reinterpret_cast<float4 *>(q + at<V>(i)) = make_float4(g[i], g[i + 1], g[i + 2], g[i + 3]);
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < V; ++i)
-                            if (e0 + i < p.E) q[i] = g[i];
+                            for (int j = i; j < i + 4; ++j)
+                                if (e0 + at<V>(j) < p.E) q[at<V>(j)] = g[j];
+                        }
                     }
                 } else {
                     uint32_t pk[V / 2];
@@ -1368,18 +1438,20 @@ route_backward_kernel(const RouteBackwardLaunch p) {
                         }
                     }
                     unsigned short *q = static_cast<unsigned short *>(p.dlogits) + out;
-                    if (p.vec_out && e0 + V <= p.E) {
-                        if constexpr (V >= 8) {
-#pragma unroll
-                            for (int i = 0; i < V / 8; ++i)
-                                reinterpret_cast<uint4 *>(q)[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-                        } else {
-                            *reinterpret_cast<uint2 *>(q) = make_uint2(pk[0], pk[1]);
-                        }
+                    if (V == 8 && p.vec_out && e0 + V <= p.E) {
+                        *reinterpret_cast<uint4 *>(q) = make_uint4(pk[0], pk[1], pk[2 % (V / 2)], pk[3 % (V / 2)]);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < V; ++i)
-                            if (e0 + i < p.E) q[i] = static_cast<unsigned short>(pk[i / 2] >> (16 * (i & 1)));
+                        for (int i = 0; i < V; i += 4) {
+                            if (p.vec_out && e0 + at<V>(i) + 4 <= p.E) {
+                                *reinterpret_cast<uint2 *>(q + at<V>(i)) = make_uint2(pk[i / 2], pk[i / 2 + 1]);
+                            } else {
+#pragma unroll
+                                for (int j = i; j < i + 4; ++j)
+                                    if (e0 + at<V>(j) < p.E)
+                                        q[at<V>(j)] = static_cast<unsigned short>(pk[j / 2] >> (16 * (j & 1)));
+                            }
+                        }
                     }
                 }
             }
@@ -1499,7 +1571,7 @@ cudaError_t launch_route(const RouteLaunch &launch, cudaStream_t st) {
     cudaError_t err = with_layout(p.E, [&](auto g, auto v) {
         constexpr int G = decltype(g)::value, V = decltype(v)::value;
         const int gs = p.E / p.n_group, lanes = gs / V;
-        p.group_lanes = p.group_topn <= 2 && gs % V == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+        p.group_lanes = V <= 8 && p.group_topn <= 2 && gs % V == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
         const dim3 grid(static_cast<unsigned>(tiles.blocks));
         const bool brief = p.dtype != MOE_DTYPE_F32 && p.sel_bias == nullptr;
         if (p.losses != nullptr)
