@@ -898,17 +898,42 @@ route_kernel(const RouteLaunch p) {
                         if (lane_best == floor) lane_best = kGone;
                     }
                     floor = max(floor, kFirst);
-                    n = 0;
+                    auto gather = [&] {
+                        n = 0;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const bool in = key[i] >= floor;
-                        const unsigned who = __ballot_sync(0xffffffffu, in) & gmask;
-                        const int place = n + __popc(who & ((1u << lane) - 1u));
-                        if (in && place < G) {
-                            slots.idx[row][place] = e0 + at<V>(i);
-                            slots.key[row][place] = key[i];
+                        for (int i = 0; i < V; ++i) {
+                            const bool in = key[i] >= floor;
+                            const unsigned who = __ballot_sync(0xffffffffu, in) & gmask;
+                            const int place = n + __popc(who & ((1u << lane) - 1u));
+                            if (in && place < G) {
+                                slots.idx[row][place] = e0 + at<V>(i);
+                                slots.key[row][place] = key[i];
+                            }
+                            n += __popc(who);
                         }
-                        n += __popc(who);
+                    };
+                    gather();
+                    if (!__all_sync(0xffffffffu, n <= G)) {
+                        // too many (more chosen experts than a quarter of the lanes, as a rule): a
+                        // floor with no fewer than `rounds` above it and no more than lanes, by halving
+                        if (n > G) {
+                            int low = floor, high = lanes_max_key<G>(gmask, best);
+                            while (static_cast<unsigned>(high) - static_cast<unsigned>(low) > 1u) {
+                                const int mid =
+                                    low + static_cast<int>((static_cast<unsigned>(high) - static_cast<unsigned>(low)) >> 1);
+                                int c = 0;
+#pragma unroll
+                                for (int i = 0; i < V; ++i) c += key[i] >= mid;
+                                c = lanes_reduce<G>(gmask, c, [](int a, int b) { return a + b; });
+                                if (c > G) low = mid;
+                                else high = mid;
+                                if (c >= rounds && c <= G) {
+                                    floor = mid;
+                                    break;
+                                }
+                            }
+                        }
+                        gather();
                     }
                 }
                 if (__all_sync(0xffffffffu, n <= G)) {
