@@ -61,7 +61,7 @@ class AdamW:
 
     `step(grads=None, max_norm=0.0)` uses the parameters' .grad where no list is given; parameters
     without a gradient are left alone. `lr` and `step_count` are device tensors: write into `lr`
-    for a schedule. After an update in place, drop the weights' MXFP8 copies
+    for a schedule. Masters are copies made here (`refresh_masters`). After an update in place, drop the weights' MXFP8 copies
     (`MxWeightCache.invalidate`)."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, masters=True,
@@ -74,6 +74,13 @@ class AdamW:
         self.exp_avg = [torch.zeros_like(p, dtype=torch.float32) for p in self.params]
         self.exp_avg_sq = [torch.zeros_like(p, dtype=torch.float32) for p in self.params]
         self.masters = [p.detach().float() if masters and p.dtype != torch.float32 else None for p in self.params]
+
+    def refresh_masters(self):
+        """Takes the masters from the parameters again, after something else wrote into those (a
+        checkpoint that was loaded); a step writes the parameters from them."""
+        for p, x in zip(self.params, self.masters):
+            if x is not None:
+                x.copy_(p.detach())
 
     def step(self, grads=None, max_norm=0.0):
         """One update; returns the gradients' norm as in adamw_step."""

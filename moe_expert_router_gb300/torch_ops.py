@@ -26,7 +26,7 @@ runs the router (keeping the fp32 logits), the routing metadata and both stages
 (keeping the pre-activation h), and `torch.ops.moe_gb300.layer_backward` runs the
 library's backward (dX with the router's term, dW_r, dW1, dW2); `register_autograd`
 joins them. Gradients reach the router through y only: topk_idx, topk_w and aux
-are returned without a gradient (the library does not differentiate aux).
+are returned without a gradient (`route`, below, has balance terms with one).
 `moe_layer(..., precision="mxfp8")` runs the expert stages and the weight gradients
 in MXFP8 (`layer_train_mx` / `layer_backward_mx`; the data gradients stay bf16, as in
 the guide's section "Expert precision") on E4M3 copies of w1 and w2 from an

@@ -240,3 +240,12 @@ def test_optimizer_matches_torch_and_replays():
         torch.testing.assert_close(a, b, rtol=2e-5, atol=2e-6)
         assert torch.equal(b.detach(), c)
     assert torch.equal(ours[2].detach(), start[2])
+
+
+def test_masters_follow_what_is_written_into_the_parameters():
+    p = torch.randn((3, 40), generator=torch.Generator().manual_seed(0)).bfloat16().to(DEV)
+    o = optim.AdamW([p], lr=0.0)
+    p.fill_(2.0)
+    o.refresh_masters()
+    o.step([torch.ones_like(p)])
+    assert (p == 2.0).all() and (o.masters[0] == 2.0).all()

@@ -156,6 +156,36 @@ def test_scores_that_tie_in_32_bits_are_told_apart(E, score):
     check(l, 6 if E > 8 else 3, score, bias=bias, n_group=2, topk_group=1, group_topn=2, backward=False)
 
 
+@pytest.mark.parametrize("E", [8, 20, 64, 128, 256, 300, 512, 1024])
+@pytest.mark.parametrize("many", [False, True])
+def test_saturated_scores_under_a_bias(E, many):
+    """Sigmoid scores that are 1 in fp32 and a bias that is the same for all: the order is the
+    logits', for a few experts of a row or all of them, with groups and without."""
+    rng = np.random.default_rng(E)
+    l = rng.normal(size=(60, E))
+    for t in range(60):
+        n = E if many else min(E, 1 + t % 7)
+        l[t, rng.permutation(E)[:n]] = rng.uniform(17.0, 24.0, size=n)
+    l[5, 0] = -np.inf
+    l = torch.tensor(l, dtype=torch.float32, device=DEV)
+    bias = torch.full((E,), 0.5, device=DEV)
+    check(l, 4, "sigmoid", bias=bias, backward=False)
+    if E % 4 == 0:
+        check(l, 4, "sigmoid", bias=bias, n_group=4, topk_group=2, group_topn=1, backward=False)
+        check(l, 3, "sigmoid", bias=bias, n_group=4, topk_group=2, group_topn=2, backward=False)
+        check(l, 3, "sigmoid", n_group=4, topk_group=3, group_topn=2, backward=False)
+
+
+@pytest.mark.parametrize("E,k", [(40, 20), (64, 31), (128, 17), (256, 24), (256, 32), (600, 30), (1024, 25)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_chosen_experts(E, k, dtype):
+    """More chosen experts than a quarter of the lanes; bf16 logits tie often."""
+    bias = torch.randn((E,), generator=torch.Generator().manual_seed(3)).mul(0.05).to(DEV)
+    for b in (None, bias, bias.bfloat16().float()):
+        check(logits(45, E, dtype, seed=E + k), k, "sigmoid", bias=b, backward=False)
+        check(logits(45, E, dtype, seed=E + k, scale=3.0), k, "softmax", bias=b, n_group=2, topk_group=2, group_topn=2)
+
+
 @pytest.mark.parametrize("E,k", [(16, 4), (64, 6), (128, 8), (256, 8), (1024, 8)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_padding_off_experts_and_sequences(E, k, score):
