@@ -374,7 +374,7 @@ bool encode_bf16_2d_strided(CUtensorMap *map, const void *base, uint64_t inner, 
 // The trainable router (route.cu). Tokens are dealt to blocks of per_block
 // consecutive ones; a (block, sequence) pair has slot block + sequence, of
 // blocks + S - 1.
-constexpr int64_t kRouteMaxBlocks = 152 * 6;
+constexpr int64_t kRouteMaxBlocks = 152 * 3;
 struct RouteTiles {
     int64_t blocks, per_block;
 };

@@ -33,7 +33,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kSms = 152;
 constexpr int kMaxGrid = kSms * 4;
-constexpr int kNormPerSm = 3, kClipPerSm = 4, kAdamPerSm = 2;   // resident blocks
+constexpr int kNormPerSm = 3, kClipPerSm = 3, kAdamPerSm = 2;   // resident blocks
 constexpr int64_t kTurn = 256;              // units that turning to a tensor counts for
 constexpr int64_t kGrain = 256;             // tensors and runs start on a multiple of these: whole lines of memory
 constexpr int64_t kLeast = 1024, kMost = 8192; // units of a run
