@@ -15,11 +15,12 @@
 // and runs cut at any vector 5.8.
 //
 // All three are bound by HBM (of 6.78 TB/s for a plain copy, over 2.8e9 bf16 gradients: the
-// norm 0.78 ms, 7.2 TB/s; clipping's second pass 1.81 ms, 6.2 TB/s; AdamW over 5.5e8 bf16
+// norm 0.78 ms, 7.2 TB/s; clipping's second pass 1.79 ms, 6.3 TB/s; AdamW over 5.5e8 bf16
 // parameters with fp32 masters 2.38 ms, 6.5 TB/s). The norm reads each element once. Clipping reads and
 // writes each once more, from the last run backwards, so that it starts on what the
 // norm has left in L2, and does nothing where f is 1. AdamW takes f as it reads the
 // gradients, which saves that pass.
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -137,42 +138,46 @@ struct Sum {
         const double back = s < 1.0f ? 0x1p-96 : 0x1p96;
         return static_cast<double>(q) * (kType == MOE_NORM_2 ? back * back : back);
     }
-    __device__ __forceinline__ void join(double a, uint32_t t) {
-        acc += a;
-        top = max(top, t);
+    __device__ __forceinline__ void join(double v) {
+        if constexpr (kType == MOE_NORM_INF) top = max(top, __float_as_uint(static_cast<float>(v)));
+        else acc += v;
+    }
+    __device__ __forceinline__ double get() const {
+        return kType == MOE_NORM_INF ? static_cast<double>(__uint_as_float(top)) : acc;
     }
 };
 
+// The block's sum or maximum, in every thread. One warp adds, from shared memory: a 64-bit
+// addition takes a warp some 60 cycles, and eight warps that reduce each their own and then
+// all the same eight values wait 3 us for them.
 template <int kType>
-__device__ __forceinline__ double block_value(Sum<kType> s) {
-    __shared__ double part[kThreads / 32];
-    __shared__ uint32_t part_top[kThreads / 32];
-    if constexpr (kType == MOE_NORM_INF) {
-        s.top = __reduce_max_sync(0xffffffffu, s.top);
-    } else {
+__device__ __forceinline__ double block_value(const Sum<kType> &s) {
+    __shared__ double part[kThreads];
+    __shared__ double value;
+    __syncthreads();
+    part[threadIdx.x] = kType == MOE_NORM_INF ? static_cast<double>(__uint_as_float(s.top)) : s.acc;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        Sum<kType> t;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s.acc += __shfl_xor_sync(0xffffffffu, s.acc, off);
+        for (int i = 0; i < kThreads / 32; ++i) t.join(part[threadIdx.x + 32 * i]);
+        if constexpr (kType == MOE_NORM_INF) {
+            t.top = __reduce_max_sync(0xffffffffu, t.top);
+        } else {
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) t.acc += __shfl_xor_sync(0xffffffffu, t.acc, off);
+        }
+        if (threadIdx.x == 0) value = t.get();
     }
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) {
-        part[threadIdx.x >> 5] = s.acc;
-        part_top[threadIdx.x >> 5] = s.top;
-    }
-    __syncthreads();
-    Sum<kType> t;
-    for (int i = 0; i < kThreads / 32; ++i) t.join(part[i], part_top[i]);
-    if constexpr (kType == MOE_NORM_INF) return static_cast<double>(__uint_as_float(t.top));
-    return t.acc;
+    return value;
 }
 
 constexpr int kBatch = 8;                   // 16-byte loads of a thread in flight
 
+// A block's part of the norm: its runs.
 template <int kType, int N>
-__global__ void __launch_bounds__(kThreads, kNormPerSm)
-norm_kernel(const __grid_constant__ Table<N> tab, double *__restrict__ part, int32_t *__restrict__ step) {
-    griddep_wait();
-    if (step != nullptr && blockIdx.x == 0 && threadIdx.x == 0) ++*step;   // AdamW's, which comes next
-    Sum<kType> sum;
+__device__ __forceinline__ void sum_runs(const Table<N> &tab, Sum<kType> &sum) {
     for (int64_t u0 = blockIdx.x * tab.runs.size; u0 < tab.runs.total; u0 += gridDim.x * tab.runs.size) {
         const int64_t u1 = min(tab.runs.total, u0 + tab.runs.size);
         for (int i = find_tensor(tab.unit, tab.runs.n, u0); i < tab.runs.n && tab.unit[i] < u1; ++i) {
@@ -185,7 +190,7 @@ norm_kernel(const __grid_constant__ Table<N> tab, double *__restrict__ part, int
                 uint4 r[kBatch];
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j)
-                    r[j] = v + j * kThreads < hi ? __ldg(body + v + j * kThreads) : make_uint4(0u, 0u, 0u, 0u);
+                    r[j] = v + j * kThreads < hi ? __ldcg(body + v + j * kThreads) : make_uint4(0u, 0u, 0u, 0u);
                 if (dtype == MOE_DTYPE_F32) {
                     float x[4 * kBatch];
 #pragma unroll
@@ -219,23 +224,32 @@ norm_kernel(const __grid_constant__ Table<N> tab, double *__restrict__ part, int
             }
         }
     }
+}
+
+template <int kType, int N>
+__global__ void __launch_bounds__(kThreads, kNormPerSm)
+norm_kernel(const __grid_constant__ Table<N> tab, double *__restrict__ part, int32_t *__restrict__ step) {
+    griddep_wait();
+    if (step != nullptr && blockIdx.x == 0 && threadIdx.x == 0) ++*step;   // AdamW's, which comes next
+    Sum<kType> sum;
+    sum_runs<kType>(tab, sum);
     const double v = block_value<kType>(sum);
     if (threadIdx.x == 0) part[blockIdx.x] = v;
+}
+
+template <int kType>
+__device__ __forceinline__ float finish(double v) {
+    if (kType != MOE_NORM_2) return static_cast<float>(v);
+    // the root in 32 bits (1.5 roundings) wherever the sum is in its range
+    return v > 1e-30 && v < 1e38 ? sqrtf(static_cast<float>(v)) : static_cast<float>(sqrt(v));
 }
 
 // The norm from the blocks' values, in order; the same in every block that asks.
 template <int kType>
 __device__ __forceinline__ float total_norm(const double *__restrict__ part, int n) {
     Sum<kType> s;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const double v = __ldcg(part + i);
-        if constexpr (kType == MOE_NORM_INF) s.join(0.0, __float_as_uint(static_cast<float>(v)));
-        else s.join(v, 0u);
-    }
-    const double v = block_value<kType>(s);
-    if (kType != MOE_NORM_2) return static_cast<float>(v);
-    // the root in 32 bits (1.5 roundings) wherever the sum is in its range
-    return v > 1e-30 && v < 1e38 ? sqrtf(static_cast<float>(v)) : static_cast<float>(sqrt(v));
+    for (int i = threadIdx.x; i < n; i += kThreads) s.join(__ldcg(part + i));
+    return finish<kType>(block_value<kType>(s));
 }
 
 // max_norm / (norm + 1e-6), at most 1; NaN stays NaN
@@ -252,15 +266,9 @@ norm_total_kernel(const double *__restrict__ part, int n, float *__restrict__ no
     if (threadIdx.x == 0) *norm = v;
 }
 
-template <int kType, int N>
-__global__ void __launch_bounds__(kThreads, kClipPerSm)
-clip_kernel(const __grid_constant__ Table<N> tab, const double *__restrict__ part, int n_part, float max_norm,
-            float *__restrict__ norm) {
-    griddep_wait();
-    const float total = total_norm<kType>(part, n_part);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
-    const float f = clip_factor(total, max_norm);
-    if (f == 1.0f) return;                  // x * 1 = x
+// A block's part of the scaling: its runs, from the last backwards.
+template <int N>
+__device__ __forceinline__ void scale_runs(const Table<N> &tab, float f) {
     const int64_t runs = (tab.runs.total + tab.runs.size - 1) / tab.runs.size;
     for (int64_t c = runs - 1 - static_cast<int64_t>(blockIdx.x); c >= 0; c -= gridDim.x) {
         const int64_t u0 = c * tab.runs.size, u1 = min(tab.runs.total, u0 + tab.runs.size);
@@ -299,6 +307,53 @@ clip_kernel(const __grid_constant__ Table<N> tab, const double *__restrict__ par
             }
             if (tab.unit[i] <= u0) break;
         }
+    }
+}
+
+template <int kType, int N>
+__global__ void __launch_bounds__(kThreads, kClipPerSm)
+clip_kernel(const __grid_constant__ Table<N> tab, const double *__restrict__ part, int n_part, float max_norm,
+            float *__restrict__ norm) {
+    griddep_wait();
+    const float total = total_norm<kType>(part, n_part);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
+    const float f = clip_factor(total, max_norm);
+    if (f == 1.0f) return;                  // x * 1 = x
+    scale_runs(tab, f);
+}
+
+// A short list of no more than kSmall units in one launch: a cluster of eight blocks, which
+// exchange their sums through shared memory. Two launches wait for each other some 3 us, and
+// cost the host as much again: 0.2 M elements in three tensors take 14.8 us a call as two
+// launches and 11.0 as one, although eight SMs need 9 us for what 50 do in 8.
+constexpr int kCluster = 8;
+constexpr int64_t kSmall = 32768;
+
+template <int kType, bool kClip>
+__global__ void __launch_bounds__(kThreads)
+small_kernel(const __grid_constant__ Table<kShort> tab, float max_norm, float *__restrict__ norm) {
+    griddep_wait();
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    __shared__ double mine;
+    Sum<kType> sum;
+    sum_runs<kType>(tab, sum);
+    const double v = block_value<kType>(sum);
+    if (threadIdx.x == 0) mine = v;
+    cluster.sync();
+    __shared__ float norm_shared;
+    if (threadIdx.x == 0) {
+        Sum<kType> all;
+#pragma unroll
+        for (int i = 0; i < kCluster; ++i) all.join(*cluster.map_shared_rank(&mine, i));
+        norm_shared = finish<kType>(all.get());
+    }
+    cluster.sync();                         // the sums are read while their blocks last
+    const float total = norm_shared;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
+    if constexpr (kClip) {
+        const float f = clip_factor(total, max_norm);
+        if (f != 1.0f) scale_runs(tab, f);
     }
 }
 
@@ -488,6 +543,23 @@ int make_runs(Runs &r, int n, int64_t total, int resident) {
     return static_cast<int>(blocks);
 }
 
+// The next at most N tensors of a list that are not empty, from `at` on; returns their units.
+template <int N>
+int64_t fill_table(const TensorList &l, int &at, Table<N> &t, int &n) {
+    int64_t total = 0;
+    n = 0;
+    for (; at < l.n && n < N; ++at) {
+        if (l.numel[at] == 0) continue;
+        t.ptr[n] = const_cast<void *>(l.ptr[at]);
+        t.numel[n] = l.numel[at];
+        t.dtype[n] = static_cast<uint8_t>(l.dtype[at]);
+        t.unit[n] = total;
+        total += grains(span_of(l.ptr[at], l.numel[at], size_of(l.dtype[at])).vecs + 1 + kTurn);
+        ++n;
+    }
+    return total;
+}
+
 // The list as tables of at most N tensors: f(table, blocks) for each.
 template <int N, typename F>
 cudaError_t for_tables(const TensorList &l, int most, F f) {
@@ -496,21 +568,40 @@ cudaError_t for_tables(const TensorList &l, int most, F f) {
     do {
         Table<N> t;
         int n = 0;
-        int64_t total = 0;
-        for (; at < l.n && n < N; ++at) {
-            if (l.numel[at] == 0) continue;
-            t.ptr[n] = const_cast<void *>(l.ptr[at]);
-            t.numel[n] = l.numel[at];
-            t.dtype[n] = static_cast<uint8_t>(l.dtype[at]);
-            t.unit[n] = total;
-            total += grains(span_of(l.ptr[at], l.numel[at], size_of(l.dtype[at])).vecs + 1 + kTurn);
-            ++n;
-        }
+        const int64_t total = fill_table(l, at, t, n);
         const int blocks = make_runs(t.runs, n, total, most);
         const cudaError_t e = f(t, blocks);
         if (e != cudaSuccess) return e;
     } while (at < l.n);
     return cudaSuccess;
+}
+
+// A short and small list in one launch; false: it is not one.
+template <int kType, bool kClip>
+bool launch_small(const TensorList &l, float max_norm, float *norm, cudaStream_t st, cudaError_t *err) {
+    if (l.n > kShort) return false;
+    Table<kShort> t;
+    int at = 0, n = 0;
+    const int64_t total = fill_table(l, at, t, n);
+    if (total > kSmall) return false;
+    t.runs.n = n;
+    t.runs.total = total;
+    t.runs.size = total > 0 ? grains((total + kCluster - 1) / kCluster) : kGrain;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    *err = cudaLaunchKernelEx(&cfg, small_kernel<kType, kClip>, t, max_norm, norm);
+    note_launches(1);
+    return true;
 }
 
 double *partials(void *ws) { return static_cast<double *>(ws); }
@@ -611,7 +702,9 @@ cudaError_t launch_grad_norm(const TensorList &grads, int norm_type, float *norm
     return with_norm_type(norm_type, [&](auto type) {
         constexpr int kType = decltype(type)::value;
         int n_part = 0;
-        cudaError_t e = norm_typed<kType>(grads, ws, nullptr, &n_part, st);
+        cudaError_t e;
+        if (launch_small<kType, false>(grads, 0.0f, norm, st, &e)) return e;
+        e = norm_typed<kType>(grads, ws, nullptr, &n_part, st);
         if (e != cudaSuccess) return e;
         e = launch_dep(norm_total_kernel<kType>, dim3(1), dim3(kThreads), 0, st,
                        static_cast<const double *>(partials(ws)), n_part, norm);
@@ -625,7 +718,9 @@ cudaError_t launch_clip_grads(const TensorList &grads, int norm_type, float max_
     return with_norm_type(norm_type, [&](auto type) {
         constexpr int kType = decltype(type)::value;
         int n_part = 0;
-        const cudaError_t e = norm_typed<kType>(grads, ws, nullptr, &n_part, st);
+        cudaError_t e;
+        if (launch_small<kType, true>(grads, max_norm, norm, st, &e)) return e;
+        e = norm_typed<kType>(grads, ws, nullptr, &n_part, st);
         if (e != cudaSuccess) return e;
         if (grads.n <= kShort) return clip_parts<kType, kShort>(grads, max_norm, norm, ws, n_part, st);
         if (grads.n <= kMiddle) return clip_parts<kType, kMiddle>(grads, max_norm, norm, ws, n_part, st);
