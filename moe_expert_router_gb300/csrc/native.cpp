@@ -165,6 +165,7 @@ PyObject *bias_update(PyObject *const *a) {
 // memory, where that is not null; with `optional` or None (address 0); not overlapping,
 // where they are written.
 struct List {
+    std::vector<const at::Tensor *> tensor;   // borrowed from the caller's list
     std::vector<void *> ptr;
     std::vector<int64_t> numel;
     std::vector<int32_t> type;
@@ -175,14 +176,17 @@ thread_local std::vector<std::pair<uint64_t, uint64_t>> t_range;
 
 bool is_list(PyObject *o) { return PyList_Check(o) || PyTuple_Check(o); }
 
-const List &list_of(List &l, PyObject *o, const char *name, int device, int dtype, PyObject *like, bool optional, bool written) {
+const List &list_of(List &l, PyObject *o, const char *name, int device, int dtype, const List *like, bool optional,
+                    bool written) {
     if (!is_list(o)) refuse(PyExc_TypeError, "%s must be a list of tensors", name);
     const Py_ssize_t n = PySequence_Fast_GET_SIZE(o);
-    if (like != nullptr && PySequence_Fast_GET_SIZE(like) != n)
+    if (like != nullptr && static_cast<Py_ssize_t>(like->tensor.size()) != n)
         refuse(PyExc_ValueError, "%s must be as many as the parameters", name);
+    l.tensor.assign(n, nullptr);
     l.ptr.assign(n, nullptr);
     l.numel.assign(n, 0);
     l.type.assign(n, MOE_DTYPE_F32);
+    const at::Device on(at::kCUDA, static_cast<at::DeviceIndex>(device));
     std::vector<std::pair<uint64_t, uint64_t>> &range = t_range;
     range.clear();
     bool sorted = true;
@@ -190,18 +194,20 @@ const List &list_of(List &l, PyObject *o, const char *name, int device, int dtyp
         PyObject *item = PySequence_Fast_GET_ITEM(o, i);
         if (optional && item == Py_None) continue;
         const at::Tensor &t = tensor(item, name);
-        if (!t.is_cuda() || t.get_device() != device) refuse(PyExc_ValueError, "%s must be CUDA tensors on one device", name);
+        if (t.device() != on) refuse(PyExc_ValueError, "%s must be CUDA tensors on one device", name);
         const int code = code_of(t.scalar_type());
         if (code < 0) refuse(PyExc_TypeError, "%s must be float32, bfloat16 or float16", name);
         if (dtype >= 0 && code != dtype) refuse(PyExc_TypeError, "%s must be %s", name, kNames[dtype]);
-        if (t.layout() != at::kStrided || !(t.is_contiguous() || t.is_non_overlapping_and_dense()))
-            refuse(PyExc_ValueError, "%s must be dense", name);
+        if (t.layout() != at::kStrided) refuse(PyExc_ValueError, "%s must be dense", name);
+        const bool plain = t.is_contiguous();
+        if (!plain && !t.is_non_overlapping_and_dense()) refuse(PyExc_ValueError, "%s must be dense", name);
         if (like != nullptr) {
-            const at::Tensor &p = tensor(PySequence_Fast_GET_ITEM(like, i), "params");
+            const at::Tensor &p = *like->tensor[i];
             if (t.sizes() != p.sizes()) refuse(PyExc_ValueError, "%s must have the parameters' shapes", name);
-            if (!(t.is_contiguous() && p.is_contiguous()) && t.strides() != p.strides())
+            if (!(plain && p.is_contiguous()) && t.strides() != p.strides())
                 refuse(PyExc_ValueError, "%s must have the parameters' order in memory", name);
         }
+        l.tensor[i] = &t;
         l.ptr[i] = t.data_ptr();
         l.numel[i] = t.numel();
         l.type[i] = code;
@@ -273,11 +279,11 @@ PyObject *clip_grads(PyObject *const *a) {
 PyObject *adamw(PyObject *const *a) {
     const int device = device_of(a[6], "lr");
     const List &p = list_of(t_lists[0], a[0], "params", device, -1, nullptr, false, true);
-    const List &g = list_of(t_lists[1], a[1], "grads", device, -1, a[0], false, false);
-    const List &m = list_of(t_lists[2], a[2], "exp_avg", device, MOE_DTYPE_F32, a[0], false, true);
-    const List &v = list_of(t_lists[3], a[3], "exp_avg_sq", device, MOE_DTYPE_F32, a[0], false, true);
+    const List &g = list_of(t_lists[1], a[1], "grads", device, -1, &p, false, false);
+    const List &m = list_of(t_lists[2], a[2], "exp_avg", device, MOE_DTYPE_F32, &p, false, true);
+    const List &v = list_of(t_lists[3], a[3], "exp_avg_sq", device, MOE_DTYPE_F32, &p, false, true);
     const List &x = t_lists[4];
-    if (a[4] != Py_None) list_of(t_lists[4], a[4], "masters", device, MOE_DTYPE_F32, a[0], true, true);
+    if (a[4] != Py_None) list_of(t_lists[4], a[4], "masters", device, MOE_DTYPE_F32, &p, true, true);
     const Scratch ws = scratch(a[9]);
     auto floats = [](const List &l) { return reinterpret_cast<float *const *>(l.ptr.data()); };
     return PyLong_FromLong(g_adamw(p.ptr.data(), p.type.data(), g.ptr.data(), g.type.data(), floats(m), floats(v),
