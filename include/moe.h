@@ -294,7 +294,8 @@ moe_status_t moe_route_workspace_size(const moe_route_shape_t *shape, size_t *by
  *   expert e is off for token t when l[t,e] = -inf: score 0, never chosen
  *   token t is live when token_mask[t] != 0 and not all its experts are off
  *   s      = softmax(l[t,:]) or sigmoid(l[t,:])
- *   key    = l without sel_bias, else s + sel_bias
+ *   key    = l without sel_bias, else s + sel_bias (a sel_bias of -inf keeps an
+ *            expert from being chosen, and out of its group's sum)
  *   groups = (n_group > 1) keep the topk_group groups with the largest sum of
  *            their group_topn best s + sel_bias
  *   topk_idx = the k experts of the kept groups with the largest key, best
@@ -312,7 +313,8 @@ moe_status_t moe_route_workspace_size(const moe_route_shape_t *shape, size_t *by
  * (with sigmoid scores the shares are normalised, so that lowering every score
  * does not lower the balance term). The order of experts, and of groups, whose
  * keys are nearer than fp32 resolves is decided in fp64. A NaN logit of a live
- * token is never chosen; with softmax it makes that token's weights NaN.
+ * token is never chosen and makes the losses NaN; with softmax it makes that
+ * token's weights NaN too, or, with sel_bias, leaves its slots over.
  * Values in rows whose mask is 0 reach no output.
  *
  * logits [T,E] with rows ld apart, dtype-aligned; sel_bias fp32 [E] or NULL;

@@ -436,8 +436,9 @@ __device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int 
         if (e0 + at<V>(i) >= p.E || !(((sure | near) >> group_of(e0 + at<V>(i))) & 1u)) continue;
         const float l = load_one(p.logits, p.dtype, row + e0 + at<V>(i));
         if (l == -INFINITY) continue;
-        open |= 1u << i;
         sel[i] = score(softmax, l) + (p.sel_bias != nullptr ? static_cast<double>(__ldg(p.sel_bias + e0 + at<V>(i))) : 0.0);
+        if (!(sel[i] > -INFINITY)) continue;
+        open |= 1u << i;
         key[i] = order_key64(sel[i]);
     }
     if (near != 0) {
@@ -668,21 +669,26 @@ route_kernel(const RouteLaunch p) {
     float *own_row = buf + row * G * V;
     // a lane's biases stay in registers where there are few
     constexpr int kHeld = V <= 8 ? V : 1;
-    float held[kHeld], bias_max = 0.0f;
+    float held[kHeld], bias_max = 0.0f;              // the largest that is finite
+    bool nonzero = false;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const float b = biased && e0 + at<V>(i) < p.E ? __ldg(p.sel_bias + e0 + at<V>(i)) : 0.0f;
         if (V <= 8) held[i % kHeld] = b;
-        bias_max = fmaxf(bias_max, fabsf(b));
+        nonzero |= !(b == 0.0f);
+        if (fabsf(b) < INFINITY) bias_max = fmaxf(bias_max, fabsf(b));
     }
     auto bias = [&](int i) {
         if (V <= 8) return held[i % kHeld];
         return biased && e0 + at<V>(i) < p.E ? __ldg(p.sel_bias + e0 + at<V>(i)) : 0.0f;
     };
-    if (biased) bias_max = lanes_max<G>(gmask, bias_max);
+    if (biased) {
+        bias_max = lanes_max<G>(gmask, bias_max);
+        nonzero = (__ballot_sync(0xffffffffu, nonzero) & gmask) != 0;
+    }
     // with no bias, or none but zeros, the order is the logits' own, without a rounding; so is
     // that of groups known by their best expert
-    const bool by_score = biased && !(bias_max == 0.0f);
+    const bool by_score = biased && nonzero;
     const bool best_only = !by_score && p.group_topn == 1;
     int seq = 0;
     float acc[kShared ? 1 : V];
@@ -1015,7 +1021,7 @@ route_kernel(const RouteLaunch p) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         const float v = own_row[e0 + at<V>(i)] + bias(i);
-                        if (l[i] != -INFINITY && v >= floor && (!grouped || (kept >> ((e0 + at<V>(i)) / gs)) & 1u)) cand |= 1u << i;
+                        if (l[i] != -INFINITY && v > -INFINITY && v >= floor && (!grouped || (kept >> ((e0 + at<V>(i)) / gs)) & 1u)) cand |= 1u << i;
                     }
                     n = lanes_reduce<G>(gmask, __popc(cand), [](int a, int b) { return a + b; });
                 }

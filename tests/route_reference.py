@@ -39,6 +39,7 @@ def route(l, k, score="softmax", normalize=True, scale=1.0, n_group=1, topk_grou
                 s[t, on] = 1.0 / (1.0 + np.exp(-l[t, on]))
             sel = s[t] + (0.0 if bias is None else np.asarray(bias, np.float64))
             rank = l[t] if bias is None else sel
+            on = [e for e in on if sel[e] > -np.inf]     # a bias of -inf keeps an expert from being chosen
             allowed = set(on)
             if n_group > 1:
                 size = E // n_group

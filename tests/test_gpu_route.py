@@ -176,6 +176,23 @@ def test_saturated_scores_under_a_bias(E, many):
         check(l, 3, "sigmoid", n_group=4, topk_group=3, group_topn=2, backward=False)
 
 
+@pytest.mark.parametrize("E", [8, 64, 256, 512])
+@pytest.mark.parametrize("others", [0.0, 0.1])
+def test_a_bias_of_minus_infinity_keeps_an_expert_out(E, others):
+    l = logits(40, E, seed=E, scale=2.0)
+    l[7] = 0.0                                           # ties
+    bias = torch.full((E,), others, device=DEV)
+    bias[1::2] = -float("inf")
+    for kw in (dict(), dict(n_group=4, topk_group=2, group_topn=1), dict(n_group=4, topk_group=3, group_topn=2)):
+        k = 4 if E > 8 else 3                            # fewer than k are left at E = 8 with groups
+        for score in ("softmax", "sigmoid"):
+            g, _ = check(l, k, score, bias=bias, **kw)
+            assert not (g["idx"][g["idx"] >= 0] % 2 == 1).any()      # -1: left over
+    bias[:] = -float("inf")
+    g, _ = check(l, 3, "sigmoid", bias=bias)
+    assert (g["idx"] == -1).all() and (g["w"] == 0).all()
+
+
 @pytest.mark.parametrize("E,k", [(40, 20), (64, 31), (128, 17), (256, 24), (256, 32), (600, 30), (1024, 25)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_many_chosen_experts(E, k, dtype):
@@ -237,6 +254,21 @@ def test_nan_and_infinity_of_a_live_token():
     l[1, 7] = float("inf")
     s = call(l, 4, "sigmoid")
     assert s["idx"][1, 0] == 7 and torch.isfinite(s["w"]).all()
+
+
+def test_nan_under_a_bias():
+    l = torch.randn((3, 300), generator=torch.Generator().manual_seed(0)).to(DEV)
+    bias = torch.full((300,), 0.25, device=DEV)
+    bias[0] = 0.5
+    clean = {score: call(l, 4, score, bias=bias) for score in ("softmax", "sigmoid")}
+    l[1, 7] = float("nan")
+    for score, c in clean.items():
+        g = call(l, 4, score, bias=bias)
+        assert torch.equal(g["idx"][[0, 2]], c["idx"][[0, 2]]) and torch.isnan(g["losses"]).all()
+        if score == "softmax":                           # every key of the row is NaN
+            assert (g["idx"][1] == -1).all() and (g["w"][1] == 0).all()
+        else:
+            assert 7 not in g["idx"][1].tolist() and (g["idx"][1] >= 0).all() and torch.isfinite(g["w"]).all()
 
 
 def test_top1_normalised_weight_has_no_gradient():
