@@ -294,7 +294,8 @@ moe_status_t moe_route_workspace_size(const moe_route_shape_t *shape, size_t *by
  *   expert e is off for token t when l[t,e] = -inf: score 0, never chosen
  *   token t is live when token_mask[t] != 0 and not all its experts are off
  *   s      = softmax(l[t,:]) or sigmoid(l[t,:])
- *   key    = l without sel_bias, else s + sel_bias (a sel_bias of -inf keeps an
+ *   key    = l without sel_bias (or where it is 0 for every expert), else
+ *            s + sel_bias (a sel_bias of -inf keeps an
  *            expert from being chosen, and out of its group's sum)
  *   groups = (n_group > 1) keep the topk_group groups with the largest sum of
  *            their group_topn best s + sel_bias

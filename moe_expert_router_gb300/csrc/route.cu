@@ -421,7 +421,7 @@ __device__ __noinline__ unsigned resolve_groups(const RouteLaunch &p, int64_t ro
 // the best stay as far as topk_group allows, then k rounds.
 template <int G, int V>
 __device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int sub, unsigned gmask, unsigned sure,
-                                         unsigned near, int *out_idx, float *out_s, double *group) {
+                                         unsigned near, bool by_score, int *out_idx, float *out_s, double *group) {
     const int e0 = first_expert<V>(sub);
     const WideScore score = wide_score<G, V>(p, row, e0, gmask);
     const bool softmax = p.score_fn == MOE_SCORE_SOFTMAX;
@@ -488,7 +488,7 @@ __device__ __noinline__ void select_wide(const RouteLaunch &p, int64_t row, int 
         }
         __syncwarp(gmask);
     }
-    if (p.sel_bias == nullptr)                       // the score's order is the logit's
+    if (!by_score)                                   // the score's order is the logit's
 #pragma unroll (V <= 8 ? V : 1)
         for (int i = 0; i < V; ++i)
             if ((open >> i) & 1u) key[i] = order_key64(load_one(p.logits, p.dtype, row + e0 + at<V>(i)));
@@ -1028,7 +1028,7 @@ route_kernel(const RouteLaunch p) {
                 if (n <= G)
                     select_near<G, V>(p, lrow, sub, gmask, cand, slots.idx[row], slots.s[row]);
                 else
-                    select_wide<G, V>(p, lrow, sub, gmask, kept & ~near_groups, near_groups, slots.idx[row], slots.s[row],
+                    select_wide<G, V>(p, lrow, sub, gmask, kept & ~near_groups, near_groups, by_score, slots.idx[row], slots.s[row],
                                       slots.group[row]);
 #pragma unroll
                 for (int q = 0; q < kOwn; ++q) {
