@@ -331,11 +331,13 @@ __device__ __noinline__ void select_near(const RouteLaunch &p, int64_t row, int 
 // ones: the experts that can be among a near group's best (no more than the error `err1` below
 // its last) are scored in 64 bits, one a lane. sel_row: the token's selection scores, -inf where
 // off. Returns the near groups that stay, `room` of them; ~0 where there are more such experts
-// than lanes. Without a bias softmax's sums need no normaliser.
+// than lanes. Without a bias softmax's sums need no normaliser; they are taken about `top`, the
+// row's largest logit, as everywhere else: a finite logit may be any distance below another (a
+// mask of -1e4), and about any but the largest its exponential leaves fp64.
 template <int G, int V>
 __device__ __noinline__ unsigned resolve_groups(const RouteLaunch &p, int64_t row, const float *sel_row, int sub,
-                                                unsigned gmask, unsigned near, int room, float err1, bool biased, int *list,
-                                                double *group) {
+                                                unsigned gmask, unsigned near, int room, float err1, bool biased, float top,
+                                                int *list, double *group) {
     const int lane = threadIdx.x & 31, e0 = first_expert<V>(sub);
     const int gs = p.E / p.n_group;
     const bool softmax = p.score_fn == MOE_SCORE_SOFTMAX;
@@ -377,8 +379,8 @@ __device__ __noinline__ unsigned resolve_groups(const RouteLaunch &p, int64_t ro
     WideScore score = {0.0, 1.0};
     if (softmax && biased) {
         score = wide_score<G, V>(p, row, e0, gmask);
-    } else if (softmax) {                            // about any common factor: the row's first listed expert
-        score.top = load_one(p.logits, p.dtype, row + list[0]);
+    } else if (softmax) {
+        score.top = top;
     }
     double v = 0.0;
     uint64_t key = 0;
@@ -818,7 +820,7 @@ route_kernel(const RouteLaunch p) {
                     const unsigned sure = kept & ~near_groups;
                     const unsigned stay = resolve_groups<G, V>(p, lrow, own_row, sub, gmask, near_groups,
                                                                p.topk_group - __popc(sure),
-                                                               rel * s_max + 2.0f * kUlp * (s_max + bias_max), by_score,
+                                                               rel * s_max + 2.0f * kUlp * (s_max + bias_max), by_score, top,
                                                                slots.idx[row], slots.group[row]);
                     if (stay != ~0u) {
                         kept = sure | stay;

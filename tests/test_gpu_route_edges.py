@@ -1,0 +1,53 @@
+"""The trainable router at the edges of its definition: large finite masks among groups,
+gradients that arrive at slots left over, NaN beside groups, near-ties behind ties, saturated
+and vanishing scores, sums over many tokens. Against the formulas in 64 bits; tolerances as
+in test_gpu_route.py where none is given."""
+import numpy as np
+import pytest
+import torch
+
+import route_reference as R
+from moe_expert_router_gb300 import binding as B
+from test_gpu_route import DEV, call, check, logits
+
+pytestmark = pytest.mark.gpu
+
+LOWEST = torch.finfo(torch.float32).min
+WIDTHS = [8, 24, 64, 128, 256, 512, 1024]                # every layout of lanes
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    B.load()
+
+
+@pytest.mark.parametrize("row,best", [
+    ([50.0, 0.0, -1e4, 3.0, 20.0, 0.0, -1e4, -1e4], [0, 4]),
+    ([0.0, 0.0, -1000.0, -30.0, -20.0, -20.0, -40.0, -40.0], [0, 1]),
+    ([50.0, -1e4, LOWEST, 3.0, 20.0, LOWEST, LOWEST, LOWEST], [0, 4])])
+def test_low_finite_logits_beside_a_group_at_the_border(row, best):
+    l = torch.tensor([row], device=DEV)
+    g, _ = check(l, 2, "softmax", n_group=4, topk_group=2, group_topn=2, backward=False)
+    assert g["idx"][0].tolist() == best
+
+
+@pytest.mark.parametrize("E,n_group", [(8, 4), (24, 4), (64, 16), (128, 8), (128, 32), (256, 16), (256, 32), (512, 32),
+                                       (1024, 32)])
+@pytest.mark.parametrize("mask", [-1e3, -1e4, LOWEST])
+def test_groups_among_low_finite_logits(E, n_group, mask):
+    """One expert far above the others, so that the sums of all other groups are within the error
+    of 32-bit ones, and experts masked by a large finite number."""
+    size = E // n_group
+    rng = np.random.default_rng(E + n_group)
+    l = rng.uniform(-30.0, 20.0, size=(60, E))
+    l[rng.random((60, E)) < rng.choice([0.2, 0.6, 0.9], size=(60, 1))] = mask
+    l[np.arange(60), rng.integers(0, E, 60)] = 50.0
+    l[3, :size] = mask                                   # a group with nothing else
+    l[5, 1:] = mask
+    l = torch.tensor(l, dtype=torch.float32, device=DEV)
+    for topn in (2, 3):
+        if topn <= size:
+            for stay in {2, n_group // 2}:
+                check(l, min(6, stay * size), "softmax", n_group=n_group, topk_group=stay, group_topn=topn, backward=False)
