@@ -337,7 +337,8 @@ moe_status_t moe_route(const void *logits, const float *sel_bias, const uint8_t 
  * Gradient of moe_route's topk_w and losses with respect to the logits:
  * dlogits [T,E], dense, of the logits' type, fully written (0 for experts that
  * are off and tokens that are not live). The selection and the counts carry no
- * gradient. dtopk_w fp32 [T,k]; dlosses fp32 [2] on the device, or NULL where
+ * gradient. dtopk_w fp32 [T,k] (whatever it holds at slots left over reaches
+ * nothing); dlosses fp32 [2] on the device, or NULL where
  * the losses are not used (counts, seq_tokens and seq_offsets are then not
  * read). topk_idx, counts and seq_tokens are moe_route's.
  */

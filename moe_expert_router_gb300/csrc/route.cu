@@ -1393,6 +1393,7 @@ route_backward_kernel(const RouteBackwardLaunch p) {
                 if (q * G >= p.k) continue;
                 if (ce[q] >= p.E) ce[q] = -1;
                 if (ce[q] >= 0) cs[q] = s_row[ce[q]];
+                else cw[q] = 0.0f;                   // the weight of a slot left over is a constant: whatever its gradient
                 chosen += cs[q];
             }
             if (p.normalize) {

@@ -51,3 +51,30 @@ def test_groups_among_low_finite_logits(E, n_group, mask):
         if topn <= size:
             for stay in {2, n_group // 2}:
                 check(l, min(6, stay * size), "softmax", n_group=n_group, topk_group=stay, group_topn=topn, backward=False)
+
+
+@pytest.mark.parametrize("E", WIDTHS)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_gradients_at_slots_left_over_reach_nothing(E, score, normalize):
+    """topk_w is the constant 0 there: infinity or NaN in its gradient (that of w log w, for one)
+    leaves the row as it is."""
+    rng = np.random.default_rng(E)
+    T, k = 41, 6
+    l = rng.normal(size=(T, E))
+    for t in range(T):
+        l[t, rng.permutation(E)[:E - 1 - t % k]] = -np.inf
+    l[7] = -np.inf
+    l = torch.tensor(l, dtype=torch.float32, device=DEV)
+    dw = rng.normal(size=(T, k)).astype(np.float32)
+    dlosses = torch.tensor([2.0, 0.5], device=DEV)
+    clean = call(l, k, score, normalize, 1.5, dw=torch.tensor(dw, device=DEV), dlosses=dlosses)
+    left = clean["idx"] < 0
+    assert left.any() and torch.isfinite(clean["dl"]).all()
+    for bad in (float("inf"), -float("inf"), float("nan")):
+        d = torch.where(left, torch.tensor(bad, device=DEV), torch.tensor(dw, device=DEV))
+        for losses, want in ((dlosses, clean), (None, None)):
+            got = call(l, k, score, normalize, 1.5, dw=d, dlosses=losses)["dl"]
+            if want is None:
+                want = call(l, k, score, normalize, 1.5, dw=torch.tensor(dw, device=DEV))
+            assert torch.equal(got, want["dl"])
