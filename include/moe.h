@@ -315,7 +315,8 @@ moe_status_t moe_route_workspace_size(const moe_route_shape_t *shape, size_t *by
  * does not lower the balance term). The order of experts, and of groups, whose
  * keys are nearer than fp32 resolves is decided in fp64 (scores below its range
  * are 0 there, and tie). A NaN logit of a live
- * token is never chosen and makes the losses NaN; with softmax it makes that
+ * token is never chosen, counts for no group, and makes the losses NaN (a NaN
+ * in sel_bias keeps its expert out like one of -inf); with softmax it makes that
  * token's weights NaN too, or, with sel_bias, leaves its slots over.
  * Values in rows whose mask is 0 reach no output.
  *

@@ -581,7 +581,7 @@ __device__ __forceinline__ void search_groups(const RouteLaunch &p, const float 
     }
 }
 
-// The groups of one token that stay, as bits; v: the lane's selection scores (-inf: off).
+// The groups of one token that stay, as bits; v: the lane's selection scores (-inf: off; no NaN).
 // Where a group is a power of two of whole lanes (`group_lanes`, from the host) and is known
 // by its best one or two, those are found in registers. Else a group is searched in `sel_row`
 // by a power of two of lanes, each taking every so many of its experts. `near`: the groups
@@ -808,7 +808,10 @@ route_kernel(const RouteLaunch p) {
             if (grouped) {
                 float v[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[i] = best_only || l[i] == -INFINITY ? l[i] : s[i] + bias(i);
+                for (int i = 0; i < V; ++i) {
+                    v[i] = best_only || l[i] == -INFINITY ? l[i] : s[i] + bias(i);
+                    v[i] = fmaxf(v[i], -INFINITY);   // NaN is as good as off: min and max would take the other value twice
+                }
                 const float n = static_cast<float>(p.group_topn);
                 kept = kept_groups<G, V>(p, v, own_row, reinterpret_cast<float *>(slots.group[row]), sub, gmask,
                                          best_only ? -1.0f : 2.0f * n * (rel * s_max + kUlp * (2.0f + n) * (s_max + bias_max)),

@@ -78,3 +78,30 @@ def test_gradients_at_slots_left_over_reach_nothing(E, score, normalize):
             if want is None:
                 want = call(l, k, score, normalize, 1.5, dw=torch.tensor(dw, device=DEV))
             assert torch.equal(got, want["dl"])
+
+
+@pytest.mark.parametrize("E,n_group", [(16, 2), (24, 4), (64, 8), (64, 2), (128, 4), (160, 8), (256, 8), (512, 4), (1024, 16)])
+@pytest.mark.parametrize("topn", [2, 3])
+@pytest.mark.parametrize("where", ["logit", "logit, a bias", "bias"])
+def test_nan_takes_no_part_in_a_groups_sum(E, n_group, topn, where):
+    """Group 0: a good expert, a NaN and poor ones; another group: two good ones a little lower."""
+    size = E // n_group
+    nan_at = {"logit": [1], "logit, a bias": [1, size - 1], "bias": [1]}[where]
+    for other in (1, n_group - 1):
+        l = torch.full((9, E), -5.0, device=DEV)
+        l[:, 0] = 2.0
+        l[:, other * size] = 1.5
+        l[:, other * size + 1] = 1.375
+        clean = l.clone()
+        bias = None if where == "logit" else torch.full((E,), 0.25, device=DEV)
+        if where == "bias":
+            bias[1] = float("nan")
+        else:
+            l[4:, nan_at] = float("nan")
+        g = call(l, 2, "sigmoid", n_group=n_group, topk_group=1, group_topn=topn, bias=bias)
+        assert (g["idx"] == torch.tensor([other * size, other * size + 1], device=DEV)).all()
+        # a NaN is as good as an expert that is off
+        off = torch.where(torch.isnan(l), -float("inf"), clean)
+        o = call(off, 2, "sigmoid", n_group=n_group, topk_group=1, group_topn=topn,
+                 bias=None if bias is None else torch.where(torch.isnan(bias), -float("inf"), bias))
+        assert torch.equal(o["idx"], g["idx"]) and torch.equal(o["w"], g["w"])
