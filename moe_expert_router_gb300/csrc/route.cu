@@ -22,11 +22,12 @@
 //   else: k rounds of a maximum, a ballot, and the winning lane looking up its next best.
 //
 // Keys that pass through exp carry an error of some 1e-7, and two experts nearer than
-// that would be chosen by rounding. Neighbouring chosen keys, and the group sums at the
-// border, are compared with the bound of that error. The rare token below it (one in
-// some thousand) is decided in 64 bits, on the experts that matter, one a lane: the
-// 64-bit pipe takes some 60 cycles for an instruction, so that scoring every expert there
-// cost such a token 20 us.
+// that would be chosen by rounding. Neighbouring chosen keys, the last of them and whatever
+// stands behind it, and the group sums at the border, are compared with the bound of that
+// error; experts of the same logit and bias are a tie, whatever the error. The rare token
+// below it (one in some thousand) is decided in 64 bits, on the experts that matter, one a
+// lane: the 64-bit pipe takes some 60 cycles for an instruction, so that scoring every expert
+// there cost such a token 20 us.
 //
 // Bound by instructions, not by memory: 131072 tokens of 128 bf16 experts (34 MB, 5 us of
 // HBM) take 58 us at 340 warp instructions a token and 0.62 issued a cycle, with 24 warps
@@ -1000,17 +1001,36 @@ route_kernel(const RouteLaunch p) {
 #pragma unroll
             for (int q = 0; q < kOwn; ++q) sv[q] = ev[q] >= 0 ? own_row[ev[q]] : 0.0f;
             if (by_score) {
+                bool tied = false;                   // the last chosen and the first not chosen are a tie
 #pragma unroll
                 for (int q = 0; q < kOwn; ++q) {
                     // this slot's key against the next one's (the last one's: the first not chosen)
                     const int b = ev[q] >= 0 ? slots.idx[row][sub + q * G + 1] : -1;
                     if (b < 0) continue;
                     const float x = key_value(slots.key[row][sub + q * G]), y = key_value(slots.key[row][sub + q * G + 1]);
-                    if (x - y <= rel * (sv[q] + own_row[b]) + kUlp * (2.0f * (fabsf(x) + fabsf(y)) + s_max) &&
+                    // beyond the last there may be others whose score, and so its error, is larger
+                    const bool border = sub + q * G == p.k - 1;
+                    const float both = border ? 2.0f * s_max : sv[q] + own_row[b];
+                    if (x - y <= rel * both + kUlp * (2.0f * (fabsf(x) + fabsf(y)) + s_max)) {
                         // not near: a tie of the same logit and bias
-                        !(load_one(p.logits, p.dtype, lrow + ev[q]) == load_one(p.logits, p.dtype, lrow + b) &&
-                          __ldg(p.sel_bias + ev[q]) == __ldg(p.sel_bias + b)))
-                        near = true;
+                        const bool same = load_one(p.logits, p.dtype, lrow + ev[q]) == load_one(p.logits, p.dtype, lrow + b) &&
+                                          __ldg(p.sel_bias + ev[q]) == __ldg(p.sel_bias + b);
+                        near |= !same;
+                        tied |= same && border;
+                    }
+                }
+                // behind a tie at the border stand experts that were compared with none: any of another
+                // logit or bias within the error of the tie's key
+                if ((__ballot_sync(0xffffffffu, tied) & gmask) != 0) {
+                    const int b = slots.idx[row][p.k];
+                    const float x = key_value(slots.key[row][p.k]), bl = load_one(p.logits, p.dtype, lrow + b);
+                    const float bb = __ldg(p.sel_bias + b), err = 2.0f * rel * s_max + kUlp * (4.0f * fabsf(x) + s_max);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float v = own_row[e0 + at<V>(i)] + bias(i);
+                        near |= l[i] != -INFINITY && fabsf(v - x) <= err && !(l[i] == bl && bias(i) == bb) &&
+                                (!grouped || (kept >> ((e0 + at<V>(i)) / gs)) & 1u);
+                    }
                 }
             }
             // the vote is the whole warp's: it stands before any branch that a token takes alone

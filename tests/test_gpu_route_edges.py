@@ -105,3 +105,52 @@ def test_nan_takes_no_part_in_a_groups_sum(E, n_group, topn, where):
         o = call(off, 2, "sigmoid", n_group=n_group, topk_group=1, group_topn=topn,
                  bias=None if bias is None else torch.where(torch.isnan(bias), -float("inf"), bias))
         assert torch.equal(o["idx"], g["idx"]) and torch.equal(o["w"], g["w"])
+
+
+@pytest.mark.parametrize("E", [4, 8, 24, 64, 128, 256, 512, 1024])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_better_expert_behind_ties(E, dtype):
+    """The first slots tie exactly (the same logit and bias), and an expert whose key equals theirs
+    in 32 bits, but is larger, has a higher index."""
+    for k in (1, 2, 8):
+        if k + 2 > E:
+            continue
+        for last in (E - 1, k + 1):
+            l = torch.full((21, E), -4.0, dtype=dtype, device=DEV)
+            l[:, :k + 1] = 18.0
+            l[::2, last] = 20.0                          # 1 - 2e-9 against 1 - 1.5e-8
+            g, _ = check(l, k, "sigmoid", bias=torch.full((E,), 0.5, device=DEV), backward=False)
+            assert g["idx"][0].tolist() == [last] + list(range(k - 1)) and g["idx"][1].tolist() == list(range(k))
+            # softmax: scores of some 1e-13 under a bias of 1
+            l = torch.full((21, E), -30.0, dtype=dtype, device=DEV)
+            l[::2, last] = -29.0
+            bias = torch.ones((E,), device=DEV)
+            if last != k + 2 and k + 3 <= E:
+                l[:, k + 2 if last == k + 1 else k + 1] = 0.0
+                bias[k + 2 if last == k + 1 else k + 1] = -5.0
+                # the selection alone: z is (log(1 + 4e-13))^2 here, below what 32 bits hold of 1 + 4e-13
+                g = call(l, k, "softmax", bias=bias)
+                r = R.route(l.double().cpu().numpy(), k, "softmax", bias=bias.cpu().numpy())
+                assert np.array_equal(g["idx"].cpu().numpy(), r["idx"]) and g["idx"][0, 0] == last
+                np.testing.assert_allclose(g["w"].cpu().numpy(), r["w"], rtol=1e-5)
+
+
+@pytest.mark.parametrize("E", WIDTHS)
+@pytest.mark.parametrize("steps", [1, 3])
+def test_many_equal_logits_and_biases(E, steps):
+    """Saturated bf16 logits of a few values under biases of a few values, as equal steps leave
+    them: ties, and near-ties among them, without and with groups."""
+    rng = np.random.default_rng(E * 10 + steps)
+    l = torch.tensor(rng.integers(16, 22, size=(80, E)), dtype=torch.bfloat16, device=DEV)
+    l[::3, E // 2:] = -3.0
+    bias = torch.tensor(0.5 + rng.integers(0, steps, E) * 2.0 ** -23, dtype=torch.float32, device=DEV)
+    for k in (1, 2, min(8, E // 2)):
+        check(l, k, "sigmoid", bias=bias, backward=False)
+        check(l, k, "sigmoid", bias=bias, n_group=4, topk_group=2, group_topn=2, backward=False)
+
+
+def test_all_logits_equal_under_biases_of_two_values():
+    for E in WIDTHS:
+        bias = torch.where(torch.arange(E, device=DEV) % 3 == 1, 0.002, 0.001)
+        g, _ = check(torch.zeros((33, E), device=DEV), 2, "sigmoid", bias=bias, backward=False)
+        assert (g["idx"] == torch.tensor([1, 4], device=DEV)).all()
