@@ -1397,16 +1397,29 @@ route_backward_kernel(const RouteBackwardLaunch p) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) s[i] *= inv;
             }
-            if (!softmax) {
+            float sum = 0.0f;                        // sum s a; softmax: sum s g
+            if (softmax) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    z[i] = dz != 0.0f ? zc * s[i] : 0.0f;
-                    s[i] = rcp_fast(1.0f + expf(-l[i]));
-                    Z += s[i];
+                for (int i = 0; i < V / 4; ++i) *fours(s_row, i) = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+            } else {
+                // the scores go to s_row; s[] keeps their derivative s (1 - s). Where s is near 1, 1 - s is exp(-l) s:
+                // subtracted, it would keep s's last digit only (6 % off at l = 16, nothing from 17 on).
+#pragma unroll
+                for (int i = 0; i < V / 4; ++i) {
+                    float four[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int c = 4 * i + j;
+                        z[c] = dz != 0.0f ? zc * s[c] : 0.0f;
+                        const float e = expf(-l[c]);
+                        four[j] = rcp_fast(1.0f + e);
+                        Z += four[j];
+                        if (terms) sum += four[j] * a(c);
+                        s[c] = four[j] * (e < 1.0f ? e * four[j] : 1.0f - four[j]);
+                    }
+                    *fours(s_row, i) = make_float4(four[0], four[1], four[2], four[3]);
                 }
             }
-#pragma unroll
-            for (int i = 0; i < V / 4; ++i) *fours(s_row, i) = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
             __syncwarp();
             // the weights' gradient, taken to the chosen scores
             float cs[kOwn], chosen = 0.0f, dot = 0.0f, to_score = p.scale;
@@ -1441,7 +1454,6 @@ route_backward_kernel(const RouteBackwardLaunch p) {
                 *fours(g_row, i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
             // through the score function
-            float sum = 0.0f;
             if (softmax) {
                 // the chosen scores' part of sum s g vanishes where the weights are normalised
                 if (terms || !p.normalize) {
@@ -1455,15 +1467,13 @@ route_backward_kernel(const RouteBackwardLaunch p) {
             } else {
                 float invZ = 0.0f;
                 if (terms) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) sum += s[i] * a(i);
                     sum = lanes_sum<G>(gmask, sum);
                     Z = lanes_sum<G>(gmask, Z);
                     invZ = 1.0f / (Z + kEps);        // a token that is not live has s = 0 and a finite factor
                     sum *= invZ;
                 }
 #pragma unroll
-                for (int i = 0; i < V; ++i) g[i] = s[i] * (1.0f - s[i]) * (g[i] + (a(i) - sum) * invZ) + z[i];
+                for (int i = 0; i < V; ++i) g[i] = s[i] * (g[i] + (a(i) - sum) * invZ) + z[i];
             }
             // an expert that is off has s = 0, but NaN beside a NaN
 #pragma unroll

@@ -154,3 +154,35 @@ def test_all_logits_equal_under_biases_of_two_values():
         bias = torch.where(torch.arange(E, device=DEV) % 3 == 1, 0.002, 0.001)
         g, _ = check(torch.zeros((33, E), device=DEV), 2, "sigmoid", bias=bias, backward=False)
         assert (g["idx"] == torch.tensor([1, 4], device=DEV)).all()
+
+
+@pytest.mark.parametrize("E", WIDTHS)
+@pytest.mark.parametrize("normalize", [True, False])
+def test_gradient_of_saturated_sigmoids(E, normalize):
+    """s (1 - s) to a relative 2e-5 also where 1 - s is far below s's last digit: 1 - s = exp(-l) s
+    carries exp's and s's errors, 2e-6 together; the rest is a sum held to its magnitudes."""
+    rng = np.random.default_rng(E)
+    T, k = 37, 3
+    l = torch.tensor(rng.uniform(-25.0, 25.0, size=(T, E)), dtype=torch.float32, device=DEV)
+    l[:9] = l[:9].abs() + 8.0
+    l[9, 0], l[9, 1], l[9, 2] = 80.0, -80.0, 200.0
+    dw = rng.normal(size=(T, k)).astype(np.float32)
+    for dbal in (0.0, 4.0):
+        g = call(l, k, "sigmoid", normalize, 1.5, dw=torch.tensor(dw, device=DEV), dlosses=torch.tensor([dbal, 0.0], device=DEV))
+        ln = l.double().cpu().numpy()
+        s, rest = 1.0 / (1.0 + np.exp(-ln)), 1.0 / (1.0 + np.exp(ln))
+        r = R.route(ln, k, "sigmoid", normalize, 1.5)
+        assert np.array_equal(g["idx"].cpu().numpy(), r["idx"])
+        gs, size = np.zeros((T, E)), np.zeros((T, E))
+        sk = np.take_along_axis(s, r["idx"], 1)
+        base = sk.sum(1, keepdims=True) + 1e-20 if normalize else np.ones((T, 1))
+        d = dw.astype(np.float64)
+        cut = (d * sk).sum(1, keepdims=True) / base * normalize
+        np.put_along_axis(gs, r["idx"], 1.5 / base * (d - cut), 1)
+        np.put_along_axis(size, r["idx"], 1.5 / base * (np.abs(d) + (np.abs(d) * sk).sum(1, keepdims=True) / base * normalize), 1)
+        a = dbal * E * r["counts"] / (k * float(T) ** 2)
+        Z = s.sum(1, keepdims=True)
+        gs += (a - (s * a).sum(1, keepdims=True) / Z) / Z
+        size += (a + (s * a).sum(1, keepdims=True) / Z) / Z
+        got = g["dl"].double().cpu().numpy()
+        assert (np.abs(got - s * rest * gs) <= 2e-5 * s * rest * size + 1e-37).all()
