@@ -1432,12 +1432,18 @@ route_backward_kernel(const RouteBackwardLaunch p) {
                 else cw[q] = 0.0f;                   // the weight of a slot left over is a constant: whatever its gradient
                 chosen += cs[q];
             }
+            float rest = 0.0f;                       // sum s g over the chosen: the denominator's 1e-20 has that part
             if (p.normalize) {
-                const float inv = 1.0f / (lanes_sum<G>(gmask, chosen) + kEps);
+                chosen = lanes_sum<G>(gmask, chosen);
+                const float inv = 1.0f / (chosen + kEps);
 #pragma unroll
                 for (int q = 0; q < kOwn; ++q) dot += cs[q] * inv * cw[q];
                 dot = lanes_sum<G>(gmask, dot);
-                to_score = p.k > 1 ? p.scale * inv : 0.0f;   // one weight alone is the constant scale
+                const float eps_share = chosen + kEps != chosen ? kEps * inv : 0.0f;
+                if (eps_share != 0.0f) rest = p.scale * dot * eps_share;
+                // one weight alone is the constant scale but for that part
+                to_score = p.scale * inv * (p.k > 1 ? 1.0f : eps_share);
+                if (p.k == 1) dot = 0.0f;
             }
 #pragma unroll
             for (int q = 0; q < kOwn; ++q)
@@ -1455,12 +1461,13 @@ route_backward_kernel(const RouteBackwardLaunch p) {
             }
             // through the score function
             if (softmax) {
-                // the chosen scores' part of sum s g vanishes where the weights are normalised
+                // with normalised weights the chosen scores' part of sum s g is `rest`
                 if (terms || !p.normalize) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) sum += s[i] * (p.normalize ? a(i) : g[i] + a(i));
                     sum = lanes_sum<G>(gmask, sum);
                 }
+                sum += rest;
                 const float minus = zc - sum;
 #pragma unroll
                 for (int i = 0; i < V; ++i) g[i] = s[i] * (g[i] + (a(i) + minus));

@@ -186,3 +186,18 @@ def test_gradient_of_saturated_sigmoids(E, normalize):
         size += (a + (s * a).sum(1, keepdims=True) / Z) / Z
         got = g["dl"].double().cpu().numpy()
         assert (np.abs(got - s * rest * gs) <= 2e-5 * s * rest * size + 1e-37).all()
+
+
+@pytest.mark.parametrize("E", WIDTHS)
+@pytest.mark.parametrize("k", [1, 3])
+def test_gradient_where_the_chosen_scores_vanish(E, k):
+    """Chosen by their bias, with scores about the 1e-20 in the denominator: it has a gradient of
+    its own, for a single weight and, through softmax, for the experts not chosen."""
+    l = logits(43, E, seed=E, scale=0.5)
+    l[:, E // 2] = torch.linspace(43.0, 52.0, 43, device=DEV)   # the others' scores: 3e-19 ... 3e-23
+    bias = torch.full((E,), 3.0, device=DEV)
+    bias[E // 2] = -3.0
+    check(l, k, "softmax", bias=bias, scale=2.0)
+    l[:, E // 2] = 1.0
+    l -= torch.linspace(40.0, 52.0, 43, device=DEV)[:, None]
+    check(l, k, "sigmoid", scale=2.0)
