@@ -945,6 +945,7 @@ route_kernel(const RouteLaunch p) {
                                 }
                             }
                         }
+                        __syncwarp();                // votes order no memory: the first places before the second
                         gather();
                     }
                 }
@@ -1050,6 +1051,7 @@ route_kernel(const RouteLaunch p) {
                     }
                     n = lanes_reduce<G>(gmask, __popc(cand), [](int a, int b) { return a + b; });
                 }
+                __syncwarp(gmask);                   // the slots are read before others are written there
                 if (n <= G)
                     select_near<G, V>(p, lrow, sub, gmask, cand, slots.idx[row], slots.s[row]);
                 else
