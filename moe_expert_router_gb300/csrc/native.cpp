@@ -109,6 +109,18 @@ void *handle(PyObject *o) {
     return p;
 }
 
+// A call's status for Python; where it succeeded, `bump` moves the version counters of what the
+// caller holds and the call has changed in place, as torch's own in-place operations do: a saved
+// tensor or a cached copy is seen to be old.
+template <typename F>
+PyObject *changed(moe_status_t status, F bump) {
+    if (status == MOE_OK) bump();
+    return PyLong_FromLong(status);
+}
+void bump(const at::Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();     // those have no counter
+}
+
 // logits, cfg, topk_idx, topk_w, sel_bias, token_mask, seq_offsets, counts, seq_tokens, losses, ws, stream
 PyObject *route(PyObject *const *a) {
     const Logits l = logits_of(a[0], a[2], a[6]);
@@ -155,9 +167,10 @@ PyObject *bias_update(PyObject *const *a) {
         refuse(PyExc_ValueError, "bias and counts differ in layers or experts");
     const double rate = PyFloat_AsDouble(a[2]);
     if (rate == -1.0 && PyErr_Occurred()) throw Refused();
-    return PyLong_FromLong(g_bias_update(as<float>(address(a[0], "bias", at::kFloat, b.sizes())),
-                                         as<int32_t>(address(a[1], "counts", at::kInt, c.sizes())), L, S, E,
-                                         static_cast<float>(rate), handle(a[3])));
+    return changed(g_bias_update(as<float>(address(a[0], "bias", at::kFloat, b.sizes())),
+                                 as<int32_t>(address(a[1], "counts", at::kInt, c.sizes())), L, S, E,
+                                 static_cast<float>(rate), handle(a[3])),
+                   [&] { bump(b); });
 }
 
 // A list's addresses, element counts and types, checked: dense CUDA tensors on one device,
@@ -223,6 +236,11 @@ const List &list_of(List &l, PyObject *o, const char *name, int device, int dtyp
     return l;
 }
 
+void bump(const List &l) {
+    for (const at::Tensor *t : l.tensor)
+        if (t != nullptr) bump(*t);
+}
+
 struct Scratch {
     void *ptr;
     size_t bytes;
@@ -270,9 +288,10 @@ PyObject *clip_grads(PyObject *const *a) {
     const Scratch ws = scratch(a[4]);
     const double most = PyFloat_AsDouble(a[2]);
     if (most == -1.0 && PyErr_Occurred()) throw Refused();
-    return PyLong_FromLong(g_clip_grads(g.ptr.data(), g.numel.data(), g.type.data(), static_cast<int32_t>(g.ptr.size()),
-                                        static_cast<int32_t>(whole(a[1])), static_cast<float>(most),
-                                        number(a[3], "norm"), ws.ptr, ws.bytes, handle(a[5])));
+    return changed(g_clip_grads(g.ptr.data(), g.numel.data(), g.type.data(), static_cast<int32_t>(g.ptr.size()),
+                                static_cast<int32_t>(whole(a[1])), static_cast<float>(most),
+                                number(a[3], "norm"), ws.ptr, ws.bytes, handle(a[5])),
+                   [&] { bump(g); });
 }
 
 // params, grads, exp_avg, exp_avg_sq, masters, cfg, lr, step, norm, ws, stream
@@ -282,15 +301,21 @@ PyObject *adamw(PyObject *const *a) {
     const List &g = list_of(t_lists[1], a[1], "grads", device, -1, &p, false, false);
     const List &m = list_of(t_lists[2], a[2], "exp_avg", device, MOE_DTYPE_F32, &p, false, true);
     const List &v = list_of(t_lists[3], a[3], "exp_avg_sq", device, MOE_DTYPE_F32, &p, false, true);
-    const List &x = t_lists[4];
-    if (a[4] != Py_None) list_of(t_lists[4], a[4], "masters", device, MOE_DTYPE_F32, &p, true, true);
+    const List *x = a[4] != Py_None ? &list_of(t_lists[4], a[4], "masters", device, MOE_DTYPE_F32, &p, true, true) : nullptr;
     const Scratch ws = scratch(a[9]);
     auto floats = [](const List &l) { return reinterpret_cast<float *const *>(l.ptr.data()); };
-    return PyLong_FromLong(g_adamw(p.ptr.data(), p.type.data(), g.ptr.data(), g.type.data(), floats(m), floats(v),
-                                   a[4] != Py_None ? floats(x) : nullptr, p.numel.data(), static_cast<int32_t>(p.ptr.size()),
-                                   as<const moe_adamw_cfg_t>(handle(a[5])), as<float>(address(a[6], "lr", at::kFloat, {1})),
-                                   as<int32_t>(address(a[7], "step", at::kInt, {1})),
-                                   number(a[8], "norm"), ws.ptr, ws.bytes, handle(a[10])));
+    return changed(g_adamw(p.ptr.data(), p.type.data(), g.ptr.data(), g.type.data(), floats(m), floats(v),
+                           x != nullptr ? floats(*x) : nullptr, p.numel.data(), static_cast<int32_t>(p.ptr.size()),
+                           as<const moe_adamw_cfg_t>(handle(a[5])), as<float>(address(a[6], "lr", at::kFloat, {1})),
+                           as<int32_t>(address(a[7], "step", at::kInt, {1})),
+                           number(a[8], "norm"), ws.ptr, ws.bytes, handle(a[10])),
+                   [&] {
+                       bump(p);
+                       bump(m);
+                       bump(v);
+                       if (x != nullptr) bump(*x);
+                       bump(tensor(a[7], "step"));
+                   });
 }
 
 // bytes, like: a workspace on that tensor's device, and an fp32 number at its end

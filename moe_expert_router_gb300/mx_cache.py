@@ -3,7 +3,8 @@
 The guide's mxfp8 path keeps the expert parameters in bf16 and holds their
 MXFP8 quantization in a cache keyed on the weight tensor's version counter;
 once per optimizer step the cache is dropped as well, because an optimizer can
-update the weights in place without bumping that counter. This module is the
+update the weights in place without bumping that counter (through `.data`, or in
+a replayed CUDA graph; this package's own calls bump it). This module is the
 same bookkeeping on the host: it calls the library's quantizer
 (``moe_mx_quantize``) and does no arithmetic of its own.
 """

@@ -1,6 +1,10 @@
 """The optimizer's end of a training step: gradient norm, clipping and AdamW over all
 parameters at once, on libmoe's kernels.
 
+What a call changes in place has its version counter moved, as by torch's own optimizers: a
+backward through weights that a step has changed is refused, and an `MxWeightCache` quantizes
+them again. A replayed graph moves no counter: call the cache's `invalidate()` beside it.
+
 Every call takes whole lists of tensors (fp32, bf16, fp16, mixed; any sizes), enqueues
 two or three kernels on the current stream and reads nothing back: the norm, the clip
 factor, the learning rate and the step count stay on the device, so a step can be
@@ -61,8 +65,7 @@ class AdamW:
 
     `step(grads=None, max_norm=0.0)` uses the parameters' .grad where no list is given; parameters
     without a gradient are left alone. `lr` and `step_count` are device tensors: write into `lr`
-    for a schedule. Masters are copies made here (`refresh_masters`). After an update in place, drop the weights' MXFP8 copies
-    (`MxWeightCache.invalidate`)."""
+    for a schedule. Masters are copies made here (`refresh_masters`)."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, masters=True,
                  skip_nonfinite=False):

@@ -1,0 +1,69 @@
+"""The optimizer's end of a step beside the rest of torch: writes that the tensors' version
+counters show, constants in the host's digits, a step count for each parameter, and lists that
+share memory."""
+import numpy as np
+import pytest
+import torch
+
+from moe_expert_router_gb300 import binding as B
+from moe_expert_router_gb300 import optim, torch_ops
+from moe_expert_router_gb300.mx_cache import MxWeightCache
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    B.load()
+
+
+def randn(*shape, seed=0, dtype=torch.float32):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).to(dtype).to(DEV)
+
+
+def test_updates_move_the_version_counters():
+    p, g = randn(40, 3, dtype=torch.bfloat16), randn(40, 3, seed=1, dtype=torch.bfloat16)
+    o = optim.AdamW([p])
+    written = [p, o.exp_avg[0], o.exp_avg_sq[0], o.masters[0], o.step_count]
+    before, read = [t._version for t in written], g._version
+    o.step([g], max_norm=1.0)
+    assert all(t._version > v for t, v in zip(written, before)) and g._version == read
+    optim.grad_norm([g])
+    assert g._version == read
+    optim.clip_grad_norm_([g], 0.1)
+    assert g._version > read
+    bias, counts = torch.zeros((8,), device=DEV), torch.ones((1, 8), dtype=torch.int32, device=DEV)
+    before = bias._version
+    B.moe_bias_update(bias, counts, 0.1)
+    assert bias._version > before
+    with torch.inference_mode():                         # a tensor without a counter
+        q = torch.ones((5,), device=DEV)
+        optim.clip_grad_norm_([q], 0.5)
+    optim.clip_grad_norm_([q], 0.25)
+    assert abs(optim.grad_norm([q]).item() - 0.25) < 1e-5
+
+
+def test_weight_copies_follow_an_update():
+    w, g = randn(2, 4, 128, dtype=torch.bfloat16), randn(2, 4, 128, seed=1, dtype=torch.bfloat16)
+    cache = MxWeightCache()
+    old = [t.clone() for t in cache.get(w)]
+    optim.AdamW([w], lr=0.5).step([g])
+    new = cache.get(w)
+    assert cache.quantizations == 2
+    fresh = MxWeightCache().get(w)
+    assert all(torch.equal(a, b) for a, b in zip(new, fresh)) and not torch.equal(new[0], old[0])
+
+
+def test_a_backward_after_the_update_is_refused():
+    T, H, I, E, k = 64, 128, 64, 4, 2
+    x, w = randn(T, H, dtype=torch.bfloat16), torch.full((T, k), 0.5, device=DEV)
+    w1 = (randn(E, 2 * I, H, seed=1) * H ** -0.5).bfloat16().requires_grad_()
+    w2 = (randn(E, H, I, seed=2) * I ** -0.5).bfloat16().requires_grad_()
+    idx = torch.arange(T * k, dtype=torch.int32, device=DEV).view(T, k) % E
+    y = torch_ops.moe_experts(x, idx, w, w1, w2)
+    optim.AdamW([w1, w2], lr=0.1).step([torch.ones_like(w1), torch.ones_like(w2)])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.float().sum().backward()

@@ -201,3 +201,20 @@ def test_gradient_where_the_chosen_scores_vanish(E, k):
     l[:, E // 2] = 1.0
     l -= torch.linspace(40.0, 52.0, 43, device=DEV)[:, None]
     check(l, k, "sigmoid", scale=2.0)
+
+
+@pytest.mark.parametrize("row", [[1.0, 0.25, -0.5, 0.0], [2.0, 0.5, -1.0, 1.0]])
+def test_sums_over_many_tokens(row):
+    """134 million equal tokens: 64 additions in a row of a thread at most, 32 rows of a block, 26
+    of the reduction, 2^-24 each, and a score's own error of 1e-6."""
+    T, E = 1 << 27, 4
+    l = torch.tensor(row, dtype=torch.bfloat16, device=DEV).repeat(T, 1)
+    out = torch.empty((T, 1), dtype=torch.int32, device=DEV), torch.empty((T, 1), device=DEV)
+    counts = torch.empty((1, E), dtype=torch.int32, device=DEV)
+    tokens, losses = torch.empty((3,), dtype=torch.int32, device=DEV), torch.empty((2,), device=DEV)
+    ws = torch.empty((B.moe_route_workspace_size(T, E, 1, 1),), dtype=torch.uint8, device=DEV)
+    B.moe_route(l, B.router_cfg(), *out, counts=counts, seq_tokens=tokens, losses=losses, ws=ws)
+    x = np.exp(np.array(row))
+    assert counts[0].tolist() == [T, 0, 0, 0] and tokens.tolist() == [T, T, 1]
+    want = np.array([E * x[0] / x.sum(), np.log(x.sum()) ** 2])
+    np.testing.assert_allclose(losses.cpu().numpy(), want, rtol=(64 + 32 + 26) * 2.0 ** -24 + 2e-6)
