@@ -309,13 +309,8 @@ PyObject *adamw(PyObject *const *a) {
                            as<const moe_adamw_cfg_t>(handle(a[5])), as<float>(address(a[6], "lr", at::kFloat, {1})),
                            as<int32_t>(address(a[7], "step", at::kInt, {1})),
                            number(a[8], "norm"), ws.ptr, ws.bytes, handle(a[10])),
-                   [&] {
-                       bump(p);
-                       bump(m);
-                       bump(v);
-                       if (x != nullptr) bump(*x);
-                       bump(tensor(a[7], "step"));
-                   });
+                   // not the optimizer's own state, which no graph saves: 10 ns each, 3 us of a call's 32 for 120 parameters
+                   [&] { bump(p); });
 }
 
 // bytes, like: a workspace on that tensor's device, and an fp32 number at its end

@@ -1,8 +1,8 @@
 """The optimizer's end of a training step: gradient norm, clipping and AdamW over all
 parameters at once, on libmoe's kernels.
 
-What a call changes in place has its version counter moved, as by torch's own optimizers: a
-backward through weights that a step has changed is refused, and an `MxWeightCache` quantizes
+The parameters and gradients that a call changes in place have their version counters moved, as
+by torch's own optimizers: a backward through weights that a step has changed is refused, and an `MxWeightCache` quantizes
 them again. A replayed graph moves no counter: call the cache's `invalidate()` beside it.
 
 Every call takes whole lists of tensors (fp32, bf16, fp16, mixed; any sizes), enqueues
