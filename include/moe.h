@@ -387,7 +387,7 @@ moe_status_t moe_clip_grads(void *const *grads, const int64_t *numel, const int3
                             void *stream);
 
 typedef struct moe_adamw_cfg {
-    float beta1, beta2;      /* in [0, 1) */
+    double beta1, beta2;     /* in [0, 1); 1 - beta is taken in fp64 and then rounded */
     float eps;               /* >= 0 */
     float weight_decay;
     float max_norm;          /* clip by the gradients' global 2-norm; 0: no clipping */

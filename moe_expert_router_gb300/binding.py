@@ -55,7 +55,7 @@ class RouteShape(ctypes.Structure):
 
 
 class AdamWCfg(ctypes.Structure):
-    _fields_ = [("beta1", ctypes.c_float), ("beta2", ctypes.c_float), ("eps", ctypes.c_float),
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_float),
                 ("weight_decay", ctypes.c_float), ("max_norm", ctypes.c_float), ("skip_nonfinite", ctypes.c_int32)]
 
 

@@ -437,7 +437,8 @@ struct AdamwLaunch {
     void *const *exp_avg;       // fp32
     void *const *exp_avg_sq;    // fp32
     void *const *masters;       // fp32, or null
-    float beta1, beta2, eps, weight_decay, max_norm;
+    double beta1, beta2;
+    float eps, weight_decay, max_norm;
     int skip_nonfinite;
     const float *lr;            // [1] device
     int32_t *step;              // [1] device

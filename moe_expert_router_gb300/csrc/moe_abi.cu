@@ -1674,7 +1674,7 @@ moe_status_t moe_adamw(void *const *params, const int32_t *param_dtype, const vo
                        float *const *masters, const int64_t *numel, int32_t n, const moe_adamw_cfg_t *cfg,
                        const float *lr, int32_t *step, float *norm, void *ws, size_t ws_bytes, void *stream) {
     if (cfg == nullptr || lr == nullptr || step == nullptr) return MOE_ERR_INVALID_ARG;
-    if (!(cfg->beta1 >= 0.0f && cfg->beta1 < 1.0f && cfg->beta2 >= 0.0f && cfg->beta2 < 1.0f && cfg->eps >= 0.0f &&
+    if (!(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0 && cfg->beta2 >= 0.0 && cfg->beta2 < 1.0 && cfg->eps >= 0.0f &&
           cfg->max_norm >= 0.0f))
         return MOE_ERR_INVALID_ARG;
     if (!aligned_to(lr, 4) || !aligned_to(step, 4) || !aligned_to(norm, 4)) return MOE_ERR_INVALID_ARG;

@@ -366,7 +366,8 @@ __global__ void adamw_count_kernel(int32_t *__restrict__ step) {
 // What a step is made of; step[0] has been counted up. `undo`: the last launch of a step, which
 // takes the count back where the step is skipped.
 struct AdamConst {
-    float beta1, beta2, eps, weight_decay, max_norm;
+    float beta1, beta2, rest1, rest2;       // rest: 1 - beta, rounded from 64 bits (of a rounded 0.999 it is off by 1.3e-5)
+    float eps, weight_decay, max_norm;
     double ln_beta1, ln_beta2;
     const double *part;
     int n_part, skip_nonfinite, undo;
@@ -400,8 +401,8 @@ __device__ __forceinline__ void begin_step(const AdamConst &k, Hyper &h) {
 
 __device__ __forceinline__ void adam_element(const Hyper &h, const AdamConst &c, float grad, float &m, float &v, float &p) {
     const float g = grad * h.factor;
-    m = c.beta1 * m + (1.0f - c.beta1) * g;
-    v = c.beta2 * v + (1.0f - c.beta2) * g * g;
+    m = c.beta1 * m + c.rest1 * g;
+    v = c.beta2 * v + c.rest2 * g * g;
     const float u = m * h.inv_c1 / (sqrtf(v * h.inv_c2) + c.eps);
     p = p - h.lr * (c.weight_decay * p + u);
 }
@@ -730,13 +731,15 @@ cudaError_t launch_clip_grads(const TensorList &grads, int norm_type, float max_
 
 cudaError_t launch_adamw(const AdamwLaunch &p, cudaStream_t st) {
     AdamConst k = {};
-    k.beta1 = p.beta1;
-    k.beta2 = p.beta2;
+    k.beta1 = static_cast<float>(p.beta1);
+    k.beta2 = static_cast<float>(p.beta2);
+    k.rest1 = static_cast<float>(1.0 - p.beta1);
+    k.rest2 = static_cast<float>(1.0 - p.beta2);
     k.eps = p.eps;
     k.weight_decay = p.weight_decay;
     k.max_norm = p.max_norm;
-    k.ln_beta1 = log(static_cast<double>(p.beta1));
-    k.ln_beta2 = log(static_cast<double>(p.beta2));
+    k.ln_beta1 = log(p.beta1);
+    k.ln_beta2 = log(p.beta2);
     k.part = partials(p.ws);
     k.skip_nonfinite = p.skip_nonfinite;
     k.lr = p.lr;

@@ -66,3 +66,20 @@ def test_a_backward_after_the_update_is_refused():
     optim.AdamW([w1, w2], lr=0.1).step([torch.ones_like(w1), torch.ones_like(w2)])
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.float().sum().backward()
+
+
+def test_second_moment_at_the_default_betas():
+    """v = (1 - b2) g^2 from nothing: 1 - 0.999 rounded once, two products, an addition of 0: four
+    roundings of 2^-24. (With 1 - b2 taken from a rounded b2 it is off by 1.3e-5.)"""
+    for betas in ((0.9, 0.999), (0.95, 0.9999)):
+        p, g = randn(3000), randn(3000, seed=1)
+        m, v = torch.zeros_like(p), torch.zeros_like(p)
+        start = p.double().cpu().numpy()
+        step, lr = torch.zeros((1,), dtype=torch.int32, device=DEV), torch.tensor([1e-3], device=DEV)
+        optim.adamw_step([p], [g], [m], [v], step, lr, betas=betas, eps=1e-8, weight_decay=0.0)
+        gn = g.double().cpu().numpy()
+        np.testing.assert_allclose(v.double().cpu().numpy(), (1 - betas[1]) * gn ** 2, rtol=4 * 2.0 ** -24)
+        np.testing.assert_allclose(m.double().cpu().numpy(), (1 - betas[0]) * gn, rtol=3 * 2.0 ** -24)
+        # the first update is lr sign(g) (eps apart)
+        want = -float(lr.item()) * gn / (np.abs(gn) + 1e-8)
+        np.testing.assert_allclose(p.double().cpu().numpy() - start, want, rtol=5e-6, atol=2.0 ** -24 * np.abs(start).max())
