@@ -392,10 +392,12 @@ typedef struct moe_adamw_cfg {
     float weight_decay;
     float max_norm;          /* clip by the gradients' global 2-norm; 0: no clipping */
     int32_t skip_nonfinite;  /* 1: where that norm is not finite, change nothing and do not count the step */
+    const int32_t *missed;   /* int32 [n] on the device: the steps that each parameter had no part in, or NULL */
 } moe_adamw_cfg_t;
 
 /*
- * One AdamW step, t = step[0] + 1 (step[0] becomes t):
+ * One AdamW step, t = step[0] + 1 (step[0] becomes t; for parameter i, t -
+ * missed[i], which counts its own steps):
  *   g = f grad, f = min(1, max_norm / (norm + 1e-6)) or 1
  *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
  *   p -= lr (weight_decay p + (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps))

@@ -56,7 +56,8 @@ class RouteShape(ctypes.Structure):
 
 class AdamWCfg(ctypes.Structure):
     _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_float),
-                ("weight_decay", ctypes.c_float), ("max_norm", ctypes.c_float), ("skip_nonfinite", ctypes.c_int32)]
+                ("weight_decay", ctypes.c_float), ("max_norm", ctypes.c_float), ("skip_nonfinite", ctypes.c_int32),
+                ("missed", ctypes.c_void_p)]
 
 
 class WsLayout(ctypes.Structure):
@@ -564,8 +565,9 @@ def moe_clip_grads(grads, max_norm, norm, ws, norm_type=2.0, stream=None):
                                                   _raw_stream(stream, norm)))
 
 
-def moe_adamw(params, grads, exp_avg, exp_avg_sq, lr, step, ws, cfg, masters=None, norm=None, stream=None):
+def moe_adamw(params, grads, exp_avg, exp_avg_sq, lr, step, ws, cfg, masters=None, norm=None, missed=None, stream=None):
     """One AdamW step over lists of tensors, in place; masters: a list with an fp32 tensor or None
-    for each parameter, or None."""
+    for each parameter, or None; missed: int32, the steps that each parameter had no part in, or
+    None (it takes the place of cfg.missed)."""
     _check("moe_adamw", _module().adamw(params, grads, exp_avg, exp_avg_sq, masters, ctypes.addressof(cfg), lr, step, norm,
-                                        ws, _raw_stream(stream, lr)))
+                                        ws, missed, _raw_stream(stream, lr)))

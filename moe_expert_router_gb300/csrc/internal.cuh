@@ -442,6 +442,7 @@ struct AdamwLaunch {
     int skip_nonfinite;
     const float *lr;            // [1] device
     int32_t *step;              // [1] device
+    const int32_t *missed;      // [n] device or null
     float *norm;                // [1] device or null
     void *ws;
 };

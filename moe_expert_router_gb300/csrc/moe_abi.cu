@@ -1677,7 +1677,8 @@ moe_status_t moe_adamw(void *const *params, const int32_t *param_dtype, const vo
     if (!(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0 && cfg->beta2 >= 0.0 && cfg->beta2 < 1.0 && cfg->eps >= 0.0f &&
           cfg->max_norm >= 0.0f))
         return MOE_ERR_INVALID_ARG;
-    if (!aligned_to(lr, 4) || !aligned_to(step, 4) || !aligned_to(norm, 4)) return MOE_ERR_INVALID_ARG;
+    if (!aligned_to(lr, 4) || !aligned_to(step, 4) || !aligned_to(norm, 4) || !aligned_to(cfg->missed, 4))
+        return MOE_ERR_INVALID_ARG;
     if (n > 0 && (param_dtype == nullptr || grad_dtype == nullptr)) return MOE_ERR_INVALID_ARG;
     const void *const *lists[] = {params, grads, reinterpret_cast<const void *const *>(exp_avg),
                                   reinterpret_cast<const void *const *>(exp_avg_sq),
@@ -1703,6 +1704,7 @@ moe_status_t moe_adamw(void *const *params, const int32_t *param_dtype, const vo
     p.skip_nonfinite = cfg->skip_nonfinite;
     p.lr = lr;
     p.step = step;
+    p.missed = cfg->missed;
     p.norm = norm;
     p.ws = ws;
     return cuda_status(launch_adamw(p, static_cast<cudaStream_t>(stream)));

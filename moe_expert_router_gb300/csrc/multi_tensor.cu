@@ -3,7 +3,7 @@
 //
 //   norm = sqrt(sum x^2), sum |x| or max |x| over every element of every tensor
 //   f    = min(1, max_norm / (norm + 1e-6)),  x <- f x
-//   AdamW, step t:  g = f grad,  m <- b1 m + (1 - b1) g,  v <- b2 v + (1 - b2) g^2
+//   AdamW, a parameter's step t:  g = f grad,  m <- b1 m + (1 - b1) g,  v <- b2 v + (1 - b2) g^2
 //                   p <- p - lr (wd p + (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps))
 //
 // Lists reach the device in the kernels' arguments (pointers, sizes and types), so a
@@ -54,6 +54,7 @@ template <int N>
 struct AdamTable {
     void *p[N], *g[N], *m[N], *v[N], *x[N];
     int64_t numel[N], unit[N];
+    int32_t which[N];                       // its place in the call's list
     uint8_t p_dtype[N], g_dtype[N];
     uint8_t head[N];                        // elements before the first vector of four, kScalar: none
     Runs runs;
@@ -62,7 +63,7 @@ constexpr uint8_t kScalar = 255;
 // a list is launched with the shortest argument block that holds it (1.7, 6.5 or 25 KB: the host
 // writes it at every launch, some 3 us for the longest)
 constexpr int kShort = 64, kMiddle = 256, kLong = 1000;
-constexpr int kAdamShort = 64, kAdamMiddle = 192, kAdamLong = 520;
+constexpr int kAdamShort = 64, kAdamMiddle = 192, kAdamLong = 500;
 static_assert(sizeof(Table<kLong>) < 32000 && sizeof(AdamTable<kAdamLong>) < 32000, "kernel arguments");
 
 // A tensor as elements before the first 16-byte vector, vectors, and elements after.
@@ -373,6 +374,7 @@ struct AdamConst {
     int n_part, skip_nonfinite, undo;
     const float *lr;
     int32_t *step;
+    const int32_t *missed;
     float *norm;
 };
 struct Hyper {
@@ -380,21 +382,33 @@ struct Hyper {
     int skip;
 };
 
-// The step's numbers, in every block, through its shared memory. 1 - b^t = -expm1(t ln b):
-// ln b comes from the host in 64 bits, and expm1 keeps fp32's digits where b^t is near 1.
-__device__ __forceinline__ void begin_step(const AdamConst &k, Hyper &h) {
+// 1 / (1 - b^t) for both b. 1 - b^t = -expm1(t ln b): ln b comes from the host in 64 bits, and
+// expm1 keeps fp32's digits where b^t is near 1.
+__device__ __forceinline__ float2 corrections(const AdamConst &k, int t) {
+    return make_float2(-1.0f / expm1f(static_cast<float>(t * k.ln_beta1)), -1.0f / expm1f(static_cast<float>(t * k.ln_beta2)));
+}
+
+// The step's numbers, in every block, through its shared memory; where parameters have missed
+// steps (`own`: one a tensor of the table), their corrections by their own counts.
+template <int N>
+__device__ __forceinline__ void begin_step(const AdamConst &k, const AdamTable<N> &tab, Hyper &h, float2 *own) {
     const float total = k.n_part > 0 ? total_norm<MOE_NORM_2>(k.part, k.n_part) : 0.0f;
     if (threadIdx.x == 0) {
         h.skip = k.skip_nonfinite && !isfinite(total);
         h.factor = k.n_part > 0 && k.max_norm > 0.0f ? clip_factor(total, k.max_norm) : 1.0f;
         const int t = *k.step;
         h.lr = *k.lr;
-        h.inv_c1 = -1.0f / expm1f(static_cast<float>(t * k.ln_beta1));
-        h.inv_c2 = -1.0f / expm1f(static_cast<float>(t * k.ln_beta2));
+        const float2 c = corrections(k, t);
+        h.inv_c1 = c.x;
+        h.inv_c2 = c.y;
         if (blockIdx.x == 0) {
             if (k.n_part > 0 && k.norm != nullptr) *k.norm = total;
             if (h.skip && k.undo) *k.step = t - 1;
         }
+    }
+    if (k.missed != nullptr) {
+        const int t = *k.step;
+        for (int i = threadIdx.x; i < tab.runs.n; i += kThreads) own[i] = corrections(k, max(1, t - k.missed[tab.which[i]]));
     }
     __syncthreads();
 }
@@ -437,13 +451,18 @@ __global__ void __launch_bounds__(kThreads, kAdamPerSm)
 adamw_kernel(const __grid_constant__ AdamTable<N> tab, const __grid_constant__ AdamConst k) {
     griddep_wait();
     __shared__ Hyper shared;
-    begin_step(k, shared);
-    const Hyper h = shared;
+    __shared__ float2 own[N];
+    begin_step(k, tab, shared, own);
+    Hyper h = shared;
     if (h.skip) return;
     for (int64_t u0 = blockIdx.x * tab.runs.size; u0 < tab.runs.total; u0 += gridDim.x * tab.runs.size) {
         const int64_t u1 = min(tab.runs.total, u0 + tab.runs.size);
         for (int i = find_tensor(tab.unit, tab.runs.n, u0); i < tab.runs.n && tab.unit[i] < u1; ++i) {
             const int pt = tab.p_dtype[i], gt = tab.g_dtype[i];
+            if (k.missed != nullptr) {
+                h.inv_c1 = own[i].x;
+                h.inv_c2 = own[i].y;
+            }
             float *m = static_cast<float *>(tab.m[i]), *v = static_cast<float *>(tab.v[i]);
             float *x = static_cast<float *>(tab.x[i]);
             const void *pin = x != nullptr ? x : tab.p[i];
@@ -675,6 +694,7 @@ cudaError_t adamw_tables(const AdamwLaunch &p, AdamConst k, cudaStream_t st) {
             t.v[n] = p.exp_avg_sq[at];
             t.x[n] = p.masters != nullptr ? p.masters[at] : nullptr;
             t.numel[n] = numel;
+            t.which[n] = at;
             t.p_dtype[n] = static_cast<uint8_t>(p.params.dtype[at]);
             t.g_dtype[n] = static_cast<uint8_t>(p.grads.dtype[at]);
             t.head[n] = vector_head(p, at);
@@ -744,6 +764,7 @@ cudaError_t launch_adamw(const AdamwLaunch &p, cudaStream_t st) {
     k.skip_nonfinite = p.skip_nonfinite;
     k.lr = p.lr;
     k.step = p.step;
+    k.missed = p.missed;
     k.norm = p.norm;
     cudaError_t e;
     if (p.norm != nullptr || p.max_norm > 0.0f || p.skip_nonfinite) {

@@ -294,7 +294,7 @@ PyObject *clip_grads(PyObject *const *a) {
                    [&] { bump(g); });
 }
 
-// params, grads, exp_avg, exp_avg_sq, masters, cfg, lr, step, norm, ws, stream
+// params, grads, exp_avg, exp_avg_sq, masters, cfg, lr, step, norm, ws, missed, stream
 PyObject *adamw(PyObject *const *a) {
     const int device = device_of(a[6], "lr");
     const List &p = list_of(t_lists[0], a[0], "params", device, -1, nullptr, false, true);
@@ -303,12 +303,14 @@ PyObject *adamw(PyObject *const *a) {
     const List &v = list_of(t_lists[3], a[3], "exp_avg_sq", device, MOE_DTYPE_F32, &p, false, true);
     const List *x = a[4] != Py_None ? &list_of(t_lists[4], a[4], "masters", device, MOE_DTYPE_F32, &p, true, true) : nullptr;
     const Scratch ws = scratch(a[9]);
+    moe_adamw_cfg_t cfg = *as<const moe_adamw_cfg_t>(handle(a[5]));
+    cfg.missed = as<const int32_t>(address(a[10], "missed", at::kInt, {static_cast<int64_t>(p.ptr.size())}));
     auto floats = [](const List &l) { return reinterpret_cast<float *const *>(l.ptr.data()); };
     return changed(g_adamw(p.ptr.data(), p.type.data(), g.ptr.data(), g.type.data(), floats(m), floats(v),
                            x != nullptr ? floats(*x) : nullptr, p.numel.data(), static_cast<int32_t>(p.ptr.size()),
-                           as<const moe_adamw_cfg_t>(handle(a[5])), as<float>(address(a[6], "lr", at::kFloat, {1})),
+                           &cfg, as<float>(address(a[6], "lr", at::kFloat, {1})),
                            as<int32_t>(address(a[7], "step", at::kInt, {1})),
-                           number(a[8], "norm"), ws.ptr, ws.bytes, handle(a[10])),
+                           number(a[8], "norm"), ws.ptr, ws.bytes, handle(a[11])),
                    // not the optimizer's own state, which no graph saves: 10 ns each, 3 us of a call's 32 for 120 parameters
                    [&] { bump(p); });
 }
@@ -356,7 +358,7 @@ PyMethodDef kMethods[] = {method<bind, 6>("bind"),
                           method<bias_update, 4>("bias_update"),
                           method<grad_norm, 5>("grad_norm"),
                           method<clip_grads, 6>("clip_grads"),
-                          method<adamw, 11>("adamw"),
+                          method<adamw, 12>("adamw"),
                           method<scratch_with_norm, 2>("scratch"),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

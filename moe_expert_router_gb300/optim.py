@@ -45,17 +45,17 @@ def clip_grad_norm_(grads, max_norm, norm_type=2.0):
 
 
 def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr, masters=None, betas=(0.9, 0.999), eps=1e-8,
-               weight_decay=0.01, max_norm=0.0, skip_nonfinite=False):
+               weight_decay=0.01, max_norm=0.0, skip_nonfinite=False, missed=None):
     """One AdamW step on tensors that the caller holds, in place. step int32 [1] and lr fp32 [1]
     are on the device; exp_avg, exp_avg_sq and masters fp32. With max_norm > 0 the gradients are
-    taken times min(1, max_norm / (their global 2-norm + 1e-6)), without being changed. Returns
-    the norm as a tensor (None where max_norm is 0 and skip_nonfinite is False)."""
+    taken times min(1, max_norm / (their global 2-norm + 1e-6)), without being changed. missed
+    int32 [n] on the device: how many of the steps each parameter had no part in. Returns the norm as a tensor (None where max_norm is 0 and skip_nonfinite is False)."""
     params, grads = _lists(params, "params"), _lists(grads, "grads")
     ws, norm = B.tensors_scratch(len(params), params[0])
     if not (max_norm > 0.0 or skip_nonfinite):
         norm = None
     cfg = B.AdamWCfg(betas[0], betas[1], eps, weight_decay, max_norm, int(bool(skip_nonfinite)))
-    B.moe_adamw(params, grads, exp_avg, exp_avg_sq, lr, step, ws, cfg, masters, norm)
+    B.moe_adamw(params, grads, exp_avg, exp_avg_sq, lr, step, ws, cfg, masters, norm, missed)
     return norm
 
 
@@ -64,7 +64,8 @@ class AdamW:
     those are updated themselves, rounded to nearest at every step).
 
     `step(grads=None, max_norm=0.0)` uses the parameters' .grad where no list is given; parameters
-    without a gradient are left alone. `lr` and `step_count` are device tensors: write into `lr`
+    without a gradient are left alone, and their bias corrections go by the steps that they took
+    part in: `step_count` less their `missed`. Those and `lr` are device tensors: write into `lr`
     for a schedule. Masters are copies made here (`refresh_masters`)."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, masters=True,
@@ -74,6 +75,8 @@ class AdamW:
         self.betas, self.eps, self.weight_decay, self.skip_nonfinite = betas, eps, weight_decay, skip_nonfinite
         self.lr = torch.full((1,), lr, dtype=torch.float32, device=device)
         self.step_count = torch.zeros((1,), dtype=torch.int32, device=device)
+        self.missed = torch.zeros((len(self.params),), dtype=torch.int32, device=device)
+        self._any_missed = False
         self.exp_avg = [torch.zeros_like(p, dtype=torch.float32) for p in self.params]
         self.exp_avg_sq = [torch.zeros_like(p, dtype=torch.float32) for p in self.params]
         self.masters = [p.detach().float() if masters and p.dtype != torch.float32 else None for p in self.params]
@@ -93,7 +96,20 @@ class AdamW:
         at = [i for i, g in enumerate(grads) if g is not None]
         if not at:
             return None
-        return adamw_step([self.params[i] for i in at], [grads[i] for i in at],
+        part = len(at) < len(grads)
+        missed = None
+        # a captured step reads the counts as they are when it is replayed
+        if self._any_missed or (self.params[0].is_cuda and torch.cuda.is_current_stream_capturing()):
+            missed = torch.cat([self.missed[i:i + 1] for i in at]) if part else self.missed
+        before = self.step_count.clone() if part else None
+        norm = adamw_step([self.params[i] for i in at], [grads[i] for i in at],
                           [self.exp_avg[i] for i in at], [self.exp_avg_sq[i] for i in at], self.step_count, self.lr,
                           [self.masters[i] for i in at], self.betas, self.eps, self.weight_decay, max_norm,
-                          self.skip_nonfinite)
+                          self.skip_nonfinite, missed)
+        if part:
+            self._any_missed = True
+            taken = self.step_count - before             # 0 where the step was skipped
+            for i, g in enumerate(grads):
+                if g is None:
+                    self.missed[i:i + 1].add_(taken)
+        return norm

@@ -83,3 +83,59 @@ def test_second_moment_at_the_default_betas():
         # the first update is lr sign(g) (eps apart)
         want = -float(lr.item()) * gn / (np.abs(gn) + 1e-8)
         np.testing.assert_allclose(p.double().cpu().numpy() - start, want, rtol=5e-6, atol=2.0 ** -24 * np.abs(start).max())
+
+
+@pytest.mark.parametrize("skip", [False, True])
+@pytest.mark.parametrize("bound", [0.0, 1.0])
+def test_parameters_count_their_own_steps(skip, bound):
+    """Against torch.optim.AdamW: a parameter whose gradient starts late, one whose gradient
+    pauses, one that never has any, an empty one; with skipped steps between."""
+    start = [randn(*s, seed=i) for i, s in enumerate(((33, 7), (1000,), (4,), (0,), (5,)))]
+    ref = [s.clone().requires_grad_(True) for s in start]
+    theirs = torch.optim.AdamW(ref, lr=0.01, weight_decay=0.1)
+    ours = [s.clone().requires_grad_(True) for s in start]
+    o = optim.AdamW(ours, lr=0.01, weight_decay=0.1, skip_nonfinite=skip)
+    taken = 0
+    for t in range(14):
+        has = [True, t >= 6, t < 3 or t > 7, t != 1, False]
+        for i, (a, b) in enumerate(zip(ref, ours)):
+            a.grad = b.grad = None
+            if has[i]:
+                a.grad, b.grad = randn(*a.shape, seed=100 + 10 * t + i), randn(*a.shape, seed=100 + 10 * t + i)
+        if skip and t in (2, 6, 8):
+            ours[0].grad[1, 1] = float("nan")
+        else:
+            if bound:
+                torch.nn.utils.clip_grad_norm_([a for a in ref if a.grad is not None], bound)
+            theirs.step()
+            taken += 1
+        o.step(max_norm=bound)
+        for a, b in zip(ref, ours):
+            torch.testing.assert_close(b, a, rtol=2e-5, atol=2e-6)
+    assert o.step_count.item() == taken and torch.equal(ours[4].detach(), start[4])
+
+
+def test_own_step_counts_in_a_captured_step():
+    """A captured step in which one parameter has no gradient, replayed, then an eager one of all."""
+    start = [randn(300, seed=1), randn(70, seed=2)]
+    ref = [s.clone().requires_grad_(True) for s in start]
+    theirs = torch.optim.AdamW(ref, lr=0.01, weight_decay=0.0)
+    o = optim.AdamW([s.clone() for s in start], lr=0.01, weight_decay=0.0)
+    g = [randn(300, seed=3), randn(70, seed=4)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        o.step([g[0], None], 1e9)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o.step([g[0], None], 1e9)
+    for _ in range(4):
+        graph.replay()
+    for t in range(8):
+        ref[0].grad, ref[1].grad = g[0].clone(), g[1].clone() if t >= 5 else None
+        theirs.step()
+        if t >= 5:
+            o.step(g, 1e9)
+    for a, b in zip(ref, o.params):
+        torch.testing.assert_close(b, a.detach(), rtol=2e-5, atol=2e-6)
