@@ -71,6 +71,13 @@ T *as(void *p) {
     return static_cast<T *>(p);
 }
 
+// The operands of a call lie on one device.
+void together(const at::Tensor &like, std::initializer_list<PyObject *> others) {
+    for (PyObject *o : others)
+        if (o != Py_None && tensor(o, "operands").device() != like.device())
+            refuse(PyExc_ValueError, "tensors must be on one device");
+}
+
 struct Logits {
     moe_route_shape_t shape;
     const void *ptr;
@@ -124,6 +131,7 @@ void bump(const at::Tensor &t) {
 // logits, cfg, topk_idx, topk_w, sel_bias, token_mask, seq_offsets, counts, seq_tokens, losses, ws, stream
 PyObject *route(PyObject *const *a) {
     const Logits l = logits_of(a[0], a[2], a[6]);
+    together(tensor(a[0], "logits"), {a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10]});
     const moe_route_shape_t &s = l.shape;
     void *ws = nullptr;
     size_t ws_bytes = 0;
@@ -146,6 +154,7 @@ PyObject *route(PyObject *const *a) {
 // logits, cfg, topk_idx, dtopk_w, dlogits, token_mask, seq_offsets, counts, seq_tokens, dlosses, stream
 PyObject *route_backward(PyObject *const *a) {
     const Logits l = logits_of(a[0], a[2], a[6]);
+    together(tensor(a[0], "logits"), {a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9]});
     const moe_route_shape_t &s = l.shape;
     return PyLong_FromLong(g_route_backward(
         l.ptr, mask_of(a[5], s.T), as<int32_t>(address(a[6], "seq_offsets", at::kInt, {s.S + 1})), &s,
@@ -160,6 +169,7 @@ PyObject *route_backward(PyObject *const *a) {
 // bias, counts, rate, stream
 PyObject *bias_update(PyObject *const *a) {
     const at::Tensor &b = tensor(a[0], "bias"), &c = tensor(a[1], "counts");
+    together(b, {a[1]});
     if (b.dim() < 1 || b.dim() > 2 || c.dim() != b.dim() + 1)
         refuse(PyExc_ValueError, "bias must be [E] and counts [S, E], or [L, E] and [L, S, E]");
     const int64_t L = b.dim() == 1 ? 1 : b.size(0), E = b.size(-1), S = c.size(-2);
@@ -177,15 +187,19 @@ PyObject *bias_update(PyObject *const *a) {
 // of the type `dtype` (-1: any of the three); like those of `like` in shape and order in
 // memory, where that is not null; with `optional` or None (address 0); not overlapping,
 // where they are written.
+using Range = std::pair<uint64_t, uint64_t>;  // of addresses, the end not among them
 struct List {
+    const char *name;
+    bool written;
     std::vector<const at::Tensor *> tensor;   // borrowed from the caller's list
     std::vector<void *> ptr;
     std::vector<int64_t> numel;
     std::vector<int32_t> type;
+    std::vector<Range> range;                 // of the tensors that are not empty, in order
+    uint64_t end;                             // the largest of theirs
 };
 // A thread's lists keep their memory from call to call, nothing of what is in them.
 thread_local List t_lists[5];
-thread_local std::vector<std::pair<uint64_t, uint64_t>> t_range;
 
 bool is_list(PyObject *o) { return PyList_Check(o) || PyTuple_Check(o); }
 
@@ -195,13 +209,16 @@ const List &list_of(List &l, PyObject *o, const char *name, int device, int dtyp
     const Py_ssize_t n = PySequence_Fast_GET_SIZE(o);
     if (like != nullptr && static_cast<Py_ssize_t>(like->tensor.size()) != n)
         refuse(PyExc_ValueError, "%s must be as many as the parameters", name);
+    l.name = name;
+    l.written = written;
     l.tensor.assign(n, nullptr);
     l.ptr.assign(n, nullptr);
     l.numel.assign(n, 0);
     l.type.assign(n, MOE_DTYPE_F32);
     const at::Device on(at::kCUDA, static_cast<at::DeviceIndex>(device));
-    std::vector<std::pair<uint64_t, uint64_t>> &range = t_range;
+    std::vector<Range> &range = l.range;
     range.clear();
+    l.end = 0;
     bool sorted = true;
     for (Py_ssize_t i = 0; i < n; ++i) {
         PyObject *item = PySequence_Fast_GET_ITEM(o, i);
@@ -224,16 +241,37 @@ const List &list_of(List &l, PyObject *o, const char *name, int device, int dtyp
         l.ptr[i] = t.data_ptr();
         l.numel[i] = t.numel();
         l.type[i] = code;
-        if (written && l.numel[i] > 0) {
+        if (l.numel[i] > 0) {
             const uint64_t at = reinterpret_cast<uint64_t>(l.ptr[i]);
             sorted = sorted && (range.empty() || range.back().first <= at);
             range.emplace_back(at, at + static_cast<uint64_t>(l.numel[i]) * (code == MOE_DTYPE_F32 ? 4 : 2));
+            l.end = std::max(l.end, range.back().second);
         }
     }
     if (!sorted) std::sort(range.begin(), range.end());
-    for (size_t i = 1; i < range.size(); ++i)
+    for (size_t i = 1; written && i < range.size(); ++i)
         if (range[i].first < range[i - 1].second) refuse(PyExc_ValueError, "%s hold the same memory twice", name);
     return l;
+}
+
+// What a call writes lies in none of its other operands: blocks would read it while others write.
+void apart(const List &a, const List &b) {
+    if (!a.written && !b.written) return;
+    if (a.range.empty() || b.range.empty() || a.end <= b.range.front().first || b.end <= a.range.front().first) return;
+    uint64_t a_end = 0, b_end = 0;            // as far as they have been walked
+    for (size_t i = 0, j = 0; i < a.range.size() || j < b.range.size();) {
+        const bool first = j == b.range.size() || (i < a.range.size() && a.range[i].first < b.range[j].first);
+        const Range &r = first ? a.range[i++] : b.range[j++];
+        if (r.first < (first ? b_end : a_end)) refuse(PyExc_ValueError, "%s and %s hold the same memory", a.name, b.name);
+        uint64_t &end = first ? a_end : b_end;
+        end = std::max(end, r.second);
+    }
+}
+void apart(const List &l, const void *ptr, size_t bytes, const char *name, bool written) {
+    const uint64_t at = reinterpret_cast<uint64_t>(ptr), end = at + bytes;
+    if (ptr == nullptr || !(written || l.written) || l.range.empty() || l.end <= at || end <= l.range.front().first) return;
+    for (const Range &r : l.range)
+        if (r.first < end && at < r.second) refuse(PyExc_ValueError, "%s and %s hold the same memory", l.name, name);
 }
 
 void bump(const List &l) {
@@ -276,21 +314,28 @@ long whole(PyObject *o) {
 // grads, norm_type, norm, ws, stream
 PyObject *grad_norm(PyObject *const *a) {
     const List &g = list_of(t_lists[0], a[0], "grads", device_of(a[2], "norm"), -1, nullptr, false, false);
+    together(tensor(a[2], "norm"), {a[3]});
     const Scratch ws = scratch(a[3]);
+    float *norm = number(a[2], "norm");
+    apart(g, norm, 4, "norm", true);
+    apart(g, ws.ptr, ws.bytes, "ws", true);
     return PyLong_FromLong(g_grad_norm(g.ptr.data(), g.numel.data(), g.type.data(), static_cast<int32_t>(g.ptr.size()),
-                                       static_cast<int32_t>(whole(a[1])), number(a[2], "norm"),
-                                       ws.ptr, ws.bytes, handle(a[4])));
+                                       static_cast<int32_t>(whole(a[1])), norm, ws.ptr, ws.bytes, handle(a[4])));
 }
 
 // grads, norm_type, max_norm, norm, ws, stream
 PyObject *clip_grads(PyObject *const *a) {
     const List &g = list_of(t_lists[0], a[0], "grads", device_of(a[3], "norm"), -1, nullptr, false, true);
+    together(tensor(a[3], "norm"), {a[4]});
     const Scratch ws = scratch(a[4]);
+    float *norm = number(a[3], "norm");
+    apart(g, norm, 4, "norm", true);
+    apart(g, ws.ptr, ws.bytes, "ws", true);
     const double most = PyFloat_AsDouble(a[2]);
     if (most == -1.0 && PyErr_Occurred()) throw Refused();
     return changed(g_clip_grads(g.ptr.data(), g.numel.data(), g.type.data(), static_cast<int32_t>(g.ptr.size()),
                                 static_cast<int32_t>(whole(a[1])), static_cast<float>(most),
-                                number(a[3], "norm"), ws.ptr, ws.bytes, handle(a[5])),
+                                norm, ws.ptr, ws.bytes, handle(a[5])),
                    [&] { bump(g); });
 }
 
@@ -302,15 +347,26 @@ PyObject *adamw(PyObject *const *a) {
     const List &m = list_of(t_lists[2], a[2], "exp_avg", device, MOE_DTYPE_F32, &p, false, true);
     const List &v = list_of(t_lists[3], a[3], "exp_avg_sq", device, MOE_DTYPE_F32, &p, false, true);
     const List *x = a[4] != Py_None ? &list_of(t_lists[4], a[4], "masters", device, MOE_DTYPE_F32, &p, true, true) : nullptr;
+    together(tensor(a[6], "lr"), {a[7], a[8], a[9], a[10]});
     const Scratch ws = scratch(a[9]);
+    const int64_t n = static_cast<int64_t>(p.ptr.size());
+    float *lr = as<float>(address(a[6], "lr", at::kFloat, {1})), *norm = number(a[8], "norm");
+    int32_t *step = as<int32_t>(address(a[7], "step", at::kInt, {1}));
     moe_adamw_cfg_t cfg = *as<const moe_adamw_cfg_t>(handle(a[5]));
-    cfg.missed = as<const int32_t>(address(a[10], "missed", at::kInt, {static_cast<int64_t>(p.ptr.size())}));
+    cfg.missed = as<const int32_t>(address(a[10], "missed", at::kInt, {n}));
+    const List *const lists[] = {&p, &g, &m, &v, x};
+    for (int i = 0; i < 5 && lists[i] != nullptr; ++i) {
+        for (int j = 0; j < i; ++j) apart(*lists[j], *lists[i]);
+        apart(*lists[i], lr, 4, "lr", false);
+        apart(*lists[i], step, 4, "step", true);
+        apart(*lists[i], norm, 4, "norm", true);
+        apart(*lists[i], ws.ptr, ws.bytes, "ws", true);
+        apart(*lists[i], cfg.missed, 4 * static_cast<size_t>(n), "missed", false);
+    }
     auto floats = [](const List &l) { return reinterpret_cast<float *const *>(l.ptr.data()); };
     return changed(g_adamw(p.ptr.data(), p.type.data(), g.ptr.data(), g.type.data(), floats(m), floats(v),
                            x != nullptr ? floats(*x) : nullptr, p.numel.data(), static_cast<int32_t>(p.ptr.size()),
-                           &cfg, as<float>(address(a[6], "lr", at::kFloat, {1})),
-                           as<int32_t>(address(a[7], "step", at::kInt, {1})),
-                           number(a[8], "norm"), ws.ptr, ws.bytes, handle(a[11])),
+                           &cfg, lr, step, norm, ws.ptr, ws.bytes, handle(a[11])),
                    // not the optimizer's own state, which no graph saves: 10 ns each, 3 us of a call's 32 for 120 parameters
                    [&] { bump(p); });
 }

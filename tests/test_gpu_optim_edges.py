@@ -139,3 +139,43 @@ def test_own_step_counts_in_a_captured_step():
             o.step(g, 1e9)
     for a, b in zip(ref, o.params):
         torch.testing.assert_close(b, a.detach(), rtol=2e-5, atol=2e-6)
+
+
+def test_lists_that_share_memory_are_refused():
+    """A tensor that a step writes may lie in no other of its lists."""
+    n = 64
+    buf = [randn(4 * n, seed=i) for i in range(5)]
+    step, lr = torch.zeros((1,), dtype=torch.int32, device=DEV), torch.tensor([0.1], device=DEV)
+
+    def lists():
+        return [[b[:n], b[2 * n:3 * n]] for b in buf]
+    before = [b.clone() for b in buf]
+    for i in range(5):
+        for j in range(5):
+            if i == j:
+                continue
+            for at in (0, 1):
+                for part in (lambda t, u: u, lambda t, u: buf[i][n - 1:2 * n - 1] if at == 0 else buf[i][3 * n - 1:4 * n - 1]):
+                    a = lists()
+                    a[j][at] = part(a[j][at], a[i][at])
+                    p, g, m, v, x = a
+                    with pytest.raises(ValueError, match="memory"):
+                        optim.adamw_step(p, g, m, v, step, lr, masters=x)
+    p, g, m, v, x = lists()
+    for k in range(5):                                   # lr and step inside a list
+        other = lists()
+        other[k][0] = torch.zeros((n,), device=DEV)
+        for bad in (dict(lr=other[k][0][3:4]), dict(step=other[k][0].view(torch.int32)[3:4])):
+            if k == 1 and "lr" in bad:                   # both are only read
+                continue
+            with pytest.raises(ValueError, match="memory"):
+                q = {**dict(step=step, lr=lr), **bad}
+                optim.adamw_step(other[0], other[1], other[2], other[3], q["step"], q["lr"], masters=other[4])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(buf, before)) and step.item() == 0
+    # neighbours, interleaved and out of order, are not shared
+    whole = torch.zeros((10 * n,), device=DEV)
+    cut = [whole[i * n:(i + 1) * n] for i in (7, 2, 9, 0, 4, 3, 8, 1, 6, 5)]
+    optim.adamw_step(cut[:2], cut[2:4], cut[4:6], cut[6:8], step, lr, masters=[cut[8], cut[9]])
+    optim.adamw_step(cut[:2], [g[0], g[0]], cut[4:6], cut[6:8], step, lr, masters=[None, cut[9]])   # a gradient read twice
+    assert step.item() == 2
