@@ -50,8 +50,14 @@ const at::Tensor &tensor(PyObject *o, const char *name) {
     return THPVariable_Unpack(o);
 }
 
-// The address of a dense CUDA tensor of the given type and shape; NULL for None.
-void *address(PyObject *o, const char *name, at::ScalarType type, at::IntArrayRef shape) {
+// The operands of a call lie on one device, that of a CUDA tensor `like`.
+void together(const at::Tensor &like, const at::Tensor &t) {
+    if (t.device() != like.device())
+        refuse(PyExc_ValueError, t.is_cuda() ? "tensors must be on one device" : "libmoe takes CUDA tensors only");
+}
+
+// The address of a dense tensor of the given type and shape on the device of `like`; NULL for None.
+void *address(PyObject *o, const char *name, const at::Tensor &like, at::ScalarType type, at::IntArrayRef shape) {
     if (o == Py_None) return nullptr;
     const at::Tensor &t = tensor(o, name);
     if (t.scalar_type() != type) refuse(PyExc_TypeError, "%s must be %s, not %s", name, c10::toString(type), c10::toString(t.scalar_type()));
@@ -61,7 +67,7 @@ void *address(PyObject *o, const char *name, at::ScalarType type, at::IntArrayRe
         for (int64_t d : t.sizes()) is += std::to_string(d) + ", ";
         refuse(PyExc_ValueError, "%s must have shape (%s), not (%s)", name, want.c_str(), is.c_str());
     }
-    if (!t.is_cuda()) refuse(PyExc_ValueError, "libmoe takes CUDA tensors only");
+    together(like, t);
     if (!t.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous", name);
     return t.data_ptr();
 }
@@ -71,17 +77,9 @@ T *as(void *p) {
     return static_cast<T *>(p);
 }
 
-// The operands of a call lie on one device.
-void together(const at::Tensor &like, std::initializer_list<PyObject *> others) {
-    for (PyObject *o : others)
-        if (o != Py_None && tensor(o, "operands").device() != like.device())
-            refuse(PyExc_ValueError, "tensors must be on one device");
-}
-
 struct Logits {
     moe_route_shape_t shape;
-    const void *ptr;
-    at::ScalarType type;
+    const at::Tensor &tensor;
 };
 
 Logits logits_of(PyObject *lo, PyObject *io, PyObject *oo) {
@@ -101,13 +99,13 @@ Logits logits_of(PyObject *lo, PyObject *io, PyObject *oo) {
         if (o.dim() != 1 || o.size(0) < 2) refuse(PyExc_ValueError, "seq_offsets must be [S + 1] with S >= 1");
         S = o.size(0) - 1;
     }
-    return {{T, E, S, ld, static_cast<int32_t>(i.size(1)), code}, l.data_ptr(), l.scalar_type()};
+    return {{T, E, S, ld, static_cast<int32_t>(i.size(1)), code}, l};
 }
 
-const uint8_t *mask_of(PyObject *o, int64_t T) {
+const uint8_t *mask_of(PyObject *o, const at::Tensor &like, int64_t T) {
     if (o == Py_None) return nullptr;
     const bool bytes = THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() == at::kByte;
-    return as<const uint8_t>(address(o, "token_mask", bytes ? at::kByte : at::kBool, {T}));
+    return as<const uint8_t>(address(o, "token_mask", like, bytes ? at::kByte : at::kBool, {T}));
 }
 
 void *handle(PyObject *o) {
@@ -131,45 +129,46 @@ void bump(const at::Tensor &t) {
 // logits, cfg, topk_idx, topk_w, sel_bias, token_mask, seq_offsets, counts, seq_tokens, losses, ws, stream
 PyObject *route(PyObject *const *a) {
     const Logits l = logits_of(a[0], a[2], a[6]);
-    together(tensor(a[0], "logits"), {a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10]});
     const moe_route_shape_t &s = l.shape;
+    const at::Tensor &on = l.tensor;
     void *ws = nullptr;
     size_t ws_bytes = 0;
     if (a[10] != Py_None) {
         const at::Tensor &t = tensor(a[10], "ws");
-        if (!t.is_cuda() || !t.is_contiguous()) refuse(PyExc_ValueError, "ws must be a contiguous CUDA tensor");
+        together(on, t);
+        if (!t.is_contiguous()) refuse(PyExc_ValueError, "ws must be contiguous");
         ws = t.data_ptr();
         ws_bytes = t.nbytes();
     }
     return PyLong_FromLong(g_route(
-        l.ptr, as<float>(address(a[4], "sel_bias", at::kFloat, {s.E})), mask_of(a[5], s.T),
-        as<int32_t>(address(a[6], "seq_offsets", at::kInt, {s.S + 1})), &s, as<const moe_router_cfg_t>(handle(a[1])),
-        as<int32_t>(address(a[2], "topk_idx", at::kInt, {s.T, s.k})),
-        as<float>(address(a[3], "topk_w", at::kFloat, {s.T, s.k})),
-        as<int32_t>(address(a[7], "counts", at::kInt, {s.S, s.E})),
-        as<int32_t>(address(a[8], "seq_tokens", at::kInt, {s.S + 2})),
-        as<float>(address(a[9], "losses", at::kFloat, {2})), ws, ws_bytes, handle(a[11])));
+        on.data_ptr(), as<float>(address(a[4], "sel_bias", on, at::kFloat, {s.E})), mask_of(a[5], on, s.T),
+        as<int32_t>(address(a[6], "seq_offsets", on, at::kInt, {s.S + 1})), &s, as<const moe_router_cfg_t>(handle(a[1])),
+        as<int32_t>(address(a[2], "topk_idx", on, at::kInt, {s.T, s.k})),
+        as<float>(address(a[3], "topk_w", on, at::kFloat, {s.T, s.k})),
+        as<int32_t>(address(a[7], "counts", on, at::kInt, {s.S, s.E})),
+        as<int32_t>(address(a[8], "seq_tokens", on, at::kInt, {s.S + 2})),
+        as<float>(address(a[9], "losses", on, at::kFloat, {2})), ws, ws_bytes, handle(a[11])));
 }
 
 // logits, cfg, topk_idx, dtopk_w, dlogits, token_mask, seq_offsets, counts, seq_tokens, dlosses, stream
 PyObject *route_backward(PyObject *const *a) {
     const Logits l = logits_of(a[0], a[2], a[6]);
-    together(tensor(a[0], "logits"), {a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9]});
     const moe_route_shape_t &s = l.shape;
+    const at::Tensor &on = l.tensor;
     return PyLong_FromLong(g_route_backward(
-        l.ptr, mask_of(a[5], s.T), as<int32_t>(address(a[6], "seq_offsets", at::kInt, {s.S + 1})), &s,
-        as<const moe_router_cfg_t>(handle(a[1])), as<int32_t>(address(a[2], "topk_idx", at::kInt, {s.T, s.k})),
-        as<float>(address(a[3], "dtopk_w", at::kFloat, {s.T, s.k})),
-        as<int32_t>(address(a[7], "counts", at::kInt, {s.S, s.E})),
-        as<int32_t>(address(a[8], "seq_tokens", at::kInt, {s.S + 2})),
-        as<float>(address(a[9], "dlosses", at::kFloat, {2})), address(a[4], "dlogits", l.type, {s.T, s.E}),
+        on.data_ptr(), mask_of(a[5], on, s.T), as<int32_t>(address(a[6], "seq_offsets", on, at::kInt, {s.S + 1})), &s,
+        as<const moe_router_cfg_t>(handle(a[1])), as<int32_t>(address(a[2], "topk_idx", on, at::kInt, {s.T, s.k})),
+        as<float>(address(a[3], "dtopk_w", on, at::kFloat, {s.T, s.k})),
+        as<int32_t>(address(a[7], "counts", on, at::kInt, {s.S, s.E})),
+        as<int32_t>(address(a[8], "seq_tokens", on, at::kInt, {s.S + 2})),
+        as<float>(address(a[9], "dlosses", on, at::kFloat, {2})), address(a[4], "dlogits", on, on.scalar_type(), {s.T, s.E}),
         handle(a[10])));
 }
 
 // bias, counts, rate, stream
 PyObject *bias_update(PyObject *const *a) {
     const at::Tensor &b = tensor(a[0], "bias"), &c = tensor(a[1], "counts");
-    together(b, {a[1]});
+    if (!b.is_cuda()) refuse(PyExc_ValueError, "libmoe takes CUDA tensors only");
     if (b.dim() < 1 || b.dim() > 2 || c.dim() != b.dim() + 1)
         refuse(PyExc_ValueError, "bias must be [E] and counts [S, E], or [L, E] and [L, S, E]");
     const int64_t L = b.dim() == 1 ? 1 : b.size(0), E = b.size(-1), S = c.size(-2);
@@ -177,8 +176,8 @@ PyObject *bias_update(PyObject *const *a) {
         refuse(PyExc_ValueError, "bias and counts differ in layers or experts");
     const double rate = PyFloat_AsDouble(a[2]);
     if (rate == -1.0 && PyErr_Occurred()) throw Refused();
-    return changed(g_bias_update(as<float>(address(a[0], "bias", at::kFloat, b.sizes())),
-                                 as<int32_t>(address(a[1], "counts", at::kInt, c.sizes())), L, S, E,
+    return changed(g_bias_update(as<float>(address(a[0], "bias", b, at::kFloat, b.sizes())),
+                                 as<int32_t>(address(a[1], "counts", b, at::kInt, c.sizes())), L, S, E,
                                  static_cast<float>(rate), handle(a[3])),
                    [&] { bump(b); });
 }
@@ -283,20 +282,21 @@ struct Scratch {
     void *ptr;
     size_t bytes;
 };
-Scratch scratch(PyObject *o) {
+Scratch scratch(PyObject *o, const at::Tensor &like) {
     const at::Tensor &t = tensor(o, "ws");
-    if (!t.is_cuda() || !t.is_contiguous()) refuse(PyExc_ValueError, "ws must be a contiguous CUDA tensor");
+    together(like, t);
+    if (!t.is_contiguous()) refuse(PyExc_ValueError, "ws must be contiguous");
     return {t.data_ptr(), t.nbytes()};
 }
 
 // The address of the fp32 number that a norm goes to (any shape of one element); NULL for None.
-float *number(PyObject *o, const char *name) {
+float *number(PyObject *o, const char *name, const at::Tensor &like) {
     if (o == Py_None) return nullptr;
     const at::Tensor &t = tensor(o, name);
     if (t.scalar_type() != at::kFloat) refuse(PyExc_TypeError, "%s must be Float, not %s", name, c10::toString(t.scalar_type()));
     if (t.numel() != 1) refuse(PyExc_ValueError, "%s must have one element", name);
-    if (!t.is_cuda()) refuse(PyExc_ValueError, "libmoe takes CUDA tensors only");
-    return t.data_ptr<float>();
+    together(like, t);
+    return static_cast<float *>(t.data_ptr());
 }
 
 int device_of(PyObject *o, const char *name) {
@@ -314,9 +314,9 @@ long whole(PyObject *o) {
 // grads, norm_type, norm, ws, stream
 PyObject *grad_norm(PyObject *const *a) {
     const List &g = list_of(t_lists[0], a[0], "grads", device_of(a[2], "norm"), -1, nullptr, false, false);
-    together(tensor(a[2], "norm"), {a[3]});
-    const Scratch ws = scratch(a[3]);
-    float *norm = number(a[2], "norm");
+    const at::Tensor &on = tensor(a[2], "norm");
+    const Scratch ws = scratch(a[3], on);
+    float *norm = number(a[2], "norm", on);
     apart(g, norm, 4, "norm", true);
     apart(g, ws.ptr, ws.bytes, "ws", true);
     return PyLong_FromLong(g_grad_norm(g.ptr.data(), g.numel.data(), g.type.data(), static_cast<int32_t>(g.ptr.size()),
@@ -326,9 +326,9 @@ PyObject *grad_norm(PyObject *const *a) {
 // grads, norm_type, max_norm, norm, ws, stream
 PyObject *clip_grads(PyObject *const *a) {
     const List &g = list_of(t_lists[0], a[0], "grads", device_of(a[3], "norm"), -1, nullptr, false, true);
-    together(tensor(a[3], "norm"), {a[4]});
-    const Scratch ws = scratch(a[4]);
-    float *norm = number(a[3], "norm");
+    const at::Tensor &on = tensor(a[3], "norm");
+    const Scratch ws = scratch(a[4], on);
+    float *norm = number(a[3], "norm", on);
     apart(g, norm, 4, "norm", true);
     apart(g, ws.ptr, ws.bytes, "ws", true);
     const double most = PyFloat_AsDouble(a[2]);
@@ -347,13 +347,13 @@ PyObject *adamw(PyObject *const *a) {
     const List &m = list_of(t_lists[2], a[2], "exp_avg", device, MOE_DTYPE_F32, &p, false, true);
     const List &v = list_of(t_lists[3], a[3], "exp_avg_sq", device, MOE_DTYPE_F32, &p, false, true);
     const List *x = a[4] != Py_None ? &list_of(t_lists[4], a[4], "masters", device, MOE_DTYPE_F32, &p, true, true) : nullptr;
-    together(tensor(a[6], "lr"), {a[7], a[8], a[9], a[10]});
-    const Scratch ws = scratch(a[9]);
+    const at::Tensor &on = tensor(a[6], "lr");
+    const Scratch ws = scratch(a[9], on);
     const int64_t n = static_cast<int64_t>(p.ptr.size());
-    float *lr = as<float>(address(a[6], "lr", at::kFloat, {1})), *norm = number(a[8], "norm");
-    int32_t *step = as<int32_t>(address(a[7], "step", at::kInt, {1}));
+    float *lr = as<float>(address(a[6], "lr", on, at::kFloat, {1})), *norm = number(a[8], "norm", on);
+    int32_t *step = as<int32_t>(address(a[7], "step", on, at::kInt, {1}));
     moe_adamw_cfg_t cfg = *as<const moe_adamw_cfg_t>(handle(a[5]));
-    cfg.missed = as<const int32_t>(address(a[10], "missed", at::kInt, {n}));
+    cfg.missed = as<const int32_t>(address(a[10], "missed", on, at::kInt, {n}));
     const List *const lists[] = {&p, &g, &m, &v, x};
     for (int i = 0; i < 5 && lists[i] != nullptr; ++i) {
         for (int j = 0; j < i; ++j) apart(*lists[j], *lists[i]);
