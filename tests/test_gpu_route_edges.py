@@ -218,3 +218,34 @@ def test_sums_over_many_tokens(row):
     assert counts[0].tolist() == [T, 0, 0, 0] and tokens.tolist() == [T, T, 1]
     want = np.array([E * x[0] / x.sum(), np.log(x.sum()) ** 2])
     np.testing.assert_allclose(losses.cpu().numpy(), want, rtol=(64 + 32 + 26) * 2.0 ** -24 + 2e-6)
+
+
+@pytest.mark.parametrize("T,E,k", [(2_000_003, 8, 2), (200_001, 600, 4), (1_000_001, 100, 8)])
+def test_sequences_longer_than_a_blocks_run(T, E, k):
+    """Statistics of packed sequences whose part of a block is added in several runs, against the
+    scores in 64 bits and the call's own indices; tolerances as above, and 4e-6 for a score's."""
+    l = torch.randn((T, E), generator=torch.Generator(device=DEV).manual_seed(E), device=DEV).bfloat16()
+    mask = torch.arange(T, device=DEV) % 7 != 3
+    cuts = [0, T // 3, T // 3 + 1, T // 2, T // 2, T]
+    offsets = torch.tensor(cuts, dtype=torch.int32, device=DEV)
+    S = len(cuts) - 1
+    idx, w = torch.empty((T, k), dtype=torch.int32, device=DEV), torch.empty((T, k), device=DEV)
+    counts = torch.empty((S, E), dtype=torch.int32, device=DEV)
+    tokens, losses = torch.empty((S + 2,), dtype=torch.int32, device=DEV), torch.empty((2,), device=DEV)
+    ws = torch.empty((B.moe_route_workspace_size(T, E, S, k),), dtype=torch.uint8, device=DEV)
+    B.moe_route(l, B.router_cfg(), idx, w, token_mask=mask, seq_offsets=offsets, counts=counts, seq_tokens=tokens,
+                losses=losses, ws=ws)
+    balance, z, used = 0.0, 0.0, 0
+    for b in range(S):
+        rows = slice(cuts[b], cuts[b + 1])
+        m = mask[rows]
+        n = int(m.sum())
+        assert torch.equal(counts[b], torch.bincount(idx[rows][m].flatten(), minlength=E).int()) and tokens[b] == n
+        if n:
+            x = l[rows][m].double()
+            balance += (E * counts[b].double() / (k * n) * torch.softmax(x, 1).sum(0) / n).sum().item()
+            z += torch.logsumexp(x, 1).square().sum().item()
+            used += 1
+    assert (idx[~mask] == -1).all() and tokens[S:].tolist() == [int(mask.sum()), used]
+    want = np.array([balance / used, z / int(mask.sum())])
+    np.testing.assert_allclose(losses.cpu().numpy(), want, rtol=(64 + 32 + 26) * 2.0 ** -24 + 4e-6)
