@@ -375,6 +375,7 @@ bool encode_bf16_2d_strided(CUtensorMap *map, const void *base, uint64_t inner, 
 // consecutive ones; a (block, sequence) pair has slot block + sequence, of
 // blocks + S - 1.
 constexpr int64_t kRouteMaxBlocks = 152 * 3;
+constexpr int64_t kRouteMaxPasses = 64;         // of a block, which adds its tokens in 32 bits; beyond, more blocks
 struct RouteTiles {
     int64_t blocks, per_block;
 };

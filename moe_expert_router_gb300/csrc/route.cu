@@ -39,10 +39,10 @@
 // own at the end of each sequence it meets (slot = block + sequence: consecutive
 // (block, sequence) pairs never share one); route_reduce_kernel adds the slots of a
 // sequence in a fixed order, so every output has the same bits on every call. They are held in
-// 32 bits: a thread adds no more than kPasses tokens in a row, a block's rows are added at the end
-// of such a run, and runs (and sequences, in the losses) with the rounding of each addition kept,
-// so that the error stays at some 2^-24 x 120 at worst however many tokens there are (added
-// one by one, 134 million of them were 8e-5 off).
+// 32 bits: a thread adds no more than 64 tokens in a row (a block has no more passes), a block
+// its rows at its end, and the slots, and the sequences in the losses, with the rounding of each
+// addition kept, so that the error stays at some 2^-24 x 120 at worst however many tokens there
+// are (with one block's tokens added one by one, 134 million of them were 8e-5 off).
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -180,6 +180,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {   // NaN where eith
     return y;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
 // A float's bits in the order of signed compares. -0 and 0 tie; NaN takes -inf's key, the
 // lowest, which an expert that is off has. Keys below kFirst are not chosen.
 __device__ __forceinline__ int order_key(float v) {
@@ -244,7 +250,6 @@ __device__ __forceinline__ void sort8(int (&k)[8]) {
 constexpr uint32_t kIndexBits = 0x1fffu;
 constexpr int kIndexMax = 1023;
 
-constexpr int kPasses = 64;                     // of a block, to a run
 // A sum with the roundings of its additions beside it.
 __device__ __forceinline__ void add_exact(float2 &sum, float v) {
     const float s = sum.x + v, b = s - sum.x;
@@ -554,7 +559,7 @@ __device__ __forceinline__ void search_groups(const RouteLaunch &p, const float 
             float a = -INFINITY, b = -INFINITY;      // the two best, a >= b
             for (int c = 0; c < n; ++c) {
                 const float v = row[part + per * i];
-                b = fmaxf(b, fminf(a, v));
+                b = fmaxf(b, min_nan(a, v));       // as in kept_groups
                 a = fmaxf(a, v);
                 i = i + 1 == n ? 0 : i + 1;
             }
@@ -595,7 +600,9 @@ __device__ __forceinline__ void search_groups(const RouteLaunch &p, const float 
     }
 }
 
-// The groups of one token that stay, as bits; v: the lane's selection scores (-inf: off; no NaN).
+// The groups of one token that stay, as bits; v: the lane's selection scores (-inf: off). NaN is as
+// good as off: in the second best it goes through a minimum that hands it on, into a maximum that
+// does not (a minimum without it would be the best, taken twice).
 // Where a group is a power of two of whole lanes (`group_lanes`, from the host) and is known
 // by its best one or two, those are found in registers. Else a group is searched in `sel_row`
 // by a power of two of lanes, each taking every so many of its experts. `near`: the groups
@@ -608,7 +615,7 @@ __device__ __forceinline__ unsigned kept_groups(const RouteLaunch &p, const floa
         float a = -INFINITY, b = -INFINITY;          // the two best, a >= b
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            b = fmaxf(b, fminf(a, vals[i]));
+            b = fmaxf(b, min_nan(a, vals[i]));
             a = fmaxf(a, vals[i]);
         }
         for (int off = 1; off < p.group_lanes; off <<= 1) {
@@ -667,8 +674,6 @@ route_kernel(const RouteLaunch p) {
     __shared__ int hist[kStats ? G * V : 1];
     __shared__ float red_z[kRows];
     __shared__ int red_n[kRows];
-    __shared__ float2 run_score[kStats ? G * V : 1], run_z;      // of the sequence's earlier runs in this block
-    __shared__ int run_n;
     griddep_wait();
     const int row = threadIdx.x / G, sub = threadIdx.x % G;
     const int lane = threadIdx.x & 31;
@@ -724,14 +729,7 @@ route_kernel(const RouteLaunch p) {
             if (kShared) own_sums[at<V>(i)] = 0.0f;
             else acc[kShared ? 0 : i] = 0.0f;
         }
-        for (int e = threadIdx.x; e < G * V; e += kThreads) {
-            hist[e] = 0;
-            run_score[e] = make_float2(0.0f, 0.0f);
-        }
-        if (threadIdx.x == 0) {
-            run_z = make_float2(0.0f, 0.0f);
-            run_n = 0;
-        }
+        for (int e = threadIdx.x; e < G * V; e += kThreads) hist[e] = 0;
         for (int b = 1; b < p.S; b += kThreads) {
             const int i = b + static_cast<int>(threadIdx.x);
             seq += __syncthreads_count(i < p.S && __ldg(p.seq_offsets + i) <= t_begin);
@@ -741,12 +739,9 @@ route_kernel(const RouteLaunch p) {
     int t = t_begin;
     while (t < t_end) {
         int seg_end = t_end;
-        bool last_run = true;                        // of the sequence in this block
         if constexpr (kStats) {
             while (seq < p.S - 1 && __ldg(p.seq_offsets + seq + 1) <= t) ++seq;
             if (seq < p.S - 1) seg_end = min(t_end, __ldg(p.seq_offsets + seq + 1));
-            last_run = seg_end - t <= kPasses * kRows;
-            if (!last_run) seg_end = t + kPasses * kRows;
         }
         for (int base = t; base < seg_end; base += kRows) {
             const int tok = base + row;
@@ -834,10 +829,7 @@ route_kernel(const RouteLaunch p) {
             if (grouped) {
                 float v[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    v[i] = best_only || l[i] == -INFINITY ? l[i] : s[i] + bias(i);
-                    v[i] = fmaxf(v[i], -INFINITY);   // NaN is as good as off: min and max would take the other value twice
-                }
+                for (int i = 0; i < V; ++i) v[i] = best_only || l[i] == -INFINITY ? l[i] : s[i] + bias(i);
                 const float n = static_cast<float>(p.group_topn);
                 kept = kept_groups<G, V>(p, v, own_row, reinterpret_cast<float *>(slots.group[row]), sub, gmask,
                                          best_only ? -1.0f : 2.0f * n * (rel * s_max + kUlp * (2.0f + n) * (s_max + bias_max)),
@@ -1026,8 +1018,8 @@ route_kernel(const RouteLaunch p) {
             }
 #pragma unroll
             for (int q = 0; q < kOwn; ++q) sv[q] = ev[q] >= 0 ? own_row[ev[q]] : 0.0f;
+            bool tied = false;                       // the last chosen and the first not chosen are a tie
             if (by_score) {
-                bool tied = false;                   // the last chosen and the first not chosen are a tie
 #pragma unroll
                 for (int q = 0; q < kOwn; ++q) {
                     // this slot's key against the next one's (the last one's: the first not chosen)
@@ -1045,9 +1037,13 @@ route_kernel(const RouteLaunch p) {
                         tied |= same && border;
                     }
                 }
+            }
+            // the vote is the whole warp's: it stands before any branch that a token takes alone
+            bool any_near = (__ballot_sync(0xffffffffu, near || tied || near_groups != 0) & gmask) != 0;
+            if (any_near && by_score && near_groups == 0) {
                 // behind a tie at the border stand experts that were compared with none: any of another
                 // logit or bias within the error of the tie's key
-                if ((__ballot_sync(0xffffffffu, tied) & gmask) != 0) {
+                if ((__ballot_sync(gmask, tied) & gmask) != 0) {
                     const int b = slots.idx[row][p.k];
                     const float x = key_value(slots.key[row][p.k]), bl = load_one(p.logits, p.dtype, lrow + b);
                     const float bb = __ldg(p.sel_bias + b), err = 2.0f * rel * s_max + kUlp * (4.0f * fabsf(x) + s_max);
@@ -1058,9 +1054,8 @@ route_kernel(const RouteLaunch p) {
                                 (!grouped || (kept >> ((e0 + at<V>(i)) / gs)) & 1u);
                     }
                 }
+                any_near = (__ballot_sync(gmask, near) & gmask) != 0;
             }
-            // the vote is the whole warp's: it stands before any branch that a token takes alone
-            const bool any_near = (__ballot_sync(0xffffffffu, near || near_groups != 0) & gmask) != 0;
             if (any_near) {
                 // candidates: no more than the error below the first key that was not chosen
                 unsigned cand = 0;
@@ -1110,7 +1105,7 @@ route_kernel(const RouteLaunch p) {
             __syncwarp();
         }
         if constexpr (kStats) {
-            // this block's sums of the run, rows in order, and with its last those of the sequence
+            // this block's sums of the sequence, rows in order
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -1131,11 +1126,7 @@ route_kernel(const RouteLaunch p) {
                 float v = 0.0f;
 #pragma unroll
                 for (int r = 0; r < kRows; ++r) v += buf[r * G * V + e];
-                float2 sum = run_score[e];
-                add_exact(sum, v);
-                run_score[e] = last_run ? make_float2(0.0f, 0.0f) : sum;
-                if (!last_run) continue;
-                p.part_score[slot * ld + e] = total_of(sum);
+                p.part_score[slot * ld + e] = v;
                 p.part_count[slot * ld + e] = hist[e];
                 hist[e] = 0;
             }
@@ -1146,15 +1137,8 @@ route_kernel(const RouteLaunch p) {
                     zz += red_z[r];
                     n += red_n[r];
                 }
-                float2 sum = run_z;
-                add_exact(sum, zz);
-                run_z = last_run ? make_float2(0.0f, 0.0f) : sum;
-                n += run_n;
-                run_n = last_run ? 0 : n;
-                if (last_run) {
-                    p.part_z[slot] = total_of(sum);
-                    p.part_n[slot] = n;
-                }
+                p.part_z[slot] = zz;
+                p.part_n[slot] = n;
             }
             __syncthreads();
         }
@@ -1192,13 +1176,14 @@ route_reduce_kernel(const RouteLaunch p) {
         const int a = q > 0 ? max(0, min(p.T, __ldg(p.seq_offsets + q))) : 0;
         const int z = q < p.S - 1 ? max(0, min(p.T, __ldg(p.seq_offsets + q + 1))) : p.T;
         const int b0 = a / p.per_block, b1 = z > a ? (z - 1) / p.per_block : b0 - 1;
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        float2 s4[4], z2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s4[i] = z2;
         int4 c = make_int4(0, 0, 0, 0);
-        float zs = 0.0f;
         int n = 0;
         for (int b = b0 + threadIdx.x; b <= b1; b += kReduceThreads) {
             n += __ldcg(p.part_n + b + q);
-            zs += __ldcg(p.part_z + b + q);
+            add_exact(z2, __ldcg(p.part_z + b + q));
         }
         if (e4 < ld) {
             for (int b = b0 + row; b <= b1; b += kRows * kBatch) {
@@ -1216,10 +1201,10 @@ route_reduce_kernel(const RouteLaunch p) {
                 }
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j) {
-                    s.x += sv[j].x;
-                    s.y += sv[j].y;
-                    s.z += sv[j].z;
-                    s.w += sv[j].w;
+                    add_exact(s4[0], sv[j].x);
+                    add_exact(s4[1], sv[j].y);
+                    add_exact(s4[2], sv[j].z);
+                    add_exact(s4[3], sv[j].w);
                     c.x += cv[j].x;
                     c.y += cv[j].y;
                     c.z += cv[j].z;
@@ -1227,6 +1212,8 @@ route_reduce_kernel(const RouteLaunch p) {
                 }
             }
         }
+        float4 s = make_float4(total_of(s4[0]), total_of(s4[1]), total_of(s4[2]), total_of(s4[3]));
+        float zs = total_of(z2);
         // the warp's four rows, then the warps in order
 #pragma unroll
         for (int off = 8; off <= 16; off <<= 1) {
@@ -1439,8 +1426,9 @@ route_backward_kernel(const RouteBackwardLaunch p) {
 #pragma unroll
                 for (int i = 0; i < V / 4; ++i) *fours(s_row, i) = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
             } else {
-                // the scores go to s_row; s[] keeps their derivative s (1 - s). Where s is near 1, 1 - s is exp(-l) s:
-                // subtracted, it would keep s's last digit only (6 % off at l = 16, nothing from 17 on).
+                // the scores go to s_row; s[] keeps their derivative s (1 - s). 1 - s is exp(-l) s: subtracted, it
+                // would keep s's last digit only (6 % off at l = 16, nothing from 17 on). Where exp(-l) is infinite
+                // and s 0, that product is NaN, of which the minimum makes 1.
 #pragma unroll
                 for (int i = 0; i < V / 4; ++i) {
                     float four[4];
@@ -1452,7 +1440,7 @@ route_backward_kernel(const RouteBackwardLaunch p) {
                         four[j] = rcp_fast(1.0f + e);
                         Z += four[j];
                         if (terms) sum += four[j] * a(c);
-                        s[c] = four[j] * (e < 1.0f ? e * four[j] : 1.0f - four[j]);
+                        s[c] = four[j] * fminf(e * four[j], 1.0f);
                     }
                     *fours(s_row, i) = make_float4(four[0], four[1], four[2], four[3]);
                 }
@@ -1669,7 +1657,8 @@ int rows_of(int E) { return E <= 64 ? 32 : E <= 128 ? 16 : E <= 512 ? 8 : 4; }
 RouteTiles route_tiles(int64_t T, int64_t E) {
     const int64_t rows = rows_of(static_cast<int>(E));
     const int64_t passes = (T + rows - 1) / rows;
-    const int64_t each = (passes + kRouteMaxBlocks - 1) / kRouteMaxBlocks;
+    int64_t each = (passes + kRouteMaxBlocks - 1) / kRouteMaxBlocks;
+    if (each > kRouteMaxPasses) each = kRouteMaxPasses;
     RouteTiles r;
     r.per_block = each * rows;
     r.blocks = (passes + each - 1) / each;
