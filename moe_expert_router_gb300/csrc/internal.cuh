@@ -374,7 +374,11 @@ bool encode_bf16_2d_strided(CUtensorMap *map, const void *base, uint64_t inner, 
 // The trainable router (route.cu). Tokens are dealt to blocks of per_block
 // consecutive ones; a (block, sequence) pair has slot block + sequence, of
 // blocks + S - 1.
-constexpr int64_t kRouteMaxBlocks = 152 * 3;
+// One wave of resident blocks: three an SM where a lane has up to eight experts, two where it
+// has more (their registers). Of forward and backward, three against two: 200 experts, 32768 tokens
+// 53 + 28 us against 60 + 34; 512 experts, 8192 tokens 42 + 17 against 33 + 16; 600 experts,
+// 32768 tokens 214 + 129 against 173 + 105. (The backward of few experts has room for four.)
+constexpr int64_t route_max_blocks(int64_t E) { return 152 * (E <= 256 ? 3 : 2); }
 constexpr int64_t kRouteMaxPasses = 64;         // of a block, which adds its tokens in 32 bits; beyond, more blocks
 struct RouteTiles {
     int64_t blocks, per_block;

@@ -1657,7 +1657,7 @@ int rows_of(int E) { return E <= 64 ? 32 : E <= 128 ? 16 : E <= 512 ? 8 : 4; }
 RouteTiles route_tiles(int64_t T, int64_t E) {
     const int64_t rows = rows_of(static_cast<int>(E));
     const int64_t passes = (T + rows - 1) / rows;
-    int64_t each = (passes + kRouteMaxBlocks - 1) / kRouteMaxBlocks;
+    int64_t each = (passes + route_max_blocks(E) - 1) / route_max_blocks(E);
     if (each > kRouteMaxPasses) each = kRouteMaxPasses;
     RouteTiles r;
     r.per_block = each * rows;
