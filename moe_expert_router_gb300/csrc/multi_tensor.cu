@@ -105,8 +105,9 @@ __device__ __forceinline__ void store_elem(void *p, int dtype, int64_t i, float 
     else static_cast<unsigned short *>(p)[i] = static_cast<unsigned short>(narrow(v, dtype));
 }
 
-// Running value of the norm. Squares are added in fp32 over 64 elements and folded
-// into 64 bits; where those 64 left fp32's comfortable range (all below 1e-12, or
+// Running value of the norm. Squares are added in fp32 over 64 elements (in four chains:
+// 18 roundings at most, which the root halves) and folded into 64 bits: all in 64 bits,
+// 1.25 TFLOP/s would hold the norm to a fifth of what memory gives. Where those 64 left fp32's comfortable range (all below 1e-12, or
 // some above 1e15) they are added again, scaled by a power of two.
 template <int kType>
 struct Sum {
@@ -148,10 +149,21 @@ struct Sum {
     }
 };
 
+// The norm from its sum.
+template <int kType>
+__device__ __forceinline__ float finish(double v) {
+    if (kType != MOE_NORM_2) return static_cast<float>(v);
+    if (!(v > 1e-30 && v < 1e38)) return static_cast<float>(sqrt(v));
+    // the root in 32 bits, and one step towards that of the 64-bit sum: rounded once, not two and a half
+    // times, since clipping multiplies everything by it
+    const float r = sqrtf(static_cast<float>(v));
+    return r + static_cast<float>(fma(-static_cast<double>(r), static_cast<double>(r), v)) * (0.5f / r);
+}
+
 // The block's sum or maximum, in every thread. One warp adds, from shared memory: a 64-bit
 // addition takes a warp some 60 cycles, and eight warps that reduce each their own and then
-// all the same eight values wait 3 us for them.
-template <int kType>
+// all the same eight values wait 3 us for them. kFinish: the norm from them.
+template <int kType, bool kFinish>
 __device__ __forceinline__ double block_value(const Sum<kType> &s) {
     __shared__ double part[kThreads];
     __shared__ double value;
@@ -168,7 +180,7 @@ __device__ __forceinline__ double block_value(const Sum<kType> &s) {
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) t.acc += __shfl_xor_sync(0xffffffffu, t.acc, off);
         }
-        if (threadIdx.x == 0) value = t.get();
+        if (threadIdx.x == 0) value = kFinish ? static_cast<double>(finish<kType>(t.get())) : t.get();
     }
     __syncthreads();
     return value;
@@ -234,15 +246,8 @@ norm_kernel(const __grid_constant__ Table<N> tab, double *__restrict__ part, int
     if (step != nullptr && blockIdx.x == 0 && threadIdx.x == 0) ++*step;   // AdamW's, which comes next
     Sum<kType> sum;
     sum_runs<kType>(tab, sum);
-    const double v = block_value<kType>(sum);
+    const double v = block_value<kType, false>(sum);
     if (threadIdx.x == 0) part[blockIdx.x] = v;
-}
-
-template <int kType>
-__device__ __forceinline__ float finish(double v) {
-    if (kType != MOE_NORM_2) return static_cast<float>(v);
-    // the root in 32 bits (1.5 roundings) wherever the sum is in its range
-    return v > 1e-30 && v < 1e38 ? sqrtf(static_cast<float>(v)) : static_cast<float>(sqrt(v));
 }
 
 // The norm from the blocks' values, in order; the same in every block that asks.
@@ -250,7 +255,7 @@ template <int kType>
 __device__ __forceinline__ float total_norm(const double *__restrict__ part, int n) {
     Sum<kType> s;
     for (int i = threadIdx.x; i < n; i += kThreads) s.join(__ldcg(part + i));
-    return finish<kType>(block_value<kType>(s));
+    return static_cast<float>(block_value<kType, true>(s));
 }
 
 // max_norm / (norm + 1e-6), at most 1; NaN stays NaN
@@ -324,9 +329,12 @@ clip_kernel(const __grid_constant__ Table<N> tab, const double *__restrict__ par
 }
 
 // A short list of no more than kSmall units in one launch: a cluster of eight blocks, which
-// exchange their sums through shared memory. Two launches wait for each other some 3 us, and
-// cost the host as much again: 0.2 M elements in three tensors take 14.8 us a call as two
-// launches and 11.0 as one, although eight SMs need 9 us for what 50 do in 8.
+// exchange their sums through shared memory. It saves the host a launch, for which eight SMs take
+// longer than fifty. Three bf16 tensors clipped, us a call one after another (us on the device),
+// one launch against two: 30 K elements 9.3 (5.2), 10.9 (7.1); 0.2 M 9.5 (9.4), 11.0 (7.3); 0.3 M,
+// 38 K units, 10.4 (10.4), 11.2 (7.1); 0.4 M, 51 K units, 12.6 (12.5), 11.0 (7.9). fp32, with half
+// the elements to a unit, and the norm alone take less on the device, and one launch pays up to
+// 300 K units. (In a replayed graph, where the device alone counts, two pay from 0.1 M on.)
 constexpr int kCluster = 8;
 constexpr int64_t kSmall = 32768;
 
@@ -339,7 +347,7 @@ small_kernel(const __grid_constant__ Table<kShort> tab, float max_norm, float *_
     __shared__ double mine;
     Sum<kType> sum;
     sum_runs<kType>(tab, sum);
-    const double v = block_value<kType>(sum);
+    const double v = block_value<kType, false>(sum);
     if (threadIdx.x == 0) mine = v;
     cluster.sync();
     __shared__ float norm_shared;
