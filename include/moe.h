@@ -373,14 +373,17 @@ moe_status_t moe_bias_update(float *bias, const int32_t *counts, int64_t L, int6
 moe_status_t moe_tensors_workspace_size(int32_t n, size_t *bytes);
 
 /* norm[0] (fp32, device) = the norm of all elements of all tensors together.
- * Sums are held in fp64, so no value of the types over- or underflows in them;
+ * A thread adds up to 64 squares (absolute values) in fp32, scaled where they leave
+ * its range, and everything else is added in fp64: a relative error of 1e-6 at
+ * worst, as a rule one rounding, and no value of the types over- or underflows.
  * NaN and infinity propagate. The same bits on every call. */
 moe_status_t moe_grad_norm(const void *const *grads, const int64_t *numel, const int32_t *dtype, int32_t n,
                            int32_t norm_type, float *norm, void *ws, size_t ws_bytes, void *stream);
 
 /* The same norm, and every element of every tensor times
  * min(1, max_norm / (norm + 1e-6)), in place (rounded once to its type;
- * untouched where the factor is 1). max_norm >= 0 (0: all become 0). A NaN norm makes every
+ * untouched where the factor is 1). The norm is that of this call's list: a bound
+ * over several lists needs one call over all of them. max_norm >= 0 (0: all become 0). A NaN norm makes every
  * element NaN and an infinite one every finite element 0. */
 moe_status_t moe_clip_grads(void *const *grads, const int64_t *numel, const int32_t *dtype, int32_t n,
                             int32_t norm_type, float max_norm, float *norm, void *ws, size_t ws_bytes,
@@ -390,7 +393,7 @@ typedef struct moe_adamw_cfg {
     double beta1, beta2;     /* in [0, 1); 1 - beta is taken in fp64 and then rounded */
     float eps;               /* >= 0 */
     float weight_decay;
-    float max_norm;          /* clip by the gradients' global 2-norm; 0: no clipping */
+    float max_norm;          /* clip by the 2-norm of all this call's gradients; 0: no clipping */
     int32_t skip_nonfinite;  /* 1: where that norm is not finite, change nothing and do not count the step */
     const int32_t *missed;   /* int32 [n] on the device: the steps that each parameter had no part in, or NULL */
 } moe_adamw_cfg_t;

@@ -6,7 +6,8 @@ by torch's own optimizers: a backward through weights that a step has changed is
 them again. A replayed graph moves no counter: call the cache's `invalidate()` beside it.
 
 Every call takes whole lists of tensors (fp32, bf16, fp16, mixed; any sizes), enqueues
-two or three kernels on the current stream and reads nothing back: the norm, the clip
+one or two kernels on the current stream (more for a list of many hundred tensors) and
+reads nothing back: the norm, the clip
 factor, the learning rate and the step count stay on the device, so a step can be
 captured into a CUDA graph and replayed.
 """
@@ -66,7 +67,9 @@ class AdamW:
     `step(grads=None, max_norm=0.0)` uses the parameters' .grad where no list is given; parameters
     without a gradient are left alone, and their bias corrections go by the steps that they took
     part in: `step_count` less their `missed`. Those and `lr` are device tensors: write into `lr`
-    for a schedule. Masters are copies made here (`refresh_masters`)."""
+    for a schedule. `max_norm` bounds the norm of this step's gradients: parameters that are to be
+    clipped together belong to one AdamW. What a checkpoint has to hold are `exp_avg`, `exp_avg_sq`,
+    `masters`, `step_count`, `missed` and `lr`: copy into them (there is no state_dict). Masters are copies made here (`refresh_masters`)."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, masters=True,
                  skip_nonfinite=False):
@@ -76,7 +79,6 @@ class AdamW:
         self.lr = torch.full((1,), lr, dtype=torch.float32, device=device)
         self.step_count = torch.zeros((1,), dtype=torch.int32, device=device)
         self.missed = torch.zeros((len(self.params),), dtype=torch.int32, device=device)
-        self._any_missed = False
         self.exp_avg = [torch.zeros_like(p, dtype=torch.float32) for p in self.params]
         self.exp_avg_sq = [torch.zeros_like(p, dtype=torch.float32) for p in self.params]
         self.masters = [p.detach().float() if masters and p.dtype != torch.float32 else None for p in self.params]
@@ -97,17 +99,13 @@ class AdamW:
         if not at:
             return None
         part = len(at) < len(grads)
-        missed = None
-        # a captured step reads the counts as they are when it is replayed
-        if self._any_missed or (self.params[0].is_cuda and torch.cuda.is_current_stream_capturing()):
-            missed = torch.cat([self.missed[i:i + 1] for i in at]) if part else self.missed
+        missed = torch.cat([self.missed[i:i + 1] for i in at]) if part else self.missed
         before = self.step_count.clone() if part else None
         norm = adamw_step([self.params[i] for i in at], [grads[i] for i in at],
                           [self.exp_avg[i] for i in at], [self.exp_avg_sq[i] for i in at], self.step_count, self.lr,
                           [self.masters[i] for i in at], self.betas, self.eps, self.weight_decay, max_norm,
                           self.skip_nonfinite, missed)
         if part:
-            self._any_missed = True
             taken = self.step_count - before             # 0 where the step was skipped
             for i, g in enumerate(grads):
                 if g is None:

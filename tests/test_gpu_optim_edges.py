@@ -179,3 +179,21 @@ def test_lists_that_share_memory_are_refused():
     optim.adamw_step(cut[:2], cut[2:4], cut[4:6], cut[6:8], step, lr, masters=[cut[8], cut[9]])
     optim.adamw_step(cut[:2], [g[0], g[0]], cut[4:6], cut[6:8], step, lr, masters=[None, cut[9]])   # a gradient read twice
     assert step.item() == 2
+
+
+def test_a_restored_optimizer_goes_on():
+    """Everything that a checkpoint holds, copied into a new AdamW: the next steps are the same."""
+    start = [randn(300, seed=1).bfloat16(), randn(70, seed=2)]
+    a = optim.AdamW([s.clone() for s in start], lr=0.01)
+    for t in range(5):
+        a.step([randn(300, seed=10 + t).bfloat16(), randn(70, seed=20 + t) if t > 2 else None], 1.0)
+    b = optim.AdamW([p.clone() for p in a.params], lr=0.5)
+    for x, y in ((a.exp_avg, b.exp_avg), (a.exp_avg_sq, b.exp_avg_sq), (a.masters, b.masters), ([a.step_count], [b.step_count]),
+                 ([a.missed], [b.missed]), ([a.lr], [b.lr])):
+        [v.copy_(u) for u, v in zip(x, y) if u is not None]
+    for t in range(3):
+        g = [randn(300, seed=30 + t).bfloat16(), randn(70, seed=40 + t)]
+        a.step(g, 1.0)
+        b.step(g, 1.0)
+    assert all(torch.equal(x, y) for x, y in zip(a.params, b.params))
+    assert a.missed.tolist() == [0, 3] and a.step_count.item() == 8
