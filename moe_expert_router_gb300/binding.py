@@ -497,7 +497,10 @@ def _raw_stream(stream, like):
     """A stream's handle as a number; the current one's of the tensor's device for None."""
     if stream is not None:
         return stream.cuda_stream
-    device = like.get_device()
+    try:
+        device = like.get_device()
+    except AttributeError:
+        raise TypeError(f"expected a torch tensor, not {type(like).__name__}") from None
     return torch._C._cuda_getCurrentRawStream(device) if device >= 0 else 0
 
 

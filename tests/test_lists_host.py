@@ -29,6 +29,14 @@ def test_adamw_configuration(lib):
         assert adamw(**kw) == 1, kw
 
 
+def test_numbers_in_place_of_tensors_are_refused():
+    x = [torch.zeros((3,))]
+    for f in (lambda: B.moe_adamw(x, x, x, x, 0.1, x[0], x[0], B.AdamWCfg()), lambda: B.moe_grad_norm(x, 0.0, x[0]),
+              lambda: B.moe_bias_update([0.0], x[0], 0.1), lambda: B.moe_route([[0.0]], B.router_cfg(), x[0], x[0])):
+        with pytest.raises(TypeError, match="torch tensor"):
+            f()
+
+
 class NoStream:
     cuda_stream = 0
 
