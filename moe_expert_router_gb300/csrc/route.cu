@@ -30,9 +30,9 @@
 // there cost such a token 20 us.
 //
 // Bound by instructions, not by memory: 131072 tokens of 128 bf16 experts (34 MB, 5 us of
-// HBM) take 58 us at 340 warp instructions a token and 0.62 issued a cycle, with 24 warps
-// an SM; their backward (67 MB) 40 us at 220. At 8192 tokens of 256 experts in groups (24
-// us, 11 us for the backward) the latency of a block's three passes is what is left.
+// HBM) take 58 us at 335 warp instructions a token and 0.61 issued a cycle, with 24 warps
+// an SM; their backward (67 MB) 39 us at 238. At 8192 tokens of 256 experts in groups (22
+// us, 11.5 us for the backward) the latency of a block's three passes is what is left.
 //
 // Statistics are sums without float atomics: a block keeps its tokens' score sums
 // in registers and its counts in shared memory, and writes them to a slot of its
