@@ -568,7 +568,8 @@ def moe_clip_grads(grads, max_norm, norm, ws, norm_type=2.0, stream=None):
                                                   _raw_stream(stream, norm)))
 
 
-def moe_adamw(params, grads, exp_avg, exp_avg_sq, lr, step, ws, cfg, masters=None, norm=None, missed=None, stream=None):
+def moe_adamw(params, grads, exp_avg, exp_avg_sq, lr, step, ws, cfg, masters=None, norm=None, stream=None,
+              missed=None):
     """One AdamW step over lists of tensors, in place; masters: a list with an fp32 tensor or None
     for each parameter, or None; missed: int32, the steps that each parameter had no part in, or
     None (it takes the place of cfg.missed)."""
