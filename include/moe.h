@@ -295,8 +295,8 @@ moe_status_t moe_route_workspace_size(const moe_route_shape_t *shape, size_t *by
  *   token t is live when token_mask[t] != 0 and not all its experts are off
  *   s      = softmax(l[t,:]) or sigmoid(l[t,:])
  *   key    = l without sel_bias (or where it is 0 for every expert), else
- *            s + sel_bias (a sel_bias of -inf keeps an
- *            expert from being chosen, and out of its group's sum)
+ *            s + sel_bias (a sel_bias of -inf or NaN keeps an expert from being
+ *            chosen, and out of its group's sum)
  *   groups = (n_group > 1) keep the topk_group groups with the largest sum of
  *            their group_topn best s + sel_bias
  *   topk_idx = the k experts of the kept groups with the largest key, best
@@ -314,10 +314,9 @@ moe_status_t moe_route_workspace_size(const moe_route_shape_t *shape, size_t *by
  * (with sigmoid scores the shares are normalised, so that lowering every score
  * does not lower the balance term). The order of experts, and of groups, whose
  * keys are nearer than fp32 resolves is decided in fp64 (scores below its range
- * are 0 there, and tie). A NaN logit of a live
- * token is never chosen, counts for no group, and makes the losses NaN (a NaN
- * in sel_bias keeps its expert out like one of -inf); with softmax it makes that
- * token's weights NaN too, or, with sel_bias, leaves its slots over.
+ * are 0 there, and tie). A NaN logit of a live token is never chosen, counts for
+ * no group, and makes the losses NaN; with softmax it makes that token's weights
+ * NaN too, or, with sel_bias, leaves its slots over.
  * Values in rows whose mask is 0 reach no output.
  *
  * logits [T,E] with rows ld apart, dtype-aligned; sel_bias fp32 [E] or NULL;
@@ -339,9 +338,9 @@ moe_status_t moe_route(const void *logits, const float *sel_bias, const uint8_t 
  * dlogits [T,E], dense, of the logits' type, fully written (0 for experts that
  * are off and tokens that are not live). The selection and the counts carry no
  * gradient. dtopk_w fp32 [T,k] (whatever it holds at slots left over reaches
- * nothing); dlosses fp32 [2] on the device, or NULL where
- * the losses are not used (counts, seq_tokens and seq_offsets are then not
- * read). topk_idx, counts and seq_tokens are moe_route's.
+ * nothing); dlosses fp32 [2] on the device, or NULL where the losses are not used
+ * (counts, seq_tokens and seq_offsets are then not read). topk_idx, counts and
+ * seq_tokens are moe_route's.
  */
 moe_status_t moe_route_backward(const void *logits, const uint8_t *token_mask, const int32_t *seq_offsets,
                                 const moe_route_shape_t *shape, const moe_router_cfg_t *cfg,
@@ -383,8 +382,9 @@ moe_status_t moe_grad_norm(const void *const *grads, const int64_t *numel, const
 /* The same norm, and every element of every tensor times
  * min(1, max_norm / (norm + 1e-6)), in place (rounded once to its type;
  * untouched where the factor is 1). The norm is that of this call's list: a bound
- * over several lists needs one call over all of them. max_norm >= 0 (0: all become 0). A NaN norm makes every
- * element NaN and an infinite one every finite element 0. */
+ * over several lists needs one call over all of them. max_norm >= 0 (0: all
+ * become 0). A NaN norm makes every element NaN and an infinite one every finite
+ * element 0. */
 moe_status_t moe_clip_grads(void *const *grads, const int64_t *numel, const int32_t *dtype, int32_t n,
                             int32_t norm_type, float max_norm, float *norm, void *ws, size_t ws_bytes,
                             void *stream);
