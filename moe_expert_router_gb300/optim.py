@@ -56,7 +56,7 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr, masters=None, betas
     if not (max_norm > 0.0 or skip_nonfinite):
         norm = None
     cfg = B.AdamWCfg(betas[0], betas[1], eps, weight_decay, max_norm, int(bool(skip_nonfinite)))
-    B.moe_adamw(params, grads, exp_avg, exp_avg_sq, lr, step, ws, cfg, masters, norm, missed)
+    B.moe_adamw(params, grads, exp_avg, exp_avg_sq, lr, step, ws, cfg, masters, norm, missed=missed)
     return norm
 
 
