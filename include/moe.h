@@ -56,6 +56,7 @@ typedef enum moe_status {
 #define MOE_DEVERR_BAD_EXPERT_INDEX 0x1  /* a topk_idx entry outside [0, E): that slot was dropped */
 #define MOE_DEVERR_WAIT_TIMEOUT     0x2  /* a pipeline wait ran out of time: outputs are invalid */
 #define MOE_DEVERR_CAPACITY         0x4  /* expert parallelism: a routed row beyond a block's capacity was dropped */
+#define MOE_DEVERR_BAD_OFFSETS      0x8  /* group offsets that decrease or leave [0, R]: no group was computed */
 
 typedef struct moe_shape {
     int64_t T;   /* tokens */
@@ -356,6 +357,114 @@ moe_status_t moe_route_backward(const void *logits, const uint8_t *token_mask, c
  */
 moe_status_t moe_bias_update(float *bias, const int32_t *counts, int64_t L, int64_t S, int64_t E, float rate,
                              void *stream);
+
+/* ------------------------------------------------------------------ the norm in front of the layer
+ *
+ * The residual stream takes a branch's output, and its root-mean-square norm goes into the
+ * router and the experts:
+ *   h = x + residual (rounded to their type; h = x without a residual)
+ *   rstd[t] = 1 / sqrt(mean_c h[t,c]^2 + eps);   y[t,c] = h[t,c] rstd[t] weight[c]
+ *   codes, scales = moe_mx_quantize of y
+ * y is the exact value rounded once, whatever T and H (with squares whose sum is within
+ * fp32's range); the same bits on every call.
+ *
+ * x, residual, h and y are of one type (dtype); weight is of that type or fp32. Rows of x
+ * and residual may lie apart; h, y and codes are dense [T,H]. Any H <= 16384; whole 16-byte
+ * vectors (all addresses, H and both ld) are the fast case. H is a multiple of 128 where
+ * codes and scales (both or neither, 16-byte aligned; words [H/128][T rounded up to 4]) are
+ * asked for. h is NULL or given where a residual is (NULL: the sum is not kept), and may be
+ * x's or residual's own memory where those are dense; so may y, where h is not stored there.
+ * y may be NULL where codes are given. rstd fp32 [T] or NULL is for the backward.
+ */
+typedef struct moe_norm_shape {
+    int64_t T;        /* rows */
+    int64_t H;        /* columns */
+    int64_t ld_x;     /* elements from a row of x to the next one, >= H (the backward: of h) */
+    int64_t ld_r;     /* the same of residual */
+    double eps;       /* >= 1e-30 */
+    int32_t dtype;    /* MOE_DTYPE_*, of x, residual, h and y */
+    int32_t w_dtype;  /* of weight: dtype or MOE_DTYPE_F32 */
+} moe_norm_shape_t;
+
+moe_status_t moe_rms_norm(const void *x, const void *residual, const void *weight, const moe_norm_shape_t *shape,
+                          void *h, void *y, float *rstd, void *codes, void *scales, void *stream);
+
+/* Bytes of workspace that moe_rms_norm_backward needs. Host-only. */
+moe_status_t moe_rms_norm_workspace_size(int64_t T, int64_t H, size_t *bytes);
+
+/*
+ * The norm's gradients: with z = h rstd and g = dy weight,
+ *   dx = rstd (g - z mean_c(g z)) + dh     (of x and of residual alike)
+ *   dweight[c] = sum_t dy[t,c] z[t,c]
+ * dy, dh, dx [T,H] dense, of dtype; dh is the gradient that reaches h by the stream itself,
+ * or NULL; dx may be dy's or dh's memory. h and rstd are moe_rms_norm's (h is x where there
+ * was no residual; rows ld_x apart). dweight [H] of w_dtype, fully written (0 for T = 0).
+ * The same bits on every call. ws: moe_rms_norm_workspace_size bytes, 16-byte aligned, not
+ * initialised.
+ */
+moe_status_t moe_rms_norm_backward(const void *dy, const void *dh, const void *h, const void *weight, const float *rstd,
+                                   const moe_norm_shape_t *shape, void *dx, void *dweight, void *ws, size_t ws_bytes,
+                                   void *stream);
+
+/* ------------------------------------------------------------------ products grouped by expert
+ *
+ * The products of the two stages on their own, for experts of another form (another
+ * activation, one matrix, one without a gate): rows that lie group by group, as
+ * moe_dispatch_rows writes them, each times its group's matrix.
+ *
+ * offsets int32 [G+1] on the device: group g has the rows offsets[g] .. offsets[g+1]-1
+ * (none, where the two are equal). Offsets do not decrease and stay in [0, R]; where they
+ * do not, no group is computed and MOE_DEVERR_BAD_OFFSETS is set in ws. Rows outside every
+ * group are not read as rows of a product (they may hold anything, NaN too), and out's are
+ * left as they were. Operands are bf16 or fp16, added in fp32 and rounded once. Limits: K
+ * and N multiples of 8, G <= 1024, R < 2^31 - 256, rows of x, out, a and b 16-byte aligned
+ * (ld multiples of 8), matrices dense. out and dw share no memory with any operand.
+ * The same bits on every call.
+ *
+ * ws: moe_grouped_workspace_size bytes, 256-byte aligned, its first 256 bytes zeroed once
+ * (moe_workspace_init); calls that share it are ordered on one stream.
+ */
+typedef struct moe_grouped_shape {
+    int64_t R;      /* rows of x and out */
+    int64_t G;      /* groups */
+    int64_t K;      /* columns of x */
+    int64_t N;      /* columns of out */
+    int64_t ld_x;   /* elements from a row of x to the next one, >= K */
+    int64_t ld_out; /* the same of out, >= N */
+    int32_t dtype;  /* MOE_DTYPE_BF16 or MOE_DTYPE_F16, of every operand */
+    int32_t flags;  /* 0 or MOE_GROUPED_W_KN */
+} moe_grouped_shape_t;
+
+/* moe_grouped_shape_t.flags: w is [G,K,N] (input by output), not [G,N,K]. */
+#define MOE_GROUPED_W_KN 0x1
+
+moe_status_t moe_grouped_workspace_size(int64_t G, size_t *bytes);
+
+/*
+ * out[r,:] = x[r,:] . w[g]^T for every row r of every group g, with w [G,N,K] as the expert
+ * weights lie, or x[r,:] . w[g] with w [G,K,N] (MOE_GROUPED_W_KN). The gradient of x is this
+ * call on the gradient of out with the other flag: dx[r,:] = dy[r,:] . w[g].
+ */
+moe_status_t moe_grouped_mm(const void *x, const void *w, const int32_t *offsets, const moe_grouped_shape_t *shape,
+                            void *out, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The gradient of the matrices: dw[g] = sum over g's rows of a[r,:]^T b[r,:], dw [G,N,K] with
+ * a [R,N] (rows ld_out apart) the gradient of out and b [R,K] (rows ld_x apart) the x of
+ * moe_grouped_mm; for w [G,K,N], a is x and b the gradient. Every group is written, one
+ * without rows with zeros. flags is 0.
+ */
+moe_status_t moe_grouped_wgrad(const void *a, const void *b, const int32_t *offsets, const moe_grouped_shape_t *shape,
+                               void *dw, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * moe_grouped_mm with w [G,N,K] on MXFP8 operands (the format of moe_mx_quantize): x_codes
+ * [R,K] with x_scales words [K/128][R rounded up to 4], w_codes [G,N,K] with w_scales words
+ * [K/128][G*N]; out bf16. K is a multiple of 128, ld_x = K, dtype MOE_DTYPE_BF16, flags 0.
+ */
+moe_status_t moe_grouped_mm_mx(const void *x_codes, const void *x_scales, const void *w_codes, const void *w_scales,
+                               const int32_t *offsets, const moe_grouped_shape_t *shape, void *out, void *ws,
+                               size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------ the optimizer's end of a step
  *
@@ -701,6 +810,20 @@ moe_status_t moe_forward_mx(const void *x, const int32_t *topk_idx, const float 
                             const void *w1_codes, const void *w1_scales, const void *w2_codes,
                             const void *w2_scales, const moe_shape_t *shape, void *y, void *ws,
                             size_t ws_bytes, void *stream);
+
+/*
+ * The same from tokens that are quantized already, as moe_rms_norm writes them: x_codes
+ * [T,H] and x_scales words [H/128][T rounded up to 4] in token order. moe_mx_dispatch copies
+ * them into routed order in the workspace (in the place of moe_mx_quantize_dispatch), and
+ * moe_forward_mx_codes is moe_forward_mx with it: the same bits as from the bf16 x that the
+ * codes were made of.
+ */
+moe_status_t moe_mx_dispatch(const void *x_codes, const void *x_scales, const moe_shape_t *shape, void *ws,
+                             size_t ws_bytes, void *stream);
+moe_status_t moe_forward_mx_codes(const void *x_codes, const void *x_scales, const int32_t *topk_idx,
+                                  const float *topk_w, const void *w1_codes, const void *w1_scales,
+                                  const void *w2_codes, const void *w2_scales, const moe_shape_t *shape, void *y,
+                                  void *ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------ MXFP8 training
  *

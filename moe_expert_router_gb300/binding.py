@@ -23,12 +23,14 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
 DEVERR_BAD_EXPERT_INDEX = 0x1
 DEVERR_WAIT_TIMEOUT = 0x2
 DEVERR_CAPACITY = 0x4
+DEVERR_BAD_OFFSETS = 0x8
 SCORE_SOFTMAX = 0
 SCORE_SIGMOID = 1
 SHAPE_TRAINING = 0x1
 SHAPE_MXFP8 = 0x2
 SHAPE_PACKED_WEIGHTS = 0x4
 DTYPE_CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+NORM_MAX_H = 16384
 NORM_CODES = {float("inf"): 0, 1.0: 1, 2.0: 2}
 
 
@@ -52,6 +54,17 @@ class RouterCfg(ctypes.Structure):
 class RouteShape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("E", ctypes.c_int64), ("S", ctypes.c_int64), ("ld", ctypes.c_int64),
                 ("k", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("ld_x", ctypes.c_int64), ("ld_r", ctypes.c_int64),
+                ("eps", ctypes.c_double), ("dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32)]
+
+
+class GroupedShape(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int64), ("G", ctypes.c_int64), ("K", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("ld_x", ctypes.c_int64), ("ld_out", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("flags", ctypes.c_int32)]
 
 
 class AdamWCfg(ctypes.Structure):
@@ -125,6 +138,15 @@ _SIG = {
     "moe_clip_grads": [_P, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_float, _P, _P, ctypes.c_size_t, _P],
     "moe_adamw": [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int32, ctypes.POINTER(AdamWCfg), _P, _P, _P, _P,
                   ctypes.c_size_t, _P],
+    "moe_mx_dispatch": [_P, _P, ctypes.POINTER(Shape), _P, ctypes.c_size_t, _P],
+    "moe_forward_mx_codes": [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(Shape), _P, _P, ctypes.c_size_t, _P],
+    "moe_rms_norm": [_P, _P, _P, ctypes.POINTER(NormShape), _P, _P, _P, _P, _P, _P],
+    "moe_rms_norm_workspace_size": [ctypes.c_int64, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_rms_norm_backward": [_P, _P, _P, _P, _P, ctypes.POINTER(NormShape), _P, _P, _P, ctypes.c_size_t, _P],
+    "moe_grouped_workspace_size": [ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_grouped_mm": [_P, _P, _P, ctypes.POINTER(GroupedShape), _P, _P, ctypes.c_size_t, _P],
+    "moe_grouped_wgrad": [_P, _P, _P, ctypes.POINTER(GroupedShape), _P, _P, ctypes.c_size_t, _P],
+    "moe_grouped_mm_mx": [_P, _P, _P, _P, _P, ctypes.POINTER(GroupedShape), _P, _P, ctypes.c_size_t, _P],
     "moe_get_device_error": [_P, ctypes.POINTER(ctypes.c_int32), _P],
     "moe_status_string": [ctypes.c_int],
     "moe_kernel_launch_count": [],
@@ -392,6 +414,19 @@ def moe_forward_mx(x, topk_idx, topk_w, w1q, w1s, w2q, w2s, shp, y, ws, stream=N
         ctypes.byref(shp), _ptr(y), _ptr(ws), _nbytes(ws), _stream(stream, ws)))
 
 
+def moe_mx_dispatch(x_codes, x_scales, shp, ws, stream=None):
+    """The MXFP8 dispatch of tokens that are quantized already (moe_rms_norm's codes and scales)."""
+    _check("moe_mx_dispatch", load().moe_mx_dispatch(
+        _ptr(x_codes), _ptr(x_scales), ctypes.byref(shp), _ptr(ws), _nbytes(ws), _stream(stream, ws)))
+
+
+def moe_forward_mx_codes(x_codes, x_scales, topk_idx, topk_w, w1q, w1s, w2q, w2s, shp, y, ws, stream=None):
+    """moe_forward_mx from tokens that are quantized already."""
+    _check("moe_forward_mx_codes", load().moe_forward_mx_codes(
+        _ptr(x_codes), _ptr(x_scales), _ptr(topk_idx), _ptr(topk_w), _ptr(w1q), _ptr(w1s), _ptr(w2q), _ptr(w2s),
+        ctypes.byref(shp), _ptr(y), _ptr(ws), _nbytes(ws), _stream(stream, ws)))
+
+
 def moe_dispatch_rows(x, shp, rows, ws, topk_w=None, row_weight=None, stream=None):
     """rows[r] = x[token of routed row r] (and row_weight[r] = its routing weight): the
     send buffer of an expert-parallel dispatch."""
@@ -488,7 +523,8 @@ def _module():
                                "(python -c 'import __graft_entry__ as g; g.build()')") from e
         native.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in
                       (lib.moe_route, lib.moe_route_backward, lib.moe_bias_update, lib.moe_grad_norm,
-                       lib.moe_clip_grads, lib.moe_adamw)])
+                       lib.moe_clip_grads, lib.moe_adamw, lib.moe_grouped_mm, lib.moe_grouped_wgrad,
+                       lib.moe_grouped_mm_mx, lib.moe_rms_norm, lib.moe_rms_norm_backward)])
         _native = native
     return _native
 
@@ -534,6 +570,71 @@ def moe_bias_update(bias, counts, rate, stream=None):
     """bias [E] or [L, E] += rate * sign(mean count - count), in place; counts int32 [S, E] or
     [L, S, E], added over the sequences."""
     _check("moe_bias_update", _module().bias_update(bias, counts, float(rate), _raw_stream(stream, bias)))
+
+
+# ------------------------------------------------------------------ the norm in front of the layer
+
+def moe_rms_norm(x, weight, y, eps=1e-6, residual=None, h=None, rstd=None, codes=None, scales=None, stream=None):
+    """y = the root-mean-square norm of h = x + residual (of x without one), times weight; x [T, H]
+    fp32, bf16 or fp16 (rows of x and residual may be apart). h (the stream, which may be x's or
+    residual's own memory), rstd fp32 [T] (for the backward) and codes uint8 [T, H] with scales
+    (``mx_scales_empty((T, H))``: y in MXFP8, H a multiple of 128) are written where given; y may be
+    None beside codes."""
+    _check("moe_rms_norm", _module().rms_norm(x, weight, y, eps, residual, h, rstd, codes, scales, _raw_stream(stream, x)))
+
+
+@functools.lru_cache(maxsize=256)
+def moe_rms_norm_workspace_size(T, H) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_rms_norm_workspace_size", load().moe_rms_norm_workspace_size(T, H, ctypes.byref(n)))
+    return int(n.value)
+
+
+def rms_norm_scratch(T, H, like) -> torch.Tensor:
+    """A workspace for the backward of T rows of H on the device of `like`."""
+    return torch.empty(moe_rms_norm_workspace_size(T, H), dtype=torch.uint8, device=like.device)
+
+
+def moe_rms_norm_backward(dy, h, weight, rstd, dx, dweight, ws, dh=None, stream=None):
+    """dx (of x and of residual) and dweight of moe_rms_norm, from dy and, where the stream h went on
+    by itself, its gradient dh."""
+    _check("moe_rms_norm_backward", _module().rms_norm_backward(dy, h, weight, rstd, dx, dweight, ws, dh,
+                                                                _raw_stream(stream, h)))
+
+
+# ------------------------------------------------------------------ products grouped by expert
+
+@functools.lru_cache(maxsize=256)
+def moe_grouped_workspace_size(G) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_grouped_workspace_size", load().moe_grouped_workspace_size(G, ctypes.byref(n)))
+    return int(n.value)
+
+
+def grouped_workspace(G, device=None) -> torch.Tensor:
+    """A workspace for the products of up to G groups, its header zeroed. Calls that share one are
+    ordered on one stream."""
+    ws = torch.empty(moe_grouped_workspace_size(G), dtype=torch.uint8, device=device or "cuda")
+    moe_workspace_init(ws)
+    return ws
+
+
+def moe_grouped_mm(x, w, offsets, out, ws, transposed=False, stream=None):
+    """out[r] = x[r] . w[g]^T for the rows offsets[g] .. offsets[g + 1] - 1 of each group g; x [R, K]
+    and out [R, N] bf16 or fp16 (rows may be apart), w [G, N, K], or with transposed w [G, K, N] and
+    out[r] = x[r] . w[g]; offsets int32 [G + 1] on the device. Rows of no group are left alone."""
+    _check("moe_grouped_mm", _module().grouped_mm(x, w, offsets, out, ws, bool(transposed), _raw_stream(stream, x)))
+
+
+def moe_grouped_wgrad(a, b, offsets, dw, ws, stream=None):
+    """dw[g] = the sum over group g's rows of a[r]^T b[r]; a [R, N], b [R, K], dw [G, N, K] of one type."""
+    _check("moe_grouped_wgrad", _module().grouped_wgrad(a, b, offsets, dw, ws, _raw_stream(stream, a)))
+
+
+def moe_grouped_mm_mx(x_codes, x_scales, w_codes, w_scales, offsets, out, ws, stream=None):
+    """moe_grouped_mm on MXFP8 operands (moe_mx_quantize's format): x [R, K], w [G, N, K], out bf16 [R, N]."""
+    _check("moe_grouped_mm_mx", _module().grouped_mm_mx(x_codes, x_scales, w_codes, w_scales, offsets, out, ws,
+                                                        _raw_stream(stream, x_codes)))
 
 
 # ------------------------------------------------------------------ lists of tensors

@@ -3,6 +3,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -190,6 +191,7 @@ struct GemmLaunch {
     int out_ld;                 // row stride of out / out2 where it differs from n_out
     int R;                      // routed rows (T * k)
     int save_h;                 // stage 1: also store h
+    int f16;                    // plain products: fp16 operands and output
     int num_sms;
 };
 
@@ -350,6 +352,49 @@ cudaError_t launch_bwd_dx(const GemmLaunch &p, cudaStream_t st);
 cudaError_t launch_bwd_dw2(const GemmLaunch &p, cudaStream_t st);
 cudaError_t launch_bwd_dw1(const GemmLaunch &p, cudaStream_t st);
 cudaError_t setup_bwd_gemm_kernels();
+
+// The norm in front of the layer (norm.cu, norm_bwd.cu).
+constexpr int64_t kNormMaxH = 16384;
+enum NormAccess { kWhole, kLoadsOne, kOne };    // of rows: in 16-byte vectors; those read, by element; all by element
+struct NormLaunch {
+    const void *x, *residual;   // rows ld_x, ld_r elements apart; residual may be null
+    const void *weight;         // of dtype, or fp32 with w_f32
+    void *h, *y;                // [T, H]; either may be null
+    float *rstd;                // [T] or null
+    uint8_t *codes;             // [T, H] or null
+    uint32_t *scales;           // words [H / 128][sf_rows]
+    int64_t T, ld_x, ld_r, sf_rows;
+    int H, dtype, w_f32;
+    int access;                 // NormAccess
+    float h_eps_hi, h_eps_lo;   // H eps, and sqrt(H), to 48 bits
+    float root_h_hi, root_h_lo;
+};
+struct NormBackwardLaunch {
+    const void *dy, *h, *dh;    // h's rows ld_h elements apart; dh may be null
+    const void *weight;
+    const float *rstd;
+    void *dx, *dweight;
+    float *part;                // [blocks, H]
+    int64_t T, ld_h, blocks;
+    int H, dtype, w_f32, access;
+};
+constexpr int64_t kNormRowsPerBlock = 64;
+int64_t rms_norm_bwd_blocks(int64_t T);
+cudaError_t launch_rms_norm(const NormLaunch &p, cudaStream_t st);
+cudaError_t launch_rms_norm_backward(const NormBackwardLaunch &p, cudaStream_t st);
+
+// The MXFP8 dispatch of rows that are quantized already: codes [T, cols] and words
+// [cols / 128][T rounded up to 4] in token order into routed order (rows.cu).
+cudaError_t launch_mx_dispatch(const uint8_t *x_codes, const uint32_t *x_scales, const int32_t *row_of,
+                               const int32_t *perm_slot, const int32_t *routed, int k, int64_t T, int64_t cols,
+                               uint8_t *codes, uint32_t *scales, cudaStream_t st);
+
+// Products grouped by the caller's offsets (grouped_mm.cu).
+enum class GroupedKind { rows, rows_t, wgrad, rows_mx };
+cudaError_t launch_grouped_tiles(const int32_t *offsets, int G, int R, int32_t *counts, int32_t *starts,
+                                 int32_t *mt_prefix, int32_t *err, cudaStream_t st);
+cudaError_t launch_grouped_mm(const GemmLaunch &p, GroupedKind kind, cudaStream_t st);
+cudaError_t setup_grouped_mm_kernels();
 
 // Per-device one-time kernel attribute set-up (dynamic shared memory limits).
 cudaError_t setup_metadata_kernels();

@@ -5,6 +5,8 @@
 #include <atomic>
 #include <mutex>
 
+#include <cmath>
+
 #include "internal.cuh"
 
 namespace moe {
@@ -382,6 +384,14 @@ moe_status_t run_mx_dispatch(const moe_shape_t &s, const void *x, const Ws &w, c
     return cuda_status(launch_mx_quantize_dispatch(static_cast<const __nv_bfloat16 *>(x), w.row_of, w.offsets + s.E,
                                                    s.k, s.T, s.H, w.x_codes, w.x_scales,
                                                    reinterpret_cast<uint8_t *>(w.obuf), st));
+}
+
+// The same from codes and scale words in token order.
+moe_status_t run_mx_dispatch_codes(const moe_shape_t &s, const void *x_codes, const void *x_scales, const Ws &w,
+                                   cudaStream_t st) {
+    return cuda_status(launch_mx_dispatch(static_cast<const uint8_t *>(x_codes), static_cast<const uint32_t *>(x_scales),
+                                          w.row_of, w.perm_slot, w.offsets + s.E, s.k, s.T, s.H, w.x_codes,
+                                          reinterpret_cast<uint32_t *>(w.x_scales), st));
 }
 
 // Stage 2 in MXFP8: E4M3 a and w2 through TMA, weighted rows into obuf, then the k-way combine.
@@ -1185,10 +1195,11 @@ moe_status_t moe_swiglu_gemm2_combine_mx(const void *a_codes, const void *a_scal
                         static_cast<cudaStream_t>(stream));
 }
 
-moe_status_t moe_forward_mx(const void *x, const int32_t *topk_idx, const float *topk_w,
-                            const void *w1_codes, const void *w1_scales, const void *w2_codes,
-                            const void *w2_scales, const moe_shape_t *shape, void *y, void *ws,
-                            size_t ws_bytes, void *stream) {
+// moe_forward_mx, from bf16 tokens (x_scales null) or from their codes.
+static moe_status_t forward_mx(const void *x, const void *x_scales, const int32_t *topk_idx, const float *topk_w,
+                               const void *w1_codes, const void *w1_scales, const void *w2_codes,
+                               const void *w2_scales, const moe_shape_t *shape, void *y, void *ws, size_t ws_bytes,
+                               void *stream) {
     moe_status_t r = check_shape(shape);
     if (r != MOE_OK) return r;
     if (shape->H % 128 || shape->I % 128) return MOE_ERR_UNSUPPORTED;
@@ -1205,10 +1216,44 @@ moe_status_t moe_forward_mx(const void *x, const int32_t *topk_idx, const float 
     const Ws w = carve(ws, *shape);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if ((r = run_metadata(*shape, topk_idx, w, st)) != MOE_OK) return r;
-    if ((r = run_mx_dispatch(*shape, x, w, st)) != MOE_OK) return r;
+    r = x_scales != nullptr ? run_mx_dispatch_codes(*shape, x, x_scales, w, st) : run_mx_dispatch(*shape, x, w, st);
+    if (r != MOE_OK) return r;
     if ((r = run_gemm1_mx(*shape, w1_codes, w1_scales, w.a_codes, w.a_scales, nullptr, w, *d, st)) != MOE_OK)
         return r;
     return run_gemm2_mx(*shape, w.a_codes, w.a_scales, topk_w, w2_codes, w2_scales, y, w, *d, st);
+}
+
+moe_status_t moe_forward_mx(const void *x, const int32_t *topk_idx, const float *topk_w,
+                            const void *w1_codes, const void *w1_scales, const void *w2_codes,
+                            const void *w2_scales, const moe_shape_t *shape, void *y, void *ws,
+                            size_t ws_bytes, void *stream) {
+    return forward_mx(x, nullptr, topk_idx, topk_w, w1_codes, w1_scales, w2_codes, w2_scales, shape, y, ws, ws_bytes,
+                      stream);
+}
+
+moe_status_t moe_forward_mx_codes(const void *x_codes, const void *x_scales, const int32_t *topk_idx,
+                                  const float *topk_w, const void *w1_codes, const void *w1_scales,
+                                  const void *w2_codes, const void *w2_scales, const moe_shape_t *shape, void *y,
+                                  void *ws, size_t ws_bytes, void *stream) {
+    const moe_status_t r = check_shape(shape);
+    if (r != MOE_OK) return r;
+    if (shape->T > 0 && (x_scales == nullptr || !aligned16(x_scales))) return MOE_ERR_INVALID_ARG;
+    return forward_mx(x_codes, x_scales, topk_idx, topk_w, w1_codes, w1_scales, w2_codes, w2_scales, shape, y, ws,
+                      ws_bytes, stream);
+}
+
+moe_status_t moe_mx_dispatch(const void *x_codes, const void *x_scales, const moe_shape_t *shape, void *ws,
+                             size_t ws_bytes, void *stream) {
+    moe_status_t r = check_shape(shape);
+    if (r != MOE_OK) return r;
+    if (shape->H % 128 || shape->I % 128) return MOE_ERR_UNSUPPORTED;
+    if (shape->T == 0) return MOE_OK;
+    if (!x_codes || !x_scales || !aligned16(x_codes) || !aligned16(x_scales)) return MOE_ERR_INVALID_ARG;
+    if ((r = check_ws(*shape, ws, ws_bytes)) != MOE_OK) return r;
+    if (!(shape->flags & MOE_SHAPE_MXFP8)) return MOE_ERR_INVALID_ARG;
+    DeviceState *d = nullptr;
+    if ((r = device_state(&d)) != MOE_OK) return r;
+    return run_mx_dispatch_codes(*shape, x_codes, x_scales, carve(ws, *shape), static_cast<cudaStream_t>(stream));
 }
 
 moe_status_t moe_dispatch_gemm1_mx_train(const void *w1_codes, const void *w1_scales, const moe_shape_t *shape,
@@ -1426,6 +1471,86 @@ uint64_t moe_kernel_launch_count(void) { return g_launches.load(std::memory_orde
 
 namespace {
 
+bool aligned_to(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+size_t dtype_size(int32_t dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+
+// Whole 16-byte vectors of experts can be read from (written to) every row.
+int rows_vectorized(const void *p, int64_t ld, int32_t dtype) {
+    return aligned16(p) && (ld * static_cast<int64_t>(dtype_size(dtype))) % 16 == 0;
+}
+
+moe_status_t check_norm(const moe_norm_shape_t *s) {
+    if (s == nullptr || s->T < 0 || s->H < 1 || s->ld_x < s->H || s->ld_r < s->H || !(s->eps >= 1e-30) ||
+        s->eps > 1e30)
+        return MOE_ERR_INVALID_ARG;
+    if (s->dtype < MOE_DTYPE_F32 || s->dtype > MOE_DTYPE_F16 ||
+        (s->w_dtype != s->dtype && s->w_dtype != MOE_DTYPE_F32))
+        return MOE_ERR_INVALID_ARG;
+    constexpr int64_t most = static_cast<int64_t>(1) << 31;
+    if (s->H > kNormMaxH || s->T >= most || s->ld_x >= most || s->ld_r >= most) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+// How the kernels reach a row: `dense`, whether the dense operands are whole 16-byte vectors, `apart`,
+// whether those with rows apart are.
+int norm_access(const moe_norm_shape_t &s, bool dense, bool apart) {
+    const bool whole = dense && s.H * static_cast<int64_t>(dtype_size(s.dtype)) % 16 == 0;
+    return whole ? (apart ? kWhole : kLoadsOne) : kOne;
+}
+
+// Workspace of the grouped products: header, then counts, starts and tile prefix of the groups.
+struct GroupedWs {
+    size_t counts, starts, mt_prefix, total;
+};
+
+GroupedWs grouped_layout(int64_t G) {
+    GroupedWs w;
+    w.counts = kWsHeaderBytes;
+    w.starts = align256(w.counts + 4 * static_cast<size_t>(G));
+    w.mt_prefix = align256(w.starts + 4 * static_cast<size_t>(G));
+    w.total = align256(w.mt_prefix + 4 * static_cast<size_t>(G + 1));
+    return w;
+}
+
+moe_status_t check_grouped(const moe_grouped_shape_t *s, const void *ws, size_t ws_bytes, bool any16, int32_t flags) {
+    if (s == nullptr || s->R < 0 || s->G < 1 || s->K < 1 || s->N < 1 || s->ld_x < s->K || s->ld_out < s->N ||
+        (s->flags & ~flags) != 0)
+        return MOE_ERR_INVALID_ARG;
+    if (s->dtype != MOE_DTYPE_BF16 && !(any16 && s->dtype == MOE_DTYPE_F16)) return MOE_ERR_UNSUPPORTED;
+    constexpr int64_t most = (static_cast<int64_t>(1) << 31) - kUnitM;
+    if (s->G > 1024 || s->K % 8 || s->N % 8 || s->ld_x % 8 || s->ld_out % 8 || s->R >= most || s->ld_x >= most ||
+        s->ld_out >= most)
+        return MOE_ERR_UNSUPPORTED;
+    // rows of all matrices, and units, are 32-bit numbers
+    if (s->G * s->N >= most || s->G * s->K >= most) return MOE_ERR_UNSUPPORTED;
+    const int64_t n_tiles = (s->N + 223) / 224, k_tiles = (s->K + kBN - 1) / kBN;
+    if ((s->R / kUnitM + s->G) * n_tiles >= most || s->G * n_tiles * k_tiles >= most) return MOE_ERR_UNSUPPORTED;
+    if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_INVALID_ARG;
+    return ws_bytes < grouped_layout(s->G).total ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+// The groups' tiles into ws, and a launch that reads them.
+moe_status_t grouped_launch(const moe_grouped_shape_t &s, const int32_t *offsets, void *ws, const DeviceState &d,
+                            cudaStream_t st, GemmLaunch *p) {
+    const GroupedWs l = grouped_layout(s.G);
+    uint8_t *b = static_cast<uint8_t *>(ws);
+    int32_t *counts = reinterpret_cast<int32_t *>(b + l.counts), *starts = reinterpret_cast<int32_t *>(b + l.starts);
+    int32_t *mt_prefix = reinterpret_cast<int32_t *>(b + l.mt_prefix);
+    *p = GemmLaunch{};
+    p->counts = counts;
+    p->offsets = starts;
+    p->mt_prefix = mt_prefix;
+    p->err = reinterpret_cast<int32_t *>(b);
+    p->sched = reinterpret_cast<int32_t *>(b + 8);
+    p->E = static_cast<int>(s.G);
+    p->k = 1;
+    p->R = static_cast<int>(s.R);
+    p->num_sms = d.num_sms;
+    p->f16 = s.dtype == MOE_DTYPE_F16;
+    return cuda_status(launch_grouped_tiles(offsets, p->E, p->R, counts, starts, mt_prefix, p->err, st));
+}
+
 struct RouteWs {
     size_t score, count, z, n, balance, seq_z, ticket, total;
 };
@@ -1462,15 +1587,6 @@ moe_status_t check_route_cfg(const moe_route_shape_t *s, const moe_router_cfg_t 
     return check_router_cfg(&m, cfg);
 }
 
-bool aligned_to(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-size_t dtype_size(int32_t dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
-
-// Whole 16-byte vectors of experts can be read from (written to) every row.
-int rows_vectorized(const void *p, int64_t ld, int32_t dtype) {
-    return aligned16(p) && (ld * static_cast<int64_t>(dtype_size(dtype))) % 16 == 0;
-}
-
 moe_status_t check_list(const void *const *ptr, const int64_t *numel, const int32_t *dtype, int32_t n,
                         bool optional = false) {
     if (n < 0 || (n > 0 && (ptr == nullptr || numel == nullptr))) return MOE_ERR_INVALID_ARG;
@@ -1495,6 +1611,207 @@ moe_status_t check_list_ws(const void *ws, size_t ws_bytes, int32_t n) {
 }  // namespace
 
 extern "C" {
+
+moe_status_t moe_rms_norm(const void *x, const void *residual, const void *weight, const moe_norm_shape_t *shape,
+                          void *h, void *y, float *rstd, void *codes, void *scales, void *stream) {
+    moe_status_t r = check_norm(shape);
+    if (r != MOE_OK) return r;
+    const moe_norm_shape_t &s = *shape;
+    if (s.T == 0) return MOE_OK;
+    if ((codes == nullptr) != (scales == nullptr) || (y == nullptr && codes == nullptr) ||
+        (h != nullptr && residual == nullptr))
+        return MOE_ERR_INVALID_ARG;
+    if (codes != nullptr && s.H % 128 != 0) return MOE_ERR_UNSUPPORTED;
+    const size_t size = dtype_size(s.dtype);
+    if (x == nullptr || weight == nullptr || !aligned_to(x, size) || !aligned_to(residual, size) ||
+        !aligned_to(h, size) || !aligned_to(y, size) || !aligned_to(weight, dtype_size(s.w_dtype)) ||
+        !aligned_to(rstd, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (h != nullptr && (h == y || (h == x && s.T > 1 && s.ld_x != s.H) || (h == residual && s.T > 1 && s.ld_r != s.H)))
+        return MOE_ERR_INVALID_ARG;
+    NormLaunch p{};
+    const bool out = rows_vectorized(h, s.H, s.dtype) && rows_vectorized(y, s.H, s.dtype) && aligned16(weight);
+    const bool in = rows_vectorized(x, s.ld_x, s.dtype) && rows_vectorized(residual, s.ld_r, s.dtype);
+    p.access = norm_access(s, out, in);
+    if (codes != nullptr && (!out || !aligned16(codes) || !aligned16(scales))) return MOE_ERR_INVALID_ARG;
+    DeviceState *d = nullptr;
+    if ((r = device_state(&d)) != MOE_OK) return r;
+    p.x = x;
+    p.residual = residual;
+    p.weight = weight;
+    p.h = h;
+    p.y = y;
+    p.rstd = rstd;
+    p.codes = static_cast<uint8_t *>(codes);
+    p.scales = static_cast<uint32_t *>(scales);
+    p.T = s.T;
+    p.ld_x = s.ld_x;
+    p.ld_r = s.ld_r;
+    p.sf_rows = static_cast<int64_t>(mx_rows(s.T));
+    p.H = static_cast<int>(s.H);
+    p.dtype = s.dtype;
+    p.w_f32 = s.w_dtype == MOE_DTYPE_F32;
+    const double h_eps = static_cast<double>(s.H) * s.eps, root = std::sqrt(static_cast<double>(s.H));
+    p.h_eps_hi = static_cast<float>(h_eps);
+    p.h_eps_lo = static_cast<float>(h_eps - p.h_eps_hi);
+    p.root_h_hi = static_cast<float>(root);
+    p.root_h_lo = static_cast<float>(root - p.root_h_hi);
+    return cuda_status(launch_rms_norm(p, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_rms_norm_workspace_size(int64_t T, int64_t H, size_t *bytes) {
+    if (bytes == nullptr || T < 0 || H < 1) return MOE_ERR_INVALID_ARG;
+    if (H > kNormMaxH || T >= (static_cast<int64_t>(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    *bytes = 4 * static_cast<size_t>(rms_norm_bwd_blocks(T)) * static_cast<size_t>(H);
+    return MOE_OK;
+}
+
+moe_status_t moe_rms_norm_backward(const void *dy, const void *dh, const void *h, const void *weight, const float *rstd,
+                                   const moe_norm_shape_t *shape, void *dx, void *dweight, void *ws, size_t ws_bytes,
+                                   void *stream) {
+    moe_status_t r = check_norm(shape);
+    if (r != MOE_OK) return r;
+    const moe_norm_shape_t &s = *shape;
+    const size_t size = dtype_size(s.dtype);
+    if (dweight == nullptr || !aligned_to(dweight, dtype_size(s.w_dtype))) return MOE_ERR_INVALID_ARG;
+    size_t need = 0;
+    if ((r = moe_rms_norm_workspace_size(s.T, s.H, &need)) != MOE_OK) return r;
+    if (s.T > 0) {
+        if (dy == nullptr || h == nullptr || weight == nullptr || rstd == nullptr || dx == nullptr ||
+            !aligned_to(dy, size) || !aligned_to(dh, size) || !aligned_to(h, size) || !aligned_to(dx, size) ||
+            !aligned_to(weight, dtype_size(s.w_dtype)) || !aligned_to(rstd, 4))
+            return MOE_ERR_INVALID_ARG;
+        if (ws == nullptr || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
+        if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+    }
+    DeviceState *d = nullptr;
+    if ((r = device_state(&d)) != MOE_OK) return r;
+    NormBackwardLaunch p{};
+    p.dy = dy;
+    p.h = h;
+    p.dh = dh;
+    p.weight = weight;
+    p.rstd = rstd;
+    p.dx = dx;
+    p.dweight = dweight;
+    p.part = static_cast<float *>(ws);
+    p.T = s.T;
+    p.ld_h = s.ld_x;
+    p.blocks = rms_norm_bwd_blocks(s.T);
+    p.H = static_cast<int>(s.H);
+    p.dtype = s.dtype;
+    p.w_f32 = s.w_dtype == MOE_DTYPE_F32;
+    const bool out = rows_vectorized(dy, s.H, s.dtype) && rows_vectorized(dh, s.H, s.dtype) &&
+                     rows_vectorized(dx, s.H, s.dtype) && aligned16(weight);
+    p.access = norm_access(s, out, rows_vectorized(h, s.ld_x, s.dtype));
+    return cuda_status(launch_rms_norm_backward(p, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_grouped_workspace_size(int64_t G, size_t *bytes) {
+    if (bytes == nullptr || G < 1) return MOE_ERR_INVALID_ARG;
+    if (G > 1024) return MOE_ERR_UNSUPPORTED;
+    *bytes = grouped_layout(G).total;
+    return MOE_OK;
+}
+
+moe_status_t moe_grouped_mm(const void *x, const void *w, const int32_t *offsets, const moe_grouped_shape_t *shape,
+                            void *out, void *ws, size_t ws_bytes, void *stream) {
+    moe_status_t r = check_grouped(shape, ws, ws_bytes, true, MOE_GROUPED_W_KN);
+    if (r != MOE_OK) return r;
+    const moe_grouped_shape_t &s = *shape;
+    if (s.R == 0) return MOE_OK;
+    if (x == nullptr || w == nullptr || offsets == nullptr || out == nullptr || !aligned16(x) || !aligned16(w) ||
+        !aligned16(out) || !aligned_to(offsets, 4))
+        return MOE_ERR_INVALID_ARG;
+    DeviceState *d = nullptr;
+    if ((r = device_state(&d)) != MOE_OK) return r;
+    const bool kn = (s.flags & MOE_GROUPED_W_KN) != 0;
+    CUtensorMap tm_x, tm_w, tm_out;
+    if (!encode_bf16_2d_strided(&tm_x, x, s.K, s.R, s.ld_x, kBK, 128) ||
+        !(kn ? encode_bf16_3d(&tm_w, w, s.N, s.K, s.G, 64, kBK)
+             : encode_bf16_2d(&tm_w, w, s.K, static_cast<uint64_t>(s.G) * s.N, kBK, 256)) ||
+        !encode_bf16_2d_strided(&tm_out, out, s.N, s.R, s.ld_out, 64, 32))
+        return MOE_ERR_CUDA;
+    GemmLaunch p;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((r = grouped_launch(s, offsets, ws, *d, st, &p)) != MOE_OK) return r;
+    p.tm_a = &tm_x;
+    p.tm_b = &tm_w;
+    p.tm_out = &tm_out;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.K = static_cast<int>(s.K);
+    p.n_out = static_cast<int>(s.N);
+    p.n_tile = kBN;
+    p.b_rows = static_cast<int>(s.N);
+    p.out_ld = static_cast<int>(s.ld_out);
+    return cuda_status(launch_grouped_mm(p, kn ? GroupedKind::rows_t : GroupedKind::rows, st));
+}
+
+moe_status_t moe_grouped_wgrad(const void *a, const void *b, const int32_t *offsets, const moe_grouped_shape_t *shape,
+                               void *dw, void *ws, size_t ws_bytes, void *stream) {
+    moe_status_t r = check_grouped(shape, ws, ws_bytes, true, 0);
+    if (r != MOE_OK) return r;
+    const moe_grouped_shape_t &s = *shape;
+    if (dw == nullptr || !aligned16(dw)) return MOE_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (s.R == 0) return cuda_status(cudaMemsetAsync(dw, 0, 2 * static_cast<size_t>(s.G) * s.N * s.K, st));
+    if (a == nullptr || b == nullptr || offsets == nullptr || !aligned16(a) || !aligned16(b) || !aligned_to(offsets, 4))
+        return MOE_ERR_INVALID_ARG;
+    DeviceState *d = nullptr;
+    if ((r = device_state(&d)) != MOE_OK) return r;
+    CUtensorMap tm_a, tm_b, tm_dw;
+    if (!encode_bf16_2d_strided(&tm_a, a, s.N, s.R, s.ld_out, 64, kBK) ||
+        !encode_bf16_2d_strided(&tm_b, b, s.K, s.R, s.ld_x, 64, kBK) ||
+        !encode_bf16_3d(&tm_dw, dw, s.K, s.N, s.G, 32, 32))
+        return MOE_ERR_CUDA;
+    GemmLaunch p;
+    if ((r = grouped_launch(s, offsets, ws, *d, st, &p)) != MOE_OK) return r;
+    p.tm_a = &tm_a;
+    p.tm_b = &tm_b;
+    p.tm_out = &tm_dw;
+    p.n_out = static_cast<int>(s.K);
+    p.n_tile = kBN;
+    p.m_total = static_cast<int>(s.N);
+    return cuda_status(launch_grouped_mm(p, GroupedKind::wgrad, st));
+}
+
+moe_status_t moe_grouped_mm_mx(const void *x_codes, const void *x_scales, const void *w_codes, const void *w_scales,
+                               const int32_t *offsets, const moe_grouped_shape_t *shape, void *out, void *ws,
+                               size_t ws_bytes, void *stream) {
+    moe_status_t r = check_grouped(shape, ws, ws_bytes, false, 0);
+    if (r != MOE_OK) return r;
+    const moe_grouped_shape_t &s = *shape;
+    if (s.K % 128 != 0 || s.ld_x != s.K) return MOE_ERR_UNSUPPORTED;
+    if (s.R == 0) return MOE_OK;
+    if (!x_codes || !x_scales || !w_codes || !w_scales || !offsets || !out) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(out) ||
+        !aligned_to(offsets, 4))
+        return MOE_ERR_INVALID_ARG;
+    DeviceState *d = nullptr;
+    if ((r = device_state(&d)) != MOE_OK) return r;
+    const uint64_t rows = static_cast<uint64_t>(s.G) * s.N;
+    CUtensorMap tm_x, tm_w, tm_out, tm_xs, tm_ws;
+    if (!encode_u8_2d(&tm_x, x_codes, s.K, s.R, 128, 128) || !encode_u8_2d(&tm_w, w_codes, s.K, rows, 128, 224) ||
+        !encode_bf16_2d_strided(&tm_out, out, s.N, s.R, s.ld_out, 32, 32) ||
+        !encode_sf_words(&tm_xs, x_scales, mx_rows(s.R), s.K / 128, kSfBoxRowsA) ||
+        !encode_sf_words(&tm_ws, w_scales, rows, s.K / 128, 224))
+        return MOE_ERR_CUDA;
+    GemmLaunch p;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((r = grouped_launch(s, offsets, ws, *d, st, &p)) != MOE_OK) return r;
+    p.tm_a = &tm_x;
+    p.tm_b = &tm_w;
+    p.tm_out = &tm_out;
+    p.tm_sfa = &tm_xs;
+    p.tm_sfb = &tm_ws;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.K = static_cast<int>(s.K);
+    p.n_out = static_cast<int>(s.N);
+    p.n_tile = 224;
+    p.b_rows = static_cast<int>(s.N);
+    p.out_ld = static_cast<int>(s.ld_out);
+    return cuda_status(launch_grouped_mm(p, GroupedKind::rows_mx, st));
+}
 
 moe_status_t moe_route_workspace_size(const moe_route_shape_t *shape, size_t *bytes) {
     const moe_status_t r = check_route_shape(shape);

@@ -1,6 +1,7 @@
 // native.cpp -- the part of the Python binding whose cost on the host shows: the router's
-// calls, short enough that a token waits for their argument checks (some 6 us through
-// Python and ctypes), and lists of tensors, 0.4 us a tensor through Python's attributes.
+// calls, the norm and the grouped products, short enough that a token waits for their argument
+// checks (some 6 us through Python and ctypes), and lists of tensors, 0.4 us a tensor through
+// Python's attributes.
 // It reads and checks the tensors and calls libmoe's C entry points; nothing else.
 //
 // CPython module `_native`: bind(addresses of the entry points), then the calls of the same
@@ -27,6 +28,11 @@ decltype(&moe_bias_update) g_bias_update = nullptr;
 decltype(&moe_grad_norm) g_grad_norm = nullptr;
 decltype(&moe_clip_grads) g_clip_grads = nullptr;
 decltype(&moe_adamw) g_adamw = nullptr;
+decltype(&moe_grouped_mm) g_grouped_mm = nullptr;
+decltype(&moe_grouped_wgrad) g_grouped_wgrad = nullptr;
+decltype(&moe_grouped_mm_mx) g_grouped_mm_mx = nullptr;
+decltype(&moe_rms_norm) g_rms_norm = nullptr;
+decltype(&moe_rms_norm_backward) g_rms_norm_backward = nullptr;
 
 int code_of(at::ScalarType t) {
     switch (t) {
@@ -379,6 +385,263 @@ PyObject *scratch_with_norm(PyObject *const *a) {
     return Py_BuildValue("(NN)", THPVariable_Wrap(std::move(ws)), THPVariable_Wrap(std::move(norm)));
 }
 
+// A matrix of `rows` x `cols` whose columns are consecutive: rows may lie apart.
+struct Rows {
+    const at::Tensor &tensor;
+    const char *name;
+    void *ptr;
+    int64_t rows, cols, ld;
+};
+Rows rows_of(PyObject *o, const char *name, const at::Tensor *like, int64_t rows, int64_t cols) {
+    const at::Tensor &t = tensor(o, name);
+    if (t.dim() != 2) refuse(PyExc_ValueError, "%s must have two dimensions", name);
+    if (!t.is_cuda()) refuse(PyExc_ValueError, "libmoe takes CUDA tensors only");
+    if (like != nullptr) {
+        together(*like, t);
+        if (t.scalar_type() != like->scalar_type())
+            refuse(PyExc_TypeError, "%s must be %s, not %s", name, c10::toString(like->scalar_type()), c10::toString(t.scalar_type()));
+    }
+    const int64_t r = t.size(0), c = t.size(1);
+    if ((rows >= 0 && r != rows) || (cols >= 0 && c != cols))
+        refuse(PyExc_ValueError, "%s must have shape (%lld, %lld), not (%lld, %lld)", name, static_cast<long long>(rows >= 0 ? rows : r),
+               static_cast<long long>(cols >= 0 ? cols : c), static_cast<long long>(r), static_cast<long long>(c));
+    if (c > 1 && t.stride(1) != 1) refuse(PyExc_ValueError, "the columns of %s must be consecutive", name);
+    const int64_t ld = r > 1 ? t.stride(0) : c;
+    if (ld < c) refuse(PyExc_ValueError, "the rows of %s overlap", name);
+    return {t, name, t.data_ptr(), r, c, ld};
+}
+
+// What a call writes lies in none of its other operands. Rows of one wide tensor's columns, as far
+// apart as the other's, interleave without meeting.
+bool meet(const void *a, int64_t rows_a, int64_t run_a, int64_t ld_a, const void *b, int64_t rows_b, int64_t run_b, int64_t ld_b) {
+    if (a == nullptr || b == nullptr || rows_a <= 0 || rows_b <= 0 || run_a <= 0 || run_b <= 0) return false;
+    const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+    if (d >= (rows_a - 1) * ld_a + run_a || -d >= (rows_b - 1) * ld_b + run_b) return false;
+    if (rows_a > 1 && rows_b > 1 && ld_a != ld_b) return true;
+    const int64_t ld = rows_a > 1 ? ld_a : rows_b > 1 ? ld_b : 0;
+    if (ld == 0) return true;
+    const int64_t at = ((d % ld) + ld) % ld;                            // of b's run in a's row
+    return at < run_a || at + run_b > ld;
+}
+void apart(const Rows &w, const Rows &r) {
+    const int64_t size = w.tensor.element_size(), other = r.tensor.element_size();
+    if (meet(w.ptr, w.rows, w.cols * size, w.ld * size, r.ptr, r.rows, r.cols * other, r.ld * other))
+        refuse(PyExc_ValueError, "%s and %s hold the same memory", w.name, r.name);
+}
+void apart(const Rows &w, const at::Tensor &t, const char *name) {
+    const int64_t size = w.tensor.element_size(), bytes = static_cast<int64_t>(t.nbytes());
+    if (t.numel() > 0 && meet(w.ptr, w.rows, w.cols * size, w.ld * size, t.data_ptr(), 1, bytes, bytes))
+        refuse(PyExc_ValueError, "%s and %s hold the same memory", w.name, name);
+}
+void apart(const at::Tensor &w, const char *name, const Rows &r) {
+    const int64_t size = r.tensor.element_size(), bytes = static_cast<int64_t>(w.nbytes());
+    if (w.numel() > 0 && meet(w.data_ptr(), 1, bytes, bytes, r.ptr, r.rows, r.cols * size, r.ld * size))
+        refuse(PyExc_ValueError, "%s and %s hold the same memory", name, r.name);
+}
+void apart(const at::Tensor &w, const char *name, const at::Tensor &t, const char *other) {
+    const int64_t bytes = static_cast<int64_t>(w.nbytes()), more = static_cast<int64_t>(t.nbytes());
+    if (bytes > 0 && more > 0 && meet(w.data_ptr(), 1, bytes, bytes, t.data_ptr(), 1, more, more))
+        refuse(PyExc_ValueError, "%s and %s hold the same memory", name, other);
+}
+
+// A dense tensor with group matrices [G, rows, cols] (-1: any).
+const at::Tensor &matrices_of(PyObject *o, const char *name, const at::Tensor &like, at::ScalarType type, int64_t rows, int64_t cols) {
+    const at::Tensor &t = tensor(o, name);
+    together(like, t);
+    if (t.scalar_type() != type) refuse(PyExc_TypeError, "%s must be %s, not %s", name, c10::toString(type), c10::toString(t.scalar_type()));
+    if (t.dim() != 3 || (rows >= 0 && t.size(1) != rows) || (cols >= 0 && t.size(2) != cols))
+        refuse(PyExc_ValueError, "%s must be a matrix for each group that fits the other operands", name);
+    if (!t.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous", name);
+    return t;
+}
+
+const int32_t *offsets_of(PyObject *o, const at::Tensor &like, int64_t G) {
+    return as<const int32_t>(address(o, "offsets", like, at::kInt, {G + 1}));
+}
+
+int grouped_type(const at::Tensor &t, const char *name) {
+    const int code = code_of(t.scalar_type());
+    if (code != MOE_DTYPE_BF16 && code != MOE_DTYPE_F16)
+        refuse(PyExc_TypeError, "%s must be bfloat16 or float16, not %s", name, c10::toString(t.scalar_type()));
+    return code;
+}
+
+// x, w, offsets, out, ws, transposed, stream
+PyObject *grouped_mm(PyObject *const *a) {
+    const Rows x = rows_of(a[0], "x", nullptr, -1, -1);
+    const at::Tensor &on = x.tensor;
+    const int code = grouped_type(on, "x");
+    const bool kn = whole(a[5]) != 0;
+    const at::Tensor &w = matrices_of(a[1], "w", on, on.scalar_type(), kn ? x.cols : -1, kn ? -1 : x.cols);
+    const int64_t G = w.size(0), N = w.size(kn ? 2 : 1);
+    const Rows out = rows_of(a[3], "out", &on, x.rows, N);
+    const int32_t *offsets = offsets_of(a[2], on, G);
+    const Scratch ws = scratch(a[4], on);
+    apart(out, x);
+    apart(out, w, "w");
+    apart(out, THPVariable_Unpack(a[2]), "offsets");
+    apart(out, THPVariable_Unpack(a[4]), "ws");
+    const moe_grouped_shape_t s{x.rows, G, x.cols, N, x.ld, out.ld, code, kn ? MOE_GROUPED_W_KN : 0};
+    return changed(g_grouped_mm(x.ptr, w.data_ptr(), offsets, &s, out.ptr, ws.ptr, ws.bytes, handle(a[6])),
+                   [&] { bump(out.tensor); });
+}
+
+// a, b, offsets, dw, ws, stream
+PyObject *grouped_wgrad(PyObject *const *a) {
+    const Rows l = rows_of(a[0], "a", nullptr, -1, -1);
+    const at::Tensor &on = l.tensor;
+    const int code = grouped_type(on, "a");
+    const Rows r = rows_of(a[1], "b", &on, l.rows, -1);
+    const at::Tensor &dw = matrices_of(a[3], "dw", on, on.scalar_type(), l.cols, r.cols);
+    const int64_t G = dw.size(0);
+    const int32_t *offsets = offsets_of(a[2], on, G);
+    const Scratch ws = scratch(a[4], on);
+    apart(dw, "dw", l);
+    apart(dw, "dw", r);
+    apart(dw, "dw", THPVariable_Unpack(a[2]), "offsets");
+    apart(dw, "dw", THPVariable_Unpack(a[4]), "ws");
+    const moe_grouped_shape_t s{l.rows, G, r.cols, l.cols, r.ld, l.ld, code, 0};
+    return changed(g_grouped_wgrad(l.ptr, r.ptr, offsets, &s, dw.data_ptr(), ws.ptr, ws.bytes, handle(a[5])), [&] { bump(dw); });
+}
+
+// x_codes, x_scales, w_codes, w_scales, offsets, out, ws, stream
+PyObject *grouped_mm_mx(PyObject *const *a) {
+    const Rows x = rows_of(a[0], "x_codes", nullptr, -1, -1);
+    const at::Tensor &on = x.tensor;
+    if (on.scalar_type() != at::kByte) refuse(PyExc_TypeError, "x_codes must be Byte, not %s", c10::toString(on.scalar_type()));
+    if (!on.is_contiguous()) refuse(PyExc_ValueError, "x_codes must be contiguous");
+    const at::Tensor &w = matrices_of(a[2], "w_codes", on, at::kByte, -1, x.cols);
+    const int64_t G = w.size(0), N = w.size(1);
+    auto words = [&](PyObject *o, const char *name, int64_t rows) {
+        const at::Tensor &t = tensor(o, name);
+        together(on, t);
+        if (t.scalar_type() != at::kByte) refuse(PyExc_TypeError, "%s must be Byte, not %s", name, c10::toString(t.scalar_type()));
+        if (!t.is_contiguous() || t.numel() != (rows + 3) / 4 * 4 * (x.cols / 32))
+            refuse(PyExc_ValueError, "%s must hold the k-block-major words of its rows rounded up to 4", name);
+        return t.data_ptr();
+    };
+    const void *xs = words(a[1], "x_scales", x.rows), *ws_w = words(a[3], "w_scales", G * N);
+    const at::Tensor &o = tensor(a[5], "out");
+    if (o.scalar_type() != at::kBFloat16) refuse(PyExc_TypeError, "out must be BFloat16, not %s", c10::toString(o.scalar_type()));
+    together(on, o);
+    const Rows out = rows_of(a[5], "out", nullptr, x.rows, N);
+    const int32_t *offsets = offsets_of(a[4], on, G);
+    const Scratch ws = scratch(a[6], on);
+    for (int i = 0; i < 5; ++i) apart(out, THPVariable_Unpack(a[i]), i == 4 ? "offsets" : i < 2 ? "x" : "w");
+    apart(out, THPVariable_Unpack(a[6]), "ws");
+    const moe_grouped_shape_t s{x.rows, G, x.cols, N, x.ld, out.ld, MOE_DTYPE_BF16, 0};
+    return changed(g_grouped_mm_mx(x.ptr, xs, w.data_ptr(), ws_w, offsets, &s, out.ptr, ws.ptr, ws.bytes, handle(a[7])),
+                   [&] { bump(out.tensor); });
+}
+
+// The weight of a norm over H columns, of the rows' type or fp32; its MOE_DTYPE_*.
+int norm_weight(PyObject *o, const char *name, const at::Tensor &on, int64_t H, void **ptr) {
+    const at::Tensor &w = tensor(o, name);
+    const at::ScalarType type = w.scalar_type() == at::kFloat ? at::kFloat : on.scalar_type();
+    *ptr = address(o, name, on, type, {H});
+    return code_of(type);
+}
+double number_of(PyObject *o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Refused();
+    return v;
+}
+// A dense [T, H] operand of the type of `on`; none where it is None.
+Rows dense(PyObject *o, const char *name, const at::Tensor &on, int64_t T, int64_t H) {
+    if (o == Py_None) return {on, name, nullptr, 0, 0, 0};
+    Rows r = rows_of(o, name, &on, T, H);
+    if (r.rows > 1 && r.ld != H) refuse(PyExc_ValueError, "%s must be contiguous", name);
+    return r;
+}
+// A written operand is apart from a read one or in its very place.
+void apart_or_same(const Rows &w, const Rows &r) {
+    if (w.ptr == nullptr || r.ptr == nullptr || (w.ptr == r.ptr && w.ld == r.ld)) return;
+    apart(w, r);
+}
+void apart_if(const Rows &w, PyObject *o, const char *name) {
+    if (w.ptr != nullptr && o != Py_None) apart(w, THPVariable_Unpack(o), name);
+}
+
+// x, weight, y, eps, residual, h, rstd, codes, scales, stream
+PyObject *rms_norm(PyObject *const *a) {
+    const Rows x = rows_of(a[0], "x", nullptr, -1, -1);
+    const at::Tensor &on = x.tensor;
+    const int code = code_of(on.scalar_type());
+    if (code < 0) refuse(PyExc_TypeError, "x must be float32, bfloat16 or float16, not %s", c10::toString(on.scalar_type()));
+    const int64_t T = x.rows, H = x.cols;
+    void *weight;
+    const int w_code = norm_weight(a[1], "weight", on, H, &weight);
+    const Rows residual = a[4] == Py_None ? Rows{on, "residual", nullptr, 0, 0, 0} : rows_of(a[4], "residual", &on, T, H);
+    const Rows y = dense(a[2], "y", on, T, H), h = dense(a[5], "h", on, T, H);
+    float *rstd = as<float>(address(a[6], "rstd", on, at::kFloat, {T}));
+    void *codes = address(a[7], "codes", on, at::kByte, {T, H}), *scales = nullptr;
+    if (a[8] != Py_None) {
+        const at::Tensor &s = tensor(a[8], "scales");
+        together(on, s);
+        if (s.scalar_type() != at::kByte) refuse(PyExc_TypeError, "scales must be Byte, not %s", c10::toString(s.scalar_type()));
+        if (!s.is_contiguous() || s.numel() != (T + 3) / 4 * 4 * (H / 32))
+            refuse(PyExc_ValueError, "scales must hold the k-block-major words of T rounded up to 4");
+        scales = s.data_ptr();
+    }
+    for (const Rows *w : {&y, &h}) {
+        apart_or_same(*w, x);
+        apart_or_same(*w, residual);
+        for (int i : {1, 6, 7, 8}) apart_if(*w, a[i], i == 1 ? "weight" : i == 6 ? "rstd" : i == 7 ? "codes" : "scales");
+    }
+    if (y.ptr != nullptr && h.ptr != nullptr) apart(y, h);
+    static const char *const names[] = {"rstd", "codes", "scales"};
+    for (int i : {6, 7, 8}) {
+        if (a[i] == Py_None) continue;
+        const at::Tensor &w = THPVariable_Unpack(a[i]);
+        apart(w, names[i - 6], x);
+        if (residual.ptr != nullptr) apart(w, names[i - 6], residual);
+        apart(w, names[i - 6], THPVariable_Unpack(a[1]), "weight");
+        for (int j = 6; j < i; ++j)
+            if (a[j] != Py_None) apart(w, names[i - 6], THPVariable_Unpack(a[j]), names[j - 6]);
+    }
+    const moe_norm_shape_t s{T, H, x.ld, residual.ptr != nullptr ? residual.ld : H, number_of(a[3]), code, w_code};
+    return changed(g_rms_norm(x.ptr, residual.ptr, weight, &s, h.ptr, y.ptr, rstd, codes, scales, handle(a[9])), [&] {
+        for (int i : {2, 5, 6, 7, 8})
+            if (a[i] != Py_None) bump(THPVariable_Unpack(a[i]));
+    });
+}
+
+// dy, h, weight, rstd, dx, dweight, ws, dh, stream
+PyObject *rms_norm_backward(PyObject *const *a) {
+    const Rows h = rows_of(a[1], "h", nullptr, -1, -1);
+    const at::Tensor &on = h.tensor;
+    const int code = code_of(on.scalar_type());
+    if (code < 0) refuse(PyExc_TypeError, "h must be float32, bfloat16 or float16, not %s", c10::toString(on.scalar_type()));
+    const int64_t T = h.rows, H = h.cols;
+    void *weight;
+    const int w_code = norm_weight(a[2], "weight", on, H, &weight);
+    const Rows dy = dense(a[0], "dy", on, T, H), dh = dense(a[7], "dh", on, T, H), dx = dense(a[4], "dx", on, T, H);
+    const float *rstd = as<const float>(address(a[3], "rstd", on, at::kFloat, {T}));
+    void *dweight = address(a[5], "dweight", on, w_code == MOE_DTYPE_F32 ? at::kFloat : on.scalar_type(), {H});
+    const Scratch ws = scratch(a[6], on);
+    apart_or_same(dx, dy);
+    apart_or_same(dx, dh);
+    if (dx.ptr != nullptr) apart(dx, h);
+    for (int i : {2, 3, 5, 6}) apart_if(dx, a[i], i == 2 ? "weight" : i == 3 ? "rstd" : i == 5 ? "dweight" : "ws");
+    for (int i : {5, 6}) {
+        if (a[i] == Py_None) continue;
+        const at::Tensor &w = THPVariable_Unpack(a[i]);
+        const char *name = i == 5 ? "dweight" : "ws";
+        apart(w, name, h);
+        if (dy.ptr != nullptr) apart(w, name, dy);
+        if (dh.ptr != nullptr) apart(w, name, dh);
+        apart(w, name, THPVariable_Unpack(a[2]), "weight");
+        if (a[3] != Py_None) apart(w, name, THPVariable_Unpack(a[3]), "rstd");
+        if (i == 6 && a[5] != Py_None) apart(w, name, THPVariable_Unpack(a[5]), "dweight");
+    }
+    const moe_norm_shape_t s{T, H, h.ld, H, 1.0, code, w_code};
+    return changed(g_rms_norm_backward(dy.ptr, dh.ptr, h.ptr, weight, rstd, &s, dx.ptr, dweight, ws.ptr, ws.bytes, handle(a[8])),
+                   [&] {
+                       for (int i : {4, 5})
+                           if (a[i] != Py_None) bump(THPVariable_Unpack(a[i]));
+                   });
+}
+
 PyObject *bind(PyObject *const *a) {
     g_route = reinterpret_cast<decltype(g_route)>(handle(a[0]));
     g_route_backward = reinterpret_cast<decltype(g_route_backward)>(handle(a[1]));
@@ -386,6 +649,11 @@ PyObject *bind(PyObject *const *a) {
     g_grad_norm = reinterpret_cast<decltype(g_grad_norm)>(handle(a[3]));
     g_clip_grads = reinterpret_cast<decltype(g_clip_grads)>(handle(a[4]));
     g_adamw = reinterpret_cast<decltype(g_adamw)>(handle(a[5]));
+    g_grouped_mm = reinterpret_cast<decltype(g_grouped_mm)>(handle(a[6]));
+    g_grouped_wgrad = reinterpret_cast<decltype(g_grouped_wgrad)>(handle(a[7]));
+    g_grouped_mm_mx = reinterpret_cast<decltype(g_grouped_mm_mx)>(handle(a[8]));
+    g_rms_norm = reinterpret_cast<decltype(g_rms_norm)>(handle(a[9]));
+    g_rms_norm_backward = reinterpret_cast<decltype(g_rms_norm_backward)>(handle(a[10]));
     Py_RETURN_NONE;
 }
 
@@ -408,7 +676,7 @@ PyMethodDef method(const char *name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(&call<F, N>)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef kMethods[] = {method<bind, 6>("bind"),
+PyMethodDef kMethods[] = {method<bind, 11>("bind"),
                           method<route, 12>("route"),
                           method<route_backward, 11>("route_backward"),
                           method<bias_update, 4>("bias_update"),
@@ -416,6 +684,11 @@ PyMethodDef kMethods[] = {method<bind, 6>("bind"),
                           method<clip_grads, 6>("clip_grads"),
                           method<adamw, 12>("adamw"),
                           method<scratch_with_norm, 2>("scratch"),
+                          method<grouped_mm, 7>("grouped_mm"),
+                          method<grouped_wgrad, 6>("grouped_wgrad"),
+                          method<grouped_mm_mx, 8>("grouped_mm_mx"),
+                          method<rms_norm, 10>("rms_norm"),
+                          method<rms_norm_backward, 9>("rms_norm_backward"),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

@@ -37,6 +37,11 @@ For training with balance terms the layer comes in two differentiable parts: `ro
 packed sequences) and `moe_experts` (dispatch, both expert stages and the combine, with a
 gradient for the routing weights too); `moe_bias_update` in the binding moves the selection
 bias from route's counts.
+
+Around the layer: `rms_norm` is the differentiable norm of the residual stream in front of it
+(`rms_norm_mx` also gives its MXFP8 form, which `forward_mx_codes` takes), and `grouped_mm`
+the differentiable product of rows with the matrix of their group, for experts of another
+form than the SwiGLU pair.
 """
 from typing import NamedTuple, Optional, Tuple
 
@@ -111,6 +116,17 @@ def _check_forward_args(x, topk_idx, topk_w, w1, w2):
     _check_routing(x, topk_idx, topk_w, w1.shape[0])
 
 
+def _check_mx_codes(w1_codes, w1_scales, w2_codes, w2_scales):
+    E, two_i, H = w1_codes.shape
+    I = two_i // 2
+    if two_i % 2 or H % 128 or I % 128:
+        raise ValueError("MXFP8 needs H and I multiples of 128")
+    _expect(w1_codes, "w1_codes", torch.uint8, (E, two_i, H))
+    _expect(w1_scales, "w1_scales", torch.uint8, (H // 128, E, two_i, 4))
+    _expect(w2_codes, "w2_codes", torch.uint8, (E, H, I))
+    _expect(w2_scales, "w2_scales", torch.uint8, (I // 128, E, H, 4))
+
+
 def _check_forward_mx_args(x, topk_idx, topk_w, w1_codes, w1_scales, w2_codes, w2_scales):
     if x.dim() != 2 or w1_codes.dim() != 3:
         raise ValueError("x must be [T, H] and w1_codes [E, 2I, H]")
@@ -118,13 +134,7 @@ def _check_forward_mx_args(x, topk_idx, topk_w, w1_codes, w1_scales, w2_codes, w
     E, two_i, H = w1_codes.shape
     if x.shape[1] != H or two_i % 2:
         raise ValueError("w1_codes must be [E, 2I, H] with H = x.shape[1]")
-    I = two_i // 2
-    if H % 128 or I % 128:
-        raise ValueError("MXFP8 needs H and I multiples of 128")
-    _expect(w1_codes, "w1_codes", torch.uint8, (E, two_i, H))
-    _expect(w1_scales, "w1_scales", torch.uint8, (H // 128, E, two_i, 4))
-    _expect(w2_codes, "w2_codes", torch.uint8, (E, H, I))
-    _expect(w2_scales, "w2_scales", torch.uint8, (I // 128, E, H, 4))
+    _check_mx_codes(w1_codes, w1_scales, w2_codes, w2_scales)
     _check_routing(x, topk_idx, topk_w, E)
 
 
@@ -608,6 +618,240 @@ def moe_experts(x, topk_idx, topk_w, w1, w2):
     one differentiable call: y bf16 [T, H]; gradients for x, topk_w, w1 and w2. Slots of -1 are
     left out: their tokens' rows get nothing from them."""
     return experts_train(x, topk_idx, topk_w, w1, w2)[0]
+
+
+# ------------------------------------------------------------------ the norm in front of the layer
+
+
+def _check_norm_args(x, weight, residual, eps):
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    if x.dtype not in B.DTYPE_CODES:
+        raise TypeError(f"x must be float32, bfloat16 or float16, not {x.dtype}")
+    if not 1 <= x.shape[1] <= B.NORM_MAX_H:
+        raise ValueError(f"H must be in [1, {B.NORM_MAX_H}], not {x.shape[1]}")
+    if not eps >= 1e-30:
+        raise ValueError(f"eps must be at least 1e-30, not {eps}")
+    if weight.dtype not in (x.dtype, torch.float32):
+        raise TypeError(f"weight must be {x.dtype} or torch.float32, not {weight.dtype}")
+    _expect(weight, "weight", weight.dtype, (x.shape[1],))
+    if residual is not None:
+        _expect(residual, "residual", x.dtype, tuple(x.shape))
+
+
+def _stream_empty(x, residual):
+    return torch.empty((0 if residual is None else x.shape[0], x.shape[1]), dtype=x.dtype, device=x.device)
+
+
+@torch.library.custom_op(f"{_LIB}::rms_norm_train", mutates_args=())
+def rms_norm_train(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6
+                   ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """moe_rms_norm: (y, h, rstd); h has no rows without a residual."""
+    _check_norm_args(x, weight, residual, eps)
+    x, weight = _rows(x), weight.contiguous()
+    residual = None if residual is None else _rows(residual)
+    y, h = torch.empty(x.shape, dtype=x.dtype, device=x.device), _stream_empty(x, residual)
+    rstd = torch.empty((x.shape[0],), dtype=torch.float32, device=x.device)
+    B.moe_rms_norm(x, weight, y, eps, residual=residual, h=None if residual is None else h, rstd=rstd)
+    return y, h, rstd
+
+
+@rms_norm_train.register_fake
+def _rms_norm_train_fake(x, weight, residual=None, eps=1e-6):
+    _check_norm_args(x, weight, residual, eps)
+    return (x.new_empty(x.shape), x.new_empty((0 if residual is None else x.shape[0], x.shape[1])),
+            x.new_empty((x.shape[0],), dtype=torch.float32))
+
+
+@torch.library.custom_op(f"{_LIB}::rms_norm_backward", mutates_args=())
+def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                      dh: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(dx, dweight) of rms_norm_train; dx is also the residual's gradient."""
+    _expect(dy, "dy", h.dtype, tuple(h.shape))
+    if dh is not None:
+        _expect(dh, "dh", h.dtype, tuple(h.shape))
+    h, weight = _rows(h), weight.contiguous()
+    dx, dweight = torch.empty(h.shape, dtype=h.dtype, device=h.device), torch.empty_like(weight)
+    B.moe_rms_norm_backward(dy.contiguous(), h, weight, rstd, dx, dweight, B.rms_norm_scratch(*h.shape, h),
+                            dh=None if dh is None else dh.contiguous())
+    return dx, dweight
+
+
+@rms_norm_backward.register_fake
+def _rms_norm_backward_fake(dy, h, weight, rstd, dh=None):
+    return h.new_empty(h.shape), weight.new_empty(weight.shape)
+
+
+def _rms_norm_setup_context(ctx, inputs, output):
+    x, weight, residual, _ = inputs
+    _, h, rstd = output
+    ctx.save_for_backward(x if residual is None else h, weight, rstd)
+    ctx.added = residual is not None
+    ctx.mark_non_differentiable(rstd)
+    ctx.set_materialize_grads(False)
+
+
+def _rms_norm_backward_rule(ctx, dy, dh, _rstd):
+    h, weight, rstd = ctx.saved_tensors
+    if dy is None:                              # the stream alone went on
+        return (dh, None, dh, None) if ctx.added else (None,) * 4
+    dx, dweight = rms_norm_backward(dy, h, weight, rstd, dh if ctx.added else None)
+    return dx, dweight, dx if ctx.added else None, None
+
+
+rms_norm_train.register_autograd(_rms_norm_backward_rule, setup_context=_rms_norm_setup_context)
+
+
+def rms_norm(x, weight, residual=None, eps=1e-6):
+    """The root-mean-square norm of x [T, H] (fp32, bf16 or fp16) times weight [H] (of x's type or
+    fp32), as one differentiable call: y; with a residual [T, H], of h = x + residual: (y, h), h
+    being the stream that goes on beside y."""
+    y, h, _ = rms_norm_train(x, weight, residual, eps)
+    return y if residual is None else (y, h)
+
+
+@torch.library.custom_op(f"{_LIB}::rms_norm_mx", mutates_args=())
+def rms_norm_mx(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6
+                ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The norm and its MXFP8 form, without a gradient: (y, h, codes, scales); y for the router, codes
+    and scales (moe_mx_quantize's of y) for forward_mx_codes; h has no rows without a residual."""
+    _check_norm_args(x, weight, residual, eps)
+    if x.shape[1] % 128:
+        raise ValueError("MXFP8 needs H a multiple of 128")
+    x, weight = _rows(x), weight.contiguous()
+    residual = None if residual is None else _rows(residual)
+    y, h = torch.empty(x.shape, dtype=x.dtype, device=x.device), _stream_empty(x, residual)
+    codes, scales = torch.empty(x.shape, dtype=torch.uint8, device=x.device), B.mx_scales_empty(tuple(x.shape), x.device)
+    B.moe_rms_norm(x, weight, y, eps, residual=residual, h=None if residual is None else h, codes=codes, scales=scales)
+    return y, h, codes, scales
+
+
+@rms_norm_mx.register_fake
+def _rms_norm_mx_fake(x, weight, residual=None, eps=1e-6):
+    _check_norm_args(x, weight, residual, eps)
+    if x.shape[1] % 128:
+        raise ValueError("MXFP8 needs H a multiple of 128")
+    T, H = x.shape
+    return (x.new_empty((T, H)), x.new_empty((0 if residual is None else T, H)), x.new_empty((T, H), dtype=torch.uint8),
+            x.new_empty((H // 128, (T + 3) // 4 * 4, 4), dtype=torch.uint8))
+
+
+@torch.library.custom_op(f"{_LIB}::forward_mx_codes", mutates_args=())
+def forward_mx_codes(x_codes: torch.Tensor, x_scales: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                     w1_codes: torch.Tensor, w1_scales: torch.Tensor, w2_codes: torch.Tensor, w2_scales: torch.Tensor
+                     ) -> torch.Tensor:
+    """forward_mx from tokens that are quantized already (rms_norm_mx's codes and scales)."""
+    _check_forward_mx_codes_args(x_codes, x_scales, topk_idx, topk_w, w1_codes, w1_scales, w2_codes, w2_scales)
+    T, H = x_codes.shape
+    E, two_i, _ = w1_codes.shape
+    shp = B.shape(T, H, two_i // 2, E, topk_idx.shape[1], mxfp8=True)
+    y = torch.empty((T, H), dtype=torch.bfloat16, device=x_codes.device)
+    B.moe_forward_mx_codes(x_codes, x_scales, topk_idx, topk_w, w1_codes, w1_scales, w2_codes, w2_scales, shp, y,
+                           B.new_workspace(shp, x_codes.device))
+    return y
+
+
+def _check_forward_mx_codes_args(x_codes, x_scales, topk_idx, topk_w, w1_codes, w1_scales, w2_codes, w2_scales):
+    if x_codes.dim() != 2:
+        raise ValueError("x_codes must be [T, H]")
+    T, H = x_codes.shape
+    _expect(x_codes, "x_codes", torch.uint8, (T, H))
+    if w1_codes.dim() != 3 or w1_codes.shape[2] != H:
+        raise ValueError("w1_codes must be [E, 2I, H] with H = x_codes.shape[1]")
+    _check_mx_codes(w1_codes, w1_scales, w2_codes, w2_scales)
+    _check_routing(x_codes, topk_idx, topk_w, w1_codes.shape[0])
+    _expect(x_scales, "x_scales", torch.uint8, (H // 128, (T + 3) // 4 * 4, 4))
+
+
+@forward_mx_codes.register_fake
+def _forward_mx_codes_fake(x_codes, x_scales, topk_idx, topk_w, w1_codes, w1_scales, w2_codes, w2_scales):
+    _check_forward_mx_codes_args(x_codes, x_scales, topk_idx, topk_w, w1_codes, w1_scales, w2_codes, w2_scales)
+    return x_codes.new_empty(x_codes.shape, dtype=torch.bfloat16)
+
+
+# ------------------------------------------------------------------ products grouped by expert
+
+
+def _check_grouped_args(x, w, offsets, transposed):
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x must be [R, K] and w a matrix for each group")
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"x must be bfloat16 or float16, not {x.dtype}")
+    G, K, N = (w.shape[0], w.shape[1], w.shape[2]) if transposed else (w.shape[0], w.shape[2], w.shape[1])
+    if x.shape[1] != K or K % 8 or N % 8 or K < 8 or N < 8 or not 1 <= G <= 1024:
+        raise ValueError(f"x has {x.shape[1]} columns, w {G} matrices for {K} into {N}: those must be equal, K and N "
+                         "multiples of 8 and at most 1024 groups")
+    _expect(w, "w", x.dtype, tuple(w.shape))
+    _expect(offsets, "offsets", torch.int32, (G + 1,))
+    return N
+
+
+def _grouped_rows(t):
+    """Rows as the products read them: 16-byte aligned, columns consecutive, rows apart by whole vectors."""
+    t = _rows(t)
+    if (t.shape[0] > 1 and t.stride(0) % 8) or t.data_ptr() % 16:
+        t = t.clone(memory_format=torch.contiguous_format)
+    return t
+
+
+@torch.library.custom_op(f"{_LIB}::grouped_rows", mutates_args=())
+def grouped_rows(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, transposed: bool = False,
+                 complete: bool = False) -> torch.Tensor:
+    """moe_grouped_mm into a new tensor; rows of no group are zeros (with complete there are none)."""
+    N = _check_grouped_args(x, w, offsets, transposed)
+    new = torch.empty if complete else torch.zeros
+    out = new((x.shape[0], N), dtype=x.dtype, device=x.device)
+    B.moe_grouped_mm(_grouped_rows(x), w.contiguous(), offsets.contiguous(), out, B.grouped_workspace(w.shape[0], x.device),
+                     transposed=transposed)
+    return out
+
+
+@grouped_rows.register_fake
+def _grouped_rows_fake(x, w, offsets, transposed=False, complete=False):
+    return x.new_empty((x.shape[0], _check_grouped_args(x, w, offsets, transposed)))
+
+
+@torch.library.custom_op(f"{_LIB}::grouped_wgrad", mutates_args=())
+def grouped_wgrad(a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
+    """moe_grouped_wgrad: [G, columns of a, columns of b]."""
+    _expect(b, "b", a.dtype, (a.shape[0], b.shape[1]))
+    G = offsets.shape[0] - 1
+    dw = torch.empty((G, a.shape[1], b.shape[1]), dtype=a.dtype, device=a.device)
+    B.moe_grouped_wgrad(_grouped_rows(a), _grouped_rows(b), offsets.contiguous(), dw, B.grouped_workspace(G, a.device))
+    return dw
+
+
+@grouped_wgrad.register_fake
+def _grouped_wgrad_fake(a, b, offsets):
+    return a.new_empty((offsets.shape[0] - 1, a.shape[1], b.shape[1]))
+
+
+def _grouped_setup_context(ctx, inputs, output):
+    x, w, offsets, transposed, complete = inputs
+    ctx.save_for_backward(x, w, offsets)
+    ctx.cfg = (transposed, complete)
+
+
+def _grouped_backward_rule(ctx, dout):
+    x, w, offsets = ctx.saved_tensors
+    transposed, complete = ctx.cfg
+    dx = grouped_rows(dout, w, offsets, not transposed, complete) if ctx.needs_input_grad[0] else None
+    dw = None
+    if ctx.needs_input_grad[1]:
+        dw = grouped_wgrad(x, dout, offsets) if transposed else grouped_wgrad(dout, x, offsets)
+    return dx, dw, None, None, None
+
+
+grouped_rows.register_autograd(_grouped_backward_rule, setup_context=_grouped_setup_context)
+
+
+def grouped_mm(x, w, offsets, transposed=False, complete=False):
+    """out[r] = x[r] . w[g]^T for the rows offsets[g] .. offsets[g + 1] - 1 of each group, as one
+    differentiable call: x [R, K] and w [G, N, K] bf16 or fp16 (transposed: w [G, K, N] and
+    out[r] = x[r] . w[g]), offsets int32 [G + 1] on the device; gradients for x and w. Rows of no
+    group come out as zeros, and so does their gradient; `complete` promises that there are none,
+    which saves clearing the result."""
+    return grouped_rows(x, w, offsets, transposed, complete)
 
 
 # the E4M3 copies of the expert weights that moe_layer(..., precision="mxfp8") uses when
