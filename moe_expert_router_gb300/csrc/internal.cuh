@@ -379,7 +379,8 @@ struct NormBackwardLaunch {
     int H, dtype, w_f32, access;
 };
 constexpr int64_t kNormRowsPerBlock = 64;
-int64_t rms_norm_bwd_blocks(int64_t T);
+int64_t rms_norm_bwd_blocks(int64_t T, int64_t H);
+cudaError_t setup_norm_kernels();
 cudaError_t launch_rms_norm(const NormLaunch &p, cudaStream_t st);
 cudaError_t launch_rms_norm_backward(const NormBackwardLaunch &p, cudaStream_t st);
 

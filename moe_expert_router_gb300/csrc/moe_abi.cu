@@ -1662,7 +1662,7 @@ moe_status_t moe_rms_norm(const void *x, const void *residual, const void *weigh
 moe_status_t moe_rms_norm_workspace_size(int64_t T, int64_t H, size_t *bytes) {
     if (bytes == nullptr || T < 0 || H < 1) return MOE_ERR_INVALID_ARG;
     if (H > kNormMaxH || T >= (static_cast<int64_t>(1) << 31)) return MOE_ERR_UNSUPPORTED;
-    *bytes = 4 * static_cast<size_t>(rms_norm_bwd_blocks(T)) * static_cast<size_t>(H);
+    *bytes = 4 * static_cast<size_t>(rms_norm_bwd_blocks(T, H)) * static_cast<size_t>(H);
     return MOE_OK;
 }
 
@@ -1697,7 +1697,7 @@ moe_status_t moe_rms_norm_backward(const void *dy, const void *dh, const void *h
     p.part = static_cast<float *>(ws);
     p.T = s.T;
     p.ld_h = s.ld_x;
-    p.blocks = rms_norm_bwd_blocks(s.T);
+    p.blocks = rms_norm_bwd_blocks(s.T, s.H);
     p.H = static_cast<int>(s.H);
     p.dtype = s.dtype;
     p.w_f32 = s.w_dtype == MOE_DTYPE_F32;

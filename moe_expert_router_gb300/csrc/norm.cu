@@ -117,25 +117,32 @@ __device__ __forceinline__ uint32_t pack2(float2 v, __half) {
 
 // ---------------------------------------------------------------- the kernel
 
-template <typename T, int TPR, int V, int ACCESS>
-__global__ void __launch_bounds__(Lane<T, TPR, V, ACCESS>::THREADS)
+// Blocks of the most threads that an SM has room for: left to itself the compiler takes 88 registers
+// for rows of 7168 (8192 of them with MXFP8: 120 us, 89 with 80), and 100 for those of 16384 (4096 of
+// them: 117 us, 87 with 64).
+template <typename L>
+constexpr int kNormBlocks = L::MOST == 256 ? 3 : (L::MOST == 512 ? 2 : 1);
+
+template <typename L>
+__global__ void __launch_bounds__(L::MOST, kNormBlocks<L>)
 rms_norm_kernel(const NormLaunch p) {
-    using L = Lane<T, TPR, V, ACCESS>;
-    constexpr int N = L::N;
-    __shared__ Pair part[TPR / 32];
+    using T = typename L::T;
+    constexpr int N = L::N, V = L::V;
+    __shared__ Pair part[32];
     griddep_wait();
     const L lane(p.H);
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * L::ROWS + threadIdx.x / TPR;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * L::ROWS + lane.row();
     if (L::ROWS > 1 && t >= p.T) return;                    // whole warps
+    const bool edge = t == 0 || t == p.T - 1;
     const T *x = static_cast<const T *>(p.x) + t * p.ld_x;
     Vec<T> h[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = lane.load(x, v);
+    for (int v = 0; v < V; ++v) h[v] = lane.template load<true>(x, v, edge);
     if (p.residual != nullptr) {
         const T *r = static_cast<const T *>(p.residual) + t * p.ld_r;
         Vec<T> b[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) b[v] = lane.load(r, v);
+        for (int v = 0; v < V; ++v) b[v] = lane.template load<true>(r, v, edge);
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -151,13 +158,16 @@ rms_norm_kernel(const NormLaunch p) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
         all = join(all, {__shfl_xor_sync(kAll, all.hi, d), __shfl_xor_sync(kAll, all.lo, d)});
-    if constexpr (TPR > 32) {
+    if constexpr (!L::WARP) {
         // every warp adds the warps' sums, in one order
         if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = all;
         __syncthreads();
-        all = part[0];
+        constexpr int WARPS = L::MOST / 32;
+        const int w = threadIdx.x & (WARPS - 1);
+        all = w < lane.tpr / 32 ? part[w] : Pair{0.f, 0.f};
 #pragma unroll
-        for (int w = 1; w < TPR / 32; ++w) all = join(all, part[w]);
+        for (int d = WARPS / 2; d > 0; d >>= 1)
+            all = join(all, {__shfl_xor_sync(kAll, all.hi, d), __shfl_xor_sync(kAll, all.lo, d)});
     }
     const Pair r = inverse_root(all, p);
     if (p.rstd != nullptr && lane.i == 0) p.rstd[t] = r.hi;
@@ -180,6 +190,7 @@ rms_norm_kernel(const NormLaunch p) {
             }
         } else {
             uint32_t *out = reinterpret_cast<uint32_t *>(&y.raw);
+            uint32_t apart = 0u;
 #pragma unroll
             for (int j = 0; j < N; j += 2) {
                 const F2 q = mul2(mul2(f2(to_float(h[v].v[j]), to_float(h[v].v[j + 1])), f2(w[j], w[j + 1])), f2(r.hi, r.hi));
@@ -187,10 +198,11 @@ rms_norm_kernel(const NormLaunch p) {
                 constexpr float kOff = 2.384185791015625e-07f;      // 2^-22
                 const uint32_t lo = pack2(split(mul2(q, f2(1.f - kOff, 1.f - kOff))), T());
                 out[j / 2] = pack2(split(mul2(q, f2(1.f + kOff, 1.f + kOff))), T());
-                if (lo != out[j / 2]) {
-                    y.v[j] = rounded_once<T>(to_float(h[v].v[j]), w[j], r);
-                    y.v[j + 1] = rounded_once<T>(to_float(h[v].v[j + 1]), w[j + 1], r);
-                }
+                apart |= lo ^ out[j / 2];
+            }
+            if (apart != 0u) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) y.v[j] = rounded_once<T>(to_float(h[v].v[j]), w[j], r);
             }
         }
         if (p.y != nullptr) lane.store(yo, v, y);
@@ -227,11 +239,10 @@ rms_norm_kernel(const NormLaunch p) {
 
 template <typename T>
 cudaError_t launch_of(const NormLaunch &p, cudaStream_t st) {
-    return with_lane<T>(p.H, p.access, [&](auto lane) {
-        using L = decltype(lane);
+    return with_plan<T>(p.H, p.access, [&](auto plan) {
+        using L = typename decltype(plan)::L;
         const int64_t blocks = (p.T + L::ROWS - 1) / L::ROWS;
-        return launch_dep(rms_norm_kernel<T, L::TPR, L::V, L::ACCESS>, dim3(static_cast<unsigned>(blocks)),
-                          dim3(L::THREADS), 0, st, p);
+        return launch_dep(rms_norm_kernel<L>, dim3(static_cast<unsigned>(blocks)), dim3(plan.threads), 0, st, p);
     });
 }
 

@@ -1,9 +1,10 @@
 // norm.cuh -- shared by the root-mean-square norm's forward (norm.cu) and backward (norm_bwd.cu).
 //
-// A row is held by TPR threads (a warp, or a block) in registers, as V "vectors" of 16 bytes a
-// thread. Aligned rows: vector v of thread i is the row's vector v TPR + i, one 16-byte access. Where only rows that are
-// read lie at odd places (kLoadsOne), the same vector is read element by element. Other rows (odd
-// widths): a vector's elements lie TPR apart, so that a warp's accesses are consecutive elements.
+// A row is held in registers by a warp (up to 64 vectors; eight rows a block) or by a block of as
+// many warps as it fills, as V "vectors" of 16 bytes a thread. Aligned rows: vector v of thread i is
+// the row's vector v threads + i, one 16-byte access. Where only rows that are read lie at odd places
+// (kLoadsOne), it is shifted out of the two aligned vectors around it. Other rows (odd widths): a vector's
+// elements lie `threads` apart, so that a warp's accesses are consecutive elements.
 #pragma once
 
 #include "internal.cuh"
@@ -33,30 +34,46 @@ union Vec {
     T v[kVec<T>];
 };
 
-// The threads of a row and their vectors.
-template <typename T_, int TPR_, int V_, int ACCESS_>
+// The threads of a row and their vectors. MOST: threads of a block at most.
+template <typename T_, int V_, int ACCESS_, bool WARP_, int MOST_>
 struct Lane {
     using T = T_;
-    static constexpr int TPR = TPR_, V = V_, N = kVec<T_>, ACCESS = ACCESS_;
-    static constexpr bool ALIGNED = ACCESS != kOne;
-    static constexpr int ROWS = TPR == 32 ? 8 : 1;          // rows of a block
-    static constexpr int THREADS = TPR * ROWS;
-    int i;                                                  // the thread within its row
-    int H;
-    __host__ __device__ explicit Lane(int h) : i(0), H(h) {
-#ifdef __CUDA_ARCH__
-        i = threadIdx.x % TPR;
-#endif
-    }
-    __device__ int column(int v, int j) const { return ALIGNED ? (v * TPR + i) * N + j : (v * N + j) * TPR + i; }
+    static constexpr int V = V_, N = kVec<T_>, ACCESS = ACCESS_, MOST = MOST_;
+    static constexpr bool ALIGNED = ACCESS != kOne, WARP = WARP_;
+    static constexpr int ROWS = WARP ? 8 : 1;               // rows of a block
+    int tpr, i, H;                                          // the row's threads, and this one among them
+    __device__ explicit Lane(int h) : tpr(WARP ? 32 : blockDim.x), i(WARP ? threadIdx.x % 32 : threadIdx.x), H(h) {}
+    __device__ int row() const { return WARP ? static_cast<int>(threadIdx.x / 32) : 0; }
+    __device__ int column(int v, int j) const { return ALIGNED ? (v * tpr + i) * N + j : (v * N + j) * tpr + i; }
     __device__ bool has(int v, int j = 0) const { return column(v, j) < H; }
-    // vector v of a row (0 past its end); `at_odds`: of one that may lie at an odd place
-    template <bool at_odds = true>
-    __device__ __forceinline__ Vec<T> load(const T *row, int v) const {
+    // vector v of a row (0 past its end); `at_odds`: of one that may lie at an odd place, and `edge`: of
+    // the first or last such row
+    template <bool at_odds = false>
+    __device__ __forceinline__ Vec<T> load(const T *row, int v, bool edge = true) const {
         Vec<T> r;
         r.raw = make_uint4(0u, 0u, 0u, 0u);
         if constexpr (ACCESS == kWhole || (ALIGNED && !at_odds)) {
             if (has(v)) r.raw = *reinterpret_cast<const uint4 *>(row + column(v, 0));
+        } else if constexpr (ALIGNED) {
+            if (!has(v)) return r;
+            const T *at = row + column(v, 0);
+            if (edge) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) r.v[j] = at[j];
+            } else {
+                // the two aligned vectors around it, shifted (both lie between the first row and the last)
+                const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at)) & 15u;
+                const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(at) - off);
+                const uint4 a = p[0], b = p[1];
+                uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int k = 0; k < 6; ++k) w[k] = (off & 8u) ? w[k + 2] : w[k];
+#pragma unroll
+                for (int k = 0; k < 5; ++k) w[k] = (off & 4u) ? w[k + 1] : w[k];
+                const uint32_t bits = (off & 3u) * 8u;
+                r.raw = make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                                   __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j)
@@ -92,36 +109,44 @@ struct Lane {
                 for (int j = 0; j < N; ++j) out[j] = has(v, j) ? __ldg(p + column(v, j)) : 0.f;
             }
         } else {
-            const Vec<T> r = load<false>(static_cast<const T *>(w), v);
+            const Vec<T> r = load(static_cast<const T *>(w), v);
 #pragma unroll
             for (int j = 0; j < N; ++j) out[j] = to_float(r.v[j]);
         }
     }
 };
 
-// Calls f with the lane type of a row of H <= 16384 elements: the fewest threads that hold it in at
-// most four vectors each; a warp up to 128 vectors, eight rows a block.
+// A lane type and its block, as a value that a launch takes its kernel from.
+template <typename T, int V, int ACCESS, bool WARP, int MOST>
+struct Plan {
+    using L = Lane<T, V, ACCESS, WARP, MOST>;
+    int threads;
+};
+
+// Calls f with the plan for a row of H <= 16384 elements. Vectors: four a thread are enough accesses
+// at once, and few warps to add up. Single elements: one vector's worth a thread, since each is an
+// access of its own.
 template <typename T, typename F>
-cudaError_t with_lane(int64_t H, int access, F f) {
-    const int64_t vecs = (H + kVec<T> - 1) / kVec<T>;
+cudaError_t with_plan(int64_t H, int access, F f) {
+    const int vecs = static_cast<int>((H + kVec<T> - 1) / kVec<T>);
+    constexpr int kWide = sizeof(T) == 4 ? 1024 : 512;
+    auto threads = [&](int v) { return ((vecs + v - 1) / v + 31) / 32 * 32; };
+    if (access == kWhole) {
+        if (vecs <= 32) return f(Plan<T, 1, kWhole, true, 256>{256});
+        if (vecs <= 64) return f(Plan<T, 2, kWhole, true, 256>{256});
+        if (vecs <= 256) return f(Plan<T, 2, kWhole, false, 256>{threads(2)});
+        if (vecs <= 1024) return f(Plan<T, 4, kWhole, false, 256>{threads(4)});
+        return f(Plan<T, 4, kWhole, false, kWide>{threads(4)});
+    }
     if (access == kLoadsOne) {
-        if (vecs <= 128) return f(Lane<T, 32, 4, kLoadsOne>(0));
-        if (vecs <= 1024) return f(Lane<T, 256, 4, kLoadsOne>(0));
-        return f(Lane<T, 1024, 4, kLoadsOne>(0));
+        if (vecs <= 64) return f(Plan<T, 2, kLoadsOne, true, 256>{256});
+        if (vecs <= 1024) return f(Plan<T, 4, kLoadsOne, false, 256>{threads(4)});
+        return f(Plan<T, 4, kLoadsOne, false, kWide>{threads(4)});
     }
-    if (access == kOne) {
-        if (vecs <= 128) return f(Lane<T, 32, 4, kOne>(0));
-        if (vecs <= 1024) return f(Lane<T, 256, 4, kOne>(0));
-        return f(Lane<T, 1024, 4, kOne>(0));
-    }
-    if (vecs <= 32) return f(Lane<T, 32, 1, kWhole>(0));
-    if (vecs <= 64) return f(Lane<T, 32, 2, kWhole>(0));
-    if (vecs <= 128) return f(Lane<T, 32, 4, kWhole>(0));
-    if (vecs <= 256) return f(Lane<T, 128, 2, kWhole>(0));
-    if (vecs <= 512) return f(Lane<T, 128, 4, kWhole>(0));
-    if (vecs <= 1024) return f(Lane<T, 256, 4, kWhole>(0));
-    if (vecs <= 2048) return f(Lane<T, 512, 4, kWhole>(0));
-    return f(Lane<T, 1024, 4, kWhole>(0));
+    if (vecs <= 32) return f(Plan<T, 1, kOne, true, 256>{256});
+    if (vecs <= 256) return f(Plan<T, 1, kOne, false, 256>{threads(1)});
+    if (vecs <= 1024) return f(Plan<T, 1, kOne, false, 1024>{threads(1)});
+    return f(Plan<T, 4, kOne, false, kWide>{threads(4)});
 }
 
 }  // namespace
