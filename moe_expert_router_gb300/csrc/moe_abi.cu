@@ -1726,6 +1726,11 @@ moe_status_t moe_grouped_mm(const void *x, const void *w, const int32_t *offsets
     DeviceState *d = nullptr;
     if ((r = device_state(&d)) != MOE_OK) return r;
     const bool kn = (s.flags & MOE_GROUPED_W_KN) != 0;
+    if (!kn && grouped_few(s.R, s.G))
+        return cuda_status(launch_grouped_few(x, w, offsets, out, static_cast<int32_t *>(ws), s.ld_x, s.ld_out,
+                                              static_cast<int>(s.R), static_cast<int>(s.G), static_cast<int>(s.K),
+                                              static_cast<int>(s.N), s.dtype == MOE_DTYPE_F16,
+                                              static_cast<cudaStream_t>(stream)));
     CUtensorMap tm_x, tm_w, tm_out;
     if (!encode_bf16_2d_strided(&tm_x, x, s.K, s.R, s.ld_x, kBK, 128) ||
         !(kn ? encode_bf16_3d(&tm_w, w, s.N, s.K, s.G, 64, kBK)

@@ -154,33 +154,33 @@ rms_norm_bwd_kernel(const NormBackwardLaunch p) {
     }
 }
 
-// dweight[c] = the sum of the blocks' parts, 32 columns a block; 32 rows at a time in fp32, then fp64.
+// dweight[c] = the sum of the blocks' parts, 32 columns a block: a warp's threads take a column each
+// and every 32nd part, 32 of them in a row, and the warps' sums are added by one warp a column.
 template <typename W>
 __global__ void __launch_bounds__(1024)
 rms_norm_dw_kernel(const float *__restrict__ part, int blocks, int H, W *__restrict__ dweight) {
-    __shared__ double sums[32][33];
+    __shared__ float sums[32][33];
     griddep_wait();
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + x;
-    double total = 0.0;
+    float total = 0.f;
     if (c < H) {
         for (int b0 = y; b0 < blocks; b0 += 32 * 32) {
             float s = 0.f;
-#pragma unroll 8
+#pragma unroll
             for (int k = 0; k < 32; ++k) {
                 const int b = b0 + 32 * k;
-                if (b < blocks) s += part[static_cast<int64_t>(b) * H + c];
+                if (b < blocks) s += __ldg(part + static_cast<int64_t>(b) * H + c);
             }
             total += s;
         }
     }
     sums[y][x] = total;
     __syncthreads();
-    if (y == 0 && c < H) {
-#pragma unroll 4
-        for (int k = 1; k < 32; ++k) total += sums[k][x];
-        dweight[c] = from_float<W>(static_cast<float>(total));
-    }
+    total = sums[x][y];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(kAll, total, d);
+    if (x == 0 && blockIdx.x * 32 + y < H) dweight[blockIdx.x * 32 + y] = from_float<W>(total);
 }
 
 template <typename T>

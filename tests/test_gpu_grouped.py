@@ -112,6 +112,30 @@ def test_few_rows(R, G, dtype):
                 assert torch.equal(run(x, matrix, offsets, out, t), want), (K, N, spread, t)
 
 
+@pytest.mark.parametrize("counts", [[64], [0, 17, 0, 30], [9, 8, 7, 0, 16, 1], [1] * 100 + [56] + [0] * 27, [2] * 128, [16, 48]])
+def test_few_rows_of_groups_of_several(counts):
+    """Around the borders of the few-row kernel: groups that take several of its blocks, rows of no group,
+    NaN in those and between rows, bad offsets."""
+    gen = torch.Generator(DEV).manual_seed(len(counts))
+    for start, pad, K, N in ((0, 0, 264, 40), (3, 8, 72, 1032)):
+        offsets, o = offsets_of(counts, start)
+        R, G = o[-1] + 2, len(counts)
+        x = whole(gen, (R, K), BF16)
+        x[:start], x[o[-1]:] = float("nan"), float("inf")
+        x, w = wide(x, pad), whole(gen, (G, N, K), BF16)
+        want = torch.full((R, N), 77.0, dtype=BF16, device=DEV)
+        for g in range(G):
+            want[o[g]:o[g + 1]] = (x[o[g]:o[g + 1]].double() @ w[g].double().t()).to(BF16)
+        out = wide(torch.full((R, N), 77.0, dtype=BF16, device=DEV), pad)
+        assert torch.equal(run(x, w, offsets, out), want)
+        bad = offsets.clone()
+        bad[-1] = R + 1
+        out.fill_(77.0)
+        ws = B.grouped_workspace(G)
+        B.moe_grouped_mm(x, w, bad, out, ws)
+        assert B.moe_get_device_error(ws) == B.DEVERR_BAD_OFFSETS and (out == 77).all()
+
+
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_real_values(dtype):
     gen = torch.Generator(DEV).manual_seed(1)
