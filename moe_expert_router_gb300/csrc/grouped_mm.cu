@@ -2,7 +2,7 @@
 // than the SwiGLU pair of the two stages: out[r] = x[r] . w[g(r)]^T (or . w[g(r)]), its gradients
 // (the same call on dy for dx; dw[g] = dy_g^T x_g), and the MXFP8 form. The products run on the
 // grouped-GEMM kernel (gemm_kernel.cuh, plain modes); the group sizes are read on the device.
-#include "gemm_kernel.cuh"
+#include "pair_gemm.cuh"
 
 namespace moe {
 
@@ -42,6 +42,27 @@ grouped_tiles_kernel(const int32_t *__restrict__ offsets, int G, int R, int32_t 
         mt_prefix[0] = 0;
         if (bad) atomicOr(err, MOE_DEVERR_BAD_OFFSETS);
     }
+}
+
+// The weight gradients' tensor maps, a thread a group: those of a and b with as many rows as end at the
+// group's last one, so that rows behind it are read as zeros. (Of bad offsets nothing is computed.)
+__global__ void __launch_bounds__(256)
+grouped_maps_kernel(const __grid_constant__ CUtensorMap a, const __grid_constant__ CUtensorMap b,
+                    const int32_t *__restrict__ offsets, int G, int R, CUtensorMap *__restrict__ maps) {
+    griddep_wait();
+    const int g = blockIdx.x * 256 + threadIdx.x;
+    if (g >= G) return;
+    const int end = max(1, min(R, offsets[g + 1]));
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(o == 0 ? &a : &b);
+        uint4 *dst = reinterpret_cast<uint4 *>(maps + 2 * g + o);
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(CUtensorMap) / 16); ++i) dst[i] = src[i];
+        asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;"
+                     ::"l"(__cvta_generic_to_global(dst)), "r"(end) : "memory");
+    }
+    asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- a few rows
@@ -206,6 +227,79 @@ cudaError_t launch_grouped_few(const void *x, const void *w, const int32_t *offs
     const cudaError_t e =
         cols == 32 ? launch_dep(f16 ? grouped_few_kernel<2, true> : grouped_few_kernel<2, false>, grid, block, 0, st, p)
                    : launch_dep(f16 ? grouped_few_kernel<1, true> : grouped_few_kernel<1, false>, grid, block, 0, st, p);
+    note_launches(1);
+    return e;
+}
+
+namespace {
+
+template <int MODE>
+cudaError_t setup_pair(int *clusters) {
+    cudaError_t e = cudaFuncSetAttribute(pair_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(kPairSmemBytes));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = kPairSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, pair_gemm_kernel<MODE>, &cfg);
+    if (e == cudaSuccess && n < *clusters) *clusters = n;
+    return e;
+}
+
+template <int MODE>
+cudaError_t launch_pair_of(const PairMaps &maps, const PairArgs &p, int clusters, cudaStream_t st) {
+    return launch_dep(pair_gemm_kernel<MODE>, dim3(2 * clusters), dim3(kPairThreads), kPairSmemBytes, st, maps, p);
+}
+
+}  // namespace
+
+cudaError_t setup_pair_kernels(int *clusters) {
+    cudaError_t e = setup_pair<kPairRows>(clusters);
+    if (e == cudaSuccess) e = setup_pair<kPairRowsT>(clusters);
+    if (e == cudaSuccess) e = setup_pair<kPairWgrad>(clusters);
+    return e;
+}
+
+cudaError_t launch_pair(const PairLaunch &l, GroupedKind kind, cudaStream_t st) {
+    PairArgs p{};
+    p.offsets = l.offsets;
+    p.err = l.err;
+    p.out = static_cast<uint16_t *>(l.out);
+    p.ld_out = l.ld_out;
+    p.R = l.R;
+    p.G = l.G;
+    p.K = l.K;
+    p.N = l.N;
+    p.n_tiles = (l.N + 255) / 256;
+    p.k_tiles = (l.K + 255) / 256;
+    p.f16 = l.f16;
+    p.a_one = l.a_one;
+    p.b_one = l.b_one;
+    p.group_maps = static_cast<const CUtensorMap *>(l.group_maps);
+    if (kind == GroupedKind::wgrad) {
+        const cudaError_t e = launch_dep(grouped_maps_kernel, dim3((l.G + 255) / 256), dim3(256), 0, st, *l.tm_a, *l.tm_b,
+                                         l.offsets, l.G, l.R, static_cast<CUtensorMap *>(l.group_maps));
+        if (e != cudaSuccess) return e;
+        note_launches(1);
+    }
+    const PairMaps maps{*l.tm_a, *l.tm_b, *(l.tm_b_wide != nullptr ? l.tm_b_wide : l.tm_b)};
+    // (at most: the rows' tiles are known on the device alone)
+    const int64_t tiles = kind == GroupedKind::wgrad ? static_cast<int64_t>(l.G) * p.n_tiles * p.k_tiles
+                                                     : (static_cast<int64_t>(l.R) / 256 + (l.R < l.G ? l.R : l.G)) * p.n_tiles;
+    const int clusters = tiles < l.clusters ? static_cast<int>(tiles) : l.clusters;
+    cudaError_t e = cudaErrorInvalidValue;
+    if (kind == GroupedKind::rows) e = launch_pair_of<kPairRows>(maps, p, clusters, st);
+    else if (kind == GroupedKind::rows_t) e = launch_pair_of<kPairRowsT>(maps, p, clusters, st);
+    else if (kind == GroupedKind::wgrad) e = launch_pair_of<kPairWgrad>(maps, p, clusters, st);
     note_launches(1);
     return e;
 }

@@ -404,6 +404,22 @@ cudaError_t launch_grouped_few(const void *x, const void *w, const int32_t *offs
 cudaError_t launch_grouped_mm(const GemmLaunch &p, GroupedKind kind, cudaStream_t st);
 cudaError_t setup_grouped_mm_kernels();
 
+// The grouped products on pairs of SMs (pair_gemm.cuh): rows and rows_t with tm_a the matrices' map, tm_b
+// and tm_b_wide those of x in boxes of 32 and 128 rows; wgrad with tm_a and tm_b those of a and b.
+// `clusters`: pairs that run at a time.
+struct PairLaunch {
+    const CUtensorMap *tm_a, *tm_b, *tm_b_wide;
+    const int32_t *offsets;
+    int32_t *err;
+    void *out;
+    int64_t ld_out;
+    int R, G, K, N, f16, clusters;
+    int a_one, b_one;           // MN-major operands: their maps are encode_bf16_atoms
+    void *group_maps;           // wgrad: two tensor maps a group, written by the launch
+};
+cudaError_t setup_pair_kernels(int *clusters);
+cudaError_t launch_pair(const PairLaunch &l, GroupedKind kind, cudaStream_t st);
+
 // Per-device one-time kernel attribute set-up (dynamic shared memory limits).
 cudaError_t setup_metadata_kernels();
 cudaError_t setup_gemm_kernels();
@@ -418,6 +434,11 @@ bool encode_bf16_2d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t
 // fill out of bounds, 128- or 64-byte swizzle as for encode_bf16_2d.
 bool encode_bf16_3d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows, uint64_t depth,
                     uint32_t box_inner, uint32_t box_rows);
+
+// A [depth, rows, cols] tensor (rows row_stride elements apart, cols a multiple of 64) as 64-column atoms, in
+// boxes of box_rows rows and two atoms: 4-D [depth, cols / 64, rows, 64], without depth (0) 3-D.
+bool encode_bf16_atoms(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t row_stride,
+                       uint64_t depth, uint32_t box_rows);
 
 // bf16 2-D view with an explicit row stride (elements): a column slice of a
 // wider row-major tensor.

@@ -20,6 +20,7 @@ struct DeviceState {
     bool ready = false;
     moe_status_t status = MOE_OK;
     int num_sms = 0;
+    int clusters = 0;           // pairs of CTAs that run at a time
 };
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
@@ -44,7 +45,8 @@ moe_status_t device_state(DeviceState **out) {
         }
         if (major != 10 || minor != 3) {
             d.status = MOE_ERR_UNSUPPORTED;
-        } else if (setup_metadata_kernels() != cudaSuccess || setup_gemm_kernels() != cudaSuccess) {
+        } else if (d.clusters = sms / 2; setup_metadata_kernels() != cudaSuccess || setup_gemm_kernels() != cudaSuccess ||
+                   setup_pair_kernels(&d.clusters) != cudaSuccess || d.clusters < 1) {
             cudaGetLastError();
             return MOE_ERR_CUDA;
         } else {
@@ -703,12 +705,21 @@ bool encode_ready() {
     return g_encode != nullptr;
 }
 
+bool encode_bf16_box(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *byte_strides,
+                     const cuuint32_t *box);
 bool encode_bf16(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims,
                  const cuuint64_t *byte_strides, uint32_t box_inner, uint32_t box_rows) {
     if (!encode_ready()) return false;
     if (box_inner * 2 != 128 && box_inner * 2 != 64) return false;
     cuuint32_t box[3] = {box_inner, box_rows, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
+    return encode_bf16_box(map, base, rank, dims, byte_strides, box);
+}
+
+bool encode_bf16_box(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *byte_strides,
+                     const cuuint32_t *box) {
+    if (!encode_ready()) return false;
+    const uint32_t box_inner = box[0];
+    cuuint32_t estr[4] = {1, 1, 1, 1};
     return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, byte_strides,
                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     box_inner * 2 == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -750,6 +761,14 @@ bool encode_bf16_2d_strided(CUtensorMap *map, const void *base, uint64_t inner, 
     cuuint64_t dims[2] = {inner, rows};
     cuuint64_t strides[1] = {row_stride * 2};
     return encode_bf16(map, base, 2, dims, strides, box_inner, box_rows);
+}
+
+bool encode_bf16_atoms(CUtensorMap *map, const void *base, uint64_t cols, uint64_t rows, uint64_t row_stride,
+                       uint64_t depth, uint32_t box_rows) {
+    cuuint64_t dims[4] = {64, rows, cols / 64, depth};
+    cuuint64_t strides[3] = {row_stride * 2, 128, rows * row_stride * 2};
+    cuuint32_t box[4] = {64, box_rows, 2, 1};
+    return encode_bf16_box(map, base, depth > 0 ? 4 : 3, dims, strides, box);
 }
 
 bool encode_bf16_3d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows, uint64_t depth,
@@ -1499,9 +1518,10 @@ int norm_access(const moe_norm_shape_t &s, bool dense, bool apart) {
     return whole ? (apart ? kWhole : kLoadsOne) : kOne;
 }
 
-// Workspace of the grouped products: header, then counts, starts and tile prefix of the groups.
+// Workspace of the grouped products: header, then counts, starts and tile prefix of the groups (MXFP8), and
+// two tensor maps of each (weight gradients).
 struct GroupedWs {
-    size_t counts, starts, mt_prefix, total;
+    size_t counts, starts, mt_prefix, maps, total;
 };
 
 GroupedWs grouped_layout(int64_t G) {
@@ -1509,7 +1529,8 @@ GroupedWs grouped_layout(int64_t G) {
     w.counts = kWsHeaderBytes;
     w.starts = align256(w.counts + 4 * static_cast<size_t>(G));
     w.mt_prefix = align256(w.starts + 4 * static_cast<size_t>(G));
-    w.total = align256(w.mt_prefix + 4 * static_cast<size_t>(G + 1));
+    w.maps = align256(w.mt_prefix + 4 * static_cast<size_t>(G + 1));
+    w.total = align256(w.maps + 2 * sizeof(CUtensorMap) * static_cast<size_t>(G));
     return w;
 }
 
@@ -1528,6 +1549,22 @@ moe_status_t check_grouped(const moe_grouped_shape_t *s, const void *ws, size_t 
     if ((s->R / kUnitM + s->G) * n_tiles >= most || s->G * n_tiles * k_tiles >= most) return MOE_ERR_UNSUPPORTED;
     if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_INVALID_ARG;
     return ws_bytes < grouped_layout(s->G).total ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+// A launch on pairs of SMs, its tensor maps and output to be filled in.
+PairLaunch pair_launch(const moe_grouped_shape_t &s, const int32_t *offsets, void *ws, const DeviceState &d) {
+    PairLaunch p{};
+    p.offsets = offsets;
+    p.err = static_cast<int32_t *>(ws);
+    p.ld_out = s.ld_out;
+    p.R = static_cast<int>(s.R);
+    p.G = static_cast<int>(s.G);
+    p.K = static_cast<int>(s.K);
+    p.N = static_cast<int>(s.N);
+    p.f16 = s.dtype == MOE_DTYPE_F16;
+    p.clusters = d.clusters;
+    p.group_maps = static_cast<uint8_t *>(ws) + grouped_layout(s.G).maps;
+    return p;
 }
 
 // The groups' tiles into ws, and a launch that reads them.
@@ -1731,25 +1768,20 @@ moe_status_t moe_grouped_mm(const void *x, const void *w, const int32_t *offsets
                                               static_cast<int>(s.R), static_cast<int>(s.G), static_cast<int>(s.K),
                                               static_cast<int>(s.N), s.dtype == MOE_DTYPE_F16,
                                               static_cast<cudaStream_t>(stream)));
-    CUtensorMap tm_x, tm_w, tm_out;
-    if (!encode_bf16_2d_strided(&tm_x, x, s.K, s.R, s.ld_x, kBK, 128) ||
-        !(kn ? encode_bf16_3d(&tm_w, w, s.N, s.K, s.G, 64, kBK)
-             : encode_bf16_2d(&tm_w, w, s.K, static_cast<uint64_t>(s.G) * s.N, kBK, 256)) ||
-        !encode_bf16_2d_strided(&tm_out, out, s.N, s.R, s.ld_out, 64, 32))
+    const bool one = s.N % 64 == 0;
+    CUtensorMap tm_x, tm_wide, tm_w;
+    if (!encode_bf16_2d_strided(&tm_x, x, s.K, s.R, s.ld_x, kBK, 32) ||
+        !encode_bf16_2d_strided(&tm_wide, x, s.K, s.R, s.ld_x, kBK, 128) ||
+        !(kn ? (one ? encode_bf16_atoms(&tm_w, w, s.N, s.K, s.N, s.G, kBK) : encode_bf16_3d(&tm_w, w, s.N, s.K, s.G, 64, kBK))
+             : encode_bf16_2d(&tm_w, w, s.K, static_cast<uint64_t>(s.G) * s.N, kBK, 128)))
         return MOE_ERR_CUDA;
-    GemmLaunch p;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if ((r = grouped_launch(s, offsets, ws, *d, st, &p)) != MOE_OK) return r;
-    p.tm_a = &tm_x;
-    p.tm_b = &tm_w;
-    p.tm_out = &tm_out;
-    p.out = static_cast<__nv_bfloat16 *>(out);
-    p.K = static_cast<int>(s.K);
-    p.n_out = static_cast<int>(s.N);
-    p.n_tile = kBN;
-    p.b_rows = static_cast<int>(s.N);
-    p.out_ld = static_cast<int>(s.ld_out);
-    return cuda_status(launch_grouped_mm(p, kn ? GroupedKind::rows_t : GroupedKind::rows, st));
+    PairLaunch p = pair_launch(s, offsets, ws, *d);
+    p.tm_a = &tm_w;
+    p.tm_b = &tm_x;
+    p.tm_b_wide = &tm_wide;
+    p.a_one = one;
+    p.out = out;
+    return cuda_status(launch_pair(p, kn ? GroupedKind::rows_t : GroupedKind::rows, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status_t moe_grouped_wgrad(const void *a, const void *b, const int32_t *offsets, const moe_grouped_shape_t *shape,
@@ -1764,20 +1796,20 @@ moe_status_t moe_grouped_wgrad(const void *a, const void *b, const int32_t *offs
         return MOE_ERR_INVALID_ARG;
     DeviceState *d = nullptr;
     if ((r = device_state(&d)) != MOE_OK) return r;
-    CUtensorMap tm_a, tm_b, tm_dw;
-    if (!encode_bf16_2d_strided(&tm_a, a, s.N, s.R, s.ld_out, 64, kBK) ||
-        !encode_bf16_2d_strided(&tm_b, b, s.K, s.R, s.ld_x, 64, kBK) ||
-        !encode_bf16_3d(&tm_dw, dw, s.K, s.N, s.G, 32, 32))
+    CUtensorMap tm_a, tm_b;
+    const bool a_one = s.N % 64 == 0, b_one = s.K % 64 == 0;
+    if (!(a_one ? encode_bf16_atoms(&tm_a, a, s.N, s.R, s.ld_out, 0, kBK)
+                : encode_bf16_2d_strided(&tm_a, a, s.N, s.R, s.ld_out, 64, kBK)) ||
+        !(b_one ? encode_bf16_atoms(&tm_b, b, s.K, s.R, s.ld_x, 0, kBK)
+                : encode_bf16_2d_strided(&tm_b, b, s.K, s.R, s.ld_x, 64, kBK)))
         return MOE_ERR_CUDA;
-    GemmLaunch p;
-    if ((r = grouped_launch(s, offsets, ws, *d, st, &p)) != MOE_OK) return r;
+    PairLaunch p = pair_launch(s, offsets, ws, *d);
     p.tm_a = &tm_a;
     p.tm_b = &tm_b;
-    p.tm_out = &tm_dw;
-    p.n_out = static_cast<int>(s.K);
-    p.n_tile = kBN;
-    p.m_total = static_cast<int>(s.N);
-    return cuda_status(launch_grouped_mm(p, GroupedKind::wgrad, st));
+    p.out = dw;
+    p.a_one = a_one;
+    p.b_one = b_one;
+    return cuda_status(launch_pair(p, GroupedKind::wgrad, st));
 }
 
 moe_status_t moe_grouped_mm_mx(const void *x_codes, const void *x_scales, const void *w_codes, const void *w_scales,

@@ -1,0 +1,496 @@
+// pair_gemm.cuh -- the grouped products on pairs of SMs: a cluster of two CTAs multiplies one tile
+// of 256 x 256 with cta_group::2 MMAs, each holding half of both operands and 128 rows of the
+// accumulator. At the bytes per flop of the one-CTA kernel's 256 x 256 unit (32 KB a CTA for a
+// 64-deep k-block of 128 x 256) that leaves half of tensor memory free, so the accumulator is
+// doubled and a tile's epilogue runs under the next tile's MMAs: what the weight gradients, whose
+// tiles add up a group's few rows only, spend half of their time on otherwise.
+//
+//   kPairRows   out[r, n] = x[r, :] . w[g, n, :]     w [G, N, K], K-major
+//   kPairRowsT  out[r, n] = x[r, :] . w[g, :, n]     w [G, K, N], MN-major
+//   kPairWgrad  dw[g, n, k] = sum over g's rows of a[r, n] b[r, k]
+//
+// In the first two the matrix is the MMA's A (256 columns n of out as its M) and the rows are its B:
+// N is any multiple of 32, so a tile takes little more tensor time than its rows need, and a group's rows
+// are cut into equal tiles (384 rows: two of 192). A lane of tensor memory is then a column of out
+// and the accumulator's columns are rows: the epilogue's stores of one row are 64 consecutive bytes
+// of a warp. In the third both operands are read MN-major over the group's rows. Its last k-block may
+// reach behind them, into rows of the next group, which may hold NaN: every group has tensor maps of
+// its own that end where it does, so that the copy engine fills zeros there (grouped_maps_kernel).
+// (Warps that zeroed those rows in shared memory cost 112 of 330 us for 24576 rows of 64 groups,
+// 2048 x 2816: the MMAs waited for them at every tile's end.)
+//
+// Roles of a CTA: warp 0 loads its halves with TMA onto the leader's barriers; warp 1 of the leader
+// issues the MMAs; warps 2 .. 9 are the epilogue. Tiles are dealt to the clusters in turn. Every CTA
+// reads the group offsets itself.
+#pragma once
+
+#include "gemm_kernel.cuh"
+
+namespace moe {
+
+namespace {
+
+enum PairMode : int { kPairRows = 0, kPairRowsT = 1, kPairWgrad = 2 };
+
+constexpr int kPairHalf = 128 * BK * 2;     // bytes of a CTA's half of one operand's k-block
+constexpr int kPairBoxRows = 32;            // rows of x in one copy: of these, or of 128
+constexpr int kMaxGroups = 1024;
+
+constexpr int kPairStages = 6;
+constexpr int kPairThreads = 64 + EPI_THREADS;
+template <int MODE> constexpr bool kPairAMn = MODE != kPairRows;
+template <int MODE> constexpr bool kPairBMn = MODE == kPairWgrad;
+
+struct __align__(1024) PairSmem {
+    uint8_t a[kPairStages][kPairHalf];
+    uint8_t b[kPairStages][kPairHalf];
+    uint8_t box[EPI_WARPS][32 * 64];        // kPairWgrad: a warp's 32 x 32 output box
+    uint64_t full[kPairStages];             // the leader's: both CTAs' halves have landed
+    uint64_t empty[kPairStages];            // the MMAs have read the stage
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];                  // the leader's: every epilogue warp of both CTAs has read it
+    uint64_t drain;
+    int start[kMaxGroups + 1];              // the groups' first rows
+    int tiles[kMaxGroups + 1];              // prefix of their row tiles (of 256 rows at most)
+    int scan[32];
+    uint32_t tmem_base;
+    int abort;
+};
+constexpr size_t kPairSmemBytes = sizeof(PairSmem) + 1024;
+static_assert(kPairSmemBytes <= 227 * 1024, "shared memory of a CTA");
+
+struct PairArgs {
+    const int32_t *offsets;
+    int32_t *err;
+    uint16_t *out;
+    int64_t ld_out;
+    int R, G;
+    int K;                  // rows: the reduction; kPairWgrad: columns of dw
+    int N;                  // columns of out; kPairWgrad: rows of dw
+    int n_tiles, k_tiles;
+    int f16;
+    int a_one, b_one;       // MN-major operands: both 64-column atoms in one copy
+    const CUtensorMap *group_maps;  // kPairWgrad: a's and b's of each group
+};
+struct PairMaps {
+    CUtensorMap a, b;
+    CUtensorMap b_wide;     // rows: x in boxes of 128 rows
+};
+
+// ---------------------------------------------------------------- cluster and pair instructions
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The leader's copy of a shared-memory object of this CTA.
+__device__ __forceinline__ uint32_t leader_addr(uint32_t addr) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+// Arrives on a barrier of either CTA. What it tells of (reads of tensor memory, which tcgen05.wait::ld has
+// seen completed) needs no release at the cluster's scope, which waits until this SM's stores to global
+// memory have been seen. (With it, in every k-block, the kernel took 2.4 times as long; at the
+// accumulators' release the weight gradients of 32 groups of 256 rows, 7168 x 4096, 591 us, and 439 without.)
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Loads into this CTA's shared memory that complete on a barrier of either CTA of the pair.
+__device__ __forceinline__ void pair_load_2d(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z,
+                                             uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+// Both 64-column atoms of a matrix's k-block: inner coordinate 0, then k, atom and group.
+__device__ __forceinline__ void pair_load_4d(uint32_t dst, const CUtensorMap *map, int32_t y, int32_t z, int32_t g,
+                                             uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(g), "r"(bar) : "memory");
+}
+// Before the first use of a tensor map that a kernel wrote.
+__device__ __forceinline__ void tensormap_acquire(const CUtensorMap *map) {
+    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+// Arrives on `bar` in both CTAs when the MMAs issued so far are done.
+__device__ __forceinline__ void pair_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+
+// ---------------------------------------------------------------- tiles
+
+struct PairTile {
+    int g, n0;              // group, first column of out (row of dw)
+    int row0, rows;         // rows of x (of this tile), or of the group
+    int k0;                 // kPairWgrad: first column of dw
+    int nkb;                // k-blocks
+};
+
+template <int MODE>
+__device__ __forceinline__ PairTile pair_tile(int u, const PairSmem &sm, const PairArgs &p) {
+    PairTile t;
+    if constexpr (MODE == kPairWgrad) {
+        const int per = p.n_tiles * p.k_tiles;
+        t.g = u / per;
+        const int rem = u - t.g * per;
+        const int n = rem / p.k_tiles;
+        t.n0 = n * 256;
+        t.k0 = (rem - n * p.k_tiles) * 256;
+        t.row0 = sm.start[t.g];
+        t.rows = sm.start[t.g + 1] - t.row0;
+        t.nkb = (t.rows + BK - 1) / BK;
+    } else {
+        int lo = 0, hi = p.G;               // tiles of group g: [tiles[g], tiles[g + 1]) * n_tiles
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (sm.tiles[mid] * p.n_tiles <= u) lo = mid; else hi = mid;
+        }
+        const int mine = sm.tiles[lo + 1] - sm.tiles[lo];
+        const int local = u - sm.tiles[lo] * p.n_tiles;
+        const int n = local / mine, m = local - n * mine;
+        const int rows = sm.start[lo + 1] - sm.start[lo];
+        const int each = ((rows + mine - 1) / mine + 31) & ~31;
+        t.g = lo;
+        t.n0 = n * 256;
+        t.k0 = 0;
+        t.row0 = sm.start[lo] + m * each;
+        t.rows = min(each, rows - m * each);
+        t.nkb = (p.K + BK - 1) / BK;
+    }
+    return t;
+}
+
+// kPairWgrad: this CTA's halves of 64 rows of a and b from `row` on.
+__device__ __forceinline__ void pair_load_rows(uint32_t sa, uint32_t sb, const CUtensorMap *ma, const CUtensorMap *mb,
+                                               const PairArgs &p, const PairTile &t, uint32_t rank, int row, uint32_t bar) {
+    const int n = t.n0 + 128 * static_cast<int>(rank), k = t.k0 + 128 * static_cast<int>(rank);
+    if (p.a_one) {
+        pair_load_3d(sa, ma, 0, row, n / 64, bar);
+    } else {
+        pair_load_2d(sa, ma, n, row, bar);
+        pair_load_2d(sa + MN_ATOM_BYTES, ma, n + 64, row, bar);
+    }
+    if (p.b_one) {
+        pair_load_3d(sb, mb, 0, row, k / 64, bar);
+    } else {
+        pair_load_2d(sb, mb, k, row, bar);
+        pair_load_2d(sb + MN_ATOM_BYTES, mb, k + 64, row, bar);
+    }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
+    griddep_launch_dependents();
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    PairSmem &sm = *reinterpret_cast<PairSmem *>(smem_raw + ((1024u - (raw & 1023u)) & 1023u));
+    volatile int *abort_flag = &sm.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(smem_addr(&sm.full[s]), 1);
+            mbar_init(smem_addr(&sm.empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_addr(&sm.acc_full[b]), 1);
+            mbar_init(smem_addr(&sm.acc_empty[b]), 2 * EPI_WARPS);
+        }
+        mbar_init(smem_addr(&sm.drain), 1);
+        sm.abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&maps.a);
+        tma_prefetch_desc(&maps.b);
+        tma_prefetch_desc(&maps.b_wide);
+    }
+    if (warp == 1) pair_tmem_alloc(smem_addr(&sm.tmem_base), 512);
+    tc_fence_before();
+    griddep_wait();
+
+    // The groups' rows and the prefix of their tiles. Offsets that decrease or leave [0, R] would send a
+    // product out of its operands: then no group has rows, and the error word says so.
+    constexpr int PER = 4;                  // groups a thread
+    static_assert(PER * kPairThreads >= kMaxGroups, "every group has a thread");
+    int first[PER], count[PER], sum = 0;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int g = threadIdx.x * PER + i;
+        first[i] = g < p.G ? p.offsets[g] : 0;
+        const int end = g < p.G ? p.offsets[g + 1] : 0;
+        bad |= g < p.G && (first[i] < 0 || end < first[i] || end > p.R);
+        count[i] = end - first[i];
+        sum += (count[i] + 255) / 256;
+    }
+    bad = __syncthreads_or(bad);
+    if (bad) sum = 0;
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) sm.scan[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += sm.scan[w];
+    int before = incl - sum;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int g = threadIdx.x * PER + i;
+        if (g < p.G) {
+            sm.start[g] = bad ? 0 : first[i];
+            if (g == p.G - 1) sm.start[p.G] = bad ? 0 : first[i] + count[i];
+            sm.tiles[g] = before;
+            before += bad ? 0 : (count[i] + 255) / 256;
+            if (g == p.G - 1) sm.tiles[p.G] = before;
+        }
+    }
+    if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, MOE_DEVERR_BAD_OFFSETS);
+    __syncthreads();
+    cluster_sync();                         // both CTAs' barriers and tensor memory are set up
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    const int total = MODE == kPairWgrad ? p.G * p.n_tiles * p.k_tiles : sm.tiles[p.G] * p.n_tiles;
+
+    if (warp == 0) {
+        // ------------------------------------------------ loads
+        if (lane == 0) {
+            int it = 0, seen = -1;
+            bool ok = true;
+            for (int u = cluster; ok && u < total; u += clusters) {
+                const PairTile t = pair_tile<MODE>(u, sm, p);
+                const CUtensorMap *ma = &maps.a, *mb = &maps.b;
+                if constexpr (MODE == kPairWgrad) {
+                    ma = p.group_maps + 2 * t.g;
+                    mb = ma + 1;
+                    if (t.g != seen) {
+                        tensormap_acquire(ma);
+                        tensormap_acquire(mb);
+                        seen = t.g;
+                    }
+                }
+                const int half = MODE == kPairWgrad ? 128 : ((t.rows + 31) & ~31) / 2;   // of the MMA's N in this CTA
+                const bool wide = MODE == kPairWgrad || half > 64;
+                const int boxes = (half + kPairBoxRows - 1) / kPairBoxRows;
+                const uint32_t bytes = kPairHalf + (wide ? kPairHalf : boxes * kPairBoxRows * BK * 2);
+                const int n = t.n0 + 128 * static_cast<int>(rank);
+                for (int kb = 0; kb < t.nkb; ++kb, ++it) {
+                    const int s = it % kPairStages;
+                    if (!mbar_wait(smem_addr(&sm.empty[s]), ((it / kPairStages) & 1) ^ 1u, abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sa = smem_addr(sm.a[s]), sb = smem_addr(sm.b[s]);
+                    // (the leader expects both CTAs' bytes: an arrival of the other with release at the
+                    // cluster's scope in every k-block made the kernel 2.4 times slower)
+                    const uint32_t bar = leader_addr(smem_addr(&sm.full[s]));
+                    if (rank == 0) mbar_arrive_expect_tx(smem_addr(&sm.full[s]), 2 * bytes);
+                    if constexpr (MODE == kPairRows) {
+                        pair_load_2d(sa, &maps.a, kb * BK, t.g * p.N + n, bar);
+                    } else if constexpr (MODE == kPairRowsT) {
+                        if (p.a_one) {
+                            pair_load_4d(sa, &maps.a, kb * BK, n / 64, t.g, bar);
+                        } else {
+                            pair_load_3d(sa, &maps.a, n, kb * BK, t.g, bar);
+                            pair_load_3d(sa + MN_ATOM_BYTES, &maps.a, n + 64, kb * BK, t.g, bar);
+                        }
+                    } else {
+                        pair_load_rows(sa, sb, ma, mb, p, t, rank, t.row0 + kb * BK, bar);
+                    }
+                    if constexpr (MODE != kPairWgrad) {
+                        const int r = t.row0 + half * static_cast<int>(rank);
+                        if (wide) {
+                            pair_load_2d(sb, &maps.b_wide, kb * BK, r, bar);
+                        } else {
+                            for (int i = 0; i < boxes; ++i)
+                                pair_load_2d(sb + i * kPairBoxRows * BK * 2, &maps.b, kb * BK, r + i * kPairBoxRows, bar);
+                        }
+                    }
+                }
+            }
+            // the last arrivals on this CTA's barriers have come before it ends
+            for (int i = max(0, it - kPairStages); ok && i < it; ++i)
+                ok = mbar_wait(smem_addr(&sm.empty[i % kPairStages]), (i / kPairStages) & 1, abort_flag, p.err);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMAs, of both CTAs by the leader
+        if (rank == 0 && lane == 0) {
+            int it = 0, n_done = 0;
+            bool ok = true, any = false;
+            for (int u = cluster; ok && u < total; u += clusters, ++n_done) {
+                const PairTile t = pair_tile<MODE>(u, sm, p);
+                const int buf = n_done & 1;
+                if (!mbar_wait(smem_addr(&sm.acc_empty[buf]), ((n_done >> 1) & 1) ^ 1u, abort_flag, p.err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int n_mma = MODE == kPairWgrad ? 256 : (t.rows + 31) & ~31;
+                uint32_t idesc = idesc_bf16_f32(256, n_mma) | (kPairAMn<MODE> ? (1u << 15) : 0u) |
+                                 (kPairBMn<MODE> ? (1u << 16) : 0u);
+                if (p.f16) idesc &= ~((1u << 7) | (1u << 10));
+                for (int kb = 0; kb < t.nkb; ++kb, ++it) {
+                    const int s = it % kPairStages;
+                    if (!mbar_wait(smem_addr(&sm.full[s]), (it / kPairStages) & 1, abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_addr(sm.a[s]), sb = smem_addr(sm.b[s]);
+#pragma unroll
+                    for (int kk = 0; kk < BK / UMMA_K; ++kk)
+                        pair_mma(tmem + buf * 256, operand_desc<kPairAMn<MODE>>(sa, kk), operand_desc<kPairBMn<MODE>>(sb, kk),
+                                 idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                    pair_commit(smem_addr(&sm.empty[s]));
+                    any = true;
+                }
+                if (!ok) break;
+                pair_commit(smem_addr(&sm.acc_full[buf]));      // at once without k-blocks: the epilogue writes zeros
+            }
+            if (!ok && any) {
+                pair_commit(smem_addr(&sm.drain));
+                drain_wait(smem_addr(&sm.drain), 0);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ epilogue
+        const int quad = warp & 3, side = (warp - 2) >> 2;      // lanes of tensor memory, half of the columns
+        const uint32_t tacc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 128 * side;
+        const uint32_t buf_addr = smem_addr(sm.box[warp - 2]);
+        const bool f16 = p.f16 != 0;
+        int n_done = 0;
+        for (int u = cluster; u < total; u += clusters, ++n_done) {
+            const PairTile t = pair_tile<MODE>(u, sm, p);
+            const int buf = n_done & 1;
+            bool ok = true;
+            if (lane == 0) ok = mbar_wait(smem_addr(&sm.acc_full[buf]), (n_done >> 1) & 1, abort_flag, p.err);
+            if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+            tc_fence_after();
+            const int n = t.n0 + 128 * static_cast<int>(rank) + 32 * quad;      // the warp's first lane
+            const uint32_t released = leader_addr(smem_addr(&sm.acc_empty[buf]));
+            if constexpr (MODE != kPairWgrad) {
+                uint16_t *dst = p.out + t.row0 * p.ld_out + n + lane;
+                const bool live = n + lane < p.N;
+                const int end = min(t.rows, 128 * side + 128);
+#pragma unroll 1
+                for (int c = 128 * side; c < end; c += 64) {
+                    uint32_t v[2][32];
+                    tmem_ld32(tacc + 256 * buf + (c - 128 * side), v[0]);
+                    if (c + 32 < end) tmem_ld32(tacc + 256 * buf + (c + 32 - 128 * side), v[1]);
+                    tmem_wait_ld();
+                    tmem_reg_fence(v[0]);
+                    tmem_reg_fence(v[1]);
+                    if (c + 64 >= end) {                    // read out: free for the tile after next
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_peer(released);
+                    }
+                    if (live) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            uint16_t *at = dst + (c + 32 * j) * p.ld_out;
+                            const int m = t.rows - c - 32 * j;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                if (i < m) *at = static_cast<uint16_t>(pack_16x2(__uint_as_float(v[j][i]), 0.f, f16));
+                                at += p.ld_out;
+                            }
+                        }
+                    }
+                }
+                if (end <= 128 * side) {                    // no rows on this side
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_peer(released);
+                }
+            } else {
+                // the warp's 128 columns in registers first, so that the accumulator is free for the tile
+                // after next while they are stored
+                const int k = t.k0 + 128 * side;
+                const bool work = k < p.K && n < p.N;
+                uint32_t pk[4][16];
+                if (work && t.rows > 0) {
+                    scaled_piece2(tacc + 256 * buf, 0, 1.0f, pk[0], pk[1], f16);
+                    scaled_piece2(tacc + 256 * buf, 64, 1.0f, pk[2], pk[3], f16);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) pk[i >> 4][i & 15] = 0u;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_peer(released);
+                if (!work) continue;
+                // turned in shared memory, so that a store covers 64 bytes of eight rows
+                const int row = lane >> 2, chunk = lane & 3;
+                uint16_t *dst = p.out + (static_cast<int64_t>(t.g) * p.N + n + row) * p.K + k + 8 * chunk;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    stage_row32(buf_addr, lane, pk[c]);
+                    __syncwarp();
+                    uint4 v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = ld_shared_v4(buf_addr + swizzled_chunk<64>(8 * i + row, chunk));
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (n + 8 * i + row < p.N && k + 32 * c + 8 * chunk < p.K)
+                            *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(8 * i) * p.K + 32 * c) = v[i];
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                         // nothing of the pair reads this CTA's memory or barriers any more
+    if (sm.abort) {
+        // copies in flight may not land in memory that another block has by then
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < kDrainLimitNs) __nanosleep(100000);
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        pair_tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace
+
+}  // namespace moe
