@@ -37,13 +37,8 @@
 // kind::mxf8f6f4.block_scale MMAs on E4M3 operands with E8M0 scales per 32
 // K-elements. The scales are k-block-major 32-bit words; each stage's words
 // arrive by TMA on a barrier of their own and the helper warps copy them into
-// tensor memory.
-//
-// Plain modes (products grouped by expert, grouped_mm.cu): kRows out[r] = x[r] .
-// w[e]^T with w [E, N, K], kRowsT out[r] = x[r] . w[e] with w [E, K, N] (MN-major),
-// kRowsWgrad dw[e] = sum over e's rows of a[r]^T b[r], kRowsMx kRows on MXFP8
-// operands. bf16 or fp16 operands (one bit of the instruction descriptor and the
-// epilogue's conversion); rows may lie apart.
+// tensor memory. kRowsMx is stage 2's product on its own (grouped_mm.cu): no routing
+// weights, rows of the output apart.
 //
 // Kernel design (one CTA per SM, persistent):
 //   work unit  = (expert e, n-tile, 256-row tile of e's routed rows) for the
@@ -112,16 +107,15 @@ enum Mode : int {
     kStage1Mx = 8,              // stage 1 in MXFP8: E4M3 x and w1, a quantized in the epilogue
     kStage2Mx = 9,              // stage 2 in MXFP8: E4M3 a and w2
     kWgradMx = 10,              // MXFP8 weight gradient: operands quantized along the expert's routed rows
-    kRows = 11, kRowsT = 12, kRowsWgrad = 13, kRowsMx = 14      // plain grouped products
+    kRowsMx = 11                // MXFP8 grouped product alone
 };
 
 template <int MODE> constexpr bool kIsMx = MODE == kStage1Mx || MODE == kStage2Mx || MODE == kWgradMx || MODE == kRowsMx;
 template <int MODE> constexpr bool kIsStage1 = MODE == kStage1 || MODE == kStage1SaveH || MODE == kStage1Mx;
-template <int MODE> constexpr bool kRing = MODE == kStage1 || MODE == kStage2 || MODE == kRows;
-template <int MODE> constexpr bool kAMn = MODE == kBwdDW2 || MODE == kBwdDW1 || MODE == kRowsWgrad;
-template <int MODE> constexpr bool kBMn = (MODE >= kBwdDA && MODE <= kBwdDW1) || MODE == kRowsT || MODE == kRowsWgrad;
-template <int MODE> constexpr bool kWeightGrad = MODE == kBwdDW2 || MODE == kBwdDW1 || MODE == kRowsWgrad;
-template <int MODE> constexpr bool kPlain = MODE == kRows || MODE == kRowsT || MODE == kRowsWgrad || MODE == kRowsMx;
+template <int MODE> constexpr bool kRing = MODE == kStage1 || MODE == kStage2;
+template <int MODE> constexpr bool kAMn = MODE == kBwdDW2 || MODE == kBwdDW1;
+template <int MODE> constexpr bool kBMn = MODE >= kBwdDA && MODE <= kBwdDW1;
+template <int MODE> constexpr bool kWeightGrad = MODE == kBwdDW2 || MODE == kBwdDW1;
 // units (expert, m-tile, n-tile) reducing over the expert's rows, written per expert
 template <int MODE> constexpr bool kPerExpertOut = kWeightGrad<MODE> || MODE == kWgradMx;
 // warps 10..13: the reduction-tail zeroing of the weight gradients, and in the
@@ -236,7 +230,6 @@ struct GemmArgs {
                                 //   quantized operands, a multiple of 128 (rows padded to whole k-blocks)
     const uint8_t *bpack;       // stage 1 / 2: the tile-packed weights (pack.cu), or null for the TMA views
     int kb_tiles;               // K tiles per packed weight slab
-    int f16;                    // plain modes: operands and outputs are fp16 (else bf16)
     int total_units;            // router / weight gradients: known on the host; else -1
 };
 
@@ -468,19 +461,10 @@ __device__ __forceinline__ void swiglu_piece(uint32_t tacc, int c, uint32_t (&pk
                             silu_mul(__uint_as_float(gv[2 * i + 1]), __uint_as_float(uv[2 * i + 1])));
 }
 
-// Two fp32 values rounded to the plain modes' 16-bit type.
-__device__ __forceinline__ uint32_t pack_16x2(float lo, float hi, bool f16) {
-    if (f16) {
-        const __half2 v = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&v);
-    }
-    return pack_bf16x2(lo, hi);
-}
-
-// 64 accumulator columns [c, c+64) scaled by w, packed to bf16 (fp16 with f16): both
-// loads in flight before the one wait.
+// 64 accumulator columns [c, c+64) scaled by w, packed to bf16: both loads in
+// flight before the one wait.
 __device__ __forceinline__ void scaled_piece2(uint32_t tacc, int c, float w, uint32_t (&pk0)[16],
-                                              uint32_t (&pk1)[16], bool f16 = false) {
+                                              uint32_t (&pk1)[16]) {
     uint32_t v0[32], v1[32];
     tmem_ld32(tacc + c, v0);
     tmem_ld32(tacc + c + 32, v1);
@@ -489,8 +473,8 @@ __device__ __forceinline__ void scaled_piece2(uint32_t tacc, int c, float w, uin
     tmem_reg_fence(v1);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        pk0[i] = pack_16x2(w * __uint_as_float(v0[2 * i]), w * __uint_as_float(v0[2 * i + 1]), f16);
-        pk1[i] = pack_16x2(w * __uint_as_float(v1[2 * i]), w * __uint_as_float(v1[2 * i + 1]), f16);
+        pk0[i] = pack_bf16x2(w * __uint_as_float(v0[2 * i]), w * __uint_as_float(v0[2 * i + 1]));
+        pk1[i] = pack_bf16x2(w * __uint_as_float(v1[2 * i]), w * __uint_as_float(v1[2 * i + 1]));
     }
 }
 
@@ -511,15 +495,15 @@ __device__ __forceinline__ void load_h_piece(const __nv_bfloat16 *hrow, int half
     }
 }
 
-// 32 accumulator columns [c, c+32) scaled by w, packed to bf16 (fp16 with f16).
-__device__ __forceinline__ void scaled_piece(uint32_t tacc, int c, float w, uint32_t (&pk)[16], bool f16 = false) {
+// 32 accumulator columns [c, c+32) scaled by w, packed to bf16.
+__device__ __forceinline__ void scaled_piece(uint32_t tacc, int c, float w, uint32_t (&pk)[16]) {
     uint32_t v[32];
     tmem_ld32(tacc + c, v);
     tmem_wait_ld();
     tmem_reg_fence(v);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-        pk[i] = pack_16x2(w * __uint_as_float(v[2 * i]), w * __uint_as_float(v[2 * i + 1]), f16);
+        pk[i] = pack_bf16x2(w * __uint_as_float(v[2 * i]), w * __uint_as_float(v[2 * i + 1]));
 }
 
 // One stage's scale words, from the tail of its B slot, in the tensor-memory
@@ -723,7 +707,7 @@ tc_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
                         tma_load_2d(sa, &maps.a, kx, t.row0, full);
                         if (two) tma_load_2d(sa + A_HALF_BYTES, &maps.a, kx, t.row0 + BM, full);
                         tma_load_2d(sb, &maps.b, kx, t.n * kUnitN<MODE>, full);
-                    } else if constexpr (MODE == kStage2 || MODE == kStage2Mx || MODE == kRows || MODE == kRowsMx) {
+                    } else if constexpr (MODE == kStage2 || MODE == kStage2Mx || MODE == kRowsMx) {
                         const int kx = kb * kStageK<MODE>;
                         tma_load_2d(sa, &maps.a, kx, t.row0, full);
                         if (two) tma_load_2d(sa + A_HALF_BYTES, &maps.a, kx, t.row0 + BM, full);
@@ -750,7 +734,7 @@ tc_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
                             if (two) tma_load_2d(sa + A_HALF_BYTES, &maps.a, kx, t.row0 + BM, full);
                             tma_load_2d(sb, &maps.b, kx, seg * g.E + t.n * BN, full);
                         }
-                    } else if constexpr (MODE == kBwdDA || MODE == kBwdDX || MODE == kRowsT) {
+                    } else if constexpr (MODE == kBwdDA || MODE == kBwdDX) {
                         // dA: dispatched dY rows; dX: dH rows
                         tma_load_2d(sa, &maps.a, kb * BK, t.row0, full);
                         if (two) tma_load_2d(sa + A_HALF_BYTES, &maps.a, kb * BK, t.row0 + BM, full);
@@ -873,10 +857,7 @@ tc_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
                         }
                     } else {
                         // the router's N follows E; the expert GEMMs use the full 256
-                        // (plain modes: operand formats 0, fp16, in place of 1, bf16)
-                        const uint32_t idesc = MODE == kRouter ? idesc_bf16_f32(BM, g.n_mma)
-                                               : kPlain<MODE> && g.f16 ? kIdesc<MODE> & ~((1u << 7) | (1u << 10))
-                                                                       : kIdesc<MODE>;
+                        const uint32_t idesc = MODE == kRouter ? idesc_bf16_f32(BM, g.n_mma) : kIdesc<MODE>;
 #pragma unroll
                         for (int kk = 0; kk < BK / UMMA_K; ++kk) {
                             const uint32_t acc = (kb > t.kb0 || kk > 0) ? 1u : 0u;
@@ -954,8 +935,6 @@ tc_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             tc_fence_after();
-            const bool f16 = kPlain<MODE> && g.f16 != 0;
-            const int64_t ld = kPlain<MODE> ? g.out_ld : g.n_out;   // elements from an output row to the next
             bool released = false;                      // this thread's acc_empty arrival done
             const int slab0 = half * BM + quad * 32;    // first unit row of this warp
             const bool full_slab = slab0 + 32 <= t.rows;
@@ -1009,7 +988,7 @@ tc_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
                         }
                     }
                 } else if constexpr (MODE == kStage2Mx || MODE == kRowsMx) {
-                    // weighted rows into obuf, 32 x 32 boxes (the unit is 224 columns wide)
+                    // weighted rows into obuf (kRowsMx: rows into out), 32 x 32 boxes (the unit is 224 columns wide)
                     constexpr int NP = kUnitN<MODE> / 32;
                     const int col0 = t.n * kUnitN<MODE>;
                     const int y = t.row0 + slab0;
@@ -1050,7 +1029,8 @@ tc_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
                         }
                     } else {
                         // partial slab: masked direct stores, piece by piece
-                        __nv_bfloat16 *dst = g.out + static_cast<int64_t>(t.row0 + row) * ld;
+                        __nv_bfloat16 *dst = g.out + static_cast<int64_t>(t.row0 + row) *
+                                                   (MODE == kRowsMx ? g.out_ld : g.n_out);
 #pragma unroll 1
                         for (int c = 0; c < kUnitN<MODE>; c += 32) {
                             const int col = col0 + c;
@@ -1060,7 +1040,7 @@ tc_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
                             if (valid) store_row32(dst + col, g.n_out - col, pk);
                         }
                     }
-                } else if constexpr (kIsStage1<MODE> || MODE == kStage2 || MODE == kBwdDX || MODE == kRows || MODE == kRowsT) {
+                } else if constexpr (kIsStage1<MODE> || MODE == kStage2 || MODE == kBwdDX) {
                     // row-grouped outputs: rows t.row0 + row, columns [col0, col0 + ncols)
                     constexpr int ncols = kIsStage1<MODE> ? BN / 2 : BN;
                     const int col0 = t.n * ncols;
@@ -1130,7 +1110,7 @@ tc_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
 #pragma unroll
                         for (int p = 0; p < NPIECE; ++p) {
                             if constexpr (MODE == kStage1) swiglu_piece(tacc, 32 * p, pk[p]);
-                            else if (p % 2 == 0) scaled_piece2(tacc, 32 * p, w, pk[p], pk[p + 1], f16);
+                            else if (p % 2 == 0) scaled_piece2(tacc, 32 * p, w, pk[p], pk[p + 1]);
                             if (p == 1) {                     // box 0 complete: stage it
                                 if (lane == 0) bulk_wait_read<0>();   // previous box read out
                                 __syncwarp();
@@ -1186,12 +1166,12 @@ tc_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
                         // path does, and releases the accumulator before storing (a unit's
                         // release waits for its slowest warp); in stage 1 and dX the extra
                         // registers spill and cost more than they save.
-                        __nv_bfloat16 *dst = g.out + static_cast<int64_t>(t.row0 + row) * ld + col0;
-                        if constexpr (MODE == kStage2 || MODE == kRows) {
+                        __nv_bfloat16 *dst = g.out + static_cast<int64_t>(t.row0 + row) * g.n_out + col0;
+                        if constexpr (MODE == kStage2) {
                             constexpr int NPIECE = ncols / 32;
                             uint32_t pk[NPIECE][16];
 #pragma unroll
-                            for (int p = 0; p < NPIECE; p += 2) scaled_piece2(tacc, 32 * p, w, pk[p], pk[p + 1], f16);
+                            for (int p = 0; p < NPIECE; p += 2) scaled_piece2(tacc, 32 * p, w, pk[p], pk[p + 1]);
                             tc_fence_before();
                             mbar_arrive(smem_addr(&sm.acc_empty));
                             released = true;
@@ -1200,11 +1180,9 @@ tc_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
                                 for (int p = 0; p < NPIECE; ++p)
                                     if (col0 + 32 * p < g.n_out) store_row32(dst + 32 * p, g.n_out - col0 - 32 * p, pk[p]);
                             }
-                            if constexpr (MODE == kStage2) {
-                                if (g.ccnt != nullptr) {
-                                    __syncwarp();
-                                    fused_combine(g, t.n, col0, valid, tok, lane);
-                                }
+                            if (g.ccnt != nullptr) {
+                                __syncwarp();
+                                fused_combine(g, t.n, col0, valid, tok, lane);
                             }
                         } else {
 #pragma unroll 1
@@ -1212,7 +1190,7 @@ tc_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
                                 if (col0 + c >= g.n_out) break;
                                 uint32_t pk[16];
                                 if constexpr (MODE == kStage1) swiglu_piece(tacc, c, pk);
-                                else scaled_piece(tacc, c, w, pk, f16);
+                                else scaled_piece(tacc, c, w, pk);
                                 if (valid) store_row32(dst + c, g.n_out - col0 - c, pk);
                             }
                         }
@@ -1367,7 +1345,7 @@ tc_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) pk[i] = 0u;
                             } else {
-                                scaled_piece(tacc, c, 1.0f, pk, f16);
+                                scaled_piece(tacc, c, 1.0f, pk);
                             }
                             if (lane == 0) bulk_wait_read<1>();
                             __syncwarp();
@@ -1441,8 +1419,7 @@ tc_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
         // then zero the block's K rows >= count in the dispatched operand (dY
         // rows: dW2's A; x rows: dW1's B) and signal tail_fixed. The other
         // operand's rows there are finite (dH and w a have their dropped-slot
-        // rows zeroed), so the padding adds nothing. kRowsWgrad's operands are the
-        // caller's, whose next rows may hold anything: both are zeroed.
+        // rows zeroed), so the padding adds nothing.
         // MXFP8 modes: each stage's scale factors into tensor memory.
         const int ht = threadIdx.x - (64 + EPI_THREADS);
         int stage = 0, q = 0;
@@ -1471,16 +1448,14 @@ tc_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
                     if (!ok) break;
                     tail_phase ^= 1u;
                     const int tail = (stage + nkb - 1) % STAGES;
+                    const uint32_t base = smem_addr(MODE == kBwdDW2 ? sm.a[tail] : sm.b[tail]);
+                    const int atoms = (MODE == kBwdDW2 && t.rows <= BM) ? 2 : 4;
                     const int per_atom = (BK - rem) * (128 / 16);          // 16-byte chunks of rows rem..BK-1
-                    auto zero_tail = [&](uint32_t base, int atoms) {
-                        for (int i = ht; i < atoms * per_atom; i += HELPER_THREADS) {
-                            const int at = i / per_atom;
-                            st_shared_v4(base + at * MN_ATOM_BYTES + rem * 128 + (i - at * per_atom) * 16, 0u, 0u, 0u,
-                                         0u);
-                        }
-                    };
-                    if constexpr (MODE != kBwdDW1) zero_tail(smem_addr(sm.a[tail]), t.rows <= BM ? 2 : 4);
-                    if constexpr (MODE != kBwdDW2) zero_tail(smem_addr(sm.b[tail]), 4);
+                    for (int i = ht; i < atoms * per_atom; i += HELPER_THREADS) {
+                        const int at = i / per_atom;
+                        st_shared_v4(base + at * MN_ATOM_BYTES + rem * 128 + (i - at * per_atom) * 16, 0u, 0u, 0u,
+                                     0u);
+                    }
                     fence_proxy_async_smem();
                     mbar_arrive(smem_addr(&sm.tail_fixed));
                 }
@@ -1565,7 +1540,6 @@ inline GemmArgs grouped_args(const GemmLaunch &p) {
     g.half = p.half;
     g.out_ld = p.out_ld;
     g.R = p.R;
-    g.f16 = p.f16;
     g.total_units = -1;
     return g;
 }

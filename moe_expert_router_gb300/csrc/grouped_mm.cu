@@ -233,15 +233,15 @@ cudaError_t launch_grouped_few(const void *x, const void *w, const int32_t *offs
 
 namespace {
 
-template <int MODE>
+template <int MODE, int MOST>
 cudaError_t setup_pair(int *clusters) {
-    cudaError_t e = cudaFuncSetAttribute(pair_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(kPairSmemBytes));
+    cudaError_t e = cudaFuncSetAttribute(pair_gemm_kernel<MODE, MOST>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(kPairSmemBytes<MODE, MOST>));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kPairThreads);
-    cfg.dynamicSmemBytes = kPairSmemBytes;
+    cfg.dynamicSmemBytes = kPairSmemBytes<MODE, MOST>;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -250,22 +250,24 @@ cudaError_t setup_pair(int *clusters) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, pair_gemm_kernel<MODE>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, pair_gemm_kernel<MODE, MOST>, &cfg);
     if (e == cudaSuccess && n < *clusters) *clusters = n;
     return e;
 }
 
-template <int MODE>
+template <int MODE, int MOST>
 cudaError_t launch_pair_of(const PairMaps &maps, const PairArgs &p, int clusters, cudaStream_t st) {
-    return launch_dep(pair_gemm_kernel<MODE>, dim3(2 * clusters), dim3(kPairThreads), kPairSmemBytes, st, maps, p);
+    return launch_dep(pair_gemm_kernel<MODE, MOST>, dim3(2 * clusters), dim3(kPairThreads), kPairSmemBytes<MODE, MOST>, st, maps, p);
 }
 
 }  // namespace
 
 cudaError_t setup_pair_kernels(int *clusters) {
-    cudaError_t e = setup_pair<kPairRows>(clusters);
-    if (e == cudaSuccess) e = setup_pair<kPairRowsT>(clusters);
-    if (e == cudaSuccess) e = setup_pair<kPairWgrad>(clusters);
+    cudaError_t e = setup_pair<kPairWgrad, 256>(clusters);
+    if (e == cudaSuccess) e = setup_pair<kPairRows, 64>(clusters);
+    if (e == cudaSuccess) e = setup_pair<kPairRows, 256>(clusters);
+    if (e == cudaSuccess) e = setup_pair<kPairRowsT, 64>(clusters);
+    if (e == cudaSuccess) e = setup_pair<kPairRowsT, 256>(clusters);
     return e;
 }
 
@@ -292,25 +294,23 @@ cudaError_t launch_pair(const PairLaunch &l, GroupedKind kind, cudaStream_t st) 
         note_launches(1);
     }
     const PairMaps maps{*l.tm_a, *l.tm_b, *(l.tm_b_wide != nullptr ? l.tm_b_wide : l.tm_b)};
+    // (32 rows a group: 141 us for 2048 of 64 groups, 4096 x 1536, and 150 in tiles of 256; 64: 173 and 155)
+    const int most = kind != GroupedKind::wgrad && l.R <= 32 * static_cast<int64_t>(l.G) ? 64 : 256;
     // (at most: the rows' tiles are known on the device alone)
     const int64_t tiles = kind == GroupedKind::wgrad ? static_cast<int64_t>(l.G) * p.n_tiles * p.k_tiles
-                                                     : (static_cast<int64_t>(l.R) / 256 + (l.R < l.G ? l.R : l.G)) * p.n_tiles;
+                                                     : (static_cast<int64_t>(l.R) / most + (l.R < l.G ? l.R : l.G)) * p.n_tiles;
     const int clusters = tiles < l.clusters ? static_cast<int>(tiles) : l.clusters;
     cudaError_t e = cudaErrorInvalidValue;
-    if (kind == GroupedKind::rows) e = launch_pair_of<kPairRows>(maps, p, clusters, st);
-    else if (kind == GroupedKind::rows_t) e = launch_pair_of<kPairRowsT>(maps, p, clusters, st);
-    else if (kind == GroupedKind::wgrad) e = launch_pair_of<kPairWgrad>(maps, p, clusters, st);
+    if (kind == GroupedKind::wgrad) e = launch_pair_of<kPairWgrad, 256>(maps, p, clusters, st);
+    else if (kind == GroupedKind::rows) e = most == 64 ? launch_pair_of<kPairRows, 64>(maps, p, clusters, st)
+                                                       : launch_pair_of<kPairRows, 256>(maps, p, clusters, st);
+    else if (kind == GroupedKind::rows_t) e = most == 64 ? launch_pair_of<kPairRowsT, 64>(maps, p, clusters, st)
+                                                         : launch_pair_of<kPairRowsT, 256>(maps, p, clusters, st);
     note_launches(1);
     return e;
 }
 
-cudaError_t setup_grouped_mm_kernels() {
-    cudaError_t e = set_gemm_smem<kRows>();
-    if (e == cudaSuccess) e = set_gemm_smem<kRowsT>();
-    if (e == cudaSuccess) e = set_gemm_smem<kRowsWgrad>();
-    if (e == cudaSuccess) e = set_gemm_smem<kRowsMx>();
-    return e;
-}
+cudaError_t setup_grouped_mm_kernels() { return set_gemm_smem<kRowsMx>(); }
 
 cudaError_t launch_grouped_tiles(const int32_t *offsets, int G, int R, int32_t *counts, int32_t *starts,
                                  int32_t *mt_prefix, int32_t *err, cudaStream_t st) {
@@ -320,24 +320,11 @@ cudaError_t launch_grouped_tiles(const int32_t *offsets, int G, int R, int32_t *
     return e;
 }
 
-cudaError_t launch_grouped_mm(const GemmLaunch &p, GroupedKind kind, cudaStream_t st) {
-    GemmArgs g = grouped_args(p);
-    int64_t units;              // at most: the rows' tiles are known on the device alone
-    if (kind == GroupedKind::wgrad) {
-        units = static_cast<int64_t>(g.E) * g.m_tiles * g.n_tiles;
-        g.total_units = static_cast<int>(units);
-    } else {
-        units = (static_cast<int64_t>(p.R) / kUnitM + (p.R < p.E ? p.R : p.E)) * g.n_tiles;
-    }
-    const int grid = units < p.num_sms ? static_cast<int>(units) : p.num_sms;
-    if (grid <= 0) return cudaSuccess;
-    switch (kind) {
-        case GroupedKind::rows: return launch_tc_gemm<kRows>(maps_of(p), g, grid, st);
-        case GroupedKind::rows_t: return launch_tc_gemm<kRowsT>(maps_of(p), g, grid, st);
-        case GroupedKind::wgrad: return launch_tc_gemm<kRowsWgrad>(maps_of(p), g, grid, st);
-        case GroupedKind::rows_mx: return launch_tc_gemm<kRowsMx>(maps_of(p), g, grid, st);
-    }
-    return cudaErrorInvalidValue;
+cudaError_t launch_grouped_mx(const GemmLaunch &p, cudaStream_t st) {
+    const GemmArgs g = grouped_args(p);
+    // at most: the rows' tiles are known on the device alone
+    const int64_t units = (static_cast<int64_t>(p.R) / kUnitM + (p.R < p.E ? p.R : p.E)) * g.n_tiles;
+    return launch_tc_gemm<kRowsMx>(maps_of(p), g, units < p.num_sms ? static_cast<int>(units) : p.num_sms, st);
 }
 
 }  // namespace moe

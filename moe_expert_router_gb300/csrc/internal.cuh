@@ -191,7 +191,6 @@ struct GemmLaunch {
     int out_ld;                 // row stride of out / out2 where it differs from n_out
     int R;                      // routed rows (T * k)
     int save_h;                 // stage 1: also store h
-    int f16;                    // plain products: fp16 operands and output
     int num_sms;
 };
 
@@ -391,7 +390,7 @@ cudaError_t launch_mx_dispatch(const uint8_t *x_codes, const uint32_t *x_scales,
                                uint8_t *codes, uint32_t *scales, cudaStream_t st);
 
 // Products grouped by the caller's offsets (grouped_mm.cu).
-enum class GroupedKind { rows, rows_t, wgrad, rows_mx };
+enum class GroupedKind { rows, rows_t, wgrad };
 cudaError_t launch_grouped_tiles(const int32_t *offsets, int G, int R, int32_t *counts, int32_t *starts,
                                  int32_t *mt_prefix, int32_t *err, cudaStream_t st);
 // The same with w [G, N, K] for a few rows, in one launch. It reads a group's matrix once for every 8 of
@@ -401,7 +400,7 @@ cudaError_t launch_grouped_tiles(const int32_t *offsets, int G, int R, int32_t *
 inline bool grouped_few(int64_t R, int64_t G) { return (R <= 64 && R <= 16 * G) || (R <= 256 && R <= 2 * G); }
 cudaError_t launch_grouped_few(const void *x, const void *w, const int32_t *offsets, void *out, int32_t *err, int64_t ld_x,
                                int64_t ld_out, int R, int G, int K, int N, bool f16, cudaStream_t st);
-cudaError_t launch_grouped_mm(const GemmLaunch &p, GroupedKind kind, cudaStream_t st);
+cudaError_t launch_grouped_mx(const GemmLaunch &p, cudaStream_t st);
 cudaError_t setup_grouped_mm_kernels();
 
 // The grouped products on pairs of SMs (pair_gemm.cuh): rows and rows_t with tm_a the matrices' map, tm_b

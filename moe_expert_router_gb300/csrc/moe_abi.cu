@@ -1567,7 +1567,7 @@ PairLaunch pair_launch(const moe_grouped_shape_t &s, const int32_t *offsets, voi
     return p;
 }
 
-// The groups' tiles into ws, and a launch that reads them.
+// The groups' tiles into ws, and a launch (MXFP8) that reads them.
 moe_status_t grouped_launch(const moe_grouped_shape_t &s, const int32_t *offsets, void *ws, const DeviceState &d,
                             cudaStream_t st, GemmLaunch *p) {
     const GroupedWs l = grouped_layout(s.G);
@@ -1584,7 +1584,6 @@ moe_status_t grouped_launch(const moe_grouped_shape_t &s, const int32_t *offsets
     p->k = 1;
     p->R = static_cast<int>(s.R);
     p->num_sms = d.num_sms;
-    p->f16 = s.dtype == MOE_DTYPE_F16;
     return cuda_status(launch_grouped_tiles(offsets, p->E, p->R, counts, starts, mt_prefix, p->err, st));
 }
 
@@ -1847,7 +1846,7 @@ moe_status_t moe_grouped_mm_mx(const void *x_codes, const void *x_scales, const 
     p.n_tile = 224;
     p.b_rows = static_cast<int>(s.N);
     p.out_ld = static_cast<int>(s.ld_out);
-    return cuda_status(launch_grouped_mm(p, GroupedKind::rows_mx, st));
+    return cuda_status(launch_grouped_mx(p, st));
 }
 
 moe_status_t moe_route_workspace_size(const moe_route_shape_t *shape, size_t *bytes) {

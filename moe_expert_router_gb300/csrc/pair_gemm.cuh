@@ -36,28 +36,33 @@ constexpr int kPairHalf = 128 * BK * 2;     // bytes of a CTA's half of one oper
 constexpr int kPairBoxRows = 32;            // rows of x in one copy: of these, or of 128
 constexpr int kMaxGroups = 1024;
 
-constexpr int kPairStages = 6;
 constexpr int kPairThreads = 64 + EPI_THREADS;
 template <int MODE> constexpr bool kPairAMn = MODE != kPairRows;
 template <int MODE> constexpr bool kPairBMn = MODE == kPairWgrad;
 
+// Shared memory for tiles of at most MOST rows of x (kPairWgrad: 256). Their bytes of a k-block in a CTA, of
+// x beside the matrix's 16 KB, leave room for ten stages or six: with few rows a tile only streams its
+// matrix, and more of it in flight counts (1024 rows of 64 groups, 4096 x 1536: 141 us, and 148 with six).
+template <int MOST> constexpr int kPairB = MOST * BK;
+template <int MOST> constexpr int kPairStagesOf = MOST == 64 ? 10 : 6;
+template <int MODE, int MOST>
 struct __align__(1024) PairSmem {
+    static constexpr int kPairStages = kPairStagesOf<MOST>;
     uint8_t a[kPairStages][kPairHalf];
-    uint8_t b[kPairStages][kPairHalf];
-    uint8_t box[EPI_WARPS][32 * 64];        // kPairWgrad: a warp's 32 x 32 output box
+    uint8_t b[kPairStages][kPairB<MOST>];
+    uint8_t box[MODE == kPairWgrad ? EPI_WARPS : 1][32 * 64];       // kPairWgrad: a warp's 32 x 32 output box
     uint64_t full[kPairStages];             // the leader's: both CTAs' halves have landed
     uint64_t empty[kPairStages];            // the MMAs have read the stage
     uint64_t acc_full[2];
     uint64_t acc_empty[2];                  // the leader's: every epilogue warp of both CTAs has read it
     uint64_t drain;
     int start[kMaxGroups + 1];              // the groups' first rows
-    int tiles[kMaxGroups + 1];              // prefix of their row tiles (of 256 rows at most)
+    int tiles[kMaxGroups + 1];              // prefix of their row tiles
     int scan[32];
     uint32_t tmem_base;
     int abort;
 };
-constexpr size_t kPairSmemBytes = sizeof(PairSmem) + 1024;
-static_assert(kPairSmemBytes <= 227 * 1024, "shared memory of a CTA");
+template <int MODE, int MOST> constexpr size_t kPairSmemBytes = sizeof(PairSmem<MODE, MOST>) + 1024;
 
 struct PairArgs {
     const int32_t *offsets;
@@ -148,6 +153,32 @@ __device__ __forceinline__ void pair_commit(uint32_t bar) {
                  ::"r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
 }
 
+// ---------------------------------------------------------------- epilogue pieces
+
+// Two fp32 values rounded to the operands' type.
+__device__ __forceinline__ uint32_t pack_16x2(float lo, float hi, bool f16) {
+    if (f16) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    return pack_bf16x2(lo, hi);
+}
+
+// 64 accumulator columns, packed: both loads in flight before the one wait.
+__device__ __forceinline__ void pair_piece2(uint32_t tacc, bool f16, uint32_t (&pk0)[16], uint32_t (&pk1)[16]) {
+    uint32_t v0[32], v1[32];
+    tmem_ld32(tacc, v0);
+    tmem_ld32(tacc + 32, v1);
+    tmem_wait_ld();
+    tmem_reg_fence(v0);
+    tmem_reg_fence(v1);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        pk0[i] = pack_16x2(__uint_as_float(v0[2 * i]), __uint_as_float(v0[2 * i + 1]), f16);
+        pk1[i] = pack_16x2(__uint_as_float(v1[2 * i]), __uint_as_float(v1[2 * i + 1]), f16);
+    }
+}
+
 // ---------------------------------------------------------------- tiles
 
 struct PairTile {
@@ -157,8 +188,8 @@ struct PairTile {
     int nkb;                // k-blocks
 };
 
-template <int MODE>
-__device__ __forceinline__ PairTile pair_tile(int u, const PairSmem &sm, const PairArgs &p) {
+template <int MODE, int MOST>
+__device__ __forceinline__ PairTile pair_tile(int u, const PairSmem<MODE, MOST> &sm, const PairArgs &p) {
     PairTile t;
     if constexpr (MODE == kPairWgrad) {
         const int per = p.n_tiles * p.k_tiles;
@@ -211,13 +242,16 @@ __device__ __forceinline__ void pair_load_rows(uint32_t sa, uint32_t sb, const C
 
 // ---------------------------------------------------------------- the kernel
 
-template <int MODE>
+template <int MODE, int MOST>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
     griddep_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
-    PairSmem &sm = *reinterpret_cast<PairSmem *>(smem_raw + ((1024u - (raw & 1023u)) & 1023u));
+    using Smem = PairSmem<MODE, MOST>;
+    constexpr int kPairStages = Smem::kPairStages;
+    static_assert(kPairSmemBytes<MODE, MOST> <= 227 * 1024, "shared memory of a CTA");
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (raw & 1023u)) & 1023u));
     volatile int *abort_flag = &sm.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -256,7 +290,7 @@ pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
         const int end = g < p.G ? p.offsets[g + 1] : 0;
         bad |= g < p.G && (first[i] < 0 || end < first[i] || end > p.R);
         count[i] = end - first[i];
-        sum += (count[i] + 255) / 256;
+        sum += (count[i] + MOST - 1) / MOST;
     }
     bad = __syncthreads_or(bad);
     if (bad) sum = 0;
@@ -277,7 +311,7 @@ pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
             sm.start[g] = bad ? 0 : first[i];
             if (g == p.G - 1) sm.start[p.G] = bad ? 0 : first[i] + count[i];
             sm.tiles[g] = before;
-            before += bad ? 0 : (count[i] + 255) / 256;
+            before += bad ? 0 : (count[i] + MOST - 1) / MOST;
             if (g == p.G - 1) sm.tiles[p.G] = before;
         }
     }
@@ -294,7 +328,7 @@ pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
             int it = 0, seen = -1;
             bool ok = true;
             for (int u = cluster; ok && u < total; u += clusters) {
-                const PairTile t = pair_tile<MODE>(u, sm, p);
+                const PairTile t = pair_tile<MODE, MOST>(u, sm, p);
                 const CUtensorMap *ma = &maps.a, *mb = &maps.b;
                 if constexpr (MODE == kPairWgrad) {
                     ma = p.group_maps + 2 * t.g;
@@ -305,10 +339,10 @@ pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
                         seen = t.g;
                     }
                 }
-                const int half = MODE == kPairWgrad ? 128 : ((t.rows + 31) & ~31) / 2;   // of the MMA's N in this CTA
-                const bool wide = MODE == kPairWgrad || half > 64;
-                const int boxes = (half + kPairBoxRows - 1) / kPairBoxRows;
-                const uint32_t bytes = kPairHalf + (wide ? kPairHalf : boxes * kPairBoxRows * BK * 2);
+                // the tile's rows in this CTA (half of the MMA's N), in one copy of 128 or in copies of 32
+                const int half = MODE == kPairWgrad ? 128 : ((t.rows + 31) & ~31) / 2;
+                const bool wide = half > 64;
+                const uint32_t bytes = kPairHalf + (wide ? 128 : (half + kPairBoxRows - 1) / kPairBoxRows * kPairBoxRows) * BK * 2;
                 const int n = t.n0 + 128 * static_cast<int>(rank);
                 for (int kb = 0; kb < t.nkb; ++kb, ++it) {
                     const int s = it % kPairStages;
@@ -335,11 +369,11 @@ pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
                     }
                     if constexpr (MODE != kPairWgrad) {
                         const int r = t.row0 + half * static_cast<int>(rank);
-                        if (wide) {
+                        if (MOST > 64 && wide) {
                             pair_load_2d(sb, &maps.b_wide, kb * BK, r, bar);
                         } else {
-                            for (int i = 0; i < boxes; ++i)
-                                pair_load_2d(sb + i * kPairBoxRows * BK * 2, &maps.b, kb * BK, r + i * kPairBoxRows, bar);
+                            for (int i = 0; i < half; i += kPairBoxRows)
+                                pair_load_2d(sb + i * BK * 2, &maps.b, kb * BK, r + i, bar);
                         }
                     }
                 }
@@ -355,7 +389,7 @@ pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
             int it = 0, n_done = 0;
             bool ok = true, any = false;
             for (int u = cluster; ok && u < total; u += clusters, ++n_done) {
-                const PairTile t = pair_tile<MODE>(u, sm, p);
+                const PairTile t = pair_tile<MODE, MOST>(u, sm, p);
                 const int buf = n_done & 1;
                 if (!mbar_wait(smem_addr(&sm.acc_empty[buf]), ((n_done >> 1) & 1) ^ 1u, abort_flag, p.err)) {
                     ok = false;
@@ -365,7 +399,7 @@ pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
                 const int n_mma = MODE == kPairWgrad ? 256 : (t.rows + 31) & ~31;
                 uint32_t idesc = idesc_bf16_f32(256, n_mma) | (kPairAMn<MODE> ? (1u << 15) : 0u) |
                                  (kPairBMn<MODE> ? (1u << 16) : 0u);
-                if (p.f16) idesc &= ~((1u << 7) | (1u << 10));
+                if (p.f16) idesc &= ~((1u << 7) | (1u << 10));      // operand formats 0, fp16, for 1, bf16
                 for (int kb = 0; kb < t.nkb; ++kb, ++it) {
                     const int s = it % kPairStages;
                     if (!mbar_wait(smem_addr(&sm.full[s]), (it / kPairStages) & 1, abort_flag, p.err)) {
@@ -394,11 +428,11 @@ pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
         // ------------------------------------------------ epilogue
         const int quad = warp & 3, side = (warp - 2) >> 2;      // lanes of tensor memory, half of the columns
         const uint32_t tacc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 128 * side;
-        const uint32_t buf_addr = smem_addr(sm.box[warp - 2]);
+        const uint32_t buf_addr = smem_addr(sm.box[MODE == kPairWgrad ? warp - 2 : 0]);
         const bool f16 = p.f16 != 0;
         int n_done = 0;
         for (int u = cluster; u < total; u += clusters, ++n_done) {
-            const PairTile t = pair_tile<MODE>(u, sm, p);
+            const PairTile t = pair_tile<MODE, MOST>(u, sm, p);
             const int buf = n_done & 1;
             bool ok = true;
             if (lane == 0) ok = mbar_wait(smem_addr(&sm.acc_full[buf]), (n_done >> 1) & 1, abort_flag, p.err);
@@ -425,12 +459,12 @@ pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
                     }
                     if (live) {
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            uint16_t *at = dst + (c + 32 * j) * p.ld_out;
-                            const int m = t.rows - c - 32 * j;
+                        for (int q = 0; q < 2; ++q) {
+                            uint16_t *at = dst + (c + 32 * q) * p.ld_out;
+                            const int m = t.rows - c - 32 * q;
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
-                                if (i < m) *at = static_cast<uint16_t>(pack_16x2(__uint_as_float(v[j][i]), 0.f, f16));
+                                if (i < m) *at = static_cast<uint16_t>(pack_16x2(__uint_as_float(v[q][i]), 0.f, f16));
                                 at += p.ld_out;
                             }
                         }
@@ -447,8 +481,8 @@ pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
                 const bool work = k < p.K && n < p.N;
                 uint32_t pk[4][16];
                 if (work && t.rows > 0) {
-                    scaled_piece2(tacc + 256 * buf, 0, 1.0f, pk[0], pk[1], f16);
-                    scaled_piece2(tacc + 256 * buf, 64, 1.0f, pk[2], pk[3], f16);
+                    pair_piece2(tacc + 256 * buf, f16, pk[0], pk[1]);
+                    pair_piece2(tacc + 256 * buf + 64, f16, pk[2], pk[3]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 64; ++i) pk[i >> 4][i & 15] = 0u;
