@@ -365,8 +365,8 @@ moe_status_t moe_bias_update(float *bias, const int32_t *counts, int64_t L, int6
  *   h = x + residual (rounded to their type; h = x without a residual)
  *   rstd[t] = 1 / sqrt(mean_c h[t,c]^2 + eps);   y[t,c] = h[t,c] rstd[t] weight[c]
  *   codes, scales = moe_mx_quantize of y
- * y is the exact value rounded once, whatever T and H (with squares whose sum is within
- * fp32's range); the same bits on every call.
+ * y is the exact value rounded once, whatever T and H (a row with an infinity has 0 for its
+ * finite elements); the same bits on every call.
  *
  * x, residual, h and y are of one type (dtype); weight is of that type or fp32. Rows of x
  * and residual may lie apart; h, y and codes are dense [T,H]. Any H <= 16384; whole 16-byte
@@ -422,7 +422,8 @@ moe_status_t moe_rms_norm_backward(const void *dy, const void *dh, const void *h
  * The same bits on every call.
  *
  * ws: moe_grouped_workspace_size bytes, 256-byte aligned, its first 256 bytes zeroed once
- * (moe_workspace_init); calls that share it are ordered on one stream.
+ * (moe_workspace_init); calls that share it are ordered on one stream. Errors found on the
+ * device are read from it with moe_get_device_error.
  */
 typedef struct moe_grouped_shape {
     int64_t R;      /* rows of x and out */

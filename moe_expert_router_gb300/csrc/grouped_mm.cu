@@ -1,14 +1,15 @@
 // grouped_mm.cu -- products of rows with the matrix of their group, for experts of another form
 // than the SwiGLU pair of the two stages: out[r] = x[r] . w[g(r)]^T (or . w[g(r)]), its gradients
-// (the same call on dy for dx; dw[g] = dy_g^T x_g), and the MXFP8 form. The products run on the
-// grouped-GEMM kernel (gemm_kernel.cuh, plain modes); the group sizes are read on the device.
+// (the same call on dy for dx; dw[g] = dy_g^T x_g), and the MXFP8 form. Many rows run on pairs of SMs
+// (pair_gemm.cuh), a few on the kernel below, MXFP8 on the grouped-GEMM kernel of the two stages
+// (gemm_kernel.cuh, kRowsMx); the group sizes are read on the device.
 #include "pair_gemm.cuh"
 
 namespace moe {
 
 namespace {
 
-// The groups' rows from the caller's offsets, one thread a group: counts, starts and the prefix
+// For the MXFP8 product: the groups' rows from the caller's offsets, one thread a group: counts, starts and the prefix
 // of 256-row tiles that the units are numbered by. Offsets that decrease or leave [0, R] would
 // send a product out of its operands: then no group has rows, and the error word says so.
 __global__ void __launch_bounds__(1024)

@@ -45,12 +45,16 @@ moe_status_t device_state(DeviceState **out) {
         }
         if (major != 10 || minor != 3) {
             d.status = MOE_ERR_UNSUPPORTED;
-        } else if (d.clusters = sms / 2; setup_metadata_kernels() != cudaSuccess || setup_gemm_kernels() != cudaSuccess ||
-                   setup_pair_kernels(&d.clusters) != cudaSuccess || d.clusters < 1) {
+        } else if (setup_metadata_kernels() != cudaSuccess || setup_gemm_kernels() != cudaSuccess) {
             cudaGetLastError();
             return MOE_ERR_CUDA;
         } else {
             d.num_sms = sms;
+            d.clusters = sms / 2;
+            if (setup_pair_kernels(&d.clusters) != cudaSuccess) {
+                cudaGetLastError();
+                d.clusters = 0;     // the grouped products alone are not supported then
+            }
             d.status = MOE_OK;
         }
         d.ready = true;
@@ -1767,6 +1771,7 @@ moe_status_t moe_grouped_mm(const void *x, const void *w, const int32_t *offsets
                                               static_cast<int>(s.R), static_cast<int>(s.G), static_cast<int>(s.K),
                                               static_cast<int>(s.N), s.dtype == MOE_DTYPE_F16,
                                               static_cast<cudaStream_t>(stream)));
+    if (d->clusters < 1) return MOE_ERR_UNSUPPORTED;
     const bool one = s.N % 64 == 0;
     CUtensorMap tm_x, tm_wide, tm_w;
     if (!encode_bf16_2d_strided(&tm_x, x, s.K, s.R, s.ld_x, kBK, 32) ||
@@ -1795,6 +1800,7 @@ moe_status_t moe_grouped_wgrad(const void *a, const void *b, const int32_t *offs
         return MOE_ERR_INVALID_ARG;
     DeviceState *d = nullptr;
     if ((r = device_state(&d)) != MOE_OK) return r;
+    if (d->clusters < 1) return MOE_ERR_UNSUPPORTED;
     CUtensorMap tm_a, tm_b;
     const bool a_one = s.N % 64 == 0, b_one = s.K % 64 == 0;
     if (!(a_one ? encode_bf16_atoms(&tm_a, a, s.N, s.R, s.ld_out, 0, kBK)

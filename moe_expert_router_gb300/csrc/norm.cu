@@ -1,7 +1,7 @@
 // norm.cu -- the norm in front of the expert layer: the residual stream takes a branch's output,
 // and its root-mean-square norm goes on, in the stream's type and, where the MXFP8 path reads it,
 // as E4M3 codes with scales too:
-//   h = x + r;  y = h w / sqrt(mean h^2 + eps);  codes, scales = MXFP8(y)
+//   h = x + r;  y = h / sqrt(mean h^2 + eps) w;  codes, scales = MXFP8(y)
 // One pass: a row stays in registers between the sum of its squares and its outputs, so x and r
 // are read once and h, y and the codes written once, which is all the memory traffic there is
 // (what bounds the kernel).
@@ -76,10 +76,10 @@ __device__ __forceinline__ Pair normal(float hi, float lo) {
     return {s, __fsub_rn(lo, __fsub_rn(s, hi))};
 }
 
-// sqrt(H) / sqrt(sum + H eps) for a sum of H squares.
-__device__ __forceinline__ Pair inverse_root(Pair sum, const NormLaunch &p) {
+// scale sqrt(H) / sqrt(sum + scale^2 H eps) for a sum of H squares of scale h; scale is a power of two.
+__device__ __forceinline__ Pair inverse_root(Pair sum, float scale, const NormLaunch &p) {
     if (!(sum.hi < __int_as_float(0x7f800000))) return {1.f / sum.hi, 0.f};     // infinity: 0; NaN
-    const Pair a = join(sum, {p.h_eps_hi, p.h_eps_lo});
+    const Pair a = join(sum, {p.h_eps_hi * scale * scale, p.h_eps_lo * scale * scale});
     const Pair n = normal(a.hi, a.lo);
     const float r = rsqrtf(n.hi);
     const float t = __fmul_rn(r, r), tl = fmaf(r, r, -t);
@@ -91,16 +91,18 @@ __device__ __forceinline__ Pair inverse_root(Pair sum, const NormLaunch &p) {
     const float rl = __fmul_rn(r, fmaf(__fmul_rn(0.375f, e), e, 0.5f * e));
     const float m = __fmul_rn(r, p.root_h_hi);
     const float ml = fmaf(r, p.root_h_hi, -m);
-    return normal(m, fmaf(r, p.root_h_lo, fmaf(rl, p.root_h_hi, ml)));
+    const Pair root = normal(m, fmaf(r, p.root_h_lo, fmaf(rl, p.root_h_hi, ml)));
+    return {root.hi * scale, root.lo * scale};
 }
 
-// The nearest number of the 16-bit type to h w rstd, from some 48 bits of it: fp32 with its last
+// (h rstd is taken first: it stays below sqrt(H), where h w may leave fp32's range.)
+// The nearest number of the 16-bit type to h rstd w, from some 48 bits of it: fp32 with its last
 // bit set where digits follow (round to odd) rounds on as the exact value would.
 template <typename T>
 __device__ __noinline__ T rounded_once(float h, float w, Pair r) {
-    const float p = __fmul_rn(h, w), pl = fmaf(h, w, -p);
-    const float y = __fmul_rn(p, r.hi);
-    const Pair n = normal(y, fmaf(p, r.lo, fmaf(pl, r.hi, fmaf(p, r.hi, -y))));
+    const float z = __fmul_rn(h, r.hi), zl = fmaf(h, r.lo, fmaf(h, r.hi, -z));
+    const float y = __fmul_rn(z, w);
+    const Pair n = normal(y, fmaf(zl, w, fmaf(z, w, -y)));
     uint32_t b = __float_as_uint(n.hi);
     if ((b & 1u) == 0u && (n.lo < 0.f || n.lo > 0.f)) b += (n.lo > 0.f) == (n.hi > 0.f) ? 1u : 0xffffffffu;
     return from_float<T>(__uint_as_float(b));
@@ -148,28 +150,39 @@ rms_norm_kernel(const NormLaunch p) {
 #pragma unroll
             for (int j = 0; j < N; ++j) h[v].v[j] = from_float<T>(to_float(h[v].v[j]) + to_float(b[v].v[j]));
     }
-    Sum2 sum = {0ull, 0ull};
+    Pair all;
+    float scale = 1.f;
+#pragma unroll 1
+    while (true) {
+        Sum2 sum = {0ull, 0ull};
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int j = 0; j < N; j += 2) add_square(sum, f2(to_float(h[v].v[j]), to_float(h[v].v[j + 1])), sizeof(T) == 2);
-    const float2 s = split(sum.s), c = split(sum.c);
-    Pair all = join({s.x, c.x}, {s.y, c.y});
+            for (int j = 0; j < N; j += 2)
+                add_square(sum, mul2(f2(to_float(h[v].v[j]), to_float(h[v].v[j + 1])), f2(scale, scale)), sizeof(T) == 2);
+        const float2 s = split(sum.s), c = split(sum.c);
+        all = join({s.x, c.x}, {s.y, c.y});
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        all = join(all, {__shfl_xor_sync(kAll, all.hi, d), __shfl_xor_sync(kAll, all.lo, d)});
-    if constexpr (!L::WARP) {
-        // every warp adds the warps' sums, in one order
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = all;
-        __syncthreads();
-        constexpr int WARPS = L::MOST / 32;
-        const int w = threadIdx.x & (WARPS - 1);
-        all = w < lane.tpr / 32 ? part[w] : Pair{0.f, 0.f};
-#pragma unroll
-        for (int d = WARPS / 2; d > 0; d >>= 1)
+        for (int d = 16; d > 0; d >>= 1)
             all = join(all, {__shfl_xor_sync(kAll, all.hi, d), __shfl_xor_sync(kAll, all.lo, d)});
+        if constexpr (!L::WARP) {
+            // every warp adds the warps' sums, in one order
+            if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = all;
+            __syncthreads();
+            constexpr int WARPS = L::MOST / 32;
+            const int w = threadIdx.x & (WARPS - 1);
+            all = w < lane.tpr / 32 ? part[w] : Pair{0.f, 0.f};
+#pragma unroll
+            for (int d = WARPS / 2; d > 0; d >>= 1)
+                all = join(all, {__shfl_xor_sync(kAll, all.hi, d), __shfl_xor_sync(kAll, all.lo, d)});
+        }
+        // a sum that its inverse's digits are lost of, or that left fp32: again, of values 2^-80 as large
+        // (the row's threads agree; infinities and NaN stay what they are)
+        if (all.hi < 1.2676506e30f || scale != 1.f) break;
+        scale = 8.271806125530277e-25f;
+        if constexpr (!L::WARP) __syncthreads();
     }
-    const Pair r = inverse_root(all, p);
+    const Pair r = inverse_root(all, scale, p);
     if (p.rstd != nullptr && lane.i == 0) p.rstd[t] = r.hi;
     const bool store_h = p.h != nullptr;
     T *ho = static_cast<T *>(p.h) + t * p.H, *yo = static_cast<T *>(p.y) + t * p.H;
@@ -182,10 +195,10 @@ rms_norm_kernel(const NormLaunch p) {
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const float q = __fmul_rn(h[v].v[j], w[j]), ql = fmaf(h[v].v[j], w[j], -q);
-                const float o = __fmul_rn(q, r.hi);
+                const float z = __fmul_rn(h[v].v[j], r.hi), zl = fmaf(h[v].v[j], r.lo, fmaf(h[v].v[j], r.hi, -z));
+                const float o = __fmul_rn(z, w[j]);
                 // (not finite: the corrections would be NaN)
-                const float more = fmaf(q, r.lo, fmaf(ql, r.hi, fmaf(q, r.hi, -o)));
+                const float more = fmaf(zl, w[j], fmaf(z, w[j], -o));
                 y.v[j] = fabsf(o) < __int_as_float(0x7f800000) ? o + more : o;
             }
         } else {
@@ -193,7 +206,7 @@ rms_norm_kernel(const NormLaunch p) {
             uint32_t apart = 0u;
 #pragma unroll
             for (int j = 0; j < N; j += 2) {
-                const F2 q = mul2(mul2(f2(to_float(h[v].v[j]), to_float(h[v].v[j + 1])), f2(w[j], w[j + 1])), f2(r.hi, r.hi));
+                const F2 q = mul2(mul2(f2(to_float(h[v].v[j]), to_float(h[v].v[j + 1])), f2(r.hi, r.hi)), f2(w[j], w[j + 1]));
                 // q is good to 3 2^-24: where both ends of its error round alike, so does the product
                 constexpr float kOff = 2.384185791015625e-07f;      // 2^-22
                 const uint32_t lo = pack2(split(mul2(q, f2(1.f - kOff, 1.f - kOff))), T());

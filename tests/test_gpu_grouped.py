@@ -201,8 +201,70 @@ def test_bad_offsets_compute_nothing(bad):
     B.moe_grouped_wgrad(out, x, offsets, dw, ws)
     assert B.moe_get_device_error(ws) == B.DEVERR_BAD_OFFSETS and (dw == 0).all()
     good = torch.tensor([0, 5, 7, 10], dtype=torch.int32, device=DEV)
+    out.fill_(77)
+    B.moe_grouped_mm(x, w.transpose(1, 2).contiguous(), offsets, out, ws, transposed=True)
+    assert B.moe_get_device_error(ws) == B.DEVERR_BAD_OFFSETS and (out == 77).all()
+    w.fill_(1)
     B.moe_grouped_mm(x, w, good, out, ws)
     assert B.moe_get_device_error(ws) == 0 and (out == 64).all()
+    xc, xs = quantized(torch.ones((10, 128), dtype=BF16, device=DEV))
+    wc, wss = quantized(torch.ones((3, 72, 128), dtype=BF16, device=DEV))
+    out.fill_(77)
+    B.moe_grouped_mm_mx(xc, xs, wc, wss, offsets, out, ws)
+    assert B.moe_get_device_error(ws) == B.DEVERR_BAD_OFFSETS and (out == 77).all()
+    B.moe_grouped_mm_mx(xc, xs, wc, wss, good, out, ws)
+    assert B.moe_get_device_error(ws) == 0 and (out == 128).all()
+
+
+@pytest.mark.parametrize("rows", [50, 900, 3000])
+def test_the_most_groups(rows):
+    gen = torch.Generator(DEV).manual_seed(rows)
+    G, K, N = 1024, 136, 72
+    counts = torch.bincount(torch.randint(0, G, (rows,), generator=gen, device=DEV) ** 2 // G, minlength=G)
+    offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).int()
+    group = torch.repeat_interleave(torch.arange(G, device=DEV), counts)
+    x, dy, w = whole(gen, (rows, K), BF16), whole(gen, (rows, N), BF16), whole(gen, (G, N, K), BF16)
+    want = torch.einsum("rk,rnk->rn", x.float(), w.float()[group]).to(BF16)
+    dx = torch.einsum("rn,rnk->rk", dy.float(), w.float()[group]).to(BF16)
+    assert torch.equal(run(x, w, offsets, torch.empty_like(dy)), want)
+    assert torch.equal(run(dy, w, offsets, torch.empty_like(x), True), dx)
+    dw, ws = torch.empty_like(w), B.grouped_workspace(G)
+    B.moe_grouped_wgrad(dy, x, offsets, dw, ws)
+    want = torch.zeros((G, N, K), device=DEV).index_add_(0, group, dy.float()[:, :, None] * x.float()[:, None])
+    assert torch.equal(dw, want.to(BF16)) and B.moe_get_device_error(ws) == 0
+    K = 128
+    x, w = x[:, :K].contiguous(), w[:, :, :K].contiguous()
+    out = torch.empty_like(dy)
+    B.moe_grouped_mm_mx(*quantized(x), *quantized(w), offsets, out, ws)
+    assert torch.equal(out, torch.einsum("rk,rnk->rn", x.float(), w.float()[group]).to(BF16))
+
+
+def test_operands_beyond_32_bits():
+    """More than 2^32 bytes, and 2^31 elements, of matrices and of rows: the last group's values."""
+    gen = torch.Generator(DEV).manual_seed(7)
+    G, N, K = 5, 20480, 22000                               # 2.25e9 elements
+    w = torch.zeros((G, N, K), dtype=BF16, device=DEV)
+    w[-1] = whole(gen, (N, K), BF16, 1)
+    for R in (6, 700):
+        counts = [0, 1, 0, 1, R - 2]
+        offsets, o = offsets_of(counts)
+        x, dy = whole(gen, (R, K), BF16, 1), whole(gen, (R, N), BF16, 1)
+        out = run(x, w, offsets, torch.full((R, N), 77.0, dtype=BF16, device=DEV))
+        assert (out[:2] == 0).all() and torch.equal(out[2:], (x[2:].float() @ w[-1].float().t()).to(BF16))
+        dx = run(dy, w, offsets, torch.full((R, K), 77.0, dtype=BF16, device=DEV), True)
+        assert (dx[:2] == 0).all() and torch.equal(dx[2:], (dy[2:].float() @ w[-1].float()).to(BF16))
+    dw = torch.full_like(w, 77.0)
+    B.moe_grouped_wgrad(dy, x, offsets, dw, B.grouped_workspace(G))
+    assert (dw[0] == 0).all() and (dw[2] == 0).all()
+    assert torch.equal(dw[-1], (dy[2:].float().t() @ x[2:].float()).to(BF16))
+    del w, dw
+    R, K, N = 140_000, 16384, 8                             # 2.3e9 elements of x
+    x = torch.zeros((R, K), dtype=BF16, device=DEV)
+    x[-1000:] = whole(gen, (1000, K), BF16, 1)
+    w = whole(gen, (2, N, K), BF16, 1)
+    offsets, _ = offsets_of([R - 1000, 1000])
+    out = run(x, w, offsets, torch.full((R, N), 77.0, dtype=BF16, device=DEV))
+    assert (out[:-1000] == 0).all() and torch.equal(out[-1000:], (x[-1000:].float() @ w[1].float().t()).to(BF16))
 
 
 def test_no_rows():

@@ -203,6 +203,37 @@ def test_other_rows_do_not_matter_and_bits_repeat():
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
 
 
+def test_operands_beyond_32_bits():
+    T, H = 140_000, 16384                                   # 2.3e9 elements
+    gen = torch.Generator(DEV).manual_seed(6)
+    x = torch.zeros((T, H), dtype=BF16, device=DEV)
+    x[-3:] = torch.randn((3, H), generator=gen, device=DEV)
+    w = (1 + 0.1 * torch.randn((H,), generator=gen, device=DEV))
+    y, rstd = torch.full_like(x, 99.0), torch.empty((T,), device=DEV)
+    codes, scales = torch.empty((T, H), dtype=torch.uint8, device=DEV), B.mx_scales_empty((T, H), DEV)
+    B.moe_rms_norm(x, w, y, rstd=rstd, codes=codes, scales=scales)
+    assert (y[:-3] == 0).all()
+    assert_y(y[-3:], reference(x[-3:], None, w, 1e-6)[1])
+    c, s = torch.empty((3, H), dtype=torch.uint8, device=DEV), B.mx_scales_empty((3, H), DEV)
+    B.moe_mx_quantize(y[-3:], c, s)
+    assert torch.equal(codes[-3:], c) and torch.equal(scales[:, -3:], s.view(H // 128, 4, 4)[:, :3])
+    dx, dw = torch.full_like(x, 99.0), torch.empty_like(w)
+    B.moe_rms_norm_backward(y, x, w, rstd, dx, dw, B.rms_norm_scratch(T, H, x))
+    dx3, dw3 = torch.empty_like(x[-3:]), torch.empty_like(w)
+    B.moe_rms_norm_backward(y[-3:], x[-3:], w, rstd[-3:], dx3, dw3, B.rms_norm_scratch(3, H, x))
+    assert (dx[:-3] == 0).all() and torch.equal(dx[-3:], dx3)
+    assert ((dw - dw3).abs() <= 1e-5 * dw3.abs() + 1e-6).all()      # the same three terms, added in other places
+
+
+def test_a_product_whose_factors_leave_fp32():
+    x = torch.full((2, 64), 3e18, device=DEV)
+    w = torch.full((64,), 1e25, device=DEV)                 # x w is beyond fp32, x rstd w is 1e25
+    for t in (torch.float32, BF16):
+        y = torch.empty((2, 64), dtype=t, device=DEV)
+        B.moe_rms_norm(x.to(t), w, y)
+        assert_y(y, reference(x.to(t), None, w, 1e-6)[1])
+
+
 def test_no_rows():
     x, w = torch.empty((0, 64), dtype=BF16, device=DEV), torch.ones((64,), device=DEV)
     B.moe_rms_norm(x, w, torch.empty_like(x))
