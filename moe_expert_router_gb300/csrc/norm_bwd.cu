@@ -154,33 +154,39 @@ rms_norm_bwd_kernel(const NormBackwardLaunch p) {
     }
 }
 
-// dweight[c] = the sum of the blocks' parts, 32 columns a block: a warp's threads take a column each
-// and every 32nd part, 32 of them in a row, and the warps' sums are added by one warp a column.
+// dweight[c] = the sum of the blocks' parts, 16 columns a block: a thread takes a column and every 64th
+// part, 10 of them in a row, and a warp adds the 64 sums of two columns.
+constexpr int kDwCols = 16;
 template <typename W>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(1024, 2)
 rms_norm_dw_kernel(const float *__restrict__ part, int blocks, int H, W *__restrict__ dweight) {
-    __shared__ float sums[32][33];
+    __shared__ float sums[64][kDwCols + 1];
     griddep_wait();
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + x;
+    const int x = threadIdx.x % kDwCols, y = threadIdx.x / kDwCols;
+    const int c0 = blockIdx.x * kDwCols;
     float total = 0.f;
-    if (c < H) {
-        for (int b0 = y; b0 < blocks; b0 += 32 * 32) {
+    if (c0 + x < H) {
+        const float *p = part + static_cast<int64_t>(y) * H + c0 + x;
+        const int64_t step = 64 * static_cast<int64_t>(H);
+#pragma unroll 1
+        for (int b0 = y; b0 < blocks; b0 += 64 * 10, p += 10 * step) {
+            float v[10];
+#pragma unroll
+            for (int k = 0; k < 10; ++k) v[k] = b0 + 64 * k < blocks ? __ldg(p + k * step) : 0.f;
             float s = 0.f;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-                const int b = b0 + 32 * k;
-                if (b < blocks) s += __ldg(part + static_cast<int64_t>(b) * H + c);
-            }
+            for (int k = 0; k < 10; ++k) s += v[k];
             total += s;
         }
     }
     sums[y][x] = total;
     __syncthreads();
-    total = sums[x][y];
+    const int lane = threadIdx.x & 31, c = threadIdx.x >> 5;
+    if (c >= kDwCols) return;
+    total = sums[lane][c] + sums[lane + 32][c];
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(kAll, total, d);
-    if (x == 0 && blockIdx.x * 32 + y < H) dweight[blockIdx.x * 32 + y] = from_float<W>(total);
+    if (lane == 0 && c0 + c < H) dweight[c0 + c] = from_float<W>(total);
 }
 
 template <typename T>
@@ -196,7 +202,7 @@ cudaError_t launch_of(const NormBackwardLaunch &p, cudaStream_t st) {
 
 template <typename W>
 cudaError_t launch_dw(const NormBackwardLaunch &p, cudaStream_t st) {
-    return launch_dep(rms_norm_dw_kernel<W>, dim3((p.H + 31) / 32), dim3(1024), 0, st, static_cast<const float *>(p.part),
+    return launch_dep(rms_norm_dw_kernel<W>, dim3((p.H + kDwCols - 1) / kDwCols), dim3(1024), 0, st, static_cast<const float *>(p.part),
                       static_cast<int>(p.blocks), p.H, static_cast<W *>(p.dweight));
 }
 
