@@ -37,8 +37,7 @@
 // kind::mxf8f6f4.block_scale MMAs on E4M3 operands with E8M0 scales per 32
 // K-elements. The scales are k-block-major 32-bit words; each stage's words
 // arrive by TMA on a barrier of their own and the helper warps copy them into
-// tensor memory. kRowsMx is stage 2's product on its own (grouped_mm.cu): no routing
-// weights, rows of the output apart.
+// tensor memory.
 //
 // Kernel design (one CTA per SM, persistent):
 //   work unit  = (expert e, n-tile, 256-row tile of e's routed rows) for the
@@ -106,11 +105,10 @@ enum Mode : int {
     kStage1SaveH = 7,           // stage 1 that also stores h for the backward
     kStage1Mx = 8,              // stage 1 in MXFP8: E4M3 x and w1, a quantized in the epilogue
     kStage2Mx = 9,              // stage 2 in MXFP8: E4M3 a and w2
-    kWgradMx = 10,              // MXFP8 weight gradient: operands quantized along the expert's routed rows
-    kRowsMx = 11                // MXFP8 grouped product alone
+    kWgradMx = 10               // MXFP8 weight gradient: operands quantized along the expert's routed rows
 };
 
-template <int MODE> constexpr bool kIsMx = MODE == kStage1Mx || MODE == kStage2Mx || MODE == kWgradMx || MODE == kRowsMx;
+template <int MODE> constexpr bool kIsMx = MODE == kStage1Mx || MODE == kStage2Mx || MODE == kWgradMx;
 template <int MODE> constexpr bool kIsStage1 = MODE == kStage1 || MODE == kStage1SaveH || MODE == kStage1Mx;
 template <int MODE> constexpr bool kRing = MODE == kStage1 || MODE == kStage2;
 template <int MODE> constexpr bool kAMn = MODE == kBwdDW2 || MODE == kBwdDW1;
@@ -124,7 +122,7 @@ template <int MODE> constexpr bool kHelpers = kWeightGrad<MODE> || kIsMx<MODE>;
 // accumulator columns of one 128-row half (a unit's output columns): 2 x 96
 // (gate, up) in stage 1 MXFP8, 224 in stage 2 MXFP8, else 256; the MXFP8 modes
 // keep the rest of tensor memory for per-stage scale factors
-template <int MODE> constexpr int kUnitN = MODE == kStage1Mx ? 192 : ((MODE == kStage2Mx || MODE == kWgradMx || MODE == kRowsMx) ? 224 : BN);
+template <int MODE> constexpr int kUnitN = MODE == kStage1Mx ? 192 : ((MODE == kStage2Mx || MODE == kWgradMx) ? 224 : BN);
 // K elements per pipeline stage (128-byte rows either way)
 template <int MODE> constexpr int kStageK = kIsMx<MODE> ? 128 : BK;
 template <int MODE> constexpr int kElemBytes = kIsMx<MODE> ? 1 : 2;
@@ -707,7 +705,7 @@ tc_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
                         tma_load_2d(sa, &maps.a, kx, t.row0, full);
                         if (two) tma_load_2d(sa + A_HALF_BYTES, &maps.a, kx, t.row0 + BM, full);
                         tma_load_2d(sb, &maps.b, kx, t.n * kUnitN<MODE>, full);
-                    } else if constexpr (MODE == kStage2 || MODE == kStage2Mx || MODE == kRowsMx) {
+                    } else if constexpr (MODE == kStage2 || MODE == kStage2Mx) {
                         const int kx = kb * kStageK<MODE>;
                         tma_load_2d(sa, &maps.a, kx, t.row0, full);
                         if (two) tma_load_2d(sa + A_HALF_BYTES, &maps.a, kx, t.row0 + BM, full);
@@ -987,8 +985,8 @@ tc_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
                                 static_cast<uint8_t>(sc);
                         }
                     }
-                } else if constexpr (MODE == kStage2Mx || MODE == kRowsMx) {
-                    // weighted rows into obuf (kRowsMx: rows into out), 32 x 32 boxes (the unit is 224 columns wide)
+                } else if constexpr (MODE == kStage2Mx) {
+                    // weighted rows into obuf, 32 x 32 boxes (the unit is 224 columns wide)
                     constexpr int NP = kUnitN<MODE> / 32;
                     const int col0 = t.n * kUnitN<MODE>;
                     const int y = t.row0 + slab0;
@@ -1029,8 +1027,7 @@ tc_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs g) {
                         }
                     } else {
                         // partial slab: masked direct stores, piece by piece
-                        __nv_bfloat16 *dst = g.out + static_cast<int64_t>(t.row0 + row) *
-                                                   (MODE == kRowsMx ? g.out_ld : g.n_out);
+                        __nv_bfloat16 *dst = g.out + static_cast<int64_t>(t.row0 + row) * g.n_out;
 #pragma unroll 1
                         for (int c = 0; c < kUnitN<MODE>; c += 32) {
                             const int col = col0 + c;

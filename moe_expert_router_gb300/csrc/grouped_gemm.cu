@@ -64,7 +64,6 @@ cudaError_t setup_gemm_kernels() {
     if (e == cudaSuccess) e = set_gemm_smem<kRouter>();
     if (e == cudaSuccess) e = setup_bwd_gemm_kernels();
     if (e == cudaSuccess) e = setup_mx_gemm_kernels();
-    if (e == cudaSuccess) e = setup_grouped_mm_kernels();
     if (e == cudaSuccess) e = setup_norm_kernels();
     return e;
 }

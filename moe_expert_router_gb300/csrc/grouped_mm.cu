@@ -1,49 +1,12 @@
 // grouped_mm.cu -- products of rows with the matrix of their group, for experts of another form
 // than the SwiGLU pair of the two stages: out[r] = x[r] . w[g(r)]^T (or . w[g(r)]), its gradients
-// (the same call on dy for dx; dw[g] = dy_g^T x_g), and the MXFP8 form. Many rows run on pairs of SMs
-// (pair_gemm.cuh), a few on the kernel below, MXFP8 on the grouped-GEMM kernel of the two stages
-// (gemm_kernel.cuh, kRowsMx); the group sizes are read on the device.
+// (the same call on dy for dx; dw[g] = dy_g^T x_g), and the MXFP8 form. They run on pairs of SMs
+// (pair_gemm.cuh), a few rows on the kernel below; the group sizes are read on the device.
 #include "pair_gemm.cuh"
 
 namespace moe {
 
 namespace {
-
-// For the MXFP8 product: the groups' rows from the caller's offsets, one thread a group: counts, starts and the prefix
-// of 256-row tiles that the units are numbered by. Offsets that decrease or leave [0, R] would
-// send a product out of its operands: then no group has rows, and the error word says so.
-__global__ void __launch_bounds__(1024)
-grouped_tiles_kernel(const int32_t *__restrict__ offsets, int G, int R, int32_t *__restrict__ counts,
-                     int32_t *__restrict__ starts, int32_t *__restrict__ mt_prefix, int32_t *__restrict__ err) {
-    __shared__ int warp_sum[32];
-    griddep_wait();
-    const int g = threadIdx.x, lane = g & 31, warp = g >> 5;
-    int a = 0, b = 0;
-    if (g < G) {
-        a = offsets[g];
-        b = offsets[g + 1];
-    }
-    const bool bad = __syncthreads_or(a < 0 || b < a || b > R);
-    const int n = bad ? 0 : b - a;
-    int sum = (n + kUnitM - 1) / kUnitM;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, sum, d);
-        if (lane >= d) sum += o;
-    }
-    if (lane == 31) warp_sum[warp] = sum;
-    __syncthreads();
-    if (g < G) {
-        for (int w = 0; w < warp; ++w) sum += warp_sum[w];
-        counts[g] = n;
-        starts[g] = bad ? 0 : a;
-        mt_prefix[g + 1] = sum;
-    }
-    if (g == 0) {
-        mt_prefix[0] = 0;
-        if (bad) atomicOr(err, MOE_DEVERR_BAD_OFFSETS);
-    }
-}
 
 // The weight gradients' tensor maps, a thread a group: those of a and b with as many rows as end at the
 // group's last one, so that rows behind it are read as zeros. (Of bad offsets nothing is computed.)
@@ -241,7 +204,7 @@ cudaError_t setup_pair(int *clusters) {
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(kPairThreads);
+    cfg.blockDim = dim3(kPairThreads<MODE>);
     cfg.dynamicSmemBytes = kPairSmemBytes<MODE, MOST>;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -257,14 +220,18 @@ cudaError_t setup_pair(int *clusters) {
 }
 
 template <int MODE, int MOST>
-cudaError_t launch_pair_of(const PairMaps &maps, const PairArgs &p, int clusters, cudaStream_t st) {
-    return launch_dep(pair_gemm_kernel<MODE, MOST>, dim3(2 * clusters), dim3(kPairThreads), kPairSmemBytes<MODE, MOST>, st, maps, p);
+cudaError_t launch_pair_of(const PairMapsOf<MODE> &maps, const PairArgs &p, int clusters, cudaStream_t st) {
+    return launch_dep(pair_gemm_kernel<MODE, MOST>, dim3(2 * clusters), dim3(kPairThreads<MODE>),
+                      kPairSmemBytes<MODE, MOST>, st, maps, p);
 }
 
 }  // namespace
 
 cudaError_t setup_pair_kernels(int *clusters) {
     cudaError_t e = setup_pair<kPairWgrad, 256>(clusters);
+    if (e == cudaSuccess) e = setup_pair<kPairMx, 64>(clusters);
+    if (e == cudaSuccess) e = setup_pair<kPairMx, 192>(clusters);
+    if (e == cudaSuccess) e = setup_pair<kPairMx, 224>(clusters);
     if (e == cudaSuccess) e = setup_pair<kPairRows, 64>(clusters);
     if (e == cudaSuccess) e = setup_pair<kPairRows, 256>(clusters);
     if (e == cudaSuccess) e = setup_pair<kPairRowsT, 64>(clusters);
@@ -295,8 +262,7 @@ cudaError_t launch_pair(const PairLaunch &l, GroupedKind kind, cudaStream_t st) 
         note_launches(1);
     }
     const PairMaps maps{*l.tm_a, *l.tm_b, *(l.tm_b_wide != nullptr ? l.tm_b_wide : l.tm_b)};
-    // (32 rows a group: 141 us for 2048 of 64 groups, 4096 x 1536, and 150 in tiles of 256; 64: 173 and 155)
-    const int most = kind != GroupedKind::wgrad && l.R <= 32 * static_cast<int64_t>(l.G) ? 64 : 256;
+    const int most = kind == GroupedKind::wgrad ? 256 : grouped_most(l.R, l.G, kind == GroupedKind::rows_mx);
     // (at most: the rows' tiles are known on the device alone)
     const int64_t tiles = kind == GroupedKind::wgrad ? static_cast<int64_t>(l.G) * p.n_tiles * p.k_tiles
                                                      : (static_cast<int64_t>(l.R) / most + (l.R < l.G ? l.R : l.G)) * p.n_tiles;
@@ -305,27 +271,15 @@ cudaError_t launch_pair(const PairLaunch &l, GroupedKind kind, cudaStream_t st) 
     if (kind == GroupedKind::wgrad) e = launch_pair_of<kPairWgrad, 256>(maps, p, clusters, st);
     else if (kind == GroupedKind::rows) e = most == 64 ? launch_pair_of<kPairRows, 64>(maps, p, clusters, st)
                                                        : launch_pair_of<kPairRows, 256>(maps, p, clusters, st);
+    else if (kind == GroupedKind::rows_mx) {
+        const PairMxMaps mx{maps, *l.tm_sfa, *l.tm_sfb};
+        e = most == 64 ? launch_pair_of<kPairMx, 64>(mx, p, clusters, st)
+            : most == 192 ? launch_pair_of<kPairMx, 192>(mx, p, clusters, st) : launch_pair_of<kPairMx, 224>(mx, p, clusters, st);
+    }
     else if (kind == GroupedKind::rows_t) e = most == 64 ? launch_pair_of<kPairRowsT, 64>(maps, p, clusters, st)
                                                          : launch_pair_of<kPairRowsT, 256>(maps, p, clusters, st);
     note_launches(1);
     return e;
-}
-
-cudaError_t setup_grouped_mm_kernels() { return set_gemm_smem<kRowsMx>(); }
-
-cudaError_t launch_grouped_tiles(const int32_t *offsets, int G, int R, int32_t *counts, int32_t *starts,
-                                 int32_t *mt_prefix, int32_t *err, cudaStream_t st) {
-    const cudaError_t e = launch_dep(grouped_tiles_kernel, dim3(1), dim3((G + 31) / 32 * 32), 0, st, offsets, G, R,
-                                     counts, starts, mt_prefix, err);
-    note_launches(1);
-    return e;
-}
-
-cudaError_t launch_grouped_mx(const GemmLaunch &p, cudaStream_t st) {
-    const GemmArgs g = grouped_args(p);
-    // at most: the rows' tiles are known on the device alone
-    const int64_t units = (static_cast<int64_t>(p.R) / kUnitM + (p.R < p.E ? p.R : p.E)) * g.n_tiles;
-    return launch_tc_gemm<kRowsMx>(maps_of(p), g, units < p.num_sms ? static_cast<int>(units) : p.num_sms, st);
 }
 
 }  // namespace moe

@@ -336,7 +336,8 @@ cudaError_t setup_mx_gemm_kernels();
 
 // MXFP8 scale words ([k_blocks][rows] 32-bit words, k-block-major; rows a
 // multiple of 4), boxes of box_rows words of one k-block, unswizzled.
-bool encode_sf_words(CUtensorMap *map, const void *base, uint64_t rows, uint64_t k_blocks, uint32_t box_rows);
+bool encode_sf_words(CUtensorMap *map, const void *base, uint64_t rows, uint64_t k_blocks, uint32_t box_rows,
+                     uint32_t box_blocks = 1);
 // Rows of the k-block-major MXFP8 scale array of a matrix with `rows` rows
 // (rounded up to 4, so that each k-block's words start 16-byte aligned).
 inline uint64_t mx_rows(uint64_t rows) { return (rows + 3) & ~static_cast<uint64_t>(3); }
@@ -390,24 +391,29 @@ cudaError_t launch_mx_dispatch(const uint8_t *x_codes, const uint32_t *x_scales,
                                uint8_t *codes, uint32_t *scales, cudaStream_t st);
 
 // Products grouped by the caller's offsets (grouped_mm.cu).
-enum class GroupedKind { rows, rows_t, wgrad };
-cudaError_t launch_grouped_tiles(const int32_t *offsets, int G, int R, int32_t *counts, int32_t *starts,
-                                 int32_t *mt_prefix, int32_t *err, cudaStream_t st);
-// The same with w [G, N, K] for a few rows, in one launch. It reads a group's matrix once for every 8 of
-// its rows; measured against the tiles of 128 rows (us): 64 rows of 4 groups 2048 x 1408 13.1 and 21.8,
-// of 8 groups 4096 x 4096 51.0 and 50.0, of one 43 and 36; 256 rows of 128 groups 4096 x 1536 228 and 257,
-// of 64 groups 2048 x 1408 66 and 66, of 16 groups 2048 x 2048 58 and 31.
-inline bool grouped_few(int64_t R, int64_t G) { return (R <= 64 && R <= 16 * G) || (R <= 256 && R <= 2 * G); }
+enum class GroupedKind { rows, rows_t, wgrad, rows_mx };
+// Rows of x in a tile at most, by the rows of a group (us). bf16: 1024 rows of 64 groups 4096 x 1536 128 in tiles
+// of 64 and 134 of 256, 4096 rows 137 and 138. MXFP8, whose scale words stand in tensor memory beside the
+// accumulators: 2048 rows of these 77 in tiles of 64 and 80 of 192, 6144 rows 83 of 192 and 85 of 224, 8192 rows
+// of one group 4096 x 4096 115 of 192 and 97 of 224.
+inline int grouped_most(int64_t R, int64_t G, bool mx) {
+    if (R <= 32 * G) return 64;
+    return !mx ? 256 : R <= 256 * G ? 192 : 224;
+}
+// moe_grouped_mm with w [G, N, K] for a few rows, in one launch. It reads a group's matrix once for every 8 of
+// its rows; measured against the pairs' tiles (us): 16 rows of one group 4096 x 4096 13 and 17, 32 rows 24 and 17;
+// 32 rows of 8 groups 46 and 45, of 8 groups 2048 x 1408 12 and 13, 64 rows of 8 groups 4096 x 4096 51 and 45;
+// 64 rows of 16 groups 4096 x 1536 34 and 39; 256 rows of 128 groups 4096 x 1536 229 and 232.
+inline bool grouped_few(int64_t R, int64_t G) { return R <= 16 || (R <= 64 && R <= 4 * G) || (R <= 256 && R <= 2 * G); }
 cudaError_t launch_grouped_few(const void *x, const void *w, const int32_t *offsets, void *out, int32_t *err, int64_t ld_x,
                                int64_t ld_out, int R, int G, int K, int N, bool f16, cudaStream_t st);
-cudaError_t launch_grouped_mx(const GemmLaunch &p, cudaStream_t st);
-cudaError_t setup_grouped_mm_kernels();
 
 // The grouped products on pairs of SMs (pair_gemm.cuh): rows and rows_t with tm_a the matrices' map, tm_b
-// and tm_b_wide those of x in boxes of 32 and 128 rows; wgrad with tm_a and tm_b those of a and b.
+// and tm_b_wide those of x in boxes of 32 and of half a tile's rows; rows_mx also with those of the scale words of
+// both; wgrad with tm_a and tm_b those of a and b.
 // `clusters`: pairs that run at a time.
 struct PairLaunch {
-    const CUtensorMap *tm_a, *tm_b, *tm_b_wide;
+    const CUtensorMap *tm_a, *tm_b, *tm_b_wide, *tm_sfa, *tm_sfb;
     const int32_t *offsets;
     int32_t *err;
     void *out;

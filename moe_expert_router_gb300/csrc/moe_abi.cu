@@ -749,11 +749,12 @@ bool encode_u8_2d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t r
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_sf_words(CUtensorMap *map, const void *base, uint64_t rows, uint64_t k_blocks, uint32_t box_rows) {
+bool encode_sf_words(CUtensorMap *map, const void *base, uint64_t rows, uint64_t k_blocks, uint32_t box_rows,
+                     uint32_t box_blocks) {
     if (!encode_ready() || rows % 4 != 0) return false;
     cuuint64_t dims[2] = {rows, k_blocks};
     cuuint64_t strides[1] = {rows * 4};
-    cuuint32_t box[2] = {box_rows, 1};
+    cuuint32_t box[2] = {box_rows, box_blocks};
     cuuint32_t estr[2] = {1, 1};
     return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
@@ -1522,18 +1523,14 @@ int norm_access(const moe_norm_shape_t &s, bool dense, bool apart) {
     return whole ? (apart ? kWhole : kLoadsOne) : kOne;
 }
 
-// Workspace of the grouped products: header, then counts, starts and tile prefix of the groups (MXFP8), and
-// two tensor maps of each (weight gradients).
+// Workspace of the grouped products: header, then two tensor maps of each group (weight gradients).
 struct GroupedWs {
-    size_t counts, starts, mt_prefix, maps, total;
+    size_t maps, total;
 };
 
 GroupedWs grouped_layout(int64_t G) {
     GroupedWs w;
-    w.counts = kWsHeaderBytes;
-    w.starts = align256(w.counts + 4 * static_cast<size_t>(G));
-    w.mt_prefix = align256(w.starts + 4 * static_cast<size_t>(G));
-    w.maps = align256(w.mt_prefix + 4 * static_cast<size_t>(G + 1));
+    w.maps = kWsHeaderBytes;
     w.total = align256(w.maps + 2 * sizeof(CUtensorMap) * static_cast<size_t>(G));
     return w;
 }
@@ -1569,26 +1566,6 @@ PairLaunch pair_launch(const moe_grouped_shape_t &s, const int32_t *offsets, voi
     p.clusters = d.clusters;
     p.group_maps = static_cast<uint8_t *>(ws) + grouped_layout(s.G).maps;
     return p;
-}
-
-// The groups' tiles into ws, and a launch (MXFP8) that reads them.
-moe_status_t grouped_launch(const moe_grouped_shape_t &s, const int32_t *offsets, void *ws, const DeviceState &d,
-                            cudaStream_t st, GemmLaunch *p) {
-    const GroupedWs l = grouped_layout(s.G);
-    uint8_t *b = static_cast<uint8_t *>(ws);
-    int32_t *counts = reinterpret_cast<int32_t *>(b + l.counts), *starts = reinterpret_cast<int32_t *>(b + l.starts);
-    int32_t *mt_prefix = reinterpret_cast<int32_t *>(b + l.mt_prefix);
-    *p = GemmLaunch{};
-    p->counts = counts;
-    p->offsets = starts;
-    p->mt_prefix = mt_prefix;
-    p->err = reinterpret_cast<int32_t *>(b);
-    p->sched = reinterpret_cast<int32_t *>(b + 8);
-    p->E = static_cast<int>(s.G);
-    p->k = 1;
-    p->R = static_cast<int>(s.R);
-    p->num_sms = d.num_sms;
-    return cuda_status(launch_grouped_tiles(offsets, p->E, p->R, counts, starts, mt_prefix, p->err, st));
 }
 
 struct RouteWs {
@@ -1831,28 +1808,23 @@ moe_status_t moe_grouped_mm_mx(const void *x_codes, const void *x_scales, const 
         return MOE_ERR_INVALID_ARG;
     DeviceState *d = nullptr;
     if ((r = device_state(&d)) != MOE_OK) return r;
+    if (d->clusters < 1) return MOE_ERR_UNSUPPORTED;
     const uint64_t rows = static_cast<uint64_t>(s.G) * s.N;
-    CUtensorMap tm_x, tm_w, tm_out, tm_xs, tm_ws;
-    if (!encode_u8_2d(&tm_x, x_codes, s.K, s.R, 128, 128) || !encode_u8_2d(&tm_w, w_codes, s.K, rows, 128, 224) ||
-        !encode_bf16_2d_strided(&tm_out, out, s.N, s.R, s.ld_out, 32, 32) ||
-        !encode_sf_words(&tm_xs, x_scales, mx_rows(s.R), s.K / 128, kSfBoxRowsA) ||
-        !encode_sf_words(&tm_ws, w_scales, rows, s.K / 128, 224))
+    const uint32_t most = static_cast<uint32_t>(grouped_most(s.R, s.G, true));
+    CUtensorMap tm_x, tm_wide, tm_w, tm_xs, tm_ws;
+    if (!encode_u8_2d(&tm_x, x_codes, s.K, s.R, 128, 32) || !encode_u8_2d(&tm_wide, x_codes, s.K, s.R, 128, most / 2) ||
+        !encode_u8_2d(&tm_w, w_codes, s.K, rows, 128, 128) ||
+        !encode_sf_words(&tm_xs, x_scales, mx_rows(s.R), s.K / 128, most + 4, most > 192 ? 2 : 4) ||
+        !encode_sf_words(&tm_ws, w_scales, rows, s.K / 128, 128, most > 192 ? 2 : 4))
         return MOE_ERR_CUDA;
-    GemmLaunch p;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if ((r = grouped_launch(s, offsets, ws, *d, st, &p)) != MOE_OK) return r;
-    p.tm_a = &tm_x;
-    p.tm_b = &tm_w;
-    p.tm_out = &tm_out;
-    p.tm_sfa = &tm_xs;
-    p.tm_sfb = &tm_ws;
-    p.out = static_cast<__nv_bfloat16 *>(out);
-    p.K = static_cast<int>(s.K);
-    p.n_out = static_cast<int>(s.N);
-    p.n_tile = 224;
-    p.b_rows = static_cast<int>(s.N);
-    p.out_ld = static_cast<int>(s.ld_out);
-    return cuda_status(launch_grouped_mx(p, st));
+    PairLaunch p = pair_launch(s, offsets, ws, *d);
+    p.tm_a = &tm_w;
+    p.tm_b = &tm_x;
+    p.tm_b_wide = &tm_wide;
+    p.tm_sfa = &tm_ws;
+    p.tm_sfb = &tm_xs;
+    p.out = out;
+    return cuda_status(launch_pair(p, GroupedKind::rows_mx, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status_t moe_route_workspace_size(const moe_route_shape_t *shape, size_t *bytes) {

@@ -8,6 +8,7 @@
 //   kPairRows   out[r, n] = x[r, :] . w[g, n, :]     w [G, N, K], K-major
 //   kPairRowsT  out[r, n] = x[r, :] . w[g, :, n]     w [G, K, N], MN-major
 //   kPairWgrad  dw[g, n, k] = sum over g's rows of a[r, n] b[r, k]
+//   kPairMx     kPairRows on MXFP8 operands
 //
 // In the first two the matrix is the MMA's A (256 columns n of out as its M) and the rows are its B:
 // N is any multiple of 32, so a tile takes little more tensor time than its rows need, and a group's rows
@@ -19,10 +20,16 @@
 // (Warps that zeroed those rows in shared memory cost 112 of 330 us for 24576 rows of 64 groups,
 // 2048 x 2816: the MMAs waited for them at every tile's end.)
 //
+// kPairMx runs the block-scaled MMAs on E4M3 codes, 128 deep a stage. The scale words (one of a row and
+// k-block) come with TMA, those of two or four k-blocks at a time, and four more warps of each CTA put them into its
+// tensor memory: those of its own half of the matrix's columns, and of all rows of x.
+//
 // Roles of a CTA: warp 0 loads its halves with TMA onto the leader's barriers; warp 1 of the leader
 // issues the MMAs; warps 2 .. 9 are the epilogue. Tiles are dealt to the clusters in turn. Every CTA
 // reads the group offsets itself.
 #pragma once
+
+#include <type_traits>
 
 #include "gemm_kernel.cuh"
 
@@ -30,27 +37,40 @@ namespace moe {
 
 namespace {
 
-enum PairMode : int { kPairRows = 0, kPairRowsT = 1, kPairWgrad = 2 };
+enum PairMode : int { kPairRows = 0, kPairRowsT = 1, kPairWgrad = 2, kPairMx = 3 };
 
 constexpr int kPairHalf = 128 * BK * 2;     // bytes of a CTA's half of one operand's k-block
-constexpr int kPairBoxRows = 32;            // rows of x in one copy: of these, or of 128
+constexpr int kPairBoxRows = 32;            // rows of x in one copy: of these, or of all that a CTA can have
 constexpr int kMaxGroups = 1024;
 
-constexpr int kPairThreads = 64 + EPI_THREADS;
-template <int MODE> constexpr bool kPairAMn = MODE != kPairRows;
+template <int MODE> constexpr int kPairThreads = 64 + EPI_THREADS + (MODE == kPairMx ? HELPER_THREADS : 0);
+template <int MODE> constexpr bool kPairAMn = MODE == kPairRowsT || MODE == kPairWgrad;
 template <int MODE> constexpr bool kPairBMn = MODE == kPairWgrad;
 
 // Shared memory for tiles of at most MOST rows of x (kPairWgrad: 256). Their bytes of a k-block in a CTA, of
 // x beside the matrix's 16 KB, leave room for ten stages or six: with few rows a tile only streams its
-// matrix, and more of it in flight counts (1024 rows of 64 groups, 4096 x 1536: 141 us, and 148 with six).
-template <int MOST> constexpr int kPairB = MOST * BK;
-template <int MOST> constexpr int kPairStagesOf = MOST == 64 ? 10 : 6;
+// matrix, and more of it in flight counts (1024 rows of 64 groups, 4096 x 1536: 128 us, and 134 with six).
+template <int MOST> constexpr int kPairB = MOST / 2 * BK * 2;
+template <int MOST> constexpr int kPairStagesOf = MOST == 64 ? 10 : MOST == 192 ? 7 : 6;
+// kPairMx: the scale words of some k-blocks in shared memory, of 128 matrix rows and, from a row whose number
+// is a multiple of 4, of MOST rows of x; in tensor memory 16 columns a k-block behind each accumulator, of four
+// k-blocks where these leave 64 columns, of two where they leave 32.
+constexpr int kSfSlots = 3;
+template <int MOST> constexpr int kSfDeepOf = MOST > 192 ? 2 : 4;
+template <int MOST> constexpr int kPairSfB = kSfDeepOf<MOST> * 512;
+template <int MOST> constexpr int kPairSfBytes = kPairSfB<MOST> + kSfDeepOf<MOST> * 4 * (MOST + 4);     // of a copy
+template <int MODE, int MOST> constexpr int kPairSf = MODE == kPairMx ? (kPairSfBytes<MOST> + 127) / 128 * 128 : 16;
 template <int MODE, int MOST>
 struct __align__(1024) PairSmem {
     static constexpr int kPairStages = kPairStagesOf<MOST>;
     uint8_t a[kPairStages][kPairHalf];
     uint8_t b[kPairStages][kPairB<MOST>];
     uint8_t box[MODE == kPairWgrad ? EPI_WARPS : 1][32 * 64];       // kPairWgrad: a warp's 32 x 32 output box
+    uint8_t sf[kSfSlots][kPairSf<MODE, MOST>];              // kPairMx: scale words
+    uint64_t sf_full[kSfSlots];             // ... have landed
+    uint64_t sf_read[kSfSlots];             // ... have been read
+    uint64_t sf_ready[2];                   // the leader's: ... are in tensor memory of both CTAs
+    uint64_t sf_free[2];                    // ... the MMAs have used them
     uint64_t full[kPairStages];             // the leader's: both CTAs' halves have landed
     uint64_t empty[kPairStages];            // the MMAs have read the stage
     uint64_t acc_full[2];
@@ -79,8 +99,12 @@ struct PairArgs {
 };
 struct PairMaps {
     CUtensorMap a, b;
-    CUtensorMap b_wide;     // rows: x in boxes of 128 rows
+    CUtensorMap b_wide;     // rows: x in boxes of MOST / 2 rows
 };
+struct PairMxMaps : PairMaps {
+    CUtensorMap sfa, sfb;   // scale words of the matrices, and of x
+};
+template <int MODE> using PairMapsOf = std::conditional_t<MODE == kPairMx, PairMxMaps, PairMaps>;
 
 // ---------------------------------------------------------------- cluster and pair instructions
 
@@ -147,6 +171,34 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ void pair_mma_mx(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sfa,
+                                            uint32_t sfb, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc) : "memory");
+}
+// One lane of a warp that runs together: always the same one. (In code that one lane runs by this choice the
+// compiler knows so, and the operands of copies and MMAs stay in uniform registers. By `lane == 0` four MMAs and a
+// commit took 565 .. 780 cycles to issue: 1024 rows of 64 groups, 4096 x 1536, 141 us, and 130 by this; MXFP8 91
+// and 76.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+// A place in a ring of N slots, and the parity of its turn.
+template <int N> struct Ring {
+    int s = 0;
+    uint32_t turn = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == N) {
+            s = 0;
+            turn ^= 1u;
+        }
+    }
+};
 // Arrives on `bar` in both CTAs when the MMAs issued so far are done.
 __device__ __forceinline__ void pair_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
@@ -217,7 +269,7 @@ __device__ __forceinline__ PairTile pair_tile(int u, const PairSmem<MODE, MOST> 
         t.k0 = 0;
         t.row0 = sm.start[lo] + m * each;
         t.rows = min(each, rows - m * each);
-        t.nkb = (p.K + BK - 1) / BK;
+        t.nkb = MODE == kPairMx ? p.K / 128 : (p.K + BK - 1) / BK;
     }
     return t;
 }
@@ -243,13 +295,13 @@ __device__ __forceinline__ void pair_load_rows(uint32_t sa, uint32_t sb, const C
 // ---------------------------------------------------------------- the kernel
 
 template <int MODE, int MOST>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<MODE>, 1)
+pair_gemm_kernel(const __grid_constant__ PairMapsOf<MODE> maps, const PairArgs p) {
     griddep_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     using Smem = PairSmem<MODE, MOST>;
-    constexpr int kPairStages = Smem::kPairStages;
+    constexpr int kPairStages = Smem::kPairStages, kSfDeep = kSfDeepOf<MOST>;
     static_assert(kPairSmemBytes<MODE, MOST> <= 227 * 1024, "shared memory of a CTA");
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (raw & 1023u)) & 1023u));
     volatile int *abort_flag = &sm.abort;
@@ -262,9 +314,17 @@ pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
             mbar_init(smem_addr(&sm.full[s]), 1);
             mbar_init(smem_addr(&sm.empty[s]), 1);
         }
+        for (int s = 0; MODE == kPairMx && s < kSfSlots; ++s) {
+            mbar_init(smem_addr(&sm.sf_full[s]), 1);
+            mbar_init(smem_addr(&sm.sf_read[s]), HELPER_WARPS);
+        }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_addr(&sm.acc_full[b]), 1);
             mbar_init(smem_addr(&sm.acc_empty[b]), 2 * EPI_WARPS);
+            if constexpr (MODE == kPairMx) {
+                mbar_init(smem_addr(&sm.sf_ready[b]), 2 * HELPER_WARPS);
+                mbar_init(smem_addr(&sm.sf_free[b]), 1);
+            }
         }
         mbar_init(smem_addr(&sm.drain), 1);
         sm.abort = 0;
@@ -272,6 +332,10 @@ pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
         tma_prefetch_desc(&maps.a);
         tma_prefetch_desc(&maps.b);
         tma_prefetch_desc(&maps.b_wide);
+        if constexpr (MODE == kPairMx) {
+            tma_prefetch_desc(&maps.sfa);
+            tma_prefetch_desc(&maps.sfb);
+        }
     }
     if (warp == 1) pair_tmem_alloc(smem_addr(&sm.tmem_base), 512);
     tc_fence_before();
@@ -280,7 +344,7 @@ pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
     // The groups' rows and the prefix of their tiles. Offsets that decrease or leave [0, R] would send a
     // product out of its operands: then no group has rows, and the error word says so.
     constexpr int PER = 4;                  // groups a thread
-    static_assert(PER * kPairThreads >= kMaxGroups, "every group has a thread");
+    static_assert(PER * kPairThreads<MODE> >= kMaxGroups, "every group has a thread");
     int first[PER], count[PER], sum = 0;
     bool bad = false;
 #pragma unroll
@@ -324,9 +388,11 @@ pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
 
     if (warp == 0) {
         // ------------------------------------------------ loads
-        if (lane == 0) {
-            int it = 0, seen = -1;
+        if (elect_one()) {
+            int seen = -1;
             bool ok = true;
+            Ring<kPairStages> at;
+            Ring<kSfSlots> sf;
             for (int u = cluster; ok && u < total; u += clusters) {
                 const PairTile t = pair_tile<MODE, MOST>(u, sm, p);
                 const CUtensorMap *ma = &maps.a, *mb = &maps.b;
@@ -339,80 +405,104 @@ pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
                         seen = t.g;
                     }
                 }
-                // the tile's rows in this CTA (half of the MMA's N), in one copy of 128 or in copies of 32
+                // the tile's rows in this CTA (half of the MMA's N), in one copy or in copies of 32
                 const int half = MODE == kPairWgrad ? 128 : ((t.rows + 31) & ~31) / 2;
                 const bool wide = half > 64;
-                const uint32_t bytes = kPairHalf + (wide ? 128 : (half + kPairBoxRows - 1) / kPairBoxRows * kPairBoxRows) * BK * 2;
+                const uint32_t bytes =
+                    kPairHalf + (wide ? MOST / 2 : (half + kPairBoxRows - 1) / kPairBoxRows * kPairBoxRows) * BK * 2;
                 const int n = t.n0 + 128 * static_cast<int>(rank);
-                for (int kb = 0; kb < t.nkb; ++kb, ++it) {
-                    const int s = it % kPairStages;
-                    if (!mbar_wait(smem_addr(&sm.empty[s]), ((it / kPairStages) & 1) ^ 1u, abort_flag, p.err)) {
-                        ok = false;
-                        break;
+                const int r = t.row0 + half * static_cast<int>(rank);
+                for (int kb = 0; kb < t.nkb; ++kb, at.next()) {
+                    if constexpr (MODE == kPairMx) {
+                        if (kb % kSfDeep == 0) {
+                            const uint32_t sff = smem_addr(&sm.sf_full[sf.s]), dst = smem_addr(sm.sf[sf.s]);
+                            ok = mbar_wait(smem_addr(&sm.sf_read[sf.s]), sf.turn ^ 1u, abort_flag, p.err);
+                            if (!ok) break;
+                            mbar_arrive_expect_tx(sff, kPairSfBytes<MOST>);
+                            tma_load_2d(dst, &maps.sfa, t.g * p.N + n, kb, sff);
+                            tma_load_2d(dst + kPairSfB<MOST>, &maps.sfb, t.row0 & ~3, kb, sff);
+                            sf.next();
+                        }
                     }
-                    const uint32_t sa = smem_addr(sm.a[s]), sb = smem_addr(sm.b[s]);
+                    ok = mbar_wait(smem_addr(&sm.empty[at.s]), at.turn ^ 1u, abort_flag, p.err);
+                    if (!ok) break;
+                    const uint32_t sa = smem_addr(sm.a[at.s]), sb = smem_addr(sm.b[at.s]);
                     // (the leader expects both CTAs' bytes: an arrival of the other with release at the
                     // cluster's scope in every k-block made the kernel 2.4 times slower)
-                    const uint32_t bar = leader_addr(smem_addr(&sm.full[s]));
-                    if (rank == 0) mbar_arrive_expect_tx(smem_addr(&sm.full[s]), 2 * bytes);
-                    if constexpr (MODE == kPairRows) {
-                        pair_load_2d(sa, &maps.a, kb * BK, t.g * p.N + n, bar);
+                    const uint32_t bar = leader_addr(smem_addr(&sm.full[at.s]));
+                    if (rank == 0) mbar_arrive_expect_tx(smem_addr(&sm.full[at.s]), 2 * bytes);
+                    const int kx = kb * (MODE == kPairMx ? 128 : BK);
+                    if constexpr (MODE == kPairRows || MODE == kPairMx) {
+                        pair_load_2d(sa, &maps.a, kx, t.g * p.N + n, bar);
                     } else if constexpr (MODE == kPairRowsT) {
                         if (p.a_one) {
-                            pair_load_4d(sa, &maps.a, kb * BK, n / 64, t.g, bar);
+                            pair_load_4d(sa, &maps.a, kx, n / 64, t.g, bar);
                         } else {
-                            pair_load_3d(sa, &maps.a, n, kb * BK, t.g, bar);
-                            pair_load_3d(sa + MN_ATOM_BYTES, &maps.a, n + 64, kb * BK, t.g, bar);
+                            pair_load_3d(sa, &maps.a, n, kx, t.g, bar);
+                            pair_load_3d(sa + MN_ATOM_BYTES, &maps.a, n + 64, kx, t.g, bar);
                         }
                     } else {
-                        pair_load_rows(sa, sb, ma, mb, p, t, rank, t.row0 + kb * BK, bar);
+                        pair_load_rows(sa, sb, ma, mb, p, t, rank, t.row0 + kx, bar);
                     }
                     if constexpr (MODE != kPairWgrad) {
-                        const int r = t.row0 + half * static_cast<int>(rank);
                         if (MOST > 64 && wide) {
-                            pair_load_2d(sb, &maps.b_wide, kb * BK, r, bar);
+                            pair_load_2d(sb, &maps.b_wide, kx, r, bar);
                         } else {
                             for (int i = 0; i < half; i += kPairBoxRows)
-                                pair_load_2d(sb + i * BK * 2, &maps.b, kb * BK, r + i, bar);
+                                pair_load_2d(sb + i * BK * 2, &maps.b, kx, r + i, bar);
                         }
                     }
                 }
             }
-            // the last arrivals on this CTA's barriers have come before it ends
-            for (int i = max(0, it - kPairStages); ok && i < it; ++i)
-                ok = mbar_wait(smem_addr(&sm.empty[i % kPairStages]), (i / kPairStages) & 1, abort_flag, p.err);
+            // the last arrivals on this CTA's barriers have come before it ends: `empty` completes once for each
+            // turn, and of a slot that was never filled the turn before the first counts as complete
+            for (int i = 0; ok && i < kPairStages; ++i, at.next())
+                ok = mbar_wait(smem_addr(&sm.empty[at.s]), at.turn ^ 1u, abort_flag, p.err);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMAs, of both CTAs by the leader
-        if (rank == 0 && lane == 0) {
-            int it = 0, n_done = 0;
+        if (rank == 0 && elect_one()) {
+            int n_done = 0;
             bool ok = true, any = false;
+            Ring<kPairStages> at;
+            Ring<2> sf;
             for (int u = cluster; ok && u < total; u += clusters, ++n_done) {
                 const PairTile t = pair_tile<MODE, MOST>(u, sm, p);
                 const int buf = n_done & 1;
-                if (!mbar_wait(smem_addr(&sm.acc_empty[buf]), ((n_done >> 1) & 1) ^ 1u, abort_flag, p.err)) {
-                    ok = false;
-                    break;
-                }
+                ok = mbar_wait(smem_addr(&sm.acc_empty[buf]), ((n_done >> 1) & 1) ^ 1u, abort_flag, p.err);
+                if (!ok) break;
                 tc_fence_after();
                 const int n_mma = MODE == kPairWgrad ? 256 : (t.rows + 31) & ~31;
                 uint32_t idesc = idesc_bf16_f32(256, n_mma) | (kPairAMn<MODE> ? (1u << 15) : 0u) |
                                  (kPairBMn<MODE> ? (1u << 16) : 0u);
                 if (p.f16) idesc &= ~((1u << 7) | (1u << 10));      // operand formats 0, fp16, for 1, bf16
-                for (int kb = 0; kb < t.nkb; ++kb, ++it) {
-                    const int s = it % kPairStages;
-                    if (!mbar_wait(smem_addr(&sm.full[s]), (it / kPairStages) & 1, abort_flag, p.err)) {
-                        ok = false;
-                        break;
-                    }
+                for (int kb = 0; kb < t.nkb; ++kb, at.next()) {
+                    ok = mbar_wait(smem_addr(&sm.full[at.s]), at.turn, abort_flag, p.err);
+                    if (MODE == kPairMx && ok && kb % kSfDeep == 0)
+                        ok = mbar_wait(smem_addr(&sm.sf_ready[sf.s]), sf.turn, abort_flag, p.err);
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t sa = smem_addr(sm.a[s]), sb = smem_addr(sm.b[s]);
+                    const bool last = MODE == kPairMx && (kb % kSfDeep == kSfDeep - 1 || kb == t.nkb - 1);
+                    const uint32_t sa = smem_addr(sm.a[at.s]), sb = smem_addr(sm.b[at.s]);
+                    if constexpr (MODE == kPairMx) {
+                        const uint32_t words = tmem + 256 * sf.s + MOST + 16 * (kb % kSfDeep);
 #pragma unroll
-                    for (int kk = 0; kk < BK / UMMA_K; ++kk)
-                        pair_mma(tmem + buf * 256, operand_desc<kPairAMn<MODE>>(sa, kk), operand_desc<kPairBMn<MODE>>(sb, kk),
-                                 idesc, (kb > 0 || kk > 0) ? 1u : 0u);
-                    pair_commit(smem_addr(&sm.empty[s]));
+                        for (int kk = 0; kk < 4; ++kk)      // K = 32 each: byte kk of the scale words
+                            pair_mma_mx(tmem + buf * 256, smem_desc_swizzled<128>(sa + kk * 32),
+                                        smem_desc_swizzled<128>(sb + kk * 32), idesc_mxf8(256, n_mma, kk), words, words + 8,
+                                        (kb > 0 || kk > 0) ? 1u : 0u);
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < BK / UMMA_K; ++kk)
+                            pair_mma(tmem + buf * 256, operand_desc<kPairAMn<MODE>>(sa, kk),
+                                     operand_desc<kPairBMn<MODE>>(sb, kk), idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    pair_commit(smem_addr(&sm.empty[at.s]));
+                    if (last) {
+                        pair_commit(smem_addr(&sm.sf_free[sf.s]));
+                        sf.next();
+                    }
                     any = true;
                 }
                 if (!ok) break;
@@ -424,7 +514,7 @@ pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
             }
         }
         __syncwarp();
-    } else {
+    } else if (warp < 2 + EPI_WARPS) {
         // ------------------------------------------------ epilogue
         const int quad = warp & 3, side = (warp - 2) >> 2;      // lanes of tensor memory, half of the columns
         const uint32_t tacc = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 128 * side;
@@ -508,6 +598,54 @@ pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs p) {
                             *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(8 * i) * p.K + 32 * c) = v[i];
                 }
             }
+        }
+    } else {
+        // ------------------------------------------------ scale words into tensor memory (kPairMx)
+        if constexpr (MODE == kPairMx) {
+            const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+            int sf = 0;
+            bool ok = true;
+            for (int u = cluster; ok && u < total; u += clusters) {
+                const PairTile t = pair_tile<MODE, MOST>(u, sm, p);
+                const int rem = t.row0 & 3;                 // the copy began at a multiple of 4
+                for (int kb = 0; kb < t.nkb; kb += kSfDeep, ++sf) {
+                    const int q = sf % kSfSlots;
+                    const uint32_t sff = smem_addr(&sm.sf_full[q]), at = smem_addr(sm.sf[q]);
+                    const uint32_t parity = (sf / kSfSlots) & 1;
+                    if (lane == 0)
+                        ok = mbar_wait(sff, parity, abort_flag, p.err) &&
+                             mbar_wait(smem_addr(&sm.sf_free[sf & 1]), ((sf >> 1) & 1) ^ 1u, abort_flag, p.err);
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                    (void)mbar_try_wait(sff, parity);       // every lane sees the phase
+                    tc_fence_after();
+                    // column j of a k-block: rows 32 j + lane of the matrix, and from column 8 on of x. (Rows behind
+                    // the tile's have any scale: their products are not stored.)
+#pragma unroll
+                    for (int d = 0; d < kSfDeep; ++d) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            if (j < 4) w[j] = ld_shared_u32(at + 512 * d + 4 * (32 * j + lane));
+                            else if (j >= 8 && j - 8 < MOST / 32)
+                                w[j] = ld_shared_u32(at + kPairSfB<MOST> + 4 * (d * (MOST + 4) + rem + 32 * (j - 8) + lane));
+                            else w[j] = 0u;
+                        }
+                        tmem_st16(mine + 256 * (sf & 1) + MOST + 16 * d, w);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_addr(&sm.sf_read[q]));
+                        mbar_arrive_peer(leader_addr(smem_addr(&sm.sf_ready[sf & 1])));
+                    }
+                }
+            }
+            // the last arrivals on this CTA's barriers have come before it ends
+            for (int i = max(0, sf - 2); ok && lane == 0 && i < sf; ++i)
+                ok = mbar_wait(smem_addr(&sm.sf_free[i & 1]), (i >> 1) & 1, abort_flag, p.err);
+            __syncwarp();
         }
     }
 

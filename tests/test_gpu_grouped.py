@@ -318,3 +318,25 @@ def test_captured_replayed_and_on_another_stream():
         assert torch.equal(dx[a:b], (dy[a:b].double() @ w[g].double()).to(BF16))
         assert torch.equal(dw[g], (dy[a:b].double().t() @ x[a:b].double()).to(BF16))
     assert B.moe_get_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("counts,K,N", [([700, 0, 1031, 224, 449], 1664, 776), ([225, 31, 190, 97], 2048, 520), ([7, 0, 13] * 30, 2944, 1032)])
+def test_mxfp8_of_many_blocks(counts, K, N):
+    """Several tiles a group, and more k-blocks than are held at a time: whole numbers whose sums stay below
+    2^24 units are exact."""
+    gen = torch.Generator(DEV).manual_seed(K)
+    offsets, o = offsets_of(counts, 2)
+    R, G = o[-1] + 3, len(counts)
+    x, w = whole(gen, (R, K), BF16, 8), whole(gen, (G, N, K), BF16, 8)
+    xc, xs = quantized(x)
+    wc, wss = quantized(w)
+    xc[:2], xc[o[-1]:] = 0x7f, 0xff                         # NaN in rows of no group
+    want = torch.full((R, N), 77.0, dtype=BF16, device=DEV)
+    for g in range(G):
+        want[o[g]:o[g + 1]] = (x[o[g]:o[g + 1]].double() @ w[g].double().t()).float().to(BF16)
+    out, ws = torch.full((R, N), 77.0, dtype=BF16, device=DEV), B.grouped_workspace(G)
+    for _ in range(3):
+        B.moe_grouped_mm_mx(xc, xs, wc, wss, offsets, out, ws)
+        assert B.moe_get_device_error(ws) == 0
+        assert torch.equal(out, want)
+        out.fill_(77.0)
