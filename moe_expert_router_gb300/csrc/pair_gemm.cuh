@@ -199,6 +199,10 @@ template <int N> struct Ring {
         }
     }
 };
+// A matrix descriptor `bytes` further on.
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t bytes) {
+    return (desc & 0xffffffff00000000ull) | (static_cast<uint32_t>(desc) + (bytes >> 4));
+}
 // Arrives on `bar` in both CTAs when the MMAs issued so far are done.
 __device__ __forceinline__ void pair_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
@@ -467,6 +471,9 @@ pair_gemm_kernel(const __grid_constant__ PairMapsOf<MODE> maps, const PairArgs p
             bool ok = true, any = false;
             Ring<kPairStages> at;
             Ring<2> sf;
+            const uint32_t full0 = smem_addr(sm.full), empty0 = smem_addr(sm.empty);
+            const uint64_t a0 = operand_desc<kPairAMn<MODE>>(smem_addr(sm.a), 0);
+            const uint64_t b0 = operand_desc<kPairBMn<MODE>>(smem_addr(sm.b), 0);
             for (int u = cluster; ok && u < total; u += clusters, ++n_done) {
                 const PairTile t = pair_tile<MODE, MOST>(u, sm, p);
                 const int buf = n_done & 1;
@@ -474,36 +481,45 @@ pair_gemm_kernel(const __grid_constant__ PairMapsOf<MODE> maps, const PairArgs p
                 if (!ok) break;
                 tc_fence_after();
                 const int n_mma = MODE == kPairWgrad ? 256 : (t.rows + 31) & ~31;
-                uint32_t idesc = idesc_bf16_f32(256, n_mma) | (kPairAMn<MODE> ? (1u << 15) : 0u) |
-                                 (kPairBMn<MODE> ? (1u << 16) : 0u);
-                if (p.f16) idesc &= ~((1u << 7) | (1u << 10));      // operand formats 0, fp16, for 1, bf16
-                for (int kb = 0; kb < t.nkb; ++kb, at.next()) {
-                    ok = mbar_wait(smem_addr(&sm.full[at.s]), at.turn, abort_flag, p.err);
-                    if (MODE == kPairMx && ok && kb % kSfDeep == 0)
-                        ok = mbar_wait(smem_addr(&sm.sf_ready[sf.s]), sf.turn, abort_flag, p.err);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const bool last = MODE == kPairMx && (kb % kSfDeep == kSfDeep - 1 || kb == t.nkb - 1);
-                    const uint32_t sa = smem_addr(sm.a[at.s]), sb = smem_addr(sm.b[at.s]);
+                uint32_t idesc = MODE == kPairMx ? idesc_mxf8(256, n_mma, 0)
+                                                 : idesc_bf16_f32(256, n_mma) | (kPairAMn<MODE> ? (1u << 15) : 0u) |
+                                                       (kPairBMn<MODE> ? (1u << 16) : 0u);
+                if (MODE != kPairMx && p.f16) idesc &= ~((1u << 7) | (1u << 10));   // operand formats 0, fp16, for 1, bf16
+                const uint32_t acc = tmem + buf * 256;
+                constexpr int DEEP = MODE == kPairMx ? kSfDeep : 1;
+                for (int kb0 = 0; ok && kb0 < t.nkb; kb0 += DEEP) {
                     if constexpr (MODE == kPairMx) {
-                        const uint32_t words = tmem + 256 * sf.s + MOST + 16 * (kb % kSfDeep);
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)      // K = 32 each: byte kk of the scale words
-                            pair_mma_mx(tmem + buf * 256, smem_desc_swizzled<128>(sa + kk * 32),
-                                        smem_desc_swizzled<128>(sb + kk * 32), idesc_mxf8(256, n_mma, kk), words, words + 8,
-                                        (kb > 0 || kk > 0) ? 1u : 0u);
-                    } else {
-#pragma unroll
-                        for (int kk = 0; kk < BK / UMMA_K; ++kk)
-                            pair_mma(tmem + buf * 256, operand_desc<kPairAMn<MODE>>(sa, kk),
-                                     operand_desc<kPairBMn<MODE>>(sb, kk), idesc, (kb > 0 || kk > 0) ? 1u : 0u);
+                        ok = mbar_wait(smem_addr(&sm.sf_ready[sf.s]), sf.turn, abort_flag, p.err);
+                        if (!ok) break;
+                        tc_fence_after();
                     }
-                    pair_commit(smem_addr(&sm.empty[at.s]));
-                    if (last) {
-                        pair_commit(smem_addr(&sm.sf_free[sf.s]));
+#pragma unroll
+                    for (int d = 0; d < DEEP; ++d) {
+                        if (d > 0 && kb0 + d >= t.nkb) break;
+                        ok = mbar_wait(full0 + 8 * at.s, at.turn, abort_flag, p.err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t da = desc_at(a0, kPairHalf * at.s), db = desc_at(b0, kPairB<MOST> * at.s);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint32_t more = d > 0 || kk > 0 ? 1u : kb0 > 0;
+                            if constexpr (MODE == kPairMx) {        // K = 32 each: byte kk of the scale words
+                                const uint32_t words = tmem + 256 * sf.s + MOST + 16 * d;
+                                pair_mma_mx(acc, desc_at(da, 32 * kk), desc_at(db, 32 * kk), idesc | idesc_mxf8(0, 0, kk), words,
+                                            words + 8, more);
+                            } else {
+                                pair_mma(acc, desc_at(da, kk * (kPairAMn<MODE> ? UMMA_K * 128 : UMMA_K * 2)),
+                                         desc_at(db, kk * (kPairBMn<MODE> ? UMMA_K * 128 : UMMA_K * 2)), idesc, more);
+                            }
+                        }
+                        pair_commit(empty0 + 8 * at.s);
+                        any = true;
+                        at.next();
+                    }
+                    if constexpr (MODE == kPairMx) {
+                        if (ok) pair_commit(smem_addr(&sm.sf_free[sf.s]));
                         sf.next();
                     }
-                    any = true;
                 }
                 if (!ok) break;
                 pair_commit(smem_addr(&sm.acc_full[buf]));      // at once without k-blocks: the epilogue writes zeros
