@@ -119,9 +119,8 @@ __device__ __forceinline__ uint32_t pack2(float2 v, __half) {
 
 // ---------------------------------------------------------------- the kernel
 
-// Blocks of the most threads that an SM has room for: left to itself the compiler takes 88 registers
-// for rows of 7168 (8192 of them with MXFP8: 120 us, 89 with 80), and 100 for those of 16384 (4096 of
-// them: 117 us, 87 with 64).
+// Blocks of the most threads that an SM has room for: left to itself the compiler takes more registers
+// (8192 rows of 7168 with MXFP8 122 us, and 92 by this; 4096 rows of 16384 120, and 95).
 template <typename L>
 constexpr int kNormBlocks = L::MOST == 256 ? 3 : (L::MOST == 512 ? 2 : 1);
 

@@ -209,7 +209,7 @@ cudaError_t launch_dw(const NormBackwardLaunch &p, cudaStream_t st) {
 }  // namespace
 
 // Blocks of the backward, as many as an SM holds and no more (each has a part of dw to write and to be
-// added: 4096 rows of 2048 in four blocks an SM 20 us, in eight 27; 16384 of 1024 38, and 32), and no
+// added: 4096 rows of 2048 in four blocks an SM 17 us, in eight 21; 16384 of 1024 34, and 27), and no
 // block has more than kNormRowsPerBlock rows a thread.
 int64_t rms_norm_bwd_blocks(int64_t T, int64_t H) {
     const int64_t wave = 152 * (H <= 512 ? 6 : H <= 1024 ? 8 : H <= 4096 ? 4 : 2);
