@@ -340,3 +340,34 @@ def test_mxfp8_of_many_blocks(counts, K, N):
         assert B.moe_get_device_error(ws) == 0
         assert torch.equal(out, want)
         out.fill_(77.0)
+
+
+def test_mxfp8_on_two_streams_and_replayed():
+    """Two calls at a time, each with a workspace of its own, and a captured one replayed on new operands."""
+    gen = torch.Generator(DEV).manual_seed(11)
+    counts, K, N = [130, 0, 300, 5], 640, 520
+    offsets, o = offsets_of(counts)
+    sets = []
+    for _ in range(3):
+        x, w = whole(gen, (o[-1], K), BF16, 8), whole(gen, (len(counts), N, K), BF16, 8)
+        want = torch.cat([(x[a:b].double() @ m.double().t()).float().to(BF16) for a, b, m in zip(o, o[1:], w)])
+        sets.append((*quantized(x), *quantized(w), want, torch.empty_like(want), B.grouped_workspace(len(counts))))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for s, (xc, xs, wc, wss, _, out, ws) in zip(streams, sets):
+            with torch.cuda.stream(s):
+                B.moe_grouped_mm_mx(xc, xs, wc, wss, offsets, out, ws)
+    torch.cuda.synchronize()
+    for _, _, _, _, want, out, ws in sets[:2]:
+        assert B.moe_get_device_error(ws) == 0 and torch.equal(out, want)
+    xc, xs, wc, wss, _, out, ws = sets[2]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.moe_grouped_mm_mx(xc, xs, wc, wss, offsets, out, ws)
+    for other in sets[:2]:
+        for dst, src in zip((xc, xs, wc, wss), other):
+            dst.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, other[4])
