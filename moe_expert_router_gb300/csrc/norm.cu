@@ -95,13 +95,23 @@ __device__ __forceinline__ Pair inverse_root(Pair sum, float scale, const NormLa
     return {root.hi * scale, root.lo * scale};
 }
 
+// From here on a product is left to 64 bits: its low part would be the difference of two infinities.
+constexpr float kMost = 1.7014118346046923e38f;             // 2^127
+
 // (h rstd is taken first: it stays below sqrt(H), where h w may leave fp32's range.)
 // The nearest number of the 16-bit type to h rstd w, from some 48 bits of it: fp32 with its last
-// bit set where digits follow (round to odd) rounds on as the exact value would.
+// bit set where digits follow (round to odd) rounds on as the exact value would. fp32 itself comes here for large
+// products alone.
 template <typename T>
 __device__ __noinline__ T rounded_once(float h, float w, Pair r) {
     const float z = __fmul_rn(h, r.hi), zl = fmaf(h, r.lo, fmaf(h, r.hi, -z));
     const float y = __fmul_rn(z, w);
+    if (sizeof(T) == 4 || !(fabsf(y) < kMost)) {
+        const double v = static_cast<double>(h) * (static_cast<double>(r.hi) + r.lo) * w;
+        if constexpr (sizeof(T) == 4) return __double2float_rn(v);
+        const float f = __double2float_rz(v);
+        return from_float<T>(static_cast<double>(f) != v ? __uint_as_float(__float_as_uint(f) | 1u) : f);
+    }
     const Pair n = normal(y, fmaf(zl, w, fmaf(z, w, -y)));
     uint32_t b = __float_as_uint(n.hi);
     if ((b & 1u) == 0u && (n.lo < 0.f || n.lo > 0.f)) b += (n.lo > 0.f) == (n.hi > 0.f) ? 1u : 0xffffffffu;
@@ -196,9 +206,7 @@ rms_norm_kernel(const NormLaunch p) {
             for (int j = 0; j < N; ++j) {
                 const float z = __fmul_rn(h[v].v[j], r.hi), zl = fmaf(h[v].v[j], r.lo, fmaf(h[v].v[j], r.hi, -z));
                 const float o = __fmul_rn(z, w[j]);
-                // (not finite: the corrections would be NaN)
-                const float more = fmaf(zl, w[j], fmaf(z, w[j], -o));
-                y.v[j] = fabsf(o) < __int_as_float(0x7f800000) ? o + more : o;
+                y.v[j] = fabsf(o) < kMost ? o + fmaf(zl, w[j], fmaf(z, w[j], -o)) : rounded_once<T>(h[v].v[j], w[j], r);
             }
         } else {
             uint32_t *out = reinterpret_cast<uint32_t *>(&y.raw);
