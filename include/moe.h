@@ -365,8 +365,11 @@ moe_status_t moe_bias_update(float *bias, const int32_t *counts, int64_t L, int6
  *   h = x + residual (rounded to their type; h = x without a residual)
  *   rstd[t] = 1 / sqrt(mean_c h[t,c]^2 + eps);   y[t,c] = h[t,c] rstd[t] weight[c]
  *   codes, scales = moe_mx_quantize of y
- * y is the exact value rounded once, whatever T and H (a row with an infinity has 0 for its
- * finite elements); the same bits on every call.
+ * y is the exact value rounded once, whatever T and H and however large the row (one with an
+ * infinity has 0 for its finite elements); the same bits on every call. Two limits of 16-bit
+ * rows: an element whose h rstd is below 2^-190 in magnitude (beside others 2^190 as large) may
+ * lose digits, and a bf16 result below 2^-126, its smallest normal number, is rounded by way of
+ * fp32 (within half its step and 2^-149).
  *
  * x, residual, h and y are of one type (dtype); weight is of that type or fp32. Rows of x
  * and residual may lie apart; h, y and codes are dense [T,H]. Any H <= 16384; whole 16-byte

@@ -11,7 +11,9 @@
 // Dekker 1971, "A floating-point technique for extending the available precision"), 1 / sqrt is
 // one Newton step on such a pair, and an element whose fp32 product lies within its error of a
 // border between two values of the 16-bit type, one in some thousand, is rounded from the product
-// to 48 bits. Two elements go through each fp32 instruction (f32x2).
+// to 48 bits (with its neighbour alone, not its vector: 8192 rows of 7168 fp16 with MXFP8 111 us, and 101). What
+// fp32's ends cut, of rows near its largest number, say, is rounded from 64 bits. Two elements go through each
+// fp32 instruction (f32x2).
 #include "norm.cuh"
 
 namespace moe {
@@ -76,7 +78,10 @@ __device__ __forceinline__ Pair normal(float hi, float lo) {
     return {s, __fsub_rn(lo, __fsub_rn(s, hi))};
 }
 
-// scale sqrt(H) / sqrt(sum + scale^2 H eps) for a sum of H squares of scale h; scale is a power of two.
+// kUp times 1 / rms, for a sum of H squares of scale h (a power of two). Rows near fp32's largest number have 1 / rms
+// below its normal ones, and their elements may lie far below them: at 2^64 as large all of it keeps its digits.
+// (1 / rms is 2^50 at most, and products, z of sqrt(H) at most, have room for y up to 2^64.)
+constexpr float kUp = 1.8446744073709552e19f, kDown = 5.421010862427522e-20f;   // 2^64, 2^-64
 __device__ __forceinline__ Pair inverse_root(Pair sum, float scale, const NormLaunch &p) {
     if (!(sum.hi < __int_as_float(0x7f800000))) return {1.f / sum.hi, 0.f};     // infinity: 0; NaN
     const Pair a = join(sum, {p.h_eps_hi * scale * scale, p.h_eps_lo * scale * scale});
@@ -92,30 +97,36 @@ __device__ __forceinline__ Pair inverse_root(Pair sum, float scale, const NormLa
     const float m = __fmul_rn(r, p.root_h_hi);
     const float ml = fmaf(r, p.root_h_hi, -m);
     const Pair root = normal(m, fmaf(r, p.root_h_lo, fmaf(rl, p.root_h_hi, ml)));
-    return {root.hi * scale, root.lo * scale};
+    return {root.hi * (scale * kUp), root.lo * (scale * kUp)};
 }
 
-// From here on a product is left to 64 bits: its low part would be the difference of two infinities.
-constexpr float kMost = 1.7014118346046923e38f;             // 2^127
+// Where z = h r or y = z w is not between these, they or their low parts may have lost digits to fp32's ends.
+constexpr float kLeast = 1.4551915228366852e-11f, kMost = 1.7014118346046923e38f;   // 2^-36, 2^127
+__device__ __forceinline__ bool inside(float z, float y) { return fminf(fabsf(z), fabsf(y)) >= kLeast && fabsf(y) < kMost; }
 
-// (h rstd is taken first: it stays below sqrt(H), where h w may leave fp32's range.)
-// The nearest number of the 16-bit type to h rstd w, from some 48 bits of it: fp32 with its last
-// bit set where digits follow (round to odd) rounds on as the exact value would. fp32 itself comes here for large
-// products alone.
+// h r / kUp w rounded once. (h r is taken first: it stays below kUp sqrt(H), where h w may leave fp32's range.) A
+// value of more digits is cut to fp32 with its last bit set where digits follow (round to odd): from there it rounds on
+// to 16 bits as it would itself.
 template <typename T>
 __device__ __noinline__ T rounded_once(float h, float w, Pair r) {
-    const float z = __fmul_rn(h, r.hi), zl = fmaf(h, r.lo, fmaf(h, r.hi, -z));
-    const float y = __fmul_rn(z, w);
-    if (sizeof(T) == 4 || !(fabsf(y) < kMost)) {
-        const double v = static_cast<double>(h) * (static_cast<double>(r.hi) + r.lo) * w;
-        if constexpr (sizeof(T) == 4) return __double2float_rn(v);
-        const float f = __double2float_rz(v);
-        return from_float<T>(static_cast<double>(f) != v ? __uint_as_float(__float_as_uint(f) | 1u) : f);
+    const float z = __fmul_rn(h, r.hi), y = __fmul_rn(z, w);
+    if (!inside(z, y)) {                                    // in 64 bits
+        if (h == 0.f || w == 0.f) return from_float<T>(y);
+        const double v = static_cast<double>(h) * ((static_cast<double>(r.hi) + r.lo) * kDown) * w;
+        if constexpr (sizeof(T) == 4) {
+            return __double2float_rn(v);
+        } else {
+            const float f = __double2float_rz(v);
+            return from_float<T>(static_cast<double>(f) != v ? __uint_as_float(__float_as_uint(f) | 1u) : f);
+        }
     }
+    // from some 48 bits
+    const float zl = fmaf(h, r.lo, fmaf(h, r.hi, -z));
     const Pair n = normal(y, fmaf(zl, w, fmaf(z, w, -y)));
+    if constexpr (sizeof(T) == 4) return n.hi * kDown;
     uint32_t b = __float_as_uint(n.hi);
     if ((b & 1u) == 0u && (n.lo < 0.f || n.lo > 0.f)) b += (n.lo > 0.f) == (n.hi > 0.f) ? 1u : 0xffffffffu;
-    return from_float<T>(__uint_as_float(b));
+    return from_float<T>(__uint_as_float(b) * kDown);
 }
 
 __device__ __forceinline__ uint32_t pack2(float2 v, __nv_bfloat16) {
@@ -130,9 +141,10 @@ __device__ __forceinline__ uint32_t pack2(float2 v, __half) {
 // ---------------------------------------------------------------- the kernel
 
 // Blocks of the most threads that an SM has room for: left to itself the compiler takes more registers
-// (8192 rows of 7168 with MXFP8 122 us, and 92 by this; 4096 rows of 16384 120, and 95).
+// (8192 rows of 7168 with MXFP8 122 us, and 92 by this; 4096 rows of 16384 120, and 95; four blocks of a warp a
+// row: 65536 rows of 512 54, and 50).
 template <typename L>
-constexpr int kNormBlocks = L::MOST == 256 ? 3 : (L::MOST == 512 ? 2 : 1);
+constexpr int kNormBlocks = L::WARP ? 4 : L::MOST == 256 ? 3 : (L::MOST == 512 ? 2 : 1);
 
 template <typename L>
 __global__ void __launch_bounds__(L::MOST, kNormBlocks<L>)
@@ -192,7 +204,7 @@ rms_norm_kernel(const NormLaunch p) {
         if constexpr (!L::WARP) __syncthreads();
     }
     const Pair r = inverse_root(all, scale, p);
-    if (p.rstd != nullptr && lane.i == 0) p.rstd[t] = r.hi;
+    if (p.rstd != nullptr && lane.i == 0) p.rstd[t] = r.hi * kDown;
     const bool store_h = p.h != nullptr;
     T *ho = static_cast<T *>(p.h) + t * p.H, *yo = static_cast<T *>(p.y) + t * p.H;
 #pragma unroll
@@ -202,27 +214,35 @@ rms_norm_kernel(const NormLaunch p) {
         lane.weight(p.weight, p.w_f32, v, w);
         Vec<T> y;
         if constexpr (sizeof(T) == 4) {
+            bool in = true;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const float z = __fmul_rn(h[v].v[j], r.hi), zl = fmaf(h[v].v[j], r.lo, fmaf(h[v].v[j], r.hi, -z));
                 const float o = __fmul_rn(z, w[j]);
-                y.v[j] = fabsf(o) < kMost ? o + fmaf(zl, w[j], fmaf(z, w[j], -o)) : rounded_once<T>(h[v].v[j], w[j], r);
+                y.v[j] = (o + fmaf(zl, w[j], fmaf(z, w[j], -o))) * kDown;
+                in &= inside(z, o);
+            }
+            if (!in) {
+#pragma unroll
+                for (int j = 0; j < N; ++j) y.v[j] = rounded_once<T>(h[v].v[j], w[j], r);
             }
         } else {
             uint32_t *out = reinterpret_cast<uint32_t *>(&y.raw);
-            uint32_t apart = 0u;
+            uint32_t apart[N / 2], any = 0u;
 #pragma unroll
             for (int j = 0; j < N; j += 2) {
                 const F2 q = mul2(mul2(f2(to_float(h[v].v[j]), to_float(h[v].v[j + 1])), f2(r.hi, r.hi)), f2(w[j], w[j + 1]));
-                // q is good to 3 2^-24: where both ends of its error round alike, so does the product
-                constexpr float kOff = 2.384185791015625e-07f;      // 2^-22
-                const uint32_t lo = pack2(split(mul2(q, f2(1.f - kOff, 1.f - kOff))), T());
-                out[j / 2] = pack2(split(mul2(q, f2(1.f + kOff, 1.f + kOff))), T());
-                apart |= lo ^ out[j / 2];
+                // q is good to 3 2^-24: where both ends of its error round alike, so does the product. The upper end is
+                // 4 2^-24 up, the lower 9 2^-24 below that; of a q that left fp32, infinity, the lower is NaN.
+                constexpr float kHi = kDown * 1.0000002384185791015625f, kLo = kDown * -5.364418029785156e-07f;
+                const F2 hi = mul2(q, f2(kHi, kHi)), lo = fma2(q, f2(kLo, kLo), hi);
+                out[j / 2] = pack2(split(hi), T());
+                any |= apart[j / 2] = out[j / 2] ^ pack2(split(lo), T());
             }
-            if (apart != 0u) {
+            if (any != 0u) {
 #pragma unroll
-                for (int j = 0; j < N; ++j) y.v[j] = rounded_once<T>(to_float(h[v].v[j]), w[j], r);
+                for (int j = 0; j < N; ++j)
+                    if (apart[j / 2] != 0u) y.v[j] = rounded_once<T>(to_float(h[v].v[j]), w[j], r);
             }
         }
         if (p.y != nullptr) lane.store(yo, v, y);
