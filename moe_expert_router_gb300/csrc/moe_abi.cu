@@ -1644,8 +1644,11 @@ moe_status_t moe_rms_norm(const void *x, const void *residual, const void *weigh
         !aligned_to(h, size) || !aligned_to(y, size) || !aligned_to(weight, dtype_size(s.w_dtype)) ||
         !aligned_to(rstd, 4))
         return MOE_ERR_INVALID_ARG;
-    if (h != nullptr && (h == y || (h == x && s.T > 1 && s.ld_x != s.H) || (h == residual && s.T > 1 && s.ld_r != s.H)))
-        return MOE_ERR_INVALID_ARG;
+    // an output in the place of rows that lie apart would write over those that other blocks have yet to read
+    auto over = [&](const void *out) {
+        return out != nullptr && s.T > 1 && ((out == x && s.ld_x != s.H) || (out == residual && s.ld_r != s.H));
+    };
+    if ((h != nullptr && h == y) || over(h) || over(y)) return MOE_ERR_INVALID_ARG;
     NormLaunch p{};
     const bool out = rows_vectorized(h, s.H, s.dtype) && rows_vectorized(y, s.H, s.dtype) && aligned16(weight);
     const bool in = rows_vectorized(x, s.ld_x, s.dtype) && rows_vectorized(residual, s.ld_r, s.dtype);
