@@ -420,8 +420,9 @@ moe_status_t moe_rms_norm_backward(const void *dy, const void *dh, const void *h
  * do not, no group is computed and MOE_DEVERR_BAD_OFFSETS is set in ws. Rows outside every
  * group are not read as rows of a product (they may hold anything, NaN too), and out's are
  * left as they were. Operands are bf16 or fp16, added in fp32 and rounded once. Limits: K
- * and N multiples of 8, G <= 1024, R < 2^31 - 256, rows of x, out, a and b 16-byte aligned
- * (ld multiples of 8), matrices dense. out and dw share no memory with any operand.
+ * and N multiples of 8, G <= 1024, R < 2^31 - 256, G K and G N (and the number of 256 x 256
+ * tiles) below 2^31 - 4096, rows of x, out, a and b 16-byte aligned (ld multiples of 8),
+ * matrices dense. out and dw share no memory with any operand.
  * The same bits on every call.
  *
  * ws: moe_grouped_workspace_size bytes, 256-byte aligned, its first 256 bytes zeroed once

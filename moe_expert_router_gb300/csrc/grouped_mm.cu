@@ -263,9 +263,7 @@ cudaError_t launch_pair(const PairLaunch &l, GroupedKind kind, cudaStream_t st) 
     }
     const PairMaps maps{*l.tm_a, *l.tm_b, *(l.tm_b_wide != nullptr ? l.tm_b_wide : l.tm_b)};
     const int most = kind == GroupedKind::wgrad ? 256 : grouped_most(l.R, l.G, kind == GroupedKind::rows_mx);
-    // (at most: the rows' tiles are known on the device alone)
-    const int64_t tiles = kind == GroupedKind::wgrad ? static_cast<int64_t>(l.G) * p.n_tiles * p.k_tiles
-                                                     : (static_cast<int64_t>(l.R) / most + (l.R < l.G ? l.R : l.G)) * p.n_tiles;
+    const int64_t tiles = kind == GroupedKind::wgrad ? grouped_matrix_tiles(l.G, l.K, l.N) : grouped_row_tiles(l.R, l.G, l.N, most);
     const int clusters = tiles < l.clusters ? static_cast<int>(tiles) : l.clusters;
     cudaError_t e = cudaErrorInvalidValue;
     if (kind == GroupedKind::wgrad) e = launch_pair_of<kPairWgrad, 256>(maps, p, clusters, st);

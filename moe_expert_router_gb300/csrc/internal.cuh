@@ -400,6 +400,12 @@ inline int grouped_most(int64_t R, int64_t G, bool mx) {
     if (R <= 32 * G) return 64;
     return !mx ? 256 : R <= 256 * G ? 192 : 224;
 }
+// Tiles of the pairs, 256 columns each: of the rows at most (how a group's are cut is known on the device alone),
+// and of the matrices' gradients. They, rows of all matrices and columns are 32-bit numbers in the kernels, which
+// count at most kGroupedReach past the last one (grouped_few_kernel: two turns of its warps, 2048 columns of K).
+constexpr int64_t kGroupedReach = 4096;
+inline int64_t grouped_row_tiles(int64_t R, int64_t G, int64_t N, int most) { return (R / most + (R < G ? R : G)) * ((N + 255) / 256); }
+inline int64_t grouped_matrix_tiles(int64_t G, int64_t K, int64_t N) { return G * ((N + 255) / 256) * ((K + 255) / 256); }
 // moe_grouped_mm with w [G, N, K] for a few rows, in one launch. It reads a group's matrix once for every 8 of
 // its rows; measured against the pairs' tiles (us): 16 rows of one group 4096 x 4096 13 and 17, 32 rows 24 and 17;
 // 32 rows of 8 groups 46 and 45, of 8 groups 2048 x 1408 12 and 13, 64 rows of 8 groups 4096 x 4096 51 and 45;

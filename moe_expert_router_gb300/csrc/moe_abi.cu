@@ -1540,14 +1540,14 @@ moe_status_t check_grouped(const moe_grouped_shape_t *s, const void *ws, size_t 
         (s->flags & ~flags) != 0)
         return MOE_ERR_INVALID_ARG;
     if (s->dtype != MOE_DTYPE_BF16 && !(any16 && s->dtype == MOE_DTYPE_F16)) return MOE_ERR_UNSUPPORTED;
-    constexpr int64_t most = (static_cast<int64_t>(1) << 31) - kUnitM;
+    constexpr int64_t top = static_cast<int64_t>(1) << 31, most = top - 256, reach = top - kGroupedReach;
     if (s->G > 1024 || s->K % 8 || s->N % 8 || s->ld_x % 8 || s->ld_out % 8 || s->R >= most || s->ld_x >= most ||
         s->ld_out >= most)
         return MOE_ERR_UNSUPPORTED;
-    // rows of all matrices, and units, are 32-bit numbers
-    if (s->G * s->N >= most || s->G * s->K >= most) return MOE_ERR_UNSUPPORTED;
-    const int64_t n_tiles = (s->N + 223) / 224, k_tiles = (s->K + kBN - 1) / kBN;
-    if ((s->R / kUnitM + s->G) * n_tiles >= most || s->G * n_tiles * k_tiles >= most) return MOE_ERR_UNSUPPORTED;
+    if (s->G * s->N >= reach || s->G * s->K >= reach) return MOE_ERR_UNSUPPORTED;
+    if (grouped_row_tiles(s->R, s->G, s->N, grouped_most(s->R, s->G, !any16)) >= reach ||
+        grouped_matrix_tiles(s->G, s->K, s->N) >= reach)
+        return MOE_ERR_UNSUPPORTED;
     if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_INVALID_ARG;
     return ws_bytes < grouped_layout(s->G).total ? MOE_ERR_WORKSPACE : MOE_OK;
 }

@@ -27,3 +27,22 @@ def test_norm_outputs_over_rows_apart(lib):
     for kw in (dict(ld_x=136, y=p), dict(residual=far, ld_r=136, y=far), dict(residual=far, ld_r=129, y=far, h=p),
                dict(residual=far, ld_x=256, y=p, h=far), dict(T=2, ld_x=136, y=p)):
         assert call(**kw) == INVALID, kw
+
+
+def test_grouped_sizes_at_the_end_of_32_bits(lib):
+    """Sizes whose counters in the kernels would pass 2^31 are refused before a launch: the few-row kernel
+    counts up to 2048 columns past K."""
+    p = 1 << 20
+
+    def calls(R=4, G=1, K=64, N=64):
+        s = B.GroupedShape(R=R, G=G, K=K, N=N, ld_x=K, ld_out=N, dtype=1, flags=0)
+        ref, n = ctypes.byref(s), 1 << 20
+        got = {lib.moe_grouped_mm(P(p), P(p), P(p), ref, P(p), P(p), n, None),
+               lib.moe_grouped_wgrad(P(p), P(p), P(p), ref, P(p), P(p), n, None)}
+        if K % 128 == 0:
+            got.add(lib.moe_grouped_mm_mx(P(p), P(p), P(p), P(p), P(p), ref, P(p), P(p), n, None))
+        return got
+    end = 2**31
+    for kw in (dict(K=end - 512), dict(K=end - 4096), dict(N=end - 512), dict(N=end - 4096), dict(G=8, K=end // 8 - 8),
+               dict(G=512, N=end // 512 - 8), dict(K=end - 264, N=8), dict(R=end - 264, N=2**16, K=8)):
+        assert calls(**kw) == {UNSUPPORTED}, kw
