@@ -437,11 +437,14 @@ typedef struct moe_grouped_shape {
     int64_t ld_x;   /* elements from a row of x to the next one, >= K */
     int64_t ld_out; /* the same of out, >= N */
     int32_t dtype;  /* MOE_DTYPE_BF16 or MOE_DTYPE_F16, of every operand */
-    int32_t flags;  /* 0 or MOE_GROUPED_W_KN */
+    int32_t flags;  /* MOE_GROUPED_* or 0 */
 } moe_grouped_shape_t;
 
 /* moe_grouped_shape_t.flags: w is [G,K,N] (input by output), not [G,N,K]. */
 #define MOE_GROUPED_W_KN 0x1
+/* Of bad offsets all of out (all of dw) becomes NaN, which a result that no one checks carries on. (They set the
+ * error word either way. moe_grouped_mm_mx does not take the flag.) */
+#define MOE_GROUPED_NAN_ON_BAD 0x4
 
 moe_status_t moe_grouped_workspace_size(int64_t G, size_t *bytes);
 
@@ -457,7 +460,8 @@ moe_status_t moe_grouped_mm(const void *x, const void *w, const int32_t *offsets
  * The gradient of the matrices: dw[g] = sum over g's rows of a[r,:]^T b[r,:], dw [G,N,K] with
  * a [R,N] (rows ld_out apart) the gradient of out and b [R,K] (rows ld_x apart) the x of
  * moe_grouped_mm; for w [G,K,N], a is x and b the gradient. Every group is written, one
- * without rows with zeros. flags is 0.
+ * without rows with zeros, and all with zeros where offsets are bad. flags is 0 or
+ * MOE_GROUPED_NAN_ON_BAD.
  */
 moe_status_t moe_grouped_wgrad(const void *a, const void *b, const int32_t *offsets, const moe_grouped_shape_t *shape,
                                void *dw, void *ws, size_t ws_bytes, void *stream);

@@ -619,16 +619,20 @@ def grouped_workspace(G, device=None) -> torch.Tensor:
     return ws
 
 
-def moe_grouped_mm(x, w, offsets, out, ws, transposed=False, stream=None):
+def moe_grouped_mm(x, w, offsets, out, ws, transposed=False, stream=None, nan_on_bad=False):
     """out[r] = x[r] . w[g]^T for the rows offsets[g] .. offsets[g + 1] - 1 of each group g; x [R, K]
     and out [R, N] bf16 or fp16 (rows may be apart), w [G, N, K], or with transposed w [G, K, N] and
-    out[r] = x[r] . w[g]; offsets int32 [G + 1] on the device. Rows of no group are left alone."""
-    _check("moe_grouped_mm", _module().grouped_mm(x, w, offsets, out, ws, bool(transposed), _raw_stream(stream, x)))
+    out[r] = x[r] . w[g]; offsets int32 [G + 1] on the device. Rows of no group are left alone. Offsets that
+    decrease or leave [0, R] set DEVERR_BAD_OFFSETS in ws and leave out alone, or with nan_on_bad fill it with
+    NaN."""
+    _check("moe_grouped_mm", _module().grouped_mm(x, w, offsets, out, ws, bool(transposed), bool(nan_on_bad),
+                                                  _raw_stream(stream, x)))
 
 
-def moe_grouped_wgrad(a, b, offsets, dw, ws, stream=None):
-    """dw[g] = the sum over group g's rows of a[r]^T b[r]; a [R, N], b [R, K], dw [G, N, K] of one type."""
-    _check("moe_grouped_wgrad", _module().grouped_wgrad(a, b, offsets, dw, ws, _raw_stream(stream, a)))
+def moe_grouped_wgrad(a, b, offsets, dw, ws, stream=None, nan_on_bad=False):
+    """dw[g] = the sum over group g's rows of a[r]^T b[r]; a [R, N], b [R, K], dw [G, N, K] of one type. Of bad
+    offsets dw is 0, or with nan_on_bad NaN."""
+    _check("moe_grouped_wgrad", _module().grouped_wgrad(a, b, offsets, dw, ws, bool(nan_on_bad), _raw_stream(stream, a)))
 
 
 def moe_grouped_mm_mx(x_codes, x_scales, w_codes, w_scales, offsets, out, ws, stream=None):

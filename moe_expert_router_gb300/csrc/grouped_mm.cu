@@ -63,6 +63,7 @@ struct GroupedFew {
     int32_t *err;
     int64_t ld_x, ld_out;
     int R, G, K, N;
+    int nan_on_bad;
 };
 
 // Weights are read once: no place in L1 for them.
@@ -97,6 +98,9 @@ grouped_few_kernel(const GroupedFew p) {
     }
     if (__syncthreads_or(bad)) {
         if (blockIdx.x == 0 && r0 == 0 && threadIdx.x == 0) atomicOr(p.err, MOE_DEVERR_BAD_OFFSETS);
+        const int n = blockIdx.x * COLS + 2 * threadIdx.x;  // of bad offsets every row and column has its block
+        if (p.nan_on_bad && 2 * threadIdx.x < COLS && n < p.N)
+            *reinterpret_cast<uint32_t *>(p.out + r0 * p.ld_out + n) = nan_16x2(F16);
         return;
     }
     const int g = found[0];
@@ -181,9 +185,9 @@ grouped_few_kernel(const GroupedFew p) {
 }  // namespace
 
 cudaError_t launch_grouped_few(const void *x, const void *w, const int32_t *offsets, void *out, int32_t *err, int64_t ld_x,
-                               int64_t ld_out, int R, int G, int K, int N, bool f16, cudaStream_t st) {
+                               int64_t ld_out, int R, int G, int K, int N, bool f16, bool nan_on_bad, cudaStream_t st) {
     GroupedFew p{static_cast<const uint16_t *>(x), static_cast<const uint16_t *>(w), offsets, static_cast<uint16_t *>(out),
-                 err, ld_x, ld_out, R, G, K, N};
+                 err, ld_x, ld_out, R, G, K, N, nan_on_bad};
     // groups of several rows: fewer reads of x (8 rows of one group, 4096 x 11008: 19.9 us, and 22.4 with
     // 16 columns); of one: more blocks (8 of 32 matrices of 4096 x 7168: 68.0 us, and 73.7 with 32)
     const int cols = R > 2 * G ? 32 : 16;
@@ -252,6 +256,7 @@ cudaError_t launch_pair(const PairLaunch &l, GroupedKind kind, cudaStream_t st) 
     p.n_tiles = (l.N + 255) / 256;
     p.k_tiles = (l.K + 255) / 256;
     p.f16 = l.f16;
+    p.nan_on_bad = l.nan_on_bad;
     p.a_one = l.a_one;
     p.b_one = l.b_one;
     p.group_maps = static_cast<const CUtensorMap *>(l.group_maps);

@@ -412,7 +412,7 @@ inline int64_t grouped_matrix_tiles(int64_t G, int64_t K, int64_t N) { return G 
 // 64 rows of 16 groups 4096 x 1536 34 and 39; 256 rows of 128 groups 4096 x 1536 229 and 232.
 inline bool grouped_few(int64_t R, int64_t G) { return R <= 16 || (R <= 64 && R <= 4 * G) || (R <= 256 && R <= 2 * G); }
 cudaError_t launch_grouped_few(const void *x, const void *w, const int32_t *offsets, void *out, int32_t *err, int64_t ld_x,
-                               int64_t ld_out, int R, int G, int K, int N, bool f16, cudaStream_t st);
+                               int64_t ld_out, int R, int G, int K, int N, bool f16, bool nan_on_bad, cudaStream_t st);
 
 // The grouped products on pairs of SMs (pair_gemm.cuh): rows and rows_t with tm_a the matrices' map, tm_b
 // and tm_b_wide those of x in boxes of 32 and of half a tile's rows; rows_mx also with those of the scale words of
@@ -425,6 +425,7 @@ struct PairLaunch {
     void *out;
     int64_t ld_out;
     int R, G, K, N, f16, clusters;
+    int nan_on_bad;             // bad offsets: out becomes NaN
     int a_one, b_one;           // MN-major operands: their maps are encode_bf16_atoms
     void *group_maps;           // wgrad: two tensor maps a group, written by the launch
 };

@@ -1563,6 +1563,7 @@ PairLaunch pair_launch(const moe_grouped_shape_t &s, const int32_t *offsets, voi
     p.K = static_cast<int>(s.K);
     p.N = static_cast<int>(s.N);
     p.f16 = s.dtype == MOE_DTYPE_F16;
+    p.nan_on_bad = (s.flags & MOE_GROUPED_NAN_ON_BAD) != 0;
     p.clusters = d.clusters;
     p.group_maps = static_cast<uint8_t *>(ws) + grouped_layout(s.G).maps;
     return p;
@@ -1736,7 +1737,7 @@ moe_status_t moe_grouped_workspace_size(int64_t G, size_t *bytes) {
 
 moe_status_t moe_grouped_mm(const void *x, const void *w, const int32_t *offsets, const moe_grouped_shape_t *shape,
                             void *out, void *ws, size_t ws_bytes, void *stream) {
-    moe_status_t r = check_grouped(shape, ws, ws_bytes, true, MOE_GROUPED_W_KN);
+    moe_status_t r = check_grouped(shape, ws, ws_bytes, true, MOE_GROUPED_W_KN | MOE_GROUPED_NAN_ON_BAD);
     if (r != MOE_OK) return r;
     const moe_grouped_shape_t &s = *shape;
     if (s.R == 0) return MOE_OK;
@@ -1750,6 +1751,7 @@ moe_status_t moe_grouped_mm(const void *x, const void *w, const int32_t *offsets
         return cuda_status(launch_grouped_few(x, w, offsets, out, static_cast<int32_t *>(ws), s.ld_x, s.ld_out,
                                               static_cast<int>(s.R), static_cast<int>(s.G), static_cast<int>(s.K),
                                               static_cast<int>(s.N), s.dtype == MOE_DTYPE_F16,
+                                              (s.flags & MOE_GROUPED_NAN_ON_BAD) != 0,
                                               static_cast<cudaStream_t>(stream)));
     if (d->clusters < 1) return MOE_ERR_UNSUPPORTED;
     const bool one = s.N % 64 == 0;
@@ -1770,7 +1772,7 @@ moe_status_t moe_grouped_mm(const void *x, const void *w, const int32_t *offsets
 
 moe_status_t moe_grouped_wgrad(const void *a, const void *b, const int32_t *offsets, const moe_grouped_shape_t *shape,
                                void *dw, void *ws, size_t ws_bytes, void *stream) {
-    moe_status_t r = check_grouped(shape, ws, ws_bytes, true, 0);
+    moe_status_t r = check_grouped(shape, ws, ws_bytes, true, MOE_GROUPED_NAN_ON_BAD);
     if (r != MOE_OK) return r;
     const moe_grouped_shape_t &s = *shape;
     if (dw == nullptr || !aligned16(dw)) return MOE_ERR_INVALID_ARG;

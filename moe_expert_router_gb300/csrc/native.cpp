@@ -466,7 +466,7 @@ int grouped_type(const at::Tensor &t, const char *name) {
     return code;
 }
 
-// x, w, offsets, out, ws, transposed, stream
+// x, w, offsets, out, ws, transposed, nan_on_bad, stream
 PyObject *grouped_mm(PyObject *const *a) {
     const Rows x = rows_of(a[0], "x", nullptr, -1, -1);
     const at::Tensor &on = x.tensor;
@@ -481,12 +481,13 @@ PyObject *grouped_mm(PyObject *const *a) {
     apart(out, w, "w");
     apart(out, THPVariable_Unpack(a[2]), "offsets");
     apart(out, THPVariable_Unpack(a[4]), "ws");
-    const moe_grouped_shape_t s{x.rows, G, x.cols, N, x.ld, out.ld, code, kn ? MOE_GROUPED_W_KN : 0};
-    return changed(g_grouped_mm(x.ptr, w.data_ptr(), offsets, &s, out.ptr, ws.ptr, ws.bytes, handle(a[6])),
+    const moe_grouped_shape_t s{x.rows, G, x.cols, N, x.ld, out.ld, code,
+                                (kn ? MOE_GROUPED_W_KN : 0) | (whole(a[6]) != 0 ? MOE_GROUPED_NAN_ON_BAD : 0)};
+    return changed(g_grouped_mm(x.ptr, w.data_ptr(), offsets, &s, out.ptr, ws.ptr, ws.bytes, handle(a[7])),
                    [&] { bump(out.tensor); });
 }
 
-// a, b, offsets, dw, ws, stream
+// a, b, offsets, dw, ws, nan_on_bad, stream
 PyObject *grouped_wgrad(PyObject *const *a) {
     const Rows l = rows_of(a[0], "a", nullptr, -1, -1);
     const at::Tensor &on = l.tensor;
@@ -500,8 +501,8 @@ PyObject *grouped_wgrad(PyObject *const *a) {
     apart(dw, "dw", r);
     apart(dw, "dw", THPVariable_Unpack(a[2]), "offsets");
     apart(dw, "dw", THPVariable_Unpack(a[4]), "ws");
-    const moe_grouped_shape_t s{l.rows, G, r.cols, l.cols, r.ld, l.ld, code, 0};
-    return changed(g_grouped_wgrad(l.ptr, r.ptr, offsets, &s, dw.data_ptr(), ws.ptr, ws.bytes, handle(a[5])), [&] { bump(dw); });
+    const moe_grouped_shape_t s{l.rows, G, r.cols, l.cols, r.ld, l.ld, code, whole(a[5]) != 0 ? MOE_GROUPED_NAN_ON_BAD : 0};
+    return changed(g_grouped_wgrad(l.ptr, r.ptr, offsets, &s, dw.data_ptr(), ws.ptr, ws.bytes, handle(a[6])), [&] { bump(dw); });
 }
 
 // x_codes, x_scales, w_codes, w_scales, offsets, out, ws, stream
@@ -684,8 +685,8 @@ PyMethodDef kMethods[] = {method<bind, 11>("bind"),
                           method<clip_grads, 6>("clip_grads"),
                           method<adamw, 12>("adamw"),
                           method<scratch_with_norm, 2>("scratch"),
-                          method<grouped_mm, 7>("grouped_mm"),
-                          method<grouped_wgrad, 6>("grouped_wgrad"),
+                          method<grouped_mm, 8>("grouped_mm"),
+                          method<grouped_wgrad, 7>("grouped_wgrad"),
                           method<grouped_mm_mx, 8>("grouped_mm_mx"),
                           method<rms_norm, 10>("rms_norm"),
                           method<rms_norm_backward, 9>("rms_norm_backward"),

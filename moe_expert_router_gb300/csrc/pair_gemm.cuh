@@ -79,6 +79,7 @@ struct __align__(1024) PairSmem {
     int start[kMaxGroups + 1];              // the groups' first rows
     int tiles[kMaxGroups + 1];              // prefix of their row tiles
     int scan[32];
+    uint32_t none;                          // kPairWgrad: what a group without rows has, two of it
     uint32_t tmem_base;
     int abort;
 };
@@ -94,6 +95,7 @@ struct PairArgs {
     int N;                  // columns of out; kPairWgrad: rows of dw
     int n_tiles, k_tiles;
     int f16;
+    int nan_on_bad;         // bad offsets: out becomes NaN
     int a_one, b_one;       // MN-major operands: both 64-column atoms in one copy
     const CUtensorMap *group_maps;  // kPairWgrad: a's and b's of each group
 };
@@ -105,6 +107,9 @@ struct PairMxMaps : PairMaps {
     CUtensorMap sfa, sfb;   // scale words of the matrices, and of x
 };
 template <int MODE> using PairMapsOf = std::conditional_t<MODE == kPairMx, PairMxMaps, PairMaps>;
+
+// Two NaN of the operands' type.
+__device__ __forceinline__ uint32_t nan_16x2(bool f16) { return f16 ? 0x7e007e00u : 0x7fc07fc0u; }
 
 // ---------------------------------------------------------------- cluster and pair instructions
 
@@ -384,6 +389,13 @@ pair_gemm_kernel(const __grid_constant__ PairMapsOf<MODE> maps, const PairArgs p
         }
     }
     if (bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, MOE_DEVERR_BAD_OFFSETS);
+    if (threadIdx.x == 0) sm.none = bad && p.nan_on_bad ? nan_16x2(p.f16) : 0u;
+    if (MODE != kPairWgrad && bad && p.nan_on_bad) {        // (no tile writes out then)
+        const int cols = p.N / 2;                           // pairs of columns: rows are 16-byte aligned
+        const int64_t step = static_cast<int64_t>(gridDim.x) * kPairThreads<MODE>;
+        for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPairThreads<MODE> + threadIdx.x; i < static_cast<int64_t>(p.R) * cols; i += step)
+            *reinterpret_cast<uint32_t *>(p.out + i / cols * p.ld_out + i % cols * 2) = nan_16x2(p.f16);
+    }
     __syncthreads();
     cluster_sync();                         // both CTAs' barriers and tensor memory are set up
     tc_fence_after();
@@ -591,7 +603,7 @@ pair_gemm_kernel(const __grid_constant__ PairMapsOf<MODE> maps, const PairArgs p
                     pair_piece2(tacc + 256 * buf + 64, f16, pk[2], pk[3]);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) pk[i >> 4][i & 15] = 0u;
+                    for (int i = 0; i < 64; ++i) pk[i >> 4][i & 15] = sm.none;
                 }
                 tc_fence_before();
                 __syncwarp();

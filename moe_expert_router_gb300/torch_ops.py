@@ -794,16 +794,22 @@ def _grouped_rows(t):
     return t
 
 
-@torch.library.custom_op(f"{_LIB}::grouped_rows", mutates_args=())
-def grouped_rows(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, transposed: bool = False,
-                 complete: bool = False) -> torch.Tensor:
-    """moe_grouped_mm into a new tensor; rows of no group are zeros (with complete there are none)."""
+def _grouped_product(x, w, offsets, transposed, complete):
+    """moe_grouped_mm into a new tensor, and the workspace that holds the call's error word."""
     N = _check_grouped_args(x, w, offsets, transposed)
     new = torch.empty if complete else torch.zeros
     out = new((x.shape[0], N), dtype=x.dtype, device=x.device)
-    B.moe_grouped_mm(_grouped_rows(x), w.contiguous(), offsets.contiguous(), out, B.grouped_workspace(w.shape[0], x.device),
-                     transposed=transposed)
-    return out
+    ws = B.grouped_workspace(w.shape[0], x.device)
+    B.moe_grouped_mm(_grouped_rows(x), w.contiguous(), offsets.contiguous(), out, ws, transposed=transposed, nan_on_bad=True)
+    return out, ws
+
+
+@torch.library.custom_op(f"{_LIB}::grouped_rows", mutates_args=())
+def grouped_rows(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, transposed: bool = False,
+                 complete: bool = False) -> torch.Tensor:
+    """moe_grouped_mm into a new tensor; rows of no group are zeros (with complete there are none), and all
+    are NaN where offsets decrease or leave the rows."""
+    return _grouped_product(x, w, offsets, transposed, complete)[0]
 
 
 @grouped_rows.register_fake
@@ -811,13 +817,28 @@ def _grouped_rows_fake(x, w, offsets, transposed=False, complete=False):
     return x.new_empty((x.shape[0], _check_grouped_args(x, w, offsets, transposed)))
 
 
+@torch.library.custom_op(f"{_LIB}::grouped_rows_checked", mutates_args=())
+def grouped_rows_checked(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, transposed: bool = False,
+                         complete: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
+    """grouped_rows with the call's error word, int32 [1] on the device: 0 or DEVERR_*."""
+    out, ws = _grouped_product(x, w, offsets, transposed, complete)
+    return out, ws[:4].view(torch.int32)
+
+
+@grouped_rows_checked.register_fake
+def _grouped_rows_checked_fake(x, w, offsets, transposed=False, complete=False):
+    N = _check_grouped_args(x, w, offsets, transposed)
+    return x.new_empty((x.shape[0], N)), x.new_empty((1,), dtype=torch.int32)
+
+
 @torch.library.custom_op(f"{_LIB}::grouped_wgrad", mutates_args=())
 def grouped_wgrad(a: torch.Tensor, b: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
-    """moe_grouped_wgrad: [G, columns of a, columns of b]."""
+    """moe_grouped_wgrad: [G, columns of a, columns of b]; NaN where offsets decrease or leave the rows."""
     _expect(b, "b", a.dtype, (a.shape[0], b.shape[1]))
     G = offsets.shape[0] - 1
     dw = torch.empty((G, a.shape[1], b.shape[1]), dtype=a.dtype, device=a.device)
-    B.moe_grouped_wgrad(_grouped_rows(a), _grouped_rows(b), offsets.contiguous(), dw, B.grouped_workspace(G, a.device))
+    B.moe_grouped_wgrad(_grouped_rows(a), _grouped_rows(b), offsets.contiguous(), dw, B.grouped_workspace(G, a.device),
+                        nan_on_bad=True)
     return dw
 
 
@@ -832,7 +853,7 @@ def _grouped_setup_context(ctx, inputs, output):
     ctx.cfg = (transposed, complete)
 
 
-def _grouped_backward_rule(ctx, dout):
+def _grouped_backward_rule(ctx, dout, _word=None):
     x, w, offsets = ctx.saved_tensors
     transposed, complete = ctx.cfg
     dx = grouped_rows(dout, w, offsets, not transposed, complete) if ctx.needs_input_grad[0] else None
@@ -842,16 +863,19 @@ def _grouped_backward_rule(ctx, dout):
     return dx, dw, None, None, None
 
 
-grouped_rows.register_autograd(_grouped_backward_rule, setup_context=_grouped_setup_context)
+for _op in (grouped_rows, grouped_rows_checked):
+    _op.register_autograd(_grouped_backward_rule, setup_context=_grouped_setup_context)
 
 
-def grouped_mm(x, w, offsets, transposed=False, complete=False):
+def grouped_mm(x, w, offsets, transposed=False, complete=False, errors=False):
     """out[r] = x[r] . w[g]^T for the rows offsets[g] .. offsets[g + 1] - 1 of each group, as one
     differentiable call: x [R, K] and w [G, N, K] bf16 or fp16 (transposed: w [G, K, N] and
     out[r] = x[r] . w[g]), offsets int32 [G + 1] on the device; gradients for x and w. Rows of no
     group come out as zeros, and so does their gradient; `complete` promises that there are none,
-    which saves clearing the result."""
-    return grouped_rows(x, w, offsets, transposed, complete)
+    which saves clearing the result. Offsets that decrease or leave the rows make everything NaN, the
+    gradients too; with `errors` the call gives (out, word), int32 [1] on the device that then is
+    DEVERR_BAD_OFFSETS (0 for a good call)."""
+    return (grouped_rows_checked if errors else grouped_rows)(x, w, offsets, transposed, complete)
 
 
 # the E4M3 copies of the expert weights that moe_layer(..., precision="mxfp8") uses when

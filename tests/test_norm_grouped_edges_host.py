@@ -2,12 +2,14 @@
 import ctypes
 
 import pytest
+import torch
 
 from moe_expert_router_gb300 import binding as B
 from moe_expert_router_gb300 import build as moe_build
+from moe_expert_router_gb300 import torch_ops
 
 P = ctypes.c_void_p
-INVALID, UNSUPPORTED = 1, 2
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 4
 
 
 @pytest.fixture(scope="module")
@@ -46,3 +48,27 @@ def test_grouped_sizes_at_the_end_of_32_bits(lib):
     for kw in (dict(K=end - 512), dict(K=end - 4096), dict(N=end - 512), dict(N=end - 4096), dict(G=8, K=end // 8 - 8),
                dict(G=512, N=end // 512 - 8), dict(K=end - 264, N=8), dict(R=end - 264, N=2**16, K=8)):
         assert calls(**kw) == {UNSUPPORTED}, kw
+
+
+def test_grouped_flags(lib):
+    """NaN for bad offsets is a flag of the 16-bit products; others are refused."""
+    p = 1 << 20
+
+    def call(f, flags):
+        s = B.GroupedShape(R=10, G=3, K=128, N=72, ld_x=128, ld_out=72, dtype=1, flags=flags)
+        args = [P(p)] * (5 if f == "moe_grouped_mm_mx" else 3)
+        return getattr(lib, f)(*args, ctypes.byref(s), P(p), P(p), 8, None)
+    for f, flags in (("moe_grouped_mm", 8), ("moe_grouped_mm", 6), ("moe_grouped_wgrad", 5), ("moe_grouped_wgrad", 2),
+                     ("moe_grouped_mm_mx", 4)):
+        assert call(f, flags) == INVALID
+    for f, flags in (("moe_grouped_mm", 4), ("moe_grouped_mm", 5), ("moe_grouped_wgrad", 4), ("moe_grouped_mm_mx", 0)):
+        assert call(f, flags) == WORKSPACE                  # the flags are taken: what fails is the workspace's size
+
+
+def test_checked_product_on_meta_tensors():
+    m = lambda *s, dtype=torch.bfloat16, grad=False: torch.empty(s, dtype=dtype, device="meta", requires_grad=grad)  # noqa: E731
+    x, w = m(10, 256, grad=True), m(3, 72, 256, grad=True)
+    out, word = torch_ops.grouped_mm(x, w, m(4, dtype=torch.int32), errors=True)
+    assert out.shape == (10, 72) and word.shape == (1,) and word.dtype == torch.int32 and not word.requires_grad
+    out.sum().backward()
+    assert x.grad.shape == x.shape and w.grad.shape == w.shape
