@@ -639,6 +639,12 @@ def _check_norm_args(x, weight, residual, eps):
         _expect(residual, "residual", x.dtype, tuple(x.shape))
 
 
+def _dense(t):
+    """A dense tensor whose address is a multiple of 16 (a view into a flat buffer need not be one): the same, or a copy."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 def _stream_empty(x, residual):
     return torch.empty((0 if residual is None else x.shape[0], x.shape[1]), dtype=x.dtype, device=x.device)
 
@@ -718,7 +724,7 @@ def rms_norm_mx(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.
     _check_norm_args(x, weight, residual, eps)
     if x.shape[1] % 128:
         raise ValueError("MXFP8 needs H a multiple of 128")
-    x, weight = _rows(x), weight.contiguous()
+    x, weight = _rows(x), _dense(weight)
     residual = None if residual is None else _rows(residual)
     y, h = torch.empty(x.shape, dtype=x.dtype, device=x.device), _stream_empty(x, residual)
     codes, scales = torch.empty(x.shape, dtype=torch.uint8, device=x.device), B.mx_scales_empty(tuple(x.shape), x.device)
@@ -746,7 +752,7 @@ def forward_mx_codes(x_codes: torch.Tensor, x_scales: torch.Tensor, topk_idx: to
     E, two_i, _ = w1_codes.shape
     shp = B.shape(T, H, two_i // 2, E, topk_idx.shape[1], mxfp8=True)
     y = torch.empty((T, H), dtype=torch.bfloat16, device=x_codes.device)
-    B.moe_forward_mx_codes(x_codes, x_scales, topk_idx, topk_w, w1_codes, w1_scales, w2_codes, w2_scales, shp, y,
+    B.moe_forward_mx_codes(_dense(x_codes), _dense(x_scales), topk_idx, topk_w, w1_codes, w1_scales, w2_codes, w2_scales, shp, y,
                            B.new_workspace(shp, x_codes.device))
     return y
 
@@ -800,7 +806,7 @@ def _grouped_product(x, w, offsets, transposed, complete):
     new = torch.empty if complete else torch.zeros
     out = new((x.shape[0], N), dtype=x.dtype, device=x.device)
     ws = B.grouped_workspace(w.shape[0], x.device)
-    B.moe_grouped_mm(_grouped_rows(x), w.contiguous(), offsets.contiguous(), out, ws, transposed=transposed, nan_on_bad=True)
+    B.moe_grouped_mm(_grouped_rows(x), _dense(w), offsets.contiguous(), out, ws, transposed=transposed, nan_on_bad=True)
     return out, ws
 
 

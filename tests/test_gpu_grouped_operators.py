@@ -92,3 +92,57 @@ def test_error_word_of_a_captured_call():
         torch.cuda.synchronize()
         assert word.item() == (B.DEVERR_BAD_OFFSETS if bad else 0)
         assert torch.isnan(out).all() if bad else torch.equal(out, want)
+
+
+def at_odd_place(t, by):
+    """The same values as a dense view `by` elements into a flat buffer."""
+    flat = torch.zeros((t.numel() + by,), dtype=t.dtype, device=DEV)
+    out = flat[by:].view(t.shape)
+    out.copy_(t)
+    return out
+
+
+def test_matrices_at_odd_places():
+    gen = torch.Generator(DEV).manual_seed(3)
+    x, dy = whole(gen, 190, 136), whole(gen, 190, 72)
+    o = torch.tensor([2, 50, 50, 181], dtype=torch.int32, device=DEV)
+    for transposed in (False, True):
+        w = whole(gen, 3, 136, 72) if transposed else whole(gen, 3, 72, 136)
+        got = []
+        for by in (0, 1, 4):
+            xs, ws = x.clone().requires_grad_(), at_odd_place(w, by).requires_grad_()
+            out = torch_ops.grouped_mm(xs, ws, o, transposed=transposed)
+            got.append((out, *torch.autograd.grad(out, (xs, ws), at_odd_place(dy, by))))
+        for other in got[1:]:
+            for a, b in zip(got[0], other):
+                assert torch.equal(a, b)
+
+
+def test_norm_weights_at_odd_places():
+    gen = torch.Generator(DEV).manual_seed(4)
+    T, H = 9, 256
+    x, r = torch.randn((T, H), generator=gen, device=DEV).to(BF16), torch.randn((T, H), generator=gen, device=DEV).to(BF16)
+    for w in (torch.randn((H,), generator=gen, device=DEV), torch.randn((H,), generator=gen, device=DEV).to(BF16)):
+        want = torch_ops.rms_norm_mx(x, w, r)
+        got = torch_ops.rms_norm_mx(x, at_odd_place(w, 3), r)
+        for a, b in zip(got[:3], want[:3]):
+            assert torch.equal(a, b)
+        assert torch.equal(got[3][:, :T], want[3][:, :T])
+        assert torch.equal(torch_ops.rms_norm(x, at_odd_place(w, 3)), torch_ops.rms_norm(x, w))
+
+
+def test_codes_at_odd_places():
+    gen = torch.Generator(DEV).manual_seed(5)
+    T, H, I, E, k = 9, 256, 128, 4, 2
+    x = torch.randn((T, H), generator=gen, device=DEV).to(BF16)
+    q = []
+    for shape in ((E, 2 * I, H), (E, H, I)):
+        m = torch.randn(shape, generator=gen, device=DEV).to(BF16)
+        q += [torch.empty(shape, dtype=torch.uint8, device=DEV), B.mx_scales_empty(shape, DEV)]
+        B.moe_mx_quantize(m, *q[-2:])
+    idx = torch.rand((T, E), generator=gen, device=DEV).topk(k, dim=1)[1].int()
+    w = torch.rand((T, k), generator=gen, device=DEV)
+    _, _, codes, scales = torch_ops.rms_norm_mx(x, torch.ones((H,), device=DEV))
+    want = torch.ops.moe_gb300.forward_mx_codes(codes, scales, idx, w, *q)
+    got = torch.ops.moe_gb300.forward_mx_codes(at_odd_place(codes, 5), at_odd_place(scales, 4), idx, w, *q)
+    assert torch.equal(got, want)
