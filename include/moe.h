@@ -383,7 +383,7 @@ typedef struct moe_norm_shape {
     int64_t T;        /* rows */
     int64_t H;        /* columns */
     int64_t ld_x;     /* elements from a row of x to the next one, >= H (the backward: of h) */
-    int64_t ld_r;     /* the same of residual */
+    int64_t ld_r;     /* the same of residual; >= H also where there is none */
     double eps;       /* >= 1e-30 */
     int32_t dtype;    /* MOE_DTYPE_*, of x, residual, h and y */
     int32_t w_dtype;  /* of weight: dtype or MOE_DTYPE_F32 */
@@ -417,9 +417,9 @@ moe_status_t moe_rms_norm_backward(const void *dy, const void *dh, const void *h
  *
  * offsets int32 [G+1] on the device: group g has the rows offsets[g] .. offsets[g+1]-1
  * (none, where the two are equal). Offsets do not decrease and stay in [0, R]; where they
- * do not, no group is computed and MOE_DEVERR_BAD_OFFSETS is set in ws. Rows outside every
- * group are not read as rows of a product (they may hold anything, NaN too), and out's are
- * left as they were. Operands are bf16 or fp16, added in fp32 and rounded once. Limits: K
+ * do not, no group is computed and MOE_DEVERR_BAD_OFFSETS is set in ws (with R = 0 there is
+ * nothing to compute, and they are not read). Rows outside every group are not read as rows
+ * of a product (they may hold anything, NaN too), and out's are left as they were. Operands are bf16 or fp16, added in fp32 and rounded once. Limits: K
  * and N multiples of 8, G <= 1024, R < 2^31 - 256, G K and G N (and the number of 256 x 256
  * tiles) below 2^31 - 4096, rows of x, out, a and b 16-byte aligned (ld multiples of 8),
  * matrices dense. out and dw share no memory with any operand.

@@ -395,7 +395,8 @@ enum class GroupedKind { rows, rows_t, wgrad, rows_mx };
 // Rows of x in a tile at most, by the rows of a group (us). bf16: 1024 rows of 64 groups 4096 x 1536 128 in tiles
 // of 64 and 134 of 256, 4096 rows 137 and 138. MXFP8, whose scale words stand in tensor memory beside the
 // accumulators: 2048 rows of these 77 in tiles of 64 and 80 of 192, 6144 rows 83 of 192 and 85 of 224, 8192 rows
-// of one group 4096 x 4096 115 of 192 and 97 of 224.
+// of one group 4096 x 4096 115 of 192 and 97 of 224. (The average decides: groups of 193 to 224 rows, where 192 cuts
+// two tiles and 224 one, and most rows in one of many groups were not measured.)
 inline int grouped_most(int64_t R, int64_t G, bool mx) {
     if (R <= 32 * G) return 64;
     return !mx ? 256 : R <= 256 * G ? 192 : 224;

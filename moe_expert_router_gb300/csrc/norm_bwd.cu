@@ -208,9 +208,12 @@ cudaError_t launch_dw(const NormBackwardLaunch &p, cudaStream_t st) {
 
 }  // namespace
 
-// Blocks of the backward, as many as an SM holds and no more (each has a part of dw to write and to be
-// added: 4096 rows of 2048 in four blocks an SM 17 us, in eight 21; 16384 of 1024 34, and 27), and no
-// block has more than kNormRowsPerBlock rows a thread.
+// Blocks of the backward, by the width alone: each has a part of dw to write and to be added (bf16: 4096 rows of
+// 2048 in four blocks an SM 17 us, in eight 21; 16384 of 1024 34, and 27). That is what an SM holds of bf16 rows of
+// 520 to 8192 columns in whole vectors, for which alone it was measured; of a warp a row, of odd widths up to 1024, of bf16 rows
+// beyond 8192 and of fp32 rows of 4096 with dh an SM holds about half of them, and the rest are a second wave. Few
+// rows get a block each, also where a block could take eight: blocks without rows write parts of 0. No block has
+// more than kNormRowsPerBlock rows a thread.
 int64_t rms_norm_bwd_blocks(int64_t T, int64_t H) {
     const int64_t wave = 152 * (H <= 512 ? 6 : H <= 1024 ? 8 : H <= 4096 ? 4 : 2);
     const int64_t few = T < wave ? T : wave, many = (T + kNormRowsPerBlock - 1) / kNormRowsPerBlock;
