@@ -42,6 +42,7 @@ enum PairMode : int { kPairRows = 0, kPairRowsT = 1, kPairWgrad = 2, kPairMx = 3
 constexpr int kPairHalf = 128 * BK * 2;     // bytes of a CTA's half of one operand's k-block
 constexpr int kPairBoxRows = 32;            // rows of x in one copy: of these, or of all that a CTA can have
 constexpr int kMaxGroups = 1024;
+constexpr uint64_t kBlockLimitNs = 2000;    // of a k-block, in a wait for a whole sum
 
 template <int MODE> constexpr int kPairThreads = 64 + EPI_THREADS + (MODE == kPairMx ? HELPER_THREADS : 0);
 template <int MODE> constexpr bool kPairAMn = MODE == kPairRowsT || MODE == kPairWgrad;
@@ -553,7 +554,11 @@ pair_gemm_kernel(const __grid_constant__ PairMapsOf<MODE> maps, const PairArgs p
             const PairTile t = pair_tile<MODE, MOST>(u, sm, p);
             const int buf = n_done & 1;
             bool ok = true;
-            if (lane == 0) ok = mbar_wait(smem_addr(&sm.acc_full[buf]), (n_done >> 1) & 1, abort_flag, p.err);
+            // (the one wait that lasts as long as a tile's sum: a k-block takes some 0.25 us, so that a second is over
+            // after 240 million rows of a group, or columns of K)
+            if (lane == 0)
+                ok = mbar_wait(smem_addr(&sm.acc_full[buf]), (n_done >> 1) & 1, abort_flag, p.err,
+                               kWaitLimitNs + kBlockLimitNs * static_cast<uint64_t>(t.nkb));
             if (!__shfl_sync(0xffffffffu, ok, 0)) break;
             tc_fence_after();
             const int n = t.n0 + 128 * static_cast<int>(rank) + 32 * quad;      // the warp's first lane
