@@ -39,9 +39,10 @@ grouped_maps_kernel(const __grid_constant__ CUtensorMap a, const __grid_constant
 // and of x's row i the same ones, and lets the product take the eight pairs for the k it likes. The
 // warps' sums are added in order.
 //
-// HBM bounds it: 8 rows through 8 of 32 matrices of 4096 x 7168 (470 MB) 68 to 71 us by the run, 6.6 to 6.9
-// TB/s where a copy has 6.8; on the kernel of many rows 94, since a 128-row tile of one row streams its 256 matrix rows in pieces of
-// 128 bytes, and 128 of 152 SMs have a tile. One row of 4096 x 4096: 6.9 us, and 35.
+// HBM bounds it: 8 rows through 8 of 32 matrices of 4096 x 7168 (470 MB) 68 to 71 us by the run, 6.6 to
+// 6.9 TB/s where a copy has 6.8; on the kernel of many rows 94, since a 128-row tile of one row streams
+// its 256 matrix rows in pieces of 128 bytes, and 128 of 152 SMs have a tile. One row of 4096 x 4096:
+// 6.9 us, and 35.
 
 constexpr int kFewWarps = 8;
 
