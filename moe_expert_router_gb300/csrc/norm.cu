@@ -104,6 +104,18 @@ __device__ __forceinline__ Pair inverse_root(Pair sum, float scale, const NormLa
 constexpr float kLeast = 1.4551915228366852e-11f, kMost = 1.7014118346046923e38f;   // 2^-36, 2^127
 __device__ __forceinline__ bool inside(float z, float y) { return fminf(fabsf(z), fabsf(y)) >= kLeast && fabsf(y) < kMost; }
 
+// The smallest and the largest magnitude of three numbers.
+__device__ __forceinline__ float least(float a, float b, float c) {
+    float r;
+    asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float most(float a, float b, float c) {
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // h r / kUp w rounded once. (h r is taken first: it stays below kUp sqrt(H), where h w may leave fp32's range.) A
 // value of more digits is cut to fp32 with its last bit set where digits follow (round to odd): from there it rounds on
 // to 16 bits as it would itself.
@@ -214,17 +226,22 @@ rms_norm_kernel(const NormLaunch p) {
         lane.weight(p.weight, p.w_f32, v, w);
         Vec<T> y;
         if constexpr (sizeof(T) == 4) {
-            bool in = true;
+            float low = kMost, top = 0.f, last = 0.f;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const float z = __fmul_rn(h[v].v[j], r.hi), zl = fmaf(h[v].v[j], r.lo, fmaf(h[v].v[j], r.hi, -z));
                 const float o = __fmul_rn(z, w[j]);
                 y.v[j] = (o + fmaf(zl, w[j], fmaf(z, w[j], -o))) * kDown;
-                in &= inside(z, o);
+                low = least(low, z, o);
+                if (j & 1) top = most(top, o, last);
+                last = o;
             }
-            if (!in) {
+            if (low < kLeast || !(top < kMost)) {           // mostly a product of 0, which has no digits to lose
 #pragma unroll
-                for (int j = 0; j < N; ++j) y.v[j] = rounded_once<T>(h[v].v[j], w[j], r);
+                for (int j = 0; j < N; ++j) {
+                    const float z = __fmul_rn(h[v].v[j], r.hi);
+                    if (!inside(z, __fmul_rn(z, w[j])) && h[v].v[j] != 0.f && w[j] != 0.f) y.v[j] = rounded_once<T>(h[v].v[j], w[j], r);
+                }
             }
         } else {
             uint32_t *out = reinterpret_cast<uint32_t *>(&y.raw);
